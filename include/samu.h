@@ -80,7 +80,8 @@ int lrs_version(void);
  * of the calls below; every call clears the word when it starts, so it covers
  * the most recent call).  SYNCHRONISES `stream`.  *status receives LRS_OK or
  * LRS_ERR_TIMEOUT (LRS_ERR_CUDA if a kernel found its shared memory
- * misaligned and copied nothing).  Returns LRS_ERR_ARG / LRS_ERR_CUDA on failure. */
+ * misaligned and copied nothing; LRS_ERR_ARG if linear_ce_forward met a
+ * target past the vocabulary).  Returns LRS_ERR_ARG / LRS_ERR_CUDA on failure. */
 int lrs_device_status(void* scratch, int* status, cudaStream_t stream);
 
 /* Self-test of the failure path of the bounded device-side waits: launches
@@ -107,7 +108,8 @@ int lrs_selftest_wait_timeout(void* scratch, cudaStream_t stream);
  * 13 SAMU decode step, 14 RG-LRU gate-projection GEMMs, 15 RG-LRU projection
  * backward GEMMs, 16 RG-LRU weight packing and dW combination, 17 RecurrentBlock
  * contractions, 18 RecurrentBlock RMSNorm (forward and backward), 19 its
- * convolution, 20 its join, 21 its fixed-order gradient sums; 9 also covers
+ * convolution, 20 its join, 21 its fixed-order gradient sums, 22 the vocabulary
+ * loss's contractions, 23 its row statistics and sums; 9 also covers
  * the bias-gradient reductions) and duration in
  * milliseconds; *count receives the number of
  * kernels launched while profiling was on.  Not thread-safe: one profiling
@@ -445,6 +447,60 @@ int rglru_block_backward(const rglru_block_params* p, const void* x, const float
 #define LRS_GEMM_TN 2
 int lrs_dense_gemm(int layout, const void* A, const void* Bm, void* C, int M, int N, int K, void* scratch,
                    cudaStream_t stream);
+
+/* ======================================================================== */
+/* Softmax cross entropy over a vocabulary                                   */
+/* ======================================================================== */
+
+/* The loss at the end of a stack of blocks, without keeping the logits:
+ *   z_tv = h_t . w_v;  z' = c tanh(z / c) for softcap c > 0, else z' = z;
+ *   lse_t = log sum_v e^{z'_tv};  loss_t = lse_t - z'_{t, target_t}.
+ * A token whose target is negative is not counted: its loss is 0, its row
+ * adds nothing to any gradient, its lse is written like every other.  A
+ * target >= V is treated the same way and reported: lrs_device_status returns
+ * LRS_ERR_ARG for the forward's scratch.  T tokens, V vocabulary entries (any
+ * number of both), D the hidden width.
+ *
+ * Scratch bytes of the forward and of the backward (for that grad_dtype);
+ * either output pointer may be NULL.  The backward's scratch holds one piece
+ * of the vocabulary's logit gradients (at most 512 MiB, or 256 columns), the
+ * forward's 16 bytes per token and 256 vocabulary entries.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as linear_ce_forward. */
+int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forward_bytes, size_t* backward_bytes);
+
+/* Forward.
+ *   h        [T,D] BF16 (in);  w [V,D] BF16 (in);  target [T] int64 (in)
+ *   softcap  0 for none
+ *   loss     [T] FP32 (out);  lse [T] FP32 (out, the backward's input)
+ *   total    two FP32 (out): the sum of the losses and the number of tokens
+ *            counted (16-byte aligned)
+ *   scratch  linear_ce_workspace_bytes().forward bytes
+ * Products of BF16 values accumulate in FP32 on the tensor cores; sums of
+ * exponentials are FP32, the sum of the losses FP64, all in a fixed order.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, softcap
+ * negative or not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8, or sizes
+ * beyond 2^31 rows or tiles), LRS_ERR_CUDA. */
+int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T, int V, int D, float softcap,
+                      float* loss, float* lse, float* total, void* scratch, cudaStream_t stream);
+
+/* Backward: for the cotangents dloss of the losses
+ *   dz'_tv = dloss_t (e^{z'_tv - lse_t} - [v = target_t]),  dz = dz' (1 - (z'/c)^2),
+ *   dh = dz w,  dw = dz^T h,
+ * with the logits formed again, one piece of the vocabulary at a time.
+ *   h, w, target, T, V, D, softcap: the forward's (in);  lse [T] FP32 (in)
+ *   dloss    [T] FP32 (in), or NULL for the mean over the tokens counted
+ *            (1 / total[1] each; total is the forward's and may be NULL only
+ *            if dloss is given)
+ *   dh [T,D], dw [V,D]: BF16 or FP32 by grad_dtype (out)
+ *   scratch  linear_ce_workspace_bytes().backward bytes
+ * dz enters the two contractions in BF16 (LRS_GRAD_BF16: the results are
+ * rounded to BF16 themselves), or as a BF16 leading part plus a BF16 remainder
+ * (LRS_GRAD_FP32: 16 significant bits, twice the products).  Deterministic:
+ * every sum runs in a fixed order.  Errors: as the forward, plus LRS_ERR_ARG
+ * for an unknown grad_dtype. */
+int linear_ce_backward(const void* h, const void* w, const int64_t* target, const float* lse, const float* dloss,
+                       const float* total, int T, int V, int D, float softcap, void* dh, void* dw, int grad_dtype,
+                       void* scratch, cudaStream_t stream);
 
 /* ======================================================================== */
 /* SAMU forward without allocation                                           */

@@ -28,6 +28,7 @@ LRS_TRANSITION_CLOSED_FORM = 1
 # names and argument kinds of every exported symbol (checked by the tests)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZP = ctypes.POINTER(ctypes.c_size_t)
 _SIGNATURES = {
     "lrs_status_string": ([_I], ctypes.c_char_p),
@@ -60,6 +61,9 @@ _SIGNATURES = {
     "rglru_block_workspace_bytes": ([_I] * 4 + [_SZP, _SZP], _I),
     "rglru_block_forward": ([_P] * 4 + [_I] * 4 + [_P] * 5, _I),
     "rglru_block_backward": ([_P] * 6 + [_I] * 4 + [_P] * 6, _I),
+    "linear_ce_workspace_bytes": ([_I] * 4 + [_SZP, _SZP], _I),
+    "linear_ce_forward": ([_P] * 3 + [_I] * 3 + [_F] + [_P] * 5, _I),
+    "linear_ce_backward": ([_P] * 6 + [_I] * 3 + [_F] + [_P] * 2 + [_I] + [_P] * 2, _I),
 }
 
 # samu_block_params / samu_block_grads (include/samu.h): one pointer per field, in order
@@ -596,6 +600,78 @@ def dense_gemm(layout: int, A, B, M: int, N: int, K: int, *, out=None, scratch=N
     return C
 
 
+# ---------------------------------------------------------------------------
+# Softmax cross entropy over a vocabulary
+# ---------------------------------------------------------------------------
+def linear_ce_workspace_bytes(T: int, V: int, D: int, grad_fp32: bool = False):
+    """(forward, backward) scratch bytes of the vocabulary loss."""
+    f = ctypes.c_size_t(0)
+    b = ctypes.c_size_t(0)
+    _check("linear_ce_workspace_bytes",
+           _load().linear_ce_workspace_bytes(T, V, D, LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16, ctypes.byref(f),
+                                             ctypes.byref(b)))
+    return int(f.value), int(b.value)
+
+
+def _ce_inputs(h, w, target):
+    dev = h.device
+    V, D = w.shape
+    T = h.numel() // D if D else 0
+    if h.dim() < 1 or h.shape[-1] != D:
+        raise ValueError(f"h: expected shape (..., {D}), got {tuple(h.shape)}")
+    _need(h, "h", torch.bfloat16, dev)
+    _need(w, "w", torch.bfloat16, dev)
+    _need(target, "target", torch.int64, dev, h.shape[:-1])
+    return dev, T, V, D
+
+
+def linear_ce_forward(h, w, target, *, softcap=0.0, out=None, scratch=None):
+    """Softmax cross entropy of the logits h w^T through ``linear_ce_forward``.
+
+    h: [..., D] BF16, w: [V, D] BF16, target: [...] int64 (negative: not counted); softcap c > 0 caps the logits
+    to c tanh(z / c).  Returns dict(loss, lse (h's leading shape, FP32), total ([sum of losses, tokens counted]),
+    scratch)."""
+    dev, T, V, D = _ce_inputs(h, w, target)
+    nscratch = linear_ce_workspace_bytes(T, V, D)[0]
+    loss = _empty(target.shape, torch.float32, dev, out, "loss")
+    lse = _empty(target.shape, torch.float32, dev, out, "lse")
+    total = _empty((2,), torch.float32, dev, out, "total")
+    if scratch is None:
+        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    if scratch.numel() < nscratch:
+        raise ValueError("scratch buffer is too small")
+    _check("linear_ce_forward", _load().linear_ce_forward(_ptr(h), _ptr(w), _ptr(target), T, V, D, softcap, _ptr(loss),
+                                                          _ptr(lse), _ptr(total), _ptr(scratch), _stream(dev)))
+    return {"loss": loss, "lse": lse, "total": total, "scratch": scratch}
+
+
+def linear_ce_backward(h, w, target, lse, dloss=None, *, total=None, softcap=0.0, grad_fp32=False, out=None,
+                       scratch=None):
+    """Backward of linear_ce_forward (``linear_ce_backward``).
+
+    dloss: [...] FP32 cotangents of the losses, or None for their mean over the tokens counted (then ``total`` is
+    the forward's).  Returns dict(dh, dw, scratch), BF16 or (grad_fp32) FP32."""
+    dev, T, V, D = _ce_inputs(h, w, target)
+    _need(lse, "lse", torch.float32, dev, target.shape)
+    _opt(dloss, "dloss", torch.float32, dev, target.shape)
+    _opt(total, "total", torch.float32, dev, (2,))
+    if dloss is None and total is None:
+        raise ValueError("total is required where dloss is None")
+    nscratch = linear_ce_workspace_bytes(T, V, D, grad_fp32)[1]
+    gdt = torch.float32 if grad_fp32 else torch.bfloat16
+    dh = _empty(h.shape, gdt, dev, out, "dh")
+    dw = _empty(w.shape, gdt, dev, out, "dw")
+    if scratch is None:
+        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    if scratch.numel() < nscratch:
+        raise ValueError("scratch buffer is too small")
+    _check("linear_ce_backward",
+           _load().linear_ce_backward(_ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(total), T, V, D,
+                                      softcap, _ptr(dh), _ptr(dw), LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16,
+                                      _ptr(scratch), _stream(dev)))
+    return {"dh": dh, "dw": dw, "scratch": scratch}
+
+
 def block_tensors_from_numpy(inp: dict, device) -> dict:
     """Device tensors of synth.block_inputs: {"x", "dout", "h0", "dhT", "reset", "params": {...}}."""
     params = {}
@@ -639,7 +715,7 @@ KERNEL_NAMES = {
     10: "samu_fwd_maps_kernel", 11: "samu_bwd_maps_kernel", 12: "samu_decode_prepare_kernel",
     13: "samu_decode_step_kernel", 14: "proj_gemm_kernel<logits>", 15: "proj_gemm_kernel<dx, dW>",
     16: "proj_pack_kernel", 17: "block_gemm_kernel", 18: "rmsnorm_kernels", 19: "conv_kernels",
-    20: "join_fwd_kernel", 21: "sum_parts_kernel",
+    20: "join_fwd_kernel", 21: "sum_parts_kernel", 22: "ce_gemm_kernel", 23: "ce_rows_kernels",
 }
 
 

@@ -79,7 +79,8 @@ enum {
     KID_SAMU_CTRL_FWD = 2, KID_SAMU_SCAN_FWD, KID_SAMU_SCAN_BWD, KID_SAMU_CTRL_BWD,
     KID_SAMU_PARAMS, KID_RGLRU_SCAN_FWD, KID_RGLRU_SCAN_BWD, KID_RGLRU_ALPHA, KID_SAMU_FWD_MAPS,
     KID_SAMU_BWD_MAPS, KID_SAMU_DECODE_PREP, KID_SAMU_DECODE_STEP, KID_RGLRU_PROJ_FWD, KID_RGLRU_PROJ_BWD,
-    KID_RGLRU_PROJ_PACK, KID_BLOCK_GEMM, KID_BLOCK_NORM, KID_BLOCK_CONV, KID_BLOCK_JOIN, KID_BLOCK_SUM
+    KID_RGLRU_PROJ_PACK, KID_BLOCK_GEMM, KID_BLOCK_NORM, KID_BLOCK_CONV, KID_BLOCK_JOIN, KID_BLOCK_SUM, KID_CE_GEMM,
+    KID_CE_ROWS
 };
 
 #define LRS_LAUNCH(id, stream, expr)            \
@@ -203,7 +204,10 @@ int lrs_device_status(void* scratch, int* status, cudaStream_t stream) {
     if (e != cudaSuccess) return LRS_ERR_CUDA;
     e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return LRS_ERR_CUDA;
-    *status = (v & kStatusLayout) ? LRS_ERR_CUDA : (v & (kStatusTimeout | kStatusUpstream)) ? LRS_ERR_TIMEOUT : LRS_OK;
+    *status = (v & kStatusLayout)                        ? LRS_ERR_CUDA
+              : (v & (kStatusTimeout | kStatusUpstream)) ? LRS_ERR_TIMEOUT
+              : (v & kStatusTarget)                      ? LRS_ERR_ARG
+                                                         : LRS_OK;
     return LRS_OK;
 }
 
@@ -1061,6 +1065,212 @@ int lrs_dense_gemm(int layout, const void* A, const void* Bm, void* C, int M, in
         g.ldo = N;
     }
     LRS_LAUNCH(KID_BLOCK_GEMM, stream, launch_block_gemm(g, A, Bm, stream, false));
+    return LRS_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Softmax cross entropy over a vocabulary
+// ---------------------------------------------------------------------------
+namespace {
+
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+int check_ce_shape(int T, int V, int D) {
+    if (T < 1 || V < 1 || D < 1) return LRS_ERR_ARG;
+    if (D % 8 != 0) return LRS_ERR_UNSUPPORTED;
+    const long long lim = 1LL << 40;
+    if ((long long)T * D > lim || (long long)V * D > lim || (long long)V + 512 > 0x7fffffffLL ||
+        (long long)T + 512 > 0x7fffffffLL || (long long)ce_m_tiles(T) * ce_n_tiles(V) > 0x7fffffffLL ||
+        (long long)ce_m_tiles(V) * ce_n_tiles(D) > 0x7fffffffLL || (long long)ce_m_tiles(T) * ce_n_tiles(D) > 0x7fffffffLL)
+        return LRS_ERR_UNSUPPORTED;
+    return LRS_OK;
+}
+
+bool softcap_ok(float c) { return c >= 0.f && c <= 3e38f; }
+
+// The forward's scratch.
+struct CeForward {
+    size_t stats, zt, sums, total;
+};
+CeForward ce_forward_layout(int T, int V) {
+    CeForward l;
+    l.stats = 256;
+    l.zt = l.stats + up256((size_t)2 * ce_n_tiles(V) * T * sizeof(float2));
+    l.sums = l.zt + up256((size_t)T * 4);
+    l.total = l.sums + up256((size_t)ce_row_ctas(T) * 16);
+    return l;
+}
+
+// The backward's: dz (and its remainders) of one piece of the vocabulary, and
+// the FP32 partial sums of dh and dw.
+struct CeBackward {
+    int piece;           // columns of a piece (a multiple of 256 unless there is one piece)
+    long long ldz;       // row stride of dz: a multiple of 8
+    int pieces;
+    size_t dz, dz2, dh, dw, total;
+};
+constexpr long long kCePieceBytes = 512LL << 20;
+
+CeBackward ce_backward_layout(int T, int V, int D, int fp32, int sms) {
+    CeBackward l;
+    const long long row = (long long)T * 2 * (fp32 ? 2 : 1);
+    const long long most = std::max(256LL, kCePieceBytes / row / 256 * 256);
+    const int pieces = (int)((V + most - 1) / most);
+    // pieces of about the same length
+    l.piece = pieces == 1 ? V : (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
+    l.pieces = (V + l.piece - 1) / l.piece;
+    l.ldz = (l.piece + 7) / 8 * 8;
+    const int sh = ce_splits(T, D, l.piece, sms), sw = ce_splits(l.piece, D, T, sms);
+    const size_t dz = up256((size_t)T * (size_t)l.ldz * 2);
+    l.dz = 256;
+    l.dz2 = l.dz + dz;
+    l.dh = l.dz2 + (fp32 ? dz : 0);
+    l.dw = l.dh + ((sh > 1 || (l.pieces > 1 && !fp32)) ? up256((size_t)sh * T * D * 4) : 0);
+    l.total = l.dw + (sw > 1 ? up256((size_t)sw * l.piece * D * 4) : 0);
+    return l;
+}
+
+}  // namespace
+
+extern "C" {
+
+int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forward_bytes, size_t* backward_bytes) {
+    const int st = check_ce_shape(T, V, D);
+    if (st != LRS_OK) return st;
+    if (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) return LRS_ERR_ARG;
+    if (forward_bytes != nullptr) *forward_bytes = ce_forward_layout(T, V).total;
+    if (backward_bytes != nullptr)
+        *backward_bytes = ce_backward_layout(T, V, D, grad_dtype == LRS_GRAD_FP32, kBlockSmsBound).total;
+    return LRS_OK;
+}
+
+int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T, int V, int D, float softcap,
+                      float* loss, float* lse, float* total, void* scratch, cudaStream_t stream) {
+    const int st = check_ce_shape(T, V, D);
+    if (st != LRS_OK) return st;
+    if (!softcap_ok(softcap) || !req(h) || !req(w) || !req(target) || !req(loss) || !req(lse) || !req(total) ||
+        !req(scratch))
+        return LRS_ERR_ARG;
+    const CeForward l = ce_forward_layout(T, V);
+    uint32_t* status = at<uint32_t>(scratch, 0);
+    if (cudaMemsetAsync(status, 0, 16, stream) != cudaSuccess) return LRS_ERR_CUDA;
+    CeGemmArgs g = {};
+    g.layout = kBgNT;
+    g.epi = kCeStats;
+    g.M = T;
+    g.N = V;
+    g.K = D;
+    g.parts = 1;
+    g.stats = at<float2>(scratch, l.stats);
+    g.zt = at<float>(scratch, l.zt);
+    g.target = target;
+    g.V = V;
+    g.softcap = softcap;
+    g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
+    g.status = status;
+    LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_gemm(g, h, nullptr, D, w, V, nullptr, nullptr, 0, 0, stream, false));
+    LRS_LAUNCH(KID_CE_ROWS, stream,
+               launch_ce_rows(g.stats, g.zt, target, 2 * ce_n_tiles(V), T, V, loss, lse, at<double>(scratch, l.sums),
+                              total, status + 1, status, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+int linear_ce_backward(const void* h, const void* w, const int64_t* target, const float* lse, const float* dloss,
+                       const float* total, int T, int V, int D, float softcap, void* dh, void* dw, int grad_dtype,
+                       void* scratch, cudaStream_t stream) {
+    const int st = check_ce_shape(T, V, D);
+    if (st != LRS_OK) return st;
+    if (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) return LRS_ERR_ARG;
+    if (!softcap_ok(softcap) || !req(h) || !req(w) || !req(target) || !req(lse) || !opt(dloss) || !opt(total) ||
+        (dloss == nullptr && total == nullptr) || !req(dh) || !req(dw) || !req(scratch))
+        return LRS_ERR_ARG;
+    const int fp32 = grad_dtype == LRS_GRAD_FP32 ? 1 : 0;
+    const CeBackward l = ce_backward_layout(T, V, D, fp32, kBlockSmsBound);
+    const int sms = block_gemm_sms();
+    uint32_t* status = at<uint32_t>(scratch, 0);
+    void* dz = at<void>(scratch, l.dz);
+    void* dz2 = fp32 ? at<void>(scratch, l.dz2) : nullptr;
+    if (cudaMemsetAsync(status, 0, 16, stream) != cudaSuccess) return LRS_ERR_CUDA;
+    // the same splits for every piece (the last may be shorter)
+    const int h_splits = ce_splits(T, D, l.piece, sms), w_splits = ce_splits(l.piece, D, T, sms);
+    // dh adds over the pieces (and the splits of a piece) in FP32
+    const bool h_part = h_splits > 1 || (l.pieces > 1 && !fp32);
+    float* hp = h_part ? at<float>(scratch, l.dh) : static_cast<float*>(dh);
+    for (int i = 0; i < l.pieces; ++i) {
+        const int v0 = i * l.piece, nv = std::min(l.piece, V - v0);
+        CeGemmArgs g = {};
+        g.layout = kBgNT;
+        g.epi = fp32 ? kCeDz2 : kCeDz;
+        g.M = T;
+        g.N = nv;
+        g.K = D;
+        g.parts = 1;
+        g.b_row = v0;
+        g.s_cols = (int)l.ldz;
+        g.target = target;
+        g.V = V;
+        g.dloss = dloss;
+        g.total = total;
+        g.lse = lse;
+        g.softcap = softcap;
+        g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
+        g.status = status;
+        LRS_LAUNCH(KID_CE_GEMM, stream,
+                   launch_ce_gemm(g, h, nullptr, D, w, V, dz, dz2, T, l.ldz, stream, i > 0 && pdl_ok()));
+        // dh (+)= dz w
+        CeGemmArgs d = {};
+        d.layout = kBgNN;
+        d.M = T;
+        d.N = D;
+        d.K = nv;
+        d.parts = fp32 ? 2 : 1;
+        d.b_row = v0;
+        d.status = status;
+        if (h_part || fp32) {
+            d.epi = kCeF32;
+            d.splits = std::min(h_splits, (nv + 63) / 64);
+            d.part = hp;
+            d.part_rows = T;
+            d.accumulate = i > 0;
+            LRS_LAUNCH(KID_CE_GEMM, stream,
+                       launch_ce_gemm(d, dz, dz2, l.ldz, w, V, nullptr, nullptr, 0, 0, stream, pdl_ok()));
+        } else {
+            d.epi = kCeStore;
+            d.s_cols = D;
+            LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_gemm(d, dz, dz2, l.ldz, w, V, dh, nullptr, T, D, stream, pdl_ok()));
+        }
+        // dw's rows of this piece = dz^T h
+        CeGemmArgs e = {};
+        e.layout = kBgTN;
+        e.M = nv;
+        e.N = D;
+        e.K = T;
+        e.parts = fp32 ? 2 : 1;
+        e.status = status;
+        e.splits = w_splits;
+        const size_t at0 = (size_t)v0 * D;
+        if (e.splits > 1 || fp32) {
+            e.epi = kCeF32;
+            e.part = e.splits > 1 ? at<float>(scratch, l.dw) : static_cast<float*>(dw) + at0;
+            e.part_rows = nv;
+            LRS_LAUNCH(KID_CE_GEMM, stream,
+                       launch_ce_gemm(e, dz, dz2, l.ldz, h, T, nullptr, nullptr, 0, 0, stream, pdl_ok()));
+            if (e.splits > 1)
+                LRS_LAUNCH(KID_CE_ROWS, stream,
+                           launch_ce_sum(e.part, (long long)nv * D, e.splits, (long long)nv * D,
+                                         static_cast<char*>(dw) + at0 * (fp32 ? 4 : 2), fp32, stream, pdl_ok()));
+        } else {
+            e.epi = kCeStore;
+            e.s_row = v0;
+            e.s_cols = D;
+            LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_gemm(e, dz, dz2, l.ldz, h, T, dw, nullptr, V, D, stream, pdl_ok()));
+        }
+    }
+    if (h_part)
+        LRS_LAUNCH(KID_CE_ROWS, stream,
+                   launch_ce_sum(hp, (long long)T * D, h_splits, (long long)T * D, dh, fp32, stream, pdl_ok()));
     return LRS_OK;
 }
 

@@ -1,0 +1,611 @@
+// Softmax cross entropy over a large vocabulary without keeping the logits:
+// the contractions, on the fifth-generation tensor cores (sm_103a).
+//
+// With hidden states h [T][D], the head w [V][D] and z = h w^T, forward and
+// backward are three contractions around row-wise softmax statistics:
+//   NT  z = h w^T        a tile of logits lives in tensor memory only; the
+//                        epilogue leaves (max, sum of exponentials) of each
+//                        row's 128 columns (forward), or
+//                        dz = dloss (e^{z - lse} - [v = target]) (backward),
+//                        the latter for one piece of the vocabulary at a time;
+//   NN  dh = dz w        A = dz [T][piece] K-major, B = w's rows as K index;
+//   TN  dw = dz^T h      both operands MN-major, the tokens as K index.
+// Unlike the block's contractions (block_gemm.cu) every extent may be ragged:
+// the TMA fills what lies outside a matrix with zeros and clips what is stored
+// there; columns past the vocabulary are zeroed in dz.
+//
+// Roles as in the block's contractions: warp 8 streams 64-wide K slices of
+// both operands by TMA (128-byte swizzle) into a ring of four stages, one
+// thread of warp 9 issues tcgen05.mma (M 128, N 256, K 16), warps 0-7 drain
+// the accumulators, two of which alternate so that a tile's epilogue runs
+// under the next tile's MMAs.  Every wait is bounded.
+#include <algorithm>
+
+#include "kernels.cuh"
+#include "tmap.cuh"
+#include "umma.cuh"
+
+namespace lrs {
+
+namespace {
+
+constexpr int kCeEpiWarps = 8;
+constexpr int kCeThreads = 32 * (kCeEpiWarps + 2);
+constexpr int kCeProducer = kCeEpiWarps, kCeIssuer = kCeEpiWarps + 1;
+constexpr int kCeK = 64;
+constexpr int kCeM = 128;
+constexpr int kCeN = 256;
+constexpr int kCeStages = 4;      // ring stages (3 where dz's remainders are staged too)
+constexpr uint32_t kCeABytes = kCeM * 128;
+constexpr uint32_t kCeBBytes = kCeN * 128;
+constexpr uint32_t kCeStageBytes = kCeABytes + kCeBBytes;
+constexpr uint32_t kCeTmemCols = 2 * kCeN;
+constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store box (64-byte swizzle)
+// Staging of the BF16 stores: two alternating boxes per epilogue warp, or two
+// pairs (leading part and remainder).
+__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) {
+    return epi == kCeDz2 ? 4 * kCeBox : (epi == kCeDz || epi == kCeStore) ? 2 * kCeBox : 0u;
+}
+__host__ __device__ constexpr int ce_stages(int epi) { return epi == kCeDz2 ? kCeStages - 1 : kCeStages; }
+constexpr size_t ce_smem(int epi) {
+    return (size_t)ce_stages(epi) * kCeStageBytes + (size_t)kCeEpiWarps * ce_stage_warp(epi) + 1024;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]), f2_to_bf2(v[4], v[5]), f2_to_bf2(v[6], v[7]));
+}
+
+struct CeItem {
+    int mt, nt, s, k0, k1;
+};
+
+// Work item i.  NT: m runs fastest inside a group of row tiles whose h stays
+// in the L2, so that a tile of w is read by the whole group at about the same
+// time.  NN, TN: n (the width D) runs fastest, so that the D tiles that read
+// the same panel of dz run together.
+__device__ __forceinline__ CeItem ce_item(const CeGemmArgs& a, int i) {
+    CeItem it;
+    if (a.layout == kBgNT) {
+        const int per = a.group * a.n_tiles;
+        const int g = i / per, r = i - g * per;
+        const int gm = min(a.group, a.m_tiles - g * a.group);
+        it.mt = g * a.group + r % gm;
+        it.nt = r / gm;
+        it.s = 0;
+    } else {
+        it.nt = i % a.n_tiles;
+        const int r = i / a.n_tiles;
+        it.mt = r % a.m_tiles;
+        it.s = r / a.m_tiles;
+    }
+    it.k0 = (int)((long long)a.ksteps * it.s / a.splits);
+    it.k1 = (int)((long long)a.ksteps * (it.s + 1) / a.splits);
+    return it;
+}
+
+// The capped logit and its slope: z' = c tanh(z / c), dz'/dz = 1 - (z'/c)^2.
+__device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a.softcap * tanhf(z * a.inv_softcap); }
+
+// Forward epilogue of one row: (max, sum e^{z - max}) of its 128 columns.
+// Columns past the vocabulary do not count; the target's logit is kept.
+template <bool CAP>
+__device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& it, int row, uint32_t taddr, int half) {
+    const int t = it.mt * kCeM + row;
+    const int c0 = half * (kCeN / 2);
+    const int v0 = it.nt * kCeN + c0;            // vocabulary index of the first column
+    const int nv = min(kCeN / 2, a.N - v0);      // columns that count (may be <= 0)
+    const bool ok = t < a.M;
+    long long tgt = -1;
+    if (ok) tgt = a.target[t] - v0;
+    float mx = -INFINITY, sum = 0.f;
+    for (int c = 0; c < kCeN / 2; c += 32) {
+        float v[2][16];
+        tmem_ld16x2(taddr + (uint32_t)(c0 + c), taddr + (uint32_t)(c0 + c + 16), v[0], v[1]);
+        if (!ok || c >= nv) continue;
+        float z[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = CAP ? ce_cap(a, v[j / 16][j % 16]) : v[j / 16][j % 16];
+        if (tgt >= c && tgt < c + 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (tgt == c + j) a.zt[t] = z[j];
+        }
+        if (nv - c < 32) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (c + j >= nv) z[j] = -INFINITY;
+        }
+        float m = z[0];
+#pragma unroll
+        for (int j = 1; j < 32; ++j) m = fmaxf(m, z[j]);
+        m = fmaxf(m, mx);
+        const float ref = m == -INFINITY ? 0.f : m;   // every logit so far is -inf: e^{-inf - 0} = 0
+        const float off = -ref * kLog2e;
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) s += ex2_approx(fmaf(z[j], kLog2e, off));
+        sum = fmaf(sum, ex2_approx(fmaf(mx, kLog2e, off)), s);
+        mx = m;
+    }
+    if (ok) a.stats[(size_t)(2 * it.nt + half) * a.M + t] = make_float2(mx, sum);
+}
+
+template <int LAYOUT, int EPI, bool CAP>
+__global__ void __launch_bounds__(kCeThreads, 1)
+    ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a2,
+                   const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_s,
+                   const __grid_constant__ CUtensorMap tm_s2, const CeGemmArgs a) {
+    constexpr int S = ce_stages(EPI);
+    extern __shared__ uint8_t ce_raw[];
+    __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_acc[2], s_free[2], s_fin;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ce_raw) + 1023u) & ~uintptr_t(1023));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_acc[i], 1);
+            mbar_init(&s_free[i], kCeEpiWarps);
+        }
+        mbar_init(&s_fin, 1);
+        s_abort = 0;
+    }
+    if (warp == kCeIssuer) {
+        tmem_alloc(&s_tmem, kCeTmemCols);
+        tmem_fence_before_sync();
+    }
+    pdl_trigger();
+    pdl_wait();
+    __syncthreads();
+    tmem_fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    volatile int* abort_flag = &s_abort;
+    auto fail = [&]() {
+        *abort_flag = 1;
+        atomicOr(a.status, kStatusTimeout);
+    };
+    const int w0 = (int)blockIdx.x, wstep = (int)gridDim.x;
+
+    if (warp == kCeProducer) {
+        if (lane == 0) {
+            uint32_t n = 0;
+            for (int w = w0; w < a.n_items && !*abort_flag; w += wstep) {
+                const CeItem it = ce_item(a, w);
+                for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
+                    const int slot = (int)(n % S);
+                    if (n >= (uint32_t)S && !mbar_wait_bounded(&s_empty[slot], ((n / S) - 1) & 1u)) {
+                        fail();
+                        break;
+                    }
+                    if (*abort_flag) break;
+                    uint8_t* sa = ring + (size_t)slot * kCeStageBytes;
+                    uint8_t* sb = sa + kCeABytes;
+                    // the remainders of dz follow its leading parts along K
+                    const bool second = a.parts == 2 && ks >= a.part_steps;
+                    const int k0 = kCeK * (second ? ks - a.part_steps : ks);
+                    const CUtensorMap* ta = second ? &tm_a2 : &tm_a;
+                    mbar_arrive_expect_tx(&s_full[slot], kCeStageBytes);
+                    if (LAYOUT == kBgNT) {
+                        tma_load_2d(sa, ta, k0, it.mt * kCeM, &s_full[slot]);
+                        tma_load_2d(sb, &tm_b, k0, a.b_row + it.nt * kCeN, &s_full[slot]);
+                        tma_load_2d(sb + kCeBBytes / 2, &tm_b, k0, a.b_row + it.nt * kCeN + 128, &s_full[slot]);
+                    } else {
+                        if (LAYOUT == kBgNN) {
+                            tma_load_2d(sa, ta, k0, it.mt * kCeM, &s_full[slot]);
+                        } else {
+                            tma_load_2d(sa, ta, it.mt * kCeM, k0, &s_full[slot]);
+                            tma_load_2d(sa + 8192, ta, it.mt * kCeM + 64, k0, &s_full[slot]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < kCeN / 64; ++j)
+                            tma_load_2d(sb + (size_t)j * 8192, &tm_b, it.nt * kCeN + 64 * j, a.b_row + k0,
+                                        &s_full[slot]);
+                    }
+                }
+            }
+            // copies still in flight land before the CTA may exit
+            const uint32_t lo = n > (uint32_t)S ? n - S : 0;
+            for (uint32_t j = lo; j < n; ++j) mbar_wait_bounded(&s_full[j % S], (j / S) & 1u);
+        }
+    } else if (warp == kCeIssuer) {
+        if (lane == 0) {
+            constexpr uint32_t idesc = umma_idesc_bf16(kCeM, kCeN) | (LAYOUT == kBgTN ? (1u << 15) : 0u) |
+                                       (LAYOUT != kBgNT ? (1u << 16) : 0u);
+            uint32_t n = 0, item = 0;
+            for (int w = w0; w < a.n_items && !*abort_flag; w += wstep, ++item) {
+                const CeItem it = ce_item(a, w);
+                const uint32_t buf = item & 1u;
+                if (item >= 2 && !mbar_wait_bounded(&s_free[buf], ((item >> 1) - 1) & 1u)) {
+                    fail();
+                    break;
+                }
+                tmem_fence_after_sync();
+                const uint32_t acc_t = tmem + buf * (uint32_t)kCeN;
+                bool ok = true;
+                for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
+                    const int slot = (int)(n % S);
+                    if (!mbar_wait_bounded(&s_full[slot], (n / S) & 1u)) {
+                        fail();
+                        ok = false;
+                        break;
+                    }
+                    tmem_fence_after_sync();
+                    const uint32_t sa = smem_u32(ring + (size_t)slot * kCeStageBytes);
+                    const uint32_t sb = sa + kCeABytes;
+#pragma unroll
+                    for (int kk = 0; kk < kCeK / 16; ++kk) {
+                        const uint64_t da = LAYOUT == kBgTN ? umma_desc_sw128_mn(sa + 2048u * kk, 8192u)
+                                                            : umma_desc_sw128(sa + 32u * kk);
+                        const uint64_t db = LAYOUT == kBgNT ? umma_desc_sw128(sb + 32u * kk)
+                                                            : umma_desc_sw128_mn(sb + 2048u * kk, 8192u);
+                        umma_bf16(acc_t, da, db, idesc, ks > it.k0 || kk > 0);
+                    }
+                    umma_commit(&s_empty[slot]);
+                }
+                if (!ok) break;
+                umma_commit(&s_acc[buf]);
+            }
+            umma_commit(&s_fin);
+            mbar_wait_bounded(&s_fin, 0);
+        }
+    } else {
+        // epilogue warps: rows 32 (warp % 4) .. + 31 of the tile, column half warp / 4
+        const int q4 = warp & 3, hf = warp >> 2;
+        const int row = 32 * q4 + lane;
+        uint8_t* stg = ring + (size_t)S * kCeStageBytes + (size_t)warp * ce_stage_warp(EPI);
+        uint32_t chunk = 0, item = 0;
+        for (int w = w0; w < a.n_items && !*abort_flag; w += wstep, ++item) {
+            const CeItem it = ce_item(a, w);
+            const uint32_t buf = item & 1u;
+            // what a row needs besides its logits is fetched while the tile is computed
+            float wgt = 0.f, lse2 = 0.f;
+            long long tgt = -1;
+            if (EPI == kCeDz || EPI == kCeDz2) {
+                const int t = it.mt * kCeM + row;
+                if (t < a.M) {
+                    const long long tg = a.target[t];
+                    tgt = tg - a.b_row - (long long)it.nt * kCeN;
+                    // a row without a valid target adds nothing to the gradients
+                    if (tg >= 0 && tg < a.V) wgt = a.dloss != nullptr ? a.dloss[t] : 1.f / a.total[1];
+                    lse2 = a.lse[t] * kLog2e;
+                }
+            }
+            if (!mbar_wait_bounded(&s_acc[buf], (item >> 1) & 1u)) {
+                if (lane == 0) fail();
+                break;
+            }
+            tmem_fence_after_sync();
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + buf * (uint32_t)kCeN;
+            if (EPI == kCeStats) {
+                ce_epi_stats<CAP>(a, it, row, taddr, hf);
+            } else if (EPI == kCeF32) {
+                const long long r = (long long)it.mt * kCeM + row;
+                float* o = a.part + ((size_t)it.s * a.part_rows + (size_t)r) * a.N + (size_t)it.nt * kCeN;
+                for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
+                    float v[2][16];
+                    tmem_ld16x2(taddr + (uint32_t)c, taddr + (uint32_t)(c + 16), v[0], v[1]);
+                    if (r >= a.M) continue;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        if (it.nt * kCeN + c + j >= a.N) continue;
+                        float4 x = make_float4(v[j / 16][j % 16], v[j / 16][j % 16 + 1], v[j / 16][j % 16 + 2],
+                                               v[j / 16][j % 16 + 3]);
+                        float4* p = reinterpret_cast<float4*>(o + c + j);
+                        if (a.accumulate) {
+                            const float4 y = *p;
+                            x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+                        }
+                        *p = x;
+                    }
+                }
+            } else {
+                // BF16 results by TMA stores from swizzled staging, 32 columns at a time
+                constexpr int kBoxes = EPI == kCeDz2 ? 2 : 1;
+                const int y = a.s_row + it.mt * kCeM + 32 * q4;
+                const bool store = it.mt * kCeM + 32 * q4 < a.M;   // rows past the matrix are clipped by the TMA
+                const int nv = a.N - it.nt * kCeN;                 // columns of this tile inside the matrix
+#pragma unroll 1
+                for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32, ++chunk) {
+                    float v[2][16], lo[2][16];
+                    tmem_ld16x2(taddr + (uint32_t)c, taddr + (uint32_t)(c + 16), v[0], v[1]);
+                    if (EPI == kCeDz || EPI == kCeDz2) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            float z = v[j / 16][j % 16], slope = 1.f;
+                            if (CAP) {
+                                const float th = tanhf(z * a.inv_softcap);
+                                z = a.softcap * th;
+                                slope = fmaf(-th, th, 1.f);
+                            }
+                            float e = ex2_approx(fmaf(z, kLog2e, -lse2));
+                            if (tgt == c + j) e -= 1.f;
+                            e *= wgt;
+                            if (CAP) e *= slope;
+                            if (c + j >= nv) e = 0.f;
+                            v[j / 16][j % 16] = e;
+                            if (EPI == kCeDz2) lo[j / 16][j % 16] = e - __bfloat162float(__float2bfloat16_rn(e));
+                        }
+                        // a row without a weight has exact zeros (its lse may be anything)
+                        if (wgt == 0.f) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = lo[j / 16][j % 16] = 0.f;
+                        }
+                    }
+                    uint8_t* box = stg + (size_t)(chunk & 1u) * kBoxes * kCeBox;
+                    if (lane == 0 && chunk >= 2) bulk_wait_read<1>();
+                    __syncwarp();
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int pu = u ^ ((lane >> 1) & 3);
+                        *reinterpret_cast<uint4*>(box + (size_t)lane * 64 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
+                        if (EPI == kCeDz2)
+                            *reinterpret_cast<uint4*>(box + kCeBox + (size_t)lane * 64 + 16 * pu) =
+                                pack8(lo[u >> 1] + 8 * (u & 1));
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (store && it.nt * kCeN + c < a.s_cols) {
+                            tma_store_2d(&tm_s, it.nt * kCeN + c, y, box);
+                            if (EPI == kCeDz2) tma_store_2d(&tm_s2, it.nt * kCeN + c, y, box + kCeBox);
+                        }
+                        bulk_commit();
+                    }
+                }
+            }
+            tmem_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_free[buf]);
+        }
+        if (lane == 0) bulk_wait_all();   // every store has completed before the CTA may exit
+    }
+    __syncthreads();
+    if (warp == kCeIssuer) {
+        tmem_fence_after_sync();
+        tmem_dealloc(tmem, kCeTmemCols);
+    }
+}
+
+// (m, s) of a row over two sets of columns.
+__device__ __forceinline__ float2 ce_join(float2 p, float2 q) {
+    const float m = fmaxf(p.x, q.x);
+    const float ref = m == -INFINITY ? 0.f : m;
+    return make_float2(m, p.y * ex2_approx((p.x - ref) * kLog2e) + q.y * ex2_approx((q.x - ref) * kLog2e));
+}
+
+// Rows' statistics joined over their `parts` column blocks, in a fixed order:
+// a CTA takes kCeRows consecutive rows, thread (row, group) the parts group,
+// group + kCeGroups, ...; then lse, loss, and the CTA's (sum of losses, number
+// of rows counted).  The last CTA to finish adds the CTAs' sums in order.
+// A target outside [0, V) is not counted; one past V sets the status word.
+template <int ROWS>
+__global__ void __launch_bounds__(256) ce_rows_kernel(const float2* __restrict__ stats, const float* __restrict__ zt,
+                                                      const int64_t* __restrict__ target, int parts, int T, int V,
+                                                      float* __restrict__ loss, float* __restrict__ lse,
+                                                      double* __restrict__ sums, float* __restrict__ total,
+                                                      uint32_t* ticket, uint32_t* status) {
+    constexpr int GROUPS = 256 / ROWS;
+    __shared__ float2 red[GROUPS][ROWS];
+    __shared__ double tot[2][8];
+    __shared__ bool last;
+    pdl_trigger();
+    pdl_wait();
+    const int r = threadIdx.x % ROWS, g = threadIdx.x / ROWS;
+    const int t = blockIdx.x * ROWS + r;
+    float2 p = make_float2(-INFINITY, 0.f);
+    if (t < T)
+        for (int i = g; i < parts; i += GROUPS) p = ce_join(p, __ldcg(stats + (size_t)i * T + t));
+    red[g][r] = p;
+    __syncthreads();
+    for (int k = GROUPS / 2; k >= 1; k >>= 1) {
+        if (g < k) red[g][r] = ce_join(red[g][r], red[g + k][r]);
+        __syncthreads();
+    }
+    double sl = 0., sc = 0.;
+    if (g == 0 && t < T) {
+        p = red[0][r];
+        const float l = p.x + logf(p.y);
+        const long long tg = target[t];
+        const bool counted = tg >= 0 && tg < V;
+        if (tg >= V) atomicOr(status, kStatusTarget);
+        const float ls = counted ? l - __ldcg(zt + t) : 0.f;
+        lse[t] = l;
+        loss[t] = ls;
+        sl = ls;
+        sc = counted ? 1. : 0.;
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        sl += __shfl_xor_sync(0xffffffffu, sl, o);
+        sc += __shfl_xor_sync(0xffffffffu, sc, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        tot[0][threadIdx.x >> 5] = sl;
+        tot[1][threadIdx.x >> 5] = sc;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sl = sc = 0.;
+        for (int i = 0; i < 8; ++i) {
+            sl += tot[0][i];
+            sc += tot[1][i];
+        }
+        sums[2 * blockIdx.x] = sl;
+        sums[2 * blockIdx.x + 1] = sc;
+        __threadfence();
+        last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    sl = sc = 0.;
+    for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) {
+        sl += __ldcg(sums + 2 * i);
+        sc += __ldcg(sums + 2 * i + 1);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        sl += __shfl_xor_sync(0xffffffffu, sl, o);
+        sc += __shfl_xor_sync(0xffffffffu, sc, o);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        tot[0][threadIdx.x >> 5] = sl;
+        tot[1][threadIdx.x >> 5] = sc;
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sl = sc = 0.;
+        for (int i = 0; i < 8; ++i) {
+            sl += tot[0][i];
+            sc += tot[1][i];
+        }
+        total[0] = (float)sl;
+        total[1] = (float)sc;
+        *ticket = 0u;
+    }
+}
+
+// out[i] = sum of part[p][i] over p in order, as FP32 or BF16; n a multiple of 4.
+template <bool F32>
+__global__ void __launch_bounds__(256) ce_sum_kernel(const float4* __restrict__ part, long long stride4, int parts,
+                                                     long long n4, void* __restrict__ out) {
+    pdl_trigger();
+    pdl_wait();
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n4; i += (long long)gridDim.x * 256) {
+        float4 s = __ldcg(part + i);
+        for (int p = 1; p < parts; ++p) {
+            const float4 v = __ldcg(part + (size_t)p * stride4 + i);
+            s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+        }
+        if (F32)
+            static_cast<float4*>(out)[i] = s;
+        else
+            static_cast<uint2*>(out)[i] = make_uint2(f2_to_bf2(s.x, s.y), f2_to_bf2(s.z, s.w));
+    }
+}
+
+// 2-D map over a row-major BF16 matrix [rows][cols] with row stride ld.
+bool ce_map(CUtensorMap* map, const void* ptr, long long cols, long long rows, long long ld, int box_cols,
+            int box_rows, CUtensorMapSwizzle sw) {
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int LAYOUT, int EPI, bool CAP>
+cudaError_t ce_launch(const CUtensorMap& ta, const CUtensorMap& ta2, const CUtensorMap& tb, const CUtensorMap& ts,
+                      const CUtensorMap& ts2, const CeGemmArgs& a, cudaStream_t s, bool pdl) {
+    auto* fn = ce_gemm_kernel<LAYOUT, EPI, CAP>;
+    constexpr size_t smem = ce_smem(EPI);
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int grid = std::min(block_gemm_sms(), a.n_items);
+    return launch_ex(fn, dim3((unsigned)grid), dim3(kCeThreads), smem, s, pdl, ta, ta2, tb, ts, ts2, a);
+}
+
+}  // namespace
+
+int ce_m_tiles(long long M) { return (int)((M + kCeM - 1) / kCeM); }
+int ce_n_tiles(long long N) { return (int)((N + kCeN - 1) / kCeN); }
+
+// Splits of the K axis when a contraction has fewer tiles than the GPU has
+// SMs: as many as fill the SMs, each at least four K steps long.
+int ce_splits(long long M, long long N, long long K, int sms) {
+    const long long tiles = (long long)ce_m_tiles(M) * ce_n_tiles(N), steps = (K + kCeK - 1) / kCeK;
+    return (int)std::max(1LL, std::min<long long>({sms / tiles, steps / 4, kCeSplitsMax}));
+}
+
+// A [M][K] (NT, NN) or [K][M] (TN) with row stride lda; A2: its remainders
+// (parts = 2); B [brows][K] (NT) or [brows][N] (NN, TN), read from row
+// a.b_row on; S, S2: the BF16 result, [s_rows][s_cols] with row stride lds.
+cudaError_t launch_ce_gemm(const CeGemmArgs& in, const void* A, const void* A2, long long lda, const void* B,
+                           long long brows, void* S, void* S2, long long s_rows, long long lds, cudaStream_t s,
+                           bool pdl) {
+    CeGemmArgs a = in;
+    CUtensorMap ta, ta2, tb, ts, ts2;
+    const long long K = a.K;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    bool ok;
+    if (a.layout == kBgTN)
+        ok = ce_map(&ta, A, lda, K, lda, 64, 64, sw) && (a.parts == 1 || ce_map(&ta2, A2, lda, K, lda, 64, 64, sw));
+    else
+        ok = ce_map(&ta, A, lda, a.M, lda, 64, kCeM, sw) &&
+             (a.parts == 1 || ce_map(&ta2, A2, lda, a.M, lda, 64, kCeM, sw));
+    ok = ok && (a.layout == kBgNT ? ce_map(&tb, B, K, brows, K, 64, kCeN / 2, sw)
+                                  : ce_map(&tb, B, a.N, brows, a.N, 64, 64, sw));
+    if (!ok) return cudaErrorInvalidValue;
+    if (a.parts == 1) ta2 = ta;
+    ts = ts2 = ta;
+    if (S != nullptr && !ce_map(&ts, S, a.s_cols, s_rows, lds, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    if (S2 != nullptr && !ce_map(&ts2, S2, a.s_cols, s_rows, lds, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    a.m_tiles = ce_m_tiles(a.M);
+    a.n_tiles = ce_n_tiles(a.N);
+    a.part_steps = (int)((K + kCeK - 1) / kCeK);
+    a.ksteps = a.parts * a.part_steps;
+    if (a.splits < 1) a.splits = 1;
+    // 32 MB of h per group of row tiles
+    a.group = (int)std::max(1LL, std::min<long long>(a.m_tiles, (32LL << 20) / (K * 2 * kCeM)));
+    const long long items = (long long)a.m_tiles * a.n_tiles * a.splits;
+    if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
+    a.n_items = (int)items;
+    const bool cap = a.softcap > 0.f;
+    switch (a.layout * 16 + a.epi) {
+        case kBgNT * 16 + kCeStats:
+            return cap ? ce_launch<kBgNT, kCeStats, true>(ta, ta2, tb, ts, ts2, a, s, pdl)
+                       : ce_launch<kBgNT, kCeStats, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        case kBgNT * 16 + kCeDz:
+            return cap ? ce_launch<kBgNT, kCeDz, true>(ta, ta2, tb, ts, ts2, a, s, pdl)
+                       : ce_launch<kBgNT, kCeDz, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        case kBgNT * 16 + kCeDz2:
+            return cap ? ce_launch<kBgNT, kCeDz2, true>(ta, ta2, tb, ts, ts2, a, s, pdl)
+                       : ce_launch<kBgNT, kCeDz2, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        case kBgNN * 16 + kCeStore: return ce_launch<kBgNN, kCeStore, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        case kBgNN * 16 + kCeF32: return ce_launch<kBgNN, kCeF32, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        case kBgTN * 16 + kCeStore: return ce_launch<kBgTN, kCeStore, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        case kBgTN * 16 + kCeF32: return ce_launch<kBgTN, kCeF32, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// Rows per CTA of the statistics kernel: 32 (a warp reads 32 rows of one part),
+// or one when there are few rows and the parts are what there is to share out.
+int ce_row_ctas(int T) { return T <= 256 ? T : (T + 31) / 32; }
+
+cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
+                           float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
+                           cudaStream_t s, bool pdl) {
+    const dim3 grid((unsigned)ce_row_ctas(T));
+    if (T <= 256)
+        return launch_ex(ce_rows_kernel<1>, grid, dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse,
+                         sums, total, ticket, status);
+    return launch_ex(ce_rows_kernel<32>, grid, dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse, sums,
+                     total, ticket, status);
+}
+
+cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,
+                          cudaStream_t s, bool pdl) {
+    const long long blocks = std::max(1LL, std::min(8192LL, (n / 4 + 255) / 256));
+    const float4* p = reinterpret_cast<const float4*>(part);
+    if (f32)
+        return launch_ex(ce_sum_kernel<true>, dim3((unsigned)blocks), dim3(256), 0, s, pdl, p, stride / 4, parts, n / 4,
+                         out);
+    return launch_ex(ce_sum_kernel<false>, dim3((unsigned)blocks), dim3(256), 0, s, pdl, p, stride / 4, parts, n / 4,
+                     out);
+}
+
+}  // namespace lrs

@@ -39,6 +39,7 @@ constexpr uint64_t kWaitLimitNs = 200ull * 1000ull * 1000ull;
 constexpr uint32_t kStatusTimeout = 1u;
 constexpr uint32_t kStatusUpstream = 2u;
 constexpr uint32_t kStatusLayout = 4u;    // a shared-memory buffer missed its required alignment (nothing copied)
+constexpr uint32_t kStatusTarget = 8u;    // a target past the vocabulary
 
 // ---------------------------------------------------------------------------
 // Memory-model primitives (PTX).

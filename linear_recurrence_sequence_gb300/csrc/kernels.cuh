@@ -529,4 +529,47 @@ cudaError_t launch_conv_bwd(const void* gv, const float* k, const uint8_t* reset
 cudaError_t launch_join_fwd(const void* gv, const void* ym, void* j, long long BL, int D, uint32_t* status,
                             const uint32_t* mixer_status, cudaStream_t s, bool pdl);
 
+// ---------------------------------------------------------------------------
+// Softmax cross entropy over a vocabulary (ce_gemm.cu).
+// ---------------------------------------------------------------------------
+// Epilogues: (max, sum of exponentials) of a row's columns; dz in BF16; dz as
+// BF16 leading parts and remainders; plain BF16; FP32 (stored or added).
+enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz2 = 2, kCeStore = 3, kCeF32 = 4 };
+constexpr int kCeSplitsMax = 32;
+
+struct CeGemmArgs {
+    int layout, epi;             // BgLayoutKind, CeEpiKind
+    int M, N, K;
+    int parts;                   // 2: operand A comes as leading parts and remainders
+    int splits;                  // of K (kCeF32 only)
+    int b_row;                   // first row of B (NT, NN: the piece of the vocabulary)
+    int s_row, s_cols;           // BF16 result: first row, columns of the matrix that is stored to
+    int accumulate;              // kCeF32: add to part
+    float* part;                 // kCeF32: [splits][part_rows][N]
+    long long part_rows;
+    float2* stats;               // kCeStats: [2 n_tiles][M]
+    float* zt;                   // kCeStats: [M] the targets' logits
+    const int64_t* target;       // [M]
+    int V;
+    const float* dloss;          // kCeDz: [M], or null: 1 / total[1]
+    const float* total;
+    const float* lse;            // kCeDz: [M]
+    float softcap, inv_softcap;  // 0: none
+    uint32_t* status;
+    int m_tiles, n_tiles, ksteps, part_steps, group, n_items;   // filled by launch_ce_gemm
+};
+
+int ce_m_tiles(long long M);
+int ce_n_tiles(long long N);
+int ce_splits(long long M, long long N, long long K, int sms);
+cudaError_t launch_ce_gemm(const CeGemmArgs& a, const void* A, const void* A2, long long lda, const void* B,
+                           long long brows, void* S, void* S2, long long s_rows, long long lds, cudaStream_t s,
+                           bool pdl);
+int ce_row_ctas(int T);
+cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
+                           float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
+                           cudaStream_t s, bool pdl);
+cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,
+                          cudaStream_t s, bool pdl);
+
 }  // namespace lrs

@@ -109,7 +109,8 @@ int lrs_selftest_wait_timeout(void* scratch, cudaStream_t stream);
  * backward GEMMs, 16 RG-LRU weight packing and dW combination, 17 RecurrentBlock
  * contractions, 18 RecurrentBlock RMSNorm (forward and backward), 19 its
  * convolution, 20 its join, 21 its fixed-order gradient sums, 22 the vocabulary
- * loss's contractions, 23 its row statistics and sums; 9 also covers
+ * loss's contractions, 23 its row statistics and sums, 24 the gated norm, 25 its
+ * gradient sums, 26 AdamW's gradient norm, 27 its update; 9 also covers
  * the bias-gradient reductions) and duration in
  * milliseconds; *count receives the number of
  * kernels launched while profiling was on.  Not thread-safe: one profiling
@@ -501,6 +502,97 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
 int linear_ce_backward(const void* h, const void* w, const int64_t* target, const float* lse, const float* dloss,
                        const float* total, int T, int V, int D, float softcap, void* dh, void* dw, int grad_dtype,
                        void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Norms before and after a residual branch, with its gate and scale         */
+/* ======================================================================== */
+
+/* Joins a bare mixer to the residual stream and forms the next layer's input:
+ *   u = scale * GeLU(gate) * RMSNorm(y; gamma_post),  r = x + u,
+ *   h = RMSNorm(r; gamma_pre),   RMSNorm(a; g) = a / sqrt(mean(a^2) + eps) * g,
+ * row by row over [T,D], with the block's GeLU (tanh form).  FP32 arithmetic
+ * throughout; r and h are rounded to BF16 once (h is formed from the unrounded r).
+ * With y NULL there is no branch: h = RMSNorm(x; gamma_pre), the norm ahead of
+ * a head; gate, gamma_post, scale and r are then NULL too.
+ *
+ * Bytes of `saved` (the rows' two reciprocal norms) and `scratch` (the
+ * backward's partial sums).  Pure host function. */
+int gated_norm_workspace_bytes(int T, int D, size_t* saved_bytes, size_t* scratch_bytes);
+
+/* Forward.
+ *   x          [T,D] BF16 (in): the residual stream
+ *   y          [T,D] BF16 (in): the branch, or NULL
+ *   gate       [T,D] BF16 (in), or NULL for 1 in place of GeLU(gate)
+ *   gamma_post, scale, gamma_pre   [D] FP32 (in), or NULL for ones
+ *   eps        in (0, 1]
+ *   r          [T,D] BF16 (out);  h [T,D] BF16 (out)
+ *   saved      gated_norm_workspace_bytes().saved bytes (out), or NULL where no
+ *              backward follows
+ * One launch; a decoding step is T = the number of sequences.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, T or D < 1, eps out of
+ * range, a gate, gamma_post, scale or r without a branch), LRS_ERR_UNSUPPORTED
+ * (D not a multiple of 8, or D > 8192), LRS_ERR_CUDA. */
+int gated_norm_forward(const void* x, const void* y, const void* gate, const float* gamma_post, const float* scale,
+                       const float* gamma_pre, int T, int D, float eps, void* r, void* h, void* saved,
+                       cudaStream_t stream);
+
+/* Backward for the cotangents dr (or NULL for zero) and dh, [T,D] BF16.
+ *   x ... eps  the forward's (in);  saved: the forward's
+ *   dx, dy, dgate [T,D] BF16 (out);  dgamma_post, dscale, dgamma_pre [D] FP32
+ *              (out, in a fixed order of summation).  dy, dgamma_post, dscale
+ *              are NULL without a branch, dgate without a gate; the gradient of
+ *              a vector that was NULL (ones) is written all the same.
+ *   scratch    gated_norm_workspace_bytes().scratch bytes
+ * Errors: as the forward. */
+int gated_norm_backward(const void* dr, const void* dh, const void* x, const void* y, const void* gate,
+                        const float* gamma_post, const float* scale, const float* gamma_pre, int T, int D, float eps,
+                        const void* saved, void* dx, void* dy, void* dgate, float* dgamma_post, float* dscale,
+                        float* dgamma_pre, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* AdamW over many tensors                                                   */
+/* ======================================================================== */
+
+/* One parameter tensor of n values and its optimiser state (device pointers).
+ *   param   FP32, or BF16 if master is given (then the rounded copy that the
+ *           layers read; the FP32 master is what the step updates)
+ *   grad    FP32 or BF16 by grad_dtype (LRS_GRAD_*)
+ *   m, v    FP32 first and second moments; or, with m_scale and v_scale, E4M3
+ *           codes with one FP32 scale for every 256 consecutive values
+ *           (ceil(n / 256) of them): m = scale code, sqrt(v) = scale code, the
+ *           scale being the largest magnitude of the 256 divided by 448.  A
+ *           sqrt(v) above 0 never rounds to 0; 256 values below 2^-100 are
+ *           stored as zeros.  All of them start as zeros.
+ *   weight_decay  of this tensor */
+typedef struct {
+    void* param; float* master; const void* grad; void* m; void* v; float* m_scale; float* v_scale;
+    int64_t n; float weight_decay; int grad_dtype;
+} lrs_adamw_tensor;
+
+/* Scratch bytes of a step over `count` tensors.  Errors: LRS_ERR_ARG. */
+int lrs_adamw_scratch_bytes(int count, size_t* bytes);
+
+/* One AdamW step over every tensor of the list (a host array, read before the
+ * call returns):
+ *   t = step + 1;  N = sqrt(sum of g^2 over every tensor);
+ *   k = max_norm / N where N > max_norm > 0, else 1;
+ *   m = b1 m + (1 - b1) k g;  v = b2 v + (1 - b2) (k g)^2;
+ *   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps).
+ *   step      one int32 (device, in/out): steps taken so far
+ *   lr        one FP32 (device, in)
+ *   max_norm  0 for no clipping; otherwise a step whose N is not finite
+ *             changes nothing (parameters, states and step keep their values)
+ *   norm      one FP32 (device, out): N; may be NULL without clipping (then it
+ *             is not written)
+ *   scratch   lrs_adamw_scratch_bytes() bytes
+ * FP32 arithmetic, bias corrections in FP64, the norm in a fixed order of
+ * summation.  Everything that changes from step to step is on the device: a
+ * captured graph steps correctly.  Two launches for up to 400 tensors.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, n < 1, one scale without
+ * the other, a negative weight decay, betas outside [0, 1), eps <= 0),
+ * LRS_ERR_UNSUPPORTED (over 2^40 values), LRS_ERR_CUDA. */
+int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, const float* lr, double beta1,
+                   double beta2, float eps, float max_norm, float* norm, void* scratch, cudaStream_t stream);
 
 /* ======================================================================== */
 /* SAMU forward without allocation                                           */

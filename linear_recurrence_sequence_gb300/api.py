@@ -29,6 +29,7 @@ LRS_TRANSITION_CLOSED_FORM = 1
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_D = ctypes.c_double
 _SZP = ctypes.POINTER(ctypes.c_size_t)
 _SIGNATURES = {
     "lrs_status_string": ([_I], ctypes.c_char_p),
@@ -64,6 +65,11 @@ _SIGNATURES = {
     "linear_ce_workspace_bytes": ([_I] * 4 + [_SZP, _SZP], _I),
     "linear_ce_forward": ([_P] * 3 + [_I] * 3 + [_F] + [_P] * 5, _I),
     "linear_ce_backward": ([_P] * 6 + [_I] * 3 + [_F] + [_P] * 2 + [_I] + [_P] * 2, _I),
+    "gated_norm_workspace_bytes": ([_I, _I, _SZP, _SZP], _I),
+    "gated_norm_forward": ([_P] * 6 + [_I, _I, _F] + [_P] * 4, _I),
+    "gated_norm_backward": ([_P] * 8 + [_I, _I, _F] + [_P] * 9, _I),
+    "lrs_adamw_scratch_bytes": ([_I, _SZP], _I),
+    "lrs_adamw_step": ([_P, _I, _P, _P, _D, _D, _F, _F] + [_P] * 3, _I),
 }
 
 # samu_block_params / samu_block_grads (include/samu.h): one pointer per field, in order
@@ -672,6 +678,184 @@ def linear_ce_backward(h, w, target, lse, dloss=None, *, total=None, softcap=0.0
     return {"dh": dh, "dw": dw, "scratch": scratch}
 
 
+# ---------------------------------------------------------------------------
+# Norms before and after a residual branch, with its gate and scale
+# ---------------------------------------------------------------------------
+def gated_norm_workspace_bytes(T: int, D: int):
+    s = ctypes.c_size_t(0)
+    c = ctypes.c_size_t(0)
+    _check("gated_norm_workspace_bytes",
+           _load().gated_norm_workspace_bytes(T, D, ctypes.byref(s), ctypes.byref(c)))
+    return int(s.value), int(c.value)
+
+
+def _gated_norm_inputs(x, y, gate, gamma_post, scale, gamma_pre):
+    dev = x.device
+    if x.dim() < 1:
+        raise ValueError("x: expected shape (..., D)")
+    D = x.shape[-1]
+    _need(x, "x", torch.bfloat16, dev)
+    _opt(y, "y", torch.bfloat16, dev, x.shape)
+    _opt(gate, "gate", torch.bfloat16, dev, x.shape)
+    for t, n in ((gamma_post, "gamma_post"), (scale, "scale"), (gamma_pre, "gamma_pre")):
+        _opt(t, n, torch.float32, dev, (D,))
+    return dev, x.numel() // D if D else 0, D
+
+
+def gated_norm_forward(x, y=None, gate=None, gamma_post=None, scale=None, gamma_pre=None, *, eps=1e-6, out=None,
+                       saved=None):
+    """r = x + scale GeLU(gate) RMSNorm(y; gamma_post), h = RMSNorm(r; gamma_pre) through ``gated_norm_forward``.
+
+    x, y, gate: [..., D] BF16; the vectors [D] FP32; anything but x may be None (no gate, ones; without y no branch:
+    h = RMSNorm(x; gamma_pre) and r is x itself).  Returns dict(r, h, saved)."""
+    dev, T, D = _gated_norm_inputs(x, y, gate, gamma_post, scale, gamma_pre)
+    nsaved, _ = gated_norm_workspace_bytes(T, D)
+    r = _empty(x.shape, torch.bfloat16, dev, out, "r") if y is not None else None
+    h = _empty(x.shape, torch.bfloat16, dev, out, "h")
+    if saved is None:
+        saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
+    if saved.numel() < nsaved:
+        raise ValueError("saved buffer is too small")
+    _check("gated_norm_forward",
+           _load().gated_norm_forward(_ptr(x), _ptr(y), _ptr(gate), _ptr(gamma_post), _ptr(scale), _ptr(gamma_pre), T,
+                                      D, eps, _ptr(r), _ptr(h), _ptr(saved), _stream(dev)))
+    return {"r": x if y is None else r, "h": h, "saved": saved}
+
+
+def gated_norm_backward(dr, dh, x, y, gate, gamma_post, scale, gamma_pre, saved, *, eps=1e-6, out=None, scratch=None):
+    """Backward of gated_norm_forward (``gated_norm_backward``).  dr may be None (zero).
+
+    Returns dict(dx, dy, dgate, dgamma_post, dscale, dgamma_pre, scratch); dy, dgamma_post, dscale are None without a
+    branch, dgate without a gate."""
+    dev, T, D = _gated_norm_inputs(x, y, gate, gamma_post, scale, gamma_pre)
+    _opt(dr, "dr", torch.bfloat16, dev, x.shape)
+    _need(dh, "dh", torch.bfloat16, dev, x.shape)
+    nsaved, nscratch = gated_norm_workspace_bytes(T, D)
+    if saved is None or saved.numel() < nsaved:
+        raise ValueError("saved must be the forward's saved buffer")
+    if scratch is None:
+        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    if scratch.numel() < nscratch:
+        raise ValueError("scratch buffer is too small")
+    o = {"dx": _empty(x.shape, torch.bfloat16, dev, out, "dx"), "dy": None, "dgate": None, "dgamma_post": None,
+         "dscale": None, "dgamma_pre": _empty((D,), torch.float32, dev, out, "dgamma_pre")}
+    if y is not None:
+        o["dy"] = _empty(x.shape, torch.bfloat16, dev, out, "dy")
+        o["dgamma_post"] = _empty((D,), torch.float32, dev, out, "dgamma_post")
+        o["dscale"] = _empty((D,), torch.float32, dev, out, "dscale")
+    if gate is not None:
+        o["dgate"] = _empty(x.shape, torch.bfloat16, dev, out, "dgate")
+    _check("gated_norm_backward",
+           _load().gated_norm_backward(_ptr(dr), _ptr(dh), _ptr(x), _ptr(y), _ptr(gate), _ptr(gamma_post), _ptr(scale),
+                                       _ptr(gamma_pre), T, D, eps, _ptr(saved), _ptr(o["dx"]), _ptr(o["dy"]),
+                                       _ptr(o["dgate"]), _ptr(o["dgamma_post"]), _ptr(o["dscale"]),
+                                       _ptr(o["dgamma_pre"]), _ptr(scratch), _stream(dev)))
+    o["scratch"] = scratch
+    return o
+
+
+# ---------------------------------------------------------------------------
+# AdamW over many tensors
+# ---------------------------------------------------------------------------
+class _AdamwTensor(ctypes.Structure):
+    """lrs_adamw_tensor (include/samu.h)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + \
+        [("n", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("grad_dtype", ctypes.c_int)]
+
+
+ADAMW_BLOCK = 256   # values that share one scale of an 8-bit state
+
+
+def adamw_state(param, bits: int = 32) -> dict:
+    """Zeroed state of one tensor: {"m", "v"} in FP32, or (bits = 8) E4M3 codes with {"m_scale", "v_scale"}."""
+    if bits not in (8, 32):
+        raise ValueError(f"bits: expected 8 or 32, got {bits}")
+    dt = torch.float32 if bits == 32 else torch.float8_e4m3fn
+    st = {k: torch.zeros(param.shape, dtype=torch.uint8 if bits == 8 else dt, device=param.device).view(dt)
+          for k in ("m", "v")}
+    if bits == 8:
+        blocks = -(-param.numel() // ADAMW_BLOCK)
+        for k in ("m_scale", "v_scale"):
+            st[k] = torch.zeros(blocks, dtype=torch.float32, device=param.device)
+    return st
+
+
+class AdamwPlan:
+    """The checked list of tensors of ``adamw_step`` (see ``adamw_plan``)."""
+
+    def __init__(self, tensors):
+        tensors = [dict(t) for t in tensors]
+        if not tensors:
+            raise ValueError("adamw_plan needs at least one tensor")
+        self.device = tensors[0]["param"].device
+        self.tensors = tensors
+        self._list = (_AdamwTensor * len(tensors))()
+        for i, t in enumerate(tensors):
+            self._set(i, t)
+        n = ctypes.c_size_t(0)
+        _check("lrs_adamw_scratch_bytes", _load().lrs_adamw_scratch_bytes(len(tensors), ctypes.byref(n)))
+        self.scratch = torch.empty(n.value, dtype=torch.uint8, device=self.device)
+
+    def _set(self, i, t):
+        dev, p, name = self.device, t["param"], f"tensors[{i}]."
+        master = t.get("master")
+        _need(p, name + "param", torch.float32 if master is None else torch.bfloat16, dev)
+        _opt(master, name + "master", torch.float32, dev, p.shape)
+        q8 = t.get("m_scale") is not None
+        for k in ("m", "v"):
+            _need(t[k], name + k, torch.float8_e4m3fn if q8 else torch.float32, dev, p.shape)
+        if q8 or t.get("v_scale") is not None:
+            blocks = -(-p.numel() // ADAMW_BLOCK)
+            for k in ("m_scale", "v_scale"):
+                _need(t.get(k), name + k, torch.float32, dev, (blocks,))
+        e = self._list[i]
+        for k in ("param", "master", "m", "v", "m_scale", "v_scale"):
+            x = t.get(k)
+            setattr(e, k, None if x is None else x.data_ptr())
+        e.n, e.weight_decay = p.numel(), float(t.get("weight_decay", 0.0))
+        self._set_grad(i, t["grad"])
+
+    def _set_grad(self, i, g):
+        p = self.tensors[i]["param"]
+        if g is None or g.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"tensors[{i}].grad: expected torch.float32 or torch.bfloat16, got {getattr(g, 'dtype', None)}")
+        _need(g, f"tensors[{i}].grad", g.dtype, self.device, p.shape)
+        self.tensors[i]["grad"] = g
+        self._list[i].grad = g.data_ptr()
+        self._list[i].grad_dtype = LRS_GRAD_FP32 if g.dtype == torch.float32 else LRS_GRAD_BF16
+
+    def set_grads(self, grads):
+        """New gradient tensors (same shapes), in the list's order."""
+        grads = list(grads)
+        if len(grads) != len(self.tensors):
+            raise ValueError(f"expected {len(self.tensors)} gradients, got {len(grads)}")
+        for i, g in enumerate(grads):
+            self._set_grad(i, g)
+
+
+def adamw_plan(tensors) -> AdamwPlan:
+    """Checks a list of {"param", "grad", "m", "v"[, "master"][, "m_scale", "v_scale"][, "weight_decay"]} once, for
+    ``adamw_step``.  param: FP32, or BF16 with an FP32 "master"; grad: FP32 or BF16; the state as ``adamw_state`` makes
+    it.  The plan keeps the tensors; ``plan.set_grads`` replaces the gradients."""
+    return AdamwPlan(tensors)
+
+
+def adamw_step(plan: AdamwPlan, step, lr, *, beta1=0.9, beta2=0.95, eps=1e-8, max_norm=0.0, out=None):
+    """One AdamW step over the plan's tensors, in place, through ``lrs_adamw_step``.
+
+    step: int32 [1], the number of steps taken (advanced); lr: FP32 [1]; max_norm > 0 clips the gradients' norm over
+    all tensors, and a step whose norm is not finite changes nothing.  Returns dict(norm (FP32 [1], None without
+    clipping), step)."""
+    dev = plan.device
+    _need(step, "step", torch.int32, dev, (1,))
+    _need(lr, "lr", torch.float32, dev, (1,))
+    norm = _empty((1,), torch.float32, dev, out, "norm") if max_norm > 0 else None
+    _check("lrs_adamw_step",
+           _load().lrs_adamw_step(ctypes.cast(plan._list, _P), len(plan.tensors), _ptr(step), _ptr(lr), beta1, beta2,
+                                  eps, max_norm, _ptr(norm), _ptr(plan.scratch), _stream(dev)))
+    return {"norm": norm, "step": step}
+
+
 def block_tensors_from_numpy(inp: dict, device) -> dict:
     """Device tensors of synth.block_inputs: {"x", "dout", "h0", "dhT", "reset", "params": {...}}."""
     params = {}
@@ -716,6 +900,7 @@ KERNEL_NAMES = {
     13: "samu_decode_step_kernel", 14: "proj_gemm_kernel<logits>", 15: "proj_gemm_kernel<dx, dW>",
     16: "proj_pack_kernel", 17: "block_gemm_kernel", 18: "rmsnorm_kernels", 19: "conv_kernels",
     20: "join_fwd_kernel", 21: "sum_parts_kernel", 22: "ce_gemm_kernel", 23: "ce_rows_kernels",
+    24: "gated_norm_kernels", 25: "sum_parts_kernel", 26: "adamw_norm_kernel", 27: "adamw_update_kernel",
 }
 
 

@@ -80,7 +80,7 @@ enum {
     KID_SAMU_PARAMS, KID_RGLRU_SCAN_FWD, KID_RGLRU_SCAN_BWD, KID_RGLRU_ALPHA, KID_SAMU_FWD_MAPS,
     KID_SAMU_BWD_MAPS, KID_SAMU_DECODE_PREP, KID_SAMU_DECODE_STEP, KID_RGLRU_PROJ_FWD, KID_RGLRU_PROJ_BWD,
     KID_RGLRU_PROJ_PACK, KID_BLOCK_GEMM, KID_BLOCK_NORM, KID_BLOCK_CONV, KID_BLOCK_JOIN, KID_BLOCK_SUM, KID_CE_GEMM,
-    KID_CE_ROWS
+    KID_CE_ROWS, KID_GATED_NORM, KID_GATED_NORM_SUM, KID_ADAMW_NORM, KID_ADAMW_UPDATE
 };
 
 #define LRS_LAUNCH(id, stream, expr)            \
@@ -1271,6 +1271,169 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     if (h_part)
         LRS_LAUNCH(KID_CE_ROWS, stream,
                    launch_ce_sum(hp, (long long)T * D, h_splits, (long long)T * D, dh, fp32, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Norms around a residual branch
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_gated_norm_shape(int T, int D) {
+    if (T < 1 || D < 1) return LRS_ERR_ARG;
+    if (D % 8 != 0 || D > 8192) return LRS_ERR_UNSUPPORTED;
+    return LRS_OK;
+}
+
+bool gated_norm_inputs_ok(const void* x, const void* y, const void* g, const float* gamma_post, const float* scale,
+                          const float* gamma_pre, float eps) {
+    // without a branch there is nothing for a gate, a scale or a second norm to act on
+    if (y == nullptr && (g != nullptr || gamma_post != nullptr || scale != nullptr)) return false;
+    return req(x) && opt(y) && opt(g) && opt(gamma_post) && opt(scale) && opt(gamma_pre) && eps > 0.f && eps <= 1.f;
+}
+
+GatedNormArgs gated_norm_args(const void* x, const void* y, const void* g, const float* gamma_post, const float* scale,
+                              const float* gamma_pre, int T, int D, float eps) {
+    GatedNormArgs a = {};
+    a.T = T;
+    a.D = D;
+    a.eps = eps;
+    a.x = static_cast<const uint4*>(x);
+    a.y = static_cast<const uint4*>(y);
+    a.g = static_cast<const uint4*>(g);
+    a.gamma_post = gamma_post;
+    a.scale = scale;
+    a.gamma_pre = gamma_pre;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int gated_norm_workspace_bytes(int T, int D, size_t* saved_bytes, size_t* scratch_bytes) {
+    const int st = check_gated_norm_shape(T, D);
+    if (st != LRS_OK) return st;
+    if (saved_bytes != nullptr) *saved_bytes = up256((size_t)T * sizeof(float2));
+    if (scratch_bytes != nullptr)
+        *scratch_bytes = up256((size_t)3 * gated_norm_bwd_ctas(T, D, kBlockSmsBound) * D * sizeof(float));
+    return LRS_OK;
+}
+
+int gated_norm_forward(const void* x, const void* y, const void* gate, const float* gamma_post, const float* scale,
+                       const float* gamma_pre, int T, int D, float eps, void* r, void* h, void* saved,
+                       cudaStream_t stream) {
+    const int st = check_gated_norm_shape(T, D);
+    if (st != LRS_OK) return st;
+    if (!gated_norm_inputs_ok(x, y, gate, gamma_post, scale, gamma_pre, eps) || (y != nullptr ? !req(r) : r != nullptr) ||
+        !req(h) || !opt(saved))
+        return LRS_ERR_ARG;
+    GatedNormArgs a = gated_norm_args(x, y, gate, gamma_post, scale, gamma_pre, T, D, eps);
+    a.r = static_cast<uint4*>(r);
+    a.h = static_cast<uint4*>(h);
+    a.rstd = static_cast<float2*>(saved);
+    LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_fwd(a, stream));
+    return LRS_OK;
+}
+
+int gated_norm_backward(const void* dr, const void* dh, const void* x, const void* y, const void* gate,
+                        const float* gamma_post, const float* scale, const float* gamma_pre, int T, int D, float eps,
+                        const void* saved, void* dx, void* dy, void* dgate, float* dgamma_post, float* dscale,
+                        float* dgamma_pre, void* scratch, cudaStream_t stream) {
+    const int st = check_gated_norm_shape(T, D);
+    if (st != LRS_OK) return st;
+    const bool branch = y != nullptr;
+    if (!gated_norm_inputs_ok(x, y, gate, gamma_post, scale, gamma_pre, eps) || !opt(dr) || !req(dh) || !req(saved) ||
+        !req(dx) || !req(dgamma_pre) || !req(scratch) ||
+        (branch ? !req(dy) || !req(dgamma_post) || !req(dscale) : dy != nullptr || dgamma_post != nullptr || dscale != nullptr) ||
+        (gate != nullptr ? !req(dgate) : dgate != nullptr))
+        return LRS_ERR_ARG;
+    GatedNormBwdArgs a = {};
+    a.f = gated_norm_args(x, y, gate, gamma_post, scale, gamma_pre, T, D, eps);
+    a.f.rstd = static_cast<float2*>(const_cast<void*>(saved));
+    a.dr = static_cast<const uint4*>(dr);
+    a.dh = static_cast<const uint4*>(dh);
+    a.dx = static_cast<uint4*>(dx);
+    a.dy = static_cast<uint4*>(dy);
+    a.dg = static_cast<uint4*>(dgate);
+    a.part = static_cast<float*>(scratch);
+    const int ctas = gated_norm_bwd_ctas(T, D, block_gemm_sms());
+    LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_bwd(a, ctas, stream));
+    float* out[3] = {dgamma_pre, dgamma_post, dscale};
+    for (int i = 0; i < (branch ? 3 : 1); ++i)
+        LRS_LAUNCH(KID_GATED_NORM_SUM, stream,
+                   launch_sum_parts(a.part + (size_t)i * ctas * D, D, ctas, D, out[i], stream, pdl_ok()));
+    return LRS_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// AdamW over many tensors
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_adamw_tensors(const lrs_adamw_tensor* ts, int count) {
+    if (ts == nullptr || count < 1) return LRS_ERR_ARG;
+    long long chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        const lrs_adamw_tensor& t = ts[i];
+        if (t.n < 1 || !req(t.param) || !opt(t.master) || !req(t.grad) || !req(t.m) || !req(t.v) || !opt(t.m_scale) ||
+            !opt(t.v_scale) || (t.m_scale == nullptr) != (t.v_scale == nullptr) ||
+            (t.grad_dtype != LRS_GRAD_BF16 && t.grad_dtype != LRS_GRAD_FP32) || !(t.weight_decay >= 0.f) ||
+            t.weight_decay > 3e38f)
+            return LRS_ERR_ARG;
+        if (t.n > (1LL << 40)) return LRS_ERR_UNSUPPORTED;
+        chunks += adam_chunks(t.n);
+        if (chunks > 0x3fffffffLL) return LRS_ERR_UNSUPPORTED;
+    }
+    return LRS_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int lrs_adamw_scratch_bytes(int count, size_t* bytes) {
+    if (count < 1 || bytes == nullptr) return LRS_ERR_ARG;
+    *bytes = adam_scratch_bytes(count);
+    return LRS_OK;
+}
+
+int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, const float* lr, double beta1,
+                   double beta2, float eps, float max_norm, float* norm, void* scratch, cudaStream_t stream) {
+    const int st = check_adamw_tensors(tensors, count);
+    if (st != LRS_OK) return st;
+    if (step == nullptr || lr == nullptr || !(beta1 >= 0. && beta1 < 1.) || !(beta2 >= 0. && beta2 < 1.) ||
+        !(eps > 0.f && eps <= 3e38f) || !(max_norm >= 0.f && max_norm <= 3e38f) ||
+        (max_norm > 0.f && norm == nullptr) || !req(scratch))
+        return LRS_ERR_ARG;
+    AdamArgs a = {};
+    a.beta1 = beta1;
+    a.beta2 = beta2;
+    a.eps = eps;
+    a.max_norm = max_norm;
+    a.lr = lr;
+    a.step = step;
+    a.norm = norm;
+    a.bias = at<float>(scratch, 0);
+    a.partial = at<float>(scratch, 256);
+    for (int i = 0; i < count; i += kAdamCap) {
+        const int k = std::min(kAdamCap, count - i);
+        int ctas = 0;
+        a.advance = i == 0;
+        if (i > 0 && max_norm == 0.f) break;   // only the step's count and bias corrections, once
+        a.partial0 = a.partials;
+        LRS_LAUNCH(KID_ADAMW_NORM, stream, launch_adamw_norm(tensors + i, k, a, &ctas, stream, i > 0 && pdl_ok()));
+        a.partials += ctas;
+    }
+    for (int i = 0; i < count; i += kAdamCap) {
+        a.advance = i == 0;
+        LRS_LAUNCH(KID_ADAMW_UPDATE, stream,
+                   launch_adamw_update(tensors + i, std::min(kAdamCap, count - i), a, stream, pdl_ok()));
+    }
     return LRS_OK;
 }
 

@@ -1,0 +1,340 @@
+// The norms before and after a residual branch, fused with its gate and its
+// scale: the join of a bare mixer (its output y, its gate branch g) with the
+// residual stream x, and the norm that feeds the next layer.
+//
+//   p = y rstd1, n = p gamma_post, u = scale GeLU(g) n, r = x + u
+//   q = r rstd2, h = q gamma_pre      rstd = 1 / sqrt(mean^2 + eps) of y, of r
+//
+// Backward for dr, dh (means over the row):
+//   a = dh gamma_pre, dx = dr + rstd2 (a - q mean(a q))
+//   dg = dx scale n GeLU'(g);  dn = dx scale GeLU(g);  b = dn gamma_post
+//   dy = rstd1 (b - p mean(b p))
+//   dgamma_pre = sum dh q, dscale = sum dx GeLU(g) n, dgamma_post = sum dn p
+// r is formed again from x, y and g, in FP32: the rounded r is not read.
+//
+// Bound by bandwidth: 10 bytes a value forward, 16 backward, each array once.
+// A thread holds 8 consecutive channels (one 16-byte load of each operand) of
+// a row that stays in registers between its two row sums; a CTA takes several
+// rows at a time where they are narrow.  The three parameter gradients add up
+// in registers over the rows of a thread, then over the CTA's row slots in
+// shared memory, one partial row a CTA, joined in a fixed order.
+#include <algorithm>
+
+#include "block_math.cuh"
+#include "kernels.cuh"
+
+namespace lrs {
+
+namespace {
+
+constexpr int kGnMaxThreads = 512;
+constexpr int kGnMaxWarps = kGnMaxThreads / 32;
+
+__device__ __forceinline__ void unpack8(const uint4 q, float (&v)[8]) {
+    float2 f;
+    f = bf2_to_f2(q.x); v[0] = f.x; v[1] = f.y;
+    f = bf2_to_f2(q.y); v[2] = f.x; v[3] = f.y;
+    f = bf2_to_f2(q.z); v[4] = f.x; v[5] = f.y;
+    f = bf2_to_f2(q.w); v[6] = f.x; v[7] = f.y;
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+    return make_uint4(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]), f2_to_bf2(v[4], v[5]), f2_to_bf2(v[6], v[7]));
+}
+__device__ __forceinline__ void load8(const float* p, int v, bool on, float fill, float (&o)[8]) {
+    if (p == nullptr || !on) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = fill;
+        return;
+    }
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * v), b = __ldg(reinterpret_cast<const float4*>(p) + 2 * v + 1);
+    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
+    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+}
+
+// GeLU and its derivative, zero where the shared form clamps its exponent
+// (below -9.67 both are under 1e-33).
+__device__ __forceinline__ float gn_gelu(float x) { return x < -9.67f ? 0.f : gelu_fwd(x); }
+__device__ __forceinline__ void gn_gelu_grad(float x, float& g, float& dg) {
+    gelu_fwd_grad(x, g, dg);
+    if (x < -9.67f) g = dg = 0.f;
+}
+
+// Sum over the threads of a row (blockDim.x of them, whole warps).  `red` is
+// this sum's own buffer: sums that follow each other use two buffers in turn,
+// so one barrier each is enough.
+__device__ __forceinline__ float row_sum(float v, float (*red)[kGnMaxWarps]) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int warps = blockDim.x >> 5;
+    if (warps == 1) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.y][threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0.f;
+    for (int w = 0; w < warps; ++w) v += red[threadIdx.y][w];
+    return v;
+}
+
+// VEC: groups of 8 channels per thread (group threadIdx.x + k blockDim.x).
+template <bool Y, bool G, int VEC>
+__global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const GatedNormArgs a) {
+    __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
+    pdl_trigger();
+    pdl_wait();
+    const int nv = a.D / 8;
+    const float inv_d = 1.f / (float)a.D;
+    int turn = 0;   // without a branch there is one sum a row: its buffers take turns
+    for (long long base = (long long)blockIdx.x * blockDim.y; base < a.T; base += (long long)gridDim.x * blockDim.y, turn ^= 1) {
+        const long long row = base + threadIdx.y;
+        uint4 qx[VEC], qy[VEC], qg[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            const size_t o = (size_t)row * nv + v;
+            const bool on = row < a.T && v < nv;
+            qx[k] = qy[k] = qg[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (on) {
+                qx[k] = __ldg(a.x + o);
+                if (Y) qy[k] = __ldg(a.y + o);
+                if (G) qg[k] = __ldg(a.g + o);
+            }
+        }
+        float r[VEC][8], rstd1 = 0.f;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) unpack8(qx[k], r[k]);
+        if (Y) {
+            float ss = 0.f;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                float y[8];
+                unpack8(qy[k], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+            }
+            rstd1 = 1.f / sqrtf(row_sum(ss, red[0]) * inv_d + a.eps);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const int v = threadIdx.x + k * blockDim.x;
+                float y[8], g[8], gp[8], sc[8];
+                unpack8(qy[k], y);
+                unpack8(qg[k], g);
+                load8(a.gamma_post, v, v < nv, 1.f, gp);
+                load8(a.scale, v, v < nv, 1.f, sc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float n = y[i] * rstd1 * gp[i];
+                    r[k][i] = fmaf(sc[i] * (G ? gn_gelu(g[i]) : 1.f), n, r[k][i]);
+                }
+            }
+        }
+        float ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(r[k][i], r[k][i], ss);
+        const float rstd2 = 1.f / sqrtf(row_sum(ss, red[Y ? 1 : turn]) * inv_d + a.eps);
+        if (row >= a.T) continue;
+        if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = make_float2(rstd1, rstd2);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            if (v >= nv) continue;
+            float gm[8], h[8];
+            load8(a.gamma_pre, v, true, 1.f, gm);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = r[k][i] * rstd2 * gm[i];
+            const size_t o = (size_t)row * nv + v;
+            if (Y) a.r[o] = pack8(r[k]);
+            a.h[o] = pack8(h);
+        }
+    }
+}
+
+template <bool Y, bool G, int VEC>
+__global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const GatedNormBwdArgs a) {
+    __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
+    extern __shared__ __align__(16) float acc[];   // [3][rows][D]
+    pdl_trigger();
+    pdl_wait();
+    const GatedNormArgs& f = a.f;
+    const int nv = f.D / 8;
+    const float inv_d = 1.f / (float)f.D;
+    float dpre[VEC][8], dpost[VEC][8], dscale[VEC][8];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dpre[k][i] = dpost[k][i] = dscale[k][i] = 0.f;
+    int turn = 0;
+    for (long long base = (long long)blockIdx.x * blockDim.y; base < f.T; base += (long long)gridDim.x * blockDim.y, turn ^= 1) {
+        const long long row = base + threadIdx.y;
+        uint4 qx[VEC], qy[VEC], qg[VEC], qr[VEC], qh[VEC];
+        float2 rs = make_float2(0.f, 0.f);
+        if (row < f.T) rs = __ldg(a.f.rstd + row);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            const size_t o = (size_t)row * nv + v;
+            qx[k] = qy[k] = qg[k] = qr[k] = qh[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < f.T && v < nv) {
+                qx[k] = __ldg(f.x + o);
+                qh[k] = __ldg(a.dh + o);
+                if (a.dr != nullptr) qr[k] = __ldg(a.dr + o);
+                if (Y) qy[k] = __ldg(f.y + o);
+                if (G) qg[k] = __ldg(f.g + o);
+            }
+        }
+        // q = r rstd2, a = dh gamma_pre, mean(a q)
+        float q[VEC][8], s = 0.f;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            float dh[8], gm[8];
+            unpack8(qx[k], q[k]);
+            unpack8(qh[k], dh);
+            load8(f.gamma_pre, v, v < nv, 1.f, gm);
+            if (Y) {
+                float y[8], g[8], gp[8], sc[8];
+                unpack8(qy[k], y);
+                unpack8(qg[k], g);
+                load8(f.gamma_post, v, v < nv, 1.f, gp);
+                load8(f.scale, v, v < nv, 1.f, sc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    q[k][i] = fmaf(sc[i] * (G ? gn_gelu(g[i]) : 1.f), y[i] * rs.x * gp[i], q[k][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                q[k][i] *= rs.y;
+                dpre[k][i] = fmaf(dh[i], q[k][i], dpre[k][i]);
+                s = fmaf(dh[i] * gm[i], q[k][i], s);
+            }
+        }
+        const float mean = row_sum(s, red[Y ? 0 : turn]) * inv_d;
+        float dx[VEC][8];
+        s = 0.f;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+            const int v = threadIdx.x + k * blockDim.x;
+            float dh[8], dr[8], gm[8];
+            unpack8(qh[k], dh);
+            unpack8(qr[k], dr);
+            load8(f.gamma_pre, v, v < nv, 1.f, gm);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dx[k][i] = fmaf(rs.y, dh[i] * gm[i] - q[k][i] * mean, dr[i]);
+            if (row < f.T && v < nv) a.dx[(size_t)row * nv + v] = pack8(dx[k]);
+            if (Y) {
+                float y[8], g[8], gp[8], sc[8], dg[8];
+                unpack8(qy[k], y);
+                unpack8(qg[k], g);
+                load8(f.gamma_post, v, v < nv, 1.f, gp);
+                load8(f.scale, v, v < nv, 1.f, sc);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    float ge = 1.f, dge = 0.f;
+                    if (G) gn_gelu_grad(g[i], ge, dge);
+                    const float p = y[i] * rs.x, n = p * gp[i], t = dx[k][i] * sc[i];
+                    dscale[k][i] = fmaf(dx[k][i] * ge, n, dscale[k][i]);
+                    dg[i] = t * n * dge;
+                    const float dn = t * ge;
+                    dpost[k][i] = fmaf(dn, p, dpost[k][i]);
+                    dx[k][i] = dn * gp[i];   // b
+                    s = fmaf(dx[k][i], p, s);
+                }
+                if (G && row < f.T && v < nv) a.dg[(size_t)row * nv + v] = pack8(dg);
+            }
+        }
+        if (Y) {
+            const float mean1 = row_sum(s, red[1]) * inv_d;
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) {
+                const int v = threadIdx.x + k * blockDim.x;
+                float y[8], dy[8];
+                unpack8(qy[k], y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) dy[i] = rs.x * (dx[k][i] - y[i] * rs.x * mean1);
+                if (row < f.T && v < nv) a.dy[(size_t)row * nv + v] = pack8(dy);
+            }
+        }
+    }
+    // the CTA's row slots in order, then one partial row of each sum
+    const int sums = Y ? 3 : 1;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        const int v = threadIdx.x + k * blockDim.x;
+        if (v >= nv) continue;
+        float* o = acc + (size_t)threadIdx.y * f.D + 8 * v;
+        const size_t stride = (size_t)blockDim.y * f.D;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            o[i] = dpre[k][i];
+            if (Y) {
+                o[stride + i] = dpost[k][i];
+                o[2 * stride + i] = dscale[k][i];
+            }
+        }
+    }
+    __syncthreads();
+    const int tid = threadIdx.y * blockDim.x + threadIdx.x;
+    for (int c = tid; c < sums * f.D; c += blockDim.x * blockDim.y) {
+        const int w = c / f.D, d = c - w * f.D;
+        float s = 0.f;
+        for (int y = 0; y < (int)blockDim.y; ++y) s += acc[((size_t)w * blockDim.y + y) * f.D + d];
+        a.part[((size_t)w * gridDim.x + blockIdx.x) * f.D + d] = s;
+    }
+}
+
+struct GnShape {
+    int vec;
+    dim3 block;
+};
+// Whole warps of threads with 8 channels each span a row; narrow rows share a
+// CTA of 256 threads.
+GnShape gn_shape(int D) {
+    GnShape s;
+    const int nv = D / 8;
+    s.vec = nv <= kGnMaxThreads ? 1 : 2;
+    const int x = ((nv + s.vec - 1) / s.vec + 31) / 32 * 32;
+    s.block = dim3((unsigned)x, (unsigned)std::max(1, 256 / x));
+    return s;
+}
+
+template <bool Y, bool G>
+cudaError_t gn_fwd(const GatedNormArgs& a, cudaStream_t s) {
+    const GnShape sh = gn_shape(a.D);
+    const long long groups = (a.T + sh.block.y - 1) / sh.block.y;
+    const long long grid = std::min<long long>(groups, 16LL * block_gemm_sms());
+    if (sh.vec == 1)
+        return launch_ex(gated_norm_fwd_kernel<Y, G, 1>, dim3((unsigned)grid), sh.block, 0, s, false, a);
+    return launch_ex(gated_norm_fwd_kernel<Y, G, 2>, dim3((unsigned)grid), sh.block, 0, s, false, a);
+}
+
+template <bool Y, bool G, int VEC>
+cudaError_t gn_bwd_as(const GatedNormBwdArgs& a, const GnShape& sh, int ctas, cudaStream_t s) {
+    const size_t smem = (size_t)(Y ? 3 : 1) * sh.block.y * a.f.D * sizeof(float);
+    auto* fn = gated_norm_bwd_kernel<Y, G, VEC>;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(fn, dim3((unsigned)ctas), sh.block, smem, s, false, a);
+}
+template <bool Y, bool G>
+cudaError_t gn_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s) {
+    const GnShape sh = gn_shape(a.f.D);
+    return sh.vec == 1 ? gn_bwd_as<Y, G, 1>(a, sh, ctas, s) : gn_bwd_as<Y, G, 2>(a, sh, ctas, s);
+}
+
+}  // namespace
+
+int gated_norm_bwd_ctas(long long T, int D, int sms) {
+    const GnShape sh = gn_shape(D);
+    return (int)std::max(1LL, std::min<long long>((T + sh.block.y - 1) / sh.block.y, 4LL * sms));
+}
+
+cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s) {
+    if (a.y == nullptr) return gn_fwd<false, false>(a, s);
+    return a.g == nullptr ? gn_fwd<true, false>(a, s) : gn_fwd<true, true>(a, s);
+}
+cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s) {
+    if (a.f.y == nullptr) return gn_bwd<false, false>(a, ctas, s);
+    return a.f.g == nullptr ? gn_bwd<true, false>(a, ctas, s) : gn_bwd<true, true>(a, ctas, s);
+}
+
+}  // namespace lrs

@@ -572,4 +572,57 @@ cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* 
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,
                           cudaStream_t s, bool pdl);
 
+// ---------------------------------------------------------------------------
+// Norms around a residual branch (gated_norm.cu).
+// ---------------------------------------------------------------------------
+struct GatedNormArgs {
+    long long T;
+    int D;
+    float eps;
+    const uint4* x;
+    const uint4* y;              // null: no branch (r = x)
+    const uint4* g;              // null: no gate
+    const float* gamma_post;     // null: ones
+    const float* scale;          // null: ones
+    const float* gamma_pre;      // null: ones
+    uint4* r;
+    uint4* h;
+    float2* rstd;                // [T] of y, of r
+};
+struct GatedNormBwdArgs {
+    GatedNormArgs f;             // the forward's inputs and rstd
+    const uint4* dr;             // null: zero
+    const uint4* dh;
+    uint4* dx;
+    uint4* dy;
+    uint4* dg;
+    float* part;                 // [3 (1 without a branch)][ctas][D]: dgamma_pre, dgamma_post, dscale
+};
+int gated_norm_bwd_ctas(long long T, int D, int sms);
+cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s);
+cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
+// AdamW over many tensors (adamw.cu).
+// ---------------------------------------------------------------------------
+using AdamTensor = lrs_adamw_tensor;
+// Tensors of one launch: the list is part of the kernel's parameters, 2.5 KB
+// or 30 KB of the 32 KB that they may hold.
+constexpr int kAdamCapSmall = 32, kAdamCap = 400;
+struct AdamArgs {
+    double beta1, beta2;
+    float eps, max_norm;
+    const float* lr;
+    int32_t* step;
+    float* norm;
+    float* bias;                 // [2]: 1 / (1 - beta^step)
+    float* partial;              // sums of squares, one a CTA of the first launches
+    int partial0, partials;      // this launch's first, and all
+    int advance;                 // the step's first launch of its kind
+};
+long long adam_chunks(long long n);
+size_t adam_scratch_bytes(int count);
+cudaError_t launch_adamw_norm(const AdamTensor* ts, int count, const AdamArgs& a, int* ctas, cudaStream_t s, bool pdl);
+cudaError_t launch_adamw_update(const AdamTensor* ts, int count, const AdamArgs& a, cudaStream_t s, bool pdl);
+
 }  // namespace lrs

@@ -9,6 +9,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -132,11 +133,14 @@ def _check(fn: str, status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(device) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+def _stream(device) -> int:
+    index = device.index if isinstance(device, torch.device) else None
+    if index is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(index)   # the same handle, without building a Stream object
 
 
 def _need(t, name, dtype, device, shape=None):
@@ -148,7 +152,7 @@ def _need(t, name, dtype, device, shape=None):
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
@@ -609,6 +613,7 @@ def dense_gemm(layout: int, A, B, M: int, N: int, K: int, *, out=None, scratch=N
 # ---------------------------------------------------------------------------
 # Softmax cross entropy over a vocabulary
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
 def linear_ce_workspace_bytes(T: int, V: int, D: int, grad_fp32: bool = False):
     """(forward, backward) scratch bytes of the vocabulary loss."""
     f = ctypes.c_size_t(0)
@@ -681,6 +686,7 @@ def linear_ce_backward(h, w, target, lse, dloss=None, *, total=None, softcap=0.0
 # ---------------------------------------------------------------------------
 # Norms before and after a residual branch, with its gate and scale
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
 def gated_norm_workspace_bytes(T: int, D: int):
     s = ctypes.c_size_t(0)
     c = ctypes.c_size_t(0)

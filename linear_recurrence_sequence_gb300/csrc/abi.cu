@@ -1318,7 +1318,9 @@ int gated_norm_workspace_bytes(int T, int D, size_t* saved_bytes, size_t* scratc
     if (st != LRS_OK) return st;
     if (saved_bytes != nullptr) *saved_bytes = up256((size_t)T * sizeof(float2));
     if (scratch_bytes != nullptr)
-        *scratch_bytes = up256((size_t)3 * gated_norm_bwd_ctas(T, D, kBlockSmsBound) * D * sizeof(float));
+        *scratch_bytes = up256((size_t)3 * D * sizeof(float) *
+                                std::max(gated_norm_bwd_ctas(T, D, true, kBlockSmsBound),
+                                         gated_norm_bwd_ctas(T, D, false, kBlockSmsBound)));
     return LRS_OK;
 }
 
@@ -1359,12 +1361,10 @@ int gated_norm_backward(const void* dr, const void* dh, const void* x, const voi
     a.dy = static_cast<uint4*>(dy);
     a.dg = static_cast<uint4*>(dgate);
     a.part = static_cast<float*>(scratch);
-    const int ctas = gated_norm_bwd_ctas(T, D, block_gemm_sms());
+    const int ctas = gated_norm_bwd_ctas(T, D, branch, block_gemm_sms());
     LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_bwd(a, ctas, stream));
-    float* out[3] = {dgamma_pre, dgamma_post, dscale};
-    for (int i = 0; i < (branch ? 3 : 1); ++i)
-        LRS_LAUNCH(KID_GATED_NORM_SUM, stream,
-                   launch_sum_parts(a.part + (size_t)i * ctas * D, D, ctas, D, out[i], stream, pdl_ok()));
+    LRS_LAUNCH(KID_GATED_NORM_SUM, stream,
+               launch_gated_norm_sum(a.part, ctas, D, branch, dgamma_pre, dgamma_post, dscale, stream, pdl_ok()));
     return LRS_OK;
 }
 
@@ -1413,6 +1413,10 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
     AdamArgs a = {};
     a.beta1 = beta1;
     a.beta2 = beta2;
+    a.b1 = (float)beta1;
+    a.c1 = (float)(1.0 - beta1);
+    a.b2 = (float)beta2;
+    a.c2 = (float)(1.0 - beta2);
     a.eps = eps;
     a.max_norm = max_norm;
     a.lr = lr;

@@ -35,6 +35,7 @@ namespace {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamBlock = 256;                             // values a scale stands for, values of a warp
 constexpr int kAdamChunk = kAdamBlock * kAdamThreads / 32;  // values of a CTA at a time
+constexpr int kAdamNormCtas = 8;                            // CTAs per SM of the norm
 constexpr float kFp8Max = 448.f;
 constexpr float kFp8Tiny = 0.001953125f;                    // 2^-9, the smallest E4M3 value above 0
 constexpr float kAdamSmall = 7.888609052210118e-31f;        // 2^-100
@@ -47,28 +48,35 @@ struct AdamList {
     int count;
 };
 
-// The tensor of chunk c, searched on from tensor i (chunks come in ascending order).
+// The tensor of chunk c: the last one that starts at or before it.
 template <int CAP>
-__device__ __forceinline__ int adam_find(const AdamList<CAP>& l, int c, int i) {
-    while (c >= l.first[i + 1]) ++i;
-    return i;
+__device__ __forceinline__ int adam_find(const AdamList<CAP>& l, int c) {
+    int lo = 0, hi = l.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (l.first[mid] <= c)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo;
 }
 
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-    const float4 q = *reinterpret_cast<const float4*>(p);
-    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
-}
-// Four values from i on of an array of n (zeros past its end).
+// Four values from i on of an array of n; FULL: all four are inside it (else
+// zeros past its end, and nothing is stored there).
+template <bool FULL>
 __device__ __forceinline__ void load_f32(const float* p, long long i, long long n, float (&v)[4]) {
-    if (i + 4 <= n) {
-        load4(p + i, v);
+    if (FULL) {
+        const float4 q = *reinterpret_cast<const float4*>(p + i);
+        v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
     } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k) v[k] = i + k < n ? p[i + k] : 0.f;
     }
 }
+template <bool FULL>
 __device__ __forceinline__ void store_f32(float* p, long long i, long long n, const float (&v)[4]) {
-    if (i + 4 <= n) {
+    if (FULL) {
         *reinterpret_cast<float4*>(p + i) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
@@ -76,8 +84,9 @@ __device__ __forceinline__ void store_f32(float* p, long long i, long long n, co
             if (i + k < n) p[i + k] = v[k];
     }
 }
+template <bool FULL>
 __device__ __forceinline__ void load_bf16(const uint16_t* p, long long i, long long n, float (&v)[4]) {
-    if (i + 4 <= n) {
+    if (FULL) {
         const uint2 q = *reinterpret_cast<const uint2*>(p + i);
         const float2 a = bf2_to_f2(q.x), b = bf2_to_f2(q.y);
         v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
@@ -86,26 +95,27 @@ __device__ __forceinline__ void load_bf16(const uint16_t* p, long long i, long l
         for (int k = 0; k < 4; ++k) v[k] = i + k < n ? __uint_as_float((uint32_t)p[i + k] << 16) : 0.f;
     }
 }
+template <bool FULL>
 __device__ __forceinline__ void store_bf16(uint16_t* p, long long i, long long n, const float (&v)[4]) {
-    const uint2 q = make_uint2(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]));
-    if (i + 4 <= n) {
-        *reinterpret_cast<uint2*>(p + i) = q;
+    const uint32_t w[2] = {f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3])};
+    if (FULL) {
+        *reinterpret_cast<uint2*>(p + i) = make_uint2(w[0], w[1]);
     } else {
-        const uint32_t w[2] = {q.x, q.y};
 #pragma unroll
         for (int k = 0; k < 4; ++k)
             if (i + k < n) p[i + k] = (uint16_t)(w[k / 2] >> (16 * (k & 1)));
     }
 }
-__device__ __forceinline__ void load_fp8(const uint8_t* p, long long i, long long n, float s, float (&v)[4]) {
+template <bool FULL>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, long long i, long long n) {
+    if (FULL) return *reinterpret_cast<const uint32_t*>(p + i);
     uint32_t q = 0;
-    if (i + 4 <= n) {
-        q = *reinterpret_cast<const uint32_t*>(p + i);
-    } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            if (i + k < n) q |= (uint32_t)p[i + k] << (8 * k);
-    }
+    for (int k = 0; k < 4; ++k)
+        if (i + k < n) q |= (uint32_t)p[i + k] << (8 * k);
+    return q;
+}
+__device__ __forceinline__ void decode(uint32_t q, float s, float (&v)[4]) {
 #pragma unroll
     for (int k = 0; k < 4; k += 2) {
         const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(q >> (8 * k)), __NV_E4M3);
@@ -114,10 +124,11 @@ __device__ __forceinline__ void load_fp8(const uint8_t* p, long long i, long lon
         v[k + 1] = f.y * s;
     }
 }
-__device__ __forceinline__ void store_fp8(uint8_t* p, long long i, long long n, const float (&v)[4]) {
+template <bool FULL>
+__device__ __forceinline__ void store_codes(uint8_t* p, long long i, long long n, const float (&v)[4]) {
     const uint32_t q = (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3) |
                        (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3) << 16;
-    if (i + 4 <= n) {
+    if (FULL) {
         *reinterpret_cast<uint32_t*>(p + i) = q;
     } else {
 #pragma unroll
@@ -165,36 +176,148 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     }
     if (a.max_norm <= 0.f) return;
     float s = 0.f;
-    int i = 0;
     for (int c = (int)blockIdx.x; c < l.first[l.count]; c += (int)gridDim.x) {
-        i = adam_find(l, c, i);
-        const AdamTensor& t = l.t[i];
-        const long long at = (long long)(c - l.first[i]) * kAdamChunk + warp * kAdamBlock + 4 * lane;
+        const int i = adam_find(l, c);
+        const long long n = l.t[i].n, at = (long long)(c - l.first[i]) * kAdamChunk + warp * kAdamBlock + 4 * lane;
+        const bool bf = l.t[i].grad_dtype == LRS_GRAD_BF16;
+        const void* gp = l.t[i].grad;
+        float g[2][4];
+        if ((long long)(c - l.first[i] + 1) * kAdamChunk <= n) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const long long e = at + 128 * k;
-            if (e >= t.n) continue;
-            float g[4];
-            if (t.grad_dtype == LRS_GRAD_BF16)
-                load_bf16(static_cast<const uint16_t*>(t.grad), e, t.n, g);
-            else
-                load_f32(static_cast<const float*>(t.grad), e, t.n, g);
+            for (int k = 0; k < 2; ++k) {
+                if (bf)
+                    load_bf16<true>(static_cast<const uint16_t*>(gp), at + 128 * k, n, g[k]);
+                else
+                    load_f32<true>(static_cast<const float*>(gp), at + 128 * k, n, g[k]);
+            }
+        } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s = fmaf(g[j], g[j], s);
+            for (int k = 0; k < 2; ++k) {
+                if (bf)
+                    load_bf16<false>(static_cast<const uint16_t*>(gp), at + 128 * k, n, g[k]);
+                else
+                    load_f32<false>(static_cast<const float*>(gp), at + 128 * k, n, g[k]);
+            }
         }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s = fmaf(g[k][j], g[k][j], s);
     }
     s = cta_sum(s, red);
     if (threadIdx.x == 0) a.partial[a.partial0 + blockIdx.x] = s;
 }
 
+// The step's scalars.
+struct AdamScalars {
+    float clip, lr, ibc1, root_ibc2, b1, c1, b2, c2, eps;
+};
+
+// 256 consecutive values of one tensor, by one warp.
+template <bool Q8, bool GRAD_BF16, bool FULL>
+__device__ __forceinline__ void adam_block(const AdamTensor& t, long long b0, int lane, const AdamScalars& a) {
+    const long long n = t.n;
+    const bool master = t.master != nullptr;
+    float* p32 = master ? t.master : static_cast<float*>(t.param);
+    float p[2][4], g[2][4], m[2][4], v[2][4];
+    float ms = 0.f, vs = 0.f;
+    uint32_t mc[2], vc[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const long long e = b0 + 128 * k + 4 * lane;
+        if (GRAD_BF16)
+            load_bf16<FULL>(static_cast<const uint16_t*>(t.grad), e, n, g[k]);
+        else
+            load_f32<FULL>(static_cast<const float*>(t.grad), e, n, g[k]);
+        load_f32<FULL>(p32, e, n, p[k]);
+        if (Q8) {
+            mc[k] = load_codes<FULL>(static_cast<const uint8_t*>(t.m), e, n);
+            vc[k] = load_codes<FULL>(static_cast<const uint8_t*>(t.v), e, n);
+        } else {
+            load_f32<FULL>(static_cast<const float*>(t.m), e, n, m[k]);
+            load_f32<FULL>(static_cast<const float*>(t.v), e, n, v[k]);
+        }
+    }
+    if (Q8) {
+        ms = t.m_scale[b0 / kAdamBlock];
+        vs = t.v_scale[b0 / kAdamBlock];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            decode(mc[k], ms, m[k]);
+            decode(vc[k], vs, v[k]);
+        }
+    }
+    const float keep = 1.f - a.lr * t.weight_decay;
+    float root[2][4];
+    uint32_t mtop = 0u, vtop = 0u;   // magnitudes as integers: their order is the values', NaN above all
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float gg = g[k][j] * a.clip;
+            const float vv = Q8 ? v[k][j] * v[k][j] : v[k][j];
+            // each product rounded by itself, as written above
+            m[k][j] = __fadd_rn(__fmul_rn(m[k][j], a.b1), __fmul_rn(gg, a.c1));
+            v[k][j] = __fadd_rn(__fmul_rn(vv, a.b2), __fmul_rn(__fmul_rn(gg, gg), a.c2));
+            // one root serves the step and the state; it and the quotient come
+            // from the SFU, within 2^-22 (the step is a small part of p)
+            root[k][j] = sqrt_approx(v[k][j]);
+            const float step = __fdividef(m[k][j] * a.ibc1, fmaf(root[k][j], a.root_ibc2, a.eps));
+            p[k][j] = fmaf(-a.lr, step, p[k][j] * keep);
+            if (Q8) {
+                mtop = max(mtop, __float_as_uint(fabsf(m[k][j])));
+                vtop = max(vtop, __float_as_uint(root[k][j]));
+            }
+        }
+    }
+    if (Q8) {
+        const float mt = __uint_as_float(__reduce_max_sync(0xffffffffu, mtop));
+        const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, vtop));
+        const float mi = mt >= kAdamSmall ? kFp8Max / mt : 0.f, vi = vt >= kAdamSmall ? kFp8Max / vt : 0.f;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                m[k][j] *= mi;
+                const float r = root[k][j] * vi;
+                v[k][j] = r > 0.f ? fmaxf(r, kFp8Tiny) : r;
+            }
+        if (lane == 0) {
+            t.m_scale[b0 / kAdamBlock] = mt >= kAdamSmall ? mt / kFp8Max : 0.f;
+            t.v_scale[b0 / kAdamBlock] = vt >= kAdamSmall ? vt / kFp8Max : 0.f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const long long e = b0 + 128 * k + 4 * lane;
+        store_f32<FULL>(p32, e, n, p[k]);
+        if (master) store_bf16<FULL>(static_cast<uint16_t*>(t.param), e, n, p[k]);
+        if (Q8) {
+            store_codes<FULL>(static_cast<uint8_t*>(t.m), e, n, m[k]);
+            store_codes<FULL>(static_cast<uint8_t*>(t.v), e, n, v[k]);
+        } else {
+            store_f32<FULL>(static_cast<float*>(t.m), e, n, m[k]);
+            store_f32<FULL>(static_cast<float*>(t.v), e, n, v[k]);
+        }
+    }
+}
+template <bool Q8, bool GRAD_BF16>
+__device__ __forceinline__ void adam_block_any(const AdamTensor& t, long long b0, int lane, const AdamScalars& a) {
+    if (b0 + kAdamBlock <= t.n)
+        adam_block<Q8, GRAD_BF16, true>(t, b0, lane, a);
+    else
+        adam_block<Q8, GRAD_BF16, false>(t, b0, lane, a);
+}
+
 template <int CAP>
-__global__ void __launch_bounds__(kAdamThreads) adamw_update_kernel(const __grid_constant__ AdamList<CAP> l,
-                                                                    const AdamArgs a) {
+__global__ void __launch_bounds__(kAdamThreads, 4) adamw_update_kernel(const __grid_constant__ AdamList<CAP> l,
+                                                                       const AdamArgs a) {
     __shared__ float red[kAdamThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     pdl_wait();
-    float clip = 1.f;
+    AdamScalars sc;
+    sc.clip = 1.f;
     if (a.max_norm > 0.f) {
         float s = 0.f;
         for (int i = threadIdx.x; i < a.partials; i += kAdamThreads) s += __ldcg(a.partial + i);
@@ -205,98 +328,37 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_update_kernel(const __grid
             if (skip) *a.step -= 1;   // no other CTA of a skipped step reads it
         }
         if (skip) return;
-        clip = norm > a.max_norm ? a.max_norm / norm : 1.f;
+        sc.clip = norm > a.max_norm ? a.max_norm / norm : 1.f;
     }
-    const float lr = __ldg(a.lr), ibc1 = __ldcg(a.bias), ibc2 = __ldcg(a.bias + 1);
-    const float b1 = (float)a.beta1, c1 = (float)(1.0 - a.beta1), b2 = (float)a.beta2, c2 = (float)(1.0 - a.beta2);
-    int i = 0;
+    sc.lr = __ldg(a.lr);
+    sc.ibc1 = __ldcg(a.bias);
+    sc.root_ibc2 = sqrtf(__ldcg(a.bias + 1));
+    sc.b1 = a.b1;
+    sc.c1 = a.c1;
+    sc.b2 = a.b2;
+    sc.c2 = a.c2;
+    sc.eps = a.eps;
     for (int c = (int)blockIdx.x; c < l.first[l.count]; c += (int)gridDim.x) {
-        i = adam_find(l, c, i);
+        const int i = adam_find(l, c);
         const AdamTensor& t = l.t[i];
-        const long long n = t.n;
         const long long b0 = (long long)(c - l.first[i]) * kAdamChunk + warp * kAdamBlock;
-        if (b0 >= n) continue;
-        const bool q8 = t.m_scale != nullptr;
-        float* p32 = t.master != nullptr ? t.master : static_cast<float*>(t.param);
-        float p[2][4], g[2][4], m[2][4], v[2][4];
-        float ms = 0.f, vs = 0.f;
-        if (q8) {
-            ms = t.m_scale[b0 / kAdamBlock];
-            vs = t.v_scale[b0 / kAdamBlock];
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const long long e = b0 + 128 * k + 4 * lane;
-            if (t.grad_dtype == LRS_GRAD_BF16)
-                load_bf16(static_cast<const uint16_t*>(t.grad), e, n, g[k]);
+        if (b0 >= t.n) continue;
+        const bool bf = t.grad_dtype == LRS_GRAD_BF16;
+        if (t.m_scale != nullptr) {
+            if (bf)
+                adam_block_any<true, true>(t, b0, lane, sc);
             else
-                load_f32(static_cast<const float*>(t.grad), e, n, g[k]);
-            load_f32(p32, e, n, p[k]);
-            if (q8) {
-                load_fp8(static_cast<const uint8_t*>(t.m), e, n, ms, m[k]);
-                load_fp8(static_cast<const uint8_t*>(t.v), e, n, vs, v[k]);
-            } else {
-                load_f32(static_cast<const float*>(t.m), e, n, m[k]);
-                load_f32(static_cast<const float*>(t.v), e, n, v[k]);
-            }
-        }
-        const float keep = 1.f - lr * t.weight_decay;
-        float mt = 0.f, vt = 0.f, root[2][4];
-        uint32_t mtop = 0u, vtop = 0u;   // magnitudes as integers: their order is the values', NaN above all
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float gg = g[k][j] * clip;
-                const float vv = q8 ? v[k][j] * v[k][j] : v[k][j];
-                // each product rounded by itself, as written above
-                m[k][j] = __fadd_rn(__fmul_rn(m[k][j], b1), __fmul_rn(gg, c1));
-                v[k][j] = __fadd_rn(__fmul_rn(vv, b2), __fmul_rn(__fmul_rn(gg, gg), c2));
-                const float step = m[k][j] * ibc1 / (sqrtf(v[k][j] * ibc2) + a.eps);
-                p[k][j] = fmaf(-lr, step, p[k][j] * keep);
-                if (q8) {
-                    root[k][j] = sqrtf(v[k][j]);
-                    mtop = max(mtop, __float_as_uint(fabsf(m[k][j])));
-                    vtop = max(vtop, __float_as_uint(root[k][j]));
-                }
-            }
-        }
-        if (q8) {
-            mt = __uint_as_float(__reduce_max_sync(0xffffffffu, mtop));
-            vt = __uint_as_float(__reduce_max_sync(0xffffffffu, vtop));
-            const float mi = mt >= kAdamSmall ? kFp8Max / mt : 0.f, vi = vt >= kAdamSmall ? kFp8Max / vt : 0.f;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    m[k][j] *= mi;
-                    const float r = root[k][j] * vi;
-                    v[k][j] = r > 0.f ? fmaxf(r, kFp8Tiny) : r;
-                }
-            if (lane == 0) {
-                t.m_scale[b0 / kAdamBlock] = mt >= kAdamSmall ? mt / kFp8Max : 0.f;
-                t.v_scale[b0 / kAdamBlock] = vt >= kAdamSmall ? vt / kFp8Max : 0.f;
-            }
-        }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const long long e = b0 + 128 * k + 4 * lane;
-            if (e >= n) continue;
-            store_f32(p32, e, n, p[k]);
-            if (t.master != nullptr) store_bf16(static_cast<uint16_t*>(t.param), e, n, p[k]);
-            if (q8) {
-                store_fp8(static_cast<uint8_t*>(t.m), e, n, m[k]);
-                store_fp8(static_cast<uint8_t*>(t.v), e, n, v[k]);
-            } else {
-                store_f32(static_cast<float*>(t.m), e, n, m[k]);
-                store_f32(static_cast<float*>(t.v), e, n, v[k]);
-            }
+                adam_block_any<true, false>(t, b0, lane, sc);
+        } else if (bf) {
+            adam_block_any<false, true>(t, b0, lane, sc);
+        } else {
+            adam_block_any<false, false>(t, b0, lane, sc);
         }
     }
 }
 
 int adam_norm_ctas(long long chunks) {
-    return (int)std::max(1LL, std::min<long long>(chunks, 4LL * block_gemm_sms()));
+    return (int)std::max(1LL, std::min<long long>(chunks, (long long)kAdamNormCtas * block_gemm_sms()));
 }
 
 // Tensors [t0, t0 + count) as one launch.
@@ -331,7 +393,7 @@ long long adam_chunks(long long n) { return (n + kAdamChunk - 1) / kAdamChunk; }
 
 size_t adam_scratch_bytes(int count) {
     const size_t launches = (size_t)(count + kAdamCap - 1) / kAdamCap;
-    return 256 + (launches * 4 * kBlockSmsBound * sizeof(float) + 255) / 256 * 256;
+    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(float) + 255) / 256 * 256;
 }
 
 cudaError_t launch_adamw_norm(const AdamTensor* ts, int count, const AdamArgs& a, int* ctas, cudaStream_t s, bool pdl) {

@@ -13,11 +13,15 @@
 // r is formed again from x, y and g, in FP32: the rounded r is not read.
 //
 // Bound by bandwidth: 10 bytes a value forward, 16 backward, each array once.
-// A thread holds 8 consecutive channels (one 16-byte load of each operand) of
-// a row that stays in registers between its two row sums; a CTA takes several
-// rows at a time where they are narrow.  The three parameter gradients add up
-// in registers over the rows of a thread, then over the CTA's row slots in
-// shared memory, one partial row a CTA, joined in a fixed order.
+// A thread holds 8 consecutive channels (16 bytes of each operand) of a row
+// that stays in registers between its two row sums; a CTA takes several rows
+// at a time where they are narrow.  Where a CTA has more than one group of
+// rows to go through, the groups arrive by bulk copies in a ring of shared
+// memory, so that the loads run ahead of the row sums' barriers; a call with
+// few rows loads them directly (no barriers to set up: a decoding step).
+// The three parameter gradients add up in registers over the rows of a thread,
+// then over the CTA's row slots in shared memory, one partial row a CTA,
+// joined in a fixed order by a second kernel.
 #include <algorithm>
 
 #include "block_math.cuh"
@@ -74,28 +78,83 @@ __device__ __forceinline__ float row_sum(float v, float (*red)[kGnMaxWarps]) {
     return v;
 }
 
+// A ring of row groups in shared memory: slot k of the ring holds NOPS
+// operands of blockDim.y rows each, as they lie in memory.
+template <int NOPS>
+struct GnRing {
+    const uint4* src[NOPS];
+    long long T;
+    int nv, stages;
+    uint8_t* buf;
+    uint64_t* full;
+
+    __device__ __forceinline__ uint32_t op_bytes() const { return blockDim.y * (uint32_t)nv * 16u; }
+    // Thread 0: asks for row group `it` of this CTA (groups blockIdx.x, + gridDim.x, ...).
+    __device__ __forceinline__ void ask(int it) const {
+        const long long row = ((long long)blockIdx.x + (long long)it * gridDim.x) * blockDim.y;
+        if (row >= T) return;
+        const uint32_t bytes = (uint32_t)min((long long)blockDim.y, T - row) * (uint32_t)nv * 16u;
+        const int slot = it % stages;
+        mbar_arrive_expect_tx(&full[slot], NOPS * bytes);
+#pragma unroll
+        for (int k = 0; k < NOPS; ++k)
+            bulk_load(buf + ((size_t)slot * NOPS + k) * op_bytes(), src[k] + (size_t)row * nv, bytes, &full[slot]);
+    }
+    // Operand k of this thread's row, group of channels v.
+    __device__ __forceinline__ uint4 get(int it, int k, int v) const {
+        return *reinterpret_cast<const uint4*>(buf + ((size_t)(it % stages) * NOPS + k) * op_bytes() +
+                                               ((size_t)threadIdx.y * nv + v) * 16u);
+    }
+    __device__ __forceinline__ bool wait(int it) const {
+        return mbar_wait_bounded(&full[it % stages], (uint32_t)(it / stages) & 1u);
+    }
+};
+constexpr int kGnStagesMax = 4;
+
 // VEC: groups of 8 channels per thread (group threadIdx.x + k blockDim.x).
-template <bool Y, bool G, int VEC>
+// RING: the rows arrive in the ring; else one group of rows a CTA, loaded directly.
+template <bool Y, bool G, int VEC, bool RING>
 __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const GatedNormArgs a) {
+    constexpr int NOPS = 1 + Y + G;
     __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
+    __shared__ __align__(8) uint64_t full[kGnStagesMax];
+    extern __shared__ __align__(128) uint8_t buf[];
     pdl_trigger();
     pdl_wait();
     const int nv = a.D / 8;
     const float inv_d = 1.f / (float)a.D;
-    int turn = 0;   // without a branch there is one sum a row: its buffers take turns
-    for (long long base = (long long)blockIdx.x * blockDim.y; base < a.T; base += (long long)gridDim.x * blockDim.y, turn ^= 1) {
+    const bool first = threadIdx.x == 0 && threadIdx.y == 0;
+    GnRing<NOPS> ring;
+    if (RING) {
+        ring.src[0] = a.x;
+        if (Y) ring.src[Y] = a.y;
+        if (G) ring.src[Y + G] = a.g;
+        ring.T = a.T;
+        ring.nv = nv;
+        ring.stages = a.stages;
+        ring.buf = buf;
+        ring.full = full;
+        if (first) {
+            for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
+            for (int i = 0; i < a.stages; ++i) ring.ask(i);
+        }
+        __syncthreads();
+    }
+    bool lost = false;
+    int it = 0;
+    for (long long base = (long long)blockIdx.x * blockDim.y; base < a.T; base += (long long)gridDim.x * blockDim.y, ++it) {
         const long long row = base + threadIdx.y;
         uint4 qx[VEC], qy[VEC], qg[VEC];
+        if (RING) lost |= !ring.wait(it);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             const size_t o = (size_t)row * nv + v;
-            const bool on = row < a.T && v < nv;
             qx[k] = qy[k] = qg[k] = make_uint4(0u, 0u, 0u, 0u);
-            if (on) {
-                qx[k] = __ldg(a.x + o);
-                if (Y) qy[k] = __ldg(a.y + o);
-                if (G) qg[k] = __ldg(a.g + o);
+            if (row < a.T && v < nv) {
+                qx[k] = RING ? ring.get(it, 0, v) : __ldg(a.x + o);
+                if (Y) qy[k] = RING ? ring.get(it, Y, v) : __ldg(a.y + o);
+                if (G) qg[k] = RING ? ring.get(it, Y + G, v) : __ldg(a.g + o);
             }
         }
         float r[VEC][8], rstd1 = 0.f;
@@ -131,9 +190,18 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
         for (int k = 0; k < VEC; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(r[k][i], r[k][i], ss);
-        const float rstd2 = 1.f / sqrtf(row_sum(ss, red[Y ? 1 : turn]) * inv_d + a.eps);
+        const float rstd2 = 1.f / sqrtf(row_sum(ss, red[Y ? 1 : it & 1]) * inv_d + a.eps);
+        if (RING) {
+            // every thread has taken its operands (rows of one warp meet no barrier in their sums)
+            if (blockDim.x == 32) __syncthreads();
+            if (first) {
+                fence_proxy_async();
+                ring.ask(it + a.stages);
+            }
+        }
         if (row >= a.T) continue;
-        if (threadIdx.x == 0 && a.rstd != nullptr) a.rstd[row] = make_float2(rstd1, rstd2);
+        if (threadIdx.x == 0 && a.rstd != nullptr)
+            a.rstd[row] = lost ? make_float2(NAN, NAN) : make_float2(rstd1, rstd2);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
@@ -141,7 +209,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
             float gm[8], h[8];
             load8(a.gamma_pre, v, true, 1.f, gm);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = r[k][i] * rstd2 * gm[i];
+            for (int i = 0; i < 8; ++i) h[i] = lost ? NAN : r[k][i] * rstd2 * gm[i];
             const size_t o = (size_t)row * nv + v;
             if (Y) a.r[o] = pack8(r[k]);
             a.h[o] = pack8(h);
@@ -151,92 +219,122 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
 
 template <bool Y, bool G, int VEC>
 __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const GatedNormBwdArgs a) {
+    constexpr int NOPS = 3 + Y + G;
     __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
-    extern __shared__ __align__(16) float acc[];   // [3][rows][D]
+    __shared__ __align__(8) uint64_t full[kGnStagesMax];
+    extern __shared__ __align__(128) uint8_t buf[];   // the ring, then the sums [3][rows][D]
     pdl_trigger();
     pdl_wait();
     const GatedNormArgs& f = a.f;
     const int nv = f.D / 8;
     const float inv_d = 1.f / (float)f.D;
+    const bool first = threadIdx.x == 0 && threadIdx.y == 0;
+    GnRing<NOPS> ring;
+    ring.src[0] = f.x;
+    ring.src[1] = a.dh;
+    ring.src[2] = a.dr != nullptr ? a.dr : a.dh;   // without dr its place is not read
+    if (Y) ring.src[2 + Y] = f.y;
+    if (G) ring.src[2 + Y + G] = f.g;
+    ring.T = f.T;
+    ring.nv = nv;
+    ring.stages = f.stages;
+    ring.buf = buf;
+    ring.full = full;
+    if (first) {
+        for (int i = 0; i < f.stages; ++i) mbar_init(&full[i], 1);
+        for (int i = 0; i < f.stages; ++i) ring.ask(i);
+    }
+    __syncthreads();
+    // a thread's channels are the same in every row: so are its vectors
+    float gm[VEC][8], gp[VEC][8], sc[VEC][8];
     float dpre[VEC][8], dpost[VEC][8], dscale[VEC][8];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k)
+    for (int k = 0; k < VEC; ++k) {
+        const int v = threadIdx.x + k * blockDim.x;
+        load8(f.gamma_pre, v, v < nv, 1.f, gm[k]);
+        if (Y) {
+            load8(f.gamma_post, v, v < nv, 1.f, gp[k]);
+            load8(f.scale, v, v < nv, 1.f, sc[k]);
+        }
 #pragma unroll
         for (int i = 0; i < 8; ++i) dpre[k][i] = dpost[k][i] = dscale[k][i] = 0.f;
-    int turn = 0;
-    for (long long base = (long long)blockIdx.x * blockDim.y; base < f.T; base += (long long)gridDim.x * blockDim.y, turn ^= 1) {
+    }
+    bool lost = false;
+    int it = 0;
+    for (long long base = (long long)blockIdx.x * blockDim.y; base < f.T; base += (long long)gridDim.x * blockDim.y, ++it) {
         const long long row = base + threadIdx.y;
         uint4 qx[VEC], qy[VEC], qg[VEC], qr[VEC], qh[VEC];
         float2 rs = make_float2(0.f, 0.f);
-        if (row < f.T) rs = __ldg(a.f.rstd + row);
+        if (row < f.T) rs = __ldg(f.rstd + row);
+        lost |= !ring.wait(it);
+        if (lost) rs = make_float2(NAN, NAN);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
-            const size_t o = (size_t)row * nv + v;
             qx[k] = qy[k] = qg[k] = qr[k] = qh[k] = make_uint4(0u, 0u, 0u, 0u);
             if (row < f.T && v < nv) {
-                qx[k] = __ldg(f.x + o);
-                qh[k] = __ldg(a.dh + o);
-                if (a.dr != nullptr) qr[k] = __ldg(a.dr + o);
-                if (Y) qy[k] = __ldg(f.y + o);
-                if (G) qg[k] = __ldg(f.g + o);
+                qx[k] = ring.get(it, 0, v);
+                qh[k] = ring.get(it, 1, v);
+                if (a.dr != nullptr) qr[k] = ring.get(it, 2, v);
+                if (Y) qy[k] = ring.get(it, 2 + Y, v);
+                if (G) qg[k] = ring.get(it, 2 + Y + G, v);
             }
         }
         // q = r rstd2, a = dh gamma_pre, mean(a q)
-        float q[VEC][8], s = 0.f;
+        float q[VEC][8], ge[VEC][8], dge[VEC][8], s = 0.f;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            const int v = threadIdx.x + k * blockDim.x;
-            float dh[8], gm[8];
+            float dh[8];
             unpack8(qx[k], q[k]);
             unpack8(qh[k], dh);
-            load8(f.gamma_pre, v, v < nv, 1.f, gm);
             if (Y) {
-                float y[8], g[8], gp[8], sc[8];
+                float y[8], g[8];
                 unpack8(qy[k], y);
                 unpack8(qg[k], g);
-                load8(f.gamma_post, v, v < nv, 1.f, gp);
-                load8(f.scale, v, v < nv, 1.f, sc);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    q[k][i] = fmaf(sc[i] * (G ? gn_gelu(g[i]) : 1.f), y[i] * rs.x * gp[i], q[k][i]);
+                for (int i = 0; i < 8; ++i) {
+                    ge[k][i] = 1.f;
+                    dge[k][i] = 0.f;
+                    if (G) gn_gelu_grad(g[i], ge[k][i], dge[k][i]);
+                    q[k][i] = fmaf(sc[k][i] * ge[k][i], y[i] * rs.x * gp[k][i], q[k][i]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 q[k][i] *= rs.y;
                 dpre[k][i] = fmaf(dh[i], q[k][i], dpre[k][i]);
-                s = fmaf(dh[i] * gm[i], q[k][i], s);
+                s = fmaf(dh[i] * gm[k][i], q[k][i], s);
             }
         }
-        const float mean = row_sum(s, red[Y ? 0 : turn]) * inv_d;
+        const float mean = row_sum(s, red[Y ? 0 : it & 1]) * inv_d;
+        // every thread has taken its operands (rows of one warp meet no barrier in their sums)
+        if (blockDim.x == 32) __syncthreads();
+        if (first) {
+            fence_proxy_async();
+            ring.ask(it + f.stages);
+        }
         float dx[VEC][8];
         s = 0.f;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
-            float dh[8], dr[8], gm[8];
+            float dh[8], dr[8];
             unpack8(qh[k], dh);
             unpack8(qr[k], dr);
-            load8(f.gamma_pre, v, v < nv, 1.f, gm);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dx[k][i] = fmaf(rs.y, dh[i] * gm[i] - q[k][i] * mean, dr[i]);
+            for (int i = 0; i < 8; ++i) dx[k][i] = fmaf(rs.y, dh[i] * gm[k][i] - q[k][i] * mean, dr[i]);
             if (row < f.T && v < nv) a.dx[(size_t)row * nv + v] = pack8(dx[k]);
             if (Y) {
-                float y[8], g[8], gp[8], sc[8], dg[8];
+                float y[8], dg[8];
                 unpack8(qy[k], y);
-                unpack8(qg[k], g);
-                load8(f.gamma_post, v, v < nv, 1.f, gp);
-                load8(f.scale, v, v < nv, 1.f, sc);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    float ge = 1.f, dge = 0.f;
-                    if (G) gn_gelu_grad(g[i], ge, dge);
-                    const float p = y[i] * rs.x, n = p * gp[i], t = dx[k][i] * sc[i];
-                    dscale[k][i] = fmaf(dx[k][i] * ge, n, dscale[k][i]);
-                    dg[i] = t * n * dge;
-                    const float dn = t * ge;
+                    const float p = y[i] * rs.x, n = p * gp[k][i], t = dx[k][i] * sc[k][i];
+                    dscale[k][i] = fmaf(dx[k][i] * ge[k][i], n, dscale[k][i]);
+                    dg[i] = t * n * dge[k][i];
+                    const float dn = t * ge[k][i];
                     dpost[k][i] = fmaf(dn, p, dpost[k][i]);
-                    dx[k][i] = dn * gp[i];   // b
+                    dx[k][i] = dn * gp[k][i];   // b
                     s = fmaf(dx[k][i], p, s);
                 }
                 if (G && row < f.T && v < nv) a.dg[(size_t)row * nv + v] = pack8(dg);
@@ -255,7 +353,10 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
             }
         }
     }
-    // the CTA's row slots in order, then one partial row of each sum
+    // the CTA's row slots in order, then one partial row of each sum (the ring
+    // is drained: every group asked for has been waited for)
+    __syncthreads();
+    float* acc = reinterpret_cast<float*>(buf);
     const int sums = Y ? 3 : 1;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
@@ -282,6 +383,29 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     }
 }
 
+// Sums blockIdx.y of the partial rows: 32 columns a CTA, warp w the rows w,
+// w + 32, ..., the warps' sums then in order.
+__global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const float* __restrict__ part, int parts, int D,
+                                                              float* o0, float* o1, float* o2) {
+    __shared__ float acc[32][33];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    const float* p = part + (size_t)blockIdx.y * parts * D;
+    float s = 0.f;
+    if (c < D) {
+#pragma unroll 4
+        for (int i = w; i < parts; i += 32) s += __ldcg(p + (size_t)i * D + c);
+    }
+    acc[w][lane] = s;
+    __syncthreads();
+    if (w != 0 || c >= D) return;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s += acc[i][lane];
+    (blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2)[c] = s;
+}
+
 struct GnShape {
     int vec;
     dim3 block;
@@ -297,19 +421,43 @@ GnShape gn_shape(int D) {
     return s;
 }
 
-template <bool Y, bool G>
-cudaError_t gn_fwd(const GatedNormArgs& a, cudaStream_t s) {
-    const GnShape sh = gn_shape(a.D);
-    const long long groups = (a.T + sh.block.y - 1) / sh.block.y;
-    const long long grid = std::min<long long>(groups, 16LL * block_gemm_sms());
-    if (sh.vec == 1)
-        return launch_ex(gated_norm_fwd_kernel<Y, G, 1>, dim3((unsigned)grid), sh.block, 0, s, false, a);
-    return launch_ex(gated_norm_fwd_kernel<Y, G, 2>, dim3((unsigned)grid), sh.block, 0, s, false, a);
+// CTAs per SM that the registers leave room for, and the ring's stages: what
+// fits beside them, two at least (a group of rows in flight while one is used).
+int gn_ctas_per_sm(const GnShape& sh, int threads_per_sm) {
+    return std::max(1, threads_per_sm / (int)(sh.block.x * sh.block.y));
+}
+int gn_stages(size_t group_bytes, int ctas_per_sm) {
+    const size_t room = 216 * 1024 / ctas_per_sm;
+    return (int)std::max<size_t>(2, std::min<size_t>(kGnStagesMax, room / group_bytes));
 }
 
 template <bool Y, bool G, int VEC>
-cudaError_t gn_bwd_as(const GatedNormBwdArgs& a, const GnShape& sh, int ctas, cudaStream_t s) {
-    const size_t smem = (size_t)(Y ? 3 : 1) * sh.block.y * a.f.D * sizeof(float);
+cudaError_t gn_fwd_as(GatedNormArgs a, const GnShape& sh, cudaStream_t s) {
+    const long long groups = (a.T + sh.block.y - 1) / sh.block.y;
+    const int per_sm = gn_ctas_per_sm(sh, VEC == 1 ? 1024 : 512);
+    const long long resident = (long long)per_sm * block_gemm_sms();
+    // one group of rows a CTA needs no ring
+    if (groups <= resident)
+        return launch_ex(gated_norm_fwd_kernel<Y, G, VEC, false>, dim3((unsigned)groups), sh.block, 0, s, false, a);
+    const size_t group = (size_t)(1 + Y + G) * sh.block.y * a.D * 2;
+    a.stages = gn_stages(group, per_sm);
+    auto* fn = gated_norm_fwd_kernel<Y, G, VEC, true>;
+    const size_t smem = group * a.stages;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(fn, dim3((unsigned)resident), sh.block, smem, s, false, a);
+}
+template <bool Y, bool G>
+cudaError_t gn_fwd(const GatedNormArgs& a, cudaStream_t s) {
+    const GnShape sh = gn_shape(a.D);
+    return sh.vec == 1 ? gn_fwd_as<Y, G, 1>(a, sh, s) : gn_fwd_as<Y, G, 2>(a, sh, s);
+}
+
+template <bool Y, bool G, int VEC>
+cudaError_t gn_bwd_as(GatedNormBwdArgs a, const GnShape& sh, int ctas, cudaStream_t s) {
+    const size_t group = (size_t)(3 + Y + G) * sh.block.y * a.f.D * 2;
+    a.f.stages = gn_stages(group, gn_ctas_per_sm(sh, Y ? 512 : 1024));
+    const size_t smem = std::max(group * a.f.stages, (size_t)(Y ? 3 : 1) * sh.block.y * a.f.D * sizeof(float));
     auto* fn = gated_norm_bwd_kernel<Y, G, VEC>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -323,9 +471,10 @@ cudaError_t gn_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s) {
 
 }  // namespace
 
-int gated_norm_bwd_ctas(long long T, int D, int sms) {
+int gated_norm_bwd_ctas(long long T, int D, bool branch, int sms) {
     const GnShape sh = gn_shape(D);
-    return (int)std::max(1LL, std::min<long long>((T + sh.block.y - 1) / sh.block.y, 4LL * sms));
+    return (int)std::max(1LL, std::min<long long>((T + sh.block.y - 1) / sh.block.y,
+                                                  (long long)gn_ctas_per_sm(sh, branch ? 512 : 1024) * sms));
 }
 
 cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s) {
@@ -335,6 +484,11 @@ cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s) {
 cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s) {
     if (a.f.y == nullptr) return gn_bwd<false, false>(a, ctas, s);
     return a.f.g == nullptr ? gn_bwd<true, false>(a, ctas, s) : gn_bwd<true, true>(a, ctas, s);
+}
+cudaError_t launch_gated_norm_sum(const float* part, int parts, int D, bool branch, float* o0, float* o1, float* o2,
+                                  cudaStream_t s, bool pdl) {
+    return launch_ex(gated_norm_sum_kernel, dim3((unsigned)((D + 31) / 32), branch ? 3u : 1u), dim3(1024), 0, s, pdl,
+                     part, parts, D, o0, o1, o2);
 }
 
 }  // namespace lrs

@@ -588,6 +588,7 @@ struct GatedNormArgs {
     uint4* r;
     uint4* h;
     float2* rstd;                // [T] of y, of r
+    int stages;                  // of the ring (filled by the launchers)
 };
 struct GatedNormBwdArgs {
     GatedNormArgs f;             // the forward's inputs and rstd
@@ -598,7 +599,9 @@ struct GatedNormBwdArgs {
     uint4* dg;
     float* part;                 // [3 (1 without a branch)][ctas][D]: dgamma_pre, dgamma_post, dscale
 };
-int gated_norm_bwd_ctas(long long T, int D, int sms);
+int gated_norm_bwd_ctas(long long T, int D, bool branch, int sms);
+cudaError_t launch_gated_norm_sum(const float* part, int parts, int D, bool branch, float* o0, float* o1, float* o2,
+                                  cudaStream_t s, bool pdl);
 cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s);
 cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s);
 
@@ -611,6 +614,7 @@ using AdamTensor = lrs_adamw_tensor;
 constexpr int kAdamCapSmall = 32, kAdamCap = 400;
 struct AdamArgs {
     double beta1, beta2;
+    float b1, c1, b2, c2;        // the betas and 1 - beta, rounded once
     float eps, max_norm;
     const float* lr;
     int32_t* step;

@@ -479,8 +479,8 @@ int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forwa
  * Products of BF16 values accumulate in FP32 on the tensor cores; sums of
  * exponentials are FP32, the sum of the losses FP64, all in a fixed order.
  * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, softcap
- * negative or not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8, or sizes
- * beyond 2^31 rows or tiles), LRS_ERR_CUDA. */
+ * negative or not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8, T or V
+ * over 2^23, D over 2^16), LRS_ERR_CUDA. */
 int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T, int V, int D, float softcap,
                       float* loss, float* lse, float* total, void* scratch, cudaStream_t stream);
 

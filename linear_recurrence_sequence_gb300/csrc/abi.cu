@@ -1080,10 +1080,9 @@ size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int check_ce_shape(int T, int V, int D) {
     if (T < 1 || V < 1 || D < 1) return LRS_ERR_ARG;
     if (D % 8 != 0) return LRS_ERR_UNSUPPORTED;
-    const long long lim = 1LL << 40;
-    if ((long long)T * D > lim || (long long)V * D > lim || (long long)V + 512 > 0x7fffffffLL ||
-        (long long)T + 512 > 0x7fffffffLL || (long long)ce_m_tiles(T) * ce_n_tiles(V) > 0x7fffffffLL ||
-        (long long)ce_m_tiles(V) * ce_n_tiles(D) > 0x7fffffffLL || (long long)ce_m_tiles(T) * ce_n_tiles(D) > 0x7fffffffLL)
+    // a tile's sum over the longest axis stays far inside the bounded waits
+    if (T > (1 << 23) || V > (1 << 23) || D > (1 << 16)) return LRS_ERR_UNSUPPORTED;
+    if ((long long)ce_m_tiles(T) * ce_n_tiles(V) > 0x7fffffffLL)
         return LRS_ERR_UNSUPPORTED;
     return LRS_OK;
 }
@@ -1318,7 +1317,7 @@ int gated_norm_workspace_bytes(int T, int D, size_t* saved_bytes, size_t* scratc
     if (st != LRS_OK) return st;
     if (saved_bytes != nullptr) *saved_bytes = up256((size_t)T * sizeof(float2));
     if (scratch_bytes != nullptr)
-        *scratch_bytes = up256((size_t)3 * D * sizeof(float) *
+        *scratch_bytes = up256((size_t)2 * D * sizeof(float) *
                                 std::max(gated_norm_bwd_ctas(T, D, true, kBlockSmsBound),
                                          gated_norm_bwd_ctas(T, D, false, kBlockSmsBound)));
     return LRS_OK;
@@ -1364,7 +1363,7 @@ int gated_norm_backward(const void* dr, const void* dh, const void* x, const voi
     const int ctas = gated_norm_bwd_ctas(T, D, branch, block_gemm_sms());
     LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_bwd(a, ctas, stream));
     LRS_LAUNCH(KID_GATED_NORM_SUM, stream,
-               launch_gated_norm_sum(a.part, ctas, D, branch, dgamma_pre, dgamma_post, dscale, stream, pdl_ok()));
+               launch_gated_norm_sum(a, ctas, dgamma_pre, dgamma_post, dscale, stream, pdl_ok()));
     return LRS_OK;
 }
 

@@ -14,12 +14,17 @@
 // the TMA fills what lies outside a matrix with zeros and clips what is stored
 // there; columns past the vocabulary are zeroed in dz.
 //
-// Roles as in the block's contractions: warp 8 streams 64-wide K slices of
-// both operands by TMA (128-byte swizzle) into a ring of four stages, one
-// thread of warp 9 issues tcgen05.mma (M 128, N 256, K 16), warps 0-7 drain
-// the accumulators, two of which alternate so that a tile's epilogue runs
-// under the next tile's MMAs.  Every wait is bounded.
+// CTA pairs (cta_group::2) take 256 x 256 tiles: each CTA loads its 128 rows
+// of A and half of B's slice, so the pair reads every operand value of its tile
+// once and shared memory holds six 64-wide K slices of it.  In each CTA warp 8
+// streams the slices by TMA (128-byte swizzle), completing on the even CTA's
+// barriers; one thread of the even CTA's warp 9 issues tcgen05.mma (M 256,
+// N 256, K 16) for both and frees the slices by commits to both; warps 0-7
+// drain the CTA's 128 accumulator rows, of which there are two sets in turn so
+// that a tile's epilogue runs under the next tile's MMAs.  Every wait is
+// bounded.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 #include "tmap.cuh"
@@ -33,11 +38,11 @@ constexpr int kCeEpiWarps = 8;
 constexpr int kCeThreads = 32 * (kCeEpiWarps + 2);
 constexpr int kCeProducer = kCeEpiWarps, kCeIssuer = kCeEpiWarps + 1;
 constexpr int kCeK = 64;
-constexpr int kCeM = 128;
+constexpr int kCeM = 256;         // rows of a pair's tile: 128 a CTA
 constexpr int kCeN = 256;
-constexpr int kCeStages = 4;      // ring stages (3 where dz's remainders are staged too)
-constexpr uint32_t kCeABytes = kCeM * 128;
-constexpr uint32_t kCeBBytes = kCeN * 128;
+constexpr int kCeStages = 6;      // ring stages (5 where dz's remainders are staged too)
+constexpr uint32_t kCeABytes = 128 * 128;   // of one CTA: 128 rows of A, 128 of B
+constexpr uint32_t kCeBBytes = 128 * 128;
 constexpr uint32_t kCeStageBytes = kCeABytes + kCeBBytes;
 constexpr uint32_t kCeTmemCols = 2 * kCeN;
 constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store box (64-byte swizzle)
@@ -59,13 +64,14 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 
 struct CeItem {
     int mt, nt, s, k0, k1;
+    int m0;   // this CTA's first row
 };
 
 // Work item i.  NT: m runs fastest inside a group of row tiles whose h stays
 // in the L2, so that a tile of w is read by the whole group at about the same
 // time.  NN, TN: n (the width D) runs fastest, so that the D tiles that read
 // the same panel of dz run together.
-__device__ __forceinline__ CeItem ce_item(const CeGemmArgs& a, int i) {
+__device__ __forceinline__ CeItem ce_item(const CeGemmArgs& a, int i, int rank) {
     CeItem it;
     if (a.layout == kBgNT) {
         const int per = a.group * a.n_tiles;
@@ -80,6 +86,7 @@ __device__ __forceinline__ CeItem ce_item(const CeGemmArgs& a, int i) {
         it.mt = r % a.m_tiles;
         it.s = r / a.m_tiles;
     }
+    it.m0 = it.mt * kCeM + 128 * rank;
     it.k0 = (int)((long long)a.ksteps * it.s / a.splits);
     it.k1 = (int)((long long)a.ksteps * (it.s + 1) / a.splits);
     return it;
@@ -92,7 +99,7 @@ __device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a
 // Columns past the vocabulary do not count; the target's logit is kept.
 template <bool CAP>
 __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& it, int row, uint32_t taddr, int half) {
-    const int t = it.mt * kCeM + row;
+    const int t = it.m0 + row;
     const int c0 = half * (kCeN / 2);
     const int v0 = it.nt * kCeN + c0;            // vocabulary index of the first column
     const int nv = min(kCeN / 2, a.N - v0);      // columns that count (may be <= 0)
@@ -139,10 +146,12 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                    const __grid_constant__ CUtensorMap tm_s2, const CeGemmArgs a) {
     constexpr int S = ce_stages(EPI);
     extern __shared__ uint8_t ce_raw[];
+    // s_full and s_free are used in the even CTA, the others in both
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_acc[2], s_free[2], s_fin;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank();
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(ce_raw) + 1023u) & ~uintptr_t(1023));
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; ++i) {
@@ -151,18 +160,19 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_acc[i], 1);
-            mbar_init(&s_free[i], kCeEpiWarps);
+            mbar_init(&s_free[i], 2 * kCeEpiWarps);
         }
         mbar_init(&s_fin, 1);
         s_abort = 0;
     }
     if (warp == kCeIssuer) {
-        tmem_alloc(&s_tmem, kCeTmemCols);
+        tmem_alloc2(&s_tmem, kCeTmemCols);
         tmem_fence_before_sync();
     }
     pdl_trigger();
     pdl_wait();
     __syncthreads();
+    cluster_sync();   // the pair's barriers and tensor memory exist
     tmem_fence_after_sync();
     const uint32_t tmem = s_tmem;
     volatile int* abort_flag = &s_abort;
@@ -170,13 +180,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         *abort_flag = 1;
         atomicOr(a.status, kStatusTimeout);
     };
-    const int w0 = (int)blockIdx.x, wstep = (int)gridDim.x;
+    const int w0 = (int)blockIdx.x / 2, wstep = (int)gridDim.x / 2;   // the same items in both CTAs
 
     if (warp == kCeProducer) {
         if (lane == 0) {
             uint32_t n = 0;
             for (int w = w0; w < a.n_items && !*abort_flag; w += wstep) {
-                const CeItem it = ce_item(a, w);
+                const CeItem it = ce_item(a, w, rank);
                 for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
                     const int slot = (int)(n % S);
                     if (n >= (uint32_t)S && !mbar_wait_bounded(&s_empty[slot], ((n / S) - 1) & 1u)) {
@@ -189,39 +199,42 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     // the remainders of dz follow its leading parts along K
                     const bool second = a.parts == 2 && ks >= a.part_steps;
                     const int k0 = kCeK * (second ? ks - a.part_steps : ks);
+                    const int n0 = it.nt * kCeN + 128 * rank;
                     const CUtensorMap* ta = second ? &tm_a2 : &tm_a;
-                    mbar_arrive_expect_tx(&s_full[slot], kCeStageBytes);
-                    if (LAYOUT == kBgNT) {
-                        tma_load_2d(sa, ta, k0, it.mt * kCeM, &s_full[slot]);
-                        tma_load_2d(sb, &tm_b, k0, a.b_row + it.nt * kCeN, &s_full[slot]);
-                        tma_load_2d(sb + kCeBBytes / 2, &tm_b, k0, a.b_row + it.nt * kCeN + 128, &s_full[slot]);
+                    // both CTAs' bytes are announced by the even one (the odd one's may land first)
+                    if (rank == 0) mbar_arrive_expect_tx(&s_full[slot], 2 * kCeStageBytes);
+                    const uint32_t bar = cluster_map(&s_full[slot], 0);
+                    if (LAYOUT == kBgTN) {
+                        tma2_load_2d(sa, ta, it.m0, k0, bar);
+                        tma2_load_2d(sa + 8192, ta, it.m0 + 64, k0, bar);
                     } else {
-                        if (LAYOUT == kBgNN) {
-                            tma_load_2d(sa, ta, k0, it.mt * kCeM, &s_full[slot]);
-                        } else {
-                            tma_load_2d(sa, ta, it.mt * kCeM, k0, &s_full[slot]);
-                            tma_load_2d(sa + 8192, ta, it.mt * kCeM + 64, k0, &s_full[slot]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < kCeN / 64; ++j)
-                            tma_load_2d(sb + (size_t)j * 8192, &tm_b, it.nt * kCeN + 64 * j, a.b_row + k0,
-                                        &s_full[slot]);
+                        tma2_load_2d(sa, ta, k0, it.m0, bar);
+                    }
+                    if (LAYOUT == kBgNT) {
+                        tma2_load_2d(sb, &tm_b, k0, a.b_row + n0, bar);
+                    } else {
+                        tma2_load_2d(sb, &tm_b, n0, a.b_row + k0, bar);
+                        tma2_load_2d(sb + 8192, &tm_b, n0 + 64, a.b_row + k0, bar);
                     }
                 }
             }
-            // copies still in flight land before the CTA may exit
+            // copies still in flight land (the even CTA's barriers count both CTAs'), and the last slices
+            // have been read, before the CTA may exit
             const uint32_t lo = n > (uint32_t)S ? n - S : 0;
-            for (uint32_t j = lo; j < n; ++j) mbar_wait_bounded(&s_full[j % S], (j / S) & 1u);
+            if (rank == 0)
+                for (uint32_t j = lo; j < n; ++j) mbar_wait_bounded(&s_full[j % S], (j / S) & 1u);
+            for (uint32_t j = lo; j < n; ++j) mbar_wait_bounded(&s_empty[j % S], (j / S) & 1u);
         }
     } else if (warp == kCeIssuer) {
-        if (lane == 0) {
+        if (lane == 0 && rank == 0) {
             constexpr uint32_t idesc = umma_idesc_bf16(kCeM, kCeN) | (LAYOUT == kBgTN ? (1u << 15) : 0u) |
                                        (LAYOUT != kBgNT ? (1u << 16) : 0u);
             uint32_t n = 0, item = 0;
             for (int w = w0; w < a.n_items && !*abort_flag; w += wstep, ++item) {
-                const CeItem it = ce_item(a, w);
+                const CeItem it = ce_item(a, w, rank);
                 const uint32_t buf = item & 1u;
-                if (item >= 2 && !mbar_wait_bounded(&s_free[buf], ((item >> 1) - 1) & 1u)) {
+                // both CTAs' epilogues have drained this accumulator's previous tile
+                if (item >= 2 && !mbar_wait_cluster(&s_free[buf], ((item >> 1) - 1) & 1u)) {
                     fail();
                     break;
                 }
@@ -230,7 +243,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 bool ok = true;
                 for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
                     const int slot = (int)(n % S);
-                    if (!mbar_wait_bounded(&s_full[slot], (n / S) & 1u)) {
+                    if (!mbar_wait_cluster(&s_full[slot], (n / S) & 1u)) {
                         fail();
                         ok = false;
                         break;
@@ -244,30 +257,31 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                                                             : umma_desc_sw128(sa + 32u * kk);
                         const uint64_t db = LAYOUT == kBgNT ? umma_desc_sw128(sb + 32u * kk)
                                                             : umma_desc_sw128_mn(sb + 2048u * kk, 8192u);
-                        umma_bf16(acc_t, da, db, idesc, ks > it.k0 || kk > 0);
+                        umma2_bf16(acc_t, da, db, idesc, ks > it.k0 || kk > 0);
                     }
-                    umma_commit(&s_empty[slot]);
+                    umma2_commit(&s_empty[slot]);
                 }
                 if (!ok) break;
-                umma_commit(&s_acc[buf]);
+                umma2_commit(&s_acc[buf]);
             }
-            umma_commit(&s_fin);
+            // every MMA issued by this thread has completed before the columns are released
+            umma2_commit_own(&s_fin);
             mbar_wait_bounded(&s_fin, 0);
         }
     } else {
-        // epilogue warps: rows 32 (warp % 4) .. + 31 of the tile, column half warp / 4
+        // epilogue warps: rows 32 (warp % 4) .. + 31 of the CTA's 128, column half warp / 4
         const int q4 = warp & 3, hf = warp >> 2;
         const int row = 32 * q4 + lane;
         uint8_t* stg = ring + (size_t)S * kCeStageBytes + (size_t)warp * ce_stage_warp(EPI);
         uint32_t chunk = 0, item = 0;
         for (int w = w0; w < a.n_items && !*abort_flag; w += wstep, ++item) {
-            const CeItem it = ce_item(a, w);
+            const CeItem it = ce_item(a, w, rank);
             const uint32_t buf = item & 1u;
             // what a row needs besides its logits is fetched while the tile is computed
             float wgt = 0.f, lse2 = 0.f;
             long long tgt = -1;
             if (EPI == kCeDz || EPI == kCeDz2) {
-                const int t = it.mt * kCeM + row;
+                const int t = it.m0 + row;
                 if (t < a.M) {
                     const long long tg = a.target[t];
                     tgt = tg - a.b_row - (long long)it.nt * kCeN;
@@ -285,7 +299,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             if (EPI == kCeStats) {
                 ce_epi_stats<CAP>(a, it, row, taddr, hf);
             } else if (EPI == kCeF32) {
-                const long long r = (long long)it.mt * kCeM + row;
+                const long long r = (long long)it.m0 + row;
                 float* o = a.part + ((size_t)it.s * a.part_rows + (size_t)r) * a.N + (size_t)it.nt * kCeN;
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
                     float v[2][16];
@@ -307,8 +321,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             } else {
                 // BF16 results by TMA stores from swizzled staging, 32 columns at a time
                 constexpr int kBoxes = EPI == kCeDz2 ? 2 : 1;
-                const int y = a.s_row + it.mt * kCeM + 32 * q4;
-                const bool store = it.mt * kCeM + 32 * q4 < a.M;   // rows past the matrix are clipped by the TMA
+                const int y = a.s_row + it.m0 + 32 * q4;
+                const bool store = it.m0 + 32 * q4 < a.M;   // rows past the matrix are clipped by the TMA
                 const int nv = a.N - it.nt * kCeN;                 // columns of this tile inside the matrix
 #pragma unroll 1
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32, ++chunk) {
@@ -361,15 +375,17 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             }
             tmem_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_free[buf]);
+            if (lane == 0) mbar_arrive_cluster(cluster_map(&s_free[buf], 0));
         }
         if (lane == 0) bulk_wait_all();   // every store has completed before the CTA may exit
     }
     __syncthreads();
+    cluster_sync();   // neither CTA leaves, or gives its columns back, while the other may still use them
     if (warp == kCeIssuer) {
         tmem_fence_after_sync();
-        tmem_dealloc(tmem, kCeTmemCols);
+        tmem_dealloc2(tmem, kCeTmemCols);
     }
+    cluster_sync();
 }
 
 // (m, s) of a row over two sets of columns.
@@ -505,6 +521,8 @@ bool ce_map(CUtensorMap* map, const void* ptr, long long cols, long long rows, l
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int ce_pairs() { return std::max(1, block_gemm_sms() / 2); }
+
 template <int LAYOUT, int EPI, bool CAP>
 cudaError_t ce_launch(const CUtensorMap& ta, const CUtensorMap& ta2, const CUtensorMap& tb, const CUtensorMap& ts,
                       const CUtensorMap& ts2, const CeGemmArgs& a, cudaStream_t s, bool pdl) {
@@ -512,8 +530,34 @@ cudaError_t ce_launch(const CUtensorMap& ta, const CUtensorMap& ta2, const CUten
     constexpr size_t smem = ce_smem(EPI);
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int grid = std::min(block_gemm_sms(), a.n_items);
-    return launch_ex(fn, dim3((unsigned)grid), dim3(kCeThreads), smem, s, pdl, ta, ta2, tb, ts, ts2, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kCeThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    // as many pairs as fit at once (asked once per device: the query is slow next to a launch)
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int pairs = cached[dev].load(std::memory_order_relaxed);
+    if (pairs < 1) {
+        cfg.gridDim = dim3(2);
+        if (cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg) != cudaSuccess || pairs < 1) pairs = ce_pairs();
+        cached[dev].store(pairs, std::memory_order_relaxed);
+    }
+    cfg.gridDim = dim3(2u * (unsigned)std::min(pairs, a.n_items));
+    if (pdl) {
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 2;
+    }
+    return cudaLaunchKernelEx(&cfg, fn, ta, ta2, tb, ts, ts2, a);
 }
 
 }  // namespace
@@ -522,10 +566,10 @@ int ce_m_tiles(long long M) { return (int)((M + kCeM - 1) / kCeM); }
 int ce_n_tiles(long long N) { return (int)((N + kCeN - 1) / kCeN); }
 
 // Splits of the K axis when a contraction has fewer tiles than the GPU has
-// SMs: as many as fill the SMs, each at least four K steps long.
+// pairs of SMs: as many as fill them, each at least four K steps long.
 int ce_splits(long long M, long long N, long long K, int sms) {
     const long long tiles = (long long)ce_m_tiles(M) * ce_n_tiles(N), steps = (K + kCeK - 1) / kCeK;
-    return (int)std::max(1LL, std::min<long long>({sms / tiles, steps / 4, kCeSplitsMax}));
+    return (int)std::max(1LL, std::min<long long>({sms / 2 / tiles, steps / 4, kCeSplitsMax}));
 }
 
 // A [M][K] (NT, NN) or [K][M] (TN) with row stride lda; A2: its remainders
@@ -542,9 +586,9 @@ cudaError_t launch_ce_gemm(const CeGemmArgs& in, const void* A, const void* A2, 
     if (a.layout == kBgTN)
         ok = ce_map(&ta, A, lda, K, lda, 64, 64, sw) && (a.parts == 1 || ce_map(&ta2, A2, lda, K, lda, 64, 64, sw));
     else
-        ok = ce_map(&ta, A, lda, a.M, lda, 64, kCeM, sw) &&
-             (a.parts == 1 || ce_map(&ta2, A2, lda, a.M, lda, 64, kCeM, sw));
-    ok = ok && (a.layout == kBgNT ? ce_map(&tb, B, K, brows, K, 64, kCeN / 2, sw)
+        ok = ce_map(&ta, A, lda, a.M, lda, 64, 128, sw) &&
+             (a.parts == 1 || ce_map(&ta2, A2, lda, a.M, lda, 64, 128, sw));
+    ok = ok && (a.layout == kBgNT ? ce_map(&tb, B, K, brows, K, 64, 128, sw)
                                   : ce_map(&tb, B, a.N, brows, a.N, 64, 64, sw));
     if (!ok) return cudaErrorInvalidValue;
     if (a.parts == 1) ta2 = ta;

@@ -7,9 +7,11 @@
 //
 // Backward for dr, dh (means over the row):
 //   a = dh gamma_pre, dx = dr + rstd2 (a - q mean(a q))
-//   dg = dx scale n GeLU'(g);  dn = dx scale GeLU(g);  b = dn gamma_post
-//   dy = rstd1 (b - p mean(b p))
-//   dgamma_pre = sum dh q, dscale = sum dx GeLU(g) n, dgamma_post = sum dn p
+//   e = dx GeLU(g);  dg = dx scale gamma_post p GeLU'(g)
+//   b = e scale gamma_post, dy = rstd1 (b - p mean(b p))
+//   dgamma_pre = sum dh q, A = sum e p, dscale = gamma_post A, dgamma_post = scale A
+// (a channel's scale and gamma_post leave the sum over the rows, so the two
+// gradients share one sum).
 // r is formed again from x, y and g, in FP32: the rounded r is not read.
 //
 // Bound by bandwidth: 10 bytes a value forward, 16 backward, each array once.
@@ -19,12 +21,11 @@
 // rows to go through, the groups arrive by bulk copies in a ring of shared
 // memory, so that the loads run ahead of the row sums' barriers; a call with
 // few rows loads them directly (no barriers to set up: a decoding step).
-// The three parameter gradients add up in registers over the rows of a thread,
-// then over the CTA's row slots in shared memory, one partial row a CTA,
-// joined in a fixed order by a second kernel.
+// The two sums add up in registers over the rows of a thread, then over the
+// CTA's row slots in shared memory, one partial row a CTA, joined in a fixed
+// order by a second kernel.
 #include <algorithm>
 
-#include "block_math.cuh"
 #include "kernels.cuh"
 
 namespace lrs {
@@ -55,12 +56,34 @@ __device__ __forceinline__ void load8(const float* p, int v, bool on, float fill
     o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
 }
 
-// GeLU and its derivative, zero where the shared form clamps its exponent
-// (below -9.67 both are under 1e-33).
-__device__ __forceinline__ float gn_gelu(float x) { return x < -9.67f ? 0.f : gelu_fwd(x); }
+// The block's GeLU, x s with s = 1 / (1 + e^{-2u}), u = sqrt(2/pi) (x + 0.044715 x^3),
+// from the SFU: e^{-2u} = 2^(x (k0 + k1 x^2)) and the reciprocal, 2^-20 relative
+// over |2u| <= 20; six operations, where the block's own form takes about 15
+// (the forward kernel was bound by them).  Its derivative is
+// s (1 + (1 - s) x (k2 + k3 x^2)) with 1 - s = e^{-2u} s.  Far below zero
+// e^{-2u} is held at 3e38, whose reciprocal is flushed to 0: both are then 0.
+constexpr float kGelu0 = -2.302208198f;    // -2 sqrt(2/pi) log2(e)
+constexpr float kGelu1 = -0.1029432397f;   // 0.044715 of it
+constexpr float kGelu2 = 1.595769122f;     // 2 sqrt(2/pi)
+constexpr float kGelu3 = 0.2140644488f;    // 3 0.044715 of it
+__device__ __forceinline__ float gn_gelu(float x) {
+    return x * rcp_approx(1.f + ex2_approx(x * fmaf(kGelu1, x * x, kGelu0)));
+}
 __device__ __forceinline__ void gn_gelu_grad(float x, float& g, float& dg) {
-    gelu_fwd_grad(x, g, dg);
-    if (x < -9.67f) g = dg = 0.f;
+    const float x2 = x * x;
+    const float e = fminf(ex2_approx(x * fmaf(kGelu1, x2, kGelu0)), 3e38f);
+    const float s = rcp_approx(1.f + e);
+    g = x * s;
+    dg = fmaf(s * (e * s), x * fmaf(kGelu3, x2, kGelu2), s);
+}
+
+// scale gamma_post of 8 channels (a missing vector is ones).
+__device__ __forceinline__ void load_product(const float* p, const float* q, int v, bool on, float (&o)[8]) {
+    float b[8];
+    load8(p, v, on, 1.f, o);
+    load8(q, v, on, 1.f, b);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= b[i];
 }
 
 // Sum over the threads of a row (blockDim.x of them, whole warps).  `red` is
@@ -140,6 +163,14 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
         }
         __syncthreads();
     }
+    // a thread's channels are the same in every row: so are its vectors
+    float gm[VEC][8], sg[VEC][8];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+        const int v = threadIdx.x + k * blockDim.x;
+        load8(a.gamma_pre, v, v < nv, 1.f, gm[k]);
+        if (Y) load_product(a.scale, a.gamma_post, v, v < nv, sg[k]);
+    }
     bool lost = false;
     int it = 0;
     for (long long base = (long long)blockIdx.x * blockDim.y; base < a.T; base += (long long)gridDim.x * blockDim.y, ++it) {
@@ -172,16 +203,13 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
             rstd1 = 1.f / sqrtf(row_sum(ss, red[0]) * inv_d + a.eps);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                const int v = threadIdx.x + k * blockDim.x;
-                float y[8], g[8], gp[8], sc[8];
+                float y[8], g[8];
                 unpack8(qy[k], y);
                 unpack8(qg[k], g);
-                load8(a.gamma_post, v, v < nv, 1.f, gp);
-                load8(a.scale, v, v < nv, 1.f, sc);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float n = y[i] * rstd1 * gp[i];
-                    r[k][i] = fmaf(sc[i] * (G ? gn_gelu(g[i]) : 1.f), n, r[k][i]);
+                    const float p = y[i] * rstd1 * sg[k][i];
+                    r[k][i] = G ? fmaf(gn_gelu(g[i]), p, r[k][i]) : r[k][i] + p;
                 }
             }
         }
@@ -206,10 +234,9 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v >= nv) continue;
-            float gm[8], h[8];
-            load8(a.gamma_pre, v, true, 1.f, gm);
+            float h[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = lost ? NAN : r[k][i] * rstd2 * gm[i];
+            for (int i = 0; i < 8; ++i) h[i] = lost ? NAN : r[k][i] * rstd2 * gm[k][i];
             const size_t o = (size_t)row * nv + v;
             if (Y) a.r[o] = pack8(r[k]);
             a.h[o] = pack8(h);
@@ -222,7 +249,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     constexpr int NOPS = 3 + Y + G;
     __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
     __shared__ __align__(8) uint64_t full[kGnStagesMax];
-    extern __shared__ __align__(128) uint8_t buf[];   // the ring, then the sums [3][rows][D]
+    extern __shared__ __align__(128) uint8_t buf[];   // the ring, then the sums [2][rows][D]
     pdl_trigger();
     pdl_wait();
     const GatedNormArgs& f = a.f;
@@ -246,18 +273,15 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     }
     __syncthreads();
     // a thread's channels are the same in every row: so are its vectors
-    float gm[VEC][8], gp[VEC][8], sc[VEC][8];
-    float dpre[VEC][8], dpost[VEC][8], dscale[VEC][8];
+    float gm[VEC][8], sg[VEC][8];
+    float dpre[VEC][8], sum[VEC][8];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
         load8(f.gamma_pre, v, v < nv, 1.f, gm[k]);
-        if (Y) {
-            load8(f.gamma_post, v, v < nv, 1.f, gp[k]);
-            load8(f.scale, v, v < nv, 1.f, sc[k]);
-        }
+        if (Y) load_product(f.scale, f.gamma_post, v, v < nv, sg[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dpre[k][i] = dpost[k][i] = dscale[k][i] = 0.f;
+        for (int i = 0; i < 8; ++i) dpre[k][i] = sum[k][i] = 0.f;
     }
     bool lost = false;
     int it = 0;
@@ -296,14 +320,15 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
                     ge[k][i] = 1.f;
                     dge[k][i] = 0.f;
                     if (G) gn_gelu_grad(g[i], ge[k][i], dge[k][i]);
-                    q[k][i] = fmaf(sc[k][i] * ge[k][i], y[i] * rs.x * gp[k][i], q[k][i]);
+                    q[k][i] = fmaf(sg[k][i] * ge[k][i], y[i] * rs.x, q[k][i]);
                 }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 q[k][i] *= rs.y;
-                dpre[k][i] = fmaf(dh[i], q[k][i], dpre[k][i]);
-                s = fmaf(dh[i] * gm[k][i], q[k][i], s);
+                const float dq = dh[i] * q[k][i];
+                dpre[k][i] += dq;
+                s = fmaf(dq, gm[k][i], s);
             }
         }
         const float mean = row_sum(s, red[Y ? 0 : it & 1]) * inv_d;
@@ -329,13 +354,11 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
                 unpack8(qy[k], y);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const float p = y[i] * rs.x, n = p * gp[k][i], t = dx[k][i] * sc[k][i];
-                    dscale[k][i] = fmaf(dx[k][i] * ge[k][i], n, dscale[k][i]);
-                    dg[i] = t * n * dge[k][i];
-                    const float dn = t * ge[k][i];
-                    dpost[k][i] = fmaf(dn, p, dpost[k][i]);
-                    dx[k][i] = dn * gp[k][i];   // b
-                    s = fmaf(dx[k][i], p, s);
+                    const float p = y[i] * rs.x, e = dx[k][i] * ge[k][i], ep = e * p;
+                    dg[i] = dx[k][i] * dge[k][i] * (p * sg[k][i]);
+                    sum[k][i] += ep;
+                    s = fmaf(ep, sg[k][i], s);
+                    dx[k][i] = e * sg[k][i];   // b
                 }
                 if (G && row < f.T && v < nv) a.dg[(size_t)row * nv + v] = pack8(dg);
             }
@@ -357,7 +380,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     // is drained: every group asked for has been waited for)
     __syncthreads();
     float* acc = reinterpret_cast<float*>(buf);
-    const int sums = Y ? 3 : 1;
+    const int sums = Y ? 2 : 1;
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
@@ -367,10 +390,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             o[i] = dpre[k][i];
-            if (Y) {
-                o[stride + i] = dpost[k][i];
-                o[2 * stride + i] = dscale[k][i];
-            }
+            if (Y) o[stride + i] = sum[k][i];
         }
     }
     __syncthreads();
@@ -383,10 +403,12 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     }
 }
 
-// Sums blockIdx.y of the partial rows: 32 columns a CTA, warp w the rows w,
-// w + 32, ..., the warps' sums then in order.
+// The partial rows of sum blockIdx.y joined: 32 columns a CTA, warp w the rows
+// w, w + 32, ..., the warps' sums then in order.
 __global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const float* __restrict__ part, int parts, int D,
-                                                              float* o0, float* o1, float* o2) {
+                                                              const float* __restrict__ gamma_post,
+                                                              const float* __restrict__ scale, float* dgamma_pre,
+                                                              float* dgamma_post, float* dscale) {
     __shared__ float acc[32][33];
     pdl_trigger();
     pdl_wait();
@@ -403,7 +425,12 @@ __global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const float* __res
     s = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += acc[i][lane];
-    (blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2)[c] = s;
+    if (blockIdx.y == 0) {
+        dgamma_pre[c] = s;
+    } else {
+        dscale[c] = s * (gamma_post != nullptr ? gamma_post[c] : 1.f);
+        dgamma_post[c] = s * (scale != nullptr ? scale[c] : 1.f);
+    }
 }
 
 struct GnShape {
@@ -457,7 +484,7 @@ template <bool Y, bool G, int VEC>
 cudaError_t gn_bwd_as(GatedNormBwdArgs a, const GnShape& sh, int ctas, cudaStream_t s) {
     const size_t group = (size_t)(3 + Y + G) * sh.block.y * a.f.D * 2;
     a.f.stages = gn_stages(group, gn_ctas_per_sm(sh, Y ? 512 : 1024));
-    const size_t smem = std::max(group * a.f.stages, (size_t)(Y ? 3 : 1) * sh.block.y * a.f.D * sizeof(float));
+    const size_t smem = std::max(group * a.f.stages, (size_t)(Y ? 2 : 1) * sh.block.y * a.f.D * sizeof(float));
     auto* fn = gated_norm_bwd_kernel<Y, G, VEC>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -485,10 +512,10 @@ cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStrea
     if (a.f.y == nullptr) return gn_bwd<false, false>(a, ctas, s);
     return a.f.g == nullptr ? gn_bwd<true, false>(a, ctas, s) : gn_bwd<true, true>(a, ctas, s);
 }
-cudaError_t launch_gated_norm_sum(const float* part, int parts, int D, bool branch, float* o0, float* o1, float* o2,
-                                  cudaStream_t s, bool pdl) {
-    return launch_ex(gated_norm_sum_kernel, dim3((unsigned)((D + 31) / 32), branch ? 3u : 1u), dim3(1024), 0, s, pdl,
-                     part, parts, D, o0, o1, o2);
+cudaError_t launch_gated_norm_sum(const GatedNormBwdArgs& a, int parts, float* dgamma_pre, float* dgamma_post,
+                                  float* dscale, cudaStream_t s, bool pdl) {
+    return launch_ex(gated_norm_sum_kernel, dim3((unsigned)((a.f.D + 31) / 32), a.f.y != nullptr ? 2u : 1u), dim3(1024),
+                     0, s, pdl, a.part, parts, a.f.D, a.f.gamma_post, a.f.scale, dgamma_pre, dgamma_post, dscale);
 }
 
 }  // namespace lrs

@@ -597,11 +597,11 @@ struct GatedNormBwdArgs {
     uint4* dx;
     uint4* dy;
     uint4* dg;
-    float* part;                 // [3 (1 without a branch)][ctas][D]: dgamma_pre, dgamma_post, dscale
+    float* part;                 // [2 (1 without a branch)][ctas][D]: sums of dh q and of e p
 };
 int gated_norm_bwd_ctas(long long T, int D, bool branch, int sms);
-cudaError_t launch_gated_norm_sum(const float* part, int parts, int D, bool branch, float* o0, float* o1, float* o2,
-                                  cudaStream_t s, bool pdl);
+cudaError_t launch_gated_norm_sum(const GatedNormBwdArgs& a, int parts, float* dgamma_pre, float* dgamma_post,
+                                  float* dscale, cudaStream_t s, bool pdl);
 cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s);
 cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s);
 

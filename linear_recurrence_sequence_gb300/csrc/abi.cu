@@ -1108,6 +1108,7 @@ struct CeBackward {
     int piece;           // columns of a piece (a multiple of 256 unless there is one piece)
     long long ldz;       // row stride of dz: a multiple of 8
     int pieces;
+    int h_splits, w_splits;   // of the sums over the piece and over the tokens
     size_t dz, dz2, dh, dw, total;
 };
 constexpr long long kCePieceBytes = 512LL << 20;
@@ -1121,7 +1122,8 @@ CeBackward ce_backward_layout(int T, int V, int D, int fp32, int sms) {
     l.piece = pieces == 1 ? V : (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
     l.pieces = (V + l.piece - 1) / l.piece;
     l.ldz = (l.piece + 7) / 8 * 8;
-    const int sh = ce_splits(T, D, l.piece, sms), sw = ce_splits(l.piece, D, T, sms);
+    ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &l.h_splits, &l.w_splits);
+    const int sh = l.h_splits, sw = l.w_splits;
     const size_t dz = up256((size_t)T * (size_t)l.ldz * 2);
     l.dz = 256;
     l.dz2 = l.dz + dz;
@@ -1156,12 +1158,9 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
     uint32_t* status = at<uint32_t>(scratch, 0);
     if (cudaMemsetAsync(status, 0, 16, stream) != cudaSuccess) return LRS_ERR_CUDA;
     CeGemmArgs g = {};
-    g.layout = kBgNT;
-    g.epi = kCeStats;
-    g.M = T;
-    g.N = V;
-    g.K = D;
-    g.parts = 1;
+    g.c[0].M = T;
+    g.c[0].N = V;
+    g.c[0].K = D;
     g.stats = at<float2>(scratch, l.stats);
     g.zt = at<float>(scratch, l.zt);
     g.target = target;
@@ -1169,7 +1168,7 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
     g.softcap = softcap;
     g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
     g.status = status;
-    LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_gemm(g, h, nullptr, D, w, V, nullptr, nullptr, 0, 0, stream, false));
+    LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, false));
     LRS_LAUNCH(KID_CE_ROWS, stream,
                launch_ce_rows(g.stats, g.zt, target, 2 * ce_n_tiles(V), T, V, loss, lse, at<double>(scratch, l.sums),
                               total, status + 1, status, stream, pdl_ok()));
@@ -1193,21 +1192,18 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     void* dz2 = fp32 ? at<void>(scratch, l.dz2) : nullptr;
     if (cudaMemsetAsync(status, 0, 16, stream) != cudaSuccess) return LRS_ERR_CUDA;
     // the same splits for every piece (the last may be shorter)
-    const int h_splits = ce_splits(T, D, l.piece, sms), w_splits = ce_splits(l.piece, D, T, sms);
+    int h_splits, w_splits;
+    ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &h_splits, &w_splits);
     // dh adds over the pieces (and the splits of a piece) in FP32
     const bool h_part = h_splits > 1 || (l.pieces > 1 && !fp32);
-    float* hp = h_part ? at<float>(scratch, l.dh) : static_cast<float*>(dh);
     for (int i = 0; i < l.pieces; ++i) {
         const int v0 = i * l.piece, nv = std::min(l.piece, V - v0);
         CeGemmArgs g = {};
-        g.layout = kBgNT;
-        g.epi = fp32 ? kCeDz2 : kCeDz;
-        g.M = T;
-        g.N = nv;
-        g.K = D;
-        g.parts = 1;
-        g.b_row = v0;
-        g.s_cols = (int)l.ldz;
+        g.c[0].M = T;
+        g.c[0].N = nv;
+        g.c[0].K = D;
+        g.c[0].b_row = v0;
+        g.c[0].s_cols = (int)l.ldz;
         g.target = target;
         g.V = V;
         g.dloss = dloss;
@@ -1216,60 +1212,38 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         g.softcap = softcap;
         g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
         g.status = status;
-        LRS_LAUNCH(KID_CE_GEMM, stream,
-                   launch_ce_gemm(g, h, nullptr, D, w, V, dz, dz2, T, l.ldz, stream, i > 0 && pdl_ok()));
-        // dh (+)= dz w
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, dz, dz2, l.ldz, stream, i > 0 && pdl_ok()));
+        // dh (+)= dz w; dw's rows of this piece = dz^T h
         CeGemmArgs d = {};
-        d.layout = kBgNN;
-        d.M = T;
-        d.N = D;
-        d.K = nv;
-        d.parts = fp32 ? 2 : 1;
-        d.b_row = v0;
         d.status = status;
-        if (h_part || fp32) {
-            d.epi = kCeF32;
-            d.splits = std::min(h_splits, (nv + 63) / 64);
-            d.part = hp;
-            d.part_rows = T;
-            d.accumulate = i > 0;
-            LRS_LAUNCH(KID_CE_GEMM, stream,
-                       launch_ce_gemm(d, dz, dz2, l.ldz, w, V, nullptr, nullptr, 0, 0, stream, pdl_ok()));
-        } else {
-            d.epi = kCeStore;
-            d.s_cols = D;
-            LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_gemm(d, dz, dz2, l.ldz, w, V, dh, nullptr, T, D, stream, pdl_ok()));
-        }
-        // dw's rows of this piece = dz^T h
-        CeGemmArgs e = {};
-        e.layout = kBgTN;
-        e.M = nv;
-        e.N = D;
-        e.K = T;
-        e.parts = fp32 ? 2 : 1;
-        e.status = status;
-        e.splits = w_splits;
+        CeSide& ch = d.c[0];
+        ch.M = T;
+        ch.N = D;
+        ch.K = nv;
+        ch.b_row = v0;
+        ch.s_cols = D;
+        ch.splits = std::min(h_splits, (nv + 63) / 64);
+        ch.part = h_part ? at<float>(scratch, l.dh) : fp32 ? static_cast<float*>(dh) : nullptr;
+        ch.accumulate = i > 0;
+        CeSide& cw = d.c[1];
+        cw.M = nv;
+        cw.N = D;
+        cw.K = T;
+        cw.s_row = v0;
+        cw.s_cols = D;
+        cw.splits = w_splits;
         const size_t at0 = (size_t)v0 * D;
-        if (e.splits > 1 || fp32) {
-            e.epi = kCeF32;
-            e.part = e.splits > 1 ? at<float>(scratch, l.dw) : static_cast<float*>(dw) + at0;
-            e.part_rows = nv;
-            LRS_LAUNCH(KID_CE_GEMM, stream,
-                       launch_ce_gemm(e, dz, dz2, l.ldz, h, T, nullptr, nullptr, 0, 0, stream, pdl_ok()));
-            if (e.splits > 1)
-                LRS_LAUNCH(KID_CE_ROWS, stream,
-                           launch_ce_sum(e.part, (long long)nv * D, e.splits, (long long)nv * D,
-                                         static_cast<char*>(dw) + at0 * (fp32 ? 4 : 2), fp32, stream, pdl_ok()));
-        } else {
-            e.epi = kCeStore;
-            e.s_row = v0;
-            e.s_cols = D;
-            LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_gemm(e, dz, dz2, l.ldz, h, T, dw, nullptr, V, D, stream, pdl_ok()));
-        }
+        cw.part = w_splits > 1 ? at<float>(scratch, l.dw) : fp32 ? static_cast<float*>(dw) + at0 : nullptr;
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_grads(d, dz, dz2, l.ldz, h, w, V, dh, dw, stream, pdl_ok()));
+        if (w_splits > 1)
+            LRS_LAUNCH(KID_CE_ROWS, stream,
+                       launch_ce_sum(cw.part, (long long)nv * D, w_splits, (long long)nv * D,
+                                     static_cast<char*>(dw) + at0 * (fp32 ? 4 : 2), fp32, stream, pdl_ok()));
     }
     if (h_part)
         LRS_LAUNCH(KID_CE_ROWS, stream,
-                   launch_ce_sum(hp, (long long)T * D, h_splits, (long long)T * D, dh, fp32, stream, pdl_ok()));
+                   launch_ce_sum(at<float>(scratch, l.dh), (long long)T * D, h_splits, (long long)T * D, dh, fp32, stream,
+                                 pdl_ok()));
     return LRS_OK;
 }
 

@@ -9,7 +9,11 @@
 //                        dz = dloss (e^{z - lse} - [v = target]) (backward),
 //                        the latter for one piece of the vocabulary at a time;
 //   NN  dh = dz w        A = dz [T][piece] K-major, B = w's rows as K index;
-//   TN  dw = dz^T h      both operands MN-major, the tokens as K index.
+//   TN  dw = dz^T h      both operands MN-major, the tokens as K index;
+// the last two in one launch: neither's tile count fills the pairs of SMs
+// evenly, and together they do (a pair with one dh tile less than the others
+// takes as many more of the shorter dw tiles; 8192 tokens x 32768 entries at
+// D 2048: 1525 us one after the other, see below together).
 // Unlike the block's contractions (block_gemm.cu) every extent may be ragged:
 // the TMA fills what lies outside a matrix with zeros and clips what is stored
 // there; columns past the vocabulary are zeroed in dz.
@@ -49,7 +53,7 @@ constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store
 // Staging of the BF16 stores: two alternating boxes per epilogue warp, or two
 // pairs (leading part and remainder).
 __host__ __device__ constexpr uint32_t ce_stage_warp(int epi) {
-    return epi == kCeDz2 ? 4 * kCeBox : (epi == kCeDz || epi == kCeStore) ? 2 * kCeBox : 0u;
+    return epi == kCeDz2 ? 4 * kCeBox : epi != kCeStats ? 2 * kCeBox : 0u;
 }
 __host__ __device__ constexpr int ce_stages(int epi) { return epi == kCeDz2 ? kCeStages - 1 : kCeStages; }
 constexpr size_t ce_smem(int epi) {
@@ -63,33 +67,57 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
 }
 
 struct CeItem {
+    int side;             // contraction (of a.c)
     int mt, nt, s, k0, k1;
-    int m0;   // this CTA's first row
+    int m0;               // this CTA's first row
 };
 
-// Work item i.  NT: m runs fastest inside a group of row tiles whose h stays
-// in the L2, so that a tile of w is read by the whole group at about the same
-// time.  NN, TN: n (the width D) runs fastest, so that the D tiles that read
-// the same panel of dz run together.
-__device__ __forceinline__ CeItem ce_item(const CeGemmArgs& a, int i, int rank) {
-    CeItem it;
-    if (a.layout == kBgNT) {
-        const int per = a.group * a.n_tiles;
+// Item k of pair `pair`; false where it has no more.
+// One contraction (the logits): the pairs take turns, rows fastest inside a
+// group of row tiles whose h stays in the L2, so that a tile of w is read by
+// the whole group at about the same time.
+// Two (dh and dw): dh's items first, in turns; the pairs that get one less
+// take `extra` more of dw's.  The tiles of D run fastest, so that those that
+// read the same panel of dz run together.
+__device__ __forceinline__ bool ce_item(const CeGemmArgs& a, bool grads, int pair, int pairs, int k, int rank, CeItem& it) {
+    const CeSide* c = a.c;
+    if (!grads) {
+        const int i = pair + k * pairs;
+        if (i >= c->n_items) return false;
+        const int per = a.group * c->n_tiles;
         const int g = i / per, r = i - g * per;
-        const int gm = min(a.group, a.m_tiles - g * a.group);
+        const int gm = min(a.group, c->m_tiles - g * a.group);
+        it.side = 0;
         it.mt = g * a.group + r % gm;
         it.nt = r / gm;
         it.s = 0;
     } else {
-        it.nt = i % a.n_tiles;
-        const int r = i / a.n_tiles;
-        it.mt = r % a.m_tiles;
-        it.s = r / a.m_tiles;
+        const int n0 = a.c[0].n_items, more = n0 % pairs;
+        const int own = n0 / pairs + (pair < more ? 1 : 0);   // dh items of this pair
+        int i;
+        if (k < own) {
+            it.side = 0;
+            i = pair + k * pairs;
+        } else {
+            it.side = 1;
+            ++c;
+            const int few = pairs - more;                     // pairs with one dh item less
+            const int r = k - own;
+            if (pair >= more && r < a.extra)
+                i = r * few + pair - more;
+            else
+                i = a.extra * few + (r - (pair >= more ? a.extra : 0)) * pairs + pair;
+            if (i >= c->n_items) return false;
+        }
+        it.nt = i % c->n_tiles;
+        const int r = i / c->n_tiles;
+        it.mt = r % c->m_tiles;
+        it.s = r / c->m_tiles;
     }
     it.m0 = it.mt * kCeM + 128 * rank;
-    it.k0 = (int)((long long)a.ksteps * it.s / a.splits);
-    it.k1 = (int)((long long)a.ksteps * (it.s + 1) / a.splits);
-    return it;
+    it.k0 = (int)((long long)c->ksteps * it.s / c->splits);
+    it.k1 = (int)((long long)c->ksteps * (it.s + 1) / c->splits);
+    return true;
 }
 
 // The capped logit and its slope: z' = c tanh(z / c), dz'/dz = 1 - (z'/c)^2.
@@ -102,8 +130,9 @@ __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& 
     const int t = it.m0 + row;
     const int c0 = half * (kCeN / 2);
     const int v0 = it.nt * kCeN + c0;            // vocabulary index of the first column
-    const int nv = min(kCeN / 2, a.N - v0);      // columns that count (may be <= 0)
-    const bool ok = t < a.M;
+    const int nv = min(kCeN / 2, a.c[0].N - v0);      // columns that count (may be <= 0)
+    const int M = a.c[0].M;
+    const bool ok = t < M;
     long long tgt = -1;
     if (ok) tgt = a.target[t] - v0;
     float mx = -INFINITY, sum = 0.f;
@@ -136,14 +165,18 @@ __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& 
         sum = fmaf(sum, ex2_approx(fmaf(mx, kLog2e, off)), s);
         mx = m;
     }
-    if (ok) a.stats[(size_t)(2 * it.nt + half) * a.M + t] = make_float2(mx, sum);
+    if (ok) a.stats[(size_t)(2 * it.nt + half) * M + t] = make_float2(mx, sum);
 }
 
-template <int LAYOUT, int EPI, bool CAP>
+// Tensor maps of both contractions: A, A's remainders, B, the BF16 result (s2: dz's remainders).
+struct CeMaps {
+    CUtensorMap a[2], a2[2], b[2], s[2], s2;
+};
+
+template <int EPI, bool CAP>
 __global__ void __launch_bounds__(kCeThreads, 1)
-    ce_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_a2,
-                   const __grid_constant__ CUtensorMap tm_b, const __grid_constant__ CUtensorMap tm_s,
-                   const __grid_constant__ CUtensorMap tm_s2, const CeGemmArgs a) {
+    ce_gemm_kernel(const __grid_constant__ CeMaps tm, const __grid_constant__ CeGemmArgs a) {
+    constexpr bool GRADS = EPI == kCeGrads;
     constexpr int S = ce_stages(EPI);
     extern __shared__ uint8_t ce_raw[];
     // s_full and s_free are used in the even CTA, the others in both
@@ -180,13 +213,16 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         *abort_flag = 1;
         atomicOr(a.status, kStatusTimeout);
     };
-    const int w0 = (int)blockIdx.x / 2, wstep = (int)gridDim.x / 2;   // the same items in both CTAs
+    const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;   // the same items in both CTAs
+    CeItem it;
 
     if (warp == kCeProducer) {
         if (lane == 0) {
             uint32_t n = 0;
-            for (int w = w0; w < a.n_items && !*abort_flag; w += wstep) {
-                const CeItem it = ce_item(a, w, rank);
+            for (int k = 0; !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k) {
+                const CeSide& c = a.c[it.side];
+                const bool tn = GRADS && it.side == 1;
+                const CUtensorMap *ta1 = &tm.a[it.side], *ta2 = &tm.a2[it.side], *tb = &tm.b[it.side];
                 for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
                     const int slot = (int)(n % S);
                     if (n >= (uint32_t)S && !mbar_wait_bounded(&s_empty[slot], ((n / S) - 1) & 1u)) {
@@ -197,24 +233,24 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     uint8_t* sa = ring + (size_t)slot * kCeStageBytes;
                     uint8_t* sb = sa + kCeABytes;
                     // the remainders of dz follow its leading parts along K
-                    const bool second = a.parts == 2 && ks >= a.part_steps;
-                    const int k0 = kCeK * (second ? ks - a.part_steps : ks);
+                    const bool second = GRADS && ks >= c.part_steps;
+                    const int k0 = kCeK * (second ? ks - c.part_steps : ks);
                     const int n0 = it.nt * kCeN + 128 * rank;
-                    const CUtensorMap* ta = second ? &tm_a2 : &tm_a;
+                    const CUtensorMap* ta = second ? ta2 : ta1;
                     // both CTAs' bytes are announced by the even one (the odd one's may land first)
                     if (rank == 0) mbar_arrive_expect_tx(&s_full[slot], 2 * kCeStageBytes);
                     const uint32_t bar = cluster_map(&s_full[slot], 0);
-                    if (LAYOUT == kBgTN) {
+                    if (tn) {
                         tma2_load_2d(sa, ta, it.m0, k0, bar);
                         tma2_load_2d(sa + 8192, ta, it.m0 + 64, k0, bar);
                     } else {
                         tma2_load_2d(sa, ta, k0, it.m0, bar);
                     }
-                    if (LAYOUT == kBgNT) {
-                        tma2_load_2d(sb, &tm_b, k0, a.b_row + n0, bar);
+                    if (!GRADS) {
+                        tma2_load_2d(sb, tb, k0, c.b_row + n0, bar);
                     } else {
-                        tma2_load_2d(sb, &tm_b, n0, a.b_row + k0, bar);
-                        tma2_load_2d(sb + 8192, &tm_b, n0 + 64, a.b_row + k0, bar);
+                        tma2_load_2d(sb, tb, n0, c.b_row + k0, bar);
+                        tma2_load_2d(sb + 8192, tb, n0 + 64, c.b_row + k0, bar);
                     }
                 }
             }
@@ -227,11 +263,10 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         }
     } else if (warp == kCeIssuer) {
         if (lane == 0 && rank == 0) {
-            constexpr uint32_t idesc = umma_idesc_bf16(kCeM, kCeN) | (LAYOUT == kBgTN ? (1u << 15) : 0u) |
-                                       (LAYOUT != kBgNT ? (1u << 16) : 0u);
             uint32_t n = 0, item = 0;
-            for (int w = w0; w < a.n_items && !*abort_flag; w += wstep, ++item) {
-                const CeItem it = ce_item(a, w, rank);
+            for (; !*abort_flag && ce_item(a, GRADS, pair, pairs, (int)item, rank, it); ++item) {
+                const bool tn = GRADS && it.side == 1;   // A MN-major too
+                const uint32_t idesc = umma_idesc_bf16(kCeM, kCeN) | (tn ? (1u << 15) : 0u) | (GRADS ? (1u << 16) : 0u);
                 const uint32_t buf = item & 1u;
                 // both CTAs' epilogues have drained this accumulator's previous tile
                 if (item >= 2 && !mbar_wait_cluster(&s_free[buf], ((item >> 1) - 1) & 1u)) {
@@ -253,10 +288,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     const uint32_t sb = sa + kCeABytes;
 #pragma unroll
                     for (int kk = 0; kk < kCeK / 16; ++kk) {
-                        const uint64_t da = LAYOUT == kBgTN ? umma_desc_sw128_mn(sa + 2048u * kk, 8192u)
-                                                            : umma_desc_sw128(sa + 32u * kk);
-                        const uint64_t db = LAYOUT == kBgNT ? umma_desc_sw128(sb + 32u * kk)
-                                                            : umma_desc_sw128_mn(sb + 2048u * kk, 8192u);
+                        const uint64_t da = tn ? umma_desc_sw128_mn(sa + 2048u * kk, 8192u) : umma_desc_sw128(sa + 32u * kk);
+                        const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + 2048u * kk, 8192u) : umma_desc_sw128(sb + 32u * kk);
                         umma2_bf16(acc_t, da, db, idesc, ks > it.k0 || kk > 0);
                     }
                     umma2_commit(&s_empty[slot]);
@@ -274,17 +307,17 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const int row = 32 * q4 + lane;
         uint8_t* stg = ring + (size_t)S * kCeStageBytes + (size_t)warp * ce_stage_warp(EPI);
         uint32_t chunk = 0, item = 0;
-        for (int w = w0; w < a.n_items && !*abort_flag; w += wstep, ++item) {
-            const CeItem it = ce_item(a, w, rank);
+        for (; !*abort_flag && ce_item(a, GRADS, pair, pairs, (int)item, rank, it); ++item) {
+            const CeSide& c0 = a.c[it.side];
             const uint32_t buf = item & 1u;
             // what a row needs besides its logits is fetched while the tile is computed
             float wgt = 0.f, lse2 = 0.f;
             long long tgt = -1;
             if (EPI == kCeDz || EPI == kCeDz2) {
                 const int t = it.m0 + row;
-                if (t < a.M) {
+                if (t < c0.M) {
                     const long long tg = a.target[t];
-                    tgt = tg - a.b_row - (long long)it.nt * kCeN;
+                    tgt = tg - c0.b_row - (long long)it.nt * kCeN;
                     // a row without a valid target adds nothing to the gradients
                     if (tg >= 0 && tg < a.V) wgt = a.dloss != nullptr ? a.dloss[t] : 1.f / a.total[1];
                     lse2 = a.lse[t] * kLog2e;
@@ -298,20 +331,20 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + buf * (uint32_t)kCeN;
             if (EPI == kCeStats) {
                 ce_epi_stats<CAP>(a, it, row, taddr, hf);
-            } else if (EPI == kCeF32) {
+            } else if (GRADS && c0.part != nullptr) {
                 const long long r = (long long)it.m0 + row;
-                float* o = a.part + ((size_t)it.s * a.part_rows + (size_t)r) * a.N + (size_t)it.nt * kCeN;
+                float* o = c0.part + ((size_t)it.s * c0.M + (size_t)r) * c0.N + (size_t)it.nt * kCeN;
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
                     float v[2][16];
                     tmem_ld16x2(taddr + (uint32_t)c, taddr + (uint32_t)(c + 16), v[0], v[1]);
-                    if (r >= a.M) continue;
+                    if (r >= c0.M) continue;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
-                        if (it.nt * kCeN + c + j >= a.N) continue;
+                        if (it.nt * kCeN + c + j >= c0.N) continue;
                         float4 x = make_float4(v[j / 16][j % 16], v[j / 16][j % 16 + 1], v[j / 16][j % 16 + 2],
                                                v[j / 16][j % 16 + 3]);
                         float4* p = reinterpret_cast<float4*>(o + c + j);
-                        if (a.accumulate) {
+                        if (c0.accumulate) {
                             const float4 y = *p;
                             x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
                         }
@@ -321,9 +354,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             } else {
                 // BF16 results by TMA stores from swizzled staging, 32 columns at a time
                 constexpr int kBoxes = EPI == kCeDz2 ? 2 : 1;
-                const int y = a.s_row + it.m0 + 32 * q4;
-                const bool store = it.m0 + 32 * q4 < a.M;   // rows past the matrix are clipped by the TMA
-                const int nv = a.N - it.nt * kCeN;                 // columns of this tile inside the matrix
+                const int y = c0.s_row + it.m0 + 32 * q4;
+                const bool store = it.m0 + 32 * q4 < c0.M;   // rows past the matrix are clipped by the TMA
+                const int nv = c0.N - it.nt * kCeN;                 // columns of this tile inside the matrix
 #pragma unroll 1
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32, ++chunk) {
                     float v[2][16], lo[2][16];
@@ -365,9 +398,9 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     fence_proxy_async();
                     __syncwarp();
                     if (lane == 0) {
-                        if (store && it.nt * kCeN + c < a.s_cols) {
-                            tma_store_2d(&tm_s, it.nt * kCeN + c, y, box);
-                            if (EPI == kCeDz2) tma_store_2d(&tm_s2, it.nt * kCeN + c, y, box + kCeBox);
+                        if (store && it.nt * kCeN + c < c0.s_cols) {
+                            tma_store_2d(&tm.s[it.side], it.nt * kCeN + c, y, box);
+                            if (EPI == kCeDz2) tma_store_2d(&tm.s2, it.nt * kCeN + c, y, box + kCeBox);
                         }
                         bulk_commit();
                     }
@@ -521,12 +554,12 @@ bool ce_map(CUtensorMap* map, const void* ptr, long long cols, long long rows, l
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+int ce_item_steps(const CeSide& c) { return std::max(1, c.ksteps / c.splits); }
 int ce_pairs() { return std::max(1, block_gemm_sms() / 2); }
 
-template <int LAYOUT, int EPI, bool CAP>
-cudaError_t ce_launch(const CUtensorMap& ta, const CUtensorMap& ta2, const CUtensorMap& tb, const CUtensorMap& ts,
-                      const CUtensorMap& ts2, const CeGemmArgs& a, cudaStream_t s, bool pdl) {
-    auto* fn = ce_gemm_kernel<LAYOUT, EPI, CAP>;
+template <int EPI, bool CAP>
+cudaError_t ce_launch(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl) {
+    auto* fn = ce_gemm_kernel<EPI, CAP>;
     constexpr size_t smem = ce_smem(EPI);
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -551,13 +584,18 @@ cudaError_t ce_launch(const CUtensorMap& ta, const CUtensorMap& ta2, const CUten
         if (cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg) != cudaSuccess || pairs < 1) pairs = ce_pairs();
         cached[dev].store(pairs, std::memory_order_relaxed);
     }
-    cfg.gridDim = dim3(2u * (unsigned)std::min(pairs, a.n_items));
+    pairs = std::min(pairs, a.c[0].n_items + a.c[1].n_items);
+    cfg.gridDim = dim3(2u * (unsigned)pairs);
+    // the pairs left with one dh item less make up for its K steps in dw items
+    a.extra = 0;
+    if (EPI == kCeGrads && a.c[0].n_items % pairs != 0)
+        a.extra = (2 * ce_item_steps(a.c[0]) + ce_item_steps(a.c[1])) / (2 * ce_item_steps(a.c[1]));
     if (pdl) {
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
         attr[1].val.programmaticStreamSerializationAllowed = 1;
         cfg.numAttrs = 2;
     }
-    return cudaLaunchKernelEx(&cfg, fn, ta, ta2, tb, ts, ts2, a);
+    return cudaLaunchKernelEx(&cfg, fn, tm, a);
 }
 
 }  // namespace
@@ -565,65 +603,76 @@ cudaError_t ce_launch(const CUtensorMap& ta, const CUtensorMap& ta2, const CUten
 int ce_m_tiles(long long M) { return (int)((M + kCeM - 1) / kCeM); }
 int ce_n_tiles(long long N) { return (int)((N + kCeN - 1) / kCeN); }
 
-// Splits of the K axis when a contraction has fewer tiles than the GPU has
-// pairs of SMs: as many as fill them, each at least four K steps long.
-int ce_splits(long long M, long long N, long long K, int sms) {
-    const long long tiles = (long long)ce_m_tiles(M) * ce_n_tiles(N), steps = (K + kCeK - 1) / kCeK;
-    return (int)std::max(1LL, std::min<long long>({sms / 2 / tiles, steps / 4, kCeSplitsMax}));
+// Splits of the K axes of dh [T][D] (K = the piece of V) and dw [piece][D]
+// (K = T), `parts` times as long with remainders: no item longer than a pair's
+// share of all the steps (or 8 steps), so that a long axis with few tiles
+// around it is spread over the pairs.
+void ce_grad_splits(long long T, long long V, long long D, int parts, int sms, int* h_splits, int* w_splits) {
+    const long long ch = parts * ((V + kCeK - 1) / kCeK), cw = parts * ((T + kCeK - 1) / kCeK);
+    const long long steps = ((long long)ce_m_tiles(T) * ch + (long long)ce_m_tiles(V) * cw) * ce_n_tiles(D);
+    const long long most = std::max(8LL, steps / std::max(1, sms / 2));
+    *h_splits = (int)std::min<long long>(kCeSplitsMax, (ch + most - 1) / most);
+    *w_splits = (int)std::min<long long>(kCeSplitsMax, (cw + most - 1) / most);
 }
 
-// A [M][K] (NT, NN) or [K][M] (TN) with row stride lda; A2: its remainders
-// (parts = 2); B [brows][K] (NT) or [brows][N] (NN, TN), read from row
-// a.b_row on; S, S2: the BF16 result, [s_rows][s_cols] with row stride lds.
-cudaError_t launch_ce_gemm(const CeGemmArgs& in, const void* A, const void* A2, long long lda, const void* B,
-                           long long brows, void* S, void* S2, long long s_rows, long long lds, cudaStream_t s,
-                           bool pdl) {
+namespace {
+
+// Fills a contraction's tile counts.
+void ce_side(CeSide& c, int parts) {
+    c.m_tiles = ce_m_tiles(c.M);
+    c.n_tiles = ce_n_tiles(c.N);
+    c.part_steps = (c.K + kCeK - 1) / kCeK;
+    c.ksteps = parts * c.part_steps;
+    if (c.splits < 1) c.splits = 1;
+    c.n_items = c.m_tiles * c.n_tiles * c.splits;
+}
+
+}  // namespace
+
+// Logits of h [T][D] and rows a.c[0].b_row on of w [V][D]: their statistics,
+// or dz [T][ldz] (and its remainders dz2).
+cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w, int V, void* dz, void* dz2,
+                             long long ldz, cudaStream_t s, bool pdl) {
     CeGemmArgs a = in;
-    CUtensorMap ta, ta2, tb, ts, ts2;
-    const long long K = a.K;
-    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B;
-    bool ok;
-    if (a.layout == kBgTN)
-        ok = ce_map(&ta, A, lda, K, lda, 64, 64, sw) && (a.parts == 1 || ce_map(&ta2, A2, lda, K, lda, 64, 64, sw));
-    else
-        ok = ce_map(&ta, A, lda, a.M, lda, 64, 128, sw) &&
-             (a.parts == 1 || ce_map(&ta2, A2, lda, a.M, lda, 64, 128, sw));
-    ok = ok && (a.layout == kBgNT ? ce_map(&tb, B, K, brows, K, 64, 128, sw)
-                                  : ce_map(&tb, B, a.N, brows, a.N, 64, 64, sw));
-    if (!ok) return cudaErrorInvalidValue;
-    if (a.parts == 1) ta2 = ta;
-    ts = ts2 = ta;
-    if (S != nullptr && !ce_map(&ts, S, a.s_cols, s_rows, lds, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+    CeSide& c = a.c[0];
+    ce_side(c, 1);
+    a.c[1].n_items = 0;
+    CeMaps tm;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!ce_map(&tm.a[0], h, c.K, c.M, c.K, 64, 128, sw) || !ce_map(&tm.b[0], w, c.K, V, c.K, 64, 128, sw))
         return cudaErrorInvalidValue;
-    if (S2 != nullptr && !ce_map(&ts2, S2, a.s_cols, s_rows, lds, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B))
-        return cudaErrorInvalidValue;
-    a.m_tiles = ce_m_tiles(a.M);
-    a.n_tiles = ce_n_tiles(a.N);
-    a.part_steps = (int)((K + kCeK - 1) / kCeK);
-    a.ksteps = a.parts * a.part_steps;
-    if (a.splits < 1) a.splits = 1;
+    tm.s[0] = tm.s2 = tm.a[0];
+    if (dz != nullptr && !ce_map(&tm.s[0], dz, c.s_cols, c.M, ldz, 32, 32, sw64)) return cudaErrorInvalidValue;
+    if (dz2 != nullptr && !ce_map(&tm.s2, dz2, c.s_cols, c.M, ldz, 32, 32, sw64)) return cudaErrorInvalidValue;
+    tm.a[1] = tm.a2[0] = tm.a2[1] = tm.b[1] = tm.s[1] = tm.a[0];
     // 32 MB of h per group of row tiles
-    a.group = (int)std::max(1LL, std::min<long long>(a.m_tiles, (32LL << 20) / (K * 2 * kCeM)));
-    const long long items = (long long)a.m_tiles * a.n_tiles * a.splits;
-    if (items > 0x7fffffffLL) return cudaErrorInvalidValue;
-    a.n_items = (int)items;
+    a.group = (int)std::max(1LL, std::min<long long>(c.m_tiles, (32LL << 20) / ((long long)c.K * 2 * kCeM)));
     const bool cap = a.softcap > 0.f;
-    switch (a.layout * 16 + a.epi) {
-        case kBgNT * 16 + kCeStats:
-            return cap ? ce_launch<kBgNT, kCeStats, true>(ta, ta2, tb, ts, ts2, a, s, pdl)
-                       : ce_launch<kBgNT, kCeStats, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        case kBgNT * 16 + kCeDz:
-            return cap ? ce_launch<kBgNT, kCeDz, true>(ta, ta2, tb, ts, ts2, a, s, pdl)
-                       : ce_launch<kBgNT, kCeDz, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        case kBgNT * 16 + kCeDz2:
-            return cap ? ce_launch<kBgNT, kCeDz2, true>(ta, ta2, tb, ts, ts2, a, s, pdl)
-                       : ce_launch<kBgNT, kCeDz2, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        case kBgNN * 16 + kCeStore: return ce_launch<kBgNN, kCeStore, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        case kBgNN * 16 + kCeF32: return ce_launch<kBgNN, kCeF32, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        case kBgTN * 16 + kCeStore: return ce_launch<kBgTN, kCeStore, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        case kBgTN * 16 + kCeF32: return ce_launch<kBgTN, kCeF32, false>(ta, ta2, tb, ts, ts2, a, s, pdl);
-        default: return cudaErrorInvalidValue;
-    }
+    if (dz == nullptr) return cap ? ce_launch<kCeStats, true>(tm, a, s, pdl) : ce_launch<kCeStats, false>(tm, a, s, pdl);
+    if (dz2 == nullptr) return cap ? ce_launch<kCeDz, true>(tm, a, s, pdl) : ce_launch<kCeDz, false>(tm, a, s, pdl);
+    return cap ? ce_launch<kCeDz2, true>(tm, a, s, pdl) : ce_launch<kCeDz2, false>(tm, a, s, pdl);
+}
+
+// a.c[0]: dh [T][D] (+)= dz w's rows b_row on; a.c[1]: dw = dz^T h, rows s_row
+// on of a matrix [V][D].  Each as FP32 into its `part`, or as BF16 into S.
+cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz2, long long ldz, const void* h,
+                            const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl) {
+    CeGemmArgs a = in;
+    const int parts = dz2 != nullptr ? 2 : 1;
+    ce_side(a.c[0], parts);
+    ce_side(a.c[1], parts);
+    const long long T = a.c[0].M, D = a.c[0].N;
+    CeMaps tm;
+    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    const void* second = dz2 != nullptr ? dz2 : dz;
+    if (!ce_map(&tm.a[0], dz, ldz, T, ldz, 64, 128, sw) || !ce_map(&tm.a2[0], second, ldz, T, ldz, 64, 128, sw) ||
+        !ce_map(&tm.a[1], dz, ldz, T, ldz, 64, 64, sw) || !ce_map(&tm.a2[1], second, ldz, T, ldz, 64, 64, sw) ||
+        !ce_map(&tm.b[0], w, D, V, D, 64, 64, sw) || !ce_map(&tm.b[1], h, D, T, D, 64, 64, sw))
+        return cudaErrorInvalidValue;
+    tm.s[0] = tm.s[1] = tm.s2 = tm.a[0];
+    if (a.c[0].part == nullptr && !ce_map(&tm.s[0], dh, D, T, D, 32, 32, sw64)) return cudaErrorInvalidValue;
+    if (a.c[1].part == nullptr && !ce_map(&tm.s[1], dw, D, V, D, 32, 32, sw64)) return cudaErrorInvalidValue;
+    return ce_launch<kCeGrads, false>(tm, a, s, pdl);
 }
 
 // Rows per CTA of the statistics kernel: 32 (a warp reads 32 rows of one part),

@@ -532,21 +532,23 @@ cudaError_t launch_join_fwd(const void* gv, const void* ym, void* j, long long B
 // ---------------------------------------------------------------------------
 // Softmax cross entropy over a vocabulary (ce_gemm.cu).
 // ---------------------------------------------------------------------------
-// Epilogues: (max, sum of exponentials) of a row's columns; dz in BF16; dz as
-// BF16 leading parts and remainders; plain BF16; FP32 (stored or added).
-enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz2 = 2, kCeStore = 3, kCeF32 = 4 };
+// What the contraction kernel does: (max, sum of exponentials) of the logits;
+// dz in BF16; dz as BF16 leading parts and remainders; dh and dw together.
+enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz2 = 2, kCeGrads = 3 };
 constexpr int kCeSplitsMax = 32;
 
-struct CeGemmArgs {
-    int layout, epi;             // BgLayoutKind, CeEpiKind
+// One contraction, M x N over K.
+struct CeSide {
     int M, N, K;
-    int parts;                   // 2: operand A comes as leading parts and remainders
-    int splits;                  // of K (kCeF32 only)
-    int b_row;                   // first row of B (NT, NN: the piece of the vocabulary)
+    int splits;                  // of K (FP32 results only)
+    int b_row;                   // first row of B (the piece of the vocabulary)
     int s_row, s_cols;           // BF16 result: first row, columns of the matrix that is stored to
-    int accumulate;              // kCeF32: add to part
-    float* part;                 // kCeF32: [splits][part_rows][N]
-    long long part_rows;
+    int accumulate;              // FP32 result: add to part
+    float* part;                 // FP32 result [splits][M][N], or null
+    int m_tiles, n_tiles, ksteps, part_steps, n_items;   // filled by the launchers
+};
+struct CeGemmArgs {
+    CeSide c[2];                 // the logits; or dh and dw
     float2* stats;               // kCeStats: [2 n_tiles][M]
     float* zt;                   // kCeStats: [M] the targets' logits
     const int64_t* target;       // [M]
@@ -556,15 +558,16 @@ struct CeGemmArgs {
     const float* lse;            // kCeDz: [M]
     float softcap, inv_softcap;  // 0: none
     uint32_t* status;
-    int m_tiles, n_tiles, ksteps, part_steps, group, n_items;   // filled by launch_ce_gemm
+    int group, extra;            // filled by the launchers: row tiles per group; dw items ahead (see ce_item)
 };
 
 int ce_m_tiles(long long M);
 int ce_n_tiles(long long N);
-int ce_splits(long long M, long long N, long long K, int sms);
-cudaError_t launch_ce_gemm(const CeGemmArgs& a, const void* A, const void* A2, long long lda, const void* B,
-                           long long brows, void* S, void* S2, long long s_rows, long long lds, cudaStream_t s,
-                           bool pdl);
+void ce_grad_splits(long long T, long long V, long long D, int parts, int sms, int* h_splits, int* w_splits);
+cudaError_t launch_ce_logits(const CeGemmArgs& a, const void* h, const void* w, int V, void* dz, void* dz2,
+                             long long ldz, cudaStream_t s, bool pdl);
+cudaError_t launch_ce_grads(const CeGemmArgs& a, const void* dz, const void* dz2, long long ldz, const void* h,
+                            const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl);
 int ce_row_ctas(int T);
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
                            float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,

@@ -1106,7 +1106,7 @@ CeForward ce_forward_layout(int T, int V) {
 // the FP32 partial sums of dh and dw.
 struct CeBackward {
     int piece;           // columns of a piece (a multiple of 256 unless there is one piece)
-    long long ldz;       // row stride of dz: a multiple of 8
+    long long ldz;       // row stride of dz: a multiple of 64
     int pieces;
     int h_splits, w_splits;   // of the sums over the piece and over the tokens
     size_t dz, dz2, dh, dw, total;
@@ -1121,7 +1121,7 @@ CeBackward ce_backward_layout(int T, int V, int D, int fp32, int sms) {
     // pieces of about the same length
     l.piece = pieces == 1 ? V : (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
     l.pieces = (V + l.piece - 1) / l.piece;
-    l.ldz = (l.piece + 7) / 8 * 8;
+    l.ldz = (l.piece + 63) / 64 * 64;
     ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &l.h_splits, &l.w_splits);
     const int sh = l.h_splits, sw = l.w_splits;
     const size_t dz = up256((size_t)T * (size_t)l.ldz * 2);
@@ -1222,7 +1222,7 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         ch.K = nv;
         ch.b_row = v0;
         ch.s_cols = D;
-        ch.splits = std::min(h_splits, (nv + 63) / 64);
+        ch.splits = std::min(h_splits, (nv + 127) / 128);
         ch.part = h_part ? at<float>(scratch, l.dh) : fp32 ? static_cast<float*>(dh) : nullptr;
         ch.accumulate = i > 0;
         CeSide& cw = d.c[1];

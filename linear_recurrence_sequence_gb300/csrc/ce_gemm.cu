@@ -41,23 +41,21 @@ namespace {
 constexpr int kCeEpiWarps = 8;
 constexpr int kCeThreads = 32 * (kCeEpiWarps + 2);
 constexpr int kCeProducer = kCeEpiWarps, kCeIssuer = kCeEpiWarps + 1;
-constexpr int kCeK = 64;
+constexpr int kCeK = 128;         // K per stage: two 64-wide (128-byte) chunks
 constexpr int kCeM = 256;         // rows of a pair's tile: 128 a CTA
 constexpr int kCeN = 256;
-constexpr int kCeStages = 6;      // ring stages (5 where dz's remainders are staged too)
-constexpr uint32_t kCeABytes = 128 * 128;   // of one CTA: 128 rows of A, 128 of B
-constexpr uint32_t kCeBBytes = 128 * 128;
+constexpr int kCeStages = 3;
+constexpr uint32_t kCeABytes = 2 * 128 * 128;   // of one CTA: 128 rows of A, 128 of B, two chunks each
+constexpr uint32_t kCeBBytes = 2 * 128 * 128;
+constexpr uint32_t kCeChunk = 128 * 128;        // a 64-column chunk of 128 rows
 constexpr uint32_t kCeStageBytes = kCeABytes + kCeBBytes;
 constexpr uint32_t kCeTmemCols = 2 * kCeN;
 constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store box (64-byte swizzle)
-// Staging of the BF16 stores: two alternating boxes per epilogue warp, or two
-// pairs (leading part and remainder).
-__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) {
-    return epi == kCeDz2 ? 4 * kCeBox : epi != kCeStats ? 2 * kCeBox : 0u;
-}
-__host__ __device__ constexpr int ce_stages(int epi) { return epi == kCeDz2 ? kCeStages - 1 : kCeStages; }
+// Staging of the BF16 stores: two boxes per epilogue warp, in turn; or one for
+// the leading parts and one for the remainders.
+__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) { return epi != kCeStats ? 2 * kCeBox : 0u; }
 constexpr size_t ce_smem(int epi) {
-    return (size_t)ce_stages(epi) * kCeStageBytes + (size_t)kCeEpiWarps * ce_stage_warp(epi) + 1024;
+    return (size_t)kCeStages * kCeStageBytes + (size_t)kCeEpiWarps * ce_stage_warp(epi) + 1024;
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -177,7 +175,7 @@ template <int EPI, bool CAP>
 __global__ void __launch_bounds__(kCeThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeMaps tm, const __grid_constant__ CeGemmArgs a) {
     constexpr bool GRADS = EPI == kCeGrads;
-    constexpr int S = ce_stages(EPI);
+    constexpr int S = kCeStages;
     extern __shared__ uint8_t ce_raw[];
     // s_full and s_free are used in the even CTA, the others in both
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_acc[2], s_free[2], s_fin;
@@ -240,17 +238,21 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     // both CTAs' bytes are announced by the even one (the odd one's may land first)
                     if (rank == 0) mbar_arrive_expect_tx(&s_full[slot], 2 * kCeStageBytes);
                     const uint32_t bar = cluster_map(&s_full[slot], 0);
-                    if (tn) {
-                        tma2_load_2d(sa, ta, it.m0, k0, bar);
-                        tma2_load_2d(sa + 8192, ta, it.m0 + 64, k0, bar);
+                    // each operand as one box of two chunks; where rows are no whole number of chunks (the
+                    // second would run into the next row), as two boxes that the matrix's edge cuts
+                    const int ax = tn ? it.m0 : k0, ay = tn ? k0 : it.m0;
+                    if (GRADS || a.whole) {
+                        tma2_load_3d(sa, ta, 0, ay, ax / 64, bar);
                     } else {
-                        tma2_load_2d(sa, ta, k0, it.m0, bar);
+                        tma2_load_2d(sa, ta, ax, ay, bar);
+                        tma2_load_2d(sa + kCeChunk, ta, ax + 64, ay, bar);
                     }
-                    if (!GRADS) {
-                        tma2_load_2d(sb, tb, k0, c.b_row + n0, bar);
+                    const int bx = GRADS ? n0 : k0, by = c.b_row + (GRADS ? k0 : n0);
+                    if (a.whole) {
+                        tma2_load_3d(sb, tb, 0, by, bx / 64, bar);
                     } else {
-                        tma2_load_2d(sb, tb, n0, c.b_row + k0, bar);
-                        tma2_load_2d(sb + 8192, tb, n0 + 64, c.b_row + k0, bar);
+                        tma2_load_2d(sb, tb, bx, by, bar);
+                        tma2_load_2d(sb + kCeChunk, tb, bx + 64, by, bar);
                     }
                 }
             }
@@ -278,7 +280,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 bool ok = true;
                 for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
                     const int slot = (int)(n % S);
-                    if (!mbar_wait_cluster(&s_full[slot], (n / S) & 1u)) {
+                    if (!mbar_wait_bounded(&s_full[slot], (n / S) & 1u)) {
                         fail();
                         ok = false;
                         break;
@@ -288,8 +290,10 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     const uint32_t sb = sa + kCeABytes;
 #pragma unroll
                     for (int kk = 0; kk < kCeK / 16; ++kk) {
-                        const uint64_t da = tn ? umma_desc_sw128_mn(sa + 2048u * kk, 8192u) : umma_desc_sw128(sa + 32u * kk);
-                        const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + 2048u * kk, 8192u) : umma_desc_sw128(sb + 32u * kk);
+                        // K-major: chunk kk / 4, 32 bytes a step; MN-major: 16 rows a step in both chunks
+                        const uint32_t kmaj = kCeChunk * (kk / 4) + 32u * (kk % 4), mn = 2048u * kk;
+                        const uint64_t da = tn ? umma_desc_sw128_mn(sa + mn, kCeChunk) : umma_desc_sw128(sa + kmaj);
+                        const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + mn, kCeChunk) : umma_desc_sw128(sb + kmaj);
                         umma2_bf16(acc_t, da, db, idesc, ks > it.k0 || kk > 0);
                     }
                     umma2_commit(&s_empty[slot]);
@@ -384,8 +388,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                             for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = lo[j / 16][j % 16] = 0.f;
                         }
                     }
-                    uint8_t* box = stg + (size_t)(chunk & 1u) * kBoxes * kCeBox;
-                    if (lane == 0 && chunk >= 2) bulk_wait_read<1>();
+                    uint8_t* box = stg + (kBoxes == 1 ? (size_t)(chunk & 1u) * kCeBox : 0);
+                    if (lane == 0) bulk_wait_read<kBoxes == 1 ? 1 : 0>();   // the box is read out
                     __syncwarp();
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
@@ -554,6 +558,21 @@ bool ce_map(CUtensorMap* map, const void* ptr, long long cols, long long rows, l
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// An operand's map: 128 rows of two 64-column chunks in one box (the columns
+// seen as [cols / 64] chunks, `whole`), or of one chunk.
+bool ce_operand(CUtensorMap* map, const void* ptr, long long cols, long long rows, long long ld, bool whole) {
+    if (!whole) return ce_map(map, ptr, cols, rows, ld, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
+    cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
+    cuuint32_t box[3] = {64, 128, 2};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int ce_item_steps(const CeSide& c) { return std::max(1, c.ksteps / c.splits); }
 int ce_pairs() { return std::max(1, block_gemm_sms() / 2); }
 
@@ -630,7 +649,7 @@ void ce_side(CeSide& c, int parts) {
 }  // namespace
 
 // Logits of h [T][D] and rows a.c[0].b_row on of w [V][D]: their statistics,
-// or dz [T][ldz] (and its remainders dz2).
+// or dz [T][ldz] (and its remainders dz2); ldz is a multiple of 64.
 cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w, int V, void* dz, void* dz2,
                              long long ldz, cudaStream_t s, bool pdl) {
     CeGemmArgs a = in;
@@ -638,8 +657,9 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
     ce_side(c, 1);
     a.c[1].n_items = 0;
     CeMaps tm;
-    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!ce_map(&tm.a[0], h, c.K, c.M, c.K, 64, 128, sw) || !ce_map(&tm.b[0], w, c.K, V, c.K, 64, 128, sw))
+    const auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    a.whole = c.K % 64 == 0;
+    if (!ce_operand(&tm.a[0], h, c.K, c.M, c.K, a.whole) || !ce_operand(&tm.b[0], w, c.K, V, c.K, a.whole))
         return cudaErrorInvalidValue;
     tm.s[0] = tm.s2 = tm.a[0];
     if (dz != nullptr && !ce_map(&tm.s[0], dz, c.s_cols, c.M, ldz, 32, 32, sw64)) return cudaErrorInvalidValue;
@@ -663,12 +683,14 @@ cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz
     ce_side(a.c[1], parts);
     const long long T = a.c[0].M, D = a.c[0].N;
     CeMaps tm;
-    const auto sw = CU_TENSOR_MAP_SWIZZLE_128B, sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
+    const auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
     const void* second = dz2 != nullptr ? dz2 : dz;
-    if (!ce_map(&tm.a[0], dz, ldz, T, ldz, 64, 128, sw) || !ce_map(&tm.a2[0], second, ldz, T, ldz, 64, 128, sw) ||
-        !ce_map(&tm.a[1], dz, ldz, T, ldz, 64, 64, sw) || !ce_map(&tm.a2[1], second, ldz, T, ldz, 64, 64, sw) ||
-        !ce_map(&tm.b[0], w, D, V, D, 64, 64, sw) || !ce_map(&tm.b[1], h, D, T, D, 64, 64, sw))
+    a.whole = D % 64 == 0;   // dz's own rows always are
+    if (!ce_operand(&tm.a[0], dz, ldz, T, ldz, true) || !ce_operand(&tm.a2[0], second, ldz, T, ldz, true) ||
+        !ce_operand(&tm.b[0], w, D, V, D, a.whole) || !ce_operand(&tm.b[1], h, D, T, D, a.whole))
         return cudaErrorInvalidValue;
+    tm.a[1] = tm.a[0];
+    tm.a2[1] = tm.a2[0];
     tm.s[0] = tm.s[1] = tm.s2 = tm.a[0];
     if (a.c[0].part == nullptr && !ce_map(&tm.s[0], dh, D, T, D, 32, 32, sw64)) return cudaErrorInvalidValue;
     if (a.c[1].part == nullptr && !ce_map(&tm.s[1], dw, D, V, D, 32, 32, sw64)) return cudaErrorInvalidValue;

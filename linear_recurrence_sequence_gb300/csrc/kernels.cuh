@@ -558,7 +558,8 @@ struct CeGemmArgs {
     const float* lse;            // kCeDz: [M]
     float softcap, inv_softcap;  // 0: none
     uint32_t* status;
-    int group, extra;            // filled by the launchers: row tiles per group; dw items ahead (see ce_item)
+    int group, extra, whole;     // filled by the launchers: row tiles per group; dw items ahead (see ce_item);
+                                 // rows of h and w are whole 64-column chunks
 };
 
 int ce_m_tiles(long long M);

@@ -105,6 +105,8 @@ def library_path() -> str:
 
 def _load():
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -144,6 +146,9 @@ def _stream(device) -> int:
 
 
 def _need(t, name, dtype, device, shape=None):
+    if t is not None and t.dtype is dtype and t.device == device and t.is_contiguous() and (
+            shape is None or t.shape == shape):
+        return t
     if t is None:
         raise ValueError(f"{name} is required")
     if t.dtype != dtype:
@@ -152,7 +157,7 @@ def _need(t, name, dtype, device, shape=None):
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
+    if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 

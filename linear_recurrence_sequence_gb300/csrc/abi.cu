@@ -1093,10 +1093,11 @@ bool softcap_ok(float c) { return c >= 0.f && c <= 3e38f; }
 struct CeForward {
     size_t stats, zt, sums, total;
 };
-CeForward ce_forward_layout(int T, int V) {
+CeForward ce_forward_layout(int T, int V, int D) {
     CeForward l;
+    const size_t parts = ce_is_few(T, D) ? ce_few_parts(T, kBlockSmsBound) : 2 * ce_n_tiles(V);
     l.stats = 256;
-    l.zt = l.stats + up256((size_t)2 * ce_n_tiles(V) * T * sizeof(float2));
+    l.zt = l.stats + up256(parts * T * sizeof(float2));
     l.sums = l.zt + up256((size_t)T * 4);
     l.total = l.sums + up256((size_t)ce_row_ctas(T) * 16);
     return l;
@@ -1141,7 +1142,7 @@ int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forwa
     const int st = check_ce_shape(T, V, D);
     if (st != LRS_OK) return st;
     if (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) return LRS_ERR_ARG;
-    if (forward_bytes != nullptr) *forward_bytes = ce_forward_layout(T, V).total;
+    if (forward_bytes != nullptr) *forward_bytes = ce_forward_layout(T, V, D).total;
     if (backward_bytes != nullptr)
         *backward_bytes = ce_backward_layout(T, V, D, grad_dtype == LRS_GRAD_FP32, kBlockSmsBound).total;
     return LRS_OK;
@@ -1154,9 +1155,8 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
     if (!softcap_ok(softcap) || !req(h) || !req(w) || !req(target) || !req(loss) || !req(lse) || !req(total) ||
         !req(scratch))
         return LRS_ERR_ARG;
-    const CeForward l = ce_forward_layout(T, V);
+    const CeForward l = ce_forward_layout(T, V, D);
     uint32_t* status = at<uint32_t>(scratch, 0);
-    if (cudaMemsetAsync(status, 0, 16, stream) != cudaSuccess) return LRS_ERR_CUDA;
     CeGemmArgs g = {};
     g.c[0].M = T;
     g.c[0].N = V;
@@ -1168,10 +1168,17 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
     g.softcap = softcap;
     g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
     g.status = status;
-    LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, false));
+    g.clear = 1;
+    int parts = 2 * ce_n_tiles(V);
+    if (ce_is_few(T, D)) {
+        parts = ce_few_parts(T, block_gemm_sms());
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_few(g, h, w, stream));
+    } else {
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, false));
+    }
     LRS_LAUNCH(KID_CE_ROWS, stream,
-               launch_ce_rows(g.stats, g.zt, target, 2 * ce_n_tiles(V), T, V, loss, lse, at<double>(scratch, l.sums),
-                              total, status + 1, status, stream, pdl_ok()));
+               launch_ce_rows(g.stats, g.zt, target, parts, T, V, loss, lse, at<double>(scratch, l.sums), total,
+                              status + 1, status, stream, pdl_ok()));
     return LRS_OK;
 }
 
@@ -1190,7 +1197,6 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     uint32_t* status = at<uint32_t>(scratch, 0);
     void* dz = at<void>(scratch, l.dz);
     void* dz2 = fp32 ? at<void>(scratch, l.dz2) : nullptr;
-    if (cudaMemsetAsync(status, 0, 16, stream) != cudaSuccess) return LRS_ERR_CUDA;
     // the same splits for every piece (the last may be shorter)
     int h_splits, w_splits;
     ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &h_splits, &w_splits);
@@ -1212,6 +1218,7 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         g.softcap = softcap;
         g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
         g.status = status;
+        g.clear = i == 0;
         LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, dz, dz2, l.ldz, stream, i > 0 && pdl_ok()));
         // dh (+)= dz w; dw's rows of this piece = dz^T h
         CeGemmArgs d = {};

@@ -51,13 +51,15 @@ constexpr uint32_t kCeChunk = 128 * 128;        // a 64-column chunk of 128 rows
 constexpr uint32_t kCeStageBytes = kCeABytes + kCeBBytes;
 constexpr uint32_t kCeTmemCols = 2 * kCeN;
 constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store box (64-byte swizzle)
-// Staging of the BF16 stores: two boxes per epilogue warp, in turn; or one for
-// the leading parts and one for the remainders.
-__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) { return epi != kCeStats ? 2 * kCeBox : 0u; }
+constexpr uint32_t kCeWideBox = 2 * kCeBox;   // [32][64] (128-byte swizzle)
+// Staging of the BF16 stores, one box per epilogue warp of [32 rows][64
+// columns]; with remainders two of [32][32], one for them.
+__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) { return epi != kCeStats ? kCeWideBox : 0u; }
 constexpr size_t ce_smem(int epi) {
     return (size_t)kCeStages * kCeStageBytes + (size_t)kCeEpiWarps * ce_stage_warp(epi) + 1024;
 }
 
+constexpr int kCeFewThreads = 1024;   // per SM, of the kernel for one token (half of it for more)
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
@@ -202,6 +204,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
     }
     pdl_trigger();
     pdl_wait();
+    // a call's first kernel clears the status word and the rows' ticket (a wait gives up 0.2 s from here at the soonest)
+    if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) a.status[0] = a.status[1] = 0u;
     __syncthreads();
     cluster_sync();   // the pair's barriers and tensor memory exist
     tmem_fence_after_sync();
@@ -236,12 +240,16 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     const int n0 = it.nt * kCeN + 128 * rank;
                     const CUtensorMap* ta = second ? ta2 : ta1;
                     // both CTAs' bytes are announced by the even one (the odd one's may land first)
-                    if (rank == 0) mbar_arrive_expect_tx(&s_full[slot], 2 * kCeStageBytes);
+                    // rows of A past the matrix are not loaded: what their accumulator rows hold is not used
+                    if (rank == 0)
+                        mbar_arrive_expect_tx(&s_full[slot],
+                                              2 * kCeStageBytes - (it.m0 + 128 < c.M ? 0u : kCeABytes));
                     const uint32_t bar = cluster_map(&s_full[slot], 0);
                     // each operand as one box of two chunks; where rows are no whole number of chunks (the
                     // second would run into the next row), as two boxes that the matrix's edge cuts
                     const int ax = tn ? it.m0 : k0, ay = tn ? k0 : it.m0;
-                    if (GRADS || a.whole) {
+                    if (it.m0 >= c.M) {
+                    } else if (GRADS || a.whole) {
                         tma2_load_3d(sa, ta, 0, ay, ax / 64, bar);
                     } else {
                         tma2_load_2d(sa, ta, ax, ay, bar);
@@ -310,7 +318,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const int q4 = warp & 3, hf = warp >> 2;
         const int row = 32 * q4 + lane;
         uint8_t* stg = ring + (size_t)S * kCeStageBytes + (size_t)warp * ce_stage_warp(EPI);
-        uint32_t chunk = 0, item = 0;
+        uint32_t item = 0;
         for (; !*abort_flag && ce_item(a, GRADS, pair, pairs, (int)item, rank, it); ++item) {
             const CeSide& c0 = a.c[it.side];
             const uint32_t buf = item & 1u;
@@ -362,7 +370,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 const bool store = it.m0 + 32 * q4 < c0.M;   // rows past the matrix are clipped by the TMA
                 const int nv = c0.N - it.nt * kCeN;                 // columns of this tile inside the matrix
 #pragma unroll 1
-                for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32, ++chunk) {
+                for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
                     float v[2][16], lo[2][16];
                     tmem_ld16x2(taddr + (uint32_t)c, taddr + (uint32_t)(c + 16), v[0], v[1]);
                     if (EPI == kCeDz || EPI == kCeDz2) {
@@ -388,24 +396,28 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                             for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = lo[j / 16][j % 16] = 0.f;
                         }
                     }
-                    uint8_t* box = stg + (kBoxes == 1 ? (size_t)(chunk & 1u) * kCeBox : 0);
-                    if (lane == 0) bulk_wait_read<kBoxes == 1 ? 1 : 0>();   // the box is read out
+                    const bool second = (c & 32) != 0;   // of a wide box
+                    if ((kBoxes == 2 || !second) && lane == 0) bulk_wait_read<0>();   // the box is read out
                     __syncwarp();
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        const int pu = u ^ ((lane >> 1) & 3);
-                        *reinterpret_cast<uint4*>(box + (size_t)lane * 64 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
-                        if (EPI == kCeDz2)
-                            *reinterpret_cast<uint4*>(box + kCeBox + (size_t)lane * 64 + 16 * pu) =
+                        if (kBoxes == 2) {
+                            const int pu = u ^ ((lane >> 1) & 3);
+                            *reinterpret_cast<uint4*>(stg + (size_t)lane * 64 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
+                            *reinterpret_cast<uint4*>(stg + kCeBox + (size_t)lane * 64 + 16 * pu) =
                                 pack8(lo[u >> 1] + 8 * (u & 1));
+                        } else {
+                            const int pu = (u + (second ? 4 : 0)) ^ (lane & 7);
+                            *reinterpret_cast<uint4*>(stg + (size_t)lane * 128 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
+                        }
                     }
+                    if (kBoxes == 1 && !second) continue;
                     fence_proxy_async();
                     __syncwarp();
-                    if (lane == 0) {
-                        if (store && it.nt * kCeN + c < c0.s_cols) {
-                            tma_store_2d(&tm.s[it.side], it.nt * kCeN + c, y, box);
-                            if (EPI == kCeDz2) tma_store_2d(&tm.s2, it.nt * kCeN + c, y, box + kCeBox);
-                        }
+                    const int x = it.nt * kCeN + c - (kBoxes == 1 ? 32 : 0);
+                    if (lane == 0 && store && x < c0.s_cols) {
+                        tma_store_2d(&tm.s[it.side], x, y, stg);
+                        if (EPI == kCeDz2) tma_store_2d(&tm.s2, x, y, stg + kCeBox);
                         bulk_commit();
                     }
                 }
@@ -432,6 +444,96 @@ __device__ __forceinline__ float2 ce_join(float2 p, float2 q) {
     return make_float2(m, p.y * ex2_approx((p.x - ref) * kLog2e) + q.y * ex2_approx((q.x - ref) * kLog2e));
 }
 
+// The statistics of a few tokens (T <= 4, RT = T rounded up to a power of two):
+// every row of w is read once by one warp, so the kernel is bound by reading w,
+// where the tensor-core tiles would spend the time of 256 rows on them and have
+// too few tiles to share out (one token, 32768 x 1024: see launch_ce_few).
+// A warp takes a run of rows, R at a time, a lane 8 channels of each (16
+// bytes); the tokens' channels come from shared memory, once for the R rows.
+// R T sums over the lanes end in one lane each by halving exchanges, and each
+// lane keeps its own running (max, sum), joined over the CTA at the end.
+template <int RT, int R>
+__global__ void __launch_bounds__(256, kCeFewThreads / 256 / (RT == 1 ? 1 : 2)) ce_few_kernel(const uint4* __restrict__ h, const uint4* __restrict__ w, int T,
+                                                     const CeGemmArgs a) {
+    constexpr int NA = RT * R;
+    static_assert(NA <= 32, "one lane a sum");
+    extern __shared__ __align__(16) uint4 sh[];   // [T][D / 8]
+    __shared__ float2 red[8][NA];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int nv = a.c[0].K / 8, V = a.c[0].N;
+    pdl_trigger();
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) a.status[0] = a.status[1] = 0u;
+    for (int i = threadIdx.x; i < T * nv; i += 256) sh[i] = __ldg(h + i);
+    __syncthreads();
+    const long long id = (long long)blockIdx.x * 8 + warp, n = (long long)gridDim.x * 8;
+    const int v0 = (int)(V * id / n), v1 = (int)(V * (id + 1) / n);
+    // this lane's sum is (row r, token t); the lanes past NA repeat others'
+    const int t = lane % RT, r = (lane / RT) % R;
+    const long long tgt = t < T ? a.target[t] : -1;
+    float mx = -INFINITY, sum = 0.f;
+    for (int v = v0; v < v1; v += R) {
+        float acc[NA];
+#pragma unroll
+        for (int i = 0; i < NA; ++i) acc[i] = 0.f;
+#pragma unroll 2
+        for (int c = lane; c < nv; c += 32) {
+            uint4 q[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                q[i] = v + i < v1 ? __ldcs(w + (size_t)(v + i) * nv + c) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < RT; ++j) {
+                const uint4 x = sh[(RT == 1 || j < T ? j : 0) * nv + c];
+                const float2 x0 = bf2_to_f2(x.x), x1 = bf2_to_f2(x.y), x2 = bf2_to_f2(x.z), x3 = bf2_to_f2(x.w);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float2 y0 = bf2_to_f2(q[i].x), y1 = bf2_to_f2(q[i].y), y2 = bf2_to_f2(q[i].z),
+                                 y3 = bf2_to_f2(q[i].w);
+                    float s = acc[i * RT + j];
+                    s = fmaf(x0.x, y0.x, s);
+                    s = fmaf(x0.y, y0.y, s);
+                    s = fmaf(x1.x, y1.x, s);
+                    s = fmaf(x1.y, y1.y, s);
+                    s = fmaf(x2.x, y2.x, s);
+                    s = fmaf(x2.y, y2.y, s);
+                    s = fmaf(x3.x, y3.x, s);
+                    s = fmaf(x3.y, y3.y, s);
+                    acc[i * RT + j] = s;
+                }
+            }
+        }
+        // halving exchanges: lane l ends with the sum of index l % NA over all lanes
+#pragma unroll
+        for (int k = NA / 2; k >= 1; k >>= 1) {
+            const bool up = (lane & k) != 0;
+#pragma unroll
+            for (int i = 0; i < k; ++i) {
+                const float give = up ? acc[i] : acc[i + k], keep = up ? acc[i + k] : acc[i];
+                acc[i] = keep + __shfl_xor_sync(0xffffffffu, give, k);
+            }
+        }
+        float z = acc[0];
+#pragma unroll
+        for (int k = NA; k < 32; k <<= 1) z += __shfl_xor_sync(0xffffffffu, z, k);
+        if (a.softcap > 0.f) z = ce_cap(a, z);
+        if (t < T && v + r < v1) {
+            if (tgt == v + r && lane < NA) a.zt[t] = z;
+            const float m = fmaxf(mx, z), ref = m == -INFINITY ? 0.f : m;
+            sum = fmaf(sum, ex2_approx((mx - ref) * kLog2e), ex2_approx((z - ref) * kLog2e));
+            mx = m;
+        }
+    }
+    if (lane < NA) red[warp][lane] = make_float2(mx, sum);
+    __syncthreads();
+    if (warp == 0 && lane < T) {
+        float2 p = make_float2(-INFINITY, 0.f);
+        for (int k = 0; k < 8; ++k)
+            for (int i = 0; i < R; ++i) p = ce_join(p, red[k][i * RT + lane]);
+        a.stats[(size_t)blockIdx.x * T + lane] = p;
+    }
+}
+
 // Rows' statistics joined over their `parts` column blocks, in a fixed order:
 // a CTA takes kCeRows consecutive rows, thread (row, group) the parts group,
 // group + kCeGroups, ...; then lse, loss, and the CTA's (sum of losses, number
@@ -452,8 +554,23 @@ __global__ void __launch_bounds__(256) ce_rows_kernel(const float2* __restrict__
     const int r = threadIdx.x % ROWS, g = threadIdx.x / ROWS;
     const int t = blockIdx.x * ROWS + r;
     float2 p = make_float2(-INFINITY, 0.f);
-    if (t < T)
-        for (int i = g; i < parts; i += GROUPS) p = ce_join(p, __ldcg(stats + (size_t)i * T + t));
+    if (t < T) {
+        // eight parts at a time: their loads together, one maximum, independent exponentials
+        for (int i = g; i < parts; i += 8 * GROUPS) {
+            float2 q[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                q[k] = i + k * GROUPS < parts ? __ldcg(stats + (size_t)(i + k * GROUPS) * T + t) : make_float2(-INFINITY, 0.f);
+            float m = p.x;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmaxf(m, q[k].x);
+            const float ref = m == -INFINITY ? 0.f : m;
+            float s = p.y * ex2_approx((p.x - ref) * kLog2e);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s = fmaf(q[k].y, ex2_approx((q[k].x - ref) * kLog2e), s);
+            p = make_float2(m, s);
+        }
+    }
     red[g][r] = p;
     __syncthreads();
     for (int k = GROUPS / 2; k >= 1; k >>= 1) {
@@ -573,6 +690,11 @@ bool ce_operand(CUtensorMap* map, const void* ptr, long long cols, long long row
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A BF16 result's map: the store boxes.
+bool ce_result(CUtensorMap* map, const void* ptr, long long cols, long long rows, long long ld, bool wide) {
+    return ce_map(map, ptr, cols, rows, ld, wide ? 64 : 32, 32, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
 int ce_item_steps(const CeSide& c) { return std::max(1, c.ksteps / c.splits); }
 int ce_pairs() { return std::max(1, block_gemm_sms() / 2); }
 
@@ -657,13 +779,12 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
     ce_side(c, 1);
     a.c[1].n_items = 0;
     CeMaps tm;
-    const auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
     a.whole = c.K % 64 == 0;
     if (!ce_operand(&tm.a[0], h, c.K, c.M, c.K, a.whole) || !ce_operand(&tm.b[0], w, c.K, V, c.K, a.whole))
         return cudaErrorInvalidValue;
     tm.s[0] = tm.s2 = tm.a[0];
-    if (dz != nullptr && !ce_map(&tm.s[0], dz, c.s_cols, c.M, ldz, 32, 32, sw64)) return cudaErrorInvalidValue;
-    if (dz2 != nullptr && !ce_map(&tm.s2, dz2, c.s_cols, c.M, ldz, 32, 32, sw64)) return cudaErrorInvalidValue;
+    if (dz != nullptr && !ce_result(&tm.s[0], dz, c.s_cols, c.M, ldz, dz2 == nullptr)) return cudaErrorInvalidValue;
+    if (dz2 != nullptr && !ce_result(&tm.s2, dz2, c.s_cols, c.M, ldz, false)) return cudaErrorInvalidValue;
     tm.a[1] = tm.a2[0] = tm.a2[1] = tm.b[1] = tm.s[1] = tm.a[0];
     // 32 MB of h per group of row tiles
     a.group = (int)std::max(1LL, std::min<long long>(c.m_tiles, (32LL << 20) / ((long long)c.K * 2 * kCeM)));
@@ -671,6 +792,19 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
     if (dz == nullptr) return cap ? ce_launch<kCeStats, true>(tm, a, s, pdl) : ce_launch<kCeStats, false>(tm, a, s, pdl);
     if (dz2 == nullptr) return cap ? ce_launch<kCeDz, true>(tm, a, s, pdl) : ce_launch<kCeDz, false>(tm, a, s, pdl);
     return cap ? ce_launch<kCeDz2, true>(tm, a, s, pdl) : ce_launch<kCeDz2, false>(tm, a, s, pdl);
+}
+
+// The statistics of T <= 4 tokens, one part a CTA.  Against 32768 x 1024 (67 MB
+// of w not in the L2, forward with its second kernel) 1, 2, 4 tokens take
+// TIME_FEW us, 29 us by the tensor-core tiles; from 6 on those are faster (30 against 34 us).
+bool ce_is_few(int T, int D) { return T <= 4 && (long long)T * D * 2 <= 48 * 1024; }
+int ce_few_parts(int T, int sms) { return kCeFewThreads / 256 / (T == 1 ? 1 : 2) * sms; }
+cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s) {
+    const int T = a.c[0].M, D = a.c[0].K;
+    auto* fn = T == 1 ? ce_few_kernel<1, 8> : T == 2 ? ce_few_kernel<2, 8> : ce_few_kernel<4, 4>;
+    const size_t smem = (size_t)T * D * 2;
+    return launch_ex(fn, dim3((unsigned)ce_few_parts(T, block_gemm_sms())), dim3(256), smem, s, false,
+                     static_cast<const uint4*>(h), static_cast<const uint4*>(w), T, a);
 }
 
 // a.c[0]: dh [T][D] (+)= dz w's rows b_row on; a.c[1]: dw = dz^T h, rows s_row
@@ -683,7 +817,6 @@ cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz
     ce_side(a.c[1], parts);
     const long long T = a.c[0].M, D = a.c[0].N;
     CeMaps tm;
-    const auto sw64 = CU_TENSOR_MAP_SWIZZLE_64B;
     const void* second = dz2 != nullptr ? dz2 : dz;
     a.whole = D % 64 == 0;   // dz's own rows always are
     if (!ce_operand(&tm.a[0], dz, ldz, T, ldz, true) || !ce_operand(&tm.a2[0], second, ldz, T, ldz, true) ||
@@ -692,24 +825,24 @@ cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz
     tm.a[1] = tm.a[0];
     tm.a2[1] = tm.a2[0];
     tm.s[0] = tm.s[1] = tm.s2 = tm.a[0];
-    if (a.c[0].part == nullptr && !ce_map(&tm.s[0], dh, D, T, D, 32, 32, sw64)) return cudaErrorInvalidValue;
-    if (a.c[1].part == nullptr && !ce_map(&tm.s[1], dw, D, V, D, 32, 32, sw64)) return cudaErrorInvalidValue;
+    if (a.c[0].part == nullptr && !ce_result(&tm.s[0], dh, D, T, D, true)) return cudaErrorInvalidValue;
+    if (a.c[1].part == nullptr && !ce_result(&tm.s[1], dw, D, V, D, true)) return cudaErrorInvalidValue;
     return ce_launch<kCeGrads, false>(tm, a, s, pdl);
 }
 
 // Rows per CTA of the statistics kernel: 32 (a warp reads 32 rows of one part),
-// or one when there are few rows and the parts are what there is to share out.
-int ce_row_ctas(int T) { return T <= 256 ? T : (T + 31) / 32; }
+// 8 or one where there are fewer rows and the parts are what there is to share
+// out.
+int ce_rows_per_cta(int T) { return T <= 256 ? 1 : T <= 8192 ? 8 : 32; }
+int ce_row_ctas(int T) { return (T + ce_rows_per_cta(T) - 1) / ce_rows_per_cta(T); }
 
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
                            float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
                            cudaStream_t s, bool pdl) {
-    const dim3 grid((unsigned)ce_row_ctas(T));
-    if (T <= 256)
-        return launch_ex(ce_rows_kernel<1>, grid, dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse,
-                         sums, total, ticket, status);
-    return launch_ex(ce_rows_kernel<32>, grid, dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse, sums,
-                     total, ticket, status);
+    const int rows = ce_rows_per_cta(T);
+    auto* fn = rows == 1 ? ce_rows_kernel<1> : rows == 8 ? ce_rows_kernel<8> : ce_rows_kernel<32>;
+    return launch_ex(fn, dim3((unsigned)ce_row_ctas(T)), dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse,
+                     sums, total, ticket, status);
 }
 
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,

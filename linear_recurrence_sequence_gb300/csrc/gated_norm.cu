@@ -87,17 +87,20 @@ __device__ __forceinline__ void load_product(const float* p, const float* q, int
 }
 
 // Sum over the threads of a row (blockDim.x of them, whole warps).  `red` is
-// this sum's own buffer: sums that follow each other use two buffers in turn,
-// so one barrier each is enough.
+// this sum's own buffer, zeros past the row's warps: sums that follow each
+// other use two buffers in turn, so one barrier each is enough.
 __device__ __forceinline__ float row_sum(float v, float (*red)[kGnMaxWarps]) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
+    if (blockDim.x == 32) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.y][threadIdx.x >> 5] = v;
     __syncthreads();
+    const float4* r = reinterpret_cast<const float4*>(red[threadIdx.y]);
     v = 0.f;
-    for (int w = 0; w < warps; ++w) v += red[threadIdx.y][w];
+    for (int w = 0; w < (int)blockDim.x; w += 128, ++r) {
+        const float4 q = *r;
+        v += (q.x + q.y) + (q.z + q.w);
+    }
     return v;
 }
 
@@ -107,31 +110,67 @@ template <int NOPS>
 struct GnRing {
     const uint4* src[NOPS];
     long long T;
-    int nv, stages;
+    int nv, stages, slot, asked;   // slot: of the current group; asked: of the next one to ask for
+    uint32_t phase, op_bytes;
+    long long next;                // first row of the next group to ask for
     uint8_t* buf;
     uint64_t* full;
+    const uint8_t* mine;           // this thread's place in the current slot
 
-    __device__ __forceinline__ uint32_t op_bytes() const { return blockDim.y * (uint32_t)nv * 16u; }
-    // Thread 0: asks for row group `it` of this CTA (groups blockIdx.x, + gridDim.x, ...).
-    __device__ __forceinline__ void ask(int it) const {
-        const long long row = ((long long)blockIdx.x + (long long)it * gridDim.x) * blockDim.y;
-        if (row >= T) return;
-        const uint32_t bytes = (uint32_t)min((long long)blockDim.y, T - row) * (uint32_t)nv * 16u;
-        const int slot = it % stages;
-        mbar_arrive_expect_tx(&full[slot], NOPS * bytes);
+    __device__ __forceinline__ void start(long long rows, int nv_, int stages_, uint8_t* buf_, uint64_t* full_) {
+        T = rows;
+        nv = nv_;
+        stages = stages_;
+        buf = buf_;
+        full = full_;
+        slot = asked = 0;
+        phase = 0u;
+        op_bytes = blockDim.y * (uint32_t)nv * 16u;
+        next = (long long)blockIdx.x * blockDim.y;
+        mine = buf + (threadIdx.y * (uint32_t)nv + threadIdx.x) * 16u;
+        if (threadIdx.x == 0 && threadIdx.y == 0) {
+            for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
+            for (int i = 0; i < stages; ++i) ask();
+        }
+        __syncthreads();
+    }
+    // Thread 0: asks for the CTA's next group of rows (groups blockIdx.x, + gridDim.x, ...).
+    __device__ __forceinline__ void ask() {
+        if (next < T) {
+            const uint32_t bytes = (uint32_t)min((long long)blockDim.y, T - next) * (uint32_t)nv * 16u;
+            mbar_arrive_expect_tx(&full[asked], NOPS * bytes);
 #pragma unroll
-        for (int k = 0; k < NOPS; ++k)
-            bulk_load(buf + ((size_t)slot * NOPS + k) * op_bytes(), src[k] + (size_t)row * nv, bytes, &full[slot]);
+            for (int k = 0; k < NOPS; ++k)
+                bulk_load(buf + (asked * NOPS + k) * op_bytes, src[k] + (size_t)next * nv, bytes, &full[asked]);
+        }
+        next += (long long)gridDim.x * blockDim.y;
+        if (++asked == stages) asked = 0;
     }
-    // Operand k of this thread's row, group of channels v.
-    __device__ __forceinline__ uint4 get(int it, int k, int v) const {
-        return *reinterpret_cast<const uint4*>(buf + ((size_t)(it % stages) * NOPS + k) * op_bytes() +
-                                               ((size_t)threadIdx.y * nv + v) * 16u);
+    // Operand k of this thread's row, its group of channels `at` threads on.
+    __device__ __forceinline__ uint4 get(int k, int at) const {
+        return *reinterpret_cast<const uint4*>(mine + (slot * NOPS + k) * op_bytes + at * 16);
     }
-    __device__ __forceinline__ bool wait(int it) const {
-        return mbar_wait_bounded(&full[it % stages], (uint32_t)(it / stages) & 1u);
+    __device__ __forceinline__ bool wait() const { return mbar_wait_bounded(&full[slot], phase); }
+    // Every thread has taken its operands (rows of one warp met no barrier in their sums): the slot is filled again.
+    __device__ __forceinline__ void taken() {
+        if (blockDim.x == 32) __syncthreads();
+        if (threadIdx.x == 0 && threadIdx.y == 0) {
+            fence_proxy_async();
+            ask();
+        }
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1u;
+        }
     }
 };
+// Zeroes the sums' buffers (the places past a row's warps stay zero).
+__device__ __forceinline__ void clear_red(float (*red)[kGnMaxThreads / 32][kGnMaxWarps]) {
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < 2 * (kGnMaxThreads / 32) * kGnMaxWarps;
+         i += blockDim.x * blockDim.y)
+        red[0][0][i] = 0.f;
+    __syncthreads();
+}
 constexpr int kGnStagesMax = 4;
 
 // VEC: groups of 8 channels per thread (group threadIdx.x + k blockDim.x).
@@ -139,29 +178,20 @@ constexpr int kGnStagesMax = 4;
 template <bool Y, bool G, int VEC, bool RING>
 __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const GatedNormArgs a) {
     constexpr int NOPS = 1 + Y + G;
-    __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
+    __shared__ __align__(16) float red[2][kGnMaxThreads / 32][kGnMaxWarps];
     __shared__ __align__(8) uint64_t full[kGnStagesMax];
     extern __shared__ __align__(128) uint8_t buf[];
     pdl_trigger();
     pdl_wait();
     const int nv = a.D / 8;
     const float inv_d = 1.f / (float)a.D;
-    const bool first = threadIdx.x == 0 && threadIdx.y == 0;
+    if (blockDim.x > 32) clear_red(red);
     GnRing<NOPS> ring;
     if (RING) {
         ring.src[0] = a.x;
         if (Y) ring.src[Y] = a.y;
         if (G) ring.src[Y + G] = a.g;
-        ring.T = a.T;
-        ring.nv = nv;
-        ring.stages = a.stages;
-        ring.buf = buf;
-        ring.full = full;
-        if (first) {
-            for (int i = 0; i < a.stages; ++i) mbar_init(&full[i], 1);
-            for (int i = 0; i < a.stages; ++i) ring.ask(i);
-        }
-        __syncthreads();
+        ring.start(a.T, nv, a.stages, buf, full);
     }
     // a thread's channels are the same in every row: so are its vectors
     float gm[VEC][8], sg[VEC][8];
@@ -176,16 +206,16 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
     for (long long base = (long long)blockIdx.x * blockDim.y; base < a.T; base += (long long)gridDim.x * blockDim.y, ++it) {
         const long long row = base + threadIdx.y;
         uint4 qx[VEC], qy[VEC], qg[VEC];
-        if (RING) lost |= !ring.wait(it);
+        if (RING) lost |= !ring.wait();
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             const size_t o = (size_t)row * nv + v;
             qx[k] = qy[k] = qg[k] = make_uint4(0u, 0u, 0u, 0u);
             if (row < a.T && v < nv) {
-                qx[k] = RING ? ring.get(it, 0, v) : __ldg(a.x + o);
-                if (Y) qy[k] = RING ? ring.get(it, Y, v) : __ldg(a.y + o);
-                if (G) qg[k] = RING ? ring.get(it, Y + G, v) : __ldg(a.g + o);
+                qx[k] = RING ? ring.get(0, k * blockDim.x) : __ldg(a.x + o);
+                if (Y) qy[k] = RING ? ring.get(Y, k * blockDim.x) : __ldg(a.y + o);
+                if (G) qg[k] = RING ? ring.get(Y + G, k * blockDim.x) : __ldg(a.g + o);
             }
         }
         float r[VEC][8], rstd1 = 0.f;
@@ -200,7 +230,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
 #pragma unroll
                 for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
             }
-            rstd1 = 1.f / sqrtf(row_sum(ss, red[0]) * inv_d + a.eps);
+            rstd1 = rsqrtf(fmaf(row_sum(ss, red[0]), inv_d, a.eps));
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 float y[8], g[8];
@@ -218,15 +248,8 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
         for (int k = 0; k < VEC; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) ss = fmaf(r[k][i], r[k][i], ss);
-        const float rstd2 = 1.f / sqrtf(row_sum(ss, red[Y ? 1 : it & 1]) * inv_d + a.eps);
-        if (RING) {
-            // every thread has taken its operands (rows of one warp meet no barrier in their sums)
-            if (blockDim.x == 32) __syncthreads();
-            if (first) {
-                fence_proxy_async();
-                ring.ask(it + a.stages);
-            }
-        }
+        const float rstd2 = rsqrtf(fmaf(row_sum(ss, red[Y ? 1 : it & 1]), inv_d, a.eps));
+        if (RING) ring.taken();
         if (row >= a.T) continue;
         if (threadIdx.x == 0 && a.rstd != nullptr)
             a.rstd[row] = lost ? make_float2(NAN, NAN) : make_float2(rstd1, rstd2);
@@ -247,7 +270,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
 template <bool Y, bool G, int VEC>
 __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const GatedNormBwdArgs a) {
     constexpr int NOPS = 3 + Y + G;
-    __shared__ float red[2][kGnMaxThreads / 32][kGnMaxWarps];
+    __shared__ __align__(16) float red[2][kGnMaxThreads / 32][kGnMaxWarps];
     __shared__ __align__(8) uint64_t full[kGnStagesMax];
     extern __shared__ __align__(128) uint8_t buf[];   // the ring, then the sums [2][rows][D]
     pdl_trigger();
@@ -255,23 +278,14 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     const GatedNormArgs& f = a.f;
     const int nv = f.D / 8;
     const float inv_d = 1.f / (float)f.D;
-    const bool first = threadIdx.x == 0 && threadIdx.y == 0;
+    if (blockDim.x > 32) clear_red(red);
     GnRing<NOPS> ring;
     ring.src[0] = f.x;
     ring.src[1] = a.dh;
     ring.src[2] = a.dr != nullptr ? a.dr : a.dh;   // without dr its place is not read
     if (Y) ring.src[2 + Y] = f.y;
     if (G) ring.src[2 + Y + G] = f.g;
-    ring.T = f.T;
-    ring.nv = nv;
-    ring.stages = f.stages;
-    ring.buf = buf;
-    ring.full = full;
-    if (first) {
-        for (int i = 0; i < f.stages; ++i) mbar_init(&full[i], 1);
-        for (int i = 0; i < f.stages; ++i) ring.ask(i);
-    }
-    __syncthreads();
+    ring.start(f.T, nv, f.stages, buf, full);
     // a thread's channels are the same in every row: so are its vectors
     float gm[VEC][8], sg[VEC][8];
     float dpre[VEC][8], sum[VEC][8];
@@ -283,25 +297,30 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
 #pragma unroll
         for (int i = 0; i < 8; ++i) dpre[k][i] = sum[k][i] = 0.f;
     }
+    // the rows' reciprocal norms, one group ahead
+    float2 ahead = make_float2(0.f, 0.f);
+    if ((long long)blockIdx.x * blockDim.y + threadIdx.y < f.T)
+        ahead = __ldg(f.rstd + (long long)blockIdx.x * blockDim.y + threadIdx.y);
     bool lost = false;
     int it = 0;
     for (long long base = (long long)blockIdx.x * blockDim.y; base < f.T; base += (long long)gridDim.x * blockDim.y, ++it) {
         const long long row = base + threadIdx.y;
         uint4 qx[VEC], qy[VEC], qg[VEC], qr[VEC], qh[VEC];
-        float2 rs = make_float2(0.f, 0.f);
-        if (row < f.T) rs = __ldg(f.rstd + row);
-        lost |= !ring.wait(it);
+        float2 rs = ahead;
+        const long long after = row + (long long)gridDim.x * blockDim.y;
+        ahead = after < f.T ? __ldg(f.rstd + after) : make_float2(0.f, 0.f);
+        lost |= !ring.wait();
         if (lost) rs = make_float2(NAN, NAN);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             qx[k] = qy[k] = qg[k] = qr[k] = qh[k] = make_uint4(0u, 0u, 0u, 0u);
             if (row < f.T && v < nv) {
-                qx[k] = ring.get(it, 0, v);
-                qh[k] = ring.get(it, 1, v);
-                if (a.dr != nullptr) qr[k] = ring.get(it, 2, v);
-                if (Y) qy[k] = ring.get(it, 2 + Y, v);
-                if (G) qg[k] = ring.get(it, 2 + Y + G, v);
+                qx[k] = ring.get(0, k * blockDim.x);
+                qh[k] = ring.get(1, k * blockDim.x);
+                if (a.dr != nullptr) qr[k] = ring.get(2, k * blockDim.x);
+                if (Y) qy[k] = ring.get(2 + Y, k * blockDim.x);
+                if (G) qg[k] = ring.get(2 + Y + G, k * blockDim.x);
             }
         }
         // q = r rstd2, a = dh gamma_pre, mean(a q)
@@ -332,12 +351,7 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
             }
         }
         const float mean = row_sum(s, red[Y ? 0 : it & 1]) * inv_d;
-        // every thread has taken its operands (rows of one warp meet no barrier in their sums)
-        if (blockDim.x == 32) __syncthreads();
-        if (first) {
-            fence_proxy_async();
-            ring.ask(it + f.stages);
-        }
+        ring.taken();
         float dx[VEC][8];
         s = 0.f;
 #pragma unroll

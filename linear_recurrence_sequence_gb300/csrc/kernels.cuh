@@ -557,7 +557,8 @@ struct CeGemmArgs {
     const float* total;
     const float* lse;            // kCeDz: [M]
     float softcap, inv_softcap;  // 0: none
-    uint32_t* status;
+    uint32_t* status;            // two words: the status, the rows' ticket
+    int clear;                   // the call's first kernel: clears both
     int group, extra, whole;     // filled by the launchers: row tiles per group; dw items ahead (see ce_item);
                                  // rows of h and w are whole 64-column chunks
 };
@@ -567,6 +568,9 @@ int ce_n_tiles(long long N);
 void ce_grad_splits(long long T, long long V, long long D, int parts, int sms, int* h_splits, int* w_splits);
 cudaError_t launch_ce_logits(const CeGemmArgs& a, const void* h, const void* w, int V, void* dz, void* dz2,
                              long long ldz, cudaStream_t s, bool pdl);
+bool ce_is_few(int T, int D);
+int ce_few_parts(int T, int sms);
+cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s);
 cudaError_t launch_ce_grads(const CeGemmArgs& a, const void* dz, const void* dz2, long long ldz, const void* h,
                             const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl);
 int ce_row_ctas(int T);

@@ -166,6 +166,13 @@ def _opt(t, name, dtype, device, shape=None):
     return None if t is None else _need(t, name, dtype, device, shape)
 
 
+def _like(t, out, key):
+    """An output of t's shape and type (cheaper to allocate than by its shape)."""
+    if out is not None and key in out and out[key] is not None:
+        return _need(out[key], key, t.dtype, t.device, t.shape)
+    return torch.empty_like(t)
+
+
 def _empty(shape, dtype, device, out, key):
     if out is not None and key in out and out[key] is not None:
         return _need(out[key], key, dtype, device, shape)
@@ -721,8 +728,8 @@ def gated_norm_forward(x, y=None, gate=None, gamma_post=None, scale=None, gamma_
     h = RMSNorm(x; gamma_pre) and r is x itself).  Returns dict(r, h, saved)."""
     dev, T, D = _gated_norm_inputs(x, y, gate, gamma_post, scale, gamma_pre)
     nsaved, _ = gated_norm_workspace_bytes(T, D)
-    r = _empty(x.shape, torch.bfloat16, dev, out, "r") if y is not None else None
-    h = _empty(x.shape, torch.bfloat16, dev, out, "h")
+    r = _like(x, out, "r") if y is not None else None
+    h = _like(x, out, "h")
     if saved is None:
         saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
     if saved.numel() < nsaved:
@@ -748,14 +755,14 @@ def gated_norm_backward(dr, dh, x, y, gate, gamma_post, scale, gamma_pre, saved,
         scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
     if scratch.numel() < nscratch:
         raise ValueError("scratch buffer is too small")
-    o = {"dx": _empty(x.shape, torch.bfloat16, dev, out, "dx"), "dy": None, "dgate": None, "dgamma_post": None,
+    o = {"dx": _like(x, out, "dx"), "dy": None, "dgate": None, "dgamma_post": None,
          "dscale": None, "dgamma_pre": _empty((D,), torch.float32, dev, out, "dgamma_pre")}
     if y is not None:
-        o["dy"] = _empty(x.shape, torch.bfloat16, dev, out, "dy")
+        o["dy"] = _like(x, out, "dy")
         o["dgamma_post"] = _empty((D,), torch.float32, dev, out, "dgamma_post")
         o["dscale"] = _empty((D,), torch.float32, dev, out, "dscale")
     if gate is not None:
-        o["dgate"] = _empty(x.shape, torch.bfloat16, dev, out, "dgate")
+        o["dgate"] = _like(x, out, "dgate")
     _check("gated_norm_backward",
            _load().gated_norm_backward(_ptr(dr), _ptr(dh), _ptr(x), _ptr(y), _ptr(gate), _ptr(gamma_post), _ptr(scale),
                                        _ptr(gamma_pre), T, D, eps, _ptr(saved), _ptr(o["dx"]), _ptr(o["dy"]),
@@ -801,6 +808,7 @@ class AdamwPlan:
         self.device = tensors[0]["param"].device
         self.tensors = tensors
         self._list = (_AdamwTensor * len(tensors))()
+        self._at = ctypes.addressof(self._list)
         for i, t in enumerate(tensors):
             self._set(i, t)
         n = ctypes.c_size_t(0)
@@ -862,8 +870,8 @@ def adamw_step(plan: AdamwPlan, step, lr, *, beta1=0.9, beta2=0.95, eps=1e-8, ma
     _need(lr, "lr", torch.float32, dev, (1,))
     norm = _empty((1,), torch.float32, dev, out, "norm") if max_norm > 0 else None
     _check("lrs_adamw_step",
-           _load().lrs_adamw_step(ctypes.cast(plan._list, _P), len(plan.tensors), _ptr(step), _ptr(lr), beta1, beta2,
-                                  eps, max_norm, _ptr(norm), _ptr(plan.scratch), _stream(dev)))
+           _load().lrs_adamw_step(plan._at, len(plan.tensors), step.data_ptr(), lr.data_ptr(), beta1, beta2, eps,
+                                  max_norm, _ptr(norm), plan.scratch.data_ptr(), _stream(dev)))
     return {"norm": norm, "step": step}
 
 

@@ -1172,9 +1172,9 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
     int parts = 2 * ce_n_tiles(V);
     if (ce_is_few(T, D)) {
         parts = ce_few_parts(T, block_gemm_sms());
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_few(g, h, w, stream));
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_few(g, h, w, stream, pdl_ok()));
     } else {
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, false));
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, pdl_ok()));
     }
     LRS_LAUNCH(KID_CE_ROWS, stream,
                launch_ce_rows(g.stats, g.zt, target, parts, T, V, loss, lse, at<double>(scratch, l.sums), total,
@@ -1219,7 +1219,7 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
         g.status = status;
         g.clear = i == 0;
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, dz, dz2, l.ldz, stream, i > 0 && pdl_ok()));
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, dz, dz2, l.ldz, stream, pdl_ok()));
         // dh (+)= dz w; dw's rows of this piece = dz^T h
         CeGemmArgs d = {};
         d.status = status;
@@ -1316,7 +1316,7 @@ int gated_norm_forward(const void* x, const void* y, const void* gate, const flo
     a.r = static_cast<uint4*>(r);
     a.h = static_cast<uint4*>(h);
     a.rstd = static_cast<float2*>(saved);
-    LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_fwd(a, stream));
+    LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_fwd(a, stream, pdl_ok()));
     return LRS_OK;
 }
 
@@ -1342,7 +1342,7 @@ int gated_norm_backward(const void* dr, const void* dh, const void* x, const voi
     a.dg = static_cast<uint4*>(dgate);
     a.part = static_cast<float*>(scratch);
     const int ctas = gated_norm_bwd_ctas(T, D, branch, block_gemm_sms());
-    LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_bwd(a, ctas, stream));
+    LRS_LAUNCH(KID_GATED_NORM, stream, launch_gated_norm_bwd(a, ctas, stream, pdl_ok()));
     LRS_LAUNCH(KID_GATED_NORM_SUM, stream,
                launch_gated_norm_sum(a, ctas, dgamma_pre, dgamma_post, dscale, stream, pdl_ok()));
     return LRS_OK;
@@ -1410,7 +1410,7 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
         a.advance = i == 0;
         if (i > 0 && max_norm == 0.f) break;   // only the step's count and bias corrections, once
         a.partial0 = a.partials;
-        LRS_LAUNCH(KID_ADAMW_NORM, stream, launch_adamw_norm(tensors + i, k, a, &ctas, stream, i > 0 && pdl_ok()));
+        LRS_LAUNCH(KID_ADAMW_NORM, stream, launch_adamw_norm(tensors + i, k, a, &ctas, stream, pdl_ok()));
         a.partials += ctas;
     }
     for (int i = 0; i < count; i += kAdamCap) {

@@ -799,11 +799,11 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
 // TIME_FEW us, 29 us by the tensor-core tiles; from 6 on those are faster (30 against 34 us).
 bool ce_is_few(int T, int D) { return T <= 4 && (long long)T * D * 2 <= 48 * 1024; }
 int ce_few_parts(int T, int sms) { return kCeFewThreads / 256 / (T == 1 ? 1 : 2) * sms; }
-cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s) {
+cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl) {
     const int T = a.c[0].M, D = a.c[0].K;
     auto* fn = T == 1 ? ce_few_kernel<1, 8> : T == 2 ? ce_few_kernel<2, 8> : ce_few_kernel<4, 4>;
     const size_t smem = (size_t)T * D * 2;
-    return launch_ex(fn, dim3((unsigned)ce_few_parts(T, block_gemm_sms())), dim3(256), smem, s, false,
+    return launch_ex(fn, dim3((unsigned)ce_few_parts(T, block_gemm_sms())), dim3(256), smem, s, pdl,
                      static_cast<const uint4*>(h), static_cast<const uint4*>(w), T, a);
 }
 

@@ -473,41 +473,41 @@ int gn_stages(size_t group_bytes, int ctas_per_sm) {
 }
 
 template <bool Y, bool G, int VEC>
-cudaError_t gn_fwd_as(GatedNormArgs a, const GnShape& sh, cudaStream_t s) {
+cudaError_t gn_fwd_as(GatedNormArgs a, const GnShape& sh, cudaStream_t s, bool pdl) {
     const long long groups = (a.T + sh.block.y - 1) / sh.block.y;
-    const int per_sm = gn_ctas_per_sm(sh, VEC == 1 ? 1024 : 512);
+    const int per_sm = gn_ctas_per_sm(sh, VEC == 2 ? 512 : Y ? 1024 : 1536);
     const long long resident = (long long)per_sm * block_gemm_sms();
     // one group of rows a CTA needs no ring
     if (groups <= resident)
-        return launch_ex(gated_norm_fwd_kernel<Y, G, VEC, false>, dim3((unsigned)groups), sh.block, 0, s, false, a);
+        return launch_ex(gated_norm_fwd_kernel<Y, G, VEC, false>, dim3((unsigned)groups), sh.block, 0, s, pdl, a);
     const size_t group = (size_t)(1 + Y + G) * sh.block.y * a.D * 2;
     a.stages = gn_stages(group, per_sm);
     auto* fn = gated_norm_fwd_kernel<Y, G, VEC, true>;
     const size_t smem = group * a.stages;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(fn, dim3((unsigned)resident), sh.block, smem, s, false, a);
+    return launch_ex(fn, dim3((unsigned)resident), sh.block, smem, s, pdl, a);
 }
 template <bool Y, bool G>
-cudaError_t gn_fwd(const GatedNormArgs& a, cudaStream_t s) {
+cudaError_t gn_fwd(const GatedNormArgs& a, cudaStream_t s, bool pdl) {
     const GnShape sh = gn_shape(a.D);
-    return sh.vec == 1 ? gn_fwd_as<Y, G, 1>(a, sh, s) : gn_fwd_as<Y, G, 2>(a, sh, s);
+    return sh.vec == 1 ? gn_fwd_as<Y, G, 1>(a, sh, s, pdl) : gn_fwd_as<Y, G, 2>(a, sh, s, pdl);
 }
 
 template <bool Y, bool G, int VEC>
-cudaError_t gn_bwd_as(GatedNormBwdArgs a, const GnShape& sh, int ctas, cudaStream_t s) {
+cudaError_t gn_bwd_as(GatedNormBwdArgs a, const GnShape& sh, int ctas, cudaStream_t s, bool pdl) {
     const size_t group = (size_t)(3 + Y + G) * sh.block.y * a.f.D * 2;
     a.f.stages = gn_stages(group, gn_ctas_per_sm(sh, Y ? 512 : 1024));
     const size_t smem = std::max(group * a.f.stages, (size_t)(Y ? 2 : 1) * sh.block.y * a.f.D * sizeof(float));
     auto* fn = gated_norm_bwd_kernel<Y, G, VEC>;
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(fn, dim3((unsigned)ctas), sh.block, smem, s, false, a);
+    return launch_ex(fn, dim3((unsigned)ctas), sh.block, smem, s, pdl, a);
 }
 template <bool Y, bool G>
-cudaError_t gn_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s) {
+cudaError_t gn_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s, bool pdl) {
     const GnShape sh = gn_shape(a.f.D);
-    return sh.vec == 1 ? gn_bwd_as<Y, G, 1>(a, sh, ctas, s) : gn_bwd_as<Y, G, 2>(a, sh, ctas, s);
+    return sh.vec == 1 ? gn_bwd_as<Y, G, 1>(a, sh, ctas, s, pdl) : gn_bwd_as<Y, G, 2>(a, sh, ctas, s, pdl);
 }
 
 }  // namespace
@@ -518,13 +518,13 @@ int gated_norm_bwd_ctas(long long T, int D, bool branch, int sms) {
                                                   (long long)gn_ctas_per_sm(sh, branch ? 512 : 1024) * sms));
 }
 
-cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s) {
-    if (a.y == nullptr) return gn_fwd<false, false>(a, s);
-    return a.g == nullptr ? gn_fwd<true, false>(a, s) : gn_fwd<true, true>(a, s);
+cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s, bool pdl) {
+    if (a.y == nullptr) return gn_fwd<false, false>(a, s, pdl);
+    return a.g == nullptr ? gn_fwd<true, false>(a, s, pdl) : gn_fwd<true, true>(a, s, pdl);
 }
-cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s) {
-    if (a.f.y == nullptr) return gn_bwd<false, false>(a, ctas, s);
-    return a.f.g == nullptr ? gn_bwd<true, false>(a, ctas, s) : gn_bwd<true, true>(a, ctas, s);
+cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s, bool pdl) {
+    if (a.f.y == nullptr) return gn_bwd<false, false>(a, ctas, s, pdl);
+    return a.f.g == nullptr ? gn_bwd<true, false>(a, ctas, s, pdl) : gn_bwd<true, true>(a, ctas, s, pdl);
 }
 cudaError_t launch_gated_norm_sum(const GatedNormBwdArgs& a, int parts, float* dgamma_pre, float* dgamma_post,
                                   float* dscale, cudaStream_t s, bool pdl) {

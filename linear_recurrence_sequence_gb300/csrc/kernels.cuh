@@ -570,7 +570,7 @@ cudaError_t launch_ce_logits(const CeGemmArgs& a, const void* h, const void* w, 
                              long long ldz, cudaStream_t s, bool pdl);
 bool ce_is_few(int T, int D);
 int ce_few_parts(int T, int sms);
-cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s);
+cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl);
 cudaError_t launch_ce_grads(const CeGemmArgs& a, const void* dz, const void* dz2, long long ldz, const void* h,
                             const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl);
 int ce_row_ctas(int T);
@@ -610,8 +610,8 @@ struct GatedNormBwdArgs {
 int gated_norm_bwd_ctas(long long T, int D, bool branch, int sms);
 cudaError_t launch_gated_norm_sum(const GatedNormBwdArgs& a, int parts, float* dgamma_pre, float* dgamma_post,
                                   float* dscale, cudaStream_t s, bool pdl);
-cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s);
-cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s);
+cudaError_t launch_gated_norm_fwd(const GatedNormArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_gated_norm_bwd(const GatedNormBwdArgs& a, int ctas, cudaStream_t s, bool pdl);
 
 // ---------------------------------------------------------------------------
 // AdamW over many tensors (adamw.cu).

@@ -863,12 +863,12 @@ def adamw_step(plan: AdamwPlan, step, lr, *, beta1=0.9, beta2=0.95, eps=1e-8, ma
     """One AdamW step over the plan's tensors, in place, through ``lrs_adamw_step``.
 
     step: int32 [1], the number of steps taken (advanced); lr: FP32 [1]; max_norm > 0 clips the gradients' norm over
-    all tensors, and a step whose norm is not finite changes nothing.  Returns dict(norm (FP32 [1], None without
+    all tensors, and a step whose norm is not finite changes nothing.  Returns dict(norm (FP32 scalar, None without
     clipping), step)."""
     dev = plan.device
     _need(step, "step", torch.int32, dev, (1,))
     _need(lr, "lr", torch.float32, dev, (1,))
-    norm = _empty((1,), torch.float32, dev, out, "norm") if max_norm > 0 else None
+    norm = _empty((), torch.float32, dev, out, "norm") if max_norm > 0 else None
     _check("lrs_adamw_step",
            _load().lrs_adamw_step(plan._at, len(plan.tensors), step.data_ptr(), lr.data_ptr(), beta1, beta2, eps,
                                   max_norm, _ptr(norm), plan.scratch.data_ptr(), _stream(dev)))

@@ -1110,7 +1110,7 @@ struct CeBackward {
     long long ldz;       // row stride of dz: a multiple of 64
     int pieces;
     int h_splits, w_splits;   // of the sums over the piece and over the tokens
-    size_t dz, dz2, dh, dw, total;
+    size_t h, dz, dz2, dh, dw, total;
 };
 constexpr long long kCePieceBytes = 512LL << 20;
 
@@ -1126,7 +1126,8 @@ CeBackward ce_backward_layout(int T, int V, int D, int fp32, int sms) {
     ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &l.h_splits, &l.w_splits);
     const int sh = l.h_splits, sw = l.w_splits;
     const size_t dz = up256((size_t)T * (size_t)l.ldz * 2);
-    l.dz = 256;
+    l.h = 256;
+    l.dz = l.h + up256((size_t)T * D * 2);
     l.dz2 = l.dz + dz;
     l.dh = l.dz2 + (fp32 ? dz : 0);
     l.dw = l.dh + ((sh > 1 || (l.pieces > 1 && !fp32)) ? up256((size_t)sh * T * D * 4) : 0);
@@ -1202,6 +1203,13 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &h_splits, &w_splits);
     // dh adds over the pieces (and the splits of a piece) in FP32
     const bool h_part = h_splits > 1 || (l.pieces > 1 && !fp32);
+    // the tokens' weights: in dz (FP32 gradients); their ratios to the largest,
+    // which is put on both results; or one for all (the mean), on both results
+    const float* dz_weight = fp32 ? dloss : nullptr;
+    const float* ratios = fp32 ? nullptr : dloss;
+    const float* count = dloss == nullptr ? total : nullptr;
+    void* hw = at<void>(scratch, l.h);
+    LRS_LAUNCH(KID_CE_ROWS, stream, launch_ce_rows_of_h(h, target, T, V, D, hw, status, stream, pdl_ok()));
     for (int i = 0; i < l.pieces; ++i) {
         const int v0 = i * l.piece, nv = std::min(l.piece, V - v0);
         CeGemmArgs g = {};
@@ -1212,17 +1220,22 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         g.c[0].s_cols = (int)l.ldz;
         g.target = target;
         g.V = V;
-        g.dloss = dloss;
-        g.total = total;
+        g.T = T;
+        g.dloss = dz_weight;
+        g.weights = ratios;
         g.lse = lse;
         g.softcap = softcap;
         g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
         g.status = status;
-        g.clear = i == 0;
         LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, dz, dz2, l.ldz, stream, pdl_ok()));
         // dh (+)= dz w; dw's rows of this piece = dz^T h
         CeGemmArgs d = {};
         d.status = status;
+        d.target = target;
+        d.T = T;
+        d.V = V;
+        d.weights = ratios;
+        d.total = count;
         CeSide& ch = d.c[0];
         ch.M = T;
         ch.N = D;
@@ -1241,7 +1254,7 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         cw.splits = w_splits;
         const size_t at0 = (size_t)v0 * D;
         cw.part = w_splits > 1 ? at<float>(scratch, l.dw) : fp32 ? static_cast<float*>(dw) + at0 : nullptr;
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_grads(d, dz, dz2, l.ldz, h, w, V, dh, dw, stream, pdl_ok()));
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_grads(d, dz, dz2, l.ldz, hw, w, V, dh, dw, stream, pdl_ok()));
         if (w_splits > 1)
             LRS_LAUNCH(KID_CE_ROWS, stream,
                        launch_ce_sum(cw.part, (long long)nv * D, w_splits, (long long)nv * D,
@@ -1403,7 +1416,7 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
     a.step = step;
     a.norm = norm;
     a.bias = at<float>(scratch, 0);
-    a.partial = at<float>(scratch, 256);
+    a.partial = at<double>(scratch, 256);
     for (int i = 0; i < count; i += kAdamCap) {
         const int k = std::min(kAdamCap, count - i);
         int ctas = 0;

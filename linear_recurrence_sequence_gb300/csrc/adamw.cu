@@ -36,7 +36,7 @@ constexpr int kAdamThreads = 256;
 constexpr int kAdamBlock = 256;                             // values a scale stands for, values of a warp
 constexpr int kAdamChunk = kAdamBlock * kAdamThreads / 32;  // values of a CTA at a time
 constexpr int kAdamNormCtas = 8;                            // CTAs per SM of the norm
-constexpr float kFp8Max = 448.f;
+constexpr float kFp8Max = 448.f, kFp8Inv = 1.f / 448.f;
 constexpr float kFp8Tiny = 0.001953125f;                    // 2^-9, the smallest E4M3 value above 0
 constexpr float kAdamSmall = 7.888609052210118e-31f;        // 2^-100
 
@@ -138,13 +138,14 @@ __device__ __forceinline__ void store_codes(uint8_t* p, long long i, long long n
 }
 
 // Sum over the CTA in a fixed order; the result in every thread.
-__device__ __forceinline__ float cta_sum(float v, float* red) {
+__device__ __forceinline__ double cta_sum(double v, double* red) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = 0.f;
+    v = 0.;
+#pragma unroll
     for (int w = 0; w < kAdamThreads / 32; ++w) v += red[w];
     return v;
 }
@@ -164,7 +165,7 @@ __device__ double adam_pow(double b, int t) {
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamList<CAP> l,
                                                                   const AdamArgs a) {
-    __shared__ float red[kAdamThreads / 32];
+    __shared__ double red[kAdamThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     pdl_wait();
@@ -175,7 +176,11 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
         a.bias[1] = (float)(1.0 / (1.0 - adam_pow(a.beta2, t)));
     }
     if (a.max_norm <= 0.f) return;
-    float s = 0.f;
+    // Eight squares at a time in FP32 (their roundings are independent and cancel
+    // over the groups), the running sum in two floats (hi + lo, the sum's own
+    // rounding kept by the exact difference): a sum right to its last FP32 bit,
+    // without FP64 arithmetic on every value.
+    float hi = 0.f, lo = 0.f;
     for (int c = (int)blockIdx.x; c < l.first[l.count]; c += (int)gridDim.x) {
         const int i = adam_find(l, c);
         const long long n = l.t[i].n, at = (long long)(c - l.first[i]) * kAdamChunk + warp * kAdamBlock + 4 * lane;
@@ -199,12 +204,17 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
                     load_f32<false>(static_cast<const float*>(gp), at + 128 * k, n, g[k]);
             }
         }
+        float q = 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s = fmaf(g[k][j], g[k][j], s);
+            for (int j = 0; j < 4; ++j) q = fmaf(g[k][j], g[k][j], q);
+        const float t = __fadd_rn(hi, q), b = __fsub_rn(t, hi);
+        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(q, b)));
+        hi = t;
     }
-    s = cta_sum(s, red);
+    // a sum that overflowed has no difference to add
+    const double s = cta_sum(isfinite(hi) ? (double)hi + (double)lo : (double)hi, red);
     if (threadIdx.x == 0) a.partial[a.partial0 + blockIdx.x] = s;
 }
 
@@ -259,9 +269,10 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, long long b0, in
             // each product rounded by itself, as written above
             m[k][j] = __fadd_rn(__fmul_rn(m[k][j], a.b1), __fmul_rn(gg, a.c1));
             v[k][j] = __fadd_rn(__fmul_rn(vv, a.b2), __fmul_rn(__fmul_rn(gg, gg), a.c2));
-            // one root serves the step and the state; it and the quotient come
-            // from the SFU, within 2^-22 (the step is a small part of p)
-            root[k][j] = sqrt_approx(v[k][j]);
+            // one root serves the step and the state: correctly rounded where it
+            // is stored (a code next to a tie follows its last bit), from the SFU
+            // like the quotient otherwise, within 2^-22 (the step is a small part of p)
+            root[k][j] = Q8 ? __fsqrt_rn(v[k][j]) : sqrt_approx(v[k][j]);
             const float step = __fdividef(m[k][j] * a.ibc1, fmaf(root[k][j], a.root_ibc2, a.eps));
             p[k][j] = fmaf(-a.lr, step, p[k][j] * keep);
             if (Q8) {
@@ -273,7 +284,9 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, long long b0, in
     if (Q8) {
         const float mt = __uint_as_float(__reduce_max_sync(0xffffffffu, mtop));
         const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, vtop));
-        const float mi = mt >= kAdamSmall ? kFp8Max / mt : 0.f, vi = vt >= kAdamSmall ? kFp8Max / vt : 0.f;
+        // one reciprocal a block and products with constants
+        const float mi = mt >= kAdamSmall ? __frcp_rn(mt) * kFp8Max : 0.f;
+        const float vi = vt >= kAdamSmall ? __frcp_rn(vt) * kFp8Max : 0.f;
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -283,8 +296,8 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, long long b0, in
                 v[k][j] = r > 0.f ? fmaxf(r, kFp8Tiny) : r;
             }
         if (lane == 0) {
-            t.m_scale[b0 / kAdamBlock] = mt >= kAdamSmall ? mt / kFp8Max : 0.f;
-            t.v_scale[b0 / kAdamBlock] = vt >= kAdamSmall ? vt / kFp8Max : 0.f;
+            t.m_scale[b0 / kAdamBlock] = mt >= kAdamSmall ? mt * kFp8Inv : 0.f;
+            t.v_scale[b0 / kAdamBlock] = vt >= kAdamSmall ? vt * kFp8Inv : 0.f;
         }
     }
 #pragma unroll
@@ -312,16 +325,16 @@ __device__ __forceinline__ void adam_block_any(const AdamTensor& t, long long b0
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads, 4) adamw_update_kernel(const __grid_constant__ AdamList<CAP> l,
                                                                        const AdamArgs a) {
-    __shared__ float red[kAdamThreads / 32];
+    __shared__ double red[kAdamThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     pdl_wait();
     AdamScalars sc;
     sc.clip = 1.f;
     if (a.max_norm > 0.f) {
-        float s = 0.f;
+        double s = 0.;
         for (int i = threadIdx.x; i < a.partials; i += kAdamThreads) s += __ldcg(a.partial + i);
-        const float norm = sqrtf(cta_sum(s, red));
+        const float norm = sqrtf((float)cta_sum(s, red));
         const bool skip = !(norm <= 3.4028234e38f);
         if (blockIdx.x == 0 && threadIdx.x == 0 && a.advance) {
             *a.norm = norm;
@@ -393,7 +406,7 @@ long long adam_chunks(long long n) { return (n + kAdamChunk - 1) / kAdamChunk; }
 
 size_t adam_scratch_bytes(int count) {
     const size_t launches = (size_t)(count + kAdamCap - 1) / kAdamCap;
-    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(float) + 255) / 256 * 256;
+    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(double) + 255) / 256 * 256;
 }
 
 cudaError_t launch_adamw_norm(const AdamTensor* ts, int count, const AdamArgs& a, int* ctas, cudaStream_t s, bool pdl) {

@@ -54,12 +54,19 @@ constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store
 constexpr uint32_t kCeWideBox = 2 * kCeBox;   // [32][64] (128-byte swizzle)
 // Staging of the BF16 stores, one box per epilogue warp of [32 rows][64
 // columns]; with remainders two of [32][32], one for them.
-__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) { return epi != kCeStats ? kCeWideBox : 0u; }
+__host__ __device__ constexpr uint32_t ce_stage_warp(int epi) {
+    return epi == kCeDz || epi == kCeDz2 || epi == kCeGrads ? kCeWideBox : 0u;
+}
 constexpr size_t ce_smem(int epi) {
     return (size_t)kCeStages * kCeStageBytes + (size_t)kCeEpiWarps * ce_stage_warp(epi) + 1024;
 }
 
 constexpr int kCeFewThreads = 1024;   // per SM, of the kernel for one token (half of it for more)
+// Stages that one accumulator adds up where the results are FP32: the tensor
+// cores' sums lose about 2e-8 of their value a step of 16 (they truncate), 6e-5
+// over 50021 vocabulary entries in two parts; 16 stages are 128 steps.
+constexpr int kCeChain = 16;
+
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ uint4 pack8(const float* v) {
@@ -120,6 +127,13 @@ __device__ __forceinline__ bool ce_item(const CeGemmArgs& a, bool grads, int pai
     return true;
 }
 
+// 32 columns of this lane's accumulator row; the warp's lanes meet first (the
+// load is one instruction of the whole warp).
+__device__ __forceinline__ void ce_columns(uint32_t taddr, float (&v)[2][16]) {
+    __syncwarp();
+    tmem_ld16x2(taddr, taddr + 16u, v[0], v[1]);
+}
+
 // The capped logit and its slope: z' = c tanh(z / c), dz'/dz = 1 - (z'/c)^2.
 __device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a.softcap * tanhf(z * a.inv_softcap); }
 
@@ -138,7 +152,7 @@ __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& 
     float mx = -INFINITY, sum = 0.f;
     for (int c = 0; c < kCeN / 2; c += 32) {
         float v[2][16];
-        tmem_ld16x2(taddr + (uint32_t)(c0 + c), taddr + (uint32_t)(c0 + c + 16), v[0], v[1]);
+        ce_columns(taddr + (uint32_t)(c0 + c), v);
         if (!ok || c >= nv) continue;
         float z[32];
 #pragma unroll
@@ -168,6 +182,24 @@ __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& 
     if (ok) a.stats[(size_t)(2 * it.nt + half) * M + t] = make_float2(mx, sum);
 }
 
+// The largest |dloss| of the tokens counted: dz is rounded to BF16 relative to
+// it, so that equal weights, whatever they are, are not rounded at all (one
+// rounding for all tokens would be an error of the whole gradient).  Every CTA's
+// epilogue warps find it for themselves, under the first tile's products.
+__device__ __forceinline__ float ce_largest_weight(const CeGemmArgs& a, uint32_t* s_weight) {
+    uint32_t m = 0u;
+    for (int t = threadIdx.x; t < a.T; t += 32 * kCeEpiWarps) {
+        const long long tg = __ldg(reinterpret_cast<const long long*>(a.target) + t);
+        if (tg >= 0 && tg < a.V) m = max(m, __float_as_uint(fabsf(__ldg(a.weights + t))));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(s_weight, m);
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kCeEpiWarps) : "memory");
+    return __uint_as_float(*reinterpret_cast<volatile uint32_t*>(s_weight));
+}
+// w / largest, exactly 1 where they are equal.
+__device__ __forceinline__ float ce_ratio(float w, float largest) { return w != 0.f ? __fdiv_rn(w, largest) : 0.f; }
+
 // Tensor maps of both contractions: A, A's remainders, B, the BF16 result (s2: dz's remainders).
 struct CeMaps {
     CUtensorMap a[2], a2[2], b[2], s[2], s2;
@@ -176,12 +208,12 @@ struct CeMaps {
 template <int EPI, bool CAP>
 __global__ void __launch_bounds__(kCeThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeMaps tm, const __grid_constant__ CeGemmArgs a) {
-    constexpr bool GRADS = EPI == kCeGrads;
+    constexpr bool GRADS = EPI == kCeGrads || EPI == kCeGrads2, CHAINS = EPI == kCeGrads2;
     constexpr int S = kCeStages;
     extern __shared__ uint8_t ce_raw[];
     // s_full and s_free are used in the even CTA, the others in both
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_acc[2], s_free[2], s_fin;
-    __shared__ uint32_t s_tmem;
+    __shared__ uint32_t s_tmem, s_weight;
     __shared__ int s_abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_ctarank();
@@ -197,6 +229,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         }
         mbar_init(&s_fin, 1);
         s_abort = 0;
+        s_weight = 0u;
     }
     if (warp == kCeIssuer) {
         tmem_alloc2(&s_tmem, kCeTmemCols);
@@ -273,41 +306,49 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         }
     } else if (warp == kCeIssuer) {
         if (lane == 0 && rank == 0) {
-            uint32_t n = 0, item = 0;
-            for (; !*abort_flag && ce_item(a, GRADS, pair, pairs, (int)item, rank, it); ++item) {
+            uint32_t n = 0, use = 0;   // stages consumed, accumulators filled
+            bool ok = true;
+            for (int k = 0; ok && !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k) {
                 const bool tn = GRADS && it.side == 1;   // A MN-major too
                 const uint32_t idesc = umma_idesc_bf16(kCeM, kCeN) | (tn ? (1u << 15) : 0u) | (GRADS ? (1u << 16) : 0u);
-                const uint32_t buf = item & 1u;
-                // both CTAs' epilogues have drained this accumulator's previous tile
-                if (item >= 2 && !mbar_wait_cluster(&s_free[buf], ((item >> 1) - 1) & 1u)) {
-                    fail();
-                    break;
-                }
-                tmem_fence_after_sync();
-                const uint32_t acc_t = tmem + buf * (uint32_t)kCeN;
-                bool ok = true;
-                for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
-                    const int slot = (int)(n % S);
-                    if (!mbar_wait_bounded(&s_full[slot], (n / S) & 1u)) {
+                for (int k0 = it.k0; ok && k0 < it.k1; k0 += kCeChain, ++use) {
+                    const int k1 = CHAINS ? min(k0 + kCeChain, it.k1) : it.k1;
+                    const uint32_t buf = use & 1u;
+                    // both CTAs' epilogues have drained this accumulator's previous contents
+                    if (use >= 2 && !mbar_wait_cluster(&s_free[buf], ((use >> 1) - 1) & 1u)) {
                         fail();
                         ok = false;
                         break;
                     }
                     tmem_fence_after_sync();
-                    const uint32_t sa = smem_u32(ring + (size_t)slot * kCeStageBytes);
-                    const uint32_t sb = sa + kCeABytes;
+                    const uint32_t acc_t = tmem + buf * (uint32_t)kCeN;
+                    for (int ks = k0; ks < k1; ++ks, ++n) {
+                        const int slot = (int)(n % S);
+                        if (!mbar_wait_bounded(&s_full[slot], (n / S) & 1u)) {
+                            fail();
+                            ok = false;
+                            break;
+                        }
+                        tmem_fence_after_sync();
+                        const uint32_t sa = smem_u32(ring + (size_t)slot * kCeStageBytes);
+                        const uint32_t sb = sa + kCeABytes;
 #pragma unroll
-                    for (int kk = 0; kk < kCeK / 16; ++kk) {
-                        // K-major: chunk kk / 4, 32 bytes a step; MN-major: 16 rows a step in both chunks
-                        const uint32_t kmaj = kCeChunk * (kk / 4) + 32u * (kk % 4), mn = 2048u * kk;
-                        const uint64_t da = tn ? umma_desc_sw128_mn(sa + mn, kCeChunk) : umma_desc_sw128(sa + kmaj);
-                        const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + mn, kCeChunk) : umma_desc_sw128(sb + kmaj);
-                        umma2_bf16(acc_t, da, db, idesc, ks > it.k0 || kk > 0);
+                        for (int kk = 0; kk < kCeK / 16; ++kk) {
+                            // K-major: chunk kk / 4, 32 bytes a step; MN-major: 16 rows a step in both chunks
+                            const uint32_t kmaj = kCeChunk * (kk / 4) + 32u * (kk % 4), mn = 2048u * kk;
+                            const uint64_t da = tn ? umma_desc_sw128_mn(sa + mn, kCeChunk) : umma_desc_sw128(sa + kmaj);
+                            const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + mn, kCeChunk) : umma_desc_sw128(sb + kmaj);
+                            umma2_bf16(acc_t, da, db, idesc, ks > k0 || kk > 0);
+                        }
+                        umma2_commit(&s_empty[slot]);
                     }
-                    umma2_commit(&s_empty[slot]);
+                    if (!ok) break;
+                    umma2_commit(&s_acc[buf]);
+                    if (!CHAINS) {
+                        ++use;
+                        break;
+                    }
                 }
-                if (!ok) break;
-                umma2_commit(&s_acc[buf]);
             }
             // every MMA issued by this thread has completed before the columns are released
             umma2_commit_own(&s_fin);
@@ -318,10 +359,61 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const int q4 = warp & 3, hf = warp >> 2;
         const int row = 32 * q4 + lane;
         uint8_t* stg = ring + (size_t)S * kCeStageBytes + (size_t)warp * ce_stage_warp(EPI);
-        uint32_t item = 0;
-        for (; !*abort_flag && ce_item(a, GRADS, pair, pairs, (int)item, rank, it); ++item) {
+        uint32_t use = 0;   // accumulators drained
+        // the common factor of the tokens' weights: left out of dz, put on its products
+        float common = 1.f;
+        if (EPI != kCeStats && a.weights != nullptr) common = ce_largest_weight(a, &s_weight);
+        if (GRADS && a.total != nullptr && a.total[1] > 0.f) common = 1.f / a.total[1];
+        for (int k = 0; !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k, ++use) {
             const CeSide& c0 = a.c[it.side];
-            const uint32_t buf = item & 1u;
+            const uint32_t buf = use & 1u;
+            if (CHAINS) {
+                // each accumulator holds at most kCeChain stages; they add up in registers
+                float sum[kCeN / 2];
+#pragma unroll
+                for (int j = 0; j < kCeN / 2; ++j) sum[j] = 0.f;
+                bool lost = false;
+                for (int k0 = it.k0; k0 < it.k1; k0 += kCeChain, ++use) {
+                    const uint32_t b = use & 1u;
+                    if (!mbar_wait_bounded(&s_acc[b], (use >> 1) & 1u)) {
+                        lost = true;
+                        break;
+                    }
+                    tmem_fence_after_sync();
+                    const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + b * (uint32_t)kCeN + hf * (kCeN / 2);
+#pragma unroll
+                    for (int c = 0; c < kCeN / 2; c += 32) {
+                        float v[2][16];
+                        ce_columns(taddr + (uint32_t)c, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c + j] += v[j / 16][j % 16];
+                    }
+                    tmem_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(cluster_map(&s_free[b], 0));
+                }
+                if (lost) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                --use;   // the loop over the items counts the last one
+                const long long r = (long long)it.m0 + row;
+                const int n0 = it.nt * kCeN + hf * (kCeN / 2);
+                float* o = c0.part + ((size_t)it.s * c0.M + (size_t)r) * c0.N + n0;
+                if (r >= c0.M) continue;
+#pragma unroll
+                for (int j = 0; j < kCeN / 2; j += 4) {
+                    if (n0 + j >= c0.N) break;
+                    float4 x = make_float4(sum[j] * common, sum[j + 1] * common, sum[j + 2] * common, sum[j + 3] * common);
+                    float4* p = reinterpret_cast<float4*>(o + j);
+                    if (c0.accumulate) {
+                        const float4 y = *p;
+                        x = make_float4(y.x + x.x, y.y + x.y, y.z + x.z, y.w + x.w);
+                    }
+                    *p = x;
+                }
+                continue;
+            }
             // what a row needs besides its logits is fetched while the tile is computed
             float wgt = 0.f, lse2 = 0.f;
             long long tgt = -1;
@@ -331,11 +423,12 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     const long long tg = a.target[t];
                     tgt = tg - c0.b_row - (long long)it.nt * kCeN;
                     // a row without a valid target adds nothing to the gradients
-                    if (tg >= 0 && tg < a.V) wgt = a.dloss != nullptr ? a.dloss[t] : 1.f / a.total[1];
+                    if (tg >= 0 && tg < a.V)
+                        wgt = a.dloss != nullptr ? a.dloss[t] : a.weights != nullptr ? ce_ratio(a.weights[t], common) : 1.f;
                     lse2 = a.lse[t] * kLog2e;
                 }
             }
-            if (!mbar_wait_bounded(&s_acc[buf], (item >> 1) & 1u)) {
+            if (!mbar_wait_bounded(&s_acc[buf], (use >> 1) & 1u)) {
                 if (lane == 0) fail();
                 break;
             }
@@ -348,13 +441,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 float* o = c0.part + ((size_t)it.s * c0.M + (size_t)r) * c0.N + (size_t)it.nt * kCeN;
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
                     float v[2][16];
-                    tmem_ld16x2(taddr + (uint32_t)c, taddr + (uint32_t)(c + 16), v[0], v[1]);
+                    ce_columns(taddr + (uint32_t)c, v);
                     if (r >= c0.M) continue;
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
                         if (it.nt * kCeN + c + j >= c0.N) continue;
-                        float4 x = make_float4(v[j / 16][j % 16], v[j / 16][j % 16 + 1], v[j / 16][j % 16 + 2],
-                                               v[j / 16][j % 16 + 3]);
+                        const float* f = &v[j / 16][j % 16];
+                        float4 x = make_float4(f[0] * common, f[1] * common, f[2] * common, f[3] * common);
                         float4* p = reinterpret_cast<float4*>(o + c + j);
                         if (c0.accumulate) {
                             const float4 y = *p;
@@ -372,7 +465,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll 1
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
                     float v[2][16], lo[2][16];
-                    tmem_ld16x2(taddr + (uint32_t)c, taddr + (uint32_t)(c + 16), v[0], v[1]);
+                    ce_columns(taddr + (uint32_t)c, v);
                     if (EPI == kCeDz || EPI == kCeDz2) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
@@ -395,6 +488,10 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = lo[j / 16][j % 16] = 0.f;
                         }
+                    }
+                    if (GRADS) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j / 16][j % 16] *= common;
                     }
                     const bool second = (c & 32) != 0;   // of a wide box
                     if ((kBoxes == 2 || !second) && lane == 0) bulk_wait_read<0>();   // the box is read out
@@ -642,6 +739,26 @@ __global__ void __launch_bounds__(256) ce_rows_kernel(const float2* __restrict__
     }
 }
 
+// The rows of h that dw = dz^T h adds up: zeros for tokens that are not
+// counted, whatever their rows hold.  One warp a row; also the backward's first
+// kernel, which clears the status word.
+__global__ void __launch_bounds__(256) ce_rows_of_h_kernel(const uint4* __restrict__ h, const int64_t* __restrict__ target,
+                                                           int T, int V, int nv, uint4* __restrict__ out,
+                                                           uint32_t* status) {
+    pdl_trigger();
+    pdl_wait();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
+    const int lane = threadIdx.x & 31;
+    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += gridDim.x * 8) {
+        const long long tg = target[t];
+        const bool counted = tg >= 0 && tg < V;
+        for (int c = lane; c < nv; c += 32) {
+            const size_t i = (size_t)t * nv + c;
+            out[i] = counted ? __ldg(h + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
 // out[i] = sum of part[p][i] over p in order, as FP32 or BF16; n a multiple of 4.
 template <bool F32>
 __global__ void __launch_bounds__(256) ce_sum_kernel(const float4* __restrict__ part, long long stride4, int parts,
@@ -729,7 +846,7 @@ cudaError_t ce_launch(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl)
     cfg.gridDim = dim3(2u * (unsigned)pairs);
     // the pairs left with one dh item less make up for its K steps in dw items
     a.extra = 0;
-    if (EPI == kCeGrads && a.c[0].n_items % pairs != 0)
+    if ((EPI == kCeGrads || EPI == kCeGrads2) && a.c[0].n_items % pairs != 0)
         a.extra = (2 * ce_item_steps(a.c[0]) + ce_item_steps(a.c[1])) / (2 * ce_item_steps(a.c[1]));
     if (pdl) {
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -827,6 +944,7 @@ cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz
     tm.s[0] = tm.s[1] = tm.s2 = tm.a[0];
     if (a.c[0].part == nullptr && !ce_result(&tm.s[0], dh, D, T, D, true)) return cudaErrorInvalidValue;
     if (a.c[1].part == nullptr && !ce_result(&tm.s[1], dw, D, V, D, true)) return cudaErrorInvalidValue;
+    if (dz2 != nullptr) return ce_launch<kCeGrads2, false>(tm, a, s, pdl);
     return ce_launch<kCeGrads, false>(tm, a, s, pdl);
 }
 
@@ -843,6 +961,13 @@ cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* 
     auto* fn = rows == 1 ? ce_rows_kernel<1> : rows == 8 ? ce_rows_kernel<8> : ce_rows_kernel<32>;
     return launch_ex(fn, dim3((unsigned)ce_row_ctas(T)), dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse,
                      sums, total, ticket, status);
+}
+
+cudaError_t launch_ce_rows_of_h(const void* h, const int64_t* target, int T, int V, int D, void* out, uint32_t* status,
+                                cudaStream_t s, bool pdl) {
+    const int grid = std::min((T + 7) / 8, 8 * block_gemm_sms());
+    return launch_ex(ce_rows_of_h_kernel, dim3((unsigned)grid), dim3(256), 0, s, pdl, static_cast<const uint4*>(h), target,
+                     T, V, D / 8, static_cast<uint4*>(out), status);
 }
 
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,

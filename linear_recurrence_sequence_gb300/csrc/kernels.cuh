@@ -533,8 +533,9 @@ cudaError_t launch_join_fwd(const void* gv, const void* ym, void* j, long long B
 // Softmax cross entropy over a vocabulary (ce_gemm.cu).
 // ---------------------------------------------------------------------------
 // What the contraction kernel does: (max, sum of exponentials) of the logits;
-// dz in BF16; dz as BF16 leading parts and remainders; dh and dw together.
-enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz2 = 2, kCeGrads = 3 };
+// dz in BF16; dz as BF16 leading parts and remainders; dh and dw together, from
+// either (the latter in FP32).
+enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz2 = 2, kCeGrads = 3, kCeGrads2 = 4 };
 constexpr int kCeSplitsMax = 32;
 
 // One contraction, M x N over K.
@@ -551,10 +552,11 @@ struct CeGemmArgs {
     CeSide c[2];                 // the logits; or dh and dw
     float2* stats;               // kCeStats: [2 n_tiles][M]
     float* zt;                   // kCeStats: [M] the targets' logits
-    const int64_t* target;       // [M]
-    int V;
-    const float* dloss;          // kCeDz: [M], or null: 1 / total[1]
-    const float* total;
+    const int64_t* target;       // [T]
+    int T, V;
+    const float* dloss;          // dz: [T] factors of its rows, or null
+    const float* weights;        // dz, the gradients: [T] factors, the largest of which is put on the gradients, or null
+    const float* total;          // the gradients: both divided by total[1], or null
     const float* lse;            // kCeDz: [M]
     float softcap, inv_softcap;  // 0: none
     uint32_t* status;            // two words: the status, the rows' ticket
@@ -577,6 +579,8 @@ int ce_row_ctas(int T);
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
                            float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
                            cudaStream_t s, bool pdl);
+cudaError_t launch_ce_rows_of_h(const void* h, const int64_t* target, int T, int V, int D, void* out, uint32_t* status,
+                                cudaStream_t s, bool pdl);
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,
                           cudaStream_t s, bool pdl);
 
@@ -628,7 +632,7 @@ struct AdamArgs {
     int32_t* step;
     float* norm;
     float* bias;                 // [2]: 1 / (1 - beta^step)
-    float* partial;              // sums of squares, one a CTA of the first launches
+    double* partial;             // sums of squares, one a CTA of the first launches
     int partial0, partials;      // this launch's first, and all
     int advance;                 // the step's first launch of its kind
 };

@@ -171,14 +171,16 @@ def test_rows_that_do_not_count_may_hold_anything():
     grads = api.linear_ce_backward(h, w, t, clean["lse"], total=clean["total"])
     bad = h.clone()
     bad[0], bad[3], bad[147] = float("nan"), float("inf"), float("-inf")
-    # the contraction dz^T h meets 0 * nan in the bad rows: they are the caller's to keep finite there,
-    # so only the loss and dh are compared
     f = api.linear_ce_forward(bad, w, t)
     b = api.linear_ce_backward(bad, w, t, f["lse"], total=f["total"])
     live = t >= 0
     assert torch.equal(f["loss"][live], clean["loss"][live]) and not f["loss"][~live].any()
     assert torch.equal(f["total"], clean["total"])
-    assert torch.equal(b["dh"], grads["dh"])
+    assert torch.equal(b["dh"], grads["dh"]) and torch.equal(b["dw"], grads["dw"])
+    dloss = torch.full((150,), 0.01, device=DEV)
+    x = api.linear_ce_backward(h, w, t, clean["lse"], dloss)
+    y = api.linear_ce_backward(bad, w, t, f["lse"], dloss)
+    assert torch.equal(x["dh"], y["dh"]) and torch.equal(x["dw"], y["dw"])
 
 
 def test_extreme_logits():

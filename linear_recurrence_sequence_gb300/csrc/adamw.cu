@@ -4,8 +4,8 @@
 //   m = b1 m + (1 - b1) k g;  v = b2 v + (1 - b2) (k g)^2
 //   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps)
 //
-// Two launches: the norm (every gradient once; without clipping one CTA that
-// only advances the step) and the update.  The list of tensors travels in the
+// Two launches: the norm (every gradient once, and a CTA that advances the step;
+// without clipping that one alone) and the update.  The list of tensors travels in the
 // kernel's parameters (one launch for up to kAdamCap tensors), so nothing has
 // to be copied to the device when gradients move from step to step.
 //
@@ -18,10 +18,13 @@
 // A block below 2^-100 is stored as zeros.  The codes are rounded once per
 // step; the step itself uses the new moments in FP32.
 //
-// Bound by bandwidth: 30 bytes a value with 32-bit states, a BF16 parameter
-// and its FP32 master, 18 with 8-bit states.  A warp takes 256 consecutive
-// values (an 8-bit block), a lane four and four, so that every array is read
-// and written in whole 128-byte lines.
+// Bound by bandwidth: 30 bytes a value with 32-bit states, an FP32 gradient, a
+// BF16 parameter and its FP32 master (562M values: the update 2.44 ms, 6.9 TB/s;
+// the norm's pass over the gradients 0.34 ms, 6.6 TB/s), 16 with 8-bit states and
+// BF16 gradients (317M values: 0.88 ms, 5.7 TB/s, as much held by the
+// conversions and roots as by memory; the norm 0.12 ms).  A warp takes 256
+// consecutive values (an 8-bit block), a lane four and four, so that every array
+// is read and written in whole 128-byte lines, and issues every load first.
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -160,61 +163,99 @@ __device__ double adam_pow(double b, int t) {
     return r;
 }
 
-// First launch of a step: sums of squares of the gradients (one partial sum a
-// CTA), and in the first CTA the step's count and bias corrections.
-template <int CAP>
-__global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamList<CAP> l,
-                                                                  const AdamArgs a) {
-    __shared__ double red[kAdamThreads / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    pdl_trigger();
-    pdl_wait();
-    if (a.advance && blockIdx.x == 0 && threadIdx.x == 0) {
-        const int t = *a.step + 1;
-        *a.step = t;
-        a.bias[0] = (float)(1.0 / (1.0 - adam_pow(a.beta1, t)));
-        a.bias[1] = (float)(1.0 / (1.0 - adam_pow(a.beta2, t)));
+// Squares of eight BF16 or four FP32 values, added to q.
+__device__ __forceinline__ void squares(const uint4 v, bool bf16, float& q) {
+    if (bf16) {
+        const float2 a = bf2_to_f2(v.x), b = bf2_to_f2(v.y), c = bf2_to_f2(v.z), d = bf2_to_f2(v.w);
+        q = fmaf(a.x, a.x, q); q = fmaf(a.y, a.y, q);
+        q = fmaf(b.x, b.x, q); q = fmaf(b.y, b.y, q);
+        q = fmaf(c.x, c.x, q); q = fmaf(c.y, c.y, q);
+        q = fmaf(d.x, d.x, q); q = fmaf(d.y, d.y, q);
+    } else {
+        const float a = __uint_as_float(v.x), b = __uint_as_float(v.y), c = __uint_as_float(v.z), d = __uint_as_float(v.w);
+        q = fmaf(a, a, q); q = fmaf(b, b, q);
+        q = fmaf(c, c, q); q = fmaf(d, d, q);
     }
-    if (a.max_norm <= 0.f) return;
-    // Eight squares at a time in FP32 (their roundings are independent and cancel
-    // over the groups), the running sum in two floats (hi + lo, the sum's own
-    // rounding kept by the exact difference): a sum right to its last FP32 bit,
-    // without FP64 arithmetic on every value.
+}
+// A running sum in two floats: the rounding of hi is kept in lo by the exact
+// difference (two-sum), so the sum is right to its last FP32 bit without FP64
+// arithmetic on every value.
+struct TwoSum {
     float hi = 0.f, lo = 0.f;
-    for (int c = (int)blockIdx.x; c < l.first[l.count]; c += (int)gridDim.x) {
-        const int i = adam_find(l, c);
-        const long long n = l.t[i].n, at = (long long)(c - l.first[i]) * kAdamChunk + warp * kAdamBlock + 4 * lane;
-        const bool bf = l.t[i].grad_dtype == LRS_GRAD_BF16;
-        const void* gp = l.t[i].grad;
-        float g[2][4];
-        if ((long long)(c - l.first[i] + 1) * kAdamChunk <= n) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (bf)
-                    load_bf16<true>(static_cast<const uint16_t*>(gp), at + 128 * k, n, g[k]);
-                else
-                    load_f32<true>(static_cast<const float*>(gp), at + 128 * k, n, g[k]);
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if (bf)
-                    load_bf16<false>(static_cast<const uint16_t*>(gp), at + 128 * k, n, g[k]);
-                else
-                    load_f32<false>(static_cast<const float*>(gp), at + 128 * k, n, g[k]);
-            }
-        }
-        float q = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) q = fmaf(g[k][j], g[k][j], q);
+    __device__ __forceinline__ void add(float q) {
         const float t = __fadd_rn(hi, q), b = __fsub_rn(t, hi);
         lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(q, b)));
         hi = t;
     }
     // a sum that overflowed has no difference to add
-    const double s = cta_sum(isfinite(hi) ? (double)hi + (double)lo : (double)hi, red);
+    __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
+};
+
+// First launch of a step: sums of squares of the gradients, one partial sum a
+// CTA; up to 32 squares at a time are added in FP32 (their
+// roundings are independent and cancel over the groups).  The last CTA advances
+// the step and forms its bias corrections in FP64, whose latency the others hide.
+template <int CAP>
+__global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamList<CAP> l,
+                                                                  const AdamArgs a) {
+    __shared__ double red[kAdamThreads / 32];
+    pdl_trigger();
+    pdl_wait();
+    int ctas = (int)gridDim.x;
+    if (a.advance) {
+        --ctas;
+        if ((int)blockIdx.x == ctas) {
+            const int t = *a.step + 1;
+            __syncthreads();
+            if (threadIdx.x == 0) *a.step = t;
+            if (threadIdx.x == 0 || threadIdx.x == 32) {
+                const int k = threadIdx.x / 32;
+                a.bias[k] = 1.f / (float)(1.0 - adam_pow(k == 0 ? a.beta1 : a.beta2, t));
+            }
+            return;
+        }
+    }
+    // groups of kNormChunks chunks, the CTAs in turns (runs of their own leave
+    // each CTA streaming from a far place of its own, which is slower)
+    constexpr int kUnroll = 4, kNormChunks = 8;
+    const int chunks = l.first[l.count];
+    TwoSum sum;
+    for (int c0 = (int)blockIdx.x * kNormChunks; c0 < chunks; c0 += ctas * kNormChunks) {
+        const int c1 = min(c0 + kNormChunks, chunks);
+        int c = c0;
+        for (int i = adam_find(l, c); c < c1; ++i) {
+            // the group's part of tensor i, in units of 16 bytes and a rest
+            const int to = min(c1, l.first[i + 1]);
+            const bool bf = l.t[i].grad_dtype == LRS_GRAD_BF16;
+            const int per = bf ? 8 : 4;
+            const long long e0 = (long long)(c - l.first[i]) * kAdamChunk;
+            const int n = (int)min((long long)(to - c) * kAdamChunk, (long long)l.t[i].n - e0), nv = n / per;
+            const uint4* g = static_cast<const uint4*>(l.t[i].grad) + e0 / per;
+            int v = threadIdx.x;
+            for (; v + (kUnroll - 1) * kAdamThreads < nv; v += kUnroll * kAdamThreads) {
+                uint4 x[kUnroll];
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) x[k] = __ldg(g + v + k * kAdamThreads);
+                float q = 0.f;
+#pragma unroll
+                for (int k = 0; k < kUnroll; ++k) squares(x[k], bf, q);
+                sum.add(q);
+            }
+            for (; v < nv; v += kAdamThreads) {
+                float q = 0.f;
+                squares(__ldg(g + v), bf, q);
+                sum.add(q);
+            }
+            const int e = nv * per + (int)threadIdx.x;
+            if (e < n) {
+                const float x = bf ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(g)[e] << 16)
+                                   : reinterpret_cast<const float*>(g)[e];
+                sum.add(x * x);
+            }
+            c = to;
+        }
+    }
+    const double s = cta_sum(sum.value(), red);
     if (threadIdx.x == 0) a.partial[a.partial0 + blockIdx.x] = s;
 }
 
@@ -387,10 +428,14 @@ cudaError_t adam_launch(const AdamTensor* ts, int count, AdamArgs a, bool update
     l.first[count] = (int)chunks;
     l.count = count;
     if (!update) {
-        *ctas = a.max_norm > 0.f ? adam_norm_ctas(chunks) : 1;
-        return launch_ex(adamw_norm_kernel<CAP>, dim3((unsigned)*ctas), dim3(kAdamThreads), 0, s, pdl, l, a);
+        // (without clipping only the CTA that advances the step)
+        *ctas = a.max_norm > 0.f ? adam_norm_ctas(chunks) : 0;
+        return launch_ex(adamw_norm_kernel<CAP>, dim3((unsigned)(*ctas + (a.advance ? 1 : 0))), dim3(kAdamThreads), 0, s, pdl, l, a);
     }
-    const long long grid = std::max(1LL, std::min<long long>(chunks, 4LL * block_gemm_sms()));
+    // 64 CTAs an SM, 16 times what is resident: handed out in order as others
+    // end, they keep to one region of memory (562M values: 2.45 ms, 2.63 with as
+    // many as are resident; from 512 on each one's first look at the norm shows)
+    const long long grid = std::max(1LL, std::min<long long>(chunks, 64LL * block_gemm_sms()));
     return launch_ex(adamw_update_kernel<CAP>, dim3((unsigned)grid), dim3(kAdamThreads), 0, s, pdl, l, a);
 }
 

@@ -3,6 +3,7 @@
 // (except lrs_device_status, which documents that it synchronises).
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include "kernels.cuh"
@@ -1209,7 +1210,6 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     const float* ratios = fp32 ? nullptr : dloss;
     const float* count = dloss == nullptr ? total : nullptr;
     void* hw = at<void>(scratch, l.h);
-    LRS_LAUNCH(KID_CE_ROWS, stream, launch_ce_rows_of_h(h, target, T, V, D, hw, status, stream, pdl_ok()));
     for (int i = 0; i < l.pieces; ++i) {
         const int v0 = i * l.piece, nv = std::min(l.piece, V - v0);
         CeGemmArgs g = {};
@@ -1223,6 +1223,11 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         g.T = T;
         g.dloss = dz_weight;
         g.weights = ratios;
+        if (i == 0) {
+            g.clear = 1;
+            g.rows_in = static_cast<const uint4*>(h);
+            g.rows_out = static_cast<uint4*>(hw);
+        }
         g.lse = lse;
         g.softcap = softcap;
         g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
@@ -1404,8 +1409,8 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
         (max_norm > 0.f && norm == nullptr) || !req(scratch))
         return LRS_ERR_ARG;
     AdamArgs a = {};
-    a.beta1 = beta1;
-    a.beta2 = beta2;
+    a.log_b1 = (float)std::log(beta1);
+    a.log_b2 = (float)std::log(beta2);
     a.b1 = (float)beta1;
     a.c1 = (float)(1.0 - beta1);
     a.b2 = (float)beta2;
@@ -1416,7 +1421,7 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
     a.step = step;
     a.norm = norm;
     a.bias = at<float>(scratch, 0);
-    a.partial = at<double>(scratch, 256);
+    a.partial = at<float2>(scratch, 256);
     for (int i = 0; i < count; i += kAdamCap) {
         const int k = std::min(kAdamCap, count - i);
         int ctas = 0;

@@ -140,27 +140,31 @@ __device__ __forceinline__ void store_codes(uint8_t* p, long long i, long long n
     }
 }
 
-// Sum over the CTA in a fixed order; the result in every thread.
-__device__ __forceinline__ double cta_sum(double v, double* red) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.;
-#pragma unroll
-    for (int w = 0; w < kAdamThreads / 32; ++w) v += red[w];
-    return v;
-}
-
-// b^t for t >= 1 by repeated squaring.
-__device__ double adam_pow(double b, int t) {
-    double r = 1.0;
-    for (; t > 0; t >>= 1) {
-        if (t & 1) r *= b;
-        b *= b;
+// A sum in two floats: the rounding of hi is kept in lo by the exact difference
+// (two-sum), so the sum is right to its last FP32 bit without FP64 arithmetic,
+// whose latency here is some tenths of a microsecond an operation.
+struct TwoSum {
+    float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ void add(float q, float q_lo = 0.f) {
+        const float t = __fadd_rn(hi, q), b = __fsub_rn(t, hi);
+        lo = __fadd_rn(__fadd_rn(lo, q_lo), __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(q, b)));
+        hi = t;
     }
-    return r;
+    // a sum that overflowed has no difference to add
+    __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
+// Sum over the CTA in a fixed order; the result in every thread.
+__device__ __forceinline__ TwoSum cta_sum(TwoSum v, float2* red) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1)
+        v.add(__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(v.hi, v.lo);
+    __syncthreads();
+    TwoSum s;
+#pragma unroll
+    for (int w = 0; w < kAdamThreads / 32; ++w) s.add(red[w].x, red[w].y);
+    return s;
 }
 
 // Squares of eight BF16 or four FP32 values, added to q.
@@ -177,28 +181,14 @@ __device__ __forceinline__ void squares(const uint4 v, bool bf16, float& q) {
         q = fmaf(c, c, q); q = fmaf(d, d, q);
     }
 }
-// A running sum in two floats: the rounding of hi is kept in lo by the exact
-// difference (two-sum), so the sum is right to its last FP32 bit without FP64
-// arithmetic on every value.
-struct TwoSum {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float q) {
-        const float t = __fadd_rn(hi, q), b = __fsub_rn(t, hi);
-        lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(q, b)));
-        hi = t;
-    }
-    // a sum that overflowed has no difference to add
-    __device__ __forceinline__ double value() const { return isfinite(hi) ? (double)hi + (double)lo : (double)hi; }
-};
-
 // First launch of a step: sums of squares of the gradients, one partial sum a
-// CTA; up to 32 squares at a time are added in FP32 (their
-// roundings are independent and cancel over the groups).  The last CTA advances
-// the step and forms its bias corrections in FP64, whose latency the others hide.
+// CTA; up to 32 squares at a time are added in FP32 (their roundings are
+// independent and cancel over the groups).  The last CTA advances the step and
+// forms its bias corrections, 1 - b^t = -expm1(t log b).
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamList<CAP> l,
                                                                   const AdamArgs a) {
-    __shared__ double red[kAdamThreads / 32];
+    __shared__ float2 red[kAdamThreads / 32];
     pdl_trigger();
     pdl_wait();
     int ctas = (int)gridDim.x;
@@ -210,18 +200,18 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
             if (threadIdx.x == 0) *a.step = t;
             if (threadIdx.x == 0 || threadIdx.x == 32) {
                 const int k = threadIdx.x / 32;
-                a.bias[k] = 1.f / (float)(1.0 - adam_pow(k == 0 ? a.beta1 : a.beta2, t));
+                a.bias[k] = -1.f / expm1f((float)t * (k == 0 ? a.log_b1 : a.log_b2));
             }
             return;
         }
     }
-    // groups of kNormChunks chunks, the CTAs in turns (runs of their own leave
-    // each CTA streaming from a far place of its own, which is slower)
-    constexpr int kUnroll = 4, kNormChunks = 8;
+    // groups of chunks, the CTAs in turns (runs of their own leave each CTA
+    // streaming from a far place of its own, which is slower)
+    constexpr int kUnroll = 4;
     const int chunks = l.first[l.count];
     TwoSum sum;
-    for (int c0 = (int)blockIdx.x * kNormChunks; c0 < chunks; c0 += ctas * kNormChunks) {
-        const int c1 = min(c0 + kNormChunks, chunks);
+    for (int c0 = (int)blockIdx.x * a.norm_group; c0 < chunks; c0 += ctas * a.norm_group) {
+        const int c1 = min(c0 + a.norm_group, chunks);
         int c = c0;
         for (int i = adam_find(l, c); c < c1; ++i) {
             // the group's part of tensor i, in units of 16 bytes and a rest
@@ -255,8 +245,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
             c = to;
         }
     }
-    const double s = cta_sum(sum.value(), red);
-    if (threadIdx.x == 0) a.partial[a.partial0 + blockIdx.x] = s;
+    const TwoSum s = cta_sum(sum, red);
+    if (threadIdx.x == 0) a.partial[a.partial0 + blockIdx.x] = make_float2(s.hi, s.lo);
 }
 
 // The step's scalars.
@@ -366,16 +356,19 @@ __device__ __forceinline__ void adam_block_any(const AdamTensor& t, long long b0
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads, 4) adamw_update_kernel(const __grid_constant__ AdamList<CAP> l,
                                                                        const AdamArgs a) {
-    __shared__ double red[kAdamThreads / 32];
+    __shared__ float2 red[kAdamThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_trigger();
     pdl_wait();
     AdamScalars sc;
     sc.clip = 1.f;
     if (a.max_norm > 0.f) {
-        double s = 0.;
-        for (int i = threadIdx.x; i < a.partials; i += kAdamThreads) s += __ldcg(a.partial + i);
-        const float norm = sqrtf((float)cta_sum(s, red));
+        TwoSum s;
+        for (int i = threadIdx.x; i < a.partials; i += kAdamThreads) {
+            const float2 q = __ldcg(a.partial + i);
+            s.add(q.x, q.y);
+        }
+        const float norm = sqrtf(cta_sum(s, red).value());
         const bool skip = !(norm <= 3.4028234e38f);
         if (blockIdx.x == 0 && threadIdx.x == 0 && a.advance) {
             *a.norm = norm;
@@ -411,10 +404,6 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_update_kernel(const __g
     }
 }
 
-int adam_norm_ctas(long long chunks) {
-    return (int)std::max(1LL, std::min<long long>(chunks, (long long)kAdamNormCtas * block_gemm_sms()));
-}
-
 // Tensors [t0, t0 + count) as one launch.
 template <int CAP>
 cudaError_t adam_launch(const AdamTensor* ts, int count, AdamArgs a, bool update, int* ctas, cudaStream_t s, bool pdl) {
@@ -429,7 +418,9 @@ cudaError_t adam_launch(const AdamTensor* ts, int count, AdamArgs a, bool update
     l.count = count;
     if (!update) {
         // (without clipping only the CTA that advances the step)
-        *ctas = a.max_norm > 0.f ? adam_norm_ctas(chunks) : 0;
+        const long long most = (long long)kAdamNormCtas * block_gemm_sms();
+        a.norm_group = (int)std::max(1LL, std::min(8LL, chunks / most));
+        *ctas = a.max_norm > 0.f ? (int)std::min((chunks + a.norm_group - 1) / a.norm_group, most) : 0;
         return launch_ex(adamw_norm_kernel<CAP>, dim3((unsigned)(*ctas + (a.advance ? 1 : 0))), dim3(kAdamThreads), 0, s, pdl, l, a);
     }
     // 64 CTAs an SM, 16 times what is resident: handed out in order as others
@@ -451,7 +442,7 @@ long long adam_chunks(long long n) { return (n + kAdamChunk - 1) / kAdamChunk; }
 
 size_t adam_scratch_bytes(int count) {
     const size_t launches = (size_t)(count + kAdamCap - 1) / kAdamCap;
-    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(double) + 255) / 256 * 256;
+    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(float2) + 255) / 256 * 256;
 }
 
 cudaError_t launch_adamw_norm(const AdamTensor* ts, int count, const AdamArgs& a, int* ctas, cudaStream_t s, bool pdl) {

@@ -200,6 +200,21 @@ __device__ __forceinline__ float ce_largest_weight(const CeGemmArgs& a, uint32_t
 // w / largest, exactly 1 where they are equal.
 __device__ __forceinline__ float ce_ratio(float w, float largest) { return w != 0.f ? __fdiv_rn(w, largest) : 0.f; }
 
+// The rows of h that dw = dz^T h adds up: zeros for tokens that are not counted,
+// whatever their rows hold.  Copied by the epilogue warps of the dz kernel, a
+// warp a row, under the first tile's products.
+__device__ __forceinline__ void ce_rows_of_h(const CeGemmArgs& a, int warp, int lane) {
+    const int nv = a.c[0].K / 8;
+    for (int t = (int)blockIdx.x * kCeEpiWarps + warp; t < a.T; t += (int)gridDim.x * kCeEpiWarps) {
+        const long long tg = a.target[t];
+        const bool counted = tg >= 0 && tg < a.V;
+        for (int c = lane; c < nv; c += 32) {
+            const size_t i = (size_t)t * nv + c;
+            a.rows_out[i] = counted ? __ldg(a.rows_in + i) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
+}
+
 // Tensor maps of both contractions: A, A's remainders, B, the BF16 result (s2: dz's remainders).
 struct CeMaps {
     CUtensorMap a[2], a2[2], b[2], s[2], s2;
@@ -363,6 +378,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         // the common factor of the tokens' weights: left out of dz, put on its products
         float common = 1.f;
         if (EPI != kCeStats && a.weights != nullptr) common = ce_largest_weight(a, &s_weight);
+        if ((EPI == kCeDz || EPI == kCeDz2) && a.rows_out != nullptr) ce_rows_of_h(a, warp, lane);
         if (GRADS && a.total != nullptr && a.total[1] > 0.f) common = 1.f / a.total[1];
         for (int k = 0; !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k, ++use) {
             const CeSide& c0 = a.c[it.side];
@@ -739,26 +755,6 @@ __global__ void __launch_bounds__(256) ce_rows_kernel(const float2* __restrict__
     }
 }
 
-// The rows of h that dw = dz^T h adds up: zeros for tokens that are not
-// counted, whatever their rows hold.  One warp a row; also the backward's first
-// kernel, which clears the status word.
-__global__ void __launch_bounds__(256) ce_rows_of_h_kernel(const uint4* __restrict__ h, const int64_t* __restrict__ target,
-                                                           int T, int V, int nv, uint4* __restrict__ out,
-                                                           uint32_t* status) {
-    pdl_trigger();
-    pdl_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0u;
-    const int lane = threadIdx.x & 31;
-    for (int t = blockIdx.x * 8 + (threadIdx.x >> 5); t < T; t += gridDim.x * 8) {
-        const long long tg = target[t];
-        const bool counted = tg >= 0 && tg < V;
-        for (int c = lane; c < nv; c += 32) {
-            const size_t i = (size_t)t * nv + c;
-            out[i] = counted ? __ldg(h + i) : make_uint4(0u, 0u, 0u, 0u);
-        }
-    }
-}
-
 // out[i] = sum of part[p][i] over p in order, as FP32 or BF16; n a multiple of 4.
 template <bool F32>
 __global__ void __launch_bounds__(256) ce_sum_kernel(const float4* __restrict__ part, long long stride4, int parts,
@@ -819,8 +815,6 @@ template <int EPI, bool CAP>
 cudaError_t ce_launch(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl) {
     auto* fn = ce_gemm_kernel<EPI, CAP>;
     constexpr size_t smem = ce_smem(EPI);
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kCeThreads);
     cfg.dynamicSmemBytes = smem;
@@ -832,15 +826,20 @@ cudaError_t ce_launch(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl)
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // as many pairs as fit at once (asked once per device: the query is slow next to a launch)
+    // once per device: the shared memory, and as many pairs as fit at once (the
+    // query is slow next to a launch)
     static std::atomic<int> cached[64];
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
-    int pairs = cached[dev].load(std::memory_order_relaxed);
+    const cudaError_t de = cudaGetDevice(&dev);
+    if (de != cudaSuccess) return de;
+    const bool keep = dev >= 0 && dev < 64;
+    int pairs = keep ? cached[dev].load(std::memory_order_acquire) : 0;
     if (pairs < 1) {
+        const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
         cfg.gridDim = dim3(2);
         if (cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg) != cudaSuccess || pairs < 1) pairs = ce_pairs();
-        cached[dev].store(pairs, std::memory_order_relaxed);
+        if (keep) cached[dev].store(pairs, std::memory_order_release);
     }
     pairs = std::min(pairs, a.c[0].n_items + a.c[1].n_items);
     cfg.gridDim = dim3(2u * (unsigned)pairs);
@@ -961,13 +960,6 @@ cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* 
     auto* fn = rows == 1 ? ce_rows_kernel<1> : rows == 8 ? ce_rows_kernel<8> : ce_rows_kernel<32>;
     return launch_ex(fn, dim3((unsigned)ce_row_ctas(T)), dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse,
                      sums, total, ticket, status);
-}
-
-cudaError_t launch_ce_rows_of_h(const void* h, const int64_t* target, int T, int V, int D, void* out, uint32_t* status,
-                                cudaStream_t s, bool pdl) {
-    const int grid = std::min((T + 7) / 8, 8 * block_gemm_sms());
-    return launch_ex(ce_rows_of_h_kernel, dim3((unsigned)grid), dim3(256), 0, s, pdl, static_cast<const uint4*>(h), target,
-                     T, V, D / 8, static_cast<uint4*>(out), status);
 }
 
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,

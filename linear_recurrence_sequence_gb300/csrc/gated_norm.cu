@@ -25,6 +25,7 @@
 // CTA's row slots in shared memory, one partial row a CTA, joined in a fixed
 // order by a second kernel.
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 
@@ -34,6 +35,7 @@ namespace {
 
 constexpr int kGnMaxThreads = 512;
 constexpr int kGnMaxWarps = kGnMaxThreads / 32;
+constexpr int kGnSmemMax = 216 * 1024;   // of the ring
 
 __device__ __forceinline__ void unpack8(const uint4 q, float (&v)[8]) {
     float2 f;
@@ -468,8 +470,21 @@ int gn_ctas_per_sm(const GnShape& sh, int threads_per_sm) {
     return std::max(1, threads_per_sm / (int)(sh.block.x * sh.block.y));
 }
 int gn_stages(size_t group_bytes, int ctas_per_sm) {
-    const size_t room = 216 * 1024 / ctas_per_sm;
+    const size_t room = kGnSmemMax / ctas_per_sm;
     return (int)std::max<size_t>(2, std::min<size_t>(kGnStagesMax, room / group_bytes));
+}
+
+// Lets `fn` use `smem` bytes of dynamic shared memory; the largest size asked
+// for so far is kept per device, so that a launch does not ask again.
+cudaError_t gn_allow(const void* fn, int smem, std::atomic<int>* allowed) {
+    int dev = 0;
+    const cudaError_t de = cudaGetDevice(&dev);
+    if (de != cudaSuccess) return de;
+    const bool keep = dev >= 0 && dev < 64;
+    if (keep && allowed[dev].load(std::memory_order_acquire) >= smem) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kGnSmemMax);
+    if (e == cudaSuccess && keep) allowed[dev].store(kGnSmemMax, std::memory_order_release);
+    return e;
 }
 
 template <bool Y, bool G, int VEC>
@@ -484,7 +499,8 @@ cudaError_t gn_fwd_as(GatedNormArgs a, const GnShape& sh, cudaStream_t s, bool p
     a.stages = gn_stages(group, per_sm);
     auto* fn = gated_norm_fwd_kernel<Y, G, VEC, true>;
     const size_t smem = group * a.stages;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<int> allowed[64];
+    const cudaError_t e = gn_allow(reinterpret_cast<const void*>(fn), (int)smem, allowed);
     if (e != cudaSuccess) return e;
     return launch_ex(fn, dim3((unsigned)resident), sh.block, smem, s, pdl, a);
 }
@@ -500,7 +516,8 @@ cudaError_t gn_bwd_as(GatedNormBwdArgs a, const GnShape& sh, int ctas, cudaStrea
     a.f.stages = gn_stages(group, gn_ctas_per_sm(sh, Y ? 512 : 1024));
     const size_t smem = std::max(group * a.f.stages, (size_t)(Y ? 2 : 1) * sh.block.y * a.f.D * sizeof(float));
     auto* fn = gated_norm_bwd_kernel<Y, G, VEC>;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<int> allowed[64];
+    const cudaError_t e = gn_allow(reinterpret_cast<const void*>(fn), (int)smem, allowed);
     if (e != cudaSuccess) return e;
     return launch_ex(fn, dim3((unsigned)ctas), sh.block, smem, s, pdl, a);
 }

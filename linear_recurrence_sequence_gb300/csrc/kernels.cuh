@@ -558,6 +558,8 @@ struct CeGemmArgs {
     const float* weights;        // dz, the gradients: [T] factors, the largest of which is put on the gradients, or null
     const float* total;          // the gradients: both divided by total[1], or null
     const float* lse;            // kCeDz: [M]
+    const uint4* rows_in;        // dz: h, whose counted rows go to rows_out (null: not copied)
+    uint4* rows_out;
     float softcap, inv_softcap;  // 0: none
     uint32_t* status;            // two words: the status, the rows' ticket
     int clear;                   // the call's first kernel: clears both
@@ -579,8 +581,6 @@ int ce_row_ctas(int T);
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
                            float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
                            cudaStream_t s, bool pdl);
-cudaError_t launch_ce_rows_of_h(const void* h, const int64_t* target, int T, int V, int D, void* out, uint32_t* status,
-                                cudaStream_t s, bool pdl);
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,
                           cudaStream_t s, bool pdl);
 
@@ -625,14 +625,15 @@ using AdamTensor = lrs_adamw_tensor;
 // or 30 KB of the 32 KB that they may hold.
 constexpr int kAdamCapSmall = 32, kAdamCap = 400;
 struct AdamArgs {
-    double beta1, beta2;
     float b1, c1, b2, c2;        // the betas and 1 - beta, rounded once
+    float log_b1, log_b2;        // the betas' logarithms (-inf for 0)
     float eps, max_norm;
     const float* lr;
     int32_t* step;
     float* norm;
     float* bias;                 // [2]: 1 / (1 - beta^step)
-    double* partial;             // sums of squares, one a CTA of the first launches
+    float2* partial;             // sums of squares (two floats each), one a CTA of the first launches
+    int norm_group;              // chunks a CTA of the norm takes at a time (filled by the launcher)
     int partial0, partials;      // this launch's first, and all
     int advance;                 // the step's first launch of its kind
 };

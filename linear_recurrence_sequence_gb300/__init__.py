@@ -12,6 +12,9 @@ from __future__ import annotations
 __all__ = [
     "samu_workspace_bytes", "samu_forward", "samu_backward",
     "rglru_workspace_bytes", "rglru_forward", "rglru_backward",
+    "linear_ce_workspace_bytes", "linear_ce_forward", "linear_ce_backward",
+    "gated_norm_workspace_bytes", "gated_norm_forward", "gated_norm_backward",
+    "adamw_state", "adamw_plan", "adamw_step",
     "device_status", "library_path",
 ]
 

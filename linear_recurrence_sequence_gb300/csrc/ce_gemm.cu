@@ -137,6 +137,36 @@ __device__ __forceinline__ void ce_columns(uint32_t taddr, float (&v)[2][16]) {
 // The capped logit and its slope: z' = c tanh(z / c), dz'/dz = 1 - (z'/c)^2.
 __device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a.softcap * tanhf(z * a.inv_softcap); }
 
+// tanh(x / c) of 32 logits in place (c the cap).  Where the whole warp's |x / c|
+// are at most 0.4, as logits mostly are, by the first seven terms of tanh's
+// Taylor series (the eighth is below 4e-9 of the value there): 9 operations
+// where tanhf takes about 25, which held the capped epilogues back (2048 tokens
+// x 50021 entries at D 1024: TIME_CAP).
+__device__ __forceinline__ void ce_tanh(const CeGemmArgs& a, float (&v)[2][16]) {
+    float top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        v[j / 16][j % 16] *= a.inv_softcap;
+        top = fmaxf(top, fabsf(v[j / 16][j % 16]));
+    }
+    // (a NaN among the logits is not seen by the maximum, and stays one in the series)
+    if (__any_sync(0xffffffffu, top > 0.4f)) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = tanhf(v[j / 16][j % 16]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float x = v[j / 16][j % 16], x2 = x * x;
+            float p = fmaf(x2, 21844.f / 6081075.f, -1382.f / 155925.f);
+            p = fmaf(p, x2, 62.f / 2835.f);
+            p = fmaf(p, x2, -17.f / 315.f);
+            p = fmaf(p, x2, 2.f / 15.f);
+            p = fmaf(p, x2, -1.f / 3.f);
+            v[j / 16][j % 16] = fmaf(p * x2, x, x);
+        }
+    }
+}
+
 // Forward epilogue of one row: (max, sum e^{z - max}) of its 128 columns.
 // Columns past the vocabulary do not count; the target's logit is kept.
 template <bool CAP>
@@ -153,10 +183,11 @@ __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& 
     for (int c = 0; c < kCeN / 2; c += 32) {
         float v[2][16];
         ce_columns(taddr + (uint32_t)(c0 + c), v);
+        if (CAP) ce_tanh(a, v);
         if (!ok || c >= nv) continue;
         float z[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) z[j] = CAP ? ce_cap(a, v[j / 16][j % 16]) : v[j / 16][j % 16];
+        for (int j = 0; j < 32; ++j) z[j] = CAP ? a.softcap * v[j / 16][j % 16] : v[j / 16][j % 16];
         if (tgt >= c && tgt < c + 32) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
@@ -483,26 +514,43 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     float v[2][16], lo[2][16];
                     ce_columns(taddr + (uint32_t)c, v);
                     if (EPI == kCeDz || EPI == kCeDz2) {
+                        if (CAP) ce_tanh(a, v);
+                        const bool mine = tgt >= c && tgt < c + 32;   // a lane in many
+                        float one = wgt;   // what the target's 1 becomes
+                        if (CAP && mine) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (tgt == c + j) one = wgt * fmaf(-v[j / 16][j % 16], v[j / 16][j % 16], 1.f);
+                        }
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
-                            float z = v[j / 16][j % 16], slope = 1.f;
-                            if (CAP) {
-                                const float th = tanhf(z * a.inv_softcap);
-                                z = a.softcap * th;
-                                slope = fmaf(-th, th, 1.f);
-                            }
-                            float e = ex2_approx(fmaf(z, kLog2e, -lse2));
-                            if (tgt == c + j) e -= 1.f;
+                            const float th = v[j / 16][j % 16];   // (the logit itself without a cap)
+                            float e = ex2_approx(fmaf(th, CAP ? a.softcap * kLog2e : kLog2e, -lse2));
                             e *= wgt;
-                            if (CAP) e *= slope;
-                            if (c + j >= nv) e = 0.f;
+                            if (CAP) e *= fmaf(-th, th, 1.f);
                             v[j / 16][j % 16] = e;
-                            if (EPI == kCeDz2) lo[j / 16][j % 16] = e - __bfloat162float(__float2bfloat16_rn(e));
+                        }
+                        if (mine) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (tgt == c + j) v[j / 16][j % 16] -= one;
+                        }
+                        if (c + 32 > nv) {   // past the vocabulary
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (c + j >= nv) v[j / 16][j % 16] = 0.f;
                         }
                         // a row without a weight has exact zeros (its lse may be anything)
                         if (wgt == 0.f) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = lo[j / 16][j % 16] = 0.f;
+                            for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = 0.f;
+                        }
+                        if (EPI == kCeDz2) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                const float e = v[j / 16][j % 16];
+                                lo[j / 16][j % 16] = e - __bfloat162float(__float2bfloat16_rn(e));
+                            }
                         }
                     }
                     if (GRADS) {

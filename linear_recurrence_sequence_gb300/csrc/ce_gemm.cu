@@ -319,10 +319,12 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     const int n0 = it.nt * kCeN + 128 * rank;
                     const CUtensorMap* ta = second ? ta2 : ta1;
                     // both CTAs' bytes are announced by the even one (the odd one's may land first)
-                    // rows of A past the matrix are not loaded: what their accumulator rows hold is not used
+                    // rows of A past the matrix (of K-major A past the next eight) are not loaded:
+                    // what their accumulator rows hold is not used
+                    const uint32_t a_bytes = tn ? kCeABytes : 2 * a.a_chunk;
                     if (rank == 0)
                         mbar_arrive_expect_tx(&s_full[slot],
-                                              2 * kCeStageBytes - (it.m0 + 128 < c.M ? 0u : kCeABytes));
+                                              2 * kCeBBytes + (it.m0 + 128 < c.M ? 2 * a_bytes : a_bytes));
                     const uint32_t bar = cluster_map(&s_full[slot], 0);
                     // each operand as one box of two chunks; where rows are no whole number of chunks (the
                     // second would run into the next row), as two boxes that the matrix's edge cuts
@@ -332,7 +334,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                         tma2_load_3d(sa, ta, 0, ay, ax / 64, bar);
                     } else {
                         tma2_load_2d(sa, ta, ax, ay, bar);
-                        tma2_load_2d(sa + kCeChunk, ta, ax + 64, ay, bar);
+                        tma2_load_2d(sa + a.a_chunk, ta, ax + 64, ay, bar);
                     }
                     const int bx = GRADS ? n0 : k0, by = c.b_row + (GRADS ? k0 : n0);
                     if (a.whole) {
@@ -381,9 +383,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kCeK / 16; ++kk) {
                             // K-major: chunk kk / 4, 32 bytes a step; MN-major: 16 rows a step in both chunks
-                            const uint32_t kmaj = kCeChunk * (kk / 4) + 32u * (kk % 4), mn = 2048u * kk;
-                            const uint64_t da = tn ? umma_desc_sw128_mn(sa + mn, kCeChunk) : umma_desc_sw128(sa + kmaj);
-                            const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + mn, kCeChunk) : umma_desc_sw128(sb + kmaj);
+                            const uint32_t at = 32u * (kk % 4), mn = 2048u * kk;
+                            const uint64_t da = tn ? umma_desc_sw128_mn(sa + mn, kCeChunk)
+                                                   : umma_desc_sw128(sa + (kk < 4 ? at : a.a_chunk + at));
+                            const uint64_t db = GRADS ? umma_desc_sw128_mn(sb + mn, kCeChunk)
+                                                      : umma_desc_sw128(sb + (kk < 4 ? at : kCeChunk + at));
                             umma2_bf16(acc_t, da, db, idesc, ks > k0 || kk > 0);
                         }
                         umma2_commit(&s_empty[slot]);
@@ -838,13 +842,14 @@ bool ce_map(CUtensorMap* map, const void* ptr, long long cols, long long rows, l
 
 // An operand's map: 128 rows of two 64-column chunks in one box (the columns
 // seen as [cols / 64] chunks, `whole`), or of one chunk.
-bool ce_operand(CUtensorMap* map, const void* ptr, long long cols, long long rows, long long ld, bool whole) {
-    if (!whole) return ce_map(map, ptr, cols, rows, ld, 64, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+bool ce_operand(CUtensorMap* map, const void* ptr, long long cols, long long rows, long long ld, bool whole,
+                int box_rows = 128) {
+    if (!whole) return ce_map(map, ptr, cols, rows, ld, 64, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
     PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
     if (fn == nullptr) return false;
     cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(cols / 64)};
     cuuint64_t strides[2] = {(cuuint64_t)ld * 2, 128};
-    cuuint32_t box[3] = {64, 128, 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 2};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -856,7 +861,13 @@ bool ce_result(CUtensorMap* map, const void* ptr, long long cols, long long rows
     return ce_map(map, ptr, cols, rows, ld, wide ? 64 : 32, 32, wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-int ce_item_steps(const CeSide& c) { return std::max(1, c.ksteps / c.splits); }
+// Rows of a box of K-major A: with few tokens only as many as there are, in whole
+// swizzle atoms (a box mostly outside the matrix takes as long to fill with
+// zeros: 16 tokens x 32768 entries at D 1024, 20.6 -> TIME_ROWS us).
+int ce_a_rows(int M) { return std::min(128, (M + 7) / 8 * 8); }
+// What an item of dh or dw costs, in K steps: its own, or its epilogue's if that is longer.
+constexpr int kCeEpiSteps = 4;
+int ce_item_steps(const CeSide& c) { return std::max(kCeEpiSteps, c.ksteps / c.splits); }
 int ce_pairs() { return std::max(1, block_gemm_sms() / 2); }
 
 template <int EPI, bool CAP>
@@ -914,7 +925,9 @@ int ce_n_tiles(long long N) { return (int)((N + kCeN - 1) / kCeN); }
 // around it is spread over the pairs.
 void ce_grad_splits(long long T, long long V, long long D, int parts, int sms, int* h_splits, int* w_splits) {
     const long long ch = parts * ((V + kCeK - 1) / kCeK), cw = parts * ((T + kCeK - 1) / kCeK);
-    const long long steps = ((long long)ce_m_tiles(T) * ch + (long long)ce_m_tiles(V) * cw) * ce_n_tiles(D);
+    const long long e = kCeEpiSteps;
+    const long long steps =
+        ((long long)ce_m_tiles(T) * std::max(e, ch) + (long long)ce_m_tiles(V) * std::max(e, cw)) * ce_n_tiles(D);
     const long long most = std::max(8LL, steps / std::max(1, sms / 2));
     *h_splits = (int)std::min<long long>(kCeSplitsMax, (ch + most - 1) / most);
     *w_splits = (int)std::min<long long>(kCeSplitsMax, (cw + most - 1) / most);
@@ -944,7 +957,9 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
     a.c[1].n_items = 0;
     CeMaps tm;
     a.whole = c.K % 64 == 0;
-    if (!ce_operand(&tm.a[0], h, c.K, c.M, c.K, a.whole) || !ce_operand(&tm.b[0], w, c.K, V, c.K, a.whole))
+    const int rows = ce_a_rows(c.M);
+    a.a_chunk = rows * 128;
+    if (!ce_operand(&tm.a[0], h, c.K, c.M, c.K, a.whole, rows) || !ce_operand(&tm.b[0], w, c.K, V, c.K, a.whole))
         return cudaErrorInvalidValue;
     tm.s[0] = tm.s2 = tm.a[0];
     if (dz != nullptr && !ce_result(&tm.s[0], dz, c.s_cols, c.M, ldz, dz2 == nullptr)) return cudaErrorInvalidValue;
@@ -983,11 +998,12 @@ cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz
     CeMaps tm;
     const void* second = dz2 != nullptr ? dz2 : dz;
     a.whole = D % 64 == 0;   // dz's own rows always are
-    if (!ce_operand(&tm.a[0], dz, ldz, T, ldz, true) || !ce_operand(&tm.a2[0], second, ldz, T, ldz, true) ||
+    const int rows = ce_a_rows((int)T);
+    a.a_chunk = rows * 128;
+    if (!ce_operand(&tm.a[0], dz, ldz, T, ldz, true, rows) || !ce_operand(&tm.a2[0], second, ldz, T, ldz, true, rows) ||
+        !ce_operand(&tm.a[1], dz, ldz, T, ldz, true) || !ce_operand(&tm.a2[1], second, ldz, T, ldz, true) ||
         !ce_operand(&tm.b[0], w, D, V, D, a.whole) || !ce_operand(&tm.b[1], h, D, T, D, a.whole))
         return cudaErrorInvalidValue;
-    tm.a[1] = tm.a[0];
-    tm.a2[1] = tm.a2[0];
     tm.s[0] = tm.s[1] = tm.s2 = tm.a[0];
     if (a.c[0].part == nullptr && !ce_result(&tm.s[0], dh, D, T, D, true)) return cudaErrorInvalidValue;
     if (a.c[1].part == nullptr && !ce_result(&tm.s[1], dw, D, V, D, true)) return cudaErrorInvalidValue;

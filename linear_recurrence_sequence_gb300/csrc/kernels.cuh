@@ -565,6 +565,7 @@ struct CeGemmArgs {
     int clear;                   // the call's first kernel: clears both
     int group, extra, whole;     // filled by the launchers: row tiles per group; dw items ahead (see ce_item);
                                  // rows of h and w are whole 64-column chunks
+    uint32_t a_chunk;            // bytes of one 64-column chunk of K-major A's box
 };
 
 int ce_m_tiles(long long M);

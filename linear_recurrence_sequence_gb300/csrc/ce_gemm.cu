@@ -13,20 +13,25 @@
 // the last two in one launch: neither's tile count fills the pairs of SMs
 // evenly, and together they do (a pair with one dh tile less than the others
 // takes as many more of the shorter dw tiles; 8192 tokens x 32768 entries at
-// D 2048: 1525 us one after the other, see below together).
-// Unlike the block's contractions (block_gemm.cu) every extent may be ragged:
+// D 2048: 1171 us, one after the other 1267; 16 tokens at D 1024: 37 and 60).
+// Measured (events around each launch): the statistics of 32768 x 32768 at
+// D 1024 1.07 ms, 2.06 PFLOP/s; dz of 8192 x 32768 at D 2048 0.58 ms, 1.9; dh and
+// dw of it 1.17 ms, 1.9.  Back to back such calls meet the power limit, at about
+// 1.7.  Unlike the block's contractions (block_gemm.cu) every extent may be ragged:
 // the TMA fills what lies outside a matrix with zeros and clips what is stored
 // there; columns past the vocabulary are zeroed in dz.
 //
 // CTA pairs (cta_group::2) take 256 x 256 tiles: each CTA loads its 128 rows
 // of A and half of B's slice, so the pair reads every operand value of its tile
-// once and shared memory holds six 64-wide K slices of it.  In each CTA warp 8
+// once and shared memory holds three 128-wide K slices of it.  In each CTA warp 8
 // streams the slices by TMA (128-byte swizzle), completing on the even CTA's
 // barriers; one thread of the even CTA's warp 9 issues tcgen05.mma (M 256,
 // N 256, K 16) for both and frees the slices by commits to both; warps 0-7
 // drain the CTA's 128 accumulator rows, of which there are two sets in turn so
 // that a tile's epilogue runs under the next tile's MMAs.  Every wait is
-// bounded.
+// bounded but the pair's allocation of tensor memory, which waits for kernels
+// that hold columns on either SM; those end by themselves (their waits are
+// bounded), and both CTAs of a cluster are resident together.
 #include <algorithm>
 #include <atomic>
 
@@ -141,7 +146,7 @@ __device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a
 // are at most 0.4, as logits mostly are, by the first seven terms of tanh's
 // Taylor series (the eighth is below 4e-9 of the value there): 9 operations
 // where tanhf takes about 25, which held the capped epilogues back (2048 tokens
-// x 50021 entries at D 1024: TIME_CAP).
+// x 50021 entries at D 1024: statistics 163 -> 145 us, dz in two parts 199 -> 169).
 __device__ __forceinline__ void ce_tanh(const CeGemmArgs& a, float (&v)[2][16]) {
     float top = 0.f;
 #pragma unroll
@@ -863,7 +868,7 @@ bool ce_result(CUtensorMap* map, const void* ptr, long long cols, long long rows
 
 // Rows of a box of K-major A: with few tokens only as many as there are, in whole
 // swizzle atoms (a box mostly outside the matrix takes as long to fill with
-// zeros: 16 tokens x 32768 entries at D 1024, 20.6 -> TIME_ROWS us).
+// zeros: 16 tokens x 32768 entries at D 1024, 26.6 -> 22.7 us).
 int ce_a_rows(int M) { return std::min(128, (M + 7) / 8 * 8); }
 // What an item of dh or dw costs, in K steps: its own, or its epilogue's if that is longer.
 constexpr int kCeEpiSteps = 4;
@@ -974,8 +979,9 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
 }
 
 // The statistics of T <= 4 tokens, one part a CTA.  Against 32768 x 1024 (67 MB
-// of w not in the L2, forward with its second kernel) 1, 2, 4 tokens take
-// TIME_FEW us, 29 us by the tensor-core tiles; from 6 on those are faster (30 against 34 us).
+// of w not in the L2, forward with its second kernel) 1, 2 and 4 tokens take 21,
+// 22 and 26 us, 29 by the tensor-core tiles, which from 6 on are faster (30
+// against 34 us).
 bool ce_is_few(int T, int D) { return T <= 4 && (long long)T * D * 2 <= 48 * 1024; }
 int ce_few_parts(int T, int sms) { return kCeFewThreads / 256 / (T == 1 ? 1 : 2) * sms; }
 cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl) {

@@ -14,7 +14,10 @@
 // gradients share one sum).
 // r is formed again from x, y and g, in FP32: the rounded r is not read.
 //
-// Bound by bandwidth: 10 bytes a value forward, 16 backward, each array once.
+// Bound by bandwidth: 10 bytes a value forward, 16 backward, each array once
+// (16384 x 1024 with branch and gate, events around each launch: 30 us, 5.6 TB/s,
+// and 48 us, 5.5 TB/s; 5001 x 2560 without a branch 12 and 22 us; 16 rows of 2048
+// in a graph 2.4 us).
 // A thread holds 8 consecutive channels (16 bytes of each operand) of a row
 // that stays in registers between its two row sums; a CTA takes several rows
 // at a time where they are narrow.  Where a CTA has more than one group of
@@ -37,25 +40,65 @@ constexpr int kGnMaxThreads = 512;
 constexpr int kGnMaxWarps = kGnMaxThreads / 32;
 constexpr int kGnSmemMax = 216 * 1024;   // of the ring
 
-__device__ __forceinline__ void unpack8(const uint4 q, float (&v)[8]) {
-    float2 f;
-    f = bf2_to_f2(q.x); v[0] = f.x; v[1] = f.y;
-    f = bf2_to_f2(q.y); v[2] = f.x; v[3] = f.y;
-    f = bf2_to_f2(q.z); v[4] = f.x; v[5] = f.y;
-    f = bf2_to_f2(q.w); v[6] = f.x; v[7] = f.y;
+// Pairs of channels in the two-wide FP32 instructions: the row arithmetic is
+// half of what these kernels issue.
+__device__ __forceinline__ uint64_t as_u64(float2 v) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(v.x), "f"(v.y));
+    return r;
 }
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-    return make_uint4(f2_to_bf2(v[0], v[1]), f2_to_bf2(v[2], v[3]), f2_to_bf2(v[4], v[5]), f2_to_bf2(v[6], v[7]));
+__device__ __forceinline__ float2 as_f2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
 }
-__device__ __forceinline__ void load8(const float* p, int v, bool on, float fill, float (&o)[8]) {
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)), "l"(as_u64(c)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(as_u64(a)), "l"(as_u64(b)));
+    return as_f2(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+__device__ __forceinline__ void unpack8(const uint4 q, float2 (&v)[4]) {
+    v[0] = bf2_to_f2(q.x);
+    v[1] = bf2_to_f2(q.y);
+    v[2] = bf2_to_f2(q.z);
+    v[3] = bf2_to_f2(q.w);
+}
+__device__ __forceinline__ uint4 pack8(const float2 (&v)[4]) {
+    return make_uint4(f2_to_bf2(v[0].x, v[0].y), f2_to_bf2(v[1].x, v[1].y), f2_to_bf2(v[2].x, v[2].y),
+                      f2_to_bf2(v[3].x, v[3].y));
+}
+// 8 channels of a vector; ones where it is missing or the thread has none.
+__device__ __forceinline__ void load8(const float* p, int v, bool on, float2 (&o)[4]) {
     if (p == nullptr || !on) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fill;
+        for (int i = 0; i < 4; ++i) o[i] = both(1.f);
         return;
     }
     const float4 a = __ldg(reinterpret_cast<const float4*>(p) + 2 * v), b = __ldg(reinterpret_cast<const float4*>(p) + 2 * v + 1);
-    o[0] = a.x; o[1] = a.y; o[2] = a.z; o[3] = a.w;
-    o[4] = b.x; o[5] = b.y; o[6] = b.z; o[7] = b.w;
+    o[0] = make_float2(a.x, a.y);
+    o[1] = make_float2(a.z, a.w);
+    o[2] = make_float2(b.x, b.y);
+    o[3] = make_float2(b.z, b.w);
+}
+// scale gamma_post of 8 channels.
+__device__ __forceinline__ void load_product(const float* p, const float* q, int v, bool on, float2 (&o)[4]) {
+    float2 b[4];
+    load8(p, v, on, o);
+    load8(q, v, on, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul2(o[i], b[i]);
 }
 
 // The block's GeLU, x s with s = 1 / (1 + e^{-2u}), u = sqrt(2/pi) (x + 0.044715 x^3),
@@ -68,24 +111,19 @@ constexpr float kGelu0 = -2.302208198f;    // -2 sqrt(2/pi) log2(e)
 constexpr float kGelu1 = -0.1029432397f;   // 0.044715 of it
 constexpr float kGelu2 = 1.595769122f;     // 2 sqrt(2/pi)
 constexpr float kGelu3 = 0.2140644488f;    // 3 0.044715 of it
-__device__ __forceinline__ float gn_gelu(float x) {
-    return x * rcp_approx(1.f + ex2_approx(x * fmaf(kGelu1, x * x, kGelu0)));
+__device__ __forceinline__ float2 gn_gelu(float2 x) {
+    const float2 t = mul2(x, fma2(both(kGelu1), mul2(x, x), both(kGelu0)));
+    const float2 e = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.f));
+    return mul2(x, make_float2(rcp_approx(e.x), rcp_approx(e.y)));
 }
-__device__ __forceinline__ void gn_gelu_grad(float x, float& g, float& dg) {
-    const float x2 = x * x;
-    const float e = fminf(ex2_approx(x * fmaf(kGelu1, x2, kGelu0)), 3e38f);
-    const float s = rcp_approx(1.f + e);
-    g = x * s;
-    dg = fmaf(s * (e * s), x * fmaf(kGelu3, x2, kGelu2), s);
-}
-
-// scale gamma_post of 8 channels (a missing vector is ones).
-__device__ __forceinline__ void load_product(const float* p, const float* q, int v, bool on, float (&o)[8]) {
-    float b[8];
-    load8(p, v, on, 1.f, o);
-    load8(q, v, on, 1.f, b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] *= b[i];
+__device__ __forceinline__ void gn_gelu_grad(float2 x, float2& g, float2& dg) {
+    const float2 x2 = mul2(x, x);
+    const float2 t = mul2(x, fma2(both(kGelu1), x2, both(kGelu0)));
+    const float2 e = make_float2(fminf(ex2_approx(t.x), 3e38f), fminf(ex2_approx(t.y), 3e38f));
+    const float2 e1 = add2(e, both(1.f));
+    const float2 s = make_float2(rcp_approx(e1.x), rcp_approx(e1.y));
+    g = mul2(x, s);
+    dg = fma2(mul2(s, mul2(e, s)), mul2(x, fma2(both(kGelu3), x2, both(kGelu2))), s);
 }
 
 // Sum over the threads of a row (blockDim.x of them, whole warps).  `red` is
@@ -196,11 +234,11 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
         ring.start(a.T, nv, a.stages, buf, full);
     }
     // a thread's channels are the same in every row: so are its vectors
-    float gm[VEC][8], sg[VEC][8];
+    float2 gm[VEC][4], sg[VEC][4];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
-        load8(a.gamma_pre, v, v < nv, 1.f, gm[k]);
+        load8(a.gamma_pre, v, v < nv, gm[k]);
         if (Y) load_product(a.scale, a.gamma_post, v, v < nv, sg[k]);
     }
     bool lost = false;
@@ -220,48 +258,50 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_fwd_kernel(const Gat
                 if (G) qg[k] = RING ? ring.get(Y + G, k * blockDim.x) : __ldg(a.g + o);
             }
         }
-        float r[VEC][8], rstd1 = 0.f;
+        float2 r[VEC][4];
+        float rstd1 = 0.f;
 #pragma unroll
         for (int k = 0; k < VEC; ++k) unpack8(qx[k], r[k]);
         if (Y) {
-            float ss = 0.f;
+            float2 ss = both(0.f);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                float y[8];
+                float2 y[4];
                 unpack8(qy[k], y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(y[i], y[i], ss);
+                for (int i = 0; i < 4; ++i) ss = fma2(y[i], y[i], ss);
             }
-            rstd1 = rsqrtf(fmaf(row_sum(ss, red[0]), inv_d, a.eps));
+            rstd1 = rsqrtf(fmaf(row_sum(ss.x + ss.y, red[0]), inv_d, a.eps));
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
-                float y[8], g[8];
+                float2 y[4], g[4];
                 unpack8(qy[k], y);
                 unpack8(qg[k], g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = y[i] * rstd1 * sg[k][i];
-                    r[k][i] = G ? fmaf(gn_gelu(g[i]), p, r[k][i]) : r[k][i] + p;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p = mul2(mul2(y[i], both(rstd1)), sg[k][i]);
+                    r[k][i] = G ? fma2(gn_gelu(g[i]), p, r[k][i]) : add2(r[k][i], p);
                 }
             }
         }
-        float ss = 0.f;
+        float2 ss = both(0.f);
 #pragma unroll
         for (int k = 0; k < VEC; ++k)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(r[k][i], r[k][i], ss);
-        const float rstd2 = rsqrtf(fmaf(row_sum(ss, red[Y ? 1 : it & 1]), inv_d, a.eps));
+            for (int i = 0; i < 4; ++i) ss = fma2(r[k][i], r[k][i], ss);
+        float rstd2 = rsqrtf(fmaf(row_sum(ss.x + ss.y, red[Y ? 1 : it & 1]), inv_d, a.eps));
+        if (lost) rstd1 = rstd2 = NAN;
         if (RING) ring.taken();
         if (row >= a.T) continue;
         if (threadIdx.x == 0 && a.rstd != nullptr)
-            a.rstd[row] = lost ? make_float2(NAN, NAN) : make_float2(rstd1, rstd2);
+            a.rstd[row] = make_float2(rstd1, rstd2);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
             if (v >= nv) continue;
-            float h[8];
+            float2 h[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = lost ? NAN : r[k][i] * rstd2 * gm[k][i];
+            for (int i = 0; i < 4; ++i) h[i] = mul2(mul2(r[k][i], both(rstd2)), gm[k][i]);
             const size_t o = (size_t)row * nv + v;
             if (Y) a.r[o] = pack8(r[k]);
             a.h[o] = pack8(h);
@@ -289,15 +329,15 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
     if (G) ring.src[2 + Y + G] = f.g;
     ring.start(f.T, nv, f.stages, buf, full);
     // a thread's channels are the same in every row: so are its vectors
-    float gm[VEC][8], sg[VEC][8];
-    float dpre[VEC][8], sum[VEC][8];
+    float2 gm[VEC][4], sg[VEC][4];
+    float2 dpre[VEC][4], sum[VEC][4];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) {
         const int v = threadIdx.x + k * blockDim.x;
-        load8(f.gamma_pre, v, v < nv, 1.f, gm[k]);
+        load8(f.gamma_pre, v, v < nv, gm[k]);
         if (Y) load_product(f.scale, f.gamma_post, v, v < nv, sg[k]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dpre[k][i] = sum[k][i] = 0.f;
+        for (int i = 0; i < 4; ++i) dpre[k][i] = sum[k][i] = both(0.f);
     }
     // the rows' reciprocal norms, one group ahead
     float2 ahead = make_float2(0.f, 0.f);
@@ -326,68 +366,74 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
             }
         }
         // q = r rstd2, a = dh gamma_pre, mean(a q)
-        float q[VEC][8], ge[VEC][8], dge[VEC][8], s = 0.f;
+        float2 q[VEC][4], ge[VEC][4], dge[VEC][4], s = both(0.f);
+        const float2 rs1 = both(rs.x), rs2 = both(rs.y);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-            float dh[8];
+            float2 dh[4];
             unpack8(qx[k], q[k]);
             unpack8(qh[k], dh);
             if (Y) {
-                float y[8], g[8];
+                float2 y[4], g[4];
                 unpack8(qy[k], y);
                 unpack8(qg[k], g);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ge[k][i] = 1.f;
-                    dge[k][i] = 0.f;
-                    if (G) gn_gelu_grad(g[i], ge[k][i], dge[k][i]);
-                    q[k][i] = fmaf(sg[k][i] * ge[k][i], y[i] * rs.x, q[k][i]);
+                for (int i = 0; i < 4; ++i) {
+                    if (G) {
+                        gn_gelu_grad(g[i], ge[k][i], dge[k][i]);
+                        q[k][i] = fma2(mul2(sg[k][i], ge[k][i]), mul2(y[i], rs1), q[k][i]);
+                    } else {
+                        q[k][i] = fma2(sg[k][i], mul2(y[i], rs1), q[k][i]);
+                    }
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q[k][i] *= rs.y;
-                const float dq = dh[i] * q[k][i];
-                dpre[k][i] += dq;
-                s = fmaf(dq, gm[k][i], s);
+            for (int i = 0; i < 4; ++i) {
+                q[k][i] = mul2(q[k][i], rs2);
+                const float2 dq = mul2(dh[i], q[k][i]);
+                dpre[k][i] = add2(dpre[k][i], dq);
+                s = fma2(dq, gm[k][i], s);
             }
         }
-        const float mean = row_sum(s, red[Y ? 0 : it & 1]) * inv_d;
+        const float mean = row_sum(s.x + s.y, red[Y ? 0 : it & 1]) * inv_d;
         ring.taken();
-        float dx[VEC][8];
-        s = 0.f;
+        float2 dx[VEC][4];
+        s = both(0.f);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
             const int v = threadIdx.x + k * blockDim.x;
-            float dh[8], dr[8];
+            float2 dh[4], dr[4];
             unpack8(qh[k], dh);
             unpack8(qr[k], dr);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) dx[k][i] = fmaf(rs.y, dh[i] * gm[k][i] - q[k][i] * mean, dr[i]);
+            for (int i = 0; i < 4; ++i)
+                dx[k][i] = fma2(rs2, fma2(q[k][i], both(-mean), mul2(dh[i], gm[k][i])), dr[i]);
             if (row < f.T && v < nv) a.dx[(size_t)row * nv + v] = pack8(dx[k]);
             if (Y) {
-                float y[8], dg[8];
+                float2 y[4], dg[4];
                 unpack8(qy[k], y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float p = y[i] * rs.x, e = dx[k][i] * ge[k][i], ep = e * p;
-                    dg[i] = dx[k][i] * dge[k][i] * (p * sg[k][i]);
-                    sum[k][i] += ep;
-                    s = fmaf(ep, sg[k][i], s);
-                    dx[k][i] = e * sg[k][i];   // b
+                for (int i = 0; i < 4; ++i) {
+                    const float2 p = mul2(y[i], rs1), e = G ? mul2(dx[k][i], ge[k][i]) : dx[k][i], ep = mul2(e, p);
+                    if (G) dg[i] = mul2(mul2(dx[k][i], dge[k][i]), mul2(p, sg[k][i]));
+                    sum[k][i] = add2(sum[k][i], ep);
+                    s = fma2(ep, sg[k][i], s);
+                    dx[k][i] = mul2(e, sg[k][i]);   // b
                 }
                 if (G && row < f.T && v < nv) a.dg[(size_t)row * nv + v] = pack8(dg);
             }
         }
         if (Y) {
-            const float mean1 = row_sum(s, red[1]) * inv_d;
+            // dy = rstd1 b - y (rstd1^2 mean)
+            const float mean1 = row_sum(s.x + s.y, red[1]) * inv_d;
+            const float2 back = both(-rs.x * rs.x * mean1);
 #pragma unroll
             for (int k = 0; k < VEC; ++k) {
                 const int v = threadIdx.x + k * blockDim.x;
-                float y[8], dy[8];
+                float2 y[4], dy[4];
                 unpack8(qy[k], y);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) dy[i] = rs.x * (dx[k][i] - y[i] * rs.x * mean1);
+                for (int i = 0; i < 4; ++i) dy[i] = fma2(rs1, dx[k][i], mul2(y[i], back));
                 if (row < f.T && v < nv) a.dy[(size_t)row * nv + v] = pack8(dy);
             }
         }
@@ -404,9 +450,9 @@ __global__ void __launch_bounds__(kGnMaxThreads) gated_norm_bwd_kernel(const Gat
         float* o = acc + (size_t)threadIdx.y * f.D + 8 * v;
         const size_t stride = (size_t)blockDim.y * f.D;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            o[i] = dpre[k][i];
-            if (Y) o[stride + i] = sum[k][i];
+        for (int i = 0; i < 4; ++i) {
+            reinterpret_cast<float2*>(o)[i] = dpre[k][i];
+            if (Y) reinterpret_cast<float2*>(o + stride)[i] = sum[k][i];
         }
     }
     __syncthreads();

@@ -139,7 +139,7 @@ def _ptr(t):
 
 
 def _stream(device) -> int:
-    index = device.index if isinstance(device, torch.device) else None
+    index = getattr(device, "index", None)
     if index is None:
         return torch.cuda.current_stream(device).cuda_stream
     return torch._C._cuda_getCurrentRawStream(index)   # the same handle, without building a Stream object
@@ -168,15 +168,15 @@ def _opt(t, name, dtype, device, shape=None):
 
 def _like(t, out, key):
     """An output of t's shape and type (cheaper to allocate than by its shape)."""
-    if out is not None and key in out and out[key] is not None:
-        return _need(out[key], key, t.dtype, t.device, t.shape)
-    return torch.empty_like(t)
+    if out is None or out.get(key) is None:
+        return torch.empty_like(t)
+    return _need(out[key], key, t.dtype, t.device, t.shape)
 
 
 def _empty(shape, dtype, device, out, key):
-    if out is not None and key in out and out[key] is not None:
-        return _need(out[key], key, dtype, device, shape)
-    return torch.empty(shape, dtype=dtype, device=device)
+    if out is None or out.get(key) is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _need(out[key], key, dtype, device, shape)
 
 
 # ---------------------------------------------------------------------------
@@ -637,15 +637,14 @@ def linear_ce_workspace_bytes(T: int, V: int, D: int, grad_fp32: bool = False):
 
 
 def _ce_inputs(h, w, target):
-    dev = h.device
+    dev, shape = h.device, h.shape
     V, D = w.shape
-    T = h.numel() // D if D else 0
-    if h.dim() < 1 or h.shape[-1] != D:
-        raise ValueError(f"h: expected shape (..., {D}), got {tuple(h.shape)}")
+    if not shape or shape[-1] != D:
+        raise ValueError(f"h: expected shape (..., {D}), got {tuple(shape)}")
     _need(h, "h", torch.bfloat16, dev)
     _need(w, "w", torch.bfloat16, dev)
-    _need(target, "target", torch.int64, dev, h.shape[:-1])
-    return dev, T, V, D
+    _need(target, "target", torch.int64, dev, shape[:-1])
+    return dev, target.numel(), V, D
 
 
 def linear_ce_forward(h, w, target, *, softcap=0.0, out=None, scratch=None):
@@ -656,15 +655,18 @@ def linear_ce_forward(h, w, target, *, softcap=0.0, out=None, scratch=None):
     scratch)."""
     dev, T, V, D = _ce_inputs(h, w, target)
     nscratch = linear_ce_workspace_bytes(T, V, D)[0]
-    loss = _empty(target.shape, torch.float32, dev, out, "loss")
-    lse = _empty(target.shape, torch.float32, dev, out, "lse")
+    shape = target.shape
+    loss = _empty(shape, torch.float32, dev, out, "loss")
+    lse = _like(loss, out, "lse")
     total = _empty((2,), torch.float32, dev, out, "total")
     if scratch is None:
         scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    if scratch.numel() < nscratch:
+    elif scratch.numel() < nscratch:
         raise ValueError("scratch buffer is too small")
-    _check("linear_ce_forward", _load().linear_ce_forward(_ptr(h), _ptr(w), _ptr(target), T, V, D, softcap, _ptr(loss),
-                                                          _ptr(lse), _ptr(total), _ptr(scratch), _stream(dev)))
+    st = _load().linear_ce_forward(h.data_ptr(), w.data_ptr(), target.data_ptr(), T, V, D, softcap, loss.data_ptr(),
+                                   lse.data_ptr(), total.data_ptr(), scratch.data_ptr(), _stream(dev))
+    if st:
+        _check("linear_ce_forward", st)
     return {"loss": loss, "lse": lse, "total": total, "scratch": scratch}
 
 
@@ -681,17 +683,20 @@ def linear_ce_backward(h, w, target, lse, dloss=None, *, total=None, softcap=0.0
     if dloss is None and total is None:
         raise ValueError("total is required where dloss is None")
     nscratch = linear_ce_workspace_bytes(T, V, D, grad_fp32)[1]
-    gdt = torch.float32 if grad_fp32 else torch.bfloat16
-    dh = _empty(h.shape, gdt, dev, out, "dh")
-    dw = _empty(w.shape, gdt, dev, out, "dw")
+    if grad_fp32:
+        dh = _empty(h.shape, torch.float32, dev, out, "dh")
+        dw = _empty(w.shape, torch.float32, dev, out, "dw")
+    else:
+        dh, dw = _like(h, out, "dh"), _like(w, out, "dw")
     if scratch is None:
         scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    if scratch.numel() < nscratch:
+    elif scratch.numel() < nscratch:
         raise ValueError("scratch buffer is too small")
-    _check("linear_ce_backward",
-           _load().linear_ce_backward(_ptr(h), _ptr(w), _ptr(target), _ptr(lse), _ptr(dloss), _ptr(total), T, V, D,
-                                      softcap, _ptr(dh), _ptr(dw), LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16,
-                                      _ptr(scratch), _stream(dev)))
+    st = _load().linear_ce_backward(h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(), _ptr(dloss),
+                                    _ptr(total), T, V, D, softcap, dh.data_ptr(), dw.data_ptr(),
+                                    LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16, scratch.data_ptr(), _stream(dev))
+    if st:
+        _check("linear_ce_backward", st)
     return {"dh": dh, "dw": dw, "scratch": scratch}
 
 
@@ -708,15 +713,22 @@ def gated_norm_workspace_bytes(T: int, D: int):
 
 
 def _gated_norm_inputs(x, y, gate, gamma_post, scale, gamma_pre):
-    dev = x.device
-    if x.dim() < 1:
+    dev, shape = x.device, x.shape
+    if not shape:
         raise ValueError("x: expected shape (..., D)")
-    D = x.shape[-1]
+    D = shape[-1]
     _need(x, "x", torch.bfloat16, dev)
-    _opt(y, "y", torch.bfloat16, dev, x.shape)
-    _opt(gate, "gate", torch.bfloat16, dev, x.shape)
-    for t, n in ((gamma_post, "gamma_post"), (scale, "scale"), (gamma_pre, "gamma_pre")):
-        _opt(t, n, torch.float32, dev, (D,))
+    if y is not None:
+        _need(y, "y", torch.bfloat16, dev, shape)
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, dev, shape)
+    vector = (D,)
+    if gamma_post is not None:
+        _need(gamma_post, "gamma_post", torch.float32, dev, vector)
+    if scale is not None:
+        _need(scale, "scale", torch.float32, dev, vector)
+    if gamma_pre is not None:
+        _need(gamma_pre, "gamma_pre", torch.float32, dev, vector)
     return dev, x.numel() // D if D else 0, D
 
 
@@ -732,11 +744,12 @@ def gated_norm_forward(x, y=None, gate=None, gamma_post=None, scale=None, gamma_
     h = _like(x, out, "h")
     if saved is None:
         saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    if saved.numel() < nsaved:
+    elif saved.numel() < nsaved:
         raise ValueError("saved buffer is too small")
-    _check("gated_norm_forward",
-           _load().gated_norm_forward(_ptr(x), _ptr(y), _ptr(gate), _ptr(gamma_post), _ptr(scale), _ptr(gamma_pre), T,
-                                      D, eps, _ptr(r), _ptr(h), _ptr(saved), _stream(dev)))
+    st = _load().gated_norm_forward(x.data_ptr(), _ptr(y), _ptr(gate), _ptr(gamma_post), _ptr(scale), _ptr(gamma_pre),
+                                    T, D, eps, _ptr(r), h.data_ptr(), saved.data_ptr(), _stream(dev))
+    if st:
+        _check("gated_norm_forward", st)
     return {"r": x if y is None else r, "h": h, "saved": saved}
 
 

@@ -477,7 +477,8 @@ int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forwa
  *            counted (16-byte aligned)
  *   scratch  linear_ce_workspace_bytes().forward bytes
  * Products of BF16 values accumulate in FP32 on the tensor cores; sums of
- * exponentials are FP32, the sum of the losses FP64, all in a fixed order.
+ * exponentials are FP32, the sum of the losses is right to its last FP32 bit, all
+ * in a fixed order.
  * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, softcap
  * negative or not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8, T or V
  * over 2^23, D over 2^16), LRS_ERR_CUDA. */

@@ -1179,7 +1179,7 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
         LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, pdl_ok()));
     }
     LRS_LAUNCH(KID_CE_ROWS, stream,
-               launch_ce_rows(g.stats, g.zt, target, parts, T, V, loss, lse, at<double>(scratch, l.sums), total,
+               launch_ce_rows(g.stats, g.zt, target, parts, T, V, loss, lse, at<int4>(scratch, l.sums), total,
                               status + 1, status, stream, pdl_ok()));
     return LRS_OK;
 }

@@ -30,6 +30,7 @@
 #include <cuda_fp8.h>
 
 #include "kernels.cuh"
+#include "twosum.cuh"
 
 namespace lrs {
 
@@ -140,24 +141,9 @@ __device__ __forceinline__ void store_codes(uint8_t* p, long long i, long long n
     }
 }
 
-// A sum in two floats: the rounding of hi is kept in lo by the exact difference
-// (two-sum), so the sum is right to its last FP32 bit without FP64 arithmetic,
-// whose latency here is some tenths of a microsecond an operation.
-struct TwoSum {
-    float hi = 0.f, lo = 0.f;
-    __device__ __forceinline__ void add(float q, float q_lo = 0.f) {
-        const float t = __fadd_rn(hi, q), b = __fsub_rn(t, hi);
-        lo = __fadd_rn(__fadd_rn(lo, q_lo), __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(q, b)));
-        hi = t;
-    }
-    // a sum that overflowed has no difference to add
-    __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
-};
 // Sum over the CTA in a fixed order; the result in every thread.
 __device__ __forceinline__ TwoSum cta_sum(TwoSum v, float2* red) {
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1)
-        v.add(__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o));
+    v = warp_sum(v);
     __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(v.hi, v.lo);
     __syncthreads();

@@ -37,6 +37,7 @@
 
 #include "kernels.cuh"
 #include "tmap.cuh"
+#include "twosum.cuh"
 #include "umma.cuh"
 
 namespace lrs {
@@ -704,6 +705,28 @@ __global__ void __launch_bounds__(256, kCeFewThreads / 256 / (RT == 1 ? 1 : 2)) 
     }
 }
 
+// The sum of the losses (in two floats) and the number of rows counted over a
+// CTA of WARPS warps, in a fixed order; the result in thread 0.
+template <int WARPS>
+__device__ __forceinline__ void ce_cta_total(TwoSum& s, int& n, float2* red, int* red_n) {
+    s = warp_sum(s);
+    n = __reduce_add_sync(0xffffffffu, n);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        red[threadIdx.x >> 5] = make_float2(s.hi, s.lo);
+        red_n[threadIdx.x >> 5] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) return;
+    s = TwoSum();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < WARPS; ++w) {
+        s.add(red[w].x, red[w].y);
+        n += red_n[w];
+    }
+}
+
 // Rows' statistics joined over their `parts` column blocks, in a fixed order:
 // a CTA takes kCeRows consecutive rows, thread (row, group) the parts group,
 // group + kCeGroups, ...; then lse, loss, and the CTA's (sum of losses, number
@@ -713,11 +736,12 @@ template <int ROWS>
 __global__ void __launch_bounds__(256) ce_rows_kernel(const float2* __restrict__ stats, const float* __restrict__ zt,
                                                       const int64_t* __restrict__ target, int parts, int T, int V,
                                                       float* __restrict__ loss, float* __restrict__ lse,
-                                                      double* __restrict__ sums, float* __restrict__ total,
+                                                      int4* __restrict__ sums, float* __restrict__ total,
                                                       uint32_t* ticket, uint32_t* status) {
     constexpr int GROUPS = 256 / ROWS;
     __shared__ float2 red[GROUPS][ROWS];
-    __shared__ double tot[2][8];
+    __shared__ float2 tot[8];
+    __shared__ int tot_n[8];
     __shared__ bool last;
     pdl_trigger();
     pdl_wait();
@@ -747,68 +771,96 @@ __global__ void __launch_bounds__(256) ce_rows_kernel(const float2* __restrict__
         if (g < k) red[g][r] = ce_join(red[g][r], red[g + k][r]);
         __syncthreads();
     }
-    double sl = 0., sc = 0.;
+    TwoSum sum;
+    int n = 0;
     if (g == 0 && t < T) {
         p = red[0][r];
         const float l = p.x + logf(p.y);
         const long long tg = target[t];
         const bool counted = tg >= 0 && tg < V;
         if (tg >= V) atomicOr(status, kStatusTarget);
-        const float ls = counted ? l - __ldcg(zt + t) : 0.f;
+        sum.hi = counted ? l - __ldcg(zt + t) : 0.f;
+        n = counted ? 1 : 0;
         lse[t] = l;
-        loss[t] = ls;
-        sl = ls;
-        sc = counted ? 1. : 0.;
+        loss[t] = sum.hi;
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        sl += __shfl_xor_sync(0xffffffffu, sl, o);
-        sc += __shfl_xor_sync(0xffffffffu, sc, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-        tot[0][threadIdx.x >> 5] = sl;
-        tot[1][threadIdx.x >> 5] = sc;
-    }
-    __syncthreads();
+    ce_cta_total<8>(sum, n, tot, tot_n);
     if (threadIdx.x == 0) {
-        sl = sc = 0.;
-        for (int i = 0; i < 8; ++i) {
-            sl += tot[0][i];
-            sc += tot[1][i];
-        }
-        sums[2 * blockIdx.x] = sl;
-        sums[2 * blockIdx.x + 1] = sc;
+        sums[blockIdx.x] = make_int4(__float_as_int(sum.hi), __float_as_int(sum.lo), n, 0);
         __threadfence();
         last = atomicAdd(ticket, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
     __threadfence();
-    sl = sc = 0.;
+    sum = TwoSum();
+    n = 0;
     for (int i = threadIdx.x; i < (int)gridDim.x; i += 256) {
-        sl += __ldcg(sums + 2 * i);
-        sc += __ldcg(sums + 2 * i + 1);
+        const int4 q = __ldcg(sums + i);
+        sum.add(__int_as_float(q.x), __int_as_float(q.y));
+        n += q.z;
     }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-        sl += __shfl_xor_sync(0xffffffffu, sl, o);
-        sc += __shfl_xor_sync(0xffffffffu, sc, o);
-    }
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        tot[0][threadIdx.x >> 5] = sl;
-        tot[1][threadIdx.x >> 5] = sc;
-    }
-    __syncthreads();
+    ce_cta_total<8>(sum, n, tot, tot_n);
     if (threadIdx.x == 0) {
-        sl = sc = 0.;
-        for (int i = 0; i < 8; ++i) {
-            sl += tot[0][i];
-            sc += tot[1][i];
-        }
-        total[0] = (float)sl;
-        total[1] = (float)sc;
+        total[0] = sum.value();
+        total[1] = (float)n;
         *ticket = 0u;
+    }
+}
+
+// The same for few rows and parts (T <= 256, T parts <= kCeRowsSmall) in one
+// CTA: no ticket, fence and second look at the sums (with the statistics, 20
+// tokens x 500 entries at D 128 13.0 -> 10.5 us, 8.3 without FP64 in the sums;
+// from about 8000 rows x parts on, more CTAs are faster).  Thread (row, group)
+// as above, a power of two of rows.
+constexpr int kCeRowsSmall = 4096;
+__global__ void __launch_bounds__(1024) ce_rows_small_kernel(const float2* __restrict__ stats,
+                                                             const float* __restrict__ zt,
+                                                             const int64_t* __restrict__ target, int parts, int T,
+                                                             int rows, int V, float* __restrict__ loss,
+                                                             float* __restrict__ lse, float* __restrict__ total,
+                                                             uint32_t* status) {
+    __shared__ float2 red[1024];
+    __shared__ float2 tot[8];
+    __shared__ int tot_n[8];
+    const int t = threadIdx.x & (rows - 1), g = threadIdx.x / rows, groups = 1024 / rows;
+    pdl_trigger();
+    pdl_wait();
+    const long long tg = g == 0 && t < T ? target[t] : -1;
+    const bool counted = tg >= 0 && tg < V;
+    float2 p = make_float2(-INFINITY, 0.f);
+    if (t < T)
+        for (int i = g; i < parts; i += groups) p = ce_join(p, __ldcg(stats + (size_t)i * T + t));
+    const float zt_t = counted ? __ldcg(zt + t) : 0.f;
+    // the groups of a row inside a warp, then over the warps
+    for (int o = rows; o < 32; o <<= 1) {
+        const float2 q = make_float2(__shfl_xor_sync(0xffffffffu, p.x, o), __shfl_xor_sync(0xffffffffu, p.y, o));
+        p = threadIdx.x & o ? ce_join(q, p) : ce_join(p, q);   // the same order in both lanes
+    }
+    red[threadIdx.x] = p;
+    __syncthreads();
+    TwoSum sum;
+    int n = 0;
+    if (g == 0 && t < T) {
+        const int step = rows < 32 ? 32 : rows;
+        for (int i = t + step; i < 1024; i += step) p = ce_join(p, red[i]);
+        const float l = p.x + logf(p.y);
+        if (tg >= V) atomicOr(status, kStatusTarget);
+        sum.hi = counted ? l - zt_t : 0.f;
+        n = counted ? 1 : 0;
+        lse[t] = l;
+        loss[t] = sum.hi;
+    }
+    // the rows are in the first eight warps
+    if (threadIdx.x >= 256) {
+        __syncthreads();
+        __syncthreads();
+        return;
+    }
+    ce_cta_total<8>(sum, n, tot, tot_n);
+    if (threadIdx.x == 0) {
+        total[0] = sum.value();
+        total[1] = (float)n;
     }
 }
 
@@ -979,9 +1031,9 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
 }
 
 // The statistics of T <= 4 tokens, one part a CTA.  Against 32768 x 1024 (67 MB
-// of w not in the L2, forward with its second kernel) 1, 2 and 4 tokens take 21,
-// 22 and 26 us, 29 by the tensor-core tiles, which from 6 on are faster (30
-// against 34 us).
+// of w not in the L2, forward with its second kernel) 1, 2 and 4 tokens took 21,
+// 22 and 26 us, 29 by the tensor-core tiles, which from 6 on were faster (30
+// against 34 us); the second kernel has since got 3 us shorter for both.
 bool ce_is_few(int T, int D) { return T <= 4 && (long long)T * D * 2 <= 48 * 1024; }
 int ce_few_parts(int T, int sms) { return kCeFewThreads / 256 / (T == 1 ? 1 : 2) * sms; }
 cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl) {
@@ -1024,8 +1076,14 @@ int ce_rows_per_cta(int T) { return T <= 256 ? 1 : T <= 8192 ? 8 : 32; }
 int ce_row_ctas(int T) { return (T + ce_rows_per_cta(T) - 1) / ce_rows_per_cta(T); }
 
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
-                           float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
+                           float* loss, float* lse, int4* sums, float* total, uint32_t* ticket, uint32_t* status,
                            cudaStream_t s, bool pdl) {
+    if (T <= 256 && (long long)T * parts <= kCeRowsSmall) {
+        int pow2 = 1;
+        while (pow2 < T) pow2 <<= 1;
+        return launch_ex(ce_rows_small_kernel, dim3(1), dim3(1024), 0, s, pdl, stats, zt, target, parts, T, pow2, V, loss,
+                         lse, total, status);
+    }
     const int rows = ce_rows_per_cta(T);
     auto* fn = rows == 1 ? ce_rows_kernel<1> : rows == 8 ? ce_rows_kernel<8> : ce_rows_kernel<32>;
     return launch_ex(fn, dim3((unsigned)ce_row_ctas(T)), dim3(256), 0, s, pdl, stats, zt, target, parts, T, V, loss, lse,

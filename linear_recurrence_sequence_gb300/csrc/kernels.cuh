@@ -580,7 +580,7 @@ cudaError_t launch_ce_grads(const CeGemmArgs& a, const void* dz, const void* dz2
                             const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl);
 int ce_row_ctas(int T);
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
-                           float* loss, float* lse, double* sums, float* total, uint32_t* ticket, uint32_t* status,
+                           float* loss, float* lse, int4* sums, float* total, uint32_t* ticket, uint32_t* status,
                            cudaStream_t s, bool pdl);
 cudaError_t launch_ce_sum(const float* part, long long stride, int parts, long long n, void* out, bool f32,
                           cudaStream_t s, bool pdl);

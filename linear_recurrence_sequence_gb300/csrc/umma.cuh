@@ -266,4 +266,13 @@ __device__ __forceinline__ void tma2_load_3d(void* dst, const CUtensorMap* map, 
         : "memory");
 }
 
+// 3-D tiled reduction (addition of FP32 values) of one box from shared memory
+// into global memory, with tma_store_3d's rules.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
+    asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
+}
+
 }  // namespace lrs

@@ -140,7 +140,7 @@ __device__ __forceinline__ void ce_columns(uint32_t taddr, float (&v)[2][16]) {
     tmem_ld16x2(taddr, taddr + 16u, v[0], v[1]);
 }
 
-// The capped logit and its slope: z' = c tanh(z / c), dz'/dz = 1 - (z'/c)^2.
+// The capped logit, z' = c tanh(z / c); its slope dz'/dz is 1 - (z'/c)^2.
 __device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a.softcap * tanhf(z * a.inv_softcap); }
 
 // tanh(x / c) of 32 logits in place (c the cap).  Where the whole warp's |x / c|
@@ -441,12 +441,13 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         const int row = 32 * q4 + lane;
         uint8_t* stg = ring + (size_t)S * kCeStageBytes + (size_t)warp * ce_stage_warp(EPI);
         uint32_t use = 0;   // accumulators drained
+        // (a warp gives up as a whole: its loads and stores are instructions of all lanes)
         // the common factor of the tokens' weights: left out of dz, put on its products
         float common = 1.f;
         if (EPI != kCeStats && a.weights != nullptr) common = ce_largest_weight(a, &s_weight);
         if ((EPI == kCeDz || EPI == kCeDz2) && a.rows_out != nullptr) ce_rows_of_h(a, warp, lane);
         if (GRADS && a.total != nullptr && a.total[1] > 0.f) common = 1.f / a.total[1];
-        for (int k = 0; !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k, ++use) {
+        for (int k = 0; !__any_sync(0xffffffffu, *abort_flag) && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k, ++use) {
             const CeSide& c0 = a.c[it.side];
             const uint32_t buf = use & 1u;
             if (CHAINS) {
@@ -457,7 +458,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 bool lost = false;
                 for (int k0 = it.k0; k0 < it.k1; k0 += kCeChain, ++use) {
                     const uint32_t b = use & 1u;
-                    if (!mbar_wait_bounded(&s_acc[b], (use >> 1) & 1u)) {
+                    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_acc[b], (use >> 1) & 1u))) {
                         lost = true;
                         break;
                     }
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     lse2 = a.lse[t] * kLog2e;
                 }
             }
-            if (!mbar_wait_bounded(&s_acc[buf], (use >> 1) & 1u)) {
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_acc[buf], (use >> 1) & 1u))) {
                 if (lane == 0) fail();
                 break;
             }

@@ -242,6 +242,59 @@ def test_new_gradients_and_a_captured_graph():
         _check(ts2, exp, before)
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_past_32_bits(bits):
+    """A tensor of more than 2^31 values: its end is updated like a tensor of its own."""
+    n, tail = (1 << 31) + 5000, 4096 + 905
+    start = n - tail
+    gen = torch.Generator().manual_seed(13)
+
+    def placed(values, dtype):
+        t = torch.zeros(n, dtype=dtype, device=DEV)
+        t[start:] = values.to(DEV)
+        return t
+
+    p = torch.randn(tail, generator=gen) * 0.05
+    big = {"param": placed(p, torch.bfloat16), "master": placed(p, torch.float32), "weight_decay": 0.1,
+           "grad": placed(torch.randn(tail, generator=gen) * 1e-2, torch.float32)}
+    for k, a in (("m", torch.randn(tail, generator=gen) * 1e-2), ("v", torch.rand(tail, generator=gen) * 1e-2)):
+        if bits == 32:
+            big[k] = placed(a if k == "m" else a * a, torch.float32)
+            continue
+        blocks, at = -(-n // 256), start // 256 * 256
+        pad = torch.zeros(blocks * 256 - at)
+        pad[start - at:n - at] = a
+        s = pad.view(-1, 256).abs().amax(1) / 448
+        codes = (pad.view(-1, 256) / s[:, None]).to(torch.float8_e4m3fn).view(-1)
+        big[k] = torch.zeros(n, dtype=torch.uint8, device=DEV).view(torch.float8_e4m3fn)
+        big[k].view(torch.uint8)[at:] = codes.view(torch.uint8)[:n - at].to(DEV)
+        big[k + "_scale"] = torch.zeros(blocks, device=DEV)
+        big[k + "_scale"][at // 256:] = s.to(DEV)
+
+    def moments():
+        if bits == 32:
+            return big["m"][start:].double(), big["v"][start:].double()
+        at = start // 256
+        sp = [big[k + "_scale"][at:].double().repeat_interleave(256)[start % 256:start % 256 + tail] for k in ("m", "v")]
+        return big["m"][start:].float().double() * sp[0], (big["v"][start:].float().double() * sp[1]) ** 2
+
+    step, lr = _scalars(2)
+    p0, g0 = big["master"][start:].double(), big["grad"][start:].double()
+    m0, v0 = moments()
+    norm = float(g0.square().sum()) ** 0.5
+    o = api.adamw_step(api.adamw_plan([big]), step, lr, beta1=B1, beta2=B2, eps=EPS, max_norm=1e9)
+    assert abs(float(o["norm"]) - norm) <= 2.0 ** -18 * norm
+    m1, v1 = B1 * m0 + (1 - B1) * g0, B2 * v0 + (1 - B2) * g0 * g0
+    ref = p0 * (1 - float(lr) * big["weight_decay"]) - \
+        float(lr) * m1 / (1 - B1 ** 3) / (torch.sqrt(v1 / (1 - B2 ** 3)) + EPS)
+    ma = B1 * m0.abs() + (1 - B1) * g0.abs()
+    most = 2.0 ** -23 * (p0.abs() + ref.abs()) + \
+        2.0 ** -17 * float(lr) * ma / (1 - B1 ** 3) / (torch.sqrt(v1 / (1 - B2 ** 3)) + EPS)
+    assert float(((big["master"][start:].double() - ref).abs() - most).max()) <= 0
+    assert not big["master"][:1 << 20].any() and not big["m"].view(torch.uint8)[:1 << 20].any()
+    assert torch.equal(big["param"][start:], big["master"][start:].to(torch.bfloat16))
+
+
 def test_repeats_bit_for_bit_on_another_stream():
     results = []
     for side in (torch.cuda.current_stream(), torch.cuda.Stream()):

@@ -169,6 +169,30 @@ def test_gradient_against_differences():
             assert abs(diff - float(b[d].view(-1)[e])) <= 2.0 ** -7 * max(rms, abs(diff)), (k, e)
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 values: the last rows of a large call agree with a call on them alone."""
+    T, D = (1 << 31) // 2048 + 40, 2048
+    i, dr, dh = _inputs(64, D, 10)
+    big = {}
+    for k in ("x", "y", "gate"):
+        big[k] = torch.zeros(T, D, dtype=torch.bfloat16, device=DEV)
+        big[k][-64:] = i[k]
+    bdr, bdh = torch.zeros_like(big["x"]), torch.zeros_like(big["x"])
+    bdr[-64:], bdh[-64:] = dr, dh
+    vectors = [i[k] for k in ("gamma_post", "scale", "gamma_pre")]
+    f = api.gated_norm_forward(big["x"], big["y"], big["gate"], *vectors)
+    b = api.gated_norm_backward(bdr, bdh, big["x"], big["y"], big["gate"], *vectors, f["saved"])
+    g = api.gated_norm_forward(**i)
+    c = api.gated_norm_backward(dr, dh, *i.values(), g["saved"])
+    for k in ("r", "h"):
+        assert torch.equal(f[k][-64:], g[k]) and not f[k][:-64].any()
+    for k in ("dx", "dy", "dgate"):
+        assert torch.equal(b[k][-64:], c[k]) and not b[k][:1 << 10].any()
+    out, sums = _definition(i, dr, dh)
+    for k, (ref, most) in sums.items():   # rows of zeros add nothing
+        assert float(((b[k].double() - ref).abs() - 2.0 ** -15 * most).max()) <= 0, k
+
+
 def test_repeats_bit_for_bit_on_another_stream():
     i, dr, dh = _inputs(3000, 1024, 8)
     f, b = _check(i, dr, dh)

@@ -227,6 +227,35 @@ def test_gradient_against_differences():
             assert abs(diff - float(g.view(-1)[i])) <= 1e-4 * max(rms, abs(diff))
 
 
+def test_offsets_past_32_bits():
+    """w and dw of more than 2^31 values: the loss knows the last rows, and dw has them."""
+    D, V = 2048, (1 << 31) // 2048 + 300
+    T = 12
+    gen = torch.Generator().manual_seed(20)
+    h = torch.randn(T, D, generator=gen).to(torch.bfloat16).to(DEV)
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device=DEV)
+    tail = (torch.randn(300, D, generator=gen) * (4.0 / D ** 0.5)).to(torch.bfloat16).to(DEV)
+    w[-300:] = tail
+    t = (V - 300 + torch.randint(0, 300, (T,), generator=gen)).to(DEV)
+    f = api.linear_ce_forward(h, w, t)
+    b = api.linear_ce_backward(h, w, t, f["lse"], total=f["total"])
+    # in 64 bits: V - 300 logits of zero beside the 300
+    z = h.double() @ tail.double().T
+    lse = torch.log(torch.exp(z).sum(1) + (V - 300))
+    at = t - (V - 300)
+    rows = torch.arange(T, device=DEV)
+    np.testing.assert_allclose(_f64(f["lse"]), _f64(lse), rtol=0, atol=TOL_ROW)
+    np.testing.assert_allclose(_f64(f["loss"]), _f64(lse - z[rows, at]), rtol=0, atol=TOL_ROW)
+    p = torch.exp(z - lse[:, None])
+    p[rows, at] -= 1
+    dz = p / T
+    assert _rel(_f64(b["dh"]), _f64(dz @ tail.double())) <= 2.0 ** -8
+    assert _rel(_f64(b["dw"][-300:]), _f64(dz.T @ h.double())) <= 2.0 ** -8
+    rest = (torch.exp(-lse)[:, None] / T * h.double()).sum(0)   # every other row's gradient is the same
+    for k in (0, 1 << 19, V - 301):
+        assert _rel(_f64(b["dw"][k]), _f64(rest)) <= 2.0 ** -7
+
+
 def test_repeats_bit_for_bit_on_another_stream():
     h, w, t = _inputs(400, 3001, 264, 16, ignored=0.1)
     f, b = _check(h, w, t, fp32=True)

@@ -22,7 +22,7 @@
 // BF16 parameter and its FP32 master (562M values: the update 2.44 ms, 6.9 TB/s;
 // the norm's pass over the gradients 0.34 ms, 6.6 TB/s), 16 with 8-bit states and
 // BF16 gradients (317M values: 0.88 ms, 5.7 TB/s, as much held by the
-// conversions and roots as by memory; the norm 0.12 ms).  A warp takes 256
+// conversions and roots as by memory; the norm 0.13 ms).  A warp takes 256
 // consecutive values (an 8-bit block), a lane four and four, so that every array
 // is read and written in whole 128-byte lines, and issues every load first.
 #include <algorithm>
@@ -193,7 +193,10 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     }
     // groups of chunks, the CTAs in turns (runs of their own leave each CTA
     // streaming from a far place of its own, which is slower)
-    constexpr int kUnroll = 4;
+    // eight loads in flight a thread (317M BF16 gradients: 4 loads 148 us, 8 loads
+    // 126; 562M FP32 ones 358 and 340); their squares enter the pair of floats in two parts of four, so that
+    // the plain FP32 sums stay short
+    constexpr int kUnroll = 8;
     const int chunks = l.first[l.count];
     TwoSum sum;
     for (int c0 = (int)blockIdx.x * a.norm_group; c0 < chunks; c0 += ctas * a.norm_group) {
@@ -212,10 +215,13 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
                 uint4 x[kUnroll];
 #pragma unroll
                 for (int k = 0; k < kUnroll; ++k) x[k] = __ldg(g + v + k * kAdamThreads);
-                float q = 0.f;
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k) squares(x[k], bf, q);
-                sum.add(q);
+                for (int h = 0; h < kUnroll; h += 4) {
+                    float q = 0.f;
+#pragma unroll
+                    for (int k = h; k < h + 4; ++k) squares(x[k], bf, q);
+                    sum.add(q);
+                }
             }
             for (; v < nv; v += kAdamThreads) {
                 float q = 0.f;

@@ -68,6 +68,8 @@ constexpr size_t ce_smem(int epi) {
 }
 
 constexpr int kCeFewThreads = 1024;   // per SM, of the kernel for one token (half of it for more)
+// The rows of h that it keeps: up to four CTAs of this and their own 1 KB fit an SM.
+constexpr size_t kCeFewSmem = 48 * 1024;
 // Stages that one accumulator adds up where the results are FP32: the tensor
 // cores' sums lose about 2e-8 of their value a step of 16 (they truncate), 6e-5
 // over 50021 vocabulary entries in two parts; 16 stages are 128 steps.
@@ -1046,11 +1048,23 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
 // of w not in the L2, forward with its second kernel) 1, 2 and 4 tokens took 21,
 // 22 and 26 us, 29 by the tensor-core tiles, which from 6 on were faster (30
 // against 34 us); the second kernel has since got 3 us shorter for both.
-bool ce_is_few(int T, int D) { return T <= 4 && (long long)T * D * 2 <= 48 * 1024; }
+bool ce_is_few(int T, int D) { return T <= 4 && (size_t)T * D * 2 <= kCeFewSmem; }
 int ce_few_parts(int T, int sms) { return kCeFewThreads / 256 / (T == 1 ? 1 : 2) * sms; }
 cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl) {
     const int T = a.c[0].M, D = a.c[0].K;
-    auto* fn = T == 1 ? ce_few_kernel<1, 8> : T == 2 ? ce_few_kernel<2, 8> : ce_few_kernel<4, 4>;
+    const int kind = T == 1 ? 0 : T == 2 ? 1 : 2;
+    auto* fn = kind == 0 ? ce_few_kernel<1, 8> : kind == 1 ? ce_few_kernel<2, 8> : ce_few_kernel<4, 4>;
+    // with the kernel's own arrays this may pass the 48 KB that need no leave; asked for once per device
+    static std::atomic<bool> allowed[3][64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool keep = dev >= 0 && dev < 64;
+    if (!keep || !allowed[kind][dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kCeFewSmem);
+        if (e != cudaSuccess) return e;
+        if (keep) allowed[kind][dev].store(true, std::memory_order_release);
+    }
     const size_t smem = (size_t)T * D * 2;
     return launch_ex(fn, dim3((unsigned)ce_few_parts(T, block_gemm_sms())), dim3(256), smem, s, pdl,
                      static_cast<const uint4*>(h), static_cast<const uint4*>(w), T, a);

@@ -312,3 +312,18 @@ def test_leading_shape_and_refusals():
     with pytest.raises(api.LrsError) as e:
         api.linear_ce_forward(h[:, :12].contiguous(), w[:, :12].contiguous(), t)
     assert e.value.status == 2
+
+
+@pytest.mark.parametrize("T,D", [(1, 24320), (1, 24328), (1, 24576), (1, 24584), (2, 12032), (2, 12040), (2, 12288),
+                                 (2, 12296), (3, 8016), (3, 8024), (3, 8192), (3, 8200), (4, 6016), (4, 6024),
+                                 (4, 6144), (4, 6152)])
+def test_few_tokens_of_wide_models(T, D):
+    """Either side of where a few tokens' rows of h stop fitting in shared memory (the inputs' sum of absolute terms
+    stays below 2^7 at a quarter of the weights' spread elsewhere)."""
+    _check(*_inputs(T, 300, D, seed=T + D, std=0.25))
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
+def test_few_capped_tokens(T, fp32):
+    _check(*_inputs(T, 4099, 64, seed=30 + T, std=4.0), softcap=5.0, fp32=fp32)

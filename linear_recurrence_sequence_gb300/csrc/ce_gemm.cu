@@ -145,11 +145,26 @@ __device__ __forceinline__ void ce_columns(uint32_t taddr, float (&v)[2][16]) {
 // The capped logit, z' = c tanh(z / c); its slope dz'/dz is 1 - (z'/c)^2.
 __device__ __forceinline__ float ce_cap(const CeGemmArgs& a, float z) { return a.softcap * tanhf(z * a.inv_softcap); }
 
-// tanh(x / c) of 32 logits in place (c the cap).  Where the whole warp's |x / c|
-// are at most 0.4, as logits mostly are, by the first seven terms of tanh's
-// Taylor series (the eighth is below 4e-9 of the value there): 9 operations
-// where tanhf takes about 25, which held the capped epilogues back (2048 tokens
-// x 50021 entries at D 1024: statistics 163 -> 145 us, dz in two parts 199 -> 169).
+// tanh(x) for |x| <= kCeSeries: the first seven terms of its Taylor series (the
+// eighth is below 4e-9 of the value there).
+constexpr float kCeSeries = 0.4f;
+__device__ __forceinline__ float ce_tanh_small(float x) {
+    const float x2 = x * x;
+    float p = fmaf(x2, 21844.f / 6081075.f, -1382.f / 155925.f);
+    p = fmaf(p, x2, 62.f / 2835.f);
+    p = fmaf(p, x2, -17.f / 315.f);
+    p = fmaf(p, x2, 2.f / 15.f);
+    p = fmaf(p, x2, -1.f / 3.f);
+    return fmaf(p * x2, x, x);
+}
+// tanh(x / c) of 32 logits in place (c the cap): the series, 9 operations, where
+// |x / c| is small, as logits mostly are, tanhf's about 25, which held the capped
+// epilogues back, for the others.  Each element goes by its own size alone, so
+// that no result depends on its neighbours in the warp (rows past the matrix among
+// them, whose accumulators hold anything); the warp decides together only whether
+// any element needs tanhf (2048 tokens x 50021 entries at D 1024, cap 30, the
+// statistics and dz in two parts: 145 and 168 us with logits of deviation 2.5, 163
+// and 199 by tanhf alone; 200 and 262 with deviation 10, where most warps form both).
 __device__ __forceinline__ void ce_tanh(const CeGemmArgs& a, float (&v)[2][16]) {
     float top = 0.f;
 #pragma unroll
@@ -157,21 +172,16 @@ __device__ __forceinline__ void ce_tanh(const CeGemmArgs& a, float (&v)[2][16]) 
         v[j / 16][j % 16] *= a.inv_softcap;
         top = fmaxf(top, fabsf(v[j / 16][j % 16]));
     }
-    // (a NaN among the logits is not seen by the maximum, and stays one in the series)
-    if (__any_sync(0xffffffffu, top > 0.4f)) {
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = tanhf(v[j / 16][j % 16]);
-    } else {
+    // (a NaN among the logits is not seen by the maximum, and stays one either way)
+    if (__any_sync(0xffffffffu, top > kCeSeries)) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-            const float x = v[j / 16][j % 16], x2 = x * x;
-            float p = fmaf(x2, 21844.f / 6081075.f, -1382.f / 155925.f);
-            p = fmaf(p, x2, 62.f / 2835.f);
-            p = fmaf(p, x2, -17.f / 315.f);
-            p = fmaf(p, x2, 2.f / 15.f);
-            p = fmaf(p, x2, -1.f / 3.f);
-            v[j / 16][j % 16] = fmaf(p * x2, x, x);
+            const float x = v[j / 16][j % 16], far = tanhf(x);
+            v[j / 16][j % 16] = fabsf(x) <= kCeSeries ? ce_tanh_small(x) : far;
         }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = ce_tanh_small(v[j / 16][j % 16]);
     }
 }
 

@@ -327,3 +327,54 @@ def test_few_tokens_of_wide_models(T, D):
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5])
 def test_few_capped_tokens(T, fp32):
     _check(*_inputs(T, 4099, 64, seed=30 + T, std=4.0), softcap=5.0, fp32=fp32)
+
+
+def _leave_in_shared_memory(value):
+    """Fills every SM's operand slots with a value: what a later launch finds where it has not written."""
+    h = torch.full((256, 1024), value, dtype=torch.bfloat16, device=DEV)
+    w = torch.full((40000, 1024), value, dtype=torch.bfloat16, device=DEV)
+    api.linear_ce_forward(h, w, torch.zeros(256, dtype=torch.int64, device=DEV))
+
+
+@pytest.mark.parametrize("T", [5, 20, 40, 60, 70, 100, 120, 333])
+def test_capped_results_do_not_depend_on_what_ran_before(T):
+    h, w, t = _inputs(T, 1000, 256, 40 + T, ignored=0.1 if T > 8 else 0.0)
+    results = []
+    for value in (0.0, 3e4, -3e4):
+        _leave_in_shared_memory(value)
+        f = api.linear_ce_forward(h, w, t, softcap=30.0)
+        _leave_in_shared_memory(value)
+        b = [api.linear_ce_backward(h, w, t, f["lse"], total=f["total"], softcap=30.0, grad_fp32=k) for k in (False, True)]
+        results.append([f["loss"], f["lse"], f["total"]] + [x[k] for x in b for k in ("dh", "dw")])
+    for r in results[1:]:
+        assert all(torch.equal(x, y) for x, y in zip(results[0], r))
+
+
+def test_capped_rows_do_not_depend_on_their_neighbours():
+    """Rows whose logits reach the cap leave the other rows as they are, bit for bit."""
+    h, w, t = _inputs(96, 700, 136, 50)
+    big = h.clone()
+    big[::2] *= 64
+    dloss = torch.full((96,), 0.01, device=DEV)
+    for fp32 in (False, True):
+        got = []
+        for x in (h, big):
+            f = api.linear_ce_forward(x, w, t, softcap=30.0)
+            b = api.linear_ce_backward(x, w, t, f["lse"], dloss, softcap=30.0, grad_fp32=fp32)
+            got.append([f["loss"], f["lse"], b["dh"]])
+        assert all(torch.equal(x[1::2], y[1::2]) for x, y in zip(*got))
+    _check(big, w, t, softcap=30.0)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_capped_rows_that_do_not_count_may_hold_anything(fp32):
+    h, w, t = _inputs(150, 600, 64, 51)
+    t[::3] = -1
+    bad = h.clone()
+    bad[0], bad[3], bad[6], bad[147] = float("nan"), float("inf"), 1e4, float("-inf")
+    got = []
+    for x in (h, bad):
+        f = api.linear_ce_forward(x, w, t, softcap=30.0)
+        b = api.linear_ce_backward(x, w, t, f["lse"], total=f["total"], softcap=30.0, grad_fp32=fp32)
+        got.append([f["loss"][t >= 0], f["total"], b["dh"], b["dw"]])
+    assert all(torch.equal(x, y) for x, y in zip(*got))

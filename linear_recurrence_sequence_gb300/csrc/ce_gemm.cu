@@ -256,20 +256,25 @@ __device__ __forceinline__ void ce_store_f32(const CUtensorMap& map, const CeSid
     }
 }
 
-// The largest |dloss| of the tokens counted: dz is rounded to BF16 relative to
-// it, so that equal weights, whatever they are, are not rounded at all (one
-// rounding for all tokens would be an error of the whole gradient).  Every CTA's
+// The largest finite |dloss| of the tokens counted (1 where none is above 0): dz
+// is rounded to BF16 relative to it, so that equal weights, whatever they are, are
+// not rounded at all (one rounding for all tokens would be an error of the whole
+// gradient).  A weight that is not finite stays in its own row of dz.  Every CTA's
 // epilogue warps find it for themselves, under the first tile's products.
 __device__ __forceinline__ float ce_largest_weight(const CeGemmArgs& a, uint32_t* s_weight) {
     uint32_t m = 0u;
     for (int t = threadIdx.x; t < a.T; t += 32 * kCeEpiWarps) {
         const long long tg = __ldg(reinterpret_cast<const long long*>(a.target) + t);
-        if (tg >= 0 && tg < a.V) m = max(m, __float_as_uint(fabsf(__ldg(a.weights + t))));
+        if (tg >= 0 && tg < a.V) {
+            const uint32_t w = __float_as_uint(fabsf(__ldg(a.weights + t)));
+            if (w < 0x7f800000u) m = max(m, w);
+        }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) atomicMax(s_weight, m);
     asm volatile("bar.sync 1, %0;" ::"n"(32 * kCeEpiWarps) : "memory");
-    return __uint_as_float(*reinterpret_cast<volatile uint32_t*>(s_weight));
+    m = *reinterpret_cast<volatile uint32_t*>(s_weight);
+    return m != 0u ? __uint_as_float(m) : 1.f;
 }
 // w / largest, exactly 1 where they are equal.
 __device__ __forceinline__ float ce_ratio(float w, float largest) { return w != 0.f ? __fdiv_rn(w, largest) : 0.f; }

@@ -378,3 +378,38 @@ def test_capped_rows_that_do_not_count_may_hold_anything(fp32):
         b = api.linear_ce_backward(x, w, t, f["lse"], total=f["total"], softcap=30.0, grad_fp32=fp32)
         got.append([f["loss"][t >= 0], f["total"], b["dh"], b["dw"]])
     assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("T,V,D", [(3, 257, 72), (200, 1111, 136)])
+def test_weights_of_either_sign(T, V, D, fp32):
+    h, w, t = _inputs(T, V, D, 60, ignored=0.2 if T > 8 else 0.0)
+    _check(h, w, t, dloss=torch.randn(T, generator=torch.Generator().manual_seed(61)).to(DEV) / T, fp32=fp32)
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_a_weight_that_is_not_finite_stays_in_its_row(bad, fp32):
+    """dh of the other tokens is what it is without that token; dw, a sum over all of them, has no finite value."""
+    h, w, t = _inputs(150, 600, 64, 62)
+    t[5] = -1
+    dloss = torch.rand(150, generator=torch.Generator().manual_seed(63)).to(DEV) / 150
+    f = api.linear_ce_forward(h, w, t)
+    dloss[17] = 0.0
+    clean = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=fp32)
+    dloss[17] = bad
+    got = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=fp32)
+    rest = torch.arange(150, device=DEV) != 17
+    assert torch.equal(got["dh"][rest], clean["dh"][rest])
+    assert not torch.isfinite(got["dh"][17]).any() and not torch.isfinite(got["dw"]).any()
+    # where no weight but that one is other than zero
+    dloss.zero_()
+    dloss[17] = bad
+    got = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=fp32)
+    assert not got["dh"][rest].any() and not torch.isfinite(got["dh"][17]).any()
+    # of a token that is not counted it reaches nothing
+    dloss.fill_(0.01)
+    clean = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=fp32)
+    dloss[5] = bad
+    got = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=fp32)
+    assert torch.equal(got["dh"], clean["dh"]) and torch.equal(got["dw"], clean["dw"])

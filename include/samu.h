@@ -22,7 +22,8 @@
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - All tensor pointers are DEVICE pointers (cudaMalloc / torch CUDA
- *    storage), row-major, contiguous, at least 16-byte aligned.
+ *    storage), row-major, contiguous, at least 16-byte aligned unless an entry
+ *    says less.
  *  - Shapes: B batch, L sequence length, D real state width, M = D / 2 complex
  *    modes.  [B,L,D] tensors put the real part of mode m in channel m and its
  *    imaginary part in channel M + m ("halves" layout).
@@ -470,7 +471,8 @@ int lrs_dense_gemm(int layout, const void* A, const void* Bm, void* C, int M, in
 int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forward_bytes, size_t* backward_bytes);
 
 /* Forward.
- *   h        [T,D] BF16 (in);  w [V,D] BF16 (in);  target [T] int64 (in)
+ *   h        [T,D] BF16 (in);  w [V,D] BF16 (in)
+ *   target   [T] int64 (in; 8-byte aligned: the tokens from the second on will do)
  *   softcap  0 for none
  *   loss     [T] FP32 (out);  lse [T] FP32 (out, the backward's input)
  *   total    two FP32 (out): the sum of the losses and the number of tokens
@@ -489,7 +491,8 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
  *   dz'_tv = dloss_t (e^{z'_tv - lse_t} - [v = target_t]),  dz = dz' (1 - (z'/c)^2),
  *   dh = dz w,  dw = dz^T h,
  * with the logits formed again, one piece of the vocabulary at a time.
- *   h, w, target, T, V, D, softcap: the forward's (in);  lse [T] FP32 (in)
+ *   h, w, target, T, V, D, softcap: the forward's (in)
+ *   lse      [T] FP32 (in; 4-byte aligned, as total here)
  *   dloss    [T] FP32 (in), or NULL for the mean over the tokens counted
  *            (1 / total[1] each; total is the forward's and may be NULL only
  *            if dloss is given)

@@ -682,6 +682,8 @@ def linear_ce_backward(h, w, target, lse, dloss=None, *, total=None, softcap=0.0
     _opt(total, "total", torch.float32, dev, (2,))
     if dloss is None and total is None:
         raise ValueError("total is required where dloss is None")
+    if dloss is not None and dloss.data_ptr() % 16:
+        dloss = dloss.clone()   # a view such as weights[1:]; the entry takes 16-byte alignment
     nscratch = linear_ce_workspace_bytes(T, V, D, grad_fp32)[1]
     if grad_fp32:
         dh = _empty(h.shape, torch.float32, dev, out, "dh")

@@ -44,6 +44,9 @@ int check_rglru_shape(int B, int L, int D) {
 bool req(const void* p) { return p != nullptr && aligned16(p); }
 // Optional pointer: null, or 16-byte aligned.
 bool opt(const void* p) { return p == nullptr || aligned16(p); }
+// Required pointer to values of T that are read one at a time: aligned to one.
+template <typename T>
+bool req_each(const T* p) { return p != nullptr && reinterpret_cast<uintptr_t>(p) % sizeof(T) == 0; }
 
 // Opt-in per-kernel event timing (lrs_profile_*): a fixed pool of CUDA event
 // pairs recorded on the launching stream around each kernel.
@@ -1154,7 +1157,7 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
                       float* loss, float* lse, float* total, void* scratch, cudaStream_t stream) {
     const int st = check_ce_shape(T, V, D);
     if (st != LRS_OK) return st;
-    if (!softcap_ok(softcap) || !req(h) || !req(w) || !req(target) || !req(loss) || !req(lse) || !req(total) ||
+    if (!softcap_ok(softcap) || !req(h) || !req(w) || !req_each(target) || !req(loss) || !req(lse) || !req(total) ||
         !req(scratch))
         return LRS_ERR_ARG;
     const CeForward l = ce_forward_layout(T, V, D);
@@ -1190,8 +1193,8 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     const int st = check_ce_shape(T, V, D);
     if (st != LRS_OK) return st;
     if (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) return LRS_ERR_ARG;
-    if (!softcap_ok(softcap) || !req(h) || !req(w) || !req(target) || !req(lse) || !opt(dloss) || !opt(total) ||
-        (dloss == nullptr && total == nullptr) || !req(dh) || !req(dw) || !req(scratch))
+    if (!softcap_ok(softcap) || !req(h) || !req(w) || !req_each(target) || !req_each(lse) || !opt(dloss) ||
+        (dloss == nullptr && total == nullptr) || (total != nullptr && !req_each(total)) || !req(dh) || !req(dw) || !req(scratch))
         return LRS_ERR_ARG;
     const int fp32 = grad_dtype == LRS_GRAD_FP32 ? 1 : 0;
     const CeBackward l = ce_backward_layout(T, V, D, fp32, kBlockSmsBound);

@@ -413,3 +413,24 @@ def test_a_weight_that_is_not_finite_stays_in_its_row(bad, fp32):
     dloss[5] = bad
     got = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=fp32)
     assert torch.equal(got["dh"], clean["dh"]) and torch.equal(got["dw"], clean["dw"])
+
+
+@pytest.mark.parametrize("T,grad_fp32", [(3, False), (70, False), (333, True)])
+def test_rows_of_a_longer_batch(T, grad_fp32):
+    """The next token's targets as a view of the tokens, and a batch's rows from the second on: contiguous, and
+    aligned to their elements only."""
+    h, w, t = _inputs(T + 1, 900, 64, 70 + T, ignored=0.1 if T > 8 else 0.0)
+    dloss = torch.rand(T + 1, generator=torch.Generator().manual_seed(71)).to(DEV) / T
+    whole = api.linear_ce_forward(h, w, t)
+    assert t[1:].data_ptr() % 16 and dloss[1:].data_ptr() % 16 and whole["lse"][1:].data_ptr() % 16
+    f = api.linear_ce_forward(h[1:], w, t[1:])
+    g = api.linear_ce_forward(h[1:], w, t[1:].clone())
+    assert all(torch.equal(f[k], g[k]) for k in ("loss", "lse", "total"))
+    pair = torch.stack([torch.zeros_like(g["total"]), g["total"]]).view(-1)[1:3]   # a total of 4-byte alignment
+    pair.copy_(g["total"])
+    for weights, total in ((dloss[1:], None), (None, pair)):
+        lse = torch.cat([g["lse"][:1], g["lse"]])[1:]
+        b = api.linear_ce_backward(h[1:], w, t[1:], lse, weights, total=total, grad_fp32=grad_fp32)
+        c = api.linear_ce_backward(h[1:], w, t[1:].clone(), g["lse"], None if weights is None else weights.clone(),
+                                   total=g["total"], grad_fp32=grad_fp32)
+        assert torch.equal(b["dh"], c["dh"]) and torch.equal(b["dw"], c["dw"])

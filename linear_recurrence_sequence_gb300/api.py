@@ -166,6 +166,26 @@ def _opt(t, name, dtype, device, shape=None):
     return None if t is None else _need(t, name, dtype, device, shape)
 
 
+def _buffer(t, name, nbytes, device):
+    """t as a caller's buffer of at least nbytes on the device; allocated where t is None."""
+    if t is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if t.device != device:
+        raise ValueError(f"{name}: expected a buffer on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous buffer")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name} buffer is too small: {t.numel() * t.element_size()} bytes of {nbytes}")
+    return t
+
+
+def _saved(t, nbytes, device):
+    """The forward's saved buffer, handed to a backward."""
+    if t is None:
+        raise ValueError("saved must be the forward's saved buffer")
+    return _buffer(t, "saved", nbytes, device)
+
+
 def _like(t, out, key):
     """An output of t's shape and type (cheaper to allocate than by its shape)."""
     if out is None or out.get(key) is None:
@@ -210,12 +230,8 @@ def samu_forward(x_sel, w, h0, reset, nu, theta, w_phi, w_r, a_phi, a_r, *, want
     y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
     y32 = _empty((B, L, D), torch.float32, dev, out, "y32") if want_y32 else None
     hT = _empty((B, M, 2), torch.float32, dev, out, "hT")
-    if saved is None:
-        saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    if saved.numel() < nsaved or scratch.numel() < nscratch:
-        raise ValueError("saved/scratch buffers are too small")
+    saved = _buffer(saved, "saved", nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     st = _load().samu_forward(_ptr(x_sel), _ptr(w), _ptr(h0), _ptr(reset), _ptr(nu), _ptr(theta),
                               _ptr(w_phi), _ptr(w_r), _ptr(a_phi), _ptr(a_r), B, L, D,
                               _ptr(y), _ptr(y32), _ptr(hT), _ptr(saved), _ptr(scratch), _stream(dev))
@@ -238,10 +254,8 @@ def samu_backward(dy, dhT, x_sel, w, h0, reset, nu, theta, w_phi, w_r, a_phi, a_
     _need(w, "w", torch.bfloat16, dev, (B, L, D))
     _opt(reset, "reset", torch.uint8, dev, (B, L))
     nsaved, nscratch = samu_workspace_bytes(B, L, D)
-    if saved is None or saved.numel() < nsaved:
-        raise ValueError("saved must be the forward's saved buffer")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    _saved(saved, nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     gdt = torch.float32 if grad_fp32 else torch.bfloat16
     o = {
         "dx_sel": _empty((B, L, D), gdt, dev, out, "dx_sel"),
@@ -308,6 +322,7 @@ def samu_get_chunk_transition() -> int:
 # ---------------------------------------------------------------------------
 # SAMU decode step
 # ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
 def samu_decode_params_floats(D: int) -> int:
     n = ctypes.c_size_t(0)
     _check("samu_decode_params_floats", _load().samu_decode_params_floats(D, ctypes.byref(n)))
@@ -326,10 +341,7 @@ def samu_decode_prepare(nu, theta, w_phi, w_r, a_phi, a_r, *, params=None):
     _need(a_phi, "a_phi", torch.float32, dev, (1,))
     _need(a_r, "a_r", torch.float32, dev, (1,))
     n = samu_decode_params_floats(D)
-    if params is None:
-        params = torch.empty(n, dtype=torch.float32, device=dev)
-    if params.numel() < n:
-        raise ValueError("params block is too small")
+    params = torch.empty(n, dtype=torch.float32, device=dev) if params is None else _buffer(params, "params", 4 * n, dev)
     _check("samu_decode_prepare", _load().samu_decode_prepare(_ptr(nu), _ptr(theta), _ptr(w_phi), _ptr(w_r),
                                                              _ptr(a_phi), _ptr(a_r), D, _ptr(params), _stream(dev)))
     return params
@@ -346,6 +358,8 @@ def samu_decode_step(x_sel, w, state, params, reset=None, *, state_out=None, wan
     _need(w, "w", torch.bfloat16, dev, (B, D))
     _need(state, "state", torch.float32, dev, (B, M, 2))
     _opt(reset, "reset", torch.uint8, dev, (B,))
+    if params is not None:
+        _buffer(params, "params", 4 * samu_decode_params_floats(D), dev)
     so = state if state_out is None else state_out
     _need(so, "state_out", torch.float32, dev, (B, M, 2))
     y = _empty((B, D), torch.bfloat16, dev, out, "y")
@@ -380,10 +394,8 @@ def rglru_forward(x, lx, la, alpha, h0, reset, *, want_y32=False, out=None, save
     y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
     y32 = _empty((B, L, D), torch.float32, dev, out, "y32") if want_y32 else None
     hT = _empty((B, D), torch.float32, dev, out, "hT")
-    if saved is None:
-        saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    saved = _buffer(saved, "saved", nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     st = _load().rglru_forward(_ptr(x), _ptr(lx), _ptr(la), _ptr(alpha), _ptr(h0), _ptr(reset), B, L, D,
                                _ptr(y), _ptr(y32), _ptr(hT), _ptr(saved), _ptr(scratch), _stream(dev))
     _check("rglru_forward", st)
@@ -397,10 +409,8 @@ def rglru_backward(dy, dhT, x, lx, la, alpha, h0, reset, saved, *, grad_fp32=Fal
     _need(dy, "dy", torch.bfloat16, dev, (B, L, D))
     _opt(dhT, "dhT", torch.float32, dev, (B, D))
     nsaved, nscratch = rglru_workspace_bytes(B, L, D)
-    if saved is None or saved.numel() < nsaved:
-        raise ValueError("saved must be the forward's saved buffer")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    _saved(saved, nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     gdt = torch.float32 if grad_fp32 else torch.bfloat16
     o = {
         "dx": _empty((B, L, D), gdt, dev, out, "dx"),
@@ -455,10 +465,8 @@ def rglru_proj_forward(x, w_x, b_x, w_a, b_a, alpha, h0, reset, *, want_y32=Fals
     y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
     y32 = _empty((B, L, D), torch.float32, dev, out, "y32") if want_y32 else None
     hT = _empty((B, D), torch.float32, dev, out, "hT")
-    if saved is None:
-        saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    saved = _buffer(saved, "saved", nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     st = _load().rglru_proj_forward(_ptr(x), _ptr(w_x), _ptr(b_x), _ptr(w_a), _ptr(b_a), _ptr(alpha), _ptr(h0),
                                     _ptr(reset), B, L, D, _ptr(y), _ptr(y32), _ptr(hT), _ptr(saved), _ptr(scratch),
                                     _stream(dev))
@@ -474,10 +482,8 @@ def rglru_proj_backward(dy, dhT, x, w_x, b_x, w_a, b_a, alpha, h0, reset, saved,
     _need(dy, "dy", torch.bfloat16, dev, (B, L, D))
     _opt(dhT, "dhT", torch.float32, dev, (B, D))
     nsaved, nscratch = rglru_proj_workspace_bytes(B, L, D)
-    if saved is None or saved.numel() < nsaved:
-        raise ValueError("saved must be the forward's saved buffer")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    _saved(saved, nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     o = {
         "dx": _empty((B, L, D), torch.float32 if grad_fp32 else torch.bfloat16, dev, out, "dx"),
         "dw_x": _empty((PROJ_BLOCKS, dk, dk), torch.float32, dev, out, "dw_x"),
@@ -557,12 +563,8 @@ def samu_block_forward(x, params: dict, h0=None, reset=None, *, out=None, saved=
     nsaved, nscratch = samu_block_workspace_bytes(B, L, Dm, D, mixer)
     y = _empty((B, L, Dm), torch.bfloat16, dev, out, "out")
     hT = _empty(sshape, torch.float32, dev, out, "hT")
-    if saved is None:
-        saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    if saved.numel() < nsaved or scratch.numel() < nscratch:
-        raise ValueError("saved/scratch buffers are too small")
+    saved = _buffer(saved, "saved", nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     fn = "samu_block_forward" if mixer == "samu" else "rglru_block_forward"
     st = getattr(_load(), fn)(ctypes.cast(ctypes.pointer(ps), _P), _ptr(x), _ptr(h0), _ptr(reset), B, L, Dm, D,
                               _ptr(y), _ptr(hT), _ptr(saved), _ptr(scratch), _stream(dev))
@@ -582,10 +584,8 @@ def samu_block_backward(dout, dhT, x, params: dict, h0, reset, saved, *, out=Non
     _opt(reset, "reset", torch.uint8, dev, (B, L))
     ps = _block_params(params, Dm, dev)
     nsaved, nscratch = samu_block_workspace_bytes(B, L, Dm, D, mixer)
-    if saved is None or saved.numel() < nsaved:
-        raise ValueError("saved must be the forward's saved buffer")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
+    _saved(saved, nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     shapes = _block_shapes(Dm, D)
     o = {"dx": _empty((B, L, Dm), torch.bfloat16, dev, out, "dx"),
          "dh0": _empty(sshape, torch.float32, dev, out, "dh0")}
@@ -615,8 +615,7 @@ def dense_gemm(layout: int, A, B, M: int, N: int, K: int, *, out=None, scratch=N
     dt = torch.float32 if layout == LRS_GEMM_TN else torch.bfloat16
     C = out if out is not None else torch.empty((M, N), dtype=dt, device=dev)
     _need(C, "C", dt, dev, (M, N))
-    if scratch is None:
-        scratch = torch.empty(256, dtype=torch.uint8, device=dev)
+    scratch = _buffer(scratch, "scratch", 256, dev)
     _check("lrs_dense_gemm", _load().lrs_dense_gemm(layout, _ptr(A), _ptr(B), _ptr(C), M, N, K, _ptr(scratch),
                                                     _stream(dev)))
     return C
@@ -659,10 +658,7 @@ def linear_ce_forward(h, w, target, *, softcap=0.0, out=None, scratch=None):
     loss = _empty(shape, torch.float32, dev, out, "loss")
     lse = _like(loss, out, "lse")
     total = _empty((2,), torch.float32, dev, out, "total")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    elif scratch.numel() < nscratch:
-        raise ValueError("scratch buffer is too small")
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     st = _load().linear_ce_forward(h.data_ptr(), w.data_ptr(), target.data_ptr(), T, V, D, softcap, loss.data_ptr(),
                                    lse.data_ptr(), total.data_ptr(), scratch.data_ptr(), _stream(dev))
     if st:
@@ -690,10 +686,7 @@ def linear_ce_backward(h, w, target, lse, dloss=None, *, total=None, softcap=0.0
         dw = _empty(w.shape, torch.float32, dev, out, "dw")
     else:
         dh, dw = _like(h, out, "dh"), _like(w, out, "dw")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    elif scratch.numel() < nscratch:
-        raise ValueError("scratch buffer is too small")
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     st = _load().linear_ce_backward(h.data_ptr(), w.data_ptr(), target.data_ptr(), lse.data_ptr(), _ptr(dloss),
                                     _ptr(total), T, V, D, softcap, dh.data_ptr(), dw.data_ptr(),
                                     LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16, scratch.data_ptr(), _stream(dev))
@@ -744,10 +737,7 @@ def gated_norm_forward(x, y=None, gate=None, gamma_post=None, scale=None, gamma_
     nsaved, _ = gated_norm_workspace_bytes(T, D)
     r = _like(x, out, "r") if y is not None else None
     h = _like(x, out, "h")
-    if saved is None:
-        saved = torch.empty(nsaved, dtype=torch.uint8, device=dev)
-    elif saved.numel() < nsaved:
-        raise ValueError("saved buffer is too small")
+    saved = _buffer(saved, "saved", nsaved, dev)
     st = _load().gated_norm_forward(x.data_ptr(), _ptr(y), _ptr(gate), _ptr(gamma_post), _ptr(scale), _ptr(gamma_pre),
                                     T, D, eps, _ptr(r), h.data_ptr(), saved.data_ptr(), _stream(dev))
     if st:
@@ -764,12 +754,8 @@ def gated_norm_backward(dr, dh, x, y, gate, gamma_post, scale, gamma_pre, saved,
     _opt(dr, "dr", torch.bfloat16, dev, x.shape)
     _need(dh, "dh", torch.bfloat16, dev, x.shape)
     nsaved, nscratch = gated_norm_workspace_bytes(T, D)
-    if saved is None or saved.numel() < nsaved:
-        raise ValueError("saved must be the forward's saved buffer")
-    if scratch is None:
-        scratch = torch.empty(nscratch, dtype=torch.uint8, device=dev)
-    if scratch.numel() < nscratch:
-        raise ValueError("scratch buffer is too small")
+    _saved(saved, nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
     o = {"dx": _like(x, out, "dx"), "dy": None, "dgate": None, "dgamma_post": None,
          "dscale": None, "dgamma_pre": _empty((D,), torch.float32, dev, out, "dgamma_pre")}
     if y is not None:

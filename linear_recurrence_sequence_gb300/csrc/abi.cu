@@ -1424,7 +1424,7 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
     a.step = step;
     a.norm = norm;
     a.bias = at<float>(scratch, 0);
-    a.partial = at<float2>(scratch, 256);
+    a.partial = at<float4>(scratch, 256);
     for (int i = 0; i < count; i += kAdamCap) {
         const int k = std::min(kAdamCap, count - i);
         int ctas = 0;

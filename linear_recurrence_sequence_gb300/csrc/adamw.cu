@@ -153,24 +153,66 @@ __device__ __forceinline__ TwoSum cta_sum(TwoSum v, float2* red) {
     return s;
 }
 
-// Squares of eight BF16 or four FP32 values, added to q.
+// Squares of eight BF16 or four FP32 values (SCALED: times 2^-96 each), added to q.
+constexpr float kAdamDown = 1.262177448e-29f, kAdamUp = 7.922816251e28f;   // 2^-96, 2^96
+template <bool SCALED>
 __device__ __forceinline__ void squares(const uint4 v, bool bf16, float& q) {
+    auto add = [&](float x) {
+        if (SCALED) x *= kAdamDown;
+        q = fmaf(x, x, q);
+    };
     if (bf16) {
         const float2 a = bf2_to_f2(v.x), b = bf2_to_f2(v.y), c = bf2_to_f2(v.z), d = bf2_to_f2(v.w);
-        q = fmaf(a.x, a.x, q); q = fmaf(a.y, a.y, q);
-        q = fmaf(b.x, b.x, q); q = fmaf(b.y, b.y, q);
-        q = fmaf(c.x, c.x, q); q = fmaf(c.y, c.y, q);
-        q = fmaf(d.x, d.x, q); q = fmaf(d.y, d.y, q);
+        add(a.x); add(a.y); add(b.x); add(b.y);
+        add(c.x); add(c.y); add(d.x); add(d.y);
     } else {
-        const float a = __uint_as_float(v.x), b = __uint_as_float(v.y), c = __uint_as_float(v.z), d = __uint_as_float(v.w);
-        q = fmaf(a, a, q); q = fmaf(b, b, q);
-        q = fmaf(c, c, q); q = fmaf(d, d, q);
+        add(__uint_as_float(v.x)); add(__uint_as_float(v.y)); add(__uint_as_float(v.z)); add(__uint_as_float(v.w));
     }
 }
+// A sum of squares whose N is in range though its squares are not: up to 32
+// squares at a time are added in FP32; a sum of them from 2^80 on (below it 2^40
+// values do not overflow) is formed again 2^-192 times as large and kept apart.
+// NaN and infinities go there too.
+constexpr float kAdamBig = 1.208925820e24f;   // 2^80
+struct SquareSum {
+    TwoSum mid, big;
+};
+// N sixteen-byte groups p[0], p[kAdamThreads], ... (x: loaded) added to a thread's
+// sum.  Those out of range are read again and `big` is in shared memory: held in
+// registers, they cost a CTA an SM (562M FP32 gradients 340 -> 350 us).
+template <int N>
+__device__ __forceinline__ void add_squares(const uint4* x, const uint4* p, bool bf16, TwoSum& mid, TwoSum& big) {
+    float q = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) squares<false>(x[k], bf16, q);
+    if (q < kAdamBig) {
+        mid.add(q);
+    } else {
+        q = 0.f;
+#pragma unroll 1
+        for (int k = 0; k < N; ++k) squares<true>(__ldg(p + k * kAdamThreads), bf16, q);
+        big.add(q);
+    }
+}
+__device__ __forceinline__ void add_square(float x, TwoSum& mid, TwoSum& big) {
+    if (x * x < kAdamBig) {
+        mid.add(x * x);
+    } else {
+        x *= kAdamDown;
+        big.add(x * x);
+    }
+}
+// Sum over the CTA, in every thread; `big` is looked at where any thread has some.
+__device__ __forceinline__ SquareSum cta_sum(const SquareSum& v, float2* red) {
+    SquareSum s;
+    s.mid = cta_sum(v.mid, red);
+    if (__syncthreads_or(v.big.hi != 0.f)) s.big = cta_sum(v.big, red);
+    return s;
+}
 // First launch of a step: sums of squares of the gradients, one partial sum a
-// CTA; up to 32 squares at a time are added in FP32 (their roundings are
-// independent and cancel over the groups).  The last CTA advances the step and
-// forms its bias corrections, 1 - b^t = -expm1(t log b).
+// CTA, in a fixed order.  A chain of 32 squares loses at most 2^-19 of its value
+// and the sums of the chains, in two floats, nothing: N is within 2^-19.  The last
+// CTA advances the step and forms its bias corrections, 1 - b^t = -expm1(t log b).
 template <int CAP>
 __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_constant__ AdamList<CAP> l,
                                                                   const AdamArgs a) {
@@ -198,6 +240,9 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
     // the plain FP32 sums stay short
     constexpr int kUnroll = 8;
     const int chunks = l.first[l.count];
+    __shared__ TwoSum bigs[kAdamThreads];
+    TwoSum& big = bigs[threadIdx.x];
+    big = TwoSum();
     TwoSum sum;
     for (int c0 = (int)blockIdx.x * a.norm_group; c0 < chunks; c0 += ctas * a.norm_group) {
         const int c1 = min(c0 + a.norm_group, chunks);
@@ -216,29 +261,27 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_norm_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < kUnroll; ++k) x[k] = __ldg(g + v + k * kAdamThreads);
 #pragma unroll
-                for (int h = 0; h < kUnroll; h += 4) {
-                    float q = 0.f;
-#pragma unroll
-                    for (int k = h; k < h + 4; ++k) squares(x[k], bf, q);
-                    sum.add(q);
-                }
+                for (int h = 0; h < kUnroll; h += 4) add_squares<4>(x + h, g + v + h * kAdamThreads, bf, sum, big);
             }
             for (; v < nv; v += kAdamThreads) {
-                float q = 0.f;
-                squares(__ldg(g + v), bf, q);
-                sum.add(q);
+                const uint4 x = __ldg(g + v);
+                add_squares<1>(&x, g + v, bf, sum, big);
             }
             const int e = nv * per + (int)threadIdx.x;
             if (e < n) {
                 const float x = bf ? __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(g)[e] << 16)
                                    : reinterpret_cast<const float*>(g)[e];
-                sum.add(x * x);
+                add_square(x, sum, big);
             }
             c = to;
         }
     }
-    const TwoSum s = cta_sum(sum, red);
-    if (threadIdx.x == 0) a.partial[a.partial0 + blockIdx.x] = make_float2(s.hi, s.lo);
+    SquareSum s;
+    s.mid = sum;
+    s.big = big;
+    s = cta_sum(s, red);
+    if (threadIdx.x == 0)
+        a.partial[a.partial0 + blockIdx.x] = make_float4(s.mid.hi, s.mid.lo, s.big.hi, s.big.lo);
 }
 
 // The step's scalars.
@@ -355,12 +398,15 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_update_kernel(const __g
     AdamScalars sc;
     sc.clip = 1.f;
     if (a.max_norm > 0.f) {
-        TwoSum s;
+        SquareSum s;
         for (int i = threadIdx.x; i < a.partials; i += kAdamThreads) {
-            const float2 q = __ldcg(a.partial + i);
-            s.add(q.x, q.y);
+            const float4 q = __ldcg(a.partial + i);
+            s.mid.add(q.x, q.y);
+            s.big.add(q.z, q.w);
         }
-        const float norm = sqrtf(cta_sum(s, red).value());
+        s = cta_sum(s, red);
+        const float norm = s.big.hi == 0.f ? sqrtf(s.mid.value())
+                                           : sqrtf(s.big.value() + s.mid.value() * kAdamDown * kAdamDown) * kAdamUp;
         const bool skip = !(norm <= 3.4028234e38f);
         if (blockIdx.x == 0 && threadIdx.x == 0 && a.advance) {
             *a.norm = norm;
@@ -434,7 +480,7 @@ long long adam_chunks(long long n) { return (n + kAdamChunk - 1) / kAdamChunk; }
 
 size_t adam_scratch_bytes(int count) {
     const size_t launches = (size_t)(count + kAdamCap - 1) / kAdamCap;
-    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(float2) + 255) / 256 * 256;
+    return 256 + (launches * kAdamNormCtas * kBlockSmsBound * sizeof(float4) + 255) / 256 * 256;
 }
 
 cudaError_t launch_adamw_norm(const AdamTensor* ts, int count, const AdamArgs& a, int* ctas, cudaStream_t s, bool pdl) {

@@ -633,7 +633,7 @@ struct AdamArgs {
     int32_t* step;
     float* norm;
     float* bias;                 // [2]: 1 / (1 - beta^step)
-    float2* partial;             // sums of squares (two floats each), one a CTA of the first launches
+    float4* partial;             // sums of squares (two floats each, those out of range apart), one a CTA of the first launches
     int norm_group;              // chunks a CTA of the norm takes at a time (filled by the launcher)
     int partial0, partials;      // this launch's first, and all
     int advance;                 // the step's first launch of its kind

@@ -339,3 +339,58 @@ def test_refusals():
     with pytest.raises(api.LrsError) as e:   # not 16-byte aligned
         api.adamw_step(api.adamw_plan([{**ts[0], "grad": odd}]), step, lr)
     assert e.value.status == 1
+
+
+def _norm_of(ts, step=0):
+    """The norm that a step reports (a bound that nothing reaches)."""
+    count, lr = _scalars(step)
+    return float(api.adamw_step(api.adamw_plan(ts), count, lr, max_norm=3e38)["norm"])
+
+
+# The norm adds at most 32 squares in one FP32 chain, each addition within u of
+# its partial sum (the products are fused), and the chains in two floats: 2^-19
+# of the sum of squares, half of that of its root, and u twice for the two last
+# roundings: within 2^-19 of the norm.
+NORM_TOL = 2.0 ** -19
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n", [1, 3, 8, 31, 255, 256, 1000, 2049, 70001, 3000017])
+def test_norm_of_equal_and_of_random_gradients(n, grad):
+    gen = torch.Generator().manual_seed(n)
+    ts = _tensors((n,), 20, grad=grad)
+    for g in (torch.full((n,), 0.1), torch.full((n,), 1.0 / 3), torch.randn(n, generator=gen)):
+        ts[0]["grad"].copy_(g)
+        exact = float(ts[0]["grad"].double().square().sum()) ** 0.5
+        assert abs(_norm_of(ts) - exact) <= NORM_TOL * exact
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("large", [1e18, 1e20, 1e30, 1e38])
+def test_gradients_whose_squares_overflow_are_clipped(large, bits, grad):
+    """A finite norm of gradients above the root of FP32's range clips them like any other."""
+    ts = _tensors(SIZES, 21, bits, True, grad, gscale=1.0)
+    for k in (1, 6, 10):
+        ts[k]["grad"][::7] *= large / 200
+    step, lr = _scalars(7)
+    norm, exp = _expected(ts, 8, float(lr), 1.0)
+    assert norm < 3e38
+    before = _before(ts)
+    o = api.adamw_step(api.adamw_plan(ts), step, lr, beta1=B1, beta2=B2, eps=EPS, max_norm=1.0)
+    assert int(step) == 8
+    assert abs(float(o["norm"]) - norm) <= NORM_TOL * norm
+    for t, e, b in zip(ts, exp, before):
+        p = t["master"].double()
+        most = 2.0 ** -23 * (b["p"].abs() + e["p"].abs()) + 2.0 ** -17 * e["step"]
+        assert float(((p - e["p"]).abs() - most).max()) <= 0
+
+
+def test_a_norm_past_the_range_changes_nothing():
+    ts = _tensors([2048] * 3, 22)
+    ts[1]["grad"].fill_(3e38)   # finite values, a norm of 1e40
+    before = [t["master"].clone() for t in ts]
+    step, lr = _scalars(4)
+    o = api.adamw_step(api.adamw_plan(ts), step, lr, max_norm=1.0)
+    assert float(o["norm"]) == float("inf") and int(step) == 4
+    assert all(torch.equal(t["master"], b) for t, b in zip(ts, before))

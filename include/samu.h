@@ -591,7 +591,9 @@ int lrs_adamw_scratch_bytes(int count, size_t* bytes);
  *   scratch   lrs_adamw_scratch_bytes() bytes
  * FP32 arithmetic; the norm in a fixed order of summation, within 2^-19 of its
  * value wherever FP32 holds that value (squares above FP32's range are scaled; of
- * gradients whose root mean square is below 2^-65, squares are lost).  Everything that changes from step to step is on the device: a
+ * gradients whose root mean square is below 2^-65, squares are lost); the
+ * quotient by the root, and the root itself with 32-bit states, within 2^-22 of the
+ * step (the GPU's fast forms).  Everything that changes from step to step is on the device: a
  * captured graph steps correctly.  Two launches for up to 400 tensors.
  * Errors: LRS_ERR_ARG (null or misaligned pointer, n < 1, one scale without
  * the other, a negative weight decay, betas outside [0, 1), eps <= 0),

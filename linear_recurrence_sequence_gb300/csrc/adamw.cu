@@ -337,8 +337,10 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, long long b0, in
             v[k][j] = __fadd_rn(__fmul_rn(vv, a.b2), __fmul_rn(__fmul_rn(gg, gg), a.c2));
             // one root serves the step and the state: correctly rounded where it
             // is stored (a code next to a tie follows its last bit), from the SFU
-            // like the quotient otherwise, within 2^-22 (the step is a small part of p)
-            root[k][j] = Q8 ? __fsqrt_rn(v[k][j]) : sqrt_approx(v[k][j]);
+            // like the quotient otherwise, within 2^-22 (the step is a small part of
+            // p; both correctly rounded: one small block 9.8 -> 11.8 us).  v may be
+            // below 2^-126: a root of 0 would leave eps alone to divide by
+            root[k][j] = Q8 ? __fsqrt_rn(v[k][j]) : sqrt_approx_full(v[k][j]);
             const float step = __fdividef(m[k][j] * a.ibc1, fmaf(root[k][j], a.root_ibc2, a.eps));
             p[k][j] = fmaf(-a.lr, step, p[k][j] * keep);
             if (Q8) {

@@ -394,3 +394,23 @@ def test_a_norm_past_the_range_changes_nothing():
     o = api.adamw_step(api.adamw_plan(ts), step, lr, max_norm=1.0)
     assert float(o["norm"]) == float("inf") and int(step) == 4
     assert all(torch.equal(t["master"], b) for t, b in zip(ts, before))
+
+
+@pytest.mark.parametrize("master", [True, False])
+@pytest.mark.parametrize("gscale", [1e-19, 1e-20, 1e-21])
+def test_tiny_gradients_with_a_tiny_eps(gscale, master):
+    """Second moments below FP32's normal range still divide the step.  v is rounded to multiples of 2^-149 twice on
+    its way (its square and its product): 2^-149 absolute, half of that relative to v in its root."""
+    ts = _tensors((5000,), 23, 32, master, fresh=True)
+    g = (1 + torch.rand(5000, generator=torch.Generator().manual_seed(24))) * gscale
+    ts[0]["grad"].copy_(g * torch.where(torch.arange(5000) % 2 == 0, 1.0, -1.0))
+    step, lr = _scalars(0)
+    g = ts[0]["grad"].double()
+    p0 = _before(ts)[0]["p"]
+    api.adamw_step(api.adamw_plan(ts), step, lr, beta1=B1, beta2=B2, eps=1e-30)
+    p = (ts[0]["master"] if master else ts[0]["param"]).double()
+    v = (1 - B2) * g * g
+    move = float(lr) * g / (torch.sqrt(v / (1 - B2)) + 1e-30)
+    off = (p - (p0 * (1 - float(lr) * ts[0]["weight_decay"]) - move)).abs()
+    most = 2.0 ** -23 * (p0.abs() + move.abs()) + move.abs() * (2.0 ** -149 / v + 2.0 ** -17)
+    assert float((off - most).max()) <= 0

@@ -105,25 +105,34 @@ __device__ __forceinline__ void load_product(const float* p, const float* q, int
 // from the SFU: e^{-2u} = 2^(x (k0 + k1 x^2)) and the reciprocal, 2^-20 relative
 // over |2u| <= 20; six operations, where the block's own form takes about 15
 // (the forward kernel was bound by them).  Its derivative is
-// s (1 + (1 - s) x (k2 + k3 x^2)) with 1 - s = e^{-2u} s.  Far below zero
-// e^{-2u} is held at 3e38, whose reciprocal is flushed to 0: both are then 0.
+// s (1 + (1 - s) x (k2 + k3 x^2)) with 1 - s = e^{-2u} s, formed at x held within
+// kGeluEnd of 0: there e^{-2u} is 2^127.6 or its reciprocal, whose own reciprocals
+// are exactly 0 (flushed) and 1, so that the derivative of any gate farther out is 0
+// or 1 and no factor overflows.
 constexpr float kGelu0 = -2.302208198f;    // -2 sqrt(2/pi) log2(e)
 constexpr float kGelu1 = -0.1029432397f;   // 0.044715 of it
 constexpr float kGelu2 = 1.595769122f;     // 2 sqrt(2/pi)
 constexpr float kGelu3 = 0.2140644488f;    // 3 0.044715 of it
+constexpr float kGeluEnd = 10.05f;
+// x, held within +-end (end > 0; NaN stays).
+__device__ __forceinline__ float hold(float x, float end) {
+    float r;
+    asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(end));
+    return r;
+}
 __device__ __forceinline__ float2 gn_gelu(float2 x) {
     const float2 t = mul2(x, fma2(both(kGelu1), mul2(x, x), both(kGelu0)));
     const float2 e = add2(make_float2(ex2_approx(t.x), ex2_approx(t.y)), both(1.f));
     return mul2(x, make_float2(rcp_approx(e.x), rcp_approx(e.y)));
 }
 __device__ __forceinline__ void gn_gelu_grad(float2 x, float2& g, float2& dg) {
-    const float2 x2 = mul2(x, x);
-    const float2 t = mul2(x, fma2(both(kGelu1), x2, both(kGelu0)));
-    const float2 e = make_float2(fminf(ex2_approx(t.x), 3e38f), fminf(ex2_approx(t.y), 3e38f));
+    const float2 c = make_float2(hold(x.x, kGeluEnd), hold(x.y, kGeluEnd)), c2 = mul2(c, c);
+    const float2 t = mul2(c, fma2(both(kGelu1), c2, both(kGelu0)));
+    const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
     const float2 e1 = add2(e, both(1.f));
     const float2 s = make_float2(rcp_approx(e1.x), rcp_approx(e1.y));
     g = mul2(x, s);
-    dg = fma2(mul2(s, mul2(e, s)), mul2(x, fma2(both(kGelu3), x2, both(kGelu2))), s);
+    dg = fma2(mul2(s, mul2(e, s)), mul2(c, fma2(both(kGelu3), c2, both(kGelu2))), s);
 }
 
 // Sum over the threads of a row (blockDim.x of them, whole warps).  `red` is

@@ -229,3 +229,20 @@ def test_refusals():
         with pytest.raises(api.LrsError) as e:
             api.gated_norm_forward(torch.zeros(2, D, dtype=torch.bfloat16, device=DEV))
         assert e.value.status == status
+
+
+def test_gates_far_outside_the_sigmoid():
+    """Gates whose cube leaves FP32's range: the derivative there is 1 or 0."""
+    i, dr, dh = _inputs(9, 256, 20)
+    for row, g in enumerate((1e12, -1e12, 1e13, -1e13, 1e14, -1e14, -3e38)):
+        i["gate"][row, 3 * row] = g
+    i["gate"][7] = -1e30
+    _, b = _check(i, dr, dh)
+    assert not b["dgate"][1, 3].any() and not b["dgate"][7].any()
+    # a gate at the end of the range overflows its row's norm (h is 0 or not finite), not its own derivative
+    i["gate"][8, 5] = 3e38
+    f = api.gated_norm_forward(**i, eps=EPS)
+    b = api.gated_norm_backward(dr, None if dh is None else torch.zeros_like(dh), *i.values(), f["saved"], eps=EPS)
+    p = i["y"][8].double() / torch.sqrt(i["y"][8].double().square().mean() + EPS)
+    ref = (dr[8].double() * i["scale"].double() * i["gamma_post"].double() * p)[5]
+    assert abs(float(b["dgate"][8, 5]) - float(ref)) <= 2.0 ** -7 * abs(float(ref))

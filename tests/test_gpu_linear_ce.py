@@ -434,3 +434,25 @@ def test_rows_of_a_longer_batch(T, grad_fp32):
         c = api.linear_ce_backward(h[1:], w, t[1:].clone(), g["lse"], None if weights is None else weights.clone(),
                                    total=g["total"], grad_fp32=grad_fp32)
         assert torch.equal(b["dh"], c["dh"]) and torch.equal(b["dw"], c["dw"])
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_pieces_of_the_vocabulary_with_weights_and_a_cap(fp32):
+    T, V, D = 70000, 5000, 8
+    assert T * V * 2 > 512 << 20
+    h, w, t = _inputs(T, V, D, 80, std=4.0)
+    keep = torch.sort(torch.randperm(T, generator=torch.Generator().manual_seed(81))[:300]).values.to(DEV)
+    # only 300 tokens are counted, so that the 64-bit definition needs only those
+    t2 = torch.full_like(t, -1)
+    t2[keep] = t[keep]
+    dloss = torch.randn(T, generator=torch.Generator().manual_seed(82)).to(DEV) / 300
+    f = api.linear_ce_forward(h, w, t2, softcap=5.0)
+    b = api.linear_ce_backward(h, w, t2, f["lse"], dloss, softcap=5.0, grad_fp32=fp32)
+    loss, _, dh, dw, bh, bw = _exact(h[keep], w, t2[keep], dloss[keep], 5.0, "fp32" if fp32 else "bf16")
+    np.testing.assert_allclose(_f64(f["loss"][keep]), loss, rtol=0, atol=TOL_ROW)
+    for got, ref, most in ((b["dh"][keep], dh, bh), (b["dw"], dw, bw)):
+        assert (np.abs(_f64(got) - ref) - most).max() <= 0
+        assert _rel(_f64(got), ref) <= (2.0 ** -16 + TOL_ROW if fp32 else 2.0 ** -8)
+    rest = torch.ones(T, dtype=torch.bool, device=DEV)
+    rest[keep] = False
+    assert not b["dh"][rest].any()

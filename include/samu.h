@@ -478,9 +478,10 @@ int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forwa
  *   total    two FP32 (out): the sum of the losses and the number of tokens
  *            counted (16-byte aligned)
  *   scratch  linear_ce_workspace_bytes().forward bytes
- * Products of BF16 values accumulate in FP32 on the tensor cores; sums of
- * exponentials are FP32, the sum of the losses is right to its last FP32 bit, all
- * in a fixed order.
+ * Products of BF16 values accumulate in FP32 on the tensor cores, which truncate
+ * (a logit is within about 1.3e-6 of its partial sums' size, chains of 1024 products
+ * being added up apart); exponentials are the GPU's fast ones (2^-22) and their sums
+ * FP32; the sum of the losses is right to its last FP32 bit; all in a fixed order.
  * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, softcap
  * negative or not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8, T or V
  * over 2^23, D over 2^16), LRS_ERR_CUDA. */
@@ -499,8 +500,10 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
  *   dh [T,D], dw [V,D]: BF16 or FP32 by grad_dtype (out)
  *   scratch  linear_ce_workspace_bytes().backward bytes
  * dz enters the two contractions in BF16 (LRS_GRAD_BF16: the results are
- * rounded to BF16 themselves), or as a BF16 leading part plus a BF16 remainder
- * (LRS_GRAD_FP32: 16 significant bits, twice the products).  Deterministic:
+ * rounded to BF16 themselves; weights that differ cost them a third more error than
+ * that rounding), or as the sum of three BF16 parts (LRS_GRAD_FP32: 24 significant
+ * bits, three times the products).  A dloss that is not finite reaches its own row of
+ * dh, and dw.  Deterministic:
  * every sum runs in a fixed order.  Errors: as the forward, plus LRS_ERR_ARG
  * for an unknown grad_dtype. */
 int linear_ce_backward(const void* h, const void* w, const int64_t* target, const float* lse, const float* dloss,

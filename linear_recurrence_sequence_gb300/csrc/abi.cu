@@ -1107,33 +1107,34 @@ CeForward ce_forward_layout(int T, int V, int D) {
     return l;
 }
 
-// The backward's: dz (and its remainders) of one piece of the vocabulary, and
+// The backward's: dz (in one part, or three) of one piece of the vocabulary, and
 // the FP32 partial sums of dh and dw.
 struct CeBackward {
     int piece;           // columns of a piece (a multiple of 256 unless there is one piece)
     long long ldz;       // row stride of dz: a multiple of 64
     int pieces;
     int h_splits, w_splits;   // of the sums over the piece and over the tokens
-    size_t h, dz, dz2, dh, dw, total;
+    int parts;
+    size_t h, dz, part_bytes, dh, dw, total;
 };
 constexpr long long kCePieceBytes = 512LL << 20;
 
 CeBackward ce_backward_layout(int T, int V, int D, int fp32, int sms) {
     CeBackward l;
-    const long long row = (long long)T * 2 * (fp32 ? 2 : 1);
+    l.parts = fp32 ? kCeParts : 1;
+    const long long row = (long long)T * 2 * l.parts;
     const long long most = std::max(256LL, kCePieceBytes / row / 256 * 256);
     const int pieces = (int)((V + most - 1) / most);
     // pieces of about the same length
     l.piece = pieces == 1 ? V : (int)(((V + pieces - 1) / pieces + 255) / 256 * 256);
     l.pieces = (V + l.piece - 1) / l.piece;
     l.ldz = (l.piece + 63) / 64 * 64;
-    ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &l.h_splits, &l.w_splits);
+    ce_grad_splits(T, l.piece, D, l.parts, sms, &l.h_splits, &l.w_splits);
     const int sh = l.h_splits, sw = l.w_splits;
-    const size_t dz = up256((size_t)T * (size_t)l.ldz * 2);
+    l.part_bytes = up256((size_t)T * (size_t)l.ldz * 2);
     l.h = 256;
     l.dz = l.h + up256((size_t)T * D * 2);
-    l.dz2 = l.dz + dz;
-    l.dh = l.dz2 + (fp32 ? dz : 0);
+    l.dh = l.dz + l.parts * l.part_bytes;
     l.dw = l.dh + ((sh > 1 || (l.pieces > 1 && !fp32)) ? up256((size_t)sh * T * D * 4) : 0);
     l.total = l.dw + (sw > 1 ? up256((size_t)sw * l.piece * D * 4) : 0);
     return l;
@@ -1179,7 +1180,7 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
         parts = ce_few_parts(T, block_gemm_sms());
         LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_few(g, h, w, stream, pdl_ok()));
     } else {
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, nullptr, 0, stream, pdl_ok()));
+        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, nullptr, 0, 0, 0, stream, pdl_ok()));
     }
     LRS_LAUNCH(KID_CE_ROWS, stream,
                launch_ce_rows(g.stats, g.zt, target, parts, T, V, loss, lse, at<int4>(scratch, l.sums), total,
@@ -1201,10 +1202,9 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
     const int sms = block_gemm_sms();
     uint32_t* status = at<uint32_t>(scratch, 0);
     void* dz = at<void>(scratch, l.dz);
-    void* dz2 = fp32 ? at<void>(scratch, l.dz2) : nullptr;
     // the same splits for every piece (the last may be shorter)
     int h_splits, w_splits;
-    ce_grad_splits(T, l.piece, D, fp32 ? 2 : 1, sms, &h_splits, &w_splits);
+    ce_grad_splits(T, l.piece, D, l.parts, sms, &h_splits, &w_splits);
     // dh adds over the pieces (and the splits of a piece) in FP32
     const bool h_part = h_splits > 1 || (l.pieces > 1 && !fp32);
     // the tokens' weights: in dz (FP32 gradients); their ratios to the largest,
@@ -1235,7 +1235,8 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         g.softcap = softcap;
         g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
         g.status = status;
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_logits(g, h, w, V, dz, dz2, l.ldz, stream, pdl_ok()));
+        LRS_LAUNCH(KID_CE_GEMM, stream,
+                   launch_ce_logits(g, h, w, V, dz, l.parts, l.part_bytes, l.ldz, stream, pdl_ok()));
         // dh (+)= dz w; dw's rows of this piece = dz^T h
         CeGemmArgs d = {};
         d.status = status;
@@ -1262,7 +1263,8 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
         cw.splits = w_splits;
         const size_t at0 = (size_t)v0 * D;
         cw.part = w_splits > 1 ? at<float>(scratch, l.dw) : fp32 ? static_cast<float*>(dw) + at0 : nullptr;
-        LRS_LAUNCH(KID_CE_GEMM, stream, launch_ce_grads(d, dz, dz2, l.ldz, hw, w, V, dh, dw, stream, pdl_ok()));
+        LRS_LAUNCH(KID_CE_GEMM, stream,
+                   launch_ce_grads(d, dz, l.parts, l.part_bytes, l.ldz, hw, w, V, dh, dw, stream, pdl_ok()));
         if (w_splits > 1)
             LRS_LAUNCH(KID_CE_ROWS, stream,
                        launch_ce_sum(cw.part, (long long)nv * D, w_splits, (long long)nv * D,

@@ -59,7 +59,7 @@ constexpr uint32_t kCeTmemCols = 2 * kCeN;
 constexpr uint32_t kCeBox = 32 * 32 * 2;   // a [32 rows][32 columns] BF16 store box (64-byte swizzle)
 constexpr uint32_t kCeWideBox = 2 * kCeBox;   // [32][64] (128-byte swizzle)
 // Staging of the stores, one box per epilogue warp: BF16 [32 rows][64 columns],
-// with remainders two of [32][32], one for them; FP32 [32][32].
+// with parts two of [32][32], taken in turns; FP32 [32][32].
 __host__ __device__ constexpr uint32_t ce_stage_warp(int epi) {
     return epi != kCeStats ? kCeWideBox : 0u;
 }
@@ -70,10 +70,17 @@ constexpr size_t ce_smem(int epi) {
 constexpr int kCeFewThreads = 1024;   // per SM, of the kernel for one token (half of it for more)
 // The rows of h that it keeps: up to four CTAs of this and their own 1 KB fit an SM.
 constexpr size_t kCeFewSmem = 48 * 1024;
-// Stages that one accumulator adds up where the results are FP32: the tensor
-// cores' sums lose about 2e-8 of their value a step of 16 (they truncate), 6e-5
-// over 50021 vocabulary entries in two parts; 16 stages are 128 steps.
-constexpr int kCeChain = 16;
+// Stages that one accumulator adds up.  The tensor cores' sums lose about 2e-8 of
+// their value a step of 16 (they truncate; 8 steps a stage), 6e-5 over 50021
+// vocabulary entries in one chain.  Chains add up in registers: those of 8 stages
+// keep the loss and lse of any width where D 1024 has them (relative error 5e-7;
+// D 4096 in one chain 2e-6), and cost a wide D nothing (8192 tokens x 65536 entries at
+// D 2048: 4.49 ms with and without).  FP32 gradients, dh and dw of 2048 x 25088 at
+// D 1024 and the error of dw: chains of 2 stages 471 us and 3.7e-7, 3: 391 and 5.1e-7,
+// 4: 378 and 6.5e-7, 8: 366 and 1.3e-6.
+__host__ __device__ constexpr int ce_chain(int epi) {
+    return epi == kCeStats || epi == kCeDz ? 8 : epi == kCeDz3 ? 4 : 3;
+}
 
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -162,9 +169,9 @@ __device__ __forceinline__ float ce_tanh_small(float x) {
 // epilogues back, for the others.  Each element goes by its own size alone, so
 // that no result depends on its neighbours in the warp (rows past the matrix among
 // them, whose accumulators hold anything); the warp decides together only whether
-// any element needs tanhf (2048 tokens x 50021 entries at D 1024, cap 30, the
-// statistics and dz in two parts: 145 and 168 us with logits of deviation 2.5, 163
-// and 199 by tanhf alone; 200 and 262 with deviation 10, where most warps form both).
+// any element needs tanhf (2048 tokens x 50021 entries at D 1024, cap 30: statistics
+// 145 us with logits of deviation 2.5, 163 by tanhf alone; 200 with deviation 10,
+// where most warps form both).
 __device__ __forceinline__ void ce_tanh(const CeGemmArgs& a, float (&v)[2][16]) {
     float top = 0.f;
 #pragma unroll
@@ -185,10 +192,21 @@ __device__ __forceinline__ void ce_tanh(const CeGemmArgs& a, float (&v)[2][16]) 
     }
 }
 
-// Forward epilogue of one row: (max, sum e^{z - max}) of its 128 columns.
+// The next 32 of this lane's 128 sums; the others move up (a loop over them needs
+// registers by constant number).
+__device__ __forceinline__ void ce_take(float (&sum)[kCeN / 2], float (&v)[2][16]) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = sum[j];
+#pragma unroll
+    for (int j = 0; j < kCeN / 2 - 32; ++j) sum[j] = sum[j + 32];
+}
+
+// Forward epilogue of one row: (max, sum e^{z - max}) of its 128 columns, read
+// from its accumulator or (CHAINS) from `sums`.
 // Columns past the vocabulary do not count; the target's logit is kept.
-template <bool CAP>
-__device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& it, int row, uint32_t taddr, int half) {
+template <bool CAP, bool CHAINS>
+__device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& it, int row, uint32_t taddr, int half,
+                                             float (&sums)[kCeN / 2]) {
     const int t = it.m0 + row;
     const int c0 = half * (kCeN / 2);
     const int v0 = it.nt * kCeN + c0;            // vocabulary index of the first column
@@ -198,9 +216,13 @@ __device__ __forceinline__ void ce_epi_stats(const CeGemmArgs& a, const CeItem& 
     long long tgt = -1;
     if (ok) tgt = a.target[t] - v0;
     float mx = -INFINITY, sum = 0.f;
+#pragma unroll 1
     for (int c = 0; c < kCeN / 2; c += 32) {
         float v[2][16];
-        ce_columns(taddr + (uint32_t)(c0 + c), v);
+        if (CHAINS)
+            ce_take(sums, v);
+        else
+            ce_columns(taddr + (uint32_t)(c0 + c), v);
         if (CAP) ce_tanh(a, v);
         if (!ok || c >= nv) continue;
         float z[32];
@@ -294,16 +316,17 @@ __device__ __forceinline__ void ce_rows_of_h(const CeGemmArgs& a, int warp, int 
     }
 }
 
-// Tensor maps of both contractions: A, A's remainders, B, the BF16 result (s2: dz's remainders).
+// Tensor maps of both contractions: A's parts, B, the result (more: dz's second and third parts).
 struct CeMaps {
-    CUtensorMap a[2], a2[2], b[2], s[2], s2;
+    CUtensorMap a[kCeParts][2], b[2], s[2], more[kCeParts - 1];
 };
 
-template <int EPI, bool CAP>
+// CHAINS: the axis in chains of ce_chain stages, added up in registers.
+template <int EPI, bool CAP, bool CHAINS>
 __global__ void __launch_bounds__(kCeThreads, 1)
     ce_gemm_kernel(const __grid_constant__ CeMaps tm, const __grid_constant__ CeGemmArgs a) {
-    constexpr bool GRADS = EPI == kCeGrads || EPI == kCeGrads2, CHAINS = EPI == kCeGrads2;
-    constexpr int S = kCeStages;
+    constexpr bool GRADS = EPI == kCeGrads || EPI == kCeGrads3;
+    constexpr int S = kCeStages, kChain = ce_chain(EPI);
     extern __shared__ uint8_t ce_raw[];
     // s_full and s_free are used in the even CTA, the others in both
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_acc[2], s_free[2], s_fin;
@@ -351,7 +374,7 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             for (int k = 0; !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k) {
                 const CeSide& c = a.c[it.side];
                 const bool tn = GRADS && it.side == 1;
-                const CUtensorMap *ta1 = &tm.a[it.side], *ta2 = &tm.a2[it.side], *tb = &tm.b[it.side];
+                const CUtensorMap* tb = &tm.b[it.side];
                 for (int ks = it.k0; ks < it.k1; ++ks, ++n) {
                     const int slot = (int)(n % S);
                     if (n >= (uint32_t)S && !mbar_wait_bounded(&s_empty[slot], ((n / S) - 1) & 1u)) {
@@ -361,11 +384,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     if (*abort_flag) break;
                     uint8_t* sa = ring + (size_t)slot * kCeStageBytes;
                     uint8_t* sb = sa + kCeABytes;
-                    // the remainders of dz follow its leading parts along K
-                    const bool second = GRADS && ks >= c.part_steps;
-                    const int k0 = kCeK * (second ? ks - c.part_steps : ks);
+                    // the parts of dz follow each other along K
+                    const int part = EPI != kCeGrads3 ? 0 : (ks >= c.part_steps) + (ks >= 2 * c.part_steps);
+                    const int k0 = kCeK * (ks - part * c.part_steps);
                     const int n0 = it.nt * kCeN + 128 * rank;
-                    const CUtensorMap* ta = second ? ta2 : ta1;
+                    const CUtensorMap* ta = &tm.a[part][it.side];
                     // both CTAs' bytes are announced by the even one (the odd one's may land first)
                     // rows of A past the matrix (of K-major A past the next eight) are not loaded:
                     // what their accumulator rows hold is not used
@@ -407,8 +430,8 @@ __global__ void __launch_bounds__(kCeThreads, 1)
             for (int k = 0; ok && !*abort_flag && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k) {
                 const bool tn = GRADS && it.side == 1;   // A MN-major too
                 const uint32_t idesc = umma_idesc_bf16(kCeM, kCeN) | (tn ? (1u << 15) : 0u) | (GRADS ? (1u << 16) : 0u);
-                for (int k0 = it.k0; ok && k0 < it.k1; k0 += kCeChain, ++use) {
-                    const int k1 = CHAINS ? min(k0 + kCeChain, it.k1) : it.k1;
+                for (int k0 = it.k0; ok && k0 < it.k1; k0 += kChain, ++use) {
+                    const int k1 = CHAINS ? min(k0 + kChain, it.k1) : it.k1;
                     const uint32_t buf = use & 1u;
                     // both CTAs' epilogues have drained this accumulator's previous contents
                     if (use >= 2 && !mbar_wait_cluster(&s_free[buf], ((use >> 1) - 1) & 1u)) {
@@ -462,29 +485,43 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         // the common factor of the tokens' weights: left out of dz, put on its products
         float common = 1.f;
         if (EPI != kCeStats && a.weights != nullptr) common = ce_largest_weight(a, &s_weight);
-        if ((EPI == kCeDz || EPI == kCeDz2) && a.rows_out != nullptr) ce_rows_of_h(a, warp, lane);
+        if ((EPI == kCeDz || EPI == kCeDz3) && a.rows_out != nullptr) ce_rows_of_h(a, warp, lane);
         if (GRADS && a.total != nullptr && a.total[1] > 0.f) common = 1.f / a.total[1];
         for (int k = 0; !__any_sync(0xffffffffu, *abort_flag) && ce_item(a, GRADS, pair, pairs, k, rank, it); ++k, ++use) {
             const CeSide& c0 = a.c[it.side];
             const uint32_t buf = use & 1u;
+            // what a row needs besides its logits is fetched while the tile is computed
+            float wgt = 0.f, lse2 = 0.f;
+            long long tgt = -1;
+            if (EPI == kCeDz || EPI == kCeDz3) {
+                const int t = it.m0 + row;
+                if (t < c0.M) {
+                    const long long tg = a.target[t];
+                    tgt = tg - c0.b_row - (long long)it.nt * kCeN;
+                    // a row without a valid target adds nothing to the gradients
+                    if (tg >= 0 && tg < a.V)
+                        wgt = a.dloss != nullptr ? a.dloss[t] : a.weights != nullptr ? ce_ratio(a.weights[t], common) : 1.f;
+                    lse2 = a.lse[t] * kLog2e;
+                }
+            }
+            const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
+            float sum[kCeN / 2];   // (CHAINS)
             if (CHAINS) {
-                // each accumulator holds at most kCeChain stages; they add up in registers
-                float sum[kCeN / 2];
+                // each accumulator holds at most kChain stages; they add up in registers
 #pragma unroll
                 for (int j = 0; j < kCeN / 2; ++j) sum[j] = 0.f;
                 bool lost = false;
-                for (int k0 = it.k0; k0 < it.k1; k0 += kCeChain, ++use) {
+                for (int k0 = it.k0; k0 < it.k1; k0 += kChain, ++use) {
                     const uint32_t b = use & 1u;
                     if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_acc[b], (use >> 1) & 1u))) {
                         lost = true;
                         break;
                     }
                     tmem_fence_after_sync();
-                    const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + b * (uint32_t)kCeN + hf * (kCeN / 2);
 #pragma unroll
                     for (int c = 0; c < kCeN / 2; c += 32) {
                         float v[2][16];
-                        ce_columns(taddr + (uint32_t)c, v);
+                        ce_columns(lanes + b * (uint32_t)kCeN + hf * (kCeN / 2) + (uint32_t)c, v);
 #pragma unroll
                         for (int j = 0; j < 32; ++j) sum[c + j] += v[j / 16][j % 16];
                     }
@@ -497,33 +534,20 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                     break;
                 }
                 --use;   // the loop over the items counts the last one
+            } else {
+                if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_acc[buf], (use >> 1) & 1u))) {
+                    if (lane == 0) fail();
+                    break;
+                }
+                tmem_fence_after_sync();
+            }
+            const uint32_t taddr = lanes + buf * (uint32_t)kCeN;   // (not CHAINS)
+            if (EPI == kCeStats) {
+                ce_epi_stats<CAP, CHAINS>(a, it, row, taddr, hf, sum);
+            } else if (EPI == kCeGrads3) {
 #pragma unroll
                 for (int c = 0; c < kCeN / 2; c += 32)
                     ce_store_f32(tm.s[it.side], c0, it, &sum[c], common, stg, hf * (kCeN / 2) + c, q4, lane);
-                continue;
-            }
-            // what a row needs besides its logits is fetched while the tile is computed
-            float wgt = 0.f, lse2 = 0.f;
-            long long tgt = -1;
-            if (EPI == kCeDz || EPI == kCeDz2) {
-                const int t = it.m0 + row;
-                if (t < c0.M) {
-                    const long long tg = a.target[t];
-                    tgt = tg - c0.b_row - (long long)it.nt * kCeN;
-                    // a row without a valid target adds nothing to the gradients
-                    if (tg >= 0 && tg < a.V)
-                        wgt = a.dloss != nullptr ? a.dloss[t] : a.weights != nullptr ? ce_ratio(a.weights[t], common) : 1.f;
-                    lse2 = a.lse[t] * kLog2e;
-                }
-            }
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&s_acc[buf], (use >> 1) & 1u))) {
-                if (lane == 0) fail();
-                break;
-            }
-            tmem_fence_after_sync();
-            const uint32_t taddr = tmem + ((uint32_t)(32 * q4) << 16) + buf * (uint32_t)kCeN;
-            if (EPI == kCeStats) {
-                ce_epi_stats<CAP>(a, it, row, taddr, hf);
             } else if (GRADS && c0.part != nullptr) {
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
                     float v[2][16];
@@ -532,15 +556,18 @@ __global__ void __launch_bounds__(kCeThreads, 1)
                 }
             } else {
                 // BF16 results by TMA stores from swizzled staging, 32 columns at a time
-                constexpr int kBoxes = EPI == kCeDz2 ? 2 : 1;
+                constexpr bool PARTS = EPI == kCeDz3;
                 const int y = c0.s_row + it.m0 + 32 * q4;
                 const bool store = it.m0 + 32 * q4 < c0.M;   // rows past the matrix are clipped by the TMA
                 const int nv = c0.N - it.nt * kCeN;                 // columns of this tile inside the matrix
 #pragma unroll 1
                 for (int c = hf * (kCeN / 2); c < (hf + 1) * (kCeN / 2); c += 32) {
-                    float v[2][16], lo[2][16];
-                    ce_columns(taddr + (uint32_t)c, v);
-                    if (EPI == kCeDz || EPI == kCeDz2) {
+                    float v[2][16];
+                    if (CHAINS)
+                        ce_take(sum, v);
+                    else
+                        ce_columns(taddr + (uint32_t)c, v);
+                    if (EPI == kCeDz || EPI == kCeDz3) {
                         if (CAP) ce_tanh(a, v);
                         const bool mine = tgt >= c && tgt < c + 32;   // a lane in many
                         float one = wgt;   // what the target's 1 becomes
@@ -572,44 +599,65 @@ __global__ void __launch_bounds__(kCeThreads, 1)
 #pragma unroll
                             for (int j = 0; j < 32; ++j) v[j / 16][j % 16] = 0.f;
                         }
-                        if (EPI == kCeDz2) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                const float e = v[j / 16][j % 16];
-                                lo[j / 16][j % 16] = e - __bfloat162float(__float2bfloat16_rn(e));
-                            }
-                        }
                     }
                     if (GRADS) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j / 16][j % 16] *= common;
                     }
+                    if (PARTS) {
+                        // each part is what BF16 holds of what the ones before it left (24 bits in all)
+                        const int x = it.nt * kCeN + c;
+#pragma unroll
+                        for (int p = 0; p < kCeParts; ++p) {
+                            const int box = (p + (c / 32) * kCeParts) & 1;   // the two boxes in turns
+                            if (lane == 0) bulk_wait_read<1>();              // the store before the last has read it
+                            __syncwarp();
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int pu = u ^ ((lane >> 1) & 3);
+                                float* e = v[u >> 1] + 8 * (u & 1);
+                                const uint4 q = pack8(e);
+                                *reinterpret_cast<uint4*>(stg + (size_t)box * kCeBox + (size_t)lane * 64 + 16 * pu) = q;
+                                if (p + 1 < kCeParts) {
+                                    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                                    for (int k = 0; k < 4; ++k) {
+                                        const float2 f = bf2_to_f2(w[k]);
+                                        e[2 * k] -= f.x;
+                                        e[2 * k + 1] -= f.y;
+                                    }
+                                }
+                            }
+                            fence_proxy_async();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (store && x < c0.s_cols)
+                                    tma_store_2d(p == 0 ? &tm.s[it.side] : &tm.more[p == 2], x, y,
+                                                 stg + (size_t)box * kCeBox);
+                                bulk_commit();   // (an empty group keeps the count)
+                            }
+                        }
+                        continue;
+                    }
                     const bool second = (c & 32) != 0;   // of a wide box
-                    if ((kBoxes == 2 || !second) && lane == 0) bulk_wait_read<0>();   // the box is read out
+                    if (!second && lane == 0) bulk_wait_read<0>();   // the box is read out
                     __syncwarp();
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
-                        if (kBoxes == 2) {
-                            const int pu = u ^ ((lane >> 1) & 3);
-                            *reinterpret_cast<uint4*>(stg + (size_t)lane * 64 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
-                            *reinterpret_cast<uint4*>(stg + kCeBox + (size_t)lane * 64 + 16 * pu) =
-                                pack8(lo[u >> 1] + 8 * (u & 1));
-                        } else {
-                            const int pu = (u + (second ? 4 : 0)) ^ (lane & 7);
-                            *reinterpret_cast<uint4*>(stg + (size_t)lane * 128 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
-                        }
+                        const int pu = (u + (second ? 4 : 0)) ^ (lane & 7);
+                        *reinterpret_cast<uint4*>(stg + (size_t)lane * 128 + 16 * pu) = pack8(v[u >> 1] + 8 * (u & 1));
                     }
-                    if (kBoxes == 1 && !second) continue;
+                    if (!second) continue;
                     fence_proxy_async();
                     __syncwarp();
-                    const int x = it.nt * kCeN + c - (kBoxes == 1 ? 32 : 0);
+                    const int x = it.nt * kCeN + c - 32;
                     if (lane == 0 && store && x < c0.s_cols) {
                         tma_store_2d(&tm.s[it.side], x, y, stg);
-                        if (EPI == kCeDz2) tma_store_2d(&tm.s2, x, y, stg + kCeBox);
                         bulk_commit();
                     }
                 }
             }
+            if (CHAINS) continue;   // the accumulators are free already
             tmem_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(cluster_map(&s_free[buf], 0));
@@ -956,9 +1004,9 @@ constexpr int kCeEpiSteps = 4;
 int ce_item_steps(const CeSide& c) { return std::max(kCeEpiSteps, c.ksteps / c.splits); }
 int ce_pairs() { return std::max(1, block_gemm_sms() / 2); }
 
-template <int EPI, bool CAP>
+template <int EPI, bool CAP, bool CHAINS>
 cudaError_t ce_launch(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl) {
-    auto* fn = ce_gemm_kernel<EPI, CAP>;
+    auto* fn = ce_gemm_kernel<EPI, CAP, CHAINS>;
     constexpr size_t smem = ce_smem(EPI);
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kCeThreads);
@@ -990,7 +1038,7 @@ cudaError_t ce_launch(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl)
     cfg.gridDim = dim3(2u * (unsigned)pairs);
     // the pairs left with one dh item less make up for its K steps in dw items
     a.extra = 0;
-    if ((EPI == kCeGrads || EPI == kCeGrads2) && a.c[0].n_items % pairs != 0)
+    if ((EPI == kCeGrads || EPI == kCeGrads3) && a.c[0].n_items % pairs != 0)
         a.extra = (2 * ce_item_steps(a.c[0]) + ce_item_steps(a.c[1])) / (2 * ce_item_steps(a.c[1]));
     if (pdl) {
         attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1006,7 +1054,7 @@ int ce_m_tiles(long long M) { return (int)((M + kCeM - 1) / kCeM); }
 int ce_n_tiles(long long N) { return (int)((N + kCeN - 1) / kCeN); }
 
 // Splits of the K axes of dh [T][D] (K = the piece of V) and dw [piece][D]
-// (K = T), `parts` times as long with remainders: no item longer than a pair's
+// (K = T), `parts` times as long: no item longer than a pair's
 // share of all the steps (or 8 steps), so that a long axis with few tiles
 // around it is spread over the pairs.
 void ce_grad_splits(long long T, long long V, long long D, int parts, int sms, int* h_splits, int* w_splits) {
@@ -1031,12 +1079,17 @@ void ce_side(CeSide& c, int parts) {
     c.n_items = c.m_tiles * c.n_tiles * c.splits;
 }
 
+template <int EPI, bool CHAINS>
+cudaError_t ce_logits_as(const CeMaps& tm, CeGemmArgs& a, cudaStream_t s, bool pdl) {
+    return a.softcap > 0.f ? ce_launch<EPI, true, CHAINS>(tm, a, s, pdl) : ce_launch<EPI, false, CHAINS>(tm, a, s, pdl);
+}
+
 }  // namespace
 
 // Logits of h [T][D] and rows a.c[0].b_row on of w [V][D]: their statistics,
-// or dz [T][ldz] (and its remainders dz2); ldz is a multiple of 64.
-cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w, int V, void* dz, void* dz2,
-                             long long ldz, cudaStream_t s, bool pdl) {
+// or dz [T][ldz] in `parts` parts (one, or kCeParts); ldz is a multiple of 64.
+cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w, int V, void* dz, int parts,
+                             size_t part_bytes, long long ldz, cudaStream_t s, bool pdl) {
     CeGemmArgs a = in;
     CeSide& c = a.c[0];
     ce_side(c, 1);
@@ -1045,18 +1098,27 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
     a.whole = c.K % 64 == 0;
     const int rows = ce_a_rows(c.M);
     a.a_chunk = rows * 128;
-    if (!ce_operand(&tm.a[0], h, c.K, c.M, c.K, a.whole, rows) || !ce_operand(&tm.b[0], w, c.K, V, c.K, a.whole))
+    if (!ce_operand(&tm.a[0][0], h, c.K, c.M, c.K, a.whole, rows) || !ce_operand(&tm.b[0], w, c.K, V, c.K, a.whole))
         return cudaErrorInvalidValue;
-    tm.s[0] = tm.s2 = tm.a[0];
-    if (dz != nullptr && !ce_result(&tm.s[0], dz, c.s_cols, c.M, ldz, dz2 == nullptr)) return cudaErrorInvalidValue;
-    if (dz2 != nullptr && !ce_result(&tm.s2, dz2, c.s_cols, c.M, ldz, false)) return cudaErrorInvalidValue;
-    tm.a[1] = tm.a2[0] = tm.a2[1] = tm.b[1] = tm.s[1] = tm.a[0];
+    for (auto& row : tm.a) row[0] = row[1] = tm.a[0][0];
+    tm.b[1] = tm.b[0];
+    for (auto* m : {&tm.s[0], &tm.s[1], &tm.more[0], &tm.more[1]}) *m = tm.a[0][0];
+    for (int p = 0; dz != nullptr && p < parts; ++p)
+        if (!ce_result(p == 0 ? &tm.s[0] : &tm.more[p - 1], static_cast<char*>(dz) + p * part_bytes, c.s_cols, c.M, ldz,
+                       parts == 1))
+            return cudaErrorInvalidValue;
     // 32 MB of h per group of row tiles
     a.group = (int)std::max(1LL, std::min<long long>(c.m_tiles, (32LL << 20) / ((long long)c.K * 2 * kCeM)));
-    const bool cap = a.softcap > 0.f;
-    if (dz == nullptr) return cap ? ce_launch<kCeStats, true>(tm, a, s, pdl) : ce_launch<kCeStats, false>(tm, a, s, pdl);
-    if (dz2 == nullptr) return cap ? ce_launch<kCeDz, true>(tm, a, s, pdl) : ce_launch<kCeDz, false>(tm, a, s, pdl);
-    return cap ? ce_launch<kCeDz2, true>(tm, a, s, pdl) : ce_launch<kCeDz2, false>(tm, a, s, pdl);
+    // dz goes by the statistics' logits: their truncations meet in e^{z - lse} and mostly cancel
+    bool chains = c.ksteps > ce_chain(kCeStats);
+    if (dz != nullptr && parts > 1) {
+        // (few tokens' statistics have none to cancel)
+        chains = chains || (ce_is_few(c.M, c.K) && c.ksteps > ce_chain(kCeDz3));
+        return chains ? ce_logits_as<kCeDz3, true>(tm, a, s, pdl) : ce_logits_as<kCeDz3, false>(tm, a, s, pdl);
+    }
+    if (dz != nullptr)
+        return chains ? ce_logits_as<kCeDz, true>(tm, a, s, pdl) : ce_logits_as<kCeDz, false>(tm, a, s, pdl);
+    return chains ? ce_logits_as<kCeStats, true>(tm, a, s, pdl) : ce_logits_as<kCeStats, false>(tm, a, s, pdl);
 }
 
 // The statistics of T <= 4 tokens, one part a CTA.  Against 32768 x 1024 (67 MB
@@ -1087,28 +1149,29 @@ cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cud
 
 // a.c[0]: dh [T][D] (+)= dz w's rows b_row on; a.c[1]: dw = dz^T h, rows s_row
 // on of a matrix [V][D].  Each as FP32 into its `part`, or as BF16 into S.
-cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, const void* dz2, long long ldz, const void* h,
-                            const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl) {
+cudaError_t launch_ce_grads(const CeGemmArgs& in, const void* dz, int parts, size_t part_bytes, long long ldz,
+                            const void* h, const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl) {
     CeGemmArgs a = in;
-    const int parts = dz2 != nullptr ? 2 : 1;
     ce_side(a.c[0], parts);
     ce_side(a.c[1], parts);
     const long long T = a.c[0].M, D = a.c[0].N;
     CeMaps tm;
-    const void* second = dz2 != nullptr ? dz2 : dz;
     a.whole = D % 64 == 0;   // dz's own rows always are
     const int rows = ce_a_rows((int)T);
     a.a_chunk = rows * 128;
-    if (!ce_operand(&tm.a[0], dz, ldz, T, ldz, true, rows) || !ce_operand(&tm.a2[0], second, ldz, T, ldz, true, rows) ||
-        !ce_operand(&tm.a[1], dz, ldz, T, ldz, true) || !ce_operand(&tm.a2[1], second, ldz, T, ldz, true) ||
-        !ce_operand(&tm.b[0], w, D, V, D, a.whole) || !ce_operand(&tm.b[1], h, D, T, D, a.whole))
+    for (int p = 0; p < kCeParts; ++p) {
+        const void* part = static_cast<const char*>(dz) + (p < parts ? p : 0) * part_bytes;
+        if (!ce_operand(&tm.a[p][0], part, ldz, T, ldz, true, rows) || !ce_operand(&tm.a[p][1], part, ldz, T, ldz, true))
+            return cudaErrorInvalidValue;
+    }
+    if (!ce_operand(&tm.b[0], w, D, V, D, a.whole) || !ce_operand(&tm.b[1], h, D, T, D, a.whole))
         return cudaErrorInvalidValue;
-    tm.s2 = tm.a[0];
+    tm.more[0] = tm.more[1] = tm.a[0][0];
     if (!(a.c[0].part != nullptr ? ce_result_f32(&tm.s[0], a.c[0]) : ce_result(&tm.s[0], dh, D, T, D, true)) ||
         !(a.c[1].part != nullptr ? ce_result_f32(&tm.s[1], a.c[1]) : ce_result(&tm.s[1], dw, D, V, D, true)))
         return cudaErrorInvalidValue;
-    if (dz2 != nullptr) return ce_launch<kCeGrads2, false>(tm, a, s, pdl);
-    return ce_launch<kCeGrads, false>(tm, a, s, pdl);
+    if (parts > 1) return ce_launch<kCeGrads3, false, true>(tm, a, s, pdl);
+    return ce_launch<kCeGrads, false, false>(tm, a, s, pdl);
 }
 
 // Rows per CTA of the statistics kernel: 32 (a warp reads 32 rows of one part),

@@ -533,9 +533,10 @@ cudaError_t launch_join_fwd(const void* gv, const void* ym, void* j, long long B
 // Softmax cross entropy over a vocabulary (ce_gemm.cu).
 // ---------------------------------------------------------------------------
 // What the contraction kernel does: (max, sum of exponentials) of the logits;
-// dz in BF16; dz as BF16 leading parts and remainders; dh and dw together, from
-// either (the latter in FP32).
-enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz2 = 2, kCeGrads = 3, kCeGrads2 = 4 };
+// dz in BF16; dz as the sum of three BF16 parts; dh and dw together, from either
+// (the latter in FP32).
+enum CeEpiKind { kCeStats = 0, kCeDz = 1, kCeDz3 = 2, kCeGrads = 3, kCeGrads3 = 4 };
+constexpr int kCeParts = 3;
 constexpr int kCeSplitsMax = 32;
 
 // One contraction, M x N over K.
@@ -571,13 +572,13 @@ struct CeGemmArgs {
 int ce_m_tiles(long long M);
 int ce_n_tiles(long long N);
 void ce_grad_splits(long long T, long long V, long long D, int parts, int sms, int* h_splits, int* w_splits);
-cudaError_t launch_ce_logits(const CeGemmArgs& a, const void* h, const void* w, int V, void* dz, void* dz2,
-                             long long ldz, cudaStream_t s, bool pdl);
+cudaError_t launch_ce_logits(const CeGemmArgs& a, const void* h, const void* w, int V, void* dz, int parts,
+                             size_t part_bytes, long long ldz, cudaStream_t s, bool pdl);
 bool ce_is_few(int T, int D);
 int ce_few_parts(int T, int sms);
 cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl);
-cudaError_t launch_ce_grads(const CeGemmArgs& a, const void* dz, const void* dz2, long long ldz, const void* h,
-                            const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl);
+cudaError_t launch_ce_grads(const CeGemmArgs& a, const void* dz, int parts, size_t part_bytes, long long ldz,
+                            const void* h, const void* w, int V, void* dh, void* dw, cudaStream_t s, bool pdl);
 int ce_row_ctas(int T);
 cudaError_t launch_ce_rows(const float2* stats, const float* zt, const int64_t* target, int parts, int T, int V,
                            float* loss, float* lse, int4* sums, float* total, uint32_t* ticket, uint32_t* status,

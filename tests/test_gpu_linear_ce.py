@@ -456,3 +456,19 @@ def test_pieces_of_the_vocabulary_with_weights_and_a_cap(fp32):
     rest = torch.ones(T, dtype=torch.bool, device=DEV)
     rest[keep] = False
     assert not b["dh"][rest].any()
+
+
+@pytest.mark.parametrize("T,V,D", [(3, 3000, 4096), (200, 1000, 4096), (300, 5000, 256), (2000, 300, 64), (9000, 40, 64),
+                                   (256, 3000, 2056)])
+def test_fp32_results_are_fp32(T, V, D):
+    """Relative L2 errors of everything that is FP32 stay below 1e-6.  The tensor cores truncate their sums, about
+    2e-8 of the value a step of 16 products; a chain of a logit has 64 steps (1.3e-6 of a number that lse and the
+    exponentials see with the same error), a chain of a gradient 24 (5e-7); dz is held to 24 bits (6e-8); FP32 and the
+    fast exponentials add 2e-7."""
+    h, w, t = _inputs(T, V, D, 90 + D, ignored=0.1 if T > 8 else 0.0)
+    dloss = torch.rand(T, generator=torch.Generator().manual_seed(91)).to(DEV) / T
+    f = api.linear_ce_forward(h, w, t)
+    b = api.linear_ce_backward(h, w, t, f["lse"], dloss, grad_fp32=True)
+    exact = _exact(h, w, t, dloss)
+    for got, ref in zip((f["loss"], f["lse"], b["dh"], b["dw"]), exact):
+        assert _rel(_f64(got), ref) <= 1e-6

@@ -1092,6 +1092,13 @@ int check_ce_shape(int T, int V, int D) {
 }
 
 bool softcap_ok(float c) { return c >= 0.f && c <= 3e38f; }
+// The cap as the kernels use it: within 2^-100 and 2^100, so that neither its
+// inverse nor its products overflow.  Outside, FP32 sees no difference (capped
+// logits of 2^-100 are 0 next to 1; a cap of 2^100 leaves logits below 2^88 alone).
+void set_softcap(CeGemmArgs& g, float c) {
+    g.softcap = c > 0.f ? std::min(std::max(c, 0x1p-100f), 0x1p100f) : 0.f;
+    g.inv_softcap = c > 0.f ? 1.f / g.softcap : 0.f;
+}
 
 // The forward's scratch.
 struct CeForward {
@@ -1171,8 +1178,7 @@ int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T
     g.zt = at<float>(scratch, l.zt);
     g.target = target;
     g.V = V;
-    g.softcap = softcap;
-    g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
+    set_softcap(g, softcap);
     g.status = status;
     g.clear = 1;
     int parts = 2 * ce_n_tiles(V);
@@ -1232,8 +1238,7 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
             g.rows_out = static_cast<uint4*>(hw);
         }
         g.lse = lse;
-        g.softcap = softcap;
-        g.inv_softcap = softcap > 0.f ? 1.f / softcap : 0.f;
+        set_softcap(g, softcap);
         g.status = status;
         LRS_LAUNCH(KID_CE_GEMM, stream,
                    launch_ce_logits(g, h, w, V, dz, l.parts, l.part_bytes, l.ldz, stream, pdl_ok()));

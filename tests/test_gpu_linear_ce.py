@@ -472,3 +472,19 @@ def test_fp32_results_are_fp32(T, V, D):
     exact = _exact(h, w, t, dloss)
     for got, ref in zip((f["loss"], f["lse"], b["dh"], b["dw"]), exact):
         assert _rel(_f64(got), ref) <= 1e-6
+
+
+@pytest.mark.parametrize("T", [2, 40])
+@pytest.mark.parametrize("softcap", [1e-44, 1e-39, 1e-38, 1e20, 2.5e38, 3e38])
+def test_caps_at_the_ends_of_their_range(T, softcap):
+    """Next to nothing (every capped logit is 0 to FP32: the loss is log V) and next to no cap at all.  (A tiny cap's
+    gradient is 0 where its logit is not.)"""
+    h, w, t = _inputs(T, 300, 64, 100)
+    softcap = float(np.float32(softcap))
+    _check(h, w, t, softcap=softcap)
+    _check(h, w, t, softcap=softcap, fp32=True)
+    h[0] = 0   # logits of exactly 0
+    f = api.linear_ce_forward(h, w, t, softcap=softcap)
+    b = api.linear_ce_backward(h, w, t, f["lse"], total=f["total"], softcap=softcap)
+    assert abs(float(f["loss"][0]) - np.log(300)) <= TOL_ROW
+    assert torch.isfinite(b["dh"]).all() and torch.isfinite(b["dw"]).all()

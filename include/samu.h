@@ -518,7 +518,7 @@ int linear_ce_backward(const void* h, const void* w, const int64_t* target, cons
  *   u = scale * GeLU(gate) * RMSNorm(y; gamma_post),  r = x + u,
  *   h = RMSNorm(r; gamma_pre),   RMSNorm(a; g) = a / sqrt(mean(a^2) + eps) * g,
  * row by row over [T,D], with the block's GeLU (tanh form).  FP32 arithmetic
- * throughout; r and h are rounded to BF16 once (h is formed from the unrounded r).
+ * throughout (the GeLU, by the GPU's fast exponential, within 2^-20); r and h are rounded to BF16 once (h is formed from the unrounded r).
  * With y NULL there is no branch: h = RMSNorm(x; gamma_pre), the norm ahead of
  * a head; gate, gamma_post, scale and r are then NULL too.
  *

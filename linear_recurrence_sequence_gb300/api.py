@@ -920,7 +920,7 @@ KERNEL_NAMES = {
     13: "samu_decode_step_kernel", 14: "proj_gemm_kernel<logits>", 15: "proj_gemm_kernel<dx, dW>",
     16: "proj_pack_kernel", 17: "block_gemm_kernel", 18: "rmsnorm_kernels", 19: "conv_kernels",
     20: "join_fwd_kernel", 21: "sum_parts_kernel", 22: "ce_gemm_kernel", 23: "ce_rows_kernels",
-    24: "gated_norm_kernels", 25: "sum_parts_kernel", 26: "adamw_norm_kernel", 27: "adamw_update_kernel",
+    24: "gated_norm_kernels", 25: "gated_norm_sum_kernel", 26: "adamw_norm_kernel", 27: "adamw_update_kernel",
 }
 
 

@@ -1121,10 +1121,11 @@ cudaError_t launch_ce_logits(const CeGemmArgs& in, const void* h, const void* w,
     return chains ? ce_logits_as<kCeStats, true>(tm, a, s, pdl) : ce_logits_as<kCeStats, false>(tm, a, s, pdl);
 }
 
-// The statistics of T <= 4 tokens, one part a CTA.  Against 32768 x 1024 (67 MB
-// of w not in the L2, forward with its second kernel) 1, 2 and 4 tokens took 21,
-// 22 and 26 us, 29 by the tensor-core tiles, which from 6 on were faster (30
-// against 34 us); the second kernel has since got 3 us shorter for both.
+// The statistics of T <= 4 tokens, one part a CTA, as long as their rows fit.
+// Events around the launch, w not in the L2, for 1, 2, 3 and 4 tokens (the
+// tensor-core tiles, which take 5 and more: the last figure): 32768 x 1024 21, 21,
+// 23, 23 (27) us; 32768 x 4096 56, 52, 62, 62 (70); 32768 x 8192 101, 93, 112, - (119);
+// 5000 x 2048 21, 16, 15, 15 (23).
 bool ce_is_few(int T, int D) { return T <= 4 && (size_t)T * D * 2 <= kCeFewSmem; }
 int ce_few_parts(int T, int sms) { return kCeFewThreads / 256 / (T == 1 ? 1 : 2) * sms; }
 cudaError_t launch_ce_few(const CeGemmArgs& a, const void* h, const void* w, cudaStream_t s, bool pdl) {

@@ -488,3 +488,13 @@ def test_caps_at_the_ends_of_their_range(T, softcap):
     b = api.linear_ce_backward(h, w, t, f["lse"], total=f["total"], softcap=softcap)
     assert abs(float(f["loss"][0]) - np.log(300)) <= TOL_ROW
     assert torch.isfinite(b["dh"]).all() and torch.isfinite(b["dw"]).all()
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("softcap", [0.0, 5.0, 30.0])
+@pytest.mark.parametrize("T,V,D", [(70, 600, 1032), (260, 300, 2112), (4, 515, 1088)])
+def test_logits_of_more_than_one_chain(T, V, D, softcap, fp32):
+    h, w, t = _inputs(T, V, D, 110 + D, ignored=0.1 if T > 8 else 0.0)
+    dloss = torch.rand(T, generator=torch.Generator().manual_seed(111)).to(DEV) / T
+    _check(h, w, t, softcap=softcap, fp32=fp32)
+    _check(h, w, t, softcap=softcap, dloss=dloss, fp32=fp32)

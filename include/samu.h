@@ -81,8 +81,8 @@ int lrs_version(void);
  * of the calls below; every call clears the word when it starts, so it covers
  * the most recent call).  SYNCHRONISES `stream`.  *status receives LRS_OK or
  * LRS_ERR_TIMEOUT (LRS_ERR_CUDA if a kernel found its shared memory
- * misaligned and copied nothing; LRS_ERR_ARG if linear_ce_forward met a
- * target past the vocabulary).  Returns LRS_ERR_ARG / LRS_ERR_CUDA on failure. */
+ * misaligned and copied nothing; LRS_ERR_ARG if linear_ce_forward or
+ * embedding_backward met a token past the vocabulary).  Returns LRS_ERR_ARG / LRS_ERR_CUDA on failure. */
 int lrs_device_status(void* scratch, int* status, cudaStream_t stream);
 
 /* Self-test of the failure path of the bounded device-side waits: launches
@@ -111,7 +111,11 @@ int lrs_selftest_wait_timeout(void* scratch, cudaStream_t stream);
  * contractions, 18 RecurrentBlock RMSNorm (forward and backward), 19 its
  * convolution, 20 its join, 21 its fixed-order gradient sums, 22 the vocabulary
  * loss's contractions, 23 its row statistics and sums, 24 the gated norm, 25 its
- * gradient sums, 26 AdamW's gradient norm, 27 its update; 9 also covers
+ * gradient sums, 26 AdamW's gradient norm, 27 its update, 28 the selective scan's
+ * forward maps, 29 its prefixes, 30 its replay, 31 its step, 32 its reverse maps,
+ * 33 its backward, 34 its gradient sums, 35 the causal convolution, 36 its step,
+ * 37 its backward, 38 its gradient sums, 39 the embedding lookup, 40 the sort of its
+ * tokens, 41 its gradient; 9 also covers
  * the bias-gradient reductions) and duration in
  * milliseconds; *count receives the number of
  * kernels launched while profiling was on.  Not thread-safe: one profiling
@@ -603,6 +607,177 @@ int lrs_adamw_scratch_bytes(int count, size_t* bytes);
  * LRS_ERR_UNSUPPORTED (over 2^40 values), LRS_ERR_CUDA. */
 int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, const float* lr, double beta1,
                    double beta2, float eps, float max_norm, float* norm, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Rows with strides                                                         */
+/* ======================================================================== */
+
+/* [B,L] rows of values that are contiguous within a row: a part of a wider
+ * projection's output need not be copied out.  Strides in elements.  Where an
+ * entry reads rows 16 bytes at a time (all but b and c of the scan), data is
+ * 16-byte aligned and both strides are multiples of 8; an input's strides may be
+ * 0 (one row for all), an output's rows must not overlap. */
+typedef struct {
+    void* data;
+    int64_t batch_stride, token_stride;
+} lrs_rows;
+
+/* ======================================================================== */
+/* Short causal convolution                                                  */
+/* ======================================================================== */
+
+/* The convolution ahead of a recurrent mixer, every channel with its own taps:
+ *   pre_t = bias + sum_{j < W} w_j x_{t-j},   y_t = SiLU(pre_t) (silu != 0) or pre_t.
+ * A sequence start (reset[b,t] != 0) at t - j + 1 .. t cuts tap j, as in the
+ * RecurrentBlock.  Inputs before the row come from `state`: its rows are the W - 1
+ * inputs before the first token, in their order (NULL: zeros).  W is 2, 3 or 4.
+ * FP32 arithmetic, one rounding to BF16 (SiLU by the GPU's fast exponential and
+ * reciprocal, 2^-20 relative).
+ *
+ * Scratch bytes of the backward.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as causal_conv_forward. */
+int causal_conv_workspace_bytes(int B, int L, int D, int W, size_t* backward_bytes);
+
+/* Forward.
+ *   x          [B,L] rows of D BF16 (in)
+ *   weight     [W,D] FP32 (in): row j multiplies the input j tokens earlier
+ *   bias       [D] FP32 (in) or NULL
+ *   state      [B,W-1,D] BF16 (in) or NULL
+ *   reset      [B,L] bytes (in) or NULL
+ *   y          [B,L,D] BF16 (out)
+ *   state_out  [B,W-1,D] BF16 (out) or NULL: the state after the row, zeros in
+ *              place of inputs before the last sequence's start.  Not `state` itself.
+ * Rows padded on the left, with a reset at the first token, give every sequence its
+ * own state_out.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a shape below 1, state_out
+ * equal to state), LRS_ERR_UNSUPPORTED (D not a multiple of 8, W not 2 to 4, over
+ * 2^30 tokens or 2^40 values), LRS_ERR_CUDA. */
+int causal_conv_forward(const lrs_rows* x, const float* weight, const float* bias, const void* state,
+                        const uint8_t* reset, int B, int L, int D, int W, int silu, void* y, void* state_out,
+                        cudaStream_t stream);
+
+/* One token of each of B sequences: x is [B] rows (token_stride is not used),
+ * reset [B], y [B,D]; the state moves on in place.  Bit for bit what the forward
+ * gives for the same inputs.  Errors: as the forward. */
+int causal_conv_step(const lrs_rows* x, const float* weight, const float* bias, void* state, const uint8_t* reset,
+                     int B, int D, int W, int silu, void* y, cudaStream_t stream);
+
+/* Backward for the cotangent dy [B,L,D] BF16.
+ *   x ... silu  the forward's (in)
+ *   dx       [B,L] rows (out), dstate [B,W-1,D] (out) or NULL: BF16 or FP32 by
+ *            grad_dtype.  A cotangent of state_out is the caller's to add to dx.
+ *   dweight  [W,D] FP32 (out);  dbias [D] FP32 (out) or NULL
+ *   scratch  causal_conv_workspace_bytes() bytes
+ * Sums in a fixed order.  Errors: as the forward, plus LRS_ERR_ARG for dstate
+ * without state and for an unknown grad_dtype. */
+int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight, const float* bias, const void* state,
+                         const uint8_t* reset, int B, int L, int D, int W, int silu, const lrs_rows* dx, float* dweight,
+                         float* dbias, void* dstate, int grad_dtype, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Selective state space scan                                                */
+/* ======================================================================== */
+
+/* A recurrent mixer beside SAMU and the RG-LRU: every channel has N real states
+ * whose decay and input follow the token,
+ *   dt_t  = softplus(delta_t + delta_bias),   a_tn = e^(-e^(a_log_n) dt_t)
+ *   h_tn  = a_tn h_{t-1,n} + dt_t x_t b_tn    (a_tn = 0 where reset[b,t] != 0)
+ *   y_t   = (sum_n c_tn h_tn + d_skip x_t) SiLU(gate_t).
+ * dt, x, gate and d_skip are a channel's own, b and c are shared by a token's
+ * channels.  A token whose delta is -inf has dt = 0: it leaves the state as it is
+ * (padding behind a sequence; padding ahead of one is cut off by a reset at its
+ * first token).  D channels, N from 1 to 64.
+ * FP32 arithmetic: exponentials by the GPU's fast one (2^-22 relative each), dt within
+ * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0); y is rounded
+ * to BF16 once.  Everything runs in a fixed order.
+ *
+ * Bytes of `saved` (what the forward keeps for a backward: the states before every
+ * eighth token, 4 N bytes for 8 values of x), of the forward's and of the backward's
+ * scratch.  Any output pointer may be NULL.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as selective_scan_forward. */
+int selective_scan_workspace_bytes(int B, int L, int D, int N, size_t* saved_bytes, size_t* forward_bytes,
+                                   size_t* backward_bytes);
+
+/* Forward.
+ *   x, delta    [B,L] rows of D BF16 (in)
+ *   a_log       [D,N] FP32 (in)
+ *   b, c        [B,L] rows of N BF16 (in; any alignment and strides)
+ *   d_skip      [D] FP32 (in) or NULL for zeros
+ *   delta_bias  [D] FP32 (in) or NULL for zeros
+ *   gate        [B,L] rows of D BF16 (in), or NULL for 1 in place of SiLU(gate)
+ *   h0          [B,D,N] FP32 (in) or NULL for zeros
+ *   reset       [B,L] bytes (in) or NULL
+ *   y           [B,L,D] BF16 (out);  hT [B,D,N] FP32 (out; may be h0)
+ *   saved       selective_scan_workspace_bytes().saved bytes (out), or NULL where no
+ *               backward follows
+ *   scratch     .forward bytes
+ * One launch, or three where batch and channels alone leave the GPU short of work.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a shape below 1),
+ * LRS_ERR_UNSUPPORTED (D not a multiple of 8, N over 64, over 2^30 tokens or 2^40
+ * values or states), LRS_ERR_CUDA. */
+int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
+                           const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
+                           const float* h0, const uint8_t* reset, int B, int L, int D, int N, void* y, float* hT,
+                           void* saved, void* scratch, cudaStream_t stream);
+
+/* One token of each of B sequences: x, delta, b, c, gate are [B] rows (token_stride
+ * is not used), reset [B], y [B,D] BF16 (out); state [B,D,N] FP32 moves on in place.
+ * One launch.  Errors: as the forward. */
+int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
+                        const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
+                        float* state, const uint8_t* reset, int B, int D, int N, void* y, cudaStream_t stream);
+
+/* Backward for the cotangents dy [B,L,D] BF16 of y and dhT [B,D,N] FP32 of hT (or
+ * NULL for zeros).
+ *   x ... reset  the forward's (in; h0 is not read: saved holds it);  saved: the forward's
+ *   dx, ddelta, dgate  [B,L] rows of D (out), db, dc [B,L,N] (out): BF16 or FP32 by
+ *            grad_dtype.  dgate is NULL without a gate.
+ *   da_log   [D,N] FP32 (out)
+ *   dd_skip, ddelta_bias  [D] FP32 (out) or NULL (and NULL without the vector)
+ *   dh0      [B,D,N] FP32 (out) or NULL
+ *   scratch  selective_scan_workspace_bytes().backward bytes
+ * Errors: as the forward, plus LRS_ERR_ARG for an output without its input and for an
+ * unknown grad_dtype. */
+int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x, const lrs_rows* delta,
+                            const float* a_log, const lrs_rows* b, const lrs_rows* c, const float* d_skip,
+                            const float* delta_bias, const lrs_rows* gate, const uint8_t* reset, int B, int L, int D,
+                            int N, const void* saved, const lrs_rows* dx, const lrs_rows* ddelta, float* da_log, void* db,
+                            void* dc, float* dd_skip, float* ddelta_bias, const lrs_rows* dgate, float* dh0,
+                            int grad_dtype, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Embedding                                                                 */
+/* ======================================================================== */
+
+/* The lookup at the bottom of a stack, y_t = scale w[token_t], and its gradient,
+ *   dw[v] = scale sum of dy_t over the tokens t with token_t = v.
+ * A negative token is padding: a row of zeros that reaches no gradient.  A token
+ * >= V has no row: its y is NaN, it reaches no gradient, and lrs_device_status
+ * returns LRS_ERR_ARG for the backward's scratch.
+ *
+ * Scratch bytes of the backward.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as embedding_forward. */
+int embedding_workspace_bytes(int T, int V, int D, size_t* backward_bytes);
+
+/* Forward.
+ *   tokens   [T] int64 (in; 8-byte aligned)
+ *   w        [V,D] (in), BF16 or FP32 by w_dtype (LRS_GRAD_BF16, LRS_GRAD_FP32)
+ *   y        [T,D] BF16 (out), rounded once
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, unknown w_dtype,
+ * scale not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8 or over 2^16, V over
+ * 2^23, T over 2^28), LRS_ERR_CUDA. */
+int embedding_forward(const int64_t* tokens, const void* w, int w_dtype, int T, int V, int D, float scale, void* y,
+                      cudaStream_t stream);
+
+/* Backward for the cotangent dy [T,D] BF16.
+ *   dw       [V,D] BF16 or FP32 by grad_dtype (out; with accumulate != 0 the gradient
+ *            is added to what dw holds, rows without a token are left as they are: a
+ *            matrix that the head shares, or several batches)
+ *   scratch  embedding_workspace_bytes() bytes
+ * FP32 sums in a fixed order (the tokens', in runs of 32), rounded once.
+ * Errors: as the forward, plus LRS_ERR_ARG for an unknown grad_dtype. */
+int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int D, float scale, void* dw, int grad_dtype,
+                       int accumulate, void* scratch, cudaStream_t stream);
 
 /* ======================================================================== */
 /* SAMU forward without allocation                                           */

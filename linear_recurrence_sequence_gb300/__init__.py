@@ -15,6 +15,9 @@ __all__ = [
     "linear_ce_workspace_bytes", "linear_ce_forward", "linear_ce_backward",
     "gated_norm_workspace_bytes", "gated_norm_forward", "gated_norm_backward",
     "adamw_state", "adamw_plan", "adamw_step",
+    "causal_conv_workspace_bytes", "causal_conv_forward", "causal_conv_step", "causal_conv_backward",
+    "selective_scan_workspace_bytes", "selective_scan_forward", "selective_scan_step", "selective_scan_backward",
+    "embedding_workspace_bytes", "embedding_forward", "embedding_backward",
     "device_status", "library_path",
 ]
 

@@ -69,6 +69,17 @@ _SIGNATURES = {
     "gated_norm_workspace_bytes": ([_I, _I, _SZP, _SZP], _I),
     "gated_norm_forward": ([_P] * 6 + [_I, _I, _F] + [_P] * 4, _I),
     "gated_norm_backward": ([_P] * 8 + [_I, _I, _F] + [_P] * 9, _I),
+    "causal_conv_workspace_bytes": ([_I] * 4 + [_SZP], _I),
+    "causal_conv_forward": ([_P] * 5 + [_I] * 5 + [_P] * 3, _I),
+    "causal_conv_step": ([_P] * 5 + [_I] * 4 + [_P] * 2, _I),
+    "causal_conv_backward": ([_P] * 6 + [_I] * 5 + [_P] * 4 + [_I] + [_P] * 2, _I),
+    "selective_scan_workspace_bytes": ([_I] * 4 + [_SZP] * 3, _I),
+    "selective_scan_forward": ([_P] * 10 + [_I] * 4 + [_P] * 5, _I),
+    "selective_scan_step": ([_P] * 10 + [_I] * 3 + [_P] * 2, _I),
+    "selective_scan_backward": ([_P] * 11 + [_I] * 4 + [_P] * 10 + [_I] + [_P] * 2, _I),
+    "embedding_workspace_bytes": ([_I] * 3 + [_SZP], _I),
+    "embedding_forward": ([_P] * 2 + [_I] * 4 + [_F] + [_P] * 2, _I),
+    "embedding_backward": ([_P] * 2 + [_I] * 3 + [_F, _P] + [_I] * 2 + [_P] * 2, _I),
     "lrs_adamw_scratch_bytes": ([_I, _SZP], _I),
     "lrs_adamw_step": ([_P, _I, _P, _P, _D, _D, _F, _F] + [_P] * 3, _I),
 }
@@ -774,6 +785,305 @@ def gated_norm_backward(dr, dh, x, y, gate, gamma_post, scale, gamma_pre, saved,
 
 
 # ---------------------------------------------------------------------------
+# Rows with strides (lrs_rows, include/samu.h)
+# ---------------------------------------------------------------------------
+class _Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("batch_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+def _rows(t, name, dtype, device, shape, vector=True):
+    """t, [B, L, width] or (a step's) [B, width], as an lrs_rows: contiguous within a row, any strides between rows
+    (multiples of 8 elements where the rows are read 16 bytes at a time)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name}: expected device {device}, got {t.device}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous within a row")
+    # the stride of a dimension of one has no meaning
+    batch = st[0] if shape[0] > 1 else 0
+    token = st[1] if len(shape) == 3 and shape[1] > 1 else 0
+    if vector and (batch % 8 or token % 8 or t.data_ptr() % 16):
+        raise ValueError(f"{name}: rows must start on 16-byte boundaries (strides that are multiples of 8)")
+    return _Rows(t.data_ptr(), batch, token)
+
+
+def _out_rows(shape, dtype, device, out, key):
+    """An output of rows: (tensor, lrs_rows).  The caller's may have strides between rows that do not overlap."""
+    if out is None or out.get(key) is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        return t, _Rows(t.data_ptr(), shape[1] * shape[2], shape[2])
+    t = out[key]
+    r = _rows(t, key, dtype, device, shape)
+    B, L, width = shape
+    if (L > 1 and r.token_stride < width) or (B > 1 and r.batch_stride < (L - 1) * r.token_stride + width):
+        raise ValueError(f"{key}: rows overlap")
+    return t, r
+
+
+def _ref(rows):
+    return None if rows is None else ctypes.addressof(rows)
+
+
+# ---------------------------------------------------------------------------
+# Short causal convolution
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def causal_conv_workspace_bytes(B: int, L: int, D: int, W: int) -> int:
+    """Scratch bytes of the convolution's backward."""
+    n = ctypes.c_size_t(0)
+    _check("causal_conv_workspace_bytes", _load().causal_conv_workspace_bytes(B, L, D, W, ctypes.byref(n)))
+    return int(n.value)
+
+
+def _conv_inputs(x, weight, bias, state, reset):
+    dev, shape = x.device, x.shape
+    if len(shape) != 3:
+        raise ValueError(f"x: expected shape (B, L, D), got {tuple(shape)}")
+    B, L, D = shape
+    _need(weight, "weight", torch.float32, dev)
+    if weight.dim() != 2 or weight.shape[1] != D:
+        raise ValueError(f"weight: expected shape (W, {D}), got {tuple(weight.shape)}")
+    W = weight.shape[0]
+    _opt(bias, "bias", torch.float32, dev, (D,))
+    _opt(state, "state", torch.bfloat16, dev, (B, W - 1, D))
+    _opt(reset, "reset", torch.uint8, dev, (B, L))
+    return dev, B, L, D, W, _rows(x, "x", torch.bfloat16, dev, shape)
+
+
+def causal_conv_forward(x, weight, bias=None, state=None, reset=None, *, silu=True, out=None):
+    """Causal convolution of every channel with its own taps, and SiLU, through ``causal_conv_forward``.
+
+    x: [B, L, D] BF16 (a view with strides between its rows will do); weight: [W, D] FP32, row j for the input j tokens
+    earlier; bias: [D] FP32; state: [B, W - 1, D] BF16, the inputs before x; reset: [B, L] uint8, sequence starts.
+    Returns dict(y, state), the state after x in a buffer of its own."""
+    dev, B, L, D, W, xr = _conv_inputs(x, weight, bias, state, reset)
+    y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
+    after = _empty((B, W - 1, D), torch.bfloat16, dev, out, "state")
+    st = _load().causal_conv_forward(_ref(xr), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), B, L, D, W,
+                                     1 if silu else 0, y.data_ptr(), after.data_ptr(), _stream(dev))
+    if st:
+        _check("causal_conv_forward", st)
+    return {"y": y, "state": after}
+
+
+def causal_conv_step(x, weight, bias, state, reset=None, *, silu=True, out=None):
+    """One token of each of B sequences through ``causal_conv_step``.  x: [B, D] BF16; state: [B, W - 1, D] BF16,
+    updated in place; reset: [B] uint8.  Returns dict(y, state)."""
+    dev, shape = x.device, x.shape
+    if len(shape) != 2:
+        raise ValueError(f"x: expected shape (B, D), got {tuple(shape)}")
+    B, D = shape
+    xr = _rows(x, "x", torch.bfloat16, dev, shape)
+    _need(weight, "weight", torch.float32, dev)
+    if weight.dim() != 2 or weight.shape[1] != D:
+        raise ValueError(f"weight: expected shape (W, {D}), got {tuple(weight.shape)}")
+    W = weight.shape[0]
+    _opt(bias, "bias", torch.float32, dev, (D,))
+    _need(state, "state", torch.bfloat16, dev, (B, W - 1, D))
+    _opt(reset, "reset", torch.uint8, dev, (B,))
+    y = _empty(shape, torch.bfloat16, dev, out, "y")
+    st = _load().causal_conv_step(_ref(xr), weight.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(reset), B, D, W,
+                                  1 if silu else 0, y.data_ptr(), _stream(dev))
+    if st:
+        _check("causal_conv_step", st)
+    return {"y": y, "state": state}
+
+
+def causal_conv_backward(dy, x, weight, bias=None, state=None, reset=None, *, silu=True, grad_fp32=False, out=None,
+                         scratch=None):
+    """Backward of causal_conv_forward (``causal_conv_backward``).
+
+    Returns dict(dx, dweight, dbias, dstate, scratch): dx and dstate BF16 or (grad_fp32) FP32, dbias None without a
+    bias, dstate None without a state."""
+    dev, B, L, D, W, xr = _conv_inputs(x, weight, bias, state, reset)
+    _need(dy, "dy", torch.bfloat16, dev, (B, L, D))
+    gdt = torch.float32 if grad_fp32 else torch.bfloat16
+    dx, dxr = _out_rows((B, L, D), gdt, dev, out, "dx")
+    o = {"dx": dx, "dweight": _empty((W, D), torch.float32, dev, out, "dweight"),
+         "dbias": None if bias is None else _empty((D,), torch.float32, dev, out, "dbias"),
+         "dstate": None if state is None else _empty((B, W - 1, D), gdt, dev, out, "dstate")}
+    scratch = _buffer(scratch, "scratch", causal_conv_workspace_bytes(B, L, D, W), dev)
+    st = _load().causal_conv_backward(dy.data_ptr(), _ref(xr), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), B,
+                                      L, D, W, 1 if silu else 0, _ref(dxr), o["dweight"].data_ptr(), _ptr(o["dbias"]),
+                                      _ptr(o["dstate"]), LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16,
+                                      scratch.data_ptr(), _stream(dev))
+    if st:
+        _check("causal_conv_backward", st)
+    o["scratch"] = scratch
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Selective state space scan
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def selective_scan_workspace_bytes(B: int, L: int, D: int, N: int):
+    """(saved, forward scratch, backward scratch) bytes of the selective scan."""
+    n = [ctypes.c_size_t(0) for _ in range(3)]
+    _check("selective_scan_workspace_bytes",
+           _load().selective_scan_workspace_bytes(B, L, D, N, *[ctypes.byref(v) for v in n]))
+    return tuple(int(v.value) for v in n)
+
+
+def _scan_inputs(x, delta, a_log, b, c, d_skip, delta_bias, gate, rank):
+    dev, shape = x.device, x.shape
+    if len(shape) != rank:
+        raise ValueError(f"x: expected shape ({'B, L, D' if rank == 3 else 'B, D'}), got {tuple(shape)}")
+    D = shape[-1]
+    _need(a_log, "a_log", torch.float32, dev)
+    if a_log.dim() != 2 or a_log.shape[0] != D:
+        raise ValueError(f"a_log: expected shape ({D}, N), got {tuple(a_log.shape)}")
+    N = a_log.shape[1]
+    bf, states = torch.bfloat16, (*shape[:-1], N)
+    rows = [_rows(x, "x", bf, dev, shape), _rows(delta, "delta", bf, dev, shape),
+            _rows(b, "b", bf, dev, states, False), _rows(c, "c", bf, dev, states, False),
+            None if gate is None else _rows(gate, "gate", bf, dev, shape)]
+    if d_skip is not None:
+        _need(d_skip, "d_skip", torch.float32, dev, (D,))
+    if delta_bias is not None:
+        _need(delta_bias, "delta_bias", torch.float32, dev, (D,))
+    return dev, D, N, rows
+
+
+def selective_scan_forward(x, delta, a_log, b, c, d_skip=None, delta_bias=None, gate=None, h0=None, reset=None, *,
+                           keep=True, out=None, saved=None, scratch=None):
+    """Selective state space scan through ``selective_scan_forward``.
+
+    x, delta, gate: [B, L, D] BF16, b, c: [B, L, N] BF16 (views with strides between their rows will do); a_log: [D, N]
+    FP32; d_skip, delta_bias: [D] FP32; h0: [B, D, N] FP32; reset: [B, L] uint8, sequence starts.  keep=False where no
+    backward follows (saved is then None).  Returns dict(y, hT, saved, scratch)."""
+    dev, D, N, (xr, dr, br, cr, gr) = _scan_inputs(x, delta, a_log, b, c, d_skip, delta_bias, gate, 3)
+    B, L = x.shape[:2]
+    _opt(h0, "h0", torch.float32, dev, (B, D, N))
+    _opt(reset, "reset", torch.uint8, dev, (B, L))
+    nsaved, nscratch, _ = selective_scan_workspace_bytes(B, L, D, N)
+    y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
+    hT = _empty((B, D, N), torch.float32, dev, out, "hT")
+    saved = _buffer(saved, "saved", nsaved, dev) if keep else None
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
+    st = _load().selective_scan_forward(_ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr), _ptr(d_skip),
+                                        _ptr(delta_bias), _ref(gr), _ptr(h0), _ptr(reset), B, L, D, N, y.data_ptr(),
+                                        hT.data_ptr(), _ptr(saved), scratch.data_ptr(), _stream(dev))
+    if st:
+        _check("selective_scan_forward", st)
+    return {"y": y, "hT": hT, "saved": saved, "scratch": scratch}
+
+
+def selective_scan_step(x, delta, a_log, b, c, d_skip, delta_bias, gate, state, reset=None, *, out=None):
+    """One token of each of B sequences through ``selective_scan_step``.  x, delta, gate: [B, D] BF16; b, c: [B, N]
+    BF16; state: [B, D, N] FP32, updated in place; reset: [B] uint8.  Returns dict(y, state)."""
+    dev, D, N, (xr, dr, br, cr, gr) = _scan_inputs(x, delta, a_log, b, c, d_skip, delta_bias, gate, 2)
+    B = x.shape[0]
+    _need(state, "state", torch.float32, dev, (B, D, N))
+    _opt(reset, "reset", torch.uint8, dev, (B,))
+    y = _empty((B, D), torch.bfloat16, dev, out, "y")
+    st = _load().selective_scan_step(_ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr), _ptr(d_skip),
+                                     _ptr(delta_bias), _ref(gr), state.data_ptr(), _ptr(reset), B, D, N, y.data_ptr(),
+                                     _stream(dev))
+    if st:
+        _check("selective_scan_step", st)
+    return {"y": y, "state": state}
+
+
+def selective_scan_backward(dy, dhT, x, delta, a_log, b, c, d_skip, delta_bias, gate, h0, reset, saved, *,
+                            grad_fp32=False, out=None, scratch=None):
+    """Backward of selective_scan_forward (``selective_scan_backward``).  dhT may be None (zero); of h0 only whether
+    there is one is looked at.
+
+    Returns dict(dx, ddelta, da_log, db, dc, dd_skip, ddelta_bias, dgate, dh0, scratch): dx, ddelta, db, dc, dgate BF16 or
+    (grad_fp32) FP32, the rest FP32; the gradient of an input that was None is None."""
+    dev, D, N, (xr, dr, br, cr, gr) = _scan_inputs(x, delta, a_log, b, c, d_skip, delta_bias, gate, 3)
+    B, L = x.shape[:2]
+    _need(dy, "dy", torch.bfloat16, dev, (B, L, D))
+    _opt(dhT, "dhT", torch.float32, dev, (B, D, N))
+    _opt(reset, "reset", torch.uint8, dev, (B, L))
+    nsaved, _, nscratch = selective_scan_workspace_bytes(B, L, D, N)
+    _saved(saved, nsaved, dev)
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
+    gdt, f32 = torch.float32 if grad_fp32 else torch.bfloat16, torch.float32
+    dx, dxr = _out_rows((B, L, D), gdt, dev, out, "dx")
+    dd, ddr = _out_rows((B, L, D), gdt, dev, out, "ddelta")
+    dg, dgr = (None, None) if gate is None else _out_rows((B, L, D), gdt, dev, out, "dgate")
+    o = {"dx": dx, "ddelta": dd, "da_log": _empty((D, N), f32, dev, out, "da_log"),
+         "db": _empty((B, L, N), gdt, dev, out, "db"), "dc": _empty((B, L, N), gdt, dev, out, "dc"),
+         "dd_skip": None if d_skip is None else _empty((D,), f32, dev, out, "dd_skip"),
+         "ddelta_bias": None if delta_bias is None else _empty((D,), f32, dev, out, "ddelta_bias"), "dgate": dg,
+         "dh0": None if h0 is None else _empty((B, D, N), f32, dev, out, "dh0")}
+    st = _load().selective_scan_backward(dy.data_ptr(), _ptr(dhT), _ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr),
+                                         _ptr(d_skip), _ptr(delta_bias), _ref(gr), _ptr(reset), B, L, D, N,
+                                         saved.data_ptr(), _ref(dxr), _ref(ddr), o["da_log"].data_ptr(),
+                                         o["db"].data_ptr(), o["dc"].data_ptr(), _ptr(o["dd_skip"]),
+                                         _ptr(o["ddelta_bias"]), _ref(dgr), _ptr(o["dh0"]),
+                                         LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16, scratch.data_ptr(), _stream(dev))
+    if st:
+        _check("selective_scan_backward", st)
+    o["scratch"] = scratch
+    return o
+
+
+# ---------------------------------------------------------------------------
+# Embedding
+# ---------------------------------------------------------------------------
+@functools.lru_cache(maxsize=1024)
+def embedding_workspace_bytes(T: int, V: int, D: int) -> int:
+    """Scratch bytes of the embedding's backward."""
+    n = ctypes.c_size_t(0)
+    _check("embedding_workspace_bytes", _load().embedding_workspace_bytes(T, V, D, ctypes.byref(n)))
+    return int(n.value)
+
+
+def embedding_forward(tokens, w, *, scale=1.0, out=None):
+    """y_t = scale w[token_t] through ``embedding_forward``.
+
+    tokens: [...] int64 (negative: padding, a row of zeros); w: [V, D] BF16 or FP32.  Returns dict(y), [..., D] BF16."""
+    dev = w.device
+    if w.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"w: expected torch.bfloat16 or torch.float32, got {w.dtype}")
+    _need(w, "w", w.dtype, dev)
+    if w.dim() != 2:
+        raise ValueError(f"w: expected shape (V, D), got {tuple(w.shape)}")
+    V, D = w.shape
+    _need(tokens, "tokens", torch.int64, dev)
+    y = _empty((*tokens.shape, D), torch.bfloat16, dev, out, "y")
+    st = _load().embedding_forward(tokens.data_ptr(), w.data_ptr(),
+                                   LRS_GRAD_FP32 if w.dtype is torch.float32 else LRS_GRAD_BF16, tokens.numel(), V, D,
+                                   scale, y.data_ptr(), _stream(dev))
+    if st:
+        _check("embedding_forward", st)
+    return {"y": y}
+
+
+def embedding_backward(dy, tokens, V, *, scale=1.0, accumulate=False, grad_fp32=False, out=None, scratch=None):
+    """Gradient of embedding_forward's matrix (``embedding_backward``).
+
+    dy: [..., D] BF16 cotangents; V: rows of the matrix.  With accumulate the gradient is added to out["dw"], as of a
+    matrix that the head shares.  Returns dict(dw, scratch), [V, D] BF16 or (grad_fp32) FP32."""
+    dev, shape = dy.device, dy.shape
+    if not shape:
+        raise ValueError("dy: expected shape (..., D)")
+    _need(dy, "dy", torch.bfloat16, dev)
+    _need(tokens, "tokens", torch.int64, dev, shape[:-1])
+    if accumulate and (out is None or out.get("dw") is None):
+        raise ValueError("accumulate adds to out[\"dw\"], which is required")
+    T, D = tokens.numel(), shape[-1]
+    nscratch = embedding_workspace_bytes(T, V, D)
+    dw = _empty((V, D), torch.float32 if grad_fp32 else torch.bfloat16, dev, out, "dw")
+    scratch = _buffer(scratch, "scratch", nscratch, dev)
+    st = _load().embedding_backward(dy.data_ptr(), tokens.data_ptr(), T, V, D, scale, dw.data_ptr(),
+                                    LRS_GRAD_FP32 if grad_fp32 else LRS_GRAD_BF16, 1 if accumulate else 0,
+                                    scratch.data_ptr(), _stream(dev))
+    if st:
+        _check("embedding_backward", st)
+    return {"dw": dw, "scratch": scratch}
+
+
+# ---------------------------------------------------------------------------
 # AdamW over many tensors
 # ---------------------------------------------------------------------------
 class _AdamwTensor(ctypes.Structure):
@@ -921,6 +1231,10 @@ KERNEL_NAMES = {
     16: "proj_pack_kernel", 17: "block_gemm_kernel", 18: "rmsnorm_kernels", 19: "conv_kernels",
     20: "join_fwd_kernel", 21: "sum_parts_kernel", 22: "ce_gemm_kernel", 23: "ce_rows_kernels",
     24: "gated_norm_kernels", 25: "gated_norm_sum_kernel", 26: "adamw_norm_kernel", 27: "adamw_update_kernel",
+    28: "ssm_maps_kernel", 29: "ssm_prefix_kernels", 30: "ssm_replay_kernel", 31: "ssm_step_kernel",
+    32: "ssm_rmaps_kernel", 33: "ssm_bwd_kernel", 34: "ssm_finish_kernel", 35: "causal_conv_fwd_kernel",
+    36: "causal_conv_step_kernel", 37: "causal_conv_bwd_kernel", 38: "causal_conv_sum_kernel",
+    39: "embedding_fwd_kernel", 40: "embedding_sort_kernel", 41: "embedding_sum_kernels",
 }
 
 

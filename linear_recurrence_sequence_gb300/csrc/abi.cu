@@ -84,7 +84,9 @@ enum {
     KID_SAMU_PARAMS, KID_RGLRU_SCAN_FWD, KID_RGLRU_SCAN_BWD, KID_RGLRU_ALPHA, KID_SAMU_FWD_MAPS,
     KID_SAMU_BWD_MAPS, KID_SAMU_DECODE_PREP, KID_SAMU_DECODE_STEP, KID_RGLRU_PROJ_FWD, KID_RGLRU_PROJ_BWD,
     KID_RGLRU_PROJ_PACK, KID_BLOCK_GEMM, KID_BLOCK_NORM, KID_BLOCK_CONV, KID_BLOCK_JOIN, KID_BLOCK_SUM, KID_CE_GEMM,
-    KID_CE_ROWS, KID_GATED_NORM, KID_GATED_NORM_SUM, KID_ADAMW_NORM, KID_ADAMW_UPDATE
+    KID_CE_ROWS, KID_GATED_NORM, KID_GATED_NORM_SUM, KID_ADAMW_NORM, KID_ADAMW_UPDATE, KID_SSM_MAPS, KID_SSM_PREFIX,
+    KID_SSM_REPLAY, KID_SSM_STEP, KID_SSM_BWD_MAPS, KID_SSM_BWD, KID_SSM_FINISH, KID_CONV_FWD, KID_CONV_STEP,
+    KID_CONV_BWD, KID_CONV_SUM, KID_EMBED_FWD, KID_EMBED_SORT, KID_EMBED_SUM
 };
 
 #define LRS_LAUNCH(id, stream, expr)            \
@@ -1446,6 +1448,390 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
         LRS_LAUNCH(KID_ADAMW_UPDATE, stream,
                    launch_adamw_update(tensors + i, std::min(kAdamCap, count - i), a, stream, pdl_ok()));
     }
+    return LRS_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Rows with strides
+// ---------------------------------------------------------------------------
+namespace {
+
+// [B,L] rows of a width's BF16 values, read 16 bytes at a time.
+bool rows_in_ok(const lrs_rows* r) {
+    return r != nullptr && req(r->data) && r->batch_stride >= 0 && r->token_stride >= 0 && r->batch_stride % 8 == 0 &&
+           r->token_stride % 8 == 0;
+}
+// The same, read a value at a time.
+bool rows_each_ok(const lrs_rows* r) {
+    return r != nullptr && req_each(static_cast<const uint16_t*>(r->data)) && r->batch_stride >= 0 && r->token_stride >= 0;
+}
+// An output's: rows that do not overlap.
+bool rows_out_ok(const lrs_rows* r, int B, int L, int width) {
+    return rows_in_ok(r) && (L == 1 || r->token_stride >= width) &&
+           (B == 1 || r->batch_stride >= (long long)(L - 1) * r->token_stride + width);
+}
+SsmRows rows_in(const lrs_rows* r) {
+    SsmRows o = {};
+    if (r != nullptr) o = {static_cast<const uint16_t*>(r->data), r->batch_stride, r->token_stride};
+    return o;
+}
+SsmOutRows rows_out(const lrs_rows* r) {
+    SsmOutRows o = {};
+    if (r != nullptr) o = {r->data, r->batch_stride, r->token_stride};
+    return o;
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Short causal convolution
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_conv_shape(int B, int L, int D, int W) {
+    if (B < 1 || L < 1 || D < 1 || W < 1) return LRS_ERR_ARG;
+    if (D % 8 != 0 || W < 2 || W > 4 || (long long)B * L > (1LL << 30) || (long long)B * L * D > (1LL << 40))
+        return LRS_ERR_UNSUPPORTED;
+    // CTAs of the launches, one for 64 tokens and 128 channels at least
+    if ((long long)B * ((L + 63) / 64) * ((D + 127) / 128) > 0x7fffffffLL) return LRS_ERR_UNSUPPORTED;
+    return LRS_OK;
+}
+
+ConvArgs conv_args(const lrs_rows* x, const float* weight, const float* bias, const void* state, const uint8_t* reset,
+                   int B, int L, int D, int W, int silu) {
+    ConvArgs a = {};
+    a.x = rows_in(x);
+    a.w = weight;
+    a.bias = bias;
+    a.state = static_cast<const uint16_t*>(state);
+    a.reset = reset;
+    a.B = B;
+    a.L = L;
+    a.D = D;
+    a.W = W;
+    a.silu = silu;
+    return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+int causal_conv_workspace_bytes(int B, int L, int D, int W, size_t* backward_bytes) {
+    const int st = check_conv_shape(B, L, D, W);
+    if (st != LRS_OK) return st;
+    if (backward_bytes != nullptr)
+        *backward_bytes = up256((size_t)conv_bwd_parts(B, L, D) * (W + 1) * D * sizeof(float));
+    return LRS_OK;
+}
+
+int causal_conv_forward(const lrs_rows* x, const float* weight, const float* bias, const void* state,
+                        const uint8_t* reset, int B, int L, int D, int W, int silu, void* y, void* state_out,
+                        cudaStream_t stream) {
+    const int st = check_conv_shape(B, L, D, W);
+    if (st != LRS_OK) return st;
+    if (!rows_in_ok(x) || !req(weight) || !opt(bias) || !opt(state) || !req(y) || !opt(state_out) ||
+        (state != nullptr && state_out == state))
+        return LRS_ERR_ARG;
+    ConvArgs a = conv_args(x, weight, bias, state, reset, B, L, D, W, silu);
+    a.y = static_cast<uint16_t*>(y);
+    a.state_out = static_cast<uint16_t*>(state_out);
+    LRS_LAUNCH(KID_CONV_FWD, stream, launch_causal_conv(a, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+int causal_conv_step(const lrs_rows* x, const float* weight, const float* bias, void* state, const uint8_t* reset,
+                     int B, int D, int W, int silu, void* y, cudaStream_t stream) {
+    const int st = check_conv_shape(B, 1, D, W);
+    if (st != LRS_OK) return st;
+    if (!rows_in_ok(x) || !req(weight) || !opt(bias) || !req(state) || !req(y)) return LRS_ERR_ARG;
+    ConvArgs a = conv_args(x, weight, bias, nullptr, reset, B, 1, D, W, silu);
+    a.y = static_cast<uint16_t*>(y);
+    a.state_out = static_cast<uint16_t*>(state);
+    LRS_LAUNCH(KID_CONV_STEP, stream, launch_causal_conv_step(a, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight, const float* bias, const void* state,
+                         const uint8_t* reset, int B, int L, int D, int W, int silu, const lrs_rows* dx, float* dweight,
+                         float* dbias, void* dstate, int grad_dtype, void* scratch, cudaStream_t stream) {
+    const int st = check_conv_shape(B, L, D, W);
+    if (st != LRS_OK) return st;
+    if (!req(dy) || !rows_in_ok(x) || !req(weight) || !opt(bias) || !opt(state) || !rows_out_ok(dx, B, L, D) ||
+        !req(dweight) || !opt(dbias) || !opt(dstate) || (state == nullptr && dstate != nullptr) || !req(scratch) ||
+        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32))
+        return LRS_ERR_ARG;
+    ConvBwdArgs g = {};
+    g.f = conv_args(x, weight, bias, state, reset, B, L, D, W, silu);
+    g.dy = static_cast<const uint16_t*>(dy);
+    g.dx = rows_out(dx);
+    g.dstate = dstate;
+    g.f32 = grad_dtype == LRS_GRAD_FP32;
+    g.parts = conv_bwd_parts(B, L, D);
+    g.part = static_cast<float*>(scratch);
+    g.dw = dweight;
+    g.dbias = dbias;
+    LRS_LAUNCH(KID_CONV_BWD, stream, launch_causal_conv_bwd(g, stream, pdl_ok()));
+    LRS_LAUNCH(KID_CONV_SUM, stream, launch_causal_conv_sum(g, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Selective state space scan
+// ---------------------------------------------------------------------------
+namespace {
+
+// Warps an SM that the chunks are to give: what the kernels' registers leave room for.
+constexpr int kSsmFwdWarps = 16, kSsmBwdWarps = 8;
+
+int check_ssm_shape(int B, int L, int D, int N) {
+    if (B < 1 || L < 1 || D < 1 || N < 1) return LRS_ERR_ARG;
+    if (D % 8 != 0 || N > 64 || (long long)B * L > (1LL << 30) || (long long)B * L * D > (1LL << 40) ||
+        (long long)B * D * N > (1LL << 40))
+        return LRS_ERR_UNSUPPORTED;
+    // CTAs of the launches: a warp's channels and 16 tokens each at least
+    const SsmSplit w = ssm_split(D, N);
+    if ((long long)B * ((L + 15) / 16) * w.groups > 0x7fffffffLL) return LRS_ERR_UNSUPPORTED;
+    return LRS_OK;
+}
+
+size_t ssm_tile_bytes(int D, int N) { return (size_t)ssm_split(D, N).groups * 256 * sizeof(float4); }
+size_t ssm_keep_bytes(int B, int L, int D, int N) {
+    return (size_t)B * ((L + kSsmKeep - 1) / kSsmKeep) * ssm_tile_bytes(D, N);
+}
+
+// Scratch of a direction: the chunks' states and sums of dt; the backward's partial sums.
+struct SsmScratch {
+    int chunk, nchunk;
+    long long part_len;
+    size_t maps, sums, dbc, part, total;
+};
+SsmScratch ssm_scratch(int B, int L, int D, int N, bool backward) {
+    SsmScratch s;
+    const SsmSplit w = ssm_split(D, N);
+    ssm_chunks(B, L, D, N, backward ? kSsmBwdWarps : kSsmFwdWarps, &s.chunk, &s.nchunk);
+    const size_t chunks = s.nchunk > 1 ? (size_t)B * s.nchunk : 0;
+    s.maps = 256;
+    s.sums = s.maps + up256(chunks * ssm_tile_bytes(D, N));
+    s.dbc = s.sums + up256(chunks * w.groups * w.channels * sizeof(float));
+    s.part = s.total = s.dbc;
+    s.part_len = (long long)w.groups * (256 + w.channels / 2);
+    if (backward) {
+        s.part = s.dbc + up256((size_t)B * L * w.ctas * 2 * (8 * w.lanes) * sizeof(float));
+        s.total = s.part + up256((size_t)B * s.nchunk * s.part_len * sizeof(float4));
+    }
+    return s;
+}
+
+bool ssm_inputs_ok(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b, const lrs_rows* c,
+                   const float* d_skip, const float* delta_bias, const lrs_rows* gate) {
+    return rows_in_ok(x) && rows_in_ok(delta) && req_each(a_log) && rows_each_ok(b) && rows_each_ok(c) && opt(d_skip) &&
+           opt(delta_bias) && (gate == nullptr || rows_in_ok(gate));
+}
+SsmArgs ssm_args(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b, const lrs_rows* c,
+                 const float* d_skip, const float* delta_bias, const lrs_rows* gate, const uint8_t* reset, int B, int L,
+                 int D, int N) {
+    SsmArgs a = {};
+    a.x = rows_in(x);
+    a.delta = rows_in(delta);
+    a.b = rows_in(b);
+    a.c = rows_in(c);
+    a.gate = rows_in(gate);
+    a.a_log = a_log;
+    a.d_skip = d_skip;
+    a.delta_bias = delta_bias;
+    a.reset = reset;
+    a.B = B;
+    a.L = L;
+    a.D = D;
+    a.N = N;
+    const SsmSplit w = ssm_split(D, N);
+    a.groups = w.groups;
+    a.ngq = w.ctas;
+    return a;
+}
+void ssm_place(SsmArgs& a, const SsmScratch& l, void* scratch) {
+    a.chunk = l.chunk;
+    a.nchunk = l.nchunk;
+    a.maps = at<float4>(scratch, l.maps);
+    a.sums = at<float>(scratch, l.sums);
+}
+
+}  // namespace
+
+extern "C" {
+
+int selective_scan_workspace_bytes(int B, int L, int D, int N, size_t* saved_bytes, size_t* forward_bytes,
+                                   size_t* backward_bytes) {
+    const int st = check_ssm_shape(B, L, D, N);
+    if (st != LRS_OK) return st;
+    if (saved_bytes != nullptr) *saved_bytes = ssm_keep_bytes(B, L, D, N);
+    if (forward_bytes != nullptr) *forward_bytes = ssm_scratch(B, L, D, N, false).total;
+    if (backward_bytes != nullptr) *backward_bytes = ssm_scratch(B, L, D, N, true).total;
+    return LRS_OK;
+}
+
+int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
+                           const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
+                           const float* h0, const uint8_t* reset, int B, int L, int D, int N, void* y, float* hT,
+                           void* saved, void* scratch, cudaStream_t stream) {
+    const int st = check_ssm_shape(B, L, D, N);
+    if (st != LRS_OK) return st;
+    if (!ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !opt(h0) || !req(y) || !req(hT) ||
+        !opt(saved) || !req(scratch))
+        return LRS_ERR_ARG;
+    SsmArgs a = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);
+    ssm_place(a, ssm_scratch(B, L, D, N, false), scratch);
+    a.h0 = h0;
+    a.y = static_cast<uint16_t*>(y);
+    a.hT = hT;
+    a.keep = static_cast<float4*>(saved);
+    if (a.nchunk > 1) {
+        LRS_LAUNCH(KID_SSM_MAPS, stream, launch_ssm_maps(a, stream, pdl_ok()));
+        LRS_LAUNCH(KID_SSM_PREFIX, stream, launch_ssm_prefix(a, false, stream, pdl_ok()));
+    }
+    LRS_LAUNCH(KID_SSM_REPLAY, stream, launch_ssm_replay(a, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
+                        const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
+                        float* state, const uint8_t* reset, int B, int D, int N, void* y, cudaStream_t stream) {
+    const int st = check_ssm_shape(B, 1, D, N);
+    if (st != LRS_OK) return st;
+    if (!ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !req(state) || !req(y)) return LRS_ERR_ARG;
+    SsmArgs a = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, 1, D, N);
+    a.y = static_cast<uint16_t*>(y);
+    LRS_LAUNCH(KID_SSM_STEP, stream, launch_ssm_step(a, state, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x, const lrs_rows* delta,
+                            const float* a_log, const lrs_rows* b, const lrs_rows* c, const float* d_skip,
+                            const float* delta_bias, const lrs_rows* gate, const uint8_t* reset, int B, int L, int D,
+                            int N, const void* saved, const lrs_rows* dx, const lrs_rows* ddelta, float* da_log, void* db,
+                            void* dc, float* dd_skip, float* ddelta_bias, const lrs_rows* dgate, float* dh0,
+                            int grad_dtype, void* scratch, cudaStream_t stream) {
+    const int st = check_ssm_shape(B, L, D, N);
+    if (st != LRS_OK) return st;
+    if (!req(dy) || !opt(dhT) || !ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !req(saved) ||
+        !rows_out_ok(dx, B, L, D) || !rows_out_ok(ddelta, B, L, D) || !req(da_log) || !req(db) || !req(dc) ||
+        !opt(dd_skip) || (d_skip == nullptr && dd_skip != nullptr) || !opt(ddelta_bias) ||
+        (delta_bias == nullptr && ddelta_bias != nullptr) ||
+        (gate != nullptr ? !rows_out_ok(dgate, B, L, D) : dgate != nullptr) || !opt(dh0) || !req(scratch) ||
+        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32))
+        return LRS_ERR_ARG;
+    const SsmScratch l = ssm_scratch(B, L, D, N, true);
+    SsmBwdArgs g = {};
+    g.f = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);
+    ssm_place(g.f, l, scratch);
+    g.f.h0 = dhT;
+    g.f.keep = static_cast<float4*>(const_cast<void*>(saved));
+    g.dy = static_cast<const uint16_t*>(dy);
+    g.dx = rows_out(dx);
+    g.ddelta = rows_out(ddelta);
+    g.dgate = rows_out(dgate);
+    g.f32 = grad_dtype == LRS_GRAD_FP32;
+    g.db = db;
+    g.dc = dc;
+    g.dbc = at<float>(scratch, l.dbc);
+    g.part = at<float4>(scratch, l.part);
+    g.part_len = l.part_len;
+    g.da_log = da_log;
+    g.dd_skip = dd_skip;
+    g.ddelta_bias = ddelta_bias;
+    g.dh0 = dh0;
+    if (g.f.nchunk > 1) {
+        LRS_LAUNCH(KID_SSM_BWD_MAPS, stream, launch_ssm_rmaps(g, stream, pdl_ok()));
+        LRS_LAUNCH(KID_SSM_PREFIX, stream, launch_ssm_prefix(g.f, true, stream, pdl_ok()));
+    }
+    LRS_LAUNCH(KID_SSM_BWD, stream, launch_ssm_bwd(g, stream, pdl_ok()));
+    LRS_LAUNCH(KID_SSM_FINISH, stream, launch_ssm_finish(g, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// Embedding
+// ---------------------------------------------------------------------------
+namespace {
+
+int check_embed_shape(int T, int V, int D) {
+    if (T < 1 || V < 1 || D < 1) return LRS_ERR_ARG;
+    if (D % 8 != 0 || T > (1 << 28) || V > (1 << 23) || D > (1 << 16)) return LRS_ERR_UNSUPPORTED;
+    return LRS_OK;
+}
+
+struct EmbedScratch {
+    size_t list, place, first, part, total;
+};
+EmbedScratch embed_scratch(int T, int V, int D) {
+    EmbedScratch s;
+    const long long owners = embed_owners(V), rows = (V + owners - 1) / owners;
+    s.list = 256;
+    s.place = s.list + up256((size_t)T * sizeof(int2));
+    s.first = s.place + up256((size_t)T * sizeof(int2));
+    s.part = s.first + up256((size_t)(owners * rows + 1) * sizeof(int));
+    s.total = s.part + up256((size_t)2 * embed_chunks(T) * D * sizeof(float));
+    return s;
+}
+
+}  // namespace
+
+extern "C" {
+
+int embedding_workspace_bytes(int T, int V, int D, size_t* backward_bytes) {
+    const int st = check_embed_shape(T, V, D);
+    if (st != LRS_OK) return st;
+    if (backward_bytes != nullptr) *backward_bytes = embed_scratch(T, V, D).total;
+    return LRS_OK;
+}
+
+int embedding_forward(const int64_t* tokens, const void* w, int w_dtype, int T, int V, int D, float scale, void* y,
+                      cudaStream_t stream) {
+    const int st = check_embed_shape(T, V, D);
+    if (st != LRS_OK) return st;
+    if (!req_each(tokens) || !req(w) || !req(y) || (w_dtype != LRS_GRAD_BF16 && w_dtype != LRS_GRAD_FP32) ||
+        !std::isfinite(scale))
+        return LRS_ERR_ARG;
+    EmbedArgs a = {tokens, w, T, V, D, w_dtype == LRS_GRAD_FP32, scale, static_cast<uint16_t*>(y)};
+    LRS_LAUNCH(KID_EMBED_FWD, stream, launch_embedding(a, stream, pdl_ok()));
+    return LRS_OK;
+}
+
+int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int D, float scale, void* dw, int grad_dtype,
+                       int accumulate, void* scratch, cudaStream_t stream) {
+    const int st = check_embed_shape(T, V, D);
+    if (st != LRS_OK) return st;
+    if (!req(dy) || !req_each(tokens) || !req(dw) || !req(scratch) ||
+        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) || !std::isfinite(scale))
+        return LRS_ERR_ARG;
+    const EmbedScratch l = embed_scratch(T, V, D);
+    EmbedBwdArgs a = {};
+    a.tokens = tokens;
+    a.dy = static_cast<const uint16_t*>(dy);
+    a.T = T;
+    a.V = V;
+    a.D = D;
+    a.scale = scale;
+    a.dw = dw;
+    a.f32 = grad_dtype == LRS_GRAD_FP32;
+    a.accumulate = accumulate != 0;
+    a.status = at<uint32_t>(scratch, 0);
+    a.owners = embed_owners(V);
+    a.list = at<int2>(scratch, l.list);
+    a.place = at<int2>(scratch, l.place);
+    a.count = at<int>(scratch, 64);
+    a.first = at<int>(scratch, l.first);
+    a.part = at<float>(scratch, l.part);
+    LRS_LAUNCH(KID_EMBED_SORT, stream, launch_embedding_sort(a, stream, pdl_ok()));
+    LRS_LAUNCH(KID_EMBED_SUM, stream, launch_embedding_sum(a, stream, pdl_ok()));
+    LRS_LAUNCH(KID_EMBED_SUM, stream, launch_embedding_join(a, stream, pdl_ok()));
     return LRS_OK;
 }
 

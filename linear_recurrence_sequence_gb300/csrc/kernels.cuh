@@ -644,4 +644,122 @@ size_t adam_scratch_bytes(int count);
 cudaError_t launch_adamw_norm(const AdamTensor* ts, int count, const AdamArgs& a, int* ctas, cudaStream_t s, bool pdl);
 cudaError_t launch_adamw_update(const AdamTensor* ts, int count, const AdamArgs& a, cudaStream_t s, bool pdl);
 
+// ---------------------------------------------------------------------------
+// Rows of BF16 (or, as an output, FP32) values: [B][L] of them, each contiguous.
+// ---------------------------------------------------------------------------
+struct SsmRows {
+    const uint16_t* p;
+    long long sb, st;            // elements from one batch row to the next, from one token to the next
+};
+struct SsmOutRows {
+    void* p;
+    long long sb, st;
+};
+
+// ---------------------------------------------------------------------------
+// Selective state space scan (ssm_scan.cu, ssm_scan_bwd.cu).
+// ---------------------------------------------------------------------------
+constexpr int kSsmKeep = 8;      // tokens between the states that a forward keeps for its backward
+struct SsmArgs {
+    SsmRows x, delta, b, c, gate;   // gate.p null: none
+    const float* a_log;          // [D][N]
+    const float* d_skip;         // [D] or null (zeros)
+    const float* delta_bias;     // [D] or null (zeros)
+    const float* h0;             // [B][D][N] or null (zeros); in the backward the cotangent of the last state
+    const uint8_t* reset;        // [B][L] or null
+    int B, L, D, N;
+    int groups, ngq;             // warps' groups of channels; CTAs that they take
+    int chunk, nchunk;           // tokens of a chunk (a multiple of 16), chunks
+    float4* maps;                // [B][nchunk][groups][8][32]
+    float* sums;                 // [B][nchunk][groups * channels of a warp]
+    uint16_t* y;                 // [B][L][D]
+    float* hT;                   // [B][D][N]
+    float4* keep;                // [B][ceil(L / kSsmKeep)][groups][8][32] or null
+};
+struct SsmBwdArgs {
+    SsmArgs f;
+    const uint16_t* dy;          // [B][L][D]
+    SsmOutRows dx, ddelta, dgate;
+    int f32;                     // they and db, dc in FP32
+    void *db, *dc;               // [B][L][N]
+    float* dbc;                  // [B L][ngq][2 padded N]
+    float4* part;                // [B nchunk][part_len]
+    long long part_len;
+    float *da_log, *dd_skip, *ddelta_bias, *dh0;   // the last three may be null
+};
+struct SsmSplit {
+    int lanes, channels;         // that share a channel; of a warp
+    int groups, ctas, warps;     // warps that span D; CTAs of a row, their warps
+};
+SsmSplit ssm_split(int D, int N);
+void ssm_chunks(int B, int L, int D, int N, int warps, int* chunk, int* nchunk);
+cudaError_t launch_ssm_maps(const SsmArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_ssm_prefix(const SsmArgs& a, bool reverse, cudaStream_t s, bool pdl);
+cudaError_t launch_ssm_replay(const SsmArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_ssm_step(const SsmArgs& a, float* state, cudaStream_t s, bool pdl);
+cudaError_t launch_ssm_rmaps(const SsmBwdArgs& g, cudaStream_t s, bool pdl);
+cudaError_t launch_ssm_bwd(const SsmBwdArgs& g, cudaStream_t s, bool pdl);
+cudaError_t launch_ssm_finish(const SsmBwdArgs& g, cudaStream_t s, bool pdl);
+
+// ---------------------------------------------------------------------------
+// Short causal convolution (causal_conv.cu).
+// ---------------------------------------------------------------------------
+struct ConvArgs {
+    SsmRows x;
+    const float* w;              // [W][D], tap j of the input j tokens earlier
+    const float* bias;           // [D] or null
+    const uint16_t* state;       // [B][W - 1][D]: the inputs before the first token, or null (zeros)
+    const uint8_t* reset;        // [B][L] or null
+    int B, L, D, W, silu;
+    uint16_t* y;                 // [B][L][D]
+    uint16_t* state_out;         // [B][W - 1][D] or null
+};
+struct ConvBwdArgs {
+    ConvArgs f;
+    const uint16_t* dy;          // [B][L][D]
+    SsmOutRows dx;
+    void* dstate;                // [B][W - 1][D] or null
+    int f32;
+    int parts;
+    float* part;                 // [parts][W + 1][D]
+    float *dw, *dbias;
+};
+int conv_bwd_parts(int B, int L, int D);
+cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_causal_conv_sum(const ConvBwdArgs& a, cudaStream_t s, bool pdl);
+
+// ---------------------------------------------------------------------------
+// Embedding (embedding.cu).
+// ---------------------------------------------------------------------------
+struct EmbedArgs {
+    const int64_t* tokens;       // [T]
+    const void* w;               // [V][D] BF16, or FP32 (w32)
+    int T, V, D, w32;
+    float scale;
+    uint16_t* y;                 // [T][D]
+};
+struct EmbedBwdArgs {
+    const int64_t* tokens;       // [T]
+    const uint16_t* dy;          // [T][D]
+    int T, V, D;
+    float scale;
+    void* dw;                    // [V][D]
+    int f32, accumulate;
+    uint32_t* status;
+    int owners;                  // CTAs that share out the vocabulary
+    int2* list;                  // [T]: an owner's positions and rows, in the tokens' order
+    int2* place;                 // [T]: positions and rows (in the owners' order), sorted
+    int* count;                  // [1]: of them
+    int* first;                  // [owners rows + 1]: each row's first place
+    float* part;                 // [2 chunks][D]
+};
+int embed_owners(int V);
+long long embed_chunks(long long T);
+cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_embedding_sort(const EmbedBwdArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_embedding_sum(const EmbedBwdArgs& a, cudaStream_t s, bool pdl);
+cudaError_t launch_embedding_join(const EmbedBwdArgs& a, cudaStream_t s, bool pdl);
+
 }  // namespace lrs

@@ -1,0 +1,226 @@
+// What the forward, backward and step kernels of the selective state space
+// scan share: the tile of channels and states of a warp, the time tile in
+// shared memory, the step softplus(raw).
+#pragma once
+
+#include <atomic>
+
+#include "kernels.cuh"
+
+namespace lrs {
+
+// A warp owns 128 / LN channels: LN lanes share four channels, 8 states each,
+// so a lane holds 4 x 8 states of one chunk of time in registers.  LN = 1, 2,
+// 4, 8 for up to 8, 16, 32, 64 states a channel.  32 states a lane are what
+// makes the operands cheap: a token's step, input, b and c are 24 words of
+// shared memory a lane, three bytes a state, and the sum over the states of a
+// channel crosses LN lanes only.
+constexpr int kSsmCh = 4;        // channels of a lane
+constexpr int kSsmSt = 8;        // states of a lane
+constexpr int kSsmVec = kSsmCh * kSsmSt / 4;   // its states as float4
+
+template <int LN>
+struct SsmWarp {
+    static constexpr int CW = 32 / LN * kSsmCh;   // channels of a warp
+    static constexpr int NP = kSsmSt * LN;        // states of a channel, padded
+    static constexpr int RL = CW / 8;             // lanes that span a row of channels, 16 bytes each
+    static constexpr int RPI = 32 / RL;           // rows that a warp's load instruction takes
+};
+
+// Lets `fn` use `most` bytes of dynamic shared memory, once per device (every
+// launch of a kernel names the same bytes, whatever it uses of them).
+inline cudaError_t allow_smem(const void* fn, size_t most, std::atomic<bool>* allowed) {
+    int dev = 0;
+    const cudaError_t de = cudaGetDevice(&dev);
+    if (de != cudaSuccess) return de;
+    const bool known = dev >= 0 && dev < 64;
+    if (known && allowed[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess && known) allowed[dev].store(true, std::memory_order_release);
+    return e;
+}
+
+// softplus(r) = max(r, 0) + log1p(e^-|r|): relative error within 2^-21 also where
+// it is far below 1 (the logarithm of 1 + w would lose w's digits).
+__device__ __forceinline__ f2x softplus2(f2x raw) {
+    // log1p(w) / w on [0, 1] within 5e-9 (a polynomial of degree 9, fitted for the
+    // least relative error over the interval)
+    constexpr float kLog1p[10] = {1.000000000e+00f,  -4.999990165e-01f, 3.332996368e-01f, -2.495413423e-01f,
+                                  1.967593879e-01f,  -1.530559212e-01f, 1.060365364e-01f, -5.695952475e-02f,
+                                  1.985145733e-02f,  -3.244024236e-03f};
+    float a, b;
+    up2(raw, a, b);
+    const f2x w = pk2(ex2_approx(-fabsf(a) * kLog2e), ex2_approx(-fabsf(b) * kLog2e));
+    f2x p = dup2(kLog1p[9]);
+#pragma unroll
+    for (int i = 8; i >= 0; --i) p = fma2(p, w, dup2(kLog1p[i]));
+    return fma2(p, w, pk2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
+}
+
+// 1 / (1 + e^-r)
+__device__ __forceinline__ float ssm_sigmoid(float r) { return rcp_approx(1.f + ex2_approx(-r * kLog2e)); }
+
+// log2 of what a state keeps in a unit of time: -e^a_log log2 e.
+__device__ __forceinline__ float ssm_rate(float a_log) { return -expf(a_log) * kLog2e; }
+
+// 8 BF16 values as FP32 pairs.
+__device__ __forceinline__ void unpack_pairs(const uint4 q, f2x (&v)[4]) {
+    v[0] = bf2x(q.x);
+    v[1] = bf2x(q.y);
+    v[2] = bf2x(q.z);
+    v[3] = bf2x(q.w);
+}
+// 8 floats of a vector, or zeros.
+__device__ __forceinline__ void load_pairs(const float* p, bool on, f2x (&v)[4]) {
+    if (p == nullptr || !on) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = 0ull;
+        return;
+    }
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = pk2(a.x, a.y);
+    v[1] = pk2(a.z, a.w);
+    v[2] = pk2(b.x, b.y);
+    v[3] = pk2(b.z, b.w);
+}
+__device__ __forceinline__ void store_pairs(float* p, const f2x (&v)[4]) {
+    float4 a, b;
+    up2(v[0], a.x, a.y);
+    up2(v[1], a.z, a.w);
+    up2(v[2], b.x, b.y);
+    up2(v[3], b.z, b.w);
+    reinterpret_cast<float4*>(p)[0] = a;
+    reinterpret_cast<float4*>(p)[1] = b;
+}
+__device__ __forceinline__ void read_pairs(const float* p, f2x (&v)[4]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = pk2(a.x, a.y);
+    v[1] = pk2(a.z, a.w);
+    v[2] = pk2(b.x, b.y);
+    v[3] = pk2(b.z, b.w);
+}
+// A lane's 8 states of one token's b or c.
+__device__ __forceinline__ void read_states(const float* p, f2x (&v)[4]) { read_pairs(p, v); }
+
+__device__ __forceinline__ float bf_up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
+
+// Rows t0 .. t0 + nt - 1 of b or c into a [T][NP] tile (zeros past N and past nt).
+template <int LN, int T>
+__device__ __forceinline__ void stage_states(const SsmRows& r, int b, int t0, int nt, int N, float* dst, int lane) {
+    constexpr int NP = SsmWarp<LN>::NP;
+    const uint16_t* p = r.p + (long long)b * r.sb + (long long)t0 * r.st;
+    uint16_t v[T * NP / 32];
+#pragma unroll
+    for (int k = 0; k < T * NP / 32; ++k) {
+        const int i = k * 32 + lane, t = i / NP, n = i % NP;
+        v[k] = t < nt && n < N ? __ldg(p + (long long)t * r.st + n) : (uint16_t)0;
+    }
+#pragma unroll
+    for (int k = 0; k < T * NP / 32; ++k) dst[k * 32 + lane] = bf_up(v[k]);
+}
+
+// The rates of a lane's states (0 past N and D, where the other operands are zeros too).
+template <int LN>
+__device__ __forceinline__ void load_rates(const float* a_log, int c0, int n0, int D, int N, f2x (&A)[kSsmCh][4]) {
+#pragma unroll
+    for (int c = 0; c < kSsmCh; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = n0 + 2 * j + e;
+                v[e] = c0 + c < D && n < N ? ssm_rate(__ldg(a_log + (long long)(c0 + c) * N + n)) : 0.f;
+            }
+            A[c][j] = pk2(v[0], v[1]);
+        }
+}
+
+// A lane's states from and to [.., D, N] rows of FP32.
+__device__ __forceinline__ void load_state(const float* s, long long row, int c0, int n0, int D, int N,
+                                           f2x (&h)[kSsmCh][4]) {
+#pragma unroll
+    for (int c = 0; c < kSsmCh; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float v[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = n0 + 2 * j + e;
+                v[e] = s != nullptr && c0 + c < D && n < N ? __ldg(s + (row * D + c0 + c) * N + n) : 0.f;
+            }
+            h[c][j] = pk2(v[0], v[1]);
+        }
+}
+__device__ __forceinline__ void store_state(float* s, long long row, int c0, int n0, int D, int N,
+                                            const f2x (&h)[kSsmCh][4]) {
+#pragma unroll
+    for (int c = 0; c < kSsmCh; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float v[2];
+            up2(h[c][j], v[0], v[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = n0 + 2 * j + e;
+                if (c0 + c < D && n < N) s[(row * D + c0 + c) * N + n] = v[e];
+            }
+        }
+}
+// The same in the kernels' own layout: [kSsmVec][32 lanes] float4 for a warp.
+__device__ __forceinline__ void load_tile_state(const float4* p, int lane, f2x (&h)[kSsmCh][4]) {
+#pragma unroll
+    for (int k = 0; k < kSsmVec; ++k) {
+        const float4 v = __ldcg(p + k * 32 + lane);
+        h[k >> 1][2 * (k & 1)] = pk2(v.x, v.y);
+        h[k >> 1][2 * (k & 1) + 1] = pk2(v.z, v.w);
+    }
+}
+__device__ __forceinline__ void store_tile_state(float4* p, int lane, const f2x (&h)[kSsmCh][4]) {
+#pragma unroll
+    for (int k = 0; k < kSsmVec; ++k) {
+        float4 v;
+        up2(h[k >> 1][2 * (k & 1)], v.x, v.y);
+        up2(h[k >> 1][2 * (k & 1) + 1], v.z, v.w);
+        p[k * 32 + lane] = v;
+    }
+}
+
+// The sum of v[c] over the LN lanes that share a channel; lane ln of them ends
+// with the sums of the channels [ln 4 / LN, ...) in v[0 ..] (LN = 8: lanes 2 c and 2 c + 1 with channel c's).
+template <int LN>
+__device__ __forceinline__ void sum_states(float (&v)[kSsmCh], int lane) {
+    if (LN == 1) return;
+    int keep = kSsmCh;
+#pragma unroll
+    for (int m = LN / 2; m >= 1; m >>= 1) {
+        if (keep > 1) {
+            keep >>= 1;
+            const bool up = lane & m;
+#pragma unroll
+            for (int i = 0; i < keep; ++i) {
+                const float send = up ? v[i] : v[i + keep], mine = up ? v[i + keep] : v[i];
+                v[i] = mine + __shfl_xor_sync(0xffffffffu, send, m);
+            }
+        } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
+        }
+    }
+}
+// Writes what sum_states left to the warp's row of channels.
+template <int LN>
+__device__ __forceinline__ void put_channels(float* row, const float (&v)[kSsmCh], int lc, int ln) {
+    float* p = row + lc * kSsmCh;
+    if (LN == 1) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    if (LN == 2) *reinterpret_cast<float2*>(p + 2 * ln) = make_float2(v[0], v[1]);
+    if (LN == 4) p[ln] = v[0];
+    if (LN == 8) p[ln >> 1] = v[0];
+}
+
+// Bit t: a sequence starts at token t0 + t (t < nt <= 32).
+__device__ __forceinline__ uint32_t start_bits(const uint8_t* reset, long long row, int nt, int lane) {
+    if (reset == nullptr) return 0u;
+    return __ballot_sync(0xffffffffu, lane < nt && __ldg(reset + row + lane) != 0);
+}
+
+}  // namespace lrs

@@ -1,0 +1,468 @@
+// The selective state space scan, forward and one token at a time.
+//
+//   dt_t = softplus(delta_t + delta_bias),  a_tn = e^(-e^a_log_n dt_t)
+//   h_tn = a_tn h_(t-1)n + dt_t x_t b_tn          (a channel's N states; a = 0 at a sequence's first token)
+//   y_t  = (sum_n c_tn h_tn + d_skip x_t) SiLU(gate_t)
+//
+// One exponential and four multiply-adds a (token, channel, state): at N = 16 a
+// value of x brings 16 of them, so the SFU (32 ex2 a clock and SM) and the FP32
+// pipe (128 operations) bound it both, at about 4 clocks a warp and state, above
+// the streams' time at HBM speed.
+//
+// The recurrence runs through time in registers (ssm.cuh: 4 channels x 8 states
+// a lane).  Time is cut into chunks so that every SM has its 16 warps:
+//   maps    each chunk but the last from a zero state: its end state, and the
+//           sum of its dt, which gives what it keeps of the state before
+//           (a product of exponentials is one exponential);
+//   prefix  the entry state of every chunk, in place;
+//   replay  each chunk again from its entry state, with the outputs.
+// The maps cost nearly as much as the replay, so where batch and channels alone
+// give enough warps (fewer than three chunks would fit) the replay runs alone.
+// A warp stages its own operands for 16 tokens: x, delta as BF16 rows (128
+// bytes of a row at N = 16), dt and dt x as FP32 into shared memory, from where
+// the lanes that share a channel read them.  No barrier between warps.
+#include <algorithm>
+
+#include "ssm.cuh"
+
+namespace lrs {
+
+namespace {
+
+constexpr int kSsmWarps = 4;       // of a CTA, at most
+constexpr int kSsmCtas = 4;        // resident per SM: 128 registers a thread
+constexpr int kSsmSms = 152;
+
+template <int LN>
+struct FwdTile {
+    static constexpr int T = LN == 1 ? 8 : 16;   // tokens
+    using W = SsmWarp<LN>;
+    float dt[T][W::CW];    // then the sums over the states
+    float k[T][W::CW];
+    float b[T][W::NP];
+    float c[T][W::NP];
+};
+
+// dt and dt x of nt tokens.
+template <int LN>
+__device__ __forceinline__ void stage_inputs(const SsmArgs& a, int b, int c0, int t0, int nt, FwdTile<LN>& s, int lane) {
+    using W = SsmWarp<LN>;
+    constexpr int IT = FwdTile<LN>::T / W::RPI;
+    const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
+    const bool on = c0 + c8 < a.D;
+    const uint16_t* px = a.x.p + (long long)b * a.x.sb + (long long)t0 * a.x.st + c0 + c8;
+    const uint16_t* pd = a.delta.p + (long long)b * a.delta.sb + (long long)t0 * a.delta.st + c0 + c8;
+    uint4 qx[IT], qd[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = r0 + i * W::RPI;
+        qx[i] = qd[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (on && r < nt) {
+            qx[i] = __ldg(reinterpret_cast<const uint4*>(px + (long long)r * a.x.st));
+            qd[i] = __ldg(reinterpret_cast<const uint4*>(pd + (long long)r * a.delta.st));
+        }
+    }
+    f2x bias[4];
+    load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = r0 + i * W::RPI;
+        f2x x[4], d[4];
+        unpack_pairs(qx[i], x);
+        unpack_pairs(qd[i], d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            // a token past the end keeps the state and adds nothing
+            d[e] = on && r < nt ? softplus2(add2(d[e], bias[e])) : 0ull;
+            x[e] = mul2(d[e], x[e]);
+        }
+        store_pairs(&s.dt[r][c8], d);
+        store_pairs(&s.k[r][c8], x);
+    }
+}
+
+// One token: h <- e^(A dt) h + k b, and (Y) the sums of c h.
+template <int LN, bool Y>
+__device__ __forceinline__ void advance(const FwdTile<LN>& s, int t, int lc, int ln, const f2x (&A)[kSsmCh][4],
+                                        f2x (&h)[kSsmCh][4], float (&y)[kSsmCh], float4& dt) {
+    dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
+    const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
+    const float ds[kSsmCh] = {dt.x, dt.y, dt.z, dt.w}, ks[kSsmCh] = {k.x, k.y, k.z, k.w};
+    f2x b[4], c[4];
+    read_states(&s.b[t][ln * kSsmSt], b);
+    if (Y) read_states(&s.c[t][ln * kSsmSt], c);
+#pragma unroll
+    for (int i = 0; i < kSsmCh; ++i) {
+        const f2x d2 = dup2(ds[i]), k2 = dup2(ks[i]);
+        f2x acc = 0ull;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            float e0, e1;
+            up2(mul2(A[i][j], d2), e0, e1);
+            h[i][j] = fma2(pk2(ex2_approx(e0), ex2_approx(e1)), h[i][j], mul2(k2, b[j]));
+            if (Y) acc = j ? fma2(h[i][j], c[j], acc) : mul2(h[i][j], c[j]);
+        }
+        if (Y) {
+            float lo, hi;
+            up2(acc, lo, hi);
+            y[i] = lo + hi;
+        }
+    }
+}
+
+struct SsmPlace {
+    int b, chunk, group, warp;
+    bool on;
+};
+// CTAs: chunk by chunk, then the groups of a row side by side (they share b and c in L1).
+__device__ __forceinline__ SsmPlace place(const SsmArgs& a, int chunks) {
+    SsmPlace p;
+    const long long i = blockIdx.x;
+    const int gq = (int)(i % a.ngq);
+    const long long r = i / a.ngq;
+    p.chunk = (int)(r % chunks);
+    p.b = (int)(r / chunks);
+    p.warp = threadIdx.x >> 5;
+    p.group = gq * (blockDim.x >> 5) + p.warp;
+    p.on = p.group < a.groups;
+    return p;
+}
+
+template <int LN>
+__global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(const SsmArgs a) {
+    using W = SsmWarp<LN>;
+    constexpr int T = FwdTile<LN>::T;
+    extern __shared__ __align__(16) uint8_t buf[];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
+    const SsmPlace p = place(a, a.nchunk - 1);
+    if (!p.on) return;
+    FwdTile<LN>& s = reinterpret_cast<FwdTile<LN>*>(buf)[p.warp];
+    const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
+    f2x A[kSsmCh][4], h[kSsmCh][4];
+    load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
+#pragma unroll
+    for (int i = 0; i < kSsmCh; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool cut = false;
+    const int end = min(a.L, (p.chunk + 1) * a.chunk);
+    for (int t0 = p.chunk * a.chunk; t0 < end; t0 += T) {
+        const int nt = min(T, end - t0);
+        __syncwarp();
+        stage_inputs<LN>(a, p.b, c0, t0, nt, s, lane);
+        stage_states<LN, T>(a.b, p.b, t0, nt, a.N, &s.b[0][0], lane);
+        const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
+        cut |= starts != 0u;
+        __syncwarp();
+#pragma unroll 2
+        for (int t = 0; t < T; ++t) {
+            if ((starts >> t) & 1u) {
+#pragma unroll
+                for (int i = 0; i < kSsmCh; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
+            }
+            float y[kSsmCh];
+            float4 dt;
+            advance<LN, false>(s, t, lc, ln, A, h, y, dt);
+            sum.x += dt.x;
+            sum.y += dt.y;
+            sum.z += dt.z;
+            sum.w += dt.w;
+        }
+    }
+    const long long slot = ((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group;
+    store_tile_state(a.maps + slot * (kSsmVec * 32), lane, h);
+    // an infinite sum: nothing is kept
+    if (cut) sum = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
+    if (ln == 0) *reinterpret_cast<float4*>(a.sums + slot * W::CW + lc * kSsmCh) = sum;
+}
+
+// Entry states of the chunks, in place of their end states: one float4 of a
+// warp's states a thread.  Backward (REV): the adjoints that reach a chunk's
+// end, from the last chunk to the first.
+template <int LN, bool REV>
+__global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a) {
+    using W = SsmWarp<LN>;
+    pdl_trigger();
+    pdl_wait();
+    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const int lane = (int)(i & 31), k = (int)(i >> 5) & (kSsmVec - 1);
+    const long long bg = i / (32 * kSsmVec);
+    const int g = (int)(bg % a.groups);
+    const long long b = bg / a.groups;
+    if (b >= a.B) return;
+    const int cw = lane / LN * kSsmCh + (k >> 1), c = g * W::CW + cw, n0 = lane % LN * kSsmSt + 4 * (k & 1);
+    float A[4], h[4];
+    const float* start = a.h0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const bool on = c < a.D && n0 + e < a.N;
+        A[e] = on ? ssm_rate(__ldg(a.a_log + (long long)c * a.N + n0 + e)) : 0.f;
+        h[e] = on && start != nullptr ? __ldg(start + (b * a.D + c) * a.N + n0 + e) : 0.f;
+    }
+    // forward: chunk i's entry from chunk i - 1's; the last chunk has no map of its own
+    const long long step = (REV ? -1 : 1) * (long long)a.groups;
+    const long long first = (b * a.nchunk + (REV ? a.nchunk - 1 : 0)) * a.groups + g;
+    float4* m = a.maps + first * (kSsmVec * 32) + k * 32 + lane;
+    const float* sums = a.sums + first * W::CW + cw;
+    constexpr int AHEAD = 8;
+    for (int q = 0; q < a.nchunk; q += AHEAD) {
+        float4 v[AHEAD];
+        float s[AHEAD];
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (q + u < a.nchunk - 1) {
+                v[u] = __ldcg(m + (q + u) * step * (kSsmVec * 32));
+                s[u] = __ldcg(sums + (q + u) * step * W::CW);
+            }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            if (q + u >= a.nchunk) break;
+            m[(q + u) * step * (kSsmVec * 32)] = make_float4(h[0], h[1], h[2], h[3]);
+            if (q + u == a.nchunk - 1) break;
+            const float e[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+            const bool cut = isinf(s[u]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = cut ? e[j] : fmaf(ex2_approx(A[j] * s[u]), h[j], e[j]);
+        }
+    }
+}
+
+template <int LN, bool KEEP>
+__global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(const SsmArgs a) {
+    using W = SsmWarp<LN>;
+    constexpr int T = FwdTile<LN>::T, IT = T / W::RPI;
+    extern __shared__ __align__(16) uint8_t buf[];
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
+    const SsmPlace p = place(a, a.nchunk);
+    if (!p.on) return;
+    FwdTile<LN>& s = reinterpret_cast<FwdTile<LN>*>(buf)[p.warp];
+    const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
+    f2x A[kSsmCh][4], h[kSsmCh][4];
+    load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
+    if (a.nchunk > 1)
+        load_tile_state(a.maps + (((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group) * (kSsmVec * 32), lane, h);
+    else
+        load_state(a.h0, p.b, ch, ln * kSsmSt, a.D, a.N, h);
+    const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
+    const bool on = c0 + c8 < a.D;
+    const int end = min(a.L, (p.chunk + 1) * a.chunk);
+    const int slots = (a.L + kSsmKeep - 1) / kSsmKeep;
+    for (int t0 = p.chunk * a.chunk; t0 < end; t0 += T) {
+        const int nt = min(T, end - t0);
+        __syncwarp();
+        stage_inputs<LN>(a, p.b, c0, t0, nt, s, lane);
+        stage_states<LN, T>(a.b, p.b, t0, nt, a.N, &s.b[0][0], lane);
+        stage_states<LN, T>(a.c, p.b, t0, nt, a.N, &s.c[0][0], lane);
+        const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
+        __syncwarp();
+#pragma unroll 2
+        for (int t = 0; t < T; ++t) {
+            if (KEEP && t % kSsmKeep == 0 && t < nt)
+                store_tile_state(a.keep + (((long long)p.b * slots + (t0 + t) / kSsmKeep) * a.groups + p.group) *
+                                              (kSsmVec * 32), lane, h);
+            if ((starts >> t) & 1u) {
+#pragma unroll
+                for (int i = 0; i < kSsmCh; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
+            }
+            float y[kSsmCh];
+            float4 dt;
+            advance<LN, true>(s, t, lc, ln, A, h, y, dt);
+            sum_states<LN>(y, lane);
+            __syncwarp();   // every lane has read the token's dt
+            put_channels<LN>(s.dt[t], y, lc, ln);
+        }
+        __syncwarp();
+        if (on) {
+            f2x skip[4];
+            load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, true, skip);
+            const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)t0 * a.x.st + c0 + c8;
+            const uint16_t* pg = a.gate.p + (long long)p.b * a.gate.sb + (long long)t0 * a.gate.st + c0 + c8;
+            uint16_t* py = a.y + ((long long)p.b * a.L + t0) * a.D + c0 + c8;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = r0 + i * W::RPI;
+                if (r >= nt) break;
+                f2x y[4], x[4];
+                read_pairs(&s.dt[r][c8], y);
+                if (a.d_skip != nullptr) {
+                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(px + (long long)r * a.x.st)), x);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[e] = fma2(skip[e], x[e], y[e]);
+                }
+                if (a.gate.p != nullptr) {
+                    f2x z[4];
+                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(pg + (long long)r * a.gate.st)), z);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float z0, z1;
+                        up2(z[e], z0, z1);
+                        y[e] = mul2(y[e], mul2(z[e], pk2(ssm_sigmoid(z0), ssm_sigmoid(z1))));
+                    }
+                }
+                *reinterpret_cast<uint4*>(py + (long long)r * a.D) =
+                    make_uint4(x2bf(y[0]), x2bf(y[1]), x2bf(y[2]), x2bf(y[3]));
+            }
+        }
+    }
+    if (p.chunk == a.nchunk - 1) store_state(a.hT, p.b, ch, ln * kSsmSt, a.D, a.N, h);
+}
+
+// One token of each of B sequences: LQ lanes share a channel, four states each
+// (16 bytes of the state row), and go through the batch.  Bound by the state,
+// read and written once in FP32.
+constexpr int kStepThreads = 256;
+template <int LQ, bool VEC>
+__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
+    pdl_trigger();
+    pdl_wait();
+    const int n0 = threadIdx.x % LQ * 4, c = blockIdx.x * (kStepThreads / LQ) + threadIdx.x / LQ;
+    const bool on = c < a.D;
+    float A[4];
+    bool live[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        live[e] = on && n0 + e < a.N;
+        A[e] = live[e] ? ssm_rate(__ldg(a.a_log + (long long)c * a.N + n0 + e)) : 0.f;
+    }
+    const float bias = on && a.delta_bias != nullptr ? __ldg(a.delta_bias + c) : 0.f;
+    const float skip = on && a.d_skip != nullptr ? __ldg(a.d_skip + c) : 0.f;
+    for (long long b = blockIdx.y; b < a.B; b += gridDim.y) {
+        float* ps = state + (b * a.D + c) * a.N + n0;
+        float h[4] = {0.f, 0.f, 0.f, 0.f}, bb[4], cc[4], x = 0.f, raw = 0.f, z = 0.f;
+        if (VEC) {
+            if (live[0]) {
+                const float4 v = *reinterpret_cast<const float4*>(ps);
+                h[0] = v.x;
+                h[1] = v.y;
+                h[2] = v.z;
+                h[3] = v.w;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!VEC && live[e]) h[e] = ps[e];
+            bb[e] = live[e] ? bf_up(__ldg(a.b.p + b * a.b.sb + n0 + e)) : 0.f;
+            cc[e] = live[e] ? bf_up(__ldg(a.c.p + b * a.c.sb + n0 + e)) : 0.f;
+        }
+        if (on) {
+            x = bf_up(__ldg(a.x.p + b * a.x.sb + c));
+            raw = bf_up(__ldg(a.delta.p + b * a.delta.sb + c)) + bias;
+            if (a.gate.p != nullptr) z = bf_up(__ldg(a.gate.p + b * a.gate.sb + c));
+        }
+        const bool start = a.reset != nullptr && __ldg(a.reset + b) != 0;
+        float dt, unused;
+        up2(softplus2(dup2(raw)), dt, unused);
+        const float k = dt * x;
+        float y = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[e] = start ? k * bb[e] : fmaf(ex2_approx(A[e] * dt), h[e], k * bb[e]);
+            y = fmaf(h[e], cc[e], y);
+        }
+        if (VEC) {
+            if (live[0]) *reinterpret_cast<float4*>(ps) = make_float4(h[0], h[1], h[2], h[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (live[e]) ps[e] = h[e];
+        }
+#pragma unroll
+        for (int m = LQ / 2; m >= 1; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+        if (on && n0 == 0) {
+            y = fmaf(skip, x, y);
+            if (a.gate.p != nullptr) y *= z * ssm_sigmoid(z);
+            a.y[b * a.D + c] = __bfloat16_as_ushort(__float2bfloat16_rn(y));
+        }
+    }
+}
+
+template <int LN>
+cudaError_t fwd_as(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
+    const SsmSplit w = ssm_split(a.D, a.N);
+    const size_t smem = w.warps * sizeof(FwdTile<LN>), most = kSsmWarps * sizeof(FwdTile<LN>);
+    const dim3 block((unsigned)w.warps * 32);
+    if (what == 0) {
+        static std::atomic<bool> allowed[64];
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_maps_kernel<LN>), most, allowed);
+        if (e != cudaSuccess) return e;
+        return launch_ex(ssm_maps_kernel<LN>, dim3((unsigned)((long long)a.B * (a.nchunk - 1) * a.ngq)), block, smem, s, pdl, a);
+    }
+    if (what == 1)
+        return launch_ex(ssm_prefix_kernel<LN, false>, dim3((unsigned)((long long)a.B * a.groups)), dim3(256), 0, s, pdl, a);
+    if (what == 2)
+        return launch_ex(ssm_prefix_kernel<LN, true>, dim3((unsigned)((long long)a.B * a.groups)), dim3(256), 0, s, pdl, a);
+    const dim3 grid((unsigned)((long long)a.B * a.nchunk * a.ngq));
+    if (a.keep != nullptr) {
+        static std::atomic<bool> allowed[64];
+        const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_replay_kernel<LN, true>), most, allowed);
+        if (e != cudaSuccess) return e;
+        return launch_ex(ssm_replay_kernel<LN, true>, grid, block, smem, s, pdl, a);
+    }
+    static std::atomic<bool> allowed[64];
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_replay_kernel<LN, false>), most, allowed);
+    if (e != cudaSuccess) return e;
+    return launch_ex(ssm_replay_kernel<LN, false>, grid, block, smem, s, pdl, a);
+}
+cudaError_t fwd(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
+    switch (ssm_split(a.D, a.N).lanes) {
+        case 1: return fwd_as<1>(a, what, s, pdl);
+        case 2: return fwd_as<2>(a, what, s, pdl);
+        case 4: return fwd_as<4>(a, what, s, pdl);
+        default: return fwd_as<8>(a, what, s, pdl);
+    }
+}
+
+template <int LQ>
+cudaError_t step_as(const SsmArgs& a, float* state, cudaStream_t s, bool pdl) {
+    const int across = (a.D + kStepThreads / LQ - 1) / (kStepThreads / LQ);
+    // eight CTAs an SM hold all their threads; the rest of the batch in turns
+    const int rows = std::max(1, std::min(a.B, std::min(65535, 8 * kSsmSms / across)));
+    const dim3 grid((unsigned)across, (unsigned)rows);
+    if (a.N % 4 == 0) return launch_ex(ssm_step_kernel<LQ, true>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
+    return launch_ex(ssm_step_kernel<LQ, false>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
+}
+
+}  // namespace
+
+SsmSplit ssm_split(int D, int N) {
+    SsmSplit w;
+    w.lanes = N <= 8 ? 1 : N <= 16 ? 2 : N <= 32 ? 4 : 8;
+    w.channels = 32 / w.lanes * kSsmCh;
+    w.groups = (D + w.channels - 1) / w.channels;
+    w.ctas = (w.groups + kSsmWarps - 1) / kSsmWarps;
+    w.warps = (w.groups + w.ctas - 1) / w.ctas;
+    return w;
+}
+// As many chunks as give `warps` warps an SM, each of two tiles of 16 tokens at
+// least; one where three would not fit.
+void ssm_chunks(int B, int L, int D, int N, int warps, int* chunk, int* nchunk) {
+    const SsmSplit w = ssm_split(D, N);
+    const long long most = (long long)kSsmSms * warps / ((long long)B * w.ctas * w.warps);
+    long long n = std::min<long long>(most, (L + 31) / 32);
+    if (n < 3) n = 1;
+    *chunk = (int)(((L + n - 1) / n + 15) / 16 * 16);
+    *nchunk = (L + *chunk - 1) / *chunk;
+}
+cudaError_t launch_ssm_maps(const SsmArgs& a, cudaStream_t s, bool pdl) { return fwd(a, 0, s, pdl); }
+cudaError_t launch_ssm_prefix(const SsmArgs& a, bool reverse, cudaStream_t s, bool pdl) {
+    return fwd(a, reverse ? 2 : 1, s, pdl);
+}
+cudaError_t launch_ssm_replay(const SsmArgs& a, cudaStream_t s, bool pdl) { return fwd(a, 3, s, pdl); }
+cudaError_t launch_ssm_step(const SsmArgs& a, float* state, cudaStream_t s, bool pdl) {
+    if (a.N <= 4) return step_as<1>(a, state, s, pdl);
+    if (a.N <= 8) return step_as<2>(a, state, s, pdl);
+    if (a.N <= 16) return step_as<4>(a, state, s, pdl);
+    if (a.N <= 32) return step_as<8>(a, state, s, pdl);
+    return step_as<16>(a, state, s, pdl);
+}
+
+}  // namespace lrs

@@ -1472,6 +1472,10 @@ bool rows_out_ok(const lrs_rows* r, int B, int L, int width) {
     return rows_in_ok(r) && (L == 1 || r->token_stride >= width) &&
            (B == 1 || r->batch_stride >= (long long)(L - 1) * r->token_stride + width);
 }
+// Whether pairs of a row's values are 4-byte words.
+bool rows_in_words(const lrs_rows* r, int width) {
+    return width % 2 == 0 && (reinterpret_cast<uintptr_t>(r->data) & 3u) == 0 && r->batch_stride % 2 == 0 && r->token_stride % 2 == 0;
+}
 SsmRows rows_in(const lrs_rows* r) {
     SsmRows o = {};
     if (r != nullptr) o = {static_cast<const uint16_t*>(r->data), r->batch_stride, r->token_stride};
@@ -1652,6 +1656,7 @@ SsmArgs ssm_args(const lrs_rows* x, const lrs_rows* delta, const float* a_log, c
     const SsmSplit w = ssm_split(D, N);
     a.groups = w.groups;
     a.ngq = w.ctas;
+    a.words = rows_in_words(b, N) && rows_in_words(c, N);
     return a;
 }
 void ssm_place(SsmArgs& a, const SsmScratch& l, void* scratch) {

@@ -669,6 +669,7 @@ struct SsmArgs {
     const uint8_t* reset;        // [B][L] or null
     int B, L, D, N;
     int groups, ngq;             // warps' groups of channels; CTAs that they take
+    int words;                   // b and c can be read two states at a time
     int chunk, nchunk;           // tokens of a chunk (a multiple of 16), chunks
     float4* maps;                // [B][nchunk][groups][8][32]
     float* sums;                 // [B][nchunk][groups * channels of a warp]

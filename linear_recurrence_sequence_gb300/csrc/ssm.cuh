@@ -104,19 +104,70 @@ __device__ __forceinline__ void read_states(const float* p, f2x (&v)[4]) { read_
 
 __device__ __forceinline__ float bf_up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
-// Rows t0 .. t0 + nt - 1 of b or c into a [T][NP] tile (zeros past N and past nt).
+// Copies into shared memory that run on while the warp computes; `bytes` 0 writes zeros.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copy4(void* dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
+// Asks for rows t0 .. t0 + nt - 1 (of T) of the warp's channels, zeros past nt and D.
 template <int LN, int T>
-__device__ __forceinline__ void stage_states(const SsmRows& r, int b, int t0, int nt, int N, float* dst, int lane) {
+__device__ __forceinline__ void ask_rows(const uint16_t* p, long long sb, long long st, int b, int t0, int nt, int c0, int D,
+                                         uint16_t* dst, int lane) {
+    using W = SsmWarp<LN>;
+    constexpr int IT = (T + W::RPI - 1) / W::RPI;
+    const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
+    const uint16_t* q = p + (long long)b * sb + (long long)t0 * st + c0 + c8;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = r0 + i * W::RPI;
+        const bool on = c0 + c8 < D && r < nt;
+        if (T % W::RPI == 0 || r < T) copy16(dst + r * W::CW + c8, on ? q + (long long)r * st : p, on);
+    }
+}
+// Rows of b or c, two states at a time (SsmArgs.words).
+template <int LN, int T>
+__device__ __forceinline__ void ask_states(const SsmRows& r, int b, int t0, int nt, int N, uint16_t* dst, int lane) {
     constexpr int NP = SsmWarp<LN>::NP;
     const uint16_t* p = r.p + (long long)b * r.sb + (long long)t0 * r.st;
-    uint16_t v[T * NP / 32];
 #pragma unroll
-    for (int k = 0; k < T * NP / 32; ++k) {
-        const int i = k * 32 + lane, t = i / NP, n = i % NP;
-        v[k] = t < nt && n < N ? __ldg(p + (long long)t * r.st + n) : (uint16_t)0;
+    for (int k = 0; k < (T * NP / 2 + 31) / 32; ++k) {
+        const int i = k * 32 + lane, t = i / (NP / 2), n = i % (NP / 2) * 2;
+        const bool on = t < nt && n < N;
+        if (T * NP / 2 % 32 == 0 || t < T) copy4(dst + t * NP + n, on ? p + (long long)t * r.st + n : r.p, on);
+    }
+}
+// The rows as FP32: from what ask_states brought, or (not `words`) a value at a time.
+template <int LN, int T>
+__device__ __forceinline__ void stage_states(const SsmRows& r, bool words, int b, int t0, int nt, int N, const uint16_t* raw,
+                                             float* dst, int lane) {
+    constexpr int NP = SsmWarp<LN>::NP, K = (T * NP / 2 + 31) / 32;
+    uint32_t v[K];
+    if (words) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+            if (T * NP / 2 % 32 == 0 || k * 32 + lane < T * NP / 2) v[k] = reinterpret_cast<const uint32_t*>(raw)[k * 32 + lane];
+    } else {
+        const uint16_t* p = r.p + (long long)b * r.sb + (long long)t0 * r.st;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int i = k * 32 + lane, t = i / (NP / 2), n = i % (NP / 2) * 2;
+            uint32_t lo = 0u, hi = 0u;
+            if (t < nt && n < N) lo = __ldg(p + (long long)t * r.st + n);
+            if (t < nt && n + 1 < N) hi = __ldg(p + (long long)t * r.st + n + 1);
+            v[k] = lo | hi << 16;
+        }
     }
 #pragma unroll
-    for (int k = 0; k < T * NP / 32; ++k) dst[k * 32 + lane] = bf_up(v[k]);
+    for (int k = 0; k < K; ++k)
+        if (T * NP / 2 % 32 == 0 || k * 32 + lane < T * NP / 2)
+            reinterpret_cast<float2*>(dst)[k * 32 + lane] = bf2_to_f2(v[k]);
 }
 
 // The rates of a lane's states (0 past N and D, where the other operands are zeros too).

@@ -18,9 +18,10 @@
 //   replay  each chunk again from its entry state, with the outputs.
 // The maps cost nearly as much as the replay, so where batch and channels alone
 // give enough warps (fewer than three chunks would fit) the replay runs alone.
-// A warp stages its own operands for 16 tokens: x, delta as BF16 rows (128
-// bytes of a row at N = 16), dt and dt x as FP32 into shared memory, from where
-// the lanes that share a channel read them.  No barrier between warps.
+// A warp stages its own operands for 8 tokens: x, delta as BF16 rows (128
+// bytes of a row at N = 16), dt and dt x as FP32 in shared memory, from where
+// the lanes that share a channel read them; the next tokens' rows are copied
+// meanwhile.  No barrier between warps.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -33,57 +34,69 @@ constexpr int kSsmWarps = 4;       // of a CTA, at most
 constexpr int kSsmCtas = 4;        // resident per SM: 128 registers a thread
 constexpr int kSsmSms = 152;
 
-template <int LN>
+// A warp's share of shared memory: the tile that it goes through, and the next
+// one's operands as they lie in memory, which arrive meanwhile.  Y: with what
+// only the outputs need.
+template <int LN, bool Y>
 struct FwdTile {
-    static constexpr int T = LN == 1 ? 8 : 16;   // tokens
+    static constexpr int T = LN == 1 ? 4 : 8;   // tokens
     using W = SsmWarp<LN>;
     float dt[T][W::CW];    // then the sums over the states
     float k[T][W::CW];
     float b[T][W::NP];
-    float c[T][W::NP];
+    float c[Y ? T : 1][Y ? W::NP : 4];
+    uint16_t x[2][T][W::CW], delta[2][T][W::CW];
+    uint16_t gate[Y ? 2 : 1][Y ? T : 1][Y ? W::CW : 8];
+    uint16_t rb[2][T][W::NP];
+    uint16_t rc[Y ? 2 : 1][Y ? T : 1][Y ? W::NP : 8];
 };
 
-// dt and dt x of nt tokens.
-template <int LN>
-__device__ __forceinline__ void stage_inputs(const SsmArgs& a, int b, int c0, int t0, int nt, FwdTile<LN>& s, int lane) {
-    using W = SsmWarp<LN>;
-    constexpr int IT = FwdTile<LN>::T / W::RPI;
-    const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
-    const bool on = c0 + c8 < a.D;
-    const uint16_t* px = a.x.p + (long long)b * a.x.sb + (long long)t0 * a.x.st + c0 + c8;
-    const uint16_t* pd = a.delta.p + (long long)b * a.delta.sb + (long long)t0 * a.delta.st + c0 + c8;
-    uint4 qx[IT], qd[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int r = r0 + i * W::RPI;
-        qx[i] = qd[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (on && r < nt) {
-            qx[i] = __ldg(reinterpret_cast<const uint4*>(px + (long long)r * a.x.st));
-            qd[i] = __ldg(reinterpret_cast<const uint4*>(pd + (long long)r * a.delta.st));
-        }
+// Asks for the operands of nt tokens.
+template <int LN, bool Y>
+__device__ __forceinline__ void ask_tile(const SsmArgs& a, int b, int c0, int t0, int nt, FwdTile<LN, Y>& s, int q, int lane) {
+    constexpr int T = FwdTile<LN, Y>::T;
+    ask_rows<LN, T>(a.x.p, a.x.sb, a.x.st, b, t0, nt, c0, a.D, &s.x[q][0][0], lane);
+    ask_rows<LN, T>(a.delta.p, a.delta.sb, a.delta.st, b, t0, nt, c0, a.D, &s.delta[q][0][0], lane);
+    if (Y && a.gate.p != nullptr)
+        ask_rows<LN, T>(a.gate.p, a.gate.sb, a.gate.st, b, t0, nt, c0, a.D, &s.gate[Y ? q : 0][0][0], lane);
+    if (a.words) {
+        ask_states<LN, T>(a.b, b, t0, nt, a.N, &s.rb[q][0][0], lane);
+        if (Y) ask_states<LN, T>(a.c, b, t0, nt, a.N, &s.rc[Y ? q : 0][0][0], lane);
     }
+    copies_commit();
+}
+
+// dt and dt x of nt tokens, b and c in FP32.
+template <int LN, bool Y>
+__device__ __forceinline__ void stage_tile(const SsmArgs& a, int b, int c0, int t0, int nt, FwdTile<LN, Y>& s, int q, int lane) {
+    using W = SsmWarp<LN>;
+    constexpr int T = FwdTile<LN, Y>::T, IT = (T + W::RPI - 1) / W::RPI;
+    const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     f2x bias[4];
-    load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
+    load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, c0 + c8 < a.D, bias);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int r = r0 + i * W::RPI;
+        if (T % W::RPI != 0 && r >= T) break;
         f2x x[4], d[4];
-        unpack_pairs(qx[i], x);
-        unpack_pairs(qd[i], d);
+        unpack_pairs(*reinterpret_cast<const uint4*>(&s.x[q][r][c8]), x);
+        unpack_pairs(*reinterpret_cast<const uint4*>(&s.delta[q][r][c8]), d);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            // a token past the end keeps the state and adds nothing
-            d[e] = on && r < nt ? softplus2(add2(d[e], bias[e])) : 0ull;
+            d[e] = softplus2(add2(d[e], bias[e]));
+            if (r >= nt) d[e] = 0ull;   // a token past the end keeps the state and adds nothing
             x[e] = mul2(d[e], x[e]);
         }
         store_pairs(&s.dt[r][c8], d);
         store_pairs(&s.k[r][c8], x);
     }
+    stage_states<LN, T>(a.b, a.words, b, t0, nt, a.N, &s.rb[q][0][0], &s.b[0][0], lane);
+    if (Y) stage_states<LN, T>(a.c, a.words, b, t0, nt, a.N, &s.rc[Y ? q : 0][0][0], &s.c[0][0], lane);
 }
 
 // One token: h <- e^(A dt) h + k b, and (Y) the sums of c h.
 template <int LN, bool Y>
-__device__ __forceinline__ void advance(const FwdTile<LN>& s, int t, int lc, int ln, const f2x (&A)[kSsmCh][4],
+__device__ __forceinline__ void advance(const FwdTile<LN, Y>& s, int t, int lc, int ln, const f2x (&A)[kSsmCh][4],
                                         f2x (&h)[kSsmCh][4], float (&y)[kSsmCh], float4& dt) {
     dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
     const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
@@ -131,14 +144,14 @@ __device__ __forceinline__ SsmPlace place(const SsmArgs& a, int chunks) {
 template <int LN>
 __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(const SsmArgs a) {
     using W = SsmWarp<LN>;
-    constexpr int T = FwdTile<LN>::T;
+    constexpr int T = FwdTile<LN, false>::T;
     extern __shared__ __align__(16) uint8_t buf[];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
     const SsmPlace p = place(a, a.nchunk - 1);
     if (!p.on) return;
-    FwdTile<LN>& s = reinterpret_cast<FwdTile<LN>*>(buf)[p.warp];
+    FwdTile<LN, false>& s = reinterpret_cast<FwdTile<LN, false>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
     f2x A[kSsmCh][4], h[kSsmCh][4];
     load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
@@ -148,15 +161,17 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(cons
         for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     bool cut = false;
-    const int end = min(a.L, (p.chunk + 1) * a.chunk);
-    for (int t0 = p.chunk * a.chunk; t0 < end; t0 += T) {
+    const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
+    ask_tile<LN, false>(a, p.b, c0, begin, min(T, end - begin), s, 0, lane);
+    for (int t0 = begin, q = 0; t0 < end; t0 += T, q ^= 1) {
         const int nt = min(T, end - t0);
-        __syncwarp();
-        stage_inputs<LN>(a, p.b, c0, t0, nt, s, lane);
-        stage_states<LN, T>(a.b, p.b, t0, nt, a.N, &s.b[0][0], lane);
         const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
         cut |= starts != 0u;
+        copies_wait();
         __syncwarp();
+        stage_tile<LN, false>(a, p.b, c0, t0, nt, s, q, lane);
+        __syncwarp();
+        if (t0 + T < end) ask_tile<LN, false>(a, p.b, c0, t0 + T, min(T, end - t0 - T), s, q ^ 1, lane);
 #pragma unroll 2
         for (int t = 0; t < T; ++t) {
             if ((starts >> t) & 1u) {
@@ -235,14 +250,14 @@ __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a) {
 template <int LN, bool KEEP>
 __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(const SsmArgs a) {
     using W = SsmWarp<LN>;
-    constexpr int T = FwdTile<LN>::T, IT = T / W::RPI;
+    constexpr int T = FwdTile<LN, true>::T, IT = (T + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
     const SsmPlace p = place(a, a.nchunk);
     if (!p.on) return;
-    FwdTile<LN>& s = reinterpret_cast<FwdTile<LN>*>(buf)[p.warp];
+    FwdTile<LN, true>& s = reinterpret_cast<FwdTile<LN, true>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
     f2x A[kSsmCh][4], h[kSsmCh][4];
     load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
@@ -252,21 +267,23 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
         load_state(a.h0, p.b, ch, ln * kSsmSt, a.D, a.N, h);
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     const bool on = c0 + c8 < a.D;
-    const int end = min(a.L, (p.chunk + 1) * a.chunk);
+    f2x skip[4];
+    load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, on, skip);
+    const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
     const int slots = (a.L + kSsmKeep - 1) / kSsmKeep;
-    for (int t0 = p.chunk * a.chunk; t0 < end; t0 += T) {
+    ask_tile<LN, true>(a, p.b, c0, begin, min(T, end - begin), s, 0, lane);
+    for (int t0 = begin, q = 0; t0 < end; t0 += T, q ^= 1) {
         const int nt = min(T, end - t0);
-        __syncwarp();
-        stage_inputs<LN>(a, p.b, c0, t0, nt, s, lane);
-        stage_states<LN, T>(a.b, p.b, t0, nt, a.N, &s.b[0][0], lane);
-        stage_states<LN, T>(a.c, p.b, t0, nt, a.N, &s.c[0][0], lane);
         const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
+        copies_wait();
         __syncwarp();
+        stage_tile<LN, true>(a, p.b, c0, t0, nt, s, q, lane);
+        __syncwarp();
+        if (t0 + T < end) ask_tile<LN, true>(a, p.b, c0, t0 + T, min(T, end - t0 - T), s, q ^ 1, lane);
+        if (KEEP && t0 % kSsmKeep == 0)
+            store_tile_state(a.keep + (((long long)p.b * slots + t0 / kSsmKeep) * a.groups + p.group) * (kSsmVec * 32), lane, h);
 #pragma unroll 2
         for (int t = 0; t < T; ++t) {
-            if (KEEP && t % kSsmKeep == 0 && t < nt)
-                store_tile_state(a.keep + (((long long)p.b * slots + (t0 + t) / kSsmKeep) * a.groups + p.group) *
-                                              (kSsmVec * 32), lane, h);
             if ((starts >> t) & 1u) {
 #pragma unroll
                 for (int i = 0; i < kSsmCh; ++i)
@@ -282,10 +299,6 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
         }
         __syncwarp();
         if (on) {
-            f2x skip[4];
-            load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, true, skip);
-            const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)t0 * a.x.st + c0 + c8;
-            const uint16_t* pg = a.gate.p + (long long)p.b * a.gate.sb + (long long)t0 * a.gate.st + c0 + c8;
             uint16_t* py = a.y + ((long long)p.b * a.L + t0) * a.D + c0 + c8;
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
@@ -293,14 +306,13 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
                 if (r >= nt) break;
                 f2x y[4], x[4];
                 read_pairs(&s.dt[r][c8], y);
-                if (a.d_skip != nullptr) {
-                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(px + (long long)r * a.x.st)), x);
+                unpack_pairs(*reinterpret_cast<const uint4*>(&s.x[q][r][c8]), x);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) y[e] = fma2(skip[e], x[e], y[e]);
-                }
+                for (int e = 0; e < 4; ++e)
+                    if (a.d_skip != nullptr) y[e] = fma2(skip[e], x[e], y[e]);
                 if (a.gate.p != nullptr) {
                     f2x z[4];
-                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(pg + (long long)r * a.gate.st)), z);
+                    unpack_pairs(*reinterpret_cast<const uint4*>(&s.gate[q][r][c8]), z);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float z0, z1;
@@ -388,9 +400,9 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs a,
 template <int LN>
 cudaError_t fwd_as(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
     const SsmSplit w = ssm_split(a.D, a.N);
-    const size_t smem = w.warps * sizeof(FwdTile<LN>), most = kSsmWarps * sizeof(FwdTile<LN>);
     const dim3 block((unsigned)w.warps * 32);
     if (what == 0) {
+        const size_t smem = w.warps * sizeof(FwdTile<LN, false>), most = kSsmWarps * sizeof(FwdTile<LN, false>);
         static std::atomic<bool> allowed[64];
         const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_maps_kernel<LN>), most, allowed);
         if (e != cudaSuccess) return e;
@@ -400,6 +412,7 @@ cudaError_t fwd_as(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
         return launch_ex(ssm_prefix_kernel<LN, false>, dim3((unsigned)((long long)a.B * a.groups)), dim3(256), 0, s, pdl, a);
     if (what == 2)
         return launch_ex(ssm_prefix_kernel<LN, true>, dim3((unsigned)((long long)a.B * a.groups)), dim3(256), 0, s, pdl, a);
+    const size_t smem = w.warps * sizeof(FwdTile<LN, true>), most = kSsmWarps * sizeof(FwdTile<LN, true>);
     const dim3 grid((unsigned)((long long)a.B * a.nchunk * a.ngq));
     if (a.keep != nullptr) {
         static std::atomic<bool> allowed[64];

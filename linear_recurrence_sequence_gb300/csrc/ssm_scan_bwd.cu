@@ -25,6 +25,7 @@
 #include <algorithm>
 
 #include "ssm.cuh"
+#include "umma.cuh"
 
 namespace lrs {
 
@@ -66,17 +67,29 @@ __device__ __forceinline__ BwdPlace bwd_place(const SsmArgs& a, int chunks, int 
 
 template <int LN>
 struct RevTile {
-    static constexpr int T = LN == 1 ? 8 : 16;
+    static constexpr int T = LN == 1 ? 4 : 8;
     using W = SsmWarp<LN>;
     float dt[T][W::CW];
     float dy[T][W::CW];
     float c[T][W::NP];
+    uint16_t delta[2][T][W::CW], y[2][T][W::CW], gate[2][T][W::CW], rc[2][T][W::NP];
 };
+
+template <int LN>
+__device__ __forceinline__ void ask_reverse(const SsmBwdArgs& g, int b, int c0, int t0, int nt, RevTile<LN>& s, int q, int lane) {
+    constexpr int T = RevTile<LN>::T;
+    const SsmArgs& a = g.f;
+    ask_rows<LN, T>(a.delta.p, a.delta.sb, a.delta.st, b, t0, nt, c0, a.D, &s.delta[q][0][0], lane);
+    ask_rows<LN, T>(g.dy, (long long)a.L * a.D, a.D, b, t0, nt, c0, a.D, &s.y[q][0][0], lane);
+    if (a.gate.p != nullptr) ask_rows<LN, T>(a.gate.p, a.gate.sb, a.gate.st, b, t0, nt, c0, a.D, &s.gate[q][0][0], lane);
+    if (a.words) ask_states<LN, T>(a.c, b, t0, nt, a.N, &s.rc[q][0][0], lane);
+    copies_commit();
+}
 
 template <int LN>
 __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmBwdArgs g) {
     using W = SsmWarp<LN>;
-    constexpr int T = RevTile<LN>::T, IT = T / W::RPI;
+    constexpr int T = RevTile<LN>::T, IT = (T + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
     pdl_trigger();
     pdl_wait();
@@ -87,7 +100,6 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
     RevTile<LN>& s = reinterpret_cast<RevTile<LN>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
-    const bool on = c0 + c8 < a.D;
     f2x A[kSsmCh][4], u[kSsmCh][4];
     load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
 #pragma unroll
@@ -97,42 +109,35 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     bool cut = false;
     const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
-    for (int t0 = begin + (end - 1 - begin) / T * T; t0 >= begin; t0 -= T) {
+    const int last = begin + (end - 1 - begin) / T * T;
+    ask_reverse<LN>(g, p.b, c0, last, end - last, s, 0, lane);
+    for (int t0 = last, q = 0; t0 >= begin; t0 -= T, q ^= 1) {
         const int nt = min(T, end - t0);
-        __syncwarp();
-        {
-            const uint16_t* pd = a.delta.p + (long long)p.b * a.delta.sb + (long long)t0 * a.delta.st + c0 + c8;
-            const uint16_t* pz = a.gate.p + (long long)p.b * a.gate.sb + (long long)t0 * a.gate.st + c0 + c8;
-            const uint16_t* py = g.dy + ((long long)p.b * a.L + t0) * a.D + c0 + c8;
-            uint4 qd[IT], qy[IT], qz[IT];
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = r0 + i * W::RPI;
-                qd[i] = qy[i] = qz[i] = make_uint4(0u, 0u, 0u, 0u);
-                if (on && r < nt) {
-                    qd[i] = __ldg(reinterpret_cast<const uint4*>(pd + (long long)r * a.delta.st));
-                    qy[i] = __ldg(reinterpret_cast<const uint4*>(py + (long long)r * a.D));
-                    if (a.gate.p != nullptr) qz[i] = __ldg(reinterpret_cast<const uint4*>(pz + (long long)r * a.gate.st));
-                }
-            }
-            f2x bias[4];
-            load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
-#pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = r0 + i * W::RPI;
-                f2x d[4], dy[4];
-                unpack_pairs(qd[i], d);
-                gated(qy[i], qz[i], a.gate.p != nullptr, dy);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) d[e] = on && r < nt ? softplus2(add2(d[e], bias[e])) : 0ull;
-                store_pairs(&s.dt[r][c8], d);
-                store_pairs(&s.dy[r][c8], dy);
-            }
-        }
-        stage_states<LN, T>(a.c, p.b, t0, nt, a.N, &s.c[0][0], lane);
         const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
         cut |= starts != 0u;
+        copies_wait();
         __syncwarp();
+        f2x bias[4];
+        load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, c0 + c8 < a.D, bias);
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = r0 + i * W::RPI;
+            if (T % W::RPI != 0 && r >= T) break;
+            f2x d[4], dy[4];
+            unpack_pairs(*reinterpret_cast<const uint4*>(&s.delta[q][r][c8]), d);
+            gated(*reinterpret_cast<const uint4*>(&s.y[q][r][c8]), *reinterpret_cast<const uint4*>(&s.gate[q][r][c8]),
+                  a.gate.p != nullptr, dy);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                d[e] = softplus2(add2(d[e], bias[e]));
+                if (r >= nt) d[e] = 0ull;
+            }
+            store_pairs(&s.dt[r][c8], d);
+            store_pairs(&s.dy[r][c8], dy);
+        }
+        stage_states<LN, T>(a.c, a.words, p.b, t0, nt, a.N, &s.rc[q][0][0], &s.c[0][0], lane);
+        __syncwarp();
+        if (t0 > begin) ask_reverse<LN>(g, p.b, c0, t0 - T, T, s, q ^ 1, lane);
 #pragma unroll 2
         for (int t = T - 1; t >= 0; --t) {
             const float4 dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
@@ -169,19 +174,39 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
 }
 
 constexpr int kBT = kSsmKeep;   // tokens of a tile of the main kernel
+constexpr int kBwdTmem = 32 * kBT;   // tensor-memory columns of a CTA
 
 template <int LN>
 struct BwdTile {
     using W = SsmWarp<LN>;
-    float4 h[kBT / 2][kSsmVec][32];   // states before the even tokens
-    float dt[kBT][W::CW];             // then s1 dt
-    float x[kBT][W::CW];              // then ddt
+    float4 kept[kSsmVec][32];         // the state before the tile
+    float dt[kBT][W::CW];
+    float k[kBT][W::CW];              // dt x, then sum G b
     float dy[kBT][W::CW];             // dy'
-    float y[kBT][W::CW];              // sums c h
+    float y[kBT][W::CW];              // sums c h, then sum A r
     float b[kBT][W::NP];
     float c[kBT][W::NP];
     float red[kBT][2 * W::NP];        // db, dc of the warp's channels
+    uint16_t x[2][kBT][W::CW], delta[2][kBT][W::CW], dys[2][kBT][W::CW], gate[2][kBT][W::CW];
+    uint16_t rb[2][kBT][W::NP], rc[2][kBT][W::NP];
 };
+
+template <int LN, bool GATE>
+__device__ __forceinline__ void ask_back(const SsmBwdArgs& g, const float4* kept, int b, int c0, int t0, int nt,
+                                         BwdTile<LN>& s, int q, int lane) {
+    const SsmArgs& a = g.f;
+#pragma unroll
+    for (int k = 0; k < kSsmVec; ++k) copy16(&s.kept[k][lane], kept + k * 32 + lane, true);
+    ask_rows<LN, kBT>(a.x.p, a.x.sb, a.x.st, b, t0, nt, c0, a.D, &s.x[q][0][0], lane);
+    ask_rows<LN, kBT>(a.delta.p, a.delta.sb, a.delta.st, b, t0, nt, c0, a.D, &s.delta[q][0][0], lane);
+    ask_rows<LN, kBT>(g.dy, (long long)a.L * a.D, a.D, b, t0, nt, c0, a.D, &s.dys[q][0][0], lane);
+    if (GATE) ask_rows<LN, kBT>(a.gate.p, a.gate.sb, a.gate.st, b, t0, nt, c0, a.D, &s.gate[q][0][0], lane);
+    if (a.words) {
+        ask_states<LN, kBT>(a.b, b, t0, nt, a.N, &s.rb[q][0][0], lane);
+        ask_states<LN, kBT>(a.c, b, t0, nt, a.N, &s.rc[q][0][0], lane);
+    }
+    copies_commit();
+}
 
 // Sums of v[0 .. 7] (four pairs) over the lanes that hold the same states; the
 // lanes write theirs to out[8].
@@ -219,90 +244,76 @@ __device__ __forceinline__ f2x decay(f2x A, f2x dt) {
     return pk2(ex2_approx(e0), ex2_approx(e1));
 }
 
-// One token's adjoint for 8 states of a channel, given a and the state before.
-__device__ __forceinline__ void adjoint(f2x y2, f2x k2, f2x d2, const f2x (&A)[4], const f2x (&a)[4], const f2x (&hp)[4],
-                                        const f2x (&b)[4], const f2x (&c)[4], f2x (&u)[4], f2x (&db)[4], f2x (&dA)[4],
-                                        float& s1, float& s2) {
-    f2x p1 = 0ull, p2 = 0ull;
+// A lane's states to and from 32 columns of tensor memory.
+__device__ __forceinline__ void states_to_tmem(uint32_t at, const f2x (&h)[kSsmCh][4]) {
+    uint32_t r[32];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const f2x G = fma2(y2, c[j], u[j]);
-        p1 = j ? fma2(G, b[j], p1) : mul2(G, b[j]);
-        db[j] = fma2(k2, G, db[j]);
-        u[j] = mul2(a[j], G);
-        const f2x r = mul2(u[j], hp[j]);
-        p2 = j ? fma2(A[j], r, p2) : mul2(A[j], r);
-        dA[j] = fma2(d2, r, dA[j]);
+    for (int i = 0; i < 16; ++i) {
+        float lo, hi;
+        up2(h[i / 4][i % 4], lo, hi);
+        r[2 * i] = __float_as_uint(lo);
+        r[2 * i + 1] = __float_as_uint(hi);
     }
-    float lo, hi;
-    up2(p1, lo, hi);
-    s1 = lo + hi;
-    up2(p2, lo, hi);
-    s2 = lo + hi;
+    tmem_st32(at, r);
 }
 
-// Tokens 2 p + 1 and 2 p of a tile.  CUT: a sequence may start at either.
-template <int LN, bool CUT>
-__device__ __forceinline__ void back_pair(BwdTile<LN>& s, int p, uint32_t starts, int lane, const f2x (&A)[kSsmCh][4],
-                                          f2x (&u)[kSsmCh][4], f2x (&dA)[kSsmCh][4]) {
+// One token's adjoint; `at`: where the state before it waits.
+template <int LN>
+__device__ __forceinline__ void back(BwdTile<LN>& s, int t, bool start, uint32_t at, int lane, const f2x (&A)[kSsmCh][4],
+                                     f2x (&u)[kSsmCh][4], f2x (&dA)[kSsmCh][4]) {
     const int ln = lane % LN, lc = lane / LN;
-    const int t0 = 2 * p, t1 = t0 + 1;
-    const float4 dt0 = *reinterpret_cast<const float4*>(&s.dt[t0][lc * kSsmCh]);
-    const float4 dt1 = *reinterpret_cast<const float4*>(&s.dt[t1][lc * kSsmCh]);
-    const float4 x0 = *reinterpret_cast<const float4*>(&s.x[t0][lc * kSsmCh]);
-    const float4 x1 = *reinterpret_cast<const float4*>(&s.x[t1][lc * kSsmCh]);
-    const float4 y0 = *reinterpret_cast<const float4*>(&s.dy[t0][lc * kSsmCh]);
-    const float4 y1 = *reinterpret_cast<const float4*>(&s.dy[t1][lc * kSsmCh]);
-    const float d0[4] = {dt0.x, dt0.y, dt0.z, dt0.w}, d1[4] = {dt1.x, dt1.y, dt1.z, dt1.w};
-    const float xs0[4] = {x0.x, x0.y, x0.z, x0.w}, xs1[4] = {x1.x, x1.y, x1.z, x1.w};
-    const float ys0[4] = {y0.x, y0.y, y0.z, y0.w}, ys1[4] = {y1.x, y1.y, y1.z, y1.w};
-    f2x b0[4], b1[4], c0[4], c1[4], db0[4], db1[4];
-    read_states(&s.b[t0][ln * kSsmSt], b0);
-    read_states(&s.b[t1][ln * kSsmSt], b1);
-    read_states(&s.c[t0][ln * kSsmSt], c0);
-    read_states(&s.c[t1][ln * kSsmSt], c1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) db0[j] = db1[j] = 0ull;
-    float dx0[kSsmCh], dx1[kSsmCh], dd0[kSsmCh], dd1[kSsmCh];
-    const bool cut0 = CUT && ((starts >> t0) & 1u), cut1 = CUT && ((starts >> t1) & 1u);
+    uint32_t hp[32];
+    tmem_ld32(at, hp);
+    const float4 dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
+    const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
+    const float4 dy = *reinterpret_cast<const float4*>(&s.dy[t][lc * kSsmCh]);
+    const float ds[4] = {dt.x, dt.y, dt.z, dt.w}, ks[4] = {k.x, k.y, k.z, k.w}, ys[4] = {dy.x, dy.y, dy.z, dy.w};
+    f2x b[4], c[4], db[4];
+    read_states(&s.b[t][ln * kSsmSt], b);
+    read_states(&s.c[t][ln * kSsmSt], c);
+    float s1[kSsmCh], s2[kSsmCh];
 #pragma unroll
     for (int i = 0; i < kSsmCh; ++i) {
-        const float4 q0 = s.h[p][2 * i][lane], q1 = s.h[p][2 * i + 1][lane];
-        f2x hp[4] = {pk2(q0.x, q0.y), pk2(q0.z, q0.w), pk2(q1.x, q1.y), pk2(q1.z, q1.w)}, hq[4], a0[4], a1[4];
-        const f2x e0 = dup2(d0[i]), e1 = dup2(d1[i]), k0 = mul2(e0, dup2(xs0[i])), k1 = mul2(e1, dup2(xs1[i]));
+        const f2x d2 = dup2(ds[i]), k2 = dup2(ks[i]), y2 = dup2(ys[i]);
+        f2x p = 0ull;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            a0[j] = decay(A[i][j], e0);
-            a1[j] = decay(A[i][j], e1);
-            if (CUT && cut0) {
-                a0[j] = 0ull;
-                hp[j] = 0ull;
-            }
-            hq[j] = fma2(a0[j], hp[j], mul2(k0, b0[j]));
-            if (CUT && cut1) {
-                a1[j] = 0ull;
-                hq[j] = 0ull;
-            }
+            const f2x G = fma2(y2, c[j], u[i][j]);
+            p = j ? fma2(G, b[j], p) : mul2(G, b[j]);
+            db[j] = i ? fma2(k2, G, db[j]) : mul2(k2, G);
+            u[i][j] = mul2(decay(A[i][j], d2), G);
         }
-        float s1, s2;
-        adjoint(dup2(ys1[i]), k1, e1, A[i], a1, hq, b1, c1, u[i], db1, dA[i], s1, s2);
-        dx1[i] = s1 * d1[i];
-        dd1[i] = fmaf(s1, xs1[i], kLn2 * s2);
-        adjoint(dup2(ys0[i]), k0, e0, A[i], a0, hp, b0, c0, u[i], db0, dA[i], s1, s2);
-        dx0[i] = s1 * d0[i];
-        dd0[i] = fmaf(s1, xs0[i], kLn2 * s2);
+        float lo, hi;
+        up2(p, lo, hi);
+        s1[i] = lo + hi;
     }
-    sum_states<LN>(dx1, lane);
-    sum_states<LN>(dd1, lane);
-    sum_states<LN>(dx0, lane);
-    sum_states<LN>(dd0, lane);
-    __syncwarp();   // every lane has read the tokens' dt and x
-    put_channels<LN>(s.dt[t1], dx1, lc, ln);
-    put_channels<LN>(s.x[t1], dd1, lc, ln);
-    put_channels<LN>(s.dt[t0], dx0, lc, ln);
-    put_channels<LN>(s.x[t0], dd0, lc, ln);
-    sum_channels<LN>(db1, &s.red[t1][ln * kSsmSt], lane);
-    sum_channels<LN>(db0, &s.red[t0][ln * kSsmSt], lane);
+    tmem_ld32_wait(hp);
+#pragma unroll
+    for (int i = 0; i < kSsmCh; ++i) {
+        const f2x d2 = dup2(ds[i]);
+        f2x p = 0ull;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const f2x r = mul2(u[i][j], pk2(__uint_as_float(hp[8 * i + 2 * j]), __uint_as_float(hp[8 * i + 2 * j + 1])));
+            p = j ? fma2(A[i][j], r, p) : mul2(A[i][j], r);
+            dA[i][j] = fma2(d2, r, dA[i][j]);
+        }
+        float lo, hi;
+        up2(p, lo, hi);
+        s2[i] = lo + hi;
+    }
+    if (start) {   // nothing goes past a start (the state before it waits as zeros)
+#pragma unroll
+        for (int i = 0; i < kSsmCh; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[i][j] = 0ull;
+    }
+    sum_states<LN>(s1, lane);
+    sum_states<LN>(s2, lane);
+    __syncwarp();   // every lane has read the token's dt x
+    put_channels<LN>(s.k[t], s1, lc, ln);
+    put_channels<LN>(s.y[t], s2, lc, ln);
+    sum_channels<LN>(db, &s.red[t][ln * kSsmSt], lane);
 }
 
 __device__ __forceinline__ void put8(void* p, long long at, bool f32, const f2x (&v)[4]) {
@@ -315,8 +326,14 @@ __device__ __forceinline__ void put8(void* p, long long at, bool f32, const f2x 
 template <int LN, bool GATE>
 __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwdArgs g) {
     using W = SsmWarp<LN>;
-    constexpr int IT = kBT / W::RPI > 0 ? kBT / W::RPI : 1;
+    constexpr int IT = (kBT + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
+    __shared__ uint32_t s_tmem;
+    // a dependent kernel may ask for tensor memory: not before every CTA of this one has its own
+    if (threadIdx.x < 32) tmem_alloc(&s_tmem, kBwdTmem);
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
     pdl_trigger();
     pdl_wait();
     const SsmArgs& a = g.f;
@@ -324,6 +341,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     const BwdPlace p = bwd_place(a, a.nchunk, 0);
     BwdTile<LN>* tiles = reinterpret_cast<BwdTile<LN>*>(buf);
     BwdTile<LN>& s = tiles[p.warp];
+    const uint32_t tmem = s_tmem + ((uint32_t)p.warp << 21);   // the warp's 32 lanes
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     const bool on = p.on && c0 + c8 < a.D;
@@ -339,79 +357,79 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
 #pragma unroll
         for (int j = 0; j < 4; ++j) dA[i][j] = 0ull;
     f2x dskip[4] = {0ull, 0ull, 0ull, 0ull}, dbias[4] = {0ull, 0ull, 0ull, 0ull};
-    f2x bias[4], skip[4];
-    load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
-    load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, on, skip);
     const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
-    const int slots = (a.L + kSsmKeep - 1) / kSsmKeep;
-    for (int t0 = begin + (end - 1 - begin) / kBT * kBT; t0 >= begin; t0 -= kBT) {
+    const int last = begin + (end - 1 - begin) / kBT * kBT;
+    const long long stride = (long long)a.groups * (kSsmVec * 32);   // of the kept states, a tile back
+    const float4* kept = a.keep + ((long long)p.b * ((a.L + kBT - 1) / kBT) + last / kBT) * stride + (long long)p.group * (kSsmVec * 32);
+    if (p.on) ask_back<LN, GATE>(g, kept, p.b, c0, last, end - last, s, 0, lane);
+    for (int t0 = last, q = 0; t0 >= begin; t0 -= kBT, q ^= 1, kept -= stride) {
         const int nt = min(kBT, end - t0);
         const long long row = (long long)p.b * a.L + t0;
-        const long long ox = (long long)p.b * a.x.sb + (long long)t0 * a.x.st + c0 + c8;
-        const long long od = (long long)p.b * a.delta.sb + (long long)t0 * a.delta.st + c0 + c8;
-        const long long oz = (long long)p.b * a.gate.sb + (long long)t0 * a.gate.st + c0 + c8;
-        const long long oy = row * a.D + c0 + c8;
         uint32_t starts = 0u;
         if (p.on) {
+            starts = start_bits(a.reset, row, nt, lane);
+            copies_wait();
+            __syncwarp();
+            f2x bias[4];
+            load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int r = r0 + i * W::RPI;
-                if (r >= kBT) break;
-                const bool in = on && r < nt;
-                uint4 qx = make_uint4(0u, 0u, 0u, 0u), qd = qx, qy = qx, qz = qx;
-                if (in) {
-                    qx = __ldg(reinterpret_cast<const uint4*>(a.x.p + ox + (long long)r * a.x.st));
-                    qd = __ldg(reinterpret_cast<const uint4*>(a.delta.p + od + (long long)r * a.delta.st));
-                    qy = __ldg(reinterpret_cast<const uint4*>(g.dy + oy + (long long)r * a.D));
-                    if (GATE) qz = __ldg(reinterpret_cast<const uint4*>(a.gate.p + oz + (long long)r * a.gate.st));
-                }
+                if (kBT % W::RPI != 0 && r >= kBT) break;
                 f2x x[4], d[4], dy[4];
-                unpack_pairs(qx, x);
-                unpack_pairs(qd, d);
-                gated(qy, qz, GATE, dy);
+                unpack_pairs(*reinterpret_cast<const uint4*>(&s.x[q][r][c8]), x);
+                unpack_pairs(*reinterpret_cast<const uint4*>(&s.delta[q][r][c8]), d);
+                gated(*reinterpret_cast<const uint4*>(&s.dys[q][r][c8]), *reinterpret_cast<const uint4*>(&s.gate[q][r][c8]), GATE,
+                      dy);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    d[e] = in ? softplus2(add2(d[e], bias[e])) : 0ull;
+                    d[e] = softplus2(add2(d[e], bias[e]));
+                    if (r >= nt) d[e] = 0ull;
                     dskip[e] = fma2(dy[e], x[e], dskip[e]);
+                    x[e] = mul2(d[e], x[e]);
                 }
                 store_pairs(&s.dt[r][c8], d);
-                store_pairs(&s.x[r][c8], x);
+                store_pairs(&s.k[r][c8], x);
                 store_pairs(&s.dy[r][c8], dy);
             }
-            stage_states<LN, kBT>(a.b, p.b, t0, nt, a.N, &s.b[0][0], lane);
-            stage_states<LN, kBT>(a.c, p.b, t0, nt, a.N, &s.c[0][0], lane);
-            starts = start_bits(a.reset, row, nt, lane);
+            stage_states<LN, kBT>(a.b, a.words, p.b, t0, nt, a.N, &s.rb[q][0][0], &s.b[0][0], lane);
+            stage_states<LN, kBT>(a.c, a.words, p.b, t0, nt, a.N, &s.rc[q][0][0], &s.c[0][0], lane);
         }
         // the other warps have taken the sums of the tile before
         __syncthreads();
         if (p.on) {
             f2x h[kSsmCh][4];
-            load_tile_state(a.keep + (((long long)p.b * slots + t0 / kSsmKeep) * a.groups + p.group) * (kSsmVec * 32), lane, h);
-#pragma unroll 2
+#pragma unroll
+            for (int k = 0; k < kSsmVec; ++k) {
+                const float4 v = s.kept[k][lane];
+                h[k >> 1][2 * (k & 1)] = pk2(v.x, v.y);
+                h[k >> 1][2 * (k & 1) + 1] = pk2(v.z, v.w);
+            }
+#pragma unroll 1
             for (int t = 0; t < kBT; ++t) {
-                if ((t & 1) == 0) store_tile_state(&s.h[t / 2][0][0], lane, h);
                 if ((starts >> t) & 1u) {
 #pragma unroll
                     for (int i = 0; i < kSsmCh; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
                 }
+                states_to_tmem(tmem + t * 32, h);
                 const float4 dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
-                const float4 x = *reinterpret_cast<const float4*>(&s.x[t][lc * kSsmCh]);
+                const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
                 const float4 dy = *reinterpret_cast<const float4*>(&s.dy[t][lc * kSsmCh]);
-                const float ds[4] = {dt.x, dt.y, dt.z, dt.w}, xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {dy.x, dy.y, dy.z, dy.w};
-                f2x b[4], c[4], dc[4] = {0ull, 0ull, 0ull, 0ull};
+                const float ds[4] = {dt.x, dt.y, dt.z, dt.w}, ks[4] = {k.x, k.y, k.z, k.w}, ys[4] = {dy.x, dy.y, dy.z, dy.w};
+                f2x b[4], c[4], dc[4];
                 read_states(&s.b[t][ln * kSsmSt], b);
                 if (GATE) read_states(&s.c[t][ln * kSsmSt], c);
                 float y[kSsmCh];
 #pragma unroll
                 for (int i = 0; i < kSsmCh; ++i) {
-                    const f2x d2 = dup2(ds[i]), k2 = mul2(d2, dup2(xs[i])), y2 = dup2(ys[i]);
+                    const f2x d2 = dup2(ds[i]), k2 = dup2(ks[i]), y2 = dup2(ys[i]);
                     f2x acc = 0ull;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         h[i][j] = fma2(decay(A[i][j], d2), h[i][j], mul2(k2, b[j]));
-                        dc[j] = fma2(y2, h[i][j], dc[j]);
+                        dc[j] = i ? fma2(y2, h[i][j], dc[j]) : mul2(y2, h[i][j]);
                         if (GATE) acc = j ? fma2(h[i][j], c[j], acc) : mul2(h[i][j], c[j]);
                     }
                     float lo, hi;
@@ -424,40 +442,21 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
                 }
                 sum_channels<LN>(dc, &s.red[t][W::NP + ln * kSsmSt], lane);
             }
-            if (starts == 0u) {
-#pragma unroll 1
-                for (int q = kBT / 2 - 1; q >= 0; --q) back_pair<LN, false>(s, q, 0u, lane, A, u, dA);
-            } else {
-#pragma unroll 1
-                for (int q = kBT / 2 - 1; q >= 0; --q) back_pair<LN, true>(s, q, starts, lane, A, u, dA);
-            }
+            tmem_st_wait();
             __syncwarp();
+            if (t0 > begin) ask_back<LN, GATE>(g, kept - stride, p.b, c0, t0 - kBT, kBT, s, q ^ 1, lane);
+            f2x skip[4];
+            load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, on, skip);
+            if (GATE) {
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = r0 + i * W::RPI;
-                if (!on || r >= nt) break;
-                f2x v[4], dy[4], t[4];
-                read_pairs(&s.dt[r][c8], v);
-                read_pairs(&s.dy[r][c8], dy);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = fma2(skip[e], dy[e], v[e]);
-                put8(g.dx.p, (long long)p.b * g.dx.sb + (long long)(t0 + r) * g.dx.st + c0 + c8, g.f32, v);
-                read_pairs(&s.x[r][c8], v);
-                unpack_pairs(__ldg(reinterpret_cast<const uint4*>(a.delta.p + od + (long long)r * a.delta.st)), t);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float r0_, r1_;
-                    up2(add2(t[e], bias[e]), r0_, r1_);
-                    v[e] = mul2(v[e], pk2(ssm_sigmoid(r0_), ssm_sigmoid(r1_)));
-                    dbias[e] = add2(dbias[e], v[e]);
-                }
-                put8(g.ddelta.p, (long long)p.b * g.ddelta.sb + (long long)(t0 + r) * g.ddelta.st + c0 + c8, g.f32, v);
-                if (GATE) {
-                    f2x z[4], x[4];
+                for (int i = 0; i < IT; ++i) {
+                    const int r = r0 + i * W::RPI;
+                    if (!on || r >= nt) break;
+                    f2x v[4], x[4], dy[4], z[4];
                     read_pairs(&s.y[r][c8], v);
-                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(a.x.p + ox + (long long)r * a.x.st)), x);
-                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(g.dy + oy + (long long)r * a.D)), dy);
-                    unpack_pairs(__ldg(reinterpret_cast<const uint4*>(a.gate.p + oz + (long long)r * a.gate.st)), z);
+                    unpack_pairs(*reinterpret_cast<const uint4*>(&s.x[q][r][c8]), x);
+                    unpack_pairs(*reinterpret_cast<const uint4*>(&s.dys[q][r][c8]), dy);
+                    unpack_pairs(*reinterpret_cast<const uint4*>(&s.gate[q][r][c8]), z);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         float z0, z1;
@@ -469,6 +468,36 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
                     }
                     put8(g.dgate.p, (long long)p.b * g.dgate.sb + (long long)(t0 + r) * g.dgate.st + c0 + c8, g.f32, v);
                 }
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int t = kBT - 1; t >= 0; --t) back<LN>(s, t, (starts >> t) & 1u, tmem + t * 32, lane, A, u, dA);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = r0 + i * W::RPI;
+                if (!on || r >= nt) break;
+                f2x v[4], s1[4], t[4], bias[4];
+                read_pairs(&s.k[r][c8], s1);
+                read_pairs(&s.dt[r][c8], t);
+                read_pairs(&s.dy[r][c8], v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fma2(s1[e], t[e], mul2(skip[e], v[e]));
+                put8(g.dx.p, (long long)p.b * g.dx.sb + (long long)(t0 + r) * g.dx.st + c0 + c8, g.f32, v);
+                read_pairs(&s.y[r][c8], v);
+                unpack_pairs(*reinterpret_cast<const uint4*>(&s.x[q][r][c8]), t);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = fma2(s1[e], t[e], mul2(dup2(kLn2), v[e]));
+                unpack_pairs(*reinterpret_cast<const uint4*>(&s.delta[q][r][c8]), t);
+                load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float w0, w1;
+                    up2(add2(t[e], bias[e]), w0, w1);
+                    v[e] = mul2(v[e], pk2(ssm_sigmoid(w0), ssm_sigmoid(w1)));
+                    dbias[e] = add2(dbias[e], v[e]);
+                }
+                put8(g.ddelta.p, (long long)p.b * g.ddelta.sb + (long long)(t0 + r) * g.ddelta.st + c0 + c8, g.f32, v);
             }
         }
         __syncthreads();
@@ -482,6 +511,10 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
             g.dbc[((row + t) * a.ngq + gq) * (2 * W::NP) + n] = v;
         }
     }
+    tmem_fence_before_sync();
+    __syncthreads();
+    tmem_fence_after_sync();
+    if (threadIdx.x < 32) tmem_dealloc(s_tmem, kBwdTmem);
     if (!p.on) return;
     const long long part = (long long)p.b * a.nchunk + p.chunk;
     // a part: dA [groups][kSsmVec][32] float4, then the two vectors [2][groups CW]

@@ -1631,10 +1631,14 @@ SsmScratch ssm_scratch(int B, int L, int D, int N, bool backward) {
     return s;
 }
 
+// Rows are addressed from the first of a tile's with 32 bits.
+bool ssm_rows_ok(const lrs_rows* r, bool each) {
+    return (each ? rows_each_ok(r) : rows_in_ok(r)) && r->token_stride <= (1LL << 26);
+}
 bool ssm_inputs_ok(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b, const lrs_rows* c,
                    const float* d_skip, const float* delta_bias, const lrs_rows* gate) {
-    return rows_in_ok(x) && rows_in_ok(delta) && req_each(a_log) && rows_each_ok(b) && rows_each_ok(c) && opt(d_skip) &&
-           opt(delta_bias) && (gate == nullptr || rows_in_ok(gate));
+    return ssm_rows_ok(x, false) && ssm_rows_ok(delta, false) && req_each(a_log) && ssm_rows_ok(b, true) &&
+           ssm_rows_ok(c, true) && opt(d_skip) && opt(delta_bias) && (gate == nullptr || ssm_rows_ok(gate, false));
 }
 SsmArgs ssm_args(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b, const lrs_rows* c,
                  const float* d_skip, const float* delta_bias, const lrs_rows* gate, const uint8_t* reset, int B, int L,
@@ -1657,6 +1661,8 @@ SsmArgs ssm_args(const lrs_rows* x, const lrs_rows* delta, const float* a_log, c
     a.groups = w.groups;
     a.ngq = w.ctas;
     a.words = rows_in_words(b, N) && rows_in_words(c, N);
+    a.quads = N % 4 == 0;   // the states are on 16-byte boundaries
+    a.rate_quads = a.quads && aligned16(a_log);
     return a;
 }
 void ssm_place(SsmArgs& a, const SsmScratch& l, void* scratch) {

@@ -670,6 +670,7 @@ struct SsmArgs {
     int B, L, D, N;
     int groups, ngq;             // warps' groups of channels; CTAs that they take
     int words;                   // b and c can be read two states at a time
+    int quads, rate_quads;       // [.., D, N] rows four at a time: states, a_log
     int chunk, nchunk;           // tokens of a chunk (a multiple of 16), chunks
     float4* maps;                // [B][nchunk][groups][8][32]
     float* sums;                 // [B][nchunk][groups * channels of a warp]

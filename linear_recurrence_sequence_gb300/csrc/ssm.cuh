@@ -10,14 +10,15 @@
 namespace lrs {
 
 // A warp owns 128 / LN channels: LN lanes share four channels, 8 states each,
-// so a lane holds 4 x 8 states of one chunk of time in registers.  LN = 1, 2,
-// 4, 8 for up to 8, 16, 32, 64 states a channel.  32 states a lane are what
-// makes the operands cheap: a token's step, input, b and c are 24 words of
-// shared memory a lane, three bytes a state, and the sum over the states of a
-// channel crosses LN lanes only.
+// so a lane holds 4 x 8 states of one chunk of time in registers, as pairs of
+// channels (FP32 arithmetic is two wide).  LN = 1, 2, 4, 8 for up to 8, 16, 32,
+// 64 states a channel.  32 states a lane are what makes the operands cheap: a
+// token's steps and inputs are 8 words of shared memory a lane, its b and c 8
+// each, which lie there twice, as the pairs that the arithmetic takes; and the
+// sum over the states of a channel crosses LN lanes only.
 constexpr int kSsmCh = 4;        // channels of a lane
 constexpr int kSsmSt = 8;        // states of a lane
-constexpr int kSsmVec = kSsmCh * kSsmSt / 4;   // its states as float4
+constexpr int kSsmVec = kSsmSt;   // its states as float4, four channels each
 
 template <int LN>
 struct SsmWarp {
@@ -99,8 +100,20 @@ __device__ __forceinline__ void read_pairs(const float* p, f2x (&v)[4]) {
     v[2] = pk2(b.x, b.y);
     v[3] = pk2(b.z, b.w);
 }
-// A lane's 8 states of one token's b or c.
-__device__ __forceinline__ void read_states(const float* p, f2x (&v)[4]) { read_pairs(p, v); }
+// A lane's states: [state][pair of channels].
+typedef f2x SsmStates[kSsmSt][kSsmCh / 2];
+__device__ __forceinline__ void clear_states(SsmStates& h) {
+#pragma unroll
+    for (int j = 0; j < kSsmSt; ++j) h[j][0] = h[j][1] = 0ull;
+}
+// Two of a token's b or c, each as a pair of equal values.
+__device__ __forceinline__ void read_twice(const float* p, f2x& v0, f2x& v1) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    v0 = pk2(q.x, q.y);
+    v1 = pk2(q.z, q.w);
+}
+// A lane's four channels as pairs.
+__device__ __forceinline__ void read_channels(const float* p, f2x (&v)[2]) { read_twice(p, v[0], v[1]); }
 
 __device__ __forceinline__ float bf_up(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
@@ -116,36 +129,40 @@ __device__ __forceinline__ void copy4(void* dst, const void* src, bool on) {
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// Asks for rows t0 .. t0 + nt - 1 (of T) of the warp's channels, zeros past nt and D.
+// Asks for nt rows (of T) of the warp's channels, zeros past nt and D.  p: the
+// first row's place of the warp's first channel.
 template <int LN, int T>
-__device__ __forceinline__ void ask_rows(const uint16_t* p, long long sb, long long st, int b, int t0, int nt, int c0, int D,
-                                         uint16_t* dst, int lane) {
+__device__ __forceinline__ void ask_rows(const uint16_t* p, long long st, int nt, int width, uint16_t* dst, int lane) {
     using W = SsmWarp<LN>;
     constexpr int IT = (T + W::RPI - 1) / W::RPI;
-    const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
-    const uint16_t* q = p + (long long)b * sb + (long long)t0 * st + c0 + c8;
+    const int c8 = lane % W::RL * 8, r0 = lane / W::RL, off = r0 * (int)st + c8;
+    uint16_t* d = dst + r0 * W::CW + c8;
+    if (nt == T && width >= W::CW) {
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+            if (T % W::RPI == 0 || r0 < T) copy16(d + i * W::RPI * W::CW, p + i * W::RPI * (int)st + off, true);
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
-        const int r = r0 + i * W::RPI;
-        const bool on = c0 + c8 < D && r < nt;
-        if (T % W::RPI == 0 || r < T) copy16(dst + r * W::CW + c8, on ? q + (long long)r * st : p, on);
+        const bool on = c8 < width && r0 + i * W::RPI < nt;
+        if (T % W::RPI == 0 || r0 < T) copy16(d + i * W::RPI * W::CW, on ? p + i * W::RPI * (int)st + off : p, on);
     }
 }
-// Rows of b or c, two states at a time (SsmArgs.words).
+// nt rows of b or c, two states at a time (SsmArgs.words).
 template <int LN, int T>
-__device__ __forceinline__ void ask_states(const SsmRows& r, int b, int t0, int nt, int N, uint16_t* dst, int lane) {
+__device__ __forceinline__ void ask_states(const uint16_t* p, long long st, int nt, int N, uint16_t* dst, int lane) {
     constexpr int NP = SsmWarp<LN>::NP;
-    const uint16_t* p = r.p + (long long)b * r.sb + (long long)t0 * r.st;
 #pragma unroll
     for (int k = 0; k < (T * NP / 2 + 31) / 32; ++k) {
         const int i = k * 32 + lane, t = i / (NP / 2), n = i % (NP / 2) * 2;
         const bool on = t < nt && n < N;
-        if (T * NP / 2 % 32 == 0 || t < T) copy4(dst + t * NP + n, on ? p + (long long)t * r.st + n : r.p, on);
+        if (T * NP / 2 % 32 == 0 || t < T) copy4(dst + 2 * i, on ? p + t * (int)st + n : p, on);
     }
 }
-// The rows as FP32: from what ask_states brought, or (not `words`) a value at a time.
+// The rows as FP32, every value twice: from what ask_states brought, or (not `words`) a value at a time.
 template <int LN, int T>
-__device__ __forceinline__ void stage_states(const SsmRows& r, bool words, int b, int t0, int nt, int N, const uint16_t* raw,
+__device__ __forceinline__ void stage_states(const uint16_t* p, long long st, bool words, int nt, int N, const uint16_t* raw,
                                              float* dst, int lane) {
     constexpr int NP = SsmWarp<LN>::NP, K = (T * NP / 2 + 31) / 32;
     uint32_t v[K];
@@ -154,93 +171,140 @@ __device__ __forceinline__ void stage_states(const SsmRows& r, bool words, int b
         for (int k = 0; k < K; ++k)
             if (T * NP / 2 % 32 == 0 || k * 32 + lane < T * NP / 2) v[k] = reinterpret_cast<const uint32_t*>(raw)[k * 32 + lane];
     } else {
-        const uint16_t* p = r.p + (long long)b * r.sb + (long long)t0 * r.st;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
             const int i = k * 32 + lane, t = i / (NP / 2), n = i % (NP / 2) * 2;
             uint32_t lo = 0u, hi = 0u;
-            if (t < nt && n < N) lo = __ldg(p + (long long)t * r.st + n);
-            if (t < nt && n + 1 < N) hi = __ldg(p + (long long)t * r.st + n + 1);
+            if (t < nt && n < N) lo = __ldg(p + t * (int)st + n);
+            if (t < nt && n + 1 < N) hi = __ldg(p + t * (int)st + n + 1);
             v[k] = lo | hi << 16;
         }
     }
 #pragma unroll
     for (int k = 0; k < K; ++k)
-        if (T * NP / 2 % 32 == 0 || k * 32 + lane < T * NP / 2)
-            reinterpret_cast<float2*>(dst)[k * 32 + lane] = bf2_to_f2(v[k]);
+        if (T * NP / 2 % 32 == 0 || k * 32 + lane < T * NP / 2) {
+            const float2 f = bf2_to_f2(v[k]);
+            reinterpret_cast<float4*>(dst)[k * 32 + lane] = make_float4(f.x, f.x, f.y, f.y);
+        }
+}
+// delta_bias of the warp's channels.
+template <int LN>
+__device__ __forceinline__ void stage_bias(const float* bias, int c0, int D, float* dst, int lane) {
+#pragma unroll
+    for (int i = lane; i < SsmWarp<LN>::CW; i += 32) dst[i] = bias != nullptr && c0 + i < D ? __ldg(bias + c0 + i) : 0.f;
 }
 
-// The rates of a lane's states (0 past N and D, where the other operands are zeros too).
-template <int LN>
-__device__ __forceinline__ void load_rates(const float* a_log, int c0, int n0, int D, int N, f2x (&A)[kSsmCh][4]) {
+// The warp's number in its CTA, the same in all its lanes for the compiler too.
+__device__ __forceinline__ int warp_of() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+
+// The first of the rows of batch row b from token t on, from channel c on.
+__device__ __forceinline__ const uint16_t* row_at(const SsmRows& r, int b, int t, int c) {
+    return r.p + (long long)b * r.sb + (long long)t * r.st + c;
+}
+
+// A lane's 4 x 8 values of a [D][N] matrix, zeros past D and N.  quads: N is a multiple of 4 and the matrix on a 16-byte
+// boundary (a lane's 8 values of a channel are one sector; one at a time they cost 8 times the L1 traffic).
+__device__ __forceinline__ void load_states(const float* m, bool quads, int c0, int n0, int D, int N, float (&v)[kSsmCh][kSsmSt]) {
+    const float* p = m + (long long)c0 * N + n0;
 #pragma unroll
-    for (int c = 0; c < kSsmCh; ++c)
+    for (int i = 0; i < kSsmCh; ++i) {
+        if (quads) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = n0 + 2 * j + e;
-                v[e] = c0 + c < D && n < N ? ssm_rate(__ldg(a_log + (long long)(c0 + c) * N + n)) : 0.f;
+            for (int j = 0; j < kSsmSt; j += 4) {
+                float4 q = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (c0 + i < D && n0 + j < N) q = __ldg(reinterpret_cast<const float4*>(p + i * N + j));
+                v[i][j] = q.x;
+                v[i][j + 1] = q.y;
+                v[i][j + 2] = q.z;
+                v[i][j + 3] = q.w;
             }
-            A[c][j] = pk2(v[0], v[1]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSsmSt; ++j) v[i][j] = c0 + i < D && n0 + j < N ? __ldg(p + i * N + j) : 0.f;
         }
+    }
+}
+// The rates of a lane's states (0 past N and D, where the other operands are zeros too).
+__device__ __forceinline__ void load_rates(const float* a_log, bool quads, int c0, int n0, int D, int N, SsmStates& A) {
+    float v[kSsmCh][kSsmSt];
+    load_states(a_log, quads, c0, n0, D, N, v);
+#pragma unroll
+    for (int i = 0; i < kSsmCh; ++i)
+#pragma unroll
+        for (int j = 0; j < kSsmSt; ++j) v[i][j] = c0 + i < D && n0 + j < N ? ssm_rate(v[i][j]) : 0.f;
+#pragma unroll
+    for (int j = 0; j < kSsmSt; ++j) {
+        A[j][0] = pk2(v[0][j], v[1][j]);
+        A[j][1] = pk2(v[2][j], v[3][j]);
+    }
 }
 
 // A lane's states from and to [.., D, N] rows of FP32.
-__device__ __forceinline__ void load_state(const float* s, long long row, int c0, int n0, int D, int N,
-                                           f2x (&h)[kSsmCh][4]) {
+__device__ __forceinline__ void load_state(const float* s, bool quads, long long row, int c0, int n0, int D, int N, SsmStates& h) {
+    clear_states(h);
+    if (s == nullptr) return;
+    float v[kSsmCh][kSsmSt];
+    load_states(s + row * D * N, quads, c0, n0, D, N, v);
 #pragma unroll
-    for (int c = 0; c < kSsmCh; ++c)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float v[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = n0 + 2 * j + e;
-                v[e] = s != nullptr && c0 + c < D && n < N ? __ldg(s + (row * D + c0 + c) * N + n) : 0.f;
-            }
-            h[c][j] = pk2(v[0], v[1]);
-        }
+    for (int j = 0; j < kSsmSt; ++j) {
+        h[j][0] = pk2(v[0][j], v[1][j]);
+        h[j][1] = pk2(v[2][j], v[3][j]);
+    }
 }
-__device__ __forceinline__ void store_state(float* s, long long row, int c0, int n0, int D, int N,
-                                            const f2x (&h)[kSsmCh][4]) {
+__device__ __forceinline__ void store_state(float* s, bool quads, long long row, int c0, int n0, int D, int N, const SsmStates& h) {
+    float v[kSsmCh][kSsmSt];
 #pragma unroll
-    for (int c = 0; c < kSsmCh; ++c)
+    for (int j = 0; j < kSsmSt; ++j) {
+        up2(h[j][0], v[0][j], v[1][j]);
+        up2(h[j][1], v[2][j], v[3][j]);
+    }
+    float* p = s + (row * D + c0) * N + n0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float v[2];
-            up2(h[c][j], v[0], v[1]);
+    for (int i = 0; i < kSsmCh; ++i) {
+        if (quads) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int n = n0 + 2 * j + e;
-                if (c0 + c < D && n < N) s[(row * D + c0 + c) * N + n] = v[e];
-            }
+            for (int j = 0; j < kSsmSt; j += 4)
+                if (c0 + i < D && n0 + j < N)
+                    *reinterpret_cast<float4*>(p + i * N + j) = make_float4(v[i][j], v[i][j + 1], v[i][j + 2], v[i][j + 3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kSsmSt; ++j)
+                if (c0 + i < D && n0 + j < N) p[i * N + j] = v[i][j];
         }
+    }
 }
 // The same in the kernels' own layout: [kSsmVec][32 lanes] float4 for a warp.
-__device__ __forceinline__ void load_tile_state(const float4* p, int lane, f2x (&h)[kSsmCh][4]) {
+__device__ __forceinline__ void load_tile_state(const float4* p, int lane, SsmStates& h) {
 #pragma unroll
     for (int k = 0; k < kSsmVec; ++k) {
         const float4 v = __ldcg(p + k * 32 + lane);
-        h[k >> 1][2 * (k & 1)] = pk2(v.x, v.y);
-        h[k >> 1][2 * (k & 1) + 1] = pk2(v.z, v.w);
+        h[k][0] = pk2(v.x, v.y);
+        h[k][1] = pk2(v.z, v.w);
     }
 }
-__device__ __forceinline__ void store_tile_state(float4* p, int lane, const f2x (&h)[kSsmCh][4]) {
+__device__ __forceinline__ void store_tile_state(float4* p, int lane, const SsmStates& h) {
 #pragma unroll
     for (int k = 0; k < kSsmVec; ++k) {
         float4 v;
-        up2(h[k >> 1][2 * (k & 1)], v.x, v.y);
-        up2(h[k >> 1][2 * (k & 1) + 1], v.z, v.w);
+        up2(h[k][0], v.x, v.y);
+        up2(h[k][1], v.z, v.w);
         p[k * 32 + lane] = v;
     }
+}
+
+// a = e^(A dt)
+__device__ __forceinline__ f2x decay(f2x A, f2x dt) {
+    float e0, e1;
+    up2(mul2(A, dt), e0, e1);
+    return pk2(ex2_approx(e0), ex2_approx(e1));
 }
 
 // The sum of v[c] over the LN lanes that share a channel; lane ln of them ends
 // with the sums of the channels [ln 4 / LN, ...) in v[0 ..] (LN = 8: lanes 2 c and 2 c + 1 with channel c's).
 template <int LN>
-__device__ __forceinline__ void sum_states(float (&v)[kSsmCh], int lane) {
+__device__ __forceinline__ void sum_states(const f2x (&v2)[2], float (&v)[kSsmCh], int lane) {
+    up2(v2[0], v[0], v[1]);
+    up2(v2[1], v[2], v[3]);
     if (LN == 1) return;
     int keep = kSsmCh;
 #pragma unroll

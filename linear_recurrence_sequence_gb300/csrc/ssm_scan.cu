@@ -41,29 +41,42 @@ template <int LN, bool Y>
 struct FwdTile {
     static constexpr int T = LN == 1 ? 4 : 8;   // tokens
     using W = SsmWarp<LN>;
+    float bias[W::CW];
     float dt[T][W::CW];    // then the sums over the states
     float k[T][W::CW];
-    float b[T][W::NP];
-    float c[Y ? T : 1][Y ? W::NP : 4];
+    float b[T][2 * W::NP];
+    float c[Y ? T : 1][Y ? 2 * W::NP : 4];
     uint16_t x[2][T][W::CW], delta[2][T][W::CW];
     uint16_t gate[Y ? 2 : 1][Y ? T : 1][Y ? W::CW : 8];
     uint16_t rb[2][T][W::NP];
     uint16_t rc[Y ? 2 : 1][Y ? T : 1][Y ? W::NP : 8];
 };
 
-// Asks for the operands of nt tokens.
+// Where the next tile's operands begin.
+struct FwdRows {
+    const uint16_t *x, *delta, *gate, *b, *c;
+};
+__device__ __forceinline__ FwdRows rows_from(const SsmArgs& a, int b, int t0, int c0) {
+    return {row_at(a.x, b, t0, c0), row_at(a.delta, b, t0, c0), row_at(a.gate, b, t0, c0), row_at(a.b, b, t0, 0),
+            row_at(a.c, b, t0, 0)};
+}
+// Asks for the operands of nt tokens, and moves on.
 template <int LN, bool Y>
-__device__ __forceinline__ void ask_tile(const SsmArgs& a, int b, int c0, int t0, int nt, FwdTile<LN, Y>& s, int q, int lane) {
+__device__ __forceinline__ void ask_tile(const SsmArgs& a, FwdRows& r, int nt, int width, FwdTile<LN, Y>& s, int q, int lane) {
     constexpr int T = FwdTile<LN, Y>::T;
-    ask_rows<LN, T>(a.x.p, a.x.sb, a.x.st, b, t0, nt, c0, a.D, &s.x[q][0][0], lane);
-    ask_rows<LN, T>(a.delta.p, a.delta.sb, a.delta.st, b, t0, nt, c0, a.D, &s.delta[q][0][0], lane);
-    if (Y && a.gate.p != nullptr)
-        ask_rows<LN, T>(a.gate.p, a.gate.sb, a.gate.st, b, t0, nt, c0, a.D, &s.gate[Y ? q : 0][0][0], lane);
+    ask_rows<LN, T>(r.x, a.x.st, nt, width, &s.x[q][0][0], lane);
+    ask_rows<LN, T>(r.delta, a.delta.st, nt, width, &s.delta[q][0][0], lane);
+    if (Y && a.gate.p != nullptr) ask_rows<LN, T>(r.gate, a.gate.st, nt, width, &s.gate[Y ? q : 0][0][0], lane);
     if (a.words) {
-        ask_states<LN, T>(a.b, b, t0, nt, a.N, &s.rb[q][0][0], lane);
-        if (Y) ask_states<LN, T>(a.c, b, t0, nt, a.N, &s.rc[Y ? q : 0][0][0], lane);
+        ask_states<LN, T>(r.b, a.b.st, nt, a.N, &s.rb[q][0][0], lane);
+        if (Y) ask_states<LN, T>(r.c, a.c.st, nt, a.N, &s.rc[Y ? q : 0][0][0], lane);
     }
     copies_commit();
+    r.x += T * a.x.st;
+    r.delta += T * a.delta.st;
+    if (Y) r.gate += T * a.gate.st;
+    r.b += T * a.b.st;
+    if (Y) r.c += T * a.c.st;
 }
 
 // dt and dt x of nt tokens, b and c in FP32.
@@ -73,7 +86,7 @@ __device__ __forceinline__ void stage_tile(const SsmArgs& a, int b, int c0, int 
     constexpr int T = FwdTile<LN, Y>::T, IT = (T + W::RPI - 1) / W::RPI;
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     f2x bias[4];
-    load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, c0 + c8 < a.D, bias);
+    read_pairs(&s.bias[c8], bias);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int r = r0 + i * W::RPI;
@@ -84,42 +97,42 @@ __device__ __forceinline__ void stage_tile(const SsmArgs& a, int b, int c0, int 
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             d[e] = softplus2(add2(d[e], bias[e]));
-            if (r >= nt) d[e] = 0ull;   // a token past the end keeps the state and adds nothing
             x[e] = mul2(d[e], x[e]);
         }
         store_pairs(&s.dt[r][c8], d);
         store_pairs(&s.k[r][c8], x);
     }
-    stage_states<LN, T>(a.b, a.words, b, t0, nt, a.N, &s.rb[q][0][0], &s.b[0][0], lane);
-    if (Y) stage_states<LN, T>(a.c, a.words, b, t0, nt, a.N, &s.rc[Y ? q : 0][0][0], &s.c[0][0], lane);
+    if (nt < T) {   // a token past the end keeps the state and adds nothing
+        const f2x none[4] = {0ull, 0ull, 0ull, 0ull};
+        for (int r = r0; r < T; r += W::RPI)
+            if (r >= nt) {
+                store_pairs(&s.dt[r][c8], none);
+                store_pairs(&s.k[r][c8], none);
+            }
+    }
+    stage_states<LN, T>(row_at(a.b, b, t0, 0), a.b.st, a.words, nt, a.N, &s.rb[q][0][0], &s.b[0][0], lane);
+    if (Y) stage_states<LN, T>(row_at(a.c, b, t0, 0), a.c.st, a.words, nt, a.N, &s.rc[Y ? q : 0][0][0], &s.c[0][0], lane);
 }
 
 // One token: h <- e^(A dt) h + k b, and (Y) the sums of c h.
 template <int LN, bool Y>
-__device__ __forceinline__ void advance(const FwdTile<LN, Y>& s, int t, int lc, int ln, const f2x (&A)[kSsmCh][4],
-                                        f2x (&h)[kSsmCh][4], float (&y)[kSsmCh], float4& dt) {
-    dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
-    const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
-    const float ds[kSsmCh] = {dt.x, dt.y, dt.z, dt.w}, ks[kSsmCh] = {k.x, k.y, k.z, k.w};
-    f2x b[4], c[4];
-    read_states(&s.b[t][ln * kSsmSt], b);
-    if (Y) read_states(&s.c[t][ln * kSsmSt], c);
+__device__ __forceinline__ void advance(const FwdTile<LN, Y>& s, int t, int lc, int ln, const SsmStates& A, SsmStates& h,
+                                        f2x (&y)[2], f2x (&dt)[2]) {
+    f2x k[2];
+    read_channels(&s.dt[t][lc * kSsmCh], dt);
+    read_channels(&s.k[t][lc * kSsmCh], k);
 #pragma unroll
-    for (int i = 0; i < kSsmCh; ++i) {
-        const f2x d2 = dup2(ds[i]), k2 = dup2(ks[i]);
-        f2x acc = 0ull;
+    for (int j = 0; j < kSsmSt; j += 2) {
+        f2x b[2], c[2];
+        read_twice(&s.b[t][2 * (ln * kSsmSt + j)], b[0], b[1]);
+        if (Y) read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float e0, e1;
-            up2(mul2(A[i][j], d2), e0, e1);
-            h[i][j] = fma2(pk2(ex2_approx(e0), ex2_approx(e1)), h[i][j], mul2(k2, b[j]));
-            if (Y) acc = j ? fma2(h[i][j], c[j], acc) : mul2(h[i][j], c[j]);
-        }
-        if (Y) {
-            float lo, hi;
-            up2(acc, lo, hi);
-            y[i] = lo + hi;
-        }
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                h[j + e][i] = fma2(decay(A[j + e][i], dt[i]), h[j + e][i], mul2(k[i], b[e]));
+                if (Y) y[i] = j + e ? fma2(h[j + e][i], c[e], y[i]) : mul2(h[j + e][i], c[e]);
+            }
     }
 }
 
@@ -135,7 +148,7 @@ __device__ __forceinline__ SsmPlace place(const SsmArgs& a, int chunks) {
     const long long r = i / a.ngq;
     p.chunk = (int)(r % chunks);
     p.b = (int)(r / chunks);
-    p.warp = threadIdx.x >> 5;
+    p.warp = warp_of();
     p.group = gq * (blockDim.x >> 5) + p.warp;
     p.on = p.group < a.groups;
     return p;
@@ -146,54 +159,59 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(cons
     using W = SsmWarp<LN>;
     constexpr int T = FwdTile<LN, false>::T;
     extern __shared__ __align__(16) uint8_t buf[];
-    pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
     const SsmPlace p = place(a, a.nchunk - 1);
     if (!p.on) return;
     FwdTile<LN, false>& s = reinterpret_cast<FwdTile<LN, false>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
-    f2x A[kSsmCh][4], h[kSsmCh][4];
-    load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
-#pragma unroll
-    for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    SsmStates A, h;
+    load_rates(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
+    clear_states(h);
+    f2x sum[2] = {0ull, 0ull};
     bool cut = false;
     const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
-    ask_tile<LN, false>(a, p.b, c0, begin, min(T, end - begin), s, 0, lane);
+    stage_bias<LN>(a.delta_bias, c0, a.D, s.bias, lane);
+    FwdRows rows = rows_from(a, p.b, begin, c0);
+    ask_tile<LN, false>(a, rows, min(T, end - begin), a.D - c0, s, 0, lane);
     for (int t0 = begin, q = 0; t0 < end; t0 += T, q ^= 1) {
         const int nt = min(T, end - t0);
         const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
-        cut |= starts != 0u;
         copies_wait();
         __syncwarp();
         stage_tile<LN, false>(a, p.b, c0, t0, nt, s, q, lane);
         __syncwarp();
-        if (t0 + T < end) ask_tile<LN, false>(a, p.b, c0, t0 + T, min(T, end - t0 - T), s, q ^ 1, lane);
-#pragma unroll 2
-        for (int t = 0; t < T; ++t) {
-            if ((starts >> t) & 1u) {
+        if (t0 + T < end) ask_tile<LN, false>(a, rows, min(T, end - t0 - T), a.D - c0, s, q ^ 1, lane);
+        // (a test for starts in the loop would keep a token's loads from moving ahead of the one before it)
+        if (starts == 0u) {
 #pragma unroll
-                for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
+            for (int t = 0; t < T; ++t) {
+                f2x y[2], dt[2];
+                advance<LN, false>(s, t, lc, ln, A, h, y, dt);
+                sum[0] = add2(sum[0], dt[0]);
+                sum[1] = add2(sum[1], dt[1]);
             }
-            float y[kSsmCh];
-            float4 dt;
+            continue;
+        }
+        cut = true;   // what the state was before is of no matter, nor is the sum
+#pragma unroll 1
+        for (int t = 0; t < T; ++t) {
+            if ((starts >> t) & 1u) clear_states(h);
+            f2x y[2], dt[2];
             advance<LN, false>(s, t, lc, ln, A, h, y, dt);
-            sum.x += dt.x;
-            sum.y += dt.y;
-            sum.z += dt.z;
-            sum.w += dt.w;
         }
     }
+    // the next kernel's CTAs may come now: come at the start, they took the places of this one's on some SMs
+    // (4 x 4096 x 1024 forward + backward 608 us, so 543)
+    pdl_trigger();
     const long long slot = ((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group;
     store_tile_state(a.maps + slot * (kSsmVec * 32), lane, h);
     // an infinite sum: nothing is kept
-    if (cut) sum = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
-    if (ln == 0) *reinterpret_cast<float4*>(a.sums + slot * W::CW + lc * kSsmCh) = sum;
+    float4 o;
+    up2(sum[0], o.x, o.y);
+    up2(sum[1], o.z, o.w);
+    if (cut) o = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
+    if (ln == 0) *reinterpret_cast<float4*>(a.sums + slot * W::CW + lc * kSsmCh) = o;
 }
 
 // Entry states of the chunks, in place of their end states: one float4 of a
@@ -202,7 +220,6 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(cons
 template <int LN, bool REV>
 __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a) {
     using W = SsmWarp<LN>;
-    pdl_trigger();
     pdl_wait();
     const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
     const int lane = (int)(i & 31), k = (int)(i >> 5) & (kSsmVec - 1);
@@ -210,39 +227,37 @@ __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a) {
     const int g = (int)(bg % a.groups);
     const long long b = bg / a.groups;
     if (b >= a.B) return;
-    const int cw = lane / LN * kSsmCh + (k >> 1), c = g * W::CW + cw, n0 = lane % LN * kSsmSt + 4 * (k & 1);
+    const int cw = lane / LN * kSsmCh, c = g * W::CW + cw, n = lane % LN * kSsmSt + k;
     float A[4], h[4];
     const float* start = a.h0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const bool on = c < a.D && n0 + e < a.N;
-        A[e] = on ? ssm_rate(__ldg(a.a_log + (long long)c * a.N + n0 + e)) : 0.f;
-        h[e] = on && start != nullptr ? __ldg(start + (b * a.D + c) * a.N + n0 + e) : 0.f;
+        const bool on = c + e < a.D && n < a.N;
+        A[e] = on ? ssm_rate(__ldg(a.a_log + (long long)(c + e) * a.N + n)) : 0.f;
+        h[e] = on && start != nullptr ? __ldg(start + (b * a.D + c + e) * a.N + n) : 0.f;
     }
     // forward: chunk i's entry from chunk i - 1's; the last chunk has no map of its own
     const long long step = (REV ? -1 : 1) * (long long)a.groups;
     const long long first = (b * a.nchunk + (REV ? a.nchunk - 1 : 0)) * a.groups + g;
     float4* m = a.maps + first * (kSsmVec * 32) + k * 32 + lane;
-    const float* sums = a.sums + first * W::CW + cw;
+    const float4* sums = reinterpret_cast<const float4*>(a.sums + first * W::CW + cw);
     constexpr int AHEAD = 8;
     for (int q = 0; q < a.nchunk; q += AHEAD) {
-        float4 v[AHEAD];
-        float s[AHEAD];
+        float4 v[AHEAD], s[AHEAD];
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u)
             if (q + u < a.nchunk - 1) {
                 v[u] = __ldcg(m + (q + u) * step * (kSsmVec * 32));
-                s[u] = __ldcg(sums + (q + u) * step * W::CW);
+                s[u] = __ldcg(sums + (q + u) * step * (W::CW / 4));
             }
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             if (q + u >= a.nchunk) break;
             m[(q + u) * step * (kSsmVec * 32)] = make_float4(h[0], h[1], h[2], h[3]);
             if (q + u == a.nchunk - 1) break;
-            const float e[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
-            const bool cut = isinf(s[u]);
+            const float e[4] = {v[u].x, v[u].y, v[u].z, v[u].w}, d[4] = {s[u].x, s[u].y, s[u].z, s[u].w};
 #pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = cut ? e[j] : fmaf(ex2_approx(A[j] * s[u]), h[j], e[j]);
+            for (int j = 0; j < 4; ++j) h[j] = isinf(d[j]) ? e[j] : fmaf(ex2_approx(A[j] * d[j]), h[j], e[j]);
         }
     }
 }
@@ -252,26 +267,27 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
     using W = SsmWarp<LN>;
     constexpr int T = FwdTile<LN, true>::T, IT = (T + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
-    pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
     const SsmPlace p = place(a, a.nchunk);
     if (!p.on) return;
     FwdTile<LN, true>& s = reinterpret_cast<FwdTile<LN, true>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
-    f2x A[kSsmCh][4], h[kSsmCh][4];
-    load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
+    SsmStates A, h;
+    load_rates(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
     if (a.nchunk > 1)
         load_tile_state(a.maps + (((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group) * (kSsmVec * 32), lane, h);
     else
-        load_state(a.h0, p.b, ch, ln * kSsmSt, a.D, a.N, h);
+        load_state(a.h0, a.quads, p.b, ch, ln * kSsmSt, a.D, a.N, h);
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     const bool on = c0 + c8 < a.D;
     f2x skip[4];
     load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, on, skip);
     const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
     const int slots = (a.L + kSsmKeep - 1) / kSsmKeep;
-    ask_tile<LN, true>(a, p.b, c0, begin, min(T, end - begin), s, 0, lane);
+    stage_bias<LN>(a.delta_bias, c0, a.D, s.bias, lane);
+    FwdRows rows = rows_from(a, p.b, begin, c0);
+    ask_tile<LN, true>(a, rows, min(T, end - begin), a.D - c0, s, 0, lane);
     for (int t0 = begin, q = 0; t0 < end; t0 += T, q ^= 1) {
         const int nt = min(T, end - t0);
         const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
@@ -279,23 +295,29 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
         __syncwarp();
         stage_tile<LN, true>(a, p.b, c0, t0, nt, s, q, lane);
         __syncwarp();
-        if (t0 + T < end) ask_tile<LN, true>(a, p.b, c0, t0 + T, min(T, end - t0 - T), s, q ^ 1, lane);
+        if (t0 + T < end) ask_tile<LN, true>(a, rows, min(T, end - t0 - T), a.D - c0, s, q ^ 1, lane);
         if (KEEP && t0 % kSsmKeep == 0)
             store_tile_state(a.keep + (((long long)p.b * slots + t0 / kSsmKeep) * a.groups + p.group) * (kSsmVec * 32), lane, h);
-#pragma unroll 2
-        for (int t = 0; t < T; ++t) {
-            if ((starts >> t) & 1u) {
+        // A token's sums take the place of its dt: every lane of a channel has read that before it takes part in the sum.
+        if (starts == 0u) {
 #pragma unroll
-                for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
+            for (int t = 0; t < T; ++t) {
+                f2x y2[2], dt[2];
+                float y[kSsmCh];
+                advance<LN, true>(s, t, lc, ln, A, h, y2, dt);
+                sum_states<LN>(y2, y, lane);
+                put_channels<LN>(s.dt[t], y, lc, ln);
             }
-            float y[kSsmCh];
-            float4 dt;
-            advance<LN, true>(s, t, lc, ln, A, h, y, dt);
-            sum_states<LN>(y, lane);
-            __syncwarp();   // every lane has read the token's dt
-            put_channels<LN>(s.dt[t], y, lc, ln);
+        } else {
+#pragma unroll 1
+            for (int t = 0; t < T; ++t) {
+                if ((starts >> t) & 1u) clear_states(h);
+                f2x y2[2], dt[2];
+                float y[kSsmCh];
+                advance<LN, true>(s, t, lc, ln, A, h, y2, dt);
+                sum_states<LN>(y2, y, lane);
+                put_channels<LN>(s.dt[t], y, lc, ln);
+            }
         }
         __syncwarp();
         if (on) {
@@ -325,7 +347,8 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
             }
         }
     }
-    if (p.chunk == a.nchunk - 1) store_state(a.hT, p.b, ch, ln * kSsmSt, a.D, a.N, h);
+    pdl_trigger();   // not before: see ssm_maps_kernel
+    if (p.chunk == a.nchunk - 1) store_state(a.hT, a.quads, p.b, ch, ln * kSsmSt, a.D, a.N, h);
 }
 
 // One token of each of B sequences: LQ lanes share a channel, four states each

@@ -59,7 +59,7 @@ __device__ __forceinline__ BwdPlace bwd_place(const SsmArgs& a, int chunks, int 
     const long long r = i / a.ngq;
     p.chunk = first + (int)(r % chunks);
     p.b = (int)(r / chunks);
-    p.warp = threadIdx.x >> 5;
+    p.warp = warp_of();
     p.group = gq * (blockDim.x >> 5) + p.warp;
     p.on = p.group < a.groups;
     return p;
@@ -69,21 +69,60 @@ template <int LN>
 struct RevTile {
     static constexpr int T = LN == 1 ? 4 : 8;
     using W = SsmWarp<LN>;
+    float bias[W::CW];
     float dt[T][W::CW];
     float dy[T][W::CW];
-    float c[T][W::NP];
+    float c[T][2 * W::NP];
     uint16_t delta[2][T][W::CW], y[2][T][W::CW], gate[2][T][W::CW], rc[2][T][W::NP];
 };
 
-template <int LN>
-__device__ __forceinline__ void ask_reverse(const SsmBwdArgs& g, int b, int c0, int t0, int nt, RevTile<LN>& s, int q, int lane) {
-    constexpr int T = RevTile<LN>::T;
+// Where the next tile's operands begin.
+struct RevRows {
+    const uint16_t *x, *delta, *gate, *dy, *b, *c;
+};
+__device__ __forceinline__ RevRows rows_from(const SsmBwdArgs& g, int b, int t0, int c0) {
     const SsmArgs& a = g.f;
-    ask_rows<LN, T>(a.delta.p, a.delta.sb, a.delta.st, b, t0, nt, c0, a.D, &s.delta[q][0][0], lane);
-    ask_rows<LN, T>(g.dy, (long long)a.L * a.D, a.D, b, t0, nt, c0, a.D, &s.y[q][0][0], lane);
-    if (a.gate.p != nullptr) ask_rows<LN, T>(a.gate.p, a.gate.sb, a.gate.st, b, t0, nt, c0, a.D, &s.gate[q][0][0], lane);
-    if (a.words) ask_states<LN, T>(a.c, b, t0, nt, a.N, &s.rc[q][0][0], lane);
+    return {row_at(a.x, b, t0, c0),  row_at(a.delta, b, t0, c0), row_at(a.gate, b, t0, c0),
+            g.dy + ((long long)b * a.L + t0) * a.D + c0, row_at(a.b, b, t0, 0), row_at(a.c, b, t0, 0)};
+}
+// T tokens back.
+template <int T>
+__device__ __forceinline__ void move_back(const SsmArgs& a, RevRows& r) {
+    r.x -= T * a.x.st;
+    r.delta -= T * a.delta.st;
+    r.gate -= T * a.gate.st;
+    r.dy -= T * (long long)a.D;
+    r.b -= T * a.b.st;
+    r.c -= T * a.c.st;
+}
+
+template <int LN>
+__device__ __forceinline__ void ask_reverse(const SsmArgs& a, RevRows& r, int nt, int width, RevTile<LN>& s, int q, int lane) {
+    constexpr int T = RevTile<LN>::T;
+    ask_rows<LN, T>(r.delta, a.delta.st, nt, width, &s.delta[q][0][0], lane);
+    ask_rows<LN, T>(r.dy, a.D, nt, width, &s.y[q][0][0], lane);
+    if (a.gate.p != nullptr) ask_rows<LN, T>(r.gate, a.gate.st, nt, width, &s.gate[q][0][0], lane);
+    if (a.words) ask_states<LN, T>(r.c, a.c.st, nt, a.N, &s.rc[q][0][0], lane);
     copies_commit();
+    move_back<T>(a, r);
+}
+
+// One token: u <- e^(A dt) (dy' c + u).
+template <int LN>
+__device__ __forceinline__ void retreat(const RevTile<LN>& s, int t, int lc, int ln, const SsmStates& A, SsmStates& u,
+                                        f2x (&dt)[2]) {
+    f2x dy[2];
+    read_channels(&s.dt[t][lc * kSsmCh], dt);
+    read_channels(&s.dy[t][lc * kSsmCh], dy);
+#pragma unroll
+    for (int j = 0; j < kSsmSt; j += 2) {
+        f2x c[2];
+        read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) u[j + e][i] = mul2(decay(A[j + e][i], dt[i]), fma2(dy[i], c[e], u[j + e][i]));
+    }
 }
 
 template <int LN>
@@ -91,7 +130,6 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
     using W = SsmWarp<LN>;
     constexpr int T = RevTile<LN>::T, IT = (T + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
-    pdl_trigger();
     pdl_wait();
     const SsmArgs& a = g.f;
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
@@ -100,25 +138,23 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
     RevTile<LN>& s = reinterpret_cast<RevTile<LN>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
-    f2x A[kSsmCh][4], u[kSsmCh][4];
-    load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
-#pragma unroll
-    for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[i][j] = 0ull;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    SsmStates A, u;
+    load_rates(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
+    clear_states(u);
+    f2x sum[2] = {0ull, 0ull};
     bool cut = false;
     const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
     const int last = begin + (end - 1 - begin) / T * T;
-    ask_reverse<LN>(g, p.b, c0, last, end - last, s, 0, lane);
+    stage_bias<LN>(a.delta_bias, c0, a.D, s.bias, lane);
+    RevRows rows = rows_from(g, p.b, last, c0);
+    ask_reverse<LN>(a, rows, end - last, a.D - c0, s, 0, lane);
     for (int t0 = last, q = 0; t0 >= begin; t0 -= T, q ^= 1) {
         const int nt = min(T, end - t0);
         const uint32_t starts = start_bits(a.reset, (long long)p.b * a.L + t0, nt, lane);
-        cut |= starts != 0u;
         copies_wait();
         __syncwarp();
         f2x bias[4];
-        load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, c0 + c8 < a.D, bias);
+        read_pairs(&s.bias[c8], bias);
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int r = r0 + i * W::RPI;
@@ -128,49 +164,44 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
             gated(*reinterpret_cast<const uint4*>(&s.y[q][r][c8]), *reinterpret_cast<const uint4*>(&s.gate[q][r][c8]),
                   a.gate.p != nullptr, dy);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                d[e] = softplus2(add2(d[e], bias[e]));
-                if (r >= nt) d[e] = 0ull;
-            }
+            for (int e = 0; e < 4; ++e) d[e] = softplus2(add2(d[e], bias[e]));
             store_pairs(&s.dt[r][c8], d);
             store_pairs(&s.dy[r][c8], dy);
         }
-        stage_states<LN, T>(a.c, a.words, p.b, t0, nt, a.N, &s.rc[q][0][0], &s.c[0][0], lane);
+        if (nt < T) {   // dy of a token past the end is zero
+            const f2x none[4] = {0ull, 0ull, 0ull, 0ull};
+            for (int r = r0; r < T; r += W::RPI)
+                if (r >= nt) store_pairs(&s.dt[r][c8], none);
+        }
+        stage_states<LN, T>(row_at(a.c, p.b, t0, 0), a.c.st, a.words, nt, a.N, &s.rc[q][0][0], &s.c[0][0], lane);
         __syncwarp();
-        if (t0 > begin) ask_reverse<LN>(g, p.b, c0, t0 - T, T, s, q ^ 1, lane);
-#pragma unroll 2
+        if (t0 > begin) ask_reverse<LN>(a, rows, T, a.D - c0, s, q ^ 1, lane);
+        if (starts == 0u) {
+#pragma unroll
+            for (int t = T - 1; t >= 0; --t) {
+                f2x dt[2];
+                retreat<LN>(s, t, lc, ln, A, u, dt);
+                sum[0] = add2(sum[0], dt[0]);
+                sum[1] = add2(sum[1], dt[1]);
+            }
+            continue;
+        }
+        cut = true;
+#pragma unroll 1
         for (int t = T - 1; t >= 0; --t) {
-            const float4 dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
-            const float4 dy = *reinterpret_cast<const float4*>(&s.dy[t][lc * kSsmCh]);
-            const float ds[kSsmCh] = {dt.x, dt.y, dt.z, dt.w}, ys[kSsmCh] = {dy.x, dy.y, dy.z, dy.w};
-            f2x c[4];
-            read_states(&s.c[t][ln * kSsmSt], c);
-#pragma unroll
-            for (int i = 0; i < kSsmCh; ++i) {
-                const f2x d2 = dup2(ds[i]), y2 = dup2(ys[i]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float e0, e1;
-                    up2(mul2(A[i][j], d2), e0, e1);
-                    u[i][j] = mul2(pk2(ex2_approx(e0), ex2_approx(e1)), fma2(y2, c[j], u[i][j]));
-                }
-            }
-            if ((starts >> t) & 1u) {
-#pragma unroll
-                for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) u[i][j] = 0ull;
-            }
-            sum.x += dt.x;
-            sum.y += dt.y;
-            sum.z += dt.z;
-            sum.w += dt.w;
+            f2x dt[2];
+            retreat<LN>(s, t, lc, ln, A, u, dt);
+            if ((starts >> t) & 1u) clear_states(u);
         }
     }
+    pdl_trigger();
     const long long slot = ((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group;
     store_tile_state(a.maps + slot * (kSsmVec * 32), lane, u);
-    if (cut) sum = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
-    if (ln == 0) *reinterpret_cast<float4*>(a.sums + slot * W::CW + lc * kSsmCh) = sum;
+    float4 o;
+    up2(sum[0], o.x, o.y);
+    up2(sum[1], o.z, o.w);
+    if (cut) o = make_float4(INFINITY, INFINITY, INFINITY, INFINITY);
+    if (ln == 0) *reinterpret_cast<float4*>(a.sums + slot * W::CW + lc * kSsmCh) = o;
 }
 
 constexpr int kBT = kSsmKeep;   // tokens of a tile of the main kernel
@@ -184,37 +215,35 @@ struct BwdTile {
     float k[kBT][W::CW];              // dt x, then sum G b
     float dy[kBT][W::CW];             // dy'
     float y[kBT][W::CW];              // sums c h, then sum A r
-    float b[kBT][W::NP];
-    float c[kBT][W::NP];
+    float b[kBT][2 * W::NP];
+    float c[kBT][2 * W::NP];
     float red[kBT][2 * W::NP];        // db, dc of the warp's channels
+    float bias[W::CW], skip[W::CW];
     uint16_t x[2][kBT][W::CW], delta[2][kBT][W::CW], dys[2][kBT][W::CW], gate[2][kBT][W::CW];
     uint16_t rb[2][kBT][W::NP], rc[2][kBT][W::NP];
 };
 
 template <int LN, bool GATE>
-__device__ __forceinline__ void ask_back(const SsmBwdArgs& g, const float4* kept, int b, int c0, int t0, int nt,
-                                         BwdTile<LN>& s, int q, int lane) {
-    const SsmArgs& a = g.f;
+__device__ __forceinline__ void ask_back(const SsmArgs& a, const float4* kept, RevRows& r, int nt, int width, BwdTile<LN>& s, int q,
+                                         int lane) {
 #pragma unroll
     for (int k = 0; k < kSsmVec; ++k) copy16(&s.kept[k][lane], kept + k * 32 + lane, true);
-    ask_rows<LN, kBT>(a.x.p, a.x.sb, a.x.st, b, t0, nt, c0, a.D, &s.x[q][0][0], lane);
-    ask_rows<LN, kBT>(a.delta.p, a.delta.sb, a.delta.st, b, t0, nt, c0, a.D, &s.delta[q][0][0], lane);
-    ask_rows<LN, kBT>(g.dy, (long long)a.L * a.D, a.D, b, t0, nt, c0, a.D, &s.dys[q][0][0], lane);
-    if (GATE) ask_rows<LN, kBT>(a.gate.p, a.gate.sb, a.gate.st, b, t0, nt, c0, a.D, &s.gate[q][0][0], lane);
+    ask_rows<LN, kBT>(r.x, a.x.st, nt, width, &s.x[q][0][0], lane);
+    ask_rows<LN, kBT>(r.delta, a.delta.st, nt, width, &s.delta[q][0][0], lane);
+    ask_rows<LN, kBT>(r.dy, a.D, nt, width, &s.dys[q][0][0], lane);
+    if (GATE) ask_rows<LN, kBT>(r.gate, a.gate.st, nt, width, &s.gate[q][0][0], lane);
     if (a.words) {
-        ask_states<LN, kBT>(a.b, b, t0, nt, a.N, &s.rb[q][0][0], lane);
-        ask_states<LN, kBT>(a.c, b, t0, nt, a.N, &s.rc[q][0][0], lane);
+        ask_states<LN, kBT>(r.b, a.b.st, nt, a.N, &s.rb[q][0][0], lane);
+        ask_states<LN, kBT>(r.c, a.c.st, nt, a.N, &s.rc[q][0][0], lane);
     }
     copies_commit();
+    move_back<kBT>(a, r);
 }
 
-// Sums of v[0 .. 7] (four pairs) over the lanes that hold the same states; the
-// lanes write theirs to out[8].
+// Sums of v[0 .. 7] over the lanes that hold the same states; the lanes write
+// theirs to out[8].
 template <int LN>
-__device__ __forceinline__ void sum_channels(const f2x (&v2)[4], float* out, int lane) {
-    float v[8];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) up2(v2[j], v[2 * j], v[2 * j + 1]);
+__device__ __forceinline__ void sum_channels(float (&v)[kSsmSt], float* out, int lane) {
     int keep = 8;
 #pragma unroll
     for (int m = 16; m >= LN; m >>= 1) {
@@ -237,80 +266,101 @@ __device__ __forceinline__ void sum_channels(const f2x (&v2)[4], float* out, int
     }
 }
 
-// a = e^(A dt)
-__device__ __forceinline__ f2x decay(f2x A, f2x dt) {
-    float e0, e1;
-    up2(mul2(A, dt), e0, e1);
-    return pk2(ex2_approx(e0), ex2_approx(e1));
-}
-
-// A lane's states to and from 32 columns of tensor memory.
-__device__ __forceinline__ void states_to_tmem(uint32_t at, const f2x (&h)[kSsmCh][4]) {
+// A lane's states into 32 columns of tensor memory.
+__device__ __forceinline__ void states_to_tmem(uint32_t at, const SsmStates& h) {
     uint32_t r[32];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         float lo, hi;
-        up2(h[i / 4][i % 4], lo, hi);
+        up2(h[i / 2][i % 2], lo, hi);
         r[2 * i] = __float_as_uint(lo);
         r[2 * i + 1] = __float_as_uint(hi);
     }
     tmem_st32(at, r);
 }
+__device__ __forceinline__ float both_of(f2x v) {
+    float lo, hi;
+    up2(v, lo, hi);
+    return lo + hi;
+}
+
+// One token's state, the one before it left at `at`; dc, and (GATE) the sums c h.
+template <int LN, bool GATE>
+__device__ __forceinline__ void forth(BwdTile<LN>& s, int t, uint32_t at, int lane, const SsmStates& A, SsmStates& h) {
+    const int ln = lane % LN, lc = lane / LN;
+    states_to_tmem(at, h);
+    f2x dt[2], k[2], dy[2], y2[2];
+    read_channels(&s.dt[t][lc * kSsmCh], dt);
+    read_channels(&s.k[t][lc * kSsmCh], k);
+    read_channels(&s.dy[t][lc * kSsmCh], dy);
+    float dc[kSsmSt], y[kSsmCh];
+#pragma unroll
+    for (int j = 0; j < kSsmSt; j += 2) {
+        f2x b[2], c[2];
+        read_twice(&s.b[t][2 * (ln * kSsmSt + j)], b[0], b[1]);
+        if (GATE) read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            f2x d = 0ull;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                h[j + e][i] = fma2(decay(A[j + e][i], dt[i]), h[j + e][i], mul2(k[i], b[e]));
+                d = i ? fma2(dy[i], h[j + e][i], d) : mul2(dy[i], h[j + e][i]);
+                if (GATE) y2[i] = j + e ? fma2(h[j + e][i], c[e], y2[i]) : mul2(h[j + e][i], c[e]);
+            }
+            dc[j + e] = both_of(d);
+        }
+    }
+    if (GATE) {
+        sum_states<LN>(y2, y, lane);
+        put_channels<LN>(s.y[t], y, lc, ln);
+    }
+    sum_channels<LN>(dc, &s.red[t][SsmWarp<LN>::NP + ln * kSsmSt], lane);
+}
 
 // One token's adjoint; `at`: where the state before it waits.
 template <int LN>
-__device__ __forceinline__ void back(BwdTile<LN>& s, int t, bool start, uint32_t at, int lane, const f2x (&A)[kSsmCh][4],
-                                     f2x (&u)[kSsmCh][4], f2x (&dA)[kSsmCh][4]) {
+__device__ __forceinline__ void back(BwdTile<LN>& s, int t, uint32_t at, int lane, const SsmStates& A, SsmStates& u,
+                                     SsmStates& dA) {
     const int ln = lane % LN, lc = lane / LN;
     uint32_t hp[32];
     tmem_ld32(at, hp);
-    const float4 dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
-    const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
-    const float4 dy = *reinterpret_cast<const float4*>(&s.dy[t][lc * kSsmCh]);
-    const float ds[4] = {dt.x, dt.y, dt.z, dt.w}, ks[4] = {k.x, k.y, k.z, k.w}, ys[4] = {dy.x, dy.y, dy.z, dy.w};
-    f2x b[4], c[4], db[4];
-    read_states(&s.b[t][ln * kSsmSt], b);
-    read_states(&s.c[t][ln * kSsmSt], c);
-    float s1[kSsmCh], s2[kSsmCh];
+    f2x dt[2], k[2], dy[2], p1[2], p2[2];
+    read_channels(&s.dt[t][lc * kSsmCh], dt);
+    read_channels(&s.k[t][lc * kSsmCh], k);
+    read_channels(&s.dy[t][lc * kSsmCh], dy);
+    float db[kSsmSt], s1[kSsmCh], s2[kSsmCh];
 #pragma unroll
-    for (int i = 0; i < kSsmCh; ++i) {
-        const f2x d2 = dup2(ds[i]), k2 = dup2(ks[i]), y2 = dup2(ys[i]);
-        f2x p = 0ull;
+    for (int j = 0; j < kSsmSt; j += 2) {
+        f2x b[2], c[2];
+        read_twice(&s.b[t][2 * (ln * kSsmSt + j)], b[0], b[1]);
+        read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f2x G = fma2(y2, c[j], u[i][j]);
-            p = j ? fma2(G, b[j], p) : mul2(G, b[j]);
-            db[j] = i ? fma2(k2, G, db[j]) : mul2(k2, G);
-            u[i][j] = mul2(decay(A[i][j], d2), G);
+        for (int e = 0; e < 2; ++e) {
+            f2x d = 0ull;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f2x G = fma2(dy[i], c[e], u[j + e][i]);
+                p1[i] = j + e ? fma2(G, b[e], p1[i]) : mul2(G, b[e]);
+                d = i ? fma2(k[i], G, d) : mul2(k[i], G);
+                u[j + e][i] = mul2(decay(A[j + e][i], dt[i]), G);
+            }
+            db[j + e] = both_of(d);
         }
-        float lo, hi;
-        up2(p, lo, hi);
-        s1[i] = lo + hi;
     }
     tmem_ld32_wait(hp);
 #pragma unroll
-    for (int i = 0; i < kSsmCh; ++i) {
-        const f2x d2 = dup2(ds[i]);
-        f2x p = 0ull;
+    for (int j = 0; j < kSsmSt; ++j)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f2x r = mul2(u[i][j], pk2(__uint_as_float(hp[8 * i + 2 * j]), __uint_as_float(hp[8 * i + 2 * j + 1])));
-            p = j ? fma2(A[i][j], r, p) : mul2(A[i][j], r);
-            dA[i][j] = fma2(d2, r, dA[i][j]);
+        for (int i = 0; i < 2; ++i) {
+            const int at_ = 4 * j + 2 * i;
+            const f2x r = mul2(u[j][i], pk2(__uint_as_float(hp[at_]), __uint_as_float(hp[at_ + 1])));
+            p2[i] = j ? fma2(A[j][i], r, p2[i]) : mul2(A[j][i], r);
+            dA[j][i] = fma2(dt[i], r, dA[j][i]);
         }
-        float lo, hi;
-        up2(p, lo, hi);
-        s2[i] = lo + hi;
-    }
-    if (start) {   // nothing goes past a start (the state before it waits as zeros)
-#pragma unroll
-        for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) u[i][j] = 0ull;
-    }
-    sum_states<LN>(s1, lane);
-    sum_states<LN>(s2, lane);
-    __syncwarp();   // every lane has read the token's dt x
+    sum_states<LN>(p1, s1, lane);
+    sum_states<LN>(p2, s2, lane);
+    // (every lane of a channel has read the token's dt x before it takes part in the sum)
     put_channels<LN>(s.k[t], s1, lc, ln);
     put_channels<LN>(s.y[t], s2, lc, ln);
     sum_channels<LN>(db, &s.red[t][ln * kSsmSt], lane);
@@ -329,12 +379,10 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     constexpr int IT = (kBT + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
     __shared__ uint32_t s_tmem;
-    // a dependent kernel may ask for tensor memory: not before every CTA of this one has its own
     if (threadIdx.x < 32) tmem_alloc(&s_tmem, kBwdTmem);
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    pdl_trigger();
     pdl_wait();
     const SsmArgs& a = g.f;
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
@@ -345,23 +393,23 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     const bool on = p.on && c0 + c8 < a.D;
-    f2x A[kSsmCh][4], u[kSsmCh][4], dA[kSsmCh][4];
-    load_rates<LN>(a.a_log, ch, ln * kSsmSt, a.D, a.N, A);
+    SsmStates A, u, dA;
+    load_rates(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
     const long long slot = ((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group;
     if (a.nchunk > 1 && p.on)
         load_tile_state(a.maps + slot * (kSsmVec * 32), lane, u);
     else
-        load_state(a.h0, p.b, ch, ln * kSsmSt, a.D, a.N, u);   // here h0 is the cotangent of the last state
-#pragma unroll
-    for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) dA[i][j] = 0ull;
+        load_state(a.h0, a.quads, p.b, ch, ln * kSsmSt, a.D, a.N, u);   // here h0 is the cotangent of the last state
+    clear_states(dA);
     f2x dskip[4] = {0ull, 0ull, 0ull, 0ull}, dbias[4] = {0ull, 0ull, 0ull, 0ull};
     const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
     const int last = begin + (end - 1 - begin) / kBT * kBT;
     const long long stride = (long long)a.groups * (kSsmVec * 32);   // of the kept states, a tile back
     const float4* kept = a.keep + ((long long)p.b * ((a.L + kBT - 1) / kBT) + last / kBT) * stride + (long long)p.group * (kSsmVec * 32);
-    if (p.on) ask_back<LN, GATE>(g, kept, p.b, c0, last, end - last, s, 0, lane);
+    stage_bias<LN>(a.delta_bias, c0, a.D, s.bias, lane);
+    stage_bias<LN>(a.d_skip, c0, a.D, s.skip, lane);
+    RevRows rows = rows_from(g, p.b, last, c0);
+    if (p.on) ask_back<LN, GATE>(a, kept, rows, end - last, a.D - c0, s, 0, lane);
     for (int t0 = last, q = 0; t0 >= begin; t0 -= kBT, q ^= 1, kept -= stride) {
         const int nt = min(kBT, end - t0);
         const long long row = (long long)p.b * a.L + t0;
@@ -371,7 +419,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
             copies_wait();
             __syncwarp();
             f2x bias[4];
-            load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
+            read_pairs(&s.bias[c8], bias);
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
                 const int r = r0 + i * W::RPI;
@@ -384,7 +432,6 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     d[e] = softplus2(add2(d[e], bias[e]));
-                    if (r >= nt) d[e] = 0ull;
                     dskip[e] = fma2(dy[e], x[e], dskip[e]);
                     x[e] = mul2(d[e], x[e]);
                 }
@@ -392,61 +439,39 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
                 store_pairs(&s.k[r][c8], x);
                 store_pairs(&s.dy[r][c8], dy);
             }
-            stage_states<LN, kBT>(a.b, a.words, p.b, t0, nt, a.N, &s.rb[q][0][0], &s.b[0][0], lane);
-            stage_states<LN, kBT>(a.c, a.words, p.b, t0, nt, a.N, &s.rc[q][0][0], &s.c[0][0], lane);
+            if (nt < kBT) {   // x and dy of a token past the end are zero
+                const f2x none[4] = {0ull, 0ull, 0ull, 0ull};
+                for (int r = r0; r < kBT; r += W::RPI)
+                    if (r >= nt) store_pairs(&s.dt[r][c8], none);
+            }
+            stage_states<LN, kBT>(row_at(a.b, p.b, t0, 0), a.b.st, a.words, nt, a.N, &s.rb[q][0][0], &s.b[0][0], lane);
+            stage_states<LN, kBT>(row_at(a.c, p.b, t0, 0), a.c.st, a.words, nt, a.N, &s.rc[q][0][0], &s.c[0][0], lane);
         }
         // the other warps have taken the sums of the tile before
         __syncthreads();
         if (p.on) {
-            f2x h[kSsmCh][4];
+            SsmStates h;
 #pragma unroll
             for (int k = 0; k < kSsmVec; ++k) {
                 const float4 v = s.kept[k][lane];
-                h[k >> 1][2 * (k & 1)] = pk2(v.x, v.y);
-                h[k >> 1][2 * (k & 1) + 1] = pk2(v.z, v.w);
+                h[k][0] = pk2(v.x, v.y);
+                h[k][1] = pk2(v.z, v.w);
             }
+            if (starts == 0u) {
+#pragma unroll 2
+                for (int t = 0; t < kBT; ++t) forth<LN, GATE>(s, t, tmem + t * 32, lane, A, h);
+            } else {
 #pragma unroll 1
-            for (int t = 0; t < kBT; ++t) {
-                if ((starts >> t) & 1u) {
-#pragma unroll
-                    for (int i = 0; i < kSsmCh; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) h[i][j] = 0ull;
+                for (int t = 0; t < kBT; ++t) {
+                    if ((starts >> t) & 1u) clear_states(h);
+                    forth<LN, GATE>(s, t, tmem + t * 32, lane, A, h);
                 }
-                states_to_tmem(tmem + t * 32, h);
-                const float4 dt = *reinterpret_cast<const float4*>(&s.dt[t][lc * kSsmCh]);
-                const float4 k = *reinterpret_cast<const float4*>(&s.k[t][lc * kSsmCh]);
-                const float4 dy = *reinterpret_cast<const float4*>(&s.dy[t][lc * kSsmCh]);
-                const float ds[4] = {dt.x, dt.y, dt.z, dt.w}, ks[4] = {k.x, k.y, k.z, k.w}, ys[4] = {dy.x, dy.y, dy.z, dy.w};
-                f2x b[4], c[4], dc[4];
-                read_states(&s.b[t][ln * kSsmSt], b);
-                if (GATE) read_states(&s.c[t][ln * kSsmSt], c);
-                float y[kSsmCh];
-#pragma unroll
-                for (int i = 0; i < kSsmCh; ++i) {
-                    const f2x d2 = dup2(ds[i]), k2 = dup2(ks[i]), y2 = dup2(ys[i]);
-                    f2x acc = 0ull;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        h[i][j] = fma2(decay(A[i][j], d2), h[i][j], mul2(k2, b[j]));
-                        dc[j] = i ? fma2(y2, h[i][j], dc[j]) : mul2(y2, h[i][j]);
-                        if (GATE) acc = j ? fma2(h[i][j], c[j], acc) : mul2(h[i][j], c[j]);
-                    }
-                    float lo, hi;
-                    up2(acc, lo, hi);
-                    y[i] = lo + hi;
-                }
-                if (GATE) {
-                    sum_states<LN>(y, lane);
-                    put_channels<LN>(s.y[t], y, lc, ln);
-                }
-                sum_channels<LN>(dc, &s.red[t][W::NP + ln * kSsmSt], lane);
             }
             tmem_st_wait();
             __syncwarp();
-            if (t0 > begin) ask_back<LN, GATE>(g, kept - stride, p.b, c0, t0 - kBT, kBT, s, q ^ 1, lane);
+            if (t0 > begin) ask_back<LN, GATE>(a, kept - stride, rows, kBT, a.D - c0, s, q ^ 1, lane);
             f2x skip[4];
-            load_pairs(a.d_skip == nullptr ? nullptr : a.d_skip + c0 + c8, on, skip);
+            read_pairs(&s.skip[c8], skip);
             if (GATE) {
 #pragma unroll
                 for (int i = 0; i < IT; ++i) {
@@ -470,8 +495,17 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
                 }
                 __syncwarp();
             }
+            if (starts == 0u) {
+#pragma unroll 2
+                for (int t = kBT - 1; t >= 0; --t) back<LN>(s, t, tmem + t * 32, lane, A, u, dA);
+            } else {
 #pragma unroll 1
-            for (int t = kBT - 1; t >= 0; --t) back<LN>(s, t, (starts >> t) & 1u, tmem + t * 32, lane, A, u, dA);
+                for (int t = kBT - 1; t >= 0; --t) {
+                    back<LN>(s, t, tmem + t * 32, lane, A, u, dA);
+                    // nothing goes past a start (the state before it waits as zeros)
+                    if ((starts >> t) & 1u) clear_states(u);
+                }
+            }
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < IT; ++i) {
@@ -489,7 +523,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = fma2(s1[e], t[e], mul2(dup2(kLn2), v[e]));
                 unpack_pairs(*reinterpret_cast<const uint4*>(&s.delta[q][r][c8]), t);
-                load_pairs(a.delta_bias == nullptr ? nullptr : a.delta_bias + c0 + c8, on, bias);
+                read_pairs(&s.bias[c8], bias);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float w0, w1;
@@ -511,6 +545,8 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
             g.dbc[((row + t) * a.ngq + gq) * (2 * W::NP) + n] = v;
         }
     }
+    // late, as in ssm_maps_kernel (and a dependent kernel that asks for tensor memory finds every CTA of this one with its own)
+    pdl_trigger();
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
@@ -539,7 +575,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
             o[1] = make_float4(v[8 * w + 4], v[8 * w + 5], v[8 * w + 6], v[8 * w + 7]);
         }
     }
-    if (p.chunk == 0 && g.dh0 != nullptr) store_state(g.dh0, p.b, ch, ln * kSsmSt, a.D, a.N, u);
+    if (p.chunk == 0 && g.dh0 != nullptr) store_state(g.dh0, a.quads, p.b, ch, ln * kSsmSt, a.D, a.N, u);
 }
 
 // The parts of the parameters' gradients joined (the first `columns` CTAs: 32
@@ -547,8 +583,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
 template <int LN>
 __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdArgs g, int columns) {
     using W = SsmWarp<LN>;
-    pdl_trigger();
-    pdl_wait();
+    pdl_wait();   // no early trigger: the next call's CTAs would take these ones' places
     const SsmArgs& a = g.f;
     if ((int)blockIdx.x >= columns) {
         const long long n = (long long)a.B * a.L * 2 * W::NP;
@@ -599,12 +634,11 @@ __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdArgs g, int
     if (col < states) {
         const int sl = (int)(col & 31), k = (int)(col >> 5) & (kSsmVec - 1);
         const long long grp = col / (kSsmVec * 32);
-        const long long c = grp * W::CW + sl / LN * kSsmCh + (k >> 1);
-        const int n0 = sl % LN * kSsmSt + 4 * (k & 1);
+        const long long c = grp * W::CW + sl / LN * kSsmCh;
+        const int n = sl % LN * kSsmSt + k;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c < a.D && n0 + j < a.N)
-                g.da_log[c * a.N + n0 + j] = -expf(__ldg(a.a_log + c * a.N + n0 + j)) * e[j];
+            if (c + j < a.D && n < a.N) g.da_log[(c + j) * a.N + n] = -expf(__ldg(a.a_log + (c + j) * a.N + n)) * e[j];
         return;
     }
     const long long at = (col - states) * 4, width = (long long)a.groups * W::CW;

@@ -115,7 +115,7 @@ int lrs_selftest_wait_timeout(void* scratch, cudaStream_t stream);
  * forward maps, 29 its prefixes, 30 its replay, 31 its step, 32 its reverse maps,
  * 33 its backward, 34 its gradient sums, 35 the causal convolution, 36 its step,
  * 37 its backward, 38 its gradient sums, 39 the embedding lookup, 40 the sort of its
- * tokens, 41 its gradient; 9 also covers
+ * tokens, 41 its gradient's sums, 42 the rows joined from several; 9 also covers
  * the bias-gradient reductions) and duration in
  * milliseconds; *count receives the number of
  * kernels launched while profiling was on.  Not thread-safe: one profiling
@@ -774,7 +774,7 @@ int embedding_forward(const int64_t* tokens, const void* w, int w_dtype, int T, 
  *            is added to what dw holds, rows without a token are left as they are: a
  *            matrix that the head shares, or several batches)
  *   scratch  embedding_workspace_bytes() bytes
- * FP32 sums in a fixed order (the tokens', in runs of 32), rounded once.
+ * FP32 sums in a fixed order (the tokens', in runs of 16), rounded once.
  * Errors: as the forward, plus LRS_ERR_ARG for an unknown grad_dtype. */
 int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int D, float scale, void* dw, int grad_dtype,
                        int accumulate, void* scratch, cudaStream_t stream);

@@ -1234,7 +1234,8 @@ KERNEL_NAMES = {
     28: "ssm_maps_kernel", 29: "ssm_prefix_kernels", 30: "ssm_replay_kernel", 31: "ssm_step_kernel",
     32: "ssm_rmaps_kernel", 33: "ssm_bwd_kernel", 34: "ssm_finish_kernel", 35: "causal_conv_fwd_kernel",
     36: "causal_conv_step_kernel", 37: "causal_conv_bwd_kernel", 38: "causal_conv_sum_kernel",
-    39: "embedding_fwd_kernel", 40: "embedding_sort_kernel", 41: "embedding_sum_kernels",
+    39: "embedding_fwd_kernel", 40: "embedding_sort_kernel", 41: "embedding_sum_kernel",
+    42: "embedding_join_kernel",
 }
 
 

@@ -86,7 +86,7 @@ enum {
     KID_RGLRU_PROJ_PACK, KID_BLOCK_GEMM, KID_BLOCK_NORM, KID_BLOCK_CONV, KID_BLOCK_JOIN, KID_BLOCK_SUM, KID_CE_GEMM,
     KID_CE_ROWS, KID_GATED_NORM, KID_GATED_NORM_SUM, KID_ADAMW_NORM, KID_ADAMW_UPDATE, KID_SSM_MAPS, KID_SSM_PREFIX,
     KID_SSM_REPLAY, KID_SSM_STEP, KID_SSM_BWD_MAPS, KID_SSM_BWD, KID_SSM_FINISH, KID_CONV_FWD, KID_CONV_STEP,
-    KID_CONV_BWD, KID_CONV_SUM, KID_EMBED_FWD, KID_EMBED_SORT, KID_EMBED_SUM
+    KID_CONV_BWD, KID_CONV_SUM, KID_EMBED_FWD, KID_EMBED_SORT, KID_EMBED_SUM, KID_EMBED_JOIN
 };
 
 #define LRS_LAUNCH(id, stream, expr)            \
@@ -1498,8 +1498,8 @@ int check_conv_shape(int B, int L, int D, int W) {
     if (B < 1 || L < 1 || D < 1 || W < 1) return LRS_ERR_ARG;
     if (D % 8 != 0 || W < 2 || W > 4 || (long long)B * L > (1LL << 30) || (long long)B * L * D > (1LL << 40))
         return LRS_ERR_UNSUPPORTED;
-    // CTAs of the launches, one for 64 tokens and 128 channels at least
-    if ((long long)B * ((L + 63) / 64) * ((D + 127) / 128) > 0x7fffffffLL) return LRS_ERR_UNSUPPORTED;
+    // CTAs of the launches, one for 64 tokens and 64 channels at least
+    if ((long long)B * ((L + 63) / 64) * ((D + 63) / 64) > 0x7fffffffLL) return LRS_ERR_UNSUPPORTED;
     return LRS_OK;
 }
 
@@ -1779,13 +1779,12 @@ int check_embed_shape(int T, int V, int D) {
 }
 
 struct EmbedScratch {
-    size_t list, place, first, part, total;
+    size_t place, first, part, total;
 };
 EmbedScratch embed_scratch(int T, int V, int D) {
     EmbedScratch s;
     const long long owners = embed_owners(V), rows = (V + owners - 1) / owners;
-    s.list = 256;
-    s.place = s.list + up256((size_t)T * sizeof(int2));
+    s.place = 256;
     s.first = s.place + up256((size_t)T * sizeof(int2));
     s.part = s.first + up256((size_t)(owners * rows + 1) * sizeof(int));
     s.total = s.part + up256((size_t)2 * embed_chunks(T) * D * sizeof(float));
@@ -1835,14 +1834,13 @@ int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int 
     a.accumulate = accumulate != 0;
     a.status = at<uint32_t>(scratch, 0);
     a.owners = embed_owners(V);
-    a.list = at<int2>(scratch, l.list);
     a.place = at<int2>(scratch, l.place);
     a.count = at<int>(scratch, 64);
     a.first = at<int>(scratch, l.first);
     a.part = at<float>(scratch, l.part);
     LRS_LAUNCH(KID_EMBED_SORT, stream, launch_embedding_sort(a, stream, pdl_ok()));
     LRS_LAUNCH(KID_EMBED_SUM, stream, launch_embedding_sum(a, stream, pdl_ok()));
-    LRS_LAUNCH(KID_EMBED_SUM, stream, launch_embedding_join(a, stream, pdl_ok()));
+    LRS_LAUNCH(KID_EMBED_JOIN, stream, launch_embedding_join(a, stream, pdl_ok()));
     return LRS_OK;
 }
 

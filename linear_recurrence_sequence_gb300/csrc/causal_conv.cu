@@ -7,11 +7,15 @@
 //   y_t   = SiLU(pre_t), or pre_t
 //   dpre  = dy SiLU'(pre),  dx_t = sum_j w_j dpre_(t+j),  dw_j = sum_t dpre_t x_(t-j)
 //
-// Bound by bandwidth: 4 bytes a value forward, 6 backward.  A thread forms a run
-// of tokens of a few channels and asks for all the rows of its window before any
-// arithmetic; the warps of a CTA take neighbouring runs, whose overlapping rows
-// meet in L1.  The backward forms pre again (x is read anyway, pre is not kept).
+// Bound by bandwidth: 4 bytes a value forward, 6 backward.  A thread walks along
+// time through a run of tokens of 4 channels, the last W inputs in
+// registers, and asks for 8 rows at a time.  The backward
+// forms pre again (x is read anyway, pre is not kept) and keeps the sums of the
+// dx of the last W tokens.  Runs are 32 tokens long where that leaves 16 warps an SM
+// (W - 1 rows before a run, and backward W - 1 tokens after it, are gone through
+// twice), else 8.
 #include <algorithm>
+#include <type_traits>
 
 #include "ssm.cuh"
 
@@ -19,25 +23,91 @@ namespace lrs {
 
 namespace {
 
-constexpr int kConvFwdRun = 8;    // tokens of a thread, 8 channels
-constexpr int kConvBwdRun = 16;   // tokens of a thread, 4 channels
+constexpr int kConvStep = 8;      // rows that a thread asks for at a time
 constexpr int kConvWarps = 8;     // runs of a CTA
+constexpr int kConvPairs = 2;   // of channels, a thread
+constexpr int kConvSms = 152;
 
-// Whether tap j of the token at bit i of the window is inside its sequence: no
-// start among the bits i - j + 1 .. i.
-__device__ __forceinline__ bool tap_live(uint32_t starts, int i, int j) {
-    return ((starts >> (i - j + 1)) & ((1u << j) - 1u)) == 0u;
+// A run's tokens, by the batch and the length of a row.
+int conv_run(int B, int L, int D) {
+    const long long warps = (long long)B * ((L + 31) / 32) * ((D + 127) / 128);
+    return warps >= 16 * kConvSms ? 32 : kConvStep;
 }
-// The starts of tokens t .. t + n - 1 of a row (n <= 32) as bits; none outside it.
+
+// P pairs of channels of a row: BF16 words, FP32 pairs.
+template <int P>
+struct Words {
+    uint32_t w[P];
+};
+template <int P>
+__device__ __forceinline__ Words<P> no_words() {
+    Words<P> o;
+#pragma unroll
+    for (int e = 0; e < P; ++e) o.w[e] = 0u;
+    return o;
+}
+template <int P>
+__device__ __forceinline__ Words<P> load_words(const uint16_t* p) {
+    Words<P> o;
+    if (P == 2) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+        o.w[0] = q.x;
+        o.w[P - 1] = q.y;
+    } else {
+        o.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    }
+    return o;
+}
+template <int P>
+__device__ __forceinline__ void store_words(uint16_t* p, const Words<P>& o) {
+    if (P == 2)
+        *reinterpret_cast<uint2*>(p) = make_uint2(o.w[0], o.w[P - 1]);
+    else
+        *reinterpret_cast<uint32_t*>(p) = o.w[0];
+}
+template <int P>
+__device__ __forceinline__ void unpack_words(const Words<P>& q, f2x (&v)[P]) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = bf2x(q.w[e]);
+}
+template <int P>
+__device__ __forceinline__ void load_vector(const float* p, f2x (&v)[P]) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+        const float2 q = __ldg(reinterpret_cast<const float2*>(p) + e);
+        v[e] = pk2(q.x, q.y);
+    }
+}
+template <int P>
+__device__ __forceinline__ void clear(f2x (&v)[P]) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) v[e] = 0ull;
+}
+template <int P>
+__device__ __forceinline__ void add_product(f2x (&acc)[P], const f2x (&a)[P], const f2x (&b)[P]) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) acc[e] = fma2(a[e], b[e], acc[e]);
+}
+// A window moves on by a token: v[1 ..] <- v[0 ..].
+template <int P, int W>
+__device__ __forceinline__ void shift_in(f2x (&v)[W][P]) {
+#pragma unroll
+    for (int j = W - 1; j > 0; --j)
+#pragma unroll
+        for (int e = 0; e < P; ++e) v[j][e] = v[j - 1][e];
+}
+// The starts of tokens t .. t + n - 1 of a row as bits, the last token's lowest (the order in which a
+// history shifts them in); none outside the row.
 template <int n>
-__device__ __forceinline__ uint32_t window_starts(const uint8_t* reset, long long row, int t, int L) {
+__device__ __forceinline__ uint32_t starts_of(const uint8_t* reset, long long row, int t, int L) {
     uint32_t st = 0u;
     if (reset != nullptr)
 #pragma unroll
-        for (int i = 0; i < n; ++i)
-            if (t + i >= 0 && t + i < L && __ldg(reset + row + t + i) != 0) st |= 1u << i;
+        for (int i = 0; i < n; ++i) st = st << 1 | (t + i >= 0 && t + i < L && __ldg(reset + row + t + i) != 0 ? 1u : 0u);
     return st;
 }
+// Whether tap j is inside its sequence: no start at the last j tokens of the history.
+__device__ __forceinline__ bool tap_live(uint32_t history, int j) { return (history & ((1u << j) - 1u)) == 0u; }
 
 __device__ __forceinline__ f2x silu2(f2x v) {
     float a, b;
@@ -45,60 +115,91 @@ __device__ __forceinline__ f2x silu2(f2x v) {
     return mul2(v, pk2(ssm_sigmoid(a), ssm_sigmoid(b)));
 }
 
+struct ConvPlace {
+    int b, c, t0, end;   // batch row, first channel, the run's tokens
+    long long tile;      // of the CTA: its runs of one batch row
+    bool on;
+};
+// width: channels of a warp
+__device__ __forceinline__ ConvPlace conv_place(const ConvArgs& a, int run, int width) {
+    ConvPlace p;
+    const int spans = (a.D + width - 1) / width, tiles = (a.L + run * kConvWarps - 1) / (run * kConvWarps);
+    p.c = (int)(blockIdx.x % spans) * width + (threadIdx.x & 31) * (width / 32);
+    p.tile = blockIdx.x / spans;
+    p.b = (int)(p.tile / tiles);
+    p.t0 = ((int)(p.tile % tiles) * kConvWarps + (threadIdx.x >> 5)) * run;
+    p.end = min(a.L, p.t0 + run);
+    p.on = p.c < a.D && p.t0 < a.L;
+    return p;
+}
+// The input at token t of the row (before it: the carried ones).
+template <int W, int P>
+__device__ __forceinline__ Words<P> conv_input(const ConvArgs& a, int b, int c, int t) {
+    if (t >= 0) return load_words<P>(a.x.p + (long long)b * a.x.sb + (long long)t * a.x.st + c);
+    if (a.state != nullptr) return load_words<P>(a.state + ((long long)b * (W - 1) + W - 1 + t) * a.D + c);
+    return no_words<P>();
+}
+
+// bias + the taps that are live; v holds the last W inputs, the newest first.
+template <int W, int P, bool CUT>
+__device__ __forceinline__ void conv_sum(const f2x (&w)[W][P], const f2x (&bias)[P], const f2x (&v)[W][P], uint32_t history,
+                                         f2x (&acc)[P]) {
+#pragma unroll
+    for (int e = 0; e < P; ++e) acc[e] = bias[e];
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        if (CUT && !tap_live(history, j)) break;   // nor any earlier input
+        add_product(acc, w[j], v[j]);
+    }
+}
+
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps) causal_conv_fwd_kernel(const ConvArgs a) {
-    constexpr int R = kConvFwdRun, H = W - 1;
+__global__ void __launch_bounds__(32 * kConvWarps, 3) causal_conv_fwd_kernel(const ConvArgs a, int run) {
+    constexpr int H = W - 1, P = kConvPairs;
     pdl_trigger();
     pdl_wait();
-    const int spans = (a.D + 255) / 256, tiles = (a.L + R * kConvWarps - 1) / (R * kConvWarps);
-    const int c = (int)(blockIdx.x % spans) * 256 + (threadIdx.x & 31) * 8;
-    const long long bt = blockIdx.x / spans;
-    const int b = (int)(bt / tiles), t0 = ((int)(bt % tiles) * kConvWarps + (threadIdx.x >> 5)) * R;
-    if (c >= a.D || t0 >= a.L) return;
-    const uint16_t* px = a.x.p + (long long)b * a.x.sb + c;
-    uint4 rows[R + H];   // inputs t0 - H + i
+    const ConvPlace p = conv_place(a, run, 64 * P);
+    if (!p.on) return;
+    f2x w[W][P], bias[P], v[W][P];
+    clear(bias);
 #pragma unroll
-    for (int i = 0; i < R + H; ++i) {
-        const int t = t0 - H + i;
-        rows[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (t >= 0 && t < a.L)
-            rows[i] = __ldg(reinterpret_cast<const uint4*>(px + (long long)t * a.x.st));
-        else if (t < 0 && a.state != nullptr)
-            rows[i] = __ldg(reinterpret_cast<const uint4*>(a.state + ((long long)b * H + H + t) * a.D + c));
-    }
-    const uint32_t st = window_starts<R + H>(a.reset, (long long)b * a.L, t0 - H, a.L);
-    f2x w[W][4], bias[4];
+    for (int j = 0; j < W; ++j) load_vector(a.w + (long long)j * a.D + p.c, w[j]);
+    if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
-    for (int j = 0; j < W; ++j) load_pairs(a.w + (long long)j * a.D + c, true, w[j]);
-    load_pairs(a.bias == nullptr ? nullptr : a.bias + c, true, bias);
+    for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
+    const long long row = (long long)p.b * a.L;
+    uint32_t history = starts_of<H>(a.reset, row, p.t0 - H, a.L);
+    const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
+    uint16_t* py = a.y + (row + p.t0) * a.D + p.c;
+    for (int t = p.t0; t < p.end; t += kConvStep, px += kConvStep * a.x.st, py += (long long)kConvStep * a.D) {
+        const int n = p.end - t;
+        Words<P> q[kConvStep];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (t0 + r >= a.L) break;
-        f2x acc[4] = {bias[0], bias[1], bias[2], bias[3]};
+        for (int r = 0; r < kConvStep; ++r) q[r] = r < n ? load_words<P>(px + r * a.x.st) : no_words<P>();
+        history = (history & ((1u << H) - 1u)) << kConvStep | starts_of<kConvStep>(a.reset, row, t, a.L);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            if (j > 0 && !tap_live(st, r + H, j)) break;   // nor any earlier input
-            f2x v[4];
-            unpack_pairs(rows[r + H - j], v);
+        for (int r = 0; r < kConvStep; ++r) {
+            shift_in(v);
+            unpack_words(q[r], v[0]);
+            if (r >= n) continue;
+            f2x acc[P];
+            if (history == 0u)
+                conv_sum<W, P, false>(w, bias, v, 0u, acc);
+            else
+                conv_sum<W, P, true>(w, bias, v, history >> (kConvStep - 1 - r), acc);
+            Words<P> o;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = fma2(w[j][e], v[e], acc[e]);
+            for (int e = 0; e < P; ++e) o.w[e] = x2bf(SILU ? silu2(acc[e]) : acc[e]);
+            store_words(py + (long long)r * a.D, o);
         }
-        if (SILU)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[e] = silu2(acc[e]);
-        *reinterpret_cast<uint4*>(a.y + ((long long)b * a.L + t0 + r) * a.D + c) =
-            make_uint4(x2bf(acc[0]), x2bf(acc[1]), x2bf(acc[2]), x2bf(acc[3]));
     }
     // the row's last inputs, as far as they belong to its last sequence
-    if (a.state_out != nullptr && t0 + R >= a.L) {
+    if (a.state_out != nullptr && p.end == a.L) {
+        history = starts_of<H>(a.reset, row, a.L - H, a.L);
 #pragma unroll
-        for (int i = 0; i < R + H; ++i) {
-            const int k = t0 - H + i - (a.L - H);
-            if (k < 0 || k >= H) continue;
-            const bool live = i == R + H - 1 || (st >> (i + 1)) == 0u;
-            *reinterpret_cast<uint4*>(a.state_out + ((long long)b * H + k) * a.D + c) =
-                live ? rows[i] : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int k = 0; k < H; ++k)   // the input k tokens before the last
+            store_words(a.state_out + ((long long)p.b * H + H - 1 - k) * a.D + p.c,
+                        tap_live(history, k) ? conv_input<W, P>(a, p.b, p.c, a.L - 1 - k) : no_words<P>());
     }
 }
 
@@ -139,148 +240,138 @@ __global__ void __launch_bounds__(128) causal_conv_step_kernel(const ConvArgs a)
     for (int k = 0; k < H; ++k) *reinterpret_cast<uint4*>(a.state_out + (b * H + k) * a.D + c) = rows[k + 1];
 }
 
-__device__ __forceinline__ void unpack4(const uint2 q, f2x (&v)[2]) {
-    v[0] = bf2x(q.x);
-    v[1] = bf2x(q.y);
-}
-__device__ __forceinline__ void put4(void* p, long long at, bool f32, const f2x (&v)[2]) {
-    if (f32) {
-        float4 o;
-        up2(v[0], o.x, o.y);
-        up2(v[1], o.z, o.w);
-        *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = o;
-    } else {
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = make_uint2(x2bf(v[0]), x2bf(v[1]));
+template <int P>
+__device__ __forceinline__ void put_channels_of(void* p, long long at, bool f32, const f2x (&v)[P]) {
+    if (!f32) {
+        Words<P> o;
+#pragma unroll
+        for (int e = 0; e < P; ++e) o.w[e] = x2bf(v[e]);
+        store_words(static_cast<uint16_t*>(p) + at, o);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < P; ++e) {
+        float2 o;
+        up2(v[e], o.x, o.y);
+        reinterpret_cast<float2*>(static_cast<float*>(p) + at)[e] = o;
     }
 }
 
+// One token backward: d becomes dpre; dx[H - j] of the token j earlier, and the
+// weights' sums (in: the token is the run's own).
+template <int W, int P, bool SILU, bool CUT>
+__device__ __forceinline__ void conv_token_back(const f2x (&w)[W][P], const f2x (&bias)[P], const f2x (&v)[W][P], uint32_t history,
+                                                bool in, f2x (&d)[P], f2x (&dx)[W][P], f2x (&dw)[W][P], f2x (&db)[P]) {
+    if (SILU) {
+        f2x pre[P];
+        conv_sum<W, P, CUT>(w, bias, v, history, pre);
+#pragma unroll
+        for (int e = 0; e < P; ++e) {
+            float p0, p1;
+            up2(pre[e], p0, p1);
+            const f2x s = pk2(ssm_sigmoid(p0), ssm_sigmoid(p1)), one = dup2(1.f);
+            d[e] = mul2(d[e], mul2(s, fma2(pre[e], sub2(one, s), one)));
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        if (CUT && !tap_live(history, j)) break;
+        add_product(dx[W - 1 - j], w[j], d);
+        if (in) add_product(dw[j], d, v[j]);
+    }
+    if (in)
+#pragma unroll
+        for (int e = 0; e < P; ++e) db[e] = add2(db[e], d[e]);
+}
+
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps) causal_conv_bwd_kernel(const ConvBwdArgs g) {
-    constexpr int R = kConvBwdRun, H = W - 1;
-    __shared__ float4 acc[kConvWarps][W + 1][32];
+__global__ void __launch_bounds__(32 * kConvWarps, 2) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
+    constexpr int H = W - 1, P = kConvPairs;
+    __shared__ f2x acc[kConvWarps][W + 1][32][P];
     pdl_trigger();
     pdl_wait();
     const ConvArgs& a = g.f;
-    const int spans = (a.D + 127) / 128, tiles = (a.L + R * kConvWarps - 1) / (R * kConvWarps);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = (int)(blockIdx.x % spans) * 128 + lane * 4;
-    const long long bt = blockIdx.x / spans;
-    const int b = (int)(bt / tiles), t0 = ((int)(bt % tiles) * kConvWarps + warp) * R;
-    f2x dw[W][2], db[2] = {0ull, 0ull};
+    const ConvPlace p = conv_place(a, run, 64 * P);
+    f2x dw[W][P], db[P];
+    clear(db);
 #pragma unroll
-    for (int j = 0; j < W; ++j) dw[j][0] = dw[j][1] = 0ull;
-    if (c < a.D && t0 < a.L) {
-        const uint16_t* px = a.x.p + (long long)b * a.x.sb + c;
-        const uint16_t* py = g.dy + (long long)b * a.L * a.D + c;
-        uint2 rows[R + 2 * H], dys[R + H];   // x from t0 - H on, dy from t0 on
-#pragma unroll
-        for (int i = 0; i < R + 2 * H; ++i) {
-            const int t = t0 - H + i;
-            rows[i] = make_uint2(0u, 0u);
-            // past the run x only serves pre
-            if (t >= 0 && t < a.L && (SILU || i < R + H))
-                rows[i] = __ldg(reinterpret_cast<const uint2*>(px + (long long)t * a.x.st));
-            else if (t < 0 && a.state != nullptr)
-                rows[i] = __ldg(reinterpret_cast<const uint2*>(a.state + ((long long)b * H + H + t) * a.D + c));
-        }
-#pragma unroll
-        for (int i = 0; i < R + H; ++i)
-            dys[i] = t0 + i < a.L ? __ldg(reinterpret_cast<const uint2*>(py + (long long)(t0 + i) * a.D))
-                                  : make_uint2(0u, 0u);
-        const uint32_t st = window_starts<R + 2 * H>(a.reset, (long long)b * a.L, t0 - H, a.L);
-        f2x w[W][2], bias[2] = {0ull, 0ull};
+    for (int j = 0; j < W; ++j) clear(dw[j]);
+    if (p.on) {
+        f2x w[W][P], bias[P], v[W][P], dx[W][P];
+        clear(bias);
 #pragma unroll
         for (int j = 0; j < W; ++j) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(a.w + (long long)j * a.D + c));
-            w[j][0] = pk2(q.x, q.y);
-            w[j][1] = pk2(q.z, q.w);
+            load_vector(a.w + (long long)j * a.D + p.c, w[j]);
+            clear(v[j]);
+            clear(dx[j]);
         }
-        if (a.bias != nullptr) {
-            const float4 q = __ldg(reinterpret_cast<const float4*>(a.bias + c));
-            bias[0] = pk2(q.x, q.y);
-            bias[1] = pk2(q.z, q.w);
-        }
-        // dx of the tokens t0 + r - H .. t0 + r while r runs
-        f2x dx[W][2];
+        if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dx[j][0] = dx[j][1] = 0ull;
+        for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
+        const long long row = (long long)p.b * a.L;
+        uint32_t history = starts_of<H>(a.reset, row, p.t0 - H, a.L);
+        // the run's tokens, then the H after it, whose taps reach into it
+        const int stop = p.end + H;
+        const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
+        const uint16_t* py = g.dy + (row + p.t0) * a.D + p.c;
+        const long long odx = (long long)p.b * g.dx.sb + p.c;
+        for (int t = p.t0; t < stop; t += kConvStep, px += kConvStep * a.x.st, py += (long long)kConvStep * a.D) {
+            Words<P> q[kConvStep], qd[kConvStep];
+            const int n = min(a.L, stop) - t;   // tokens that there are (may be none)
 #pragma unroll
-        for (int r = 0; r < R + H; ++r) {
-            f2x d[2];
-            unpack4(dys[r], d);
-            if (SILU) {
-                f2x pre[2] = {bias[0], bias[1]};
-#pragma unroll
-                for (int j = 0; j < W; ++j) {
-                    if (j > 0 && !tap_live(st, r + H, j)) break;
-                    f2x v[2];
-                    unpack4(rows[r + H - j], v);
-                    pre[0] = fma2(w[j][0], v[0], pre[0]);
-                    pre[1] = fma2(w[j][1], v[1], pre[1]);
-                }
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float p0, p1;
-                    up2(pre[e], p0, p1);
-                    const f2x s = pk2(ssm_sigmoid(p0), ssm_sigmoid(p1)), one = dup2(1.f);
-                    d[e] = mul2(d[e], mul2(s, fma2(pre[e], sub2(one, s), one)));
-                }
-                if (t0 + r >= a.L) d[0] = d[1] = 0ull;
-            }
-            // tap j reaches token t0 + r - j, which is dx[H - j] of the window
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if (j > 0 && !tap_live(st, r + H, j)) break;
-                dx[H - j][0] = fma2(w[j][0], d[0], dx[H - j][0]);
-                dx[H - j][1] = fma2(w[j][1], d[1], dx[H - j][1]);
-                if (r < R) {
-                    f2x v[2];
-                    unpack4(rows[r + H - j], v);
-                    dw[j][0] = fma2(d[0], v[0], dw[j][0]);
-                    dw[j][1] = fma2(d[1], v[1], dw[j][1]);
+            for (int r = 0; r < kConvStep; ++r) {
+                q[r] = qd[r] = no_words<P>();
+                if (r < n) {
+                    q[r] = load_words<P>(px + r * a.x.st);
+                    qd[r] = load_words<P>(py + (long long)r * a.D);
                 }
             }
-            if (r < R) {
-                db[0] = add2(db[0], d[0]);
-                db[1] = add2(db[1], d[1]);
-            }
-            // the window's first token has all its taps: t0 + r - H.  Before the run it is another
-            // thread's, before the row an input carried in.
-            const int t = t0 + r - H;
-            if (r >= H) {
-                if (t < a.L) put4(g.dx.p, (long long)b * g.dx.sb + (long long)t * g.dx.st + c, g.f32, dx[0]);
-            } else if (t0 == 0 && g.dstate != nullptr) {
-                put4(g.dstate, ((long long)b * H + r) * a.D + c, g.f32, dx[0]);
-            }
+            history = (history & ((1u << H) - 1u)) << kConvStep | starts_of<kConvStep>(a.reset, row, t, a.L);
 #pragma unroll
-            for (int j = 0; j < H; ++j) {
-                dx[j][0] = dx[j + 1][0];
-                dx[j][1] = dx[j + 1][1];
+            for (int r = 0; r < kConvStep; ++r) {
+                if (t + r >= stop) break;
+                shift_in(v);
+                unpack_words(q[r], v[0]);
+                if (r < n) {
+                    f2x d[P];
+                    unpack_words(qd[r], d);
+                    const bool in = t + r < p.end;
+                    if (history == 0u)
+                        conv_token_back<W, P, SILU, false>(w, bias, v, 0u, in, d, dx, dw, db);
+                    else
+                        conv_token_back<W, P, SILU, true>(w, bias, v, history >> (kConvStep - 1 - r), in, d, dx, dw, db);
+                }
+                // dx[0] is whole now: the token H earlier.  Before the run it is another thread's, before the row an
+                // input carried in.
+                const int at = t + r - H;
+                if (at >= p.t0)
+                    put_channels_of(g.dx.p, odx + (long long)at * g.dx.st, g.f32, dx[0]);
+                else if (p.t0 == 0 && g.dstate != nullptr)
+                    put_channels_of(g.dstate, ((long long)p.b * H + H + at) * a.D + p.c, g.f32, dx[0]);
+#pragma unroll
+                for (int j = 0; j < H; ++j)
+#pragma unroll
+                    for (int e = 0; e < P; ++e) dx[j][e] = dx[j + 1][e];
+                clear(dx[H]);
             }
-            dx[H][0] = dx[H][1] = 0ull;
         }
     }
 #pragma unroll
-    for (int j = 0; j <= W; ++j) {
-        float4 o;
-        up2(j < W ? dw[j < W ? j : 0][0] : db[0], o.x, o.y);
-        up2(j < W ? dw[j < W ? j : 0][1] : db[1], o.z, o.w);
-        acc[warp][j][lane] = o;
-    }
+    for (int j = 0; j <= W; ++j)
+#pragma unroll
+        for (int e = 0; e < P; ++e) acc[warp][j][lane][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
     __syncthreads();
-    for (int i = threadIdx.x; i < (W + 1) * 32; i += 32 * kConvWarps) {
-        const int j = i / 32, l = i % 32, cc = (int)(blockIdx.x % spans) * 128 + l * 4;
-        if (cc >= a.D) continue;
-        float4 v = acc[0][j][l];
+    const int width = 64 * P, spans = (a.D + width - 1) / width;
+    for (int i = threadIdx.x; i < (W + 1) * 32 * P; i += 32 * kConvWarps) {
+        const int j = i / (32 * P), l = i % (32 * P), c = (int)(blockIdx.x % spans) * width + l * 2;
+        if (c >= a.D) continue;
+        f2x s = acc[0][j][l / P][l % P];
 #pragma unroll
-        for (int k = 1; k < kConvWarps; ++k) {
-            const float4 q = acc[k][j][l];
-            v.x += q.x;
-            v.y += q.y;
-            v.z += q.z;
-            v.w += q.w;
-        }
-        *reinterpret_cast<float4*>(g.part + (bt * (W + 1) + j) * a.D + cc) = v;
+        for (int k = 1; k < kConvWarps; ++k) s = add2(s, acc[k][j][l / P][l % P]);
+        float2 o;
+        up2(s, o.x, o.y);
+        *reinterpret_cast<float2*>(g.part + (p.tile * (W + 1) + j) * a.D + c) = o;
     }
 }
 
@@ -324,16 +415,16 @@ cudaError_t by_width(int W, int silu, F&& f) {
 }  // namespace
 
 int conv_bwd_parts(int B, int L, int D) {
-    const int tokens = kConvBwdRun * kConvWarps;
+    const int tokens = conv_run(B, L, D) * kConvWarps;
     return B * ((L + tokens - 1) / tokens);
 }
 
 cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl) {
-    const long long tiles = (a.L + kConvFwdRun * kConvWarps - 1) / (kConvFwdRun * kConvWarps);
-    const dim3 grid((unsigned)(a.B * tiles * ((a.D + 255) / 256)));
+    const int run = conv_run(a.B, a.L, a.D);
+    const dim3 grid((unsigned)((long long)conv_bwd_parts(a.B, a.L, a.D) * ((a.D + 64 * kConvPairs - 1) / (64 * kConvPairs))));
     return by_width(a.W, a.silu, [&](auto w, auto silu) {
         return launch_ex(causal_conv_fwd_kernel<decltype(w)::value, decltype(silu)::value>, grid, dim3(32 * kConvWarps), 0, s,
-                         pdl, a);
+                         pdl, a, run);
     });
 }
 cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl) {
@@ -343,10 +434,11 @@ cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl)
     });
 }
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& g, cudaStream_t s, bool pdl) {
-    const dim3 grid((unsigned)((long long)g.parts * ((g.f.D + 127) / 128)));
+    const dim3 grid((unsigned)((long long)g.parts * ((g.f.D + 64 * kConvPairs - 1) / (64 * kConvPairs))));
+    const int run = conv_run(g.f.B, g.f.L, g.f.D);
     return by_width(g.f.W, g.f.silu, [&](auto w, auto silu) {
         return launch_ex(causal_conv_bwd_kernel<decltype(w)::value, decltype(silu)::value>, grid, dim3(32 * kConvWarps), 0, s,
-                         pdl, g);
+                         pdl, g, run);
     });
 }
 cudaError_t launch_causal_conv_sum(const ConvBwdArgs& g, cudaStream_t s, bool pdl) {

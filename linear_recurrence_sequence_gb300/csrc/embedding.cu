@@ -9,11 +9,11 @@
 // that reach over chunks are joined from partial sums in their order.
 //   sort   `owners` CTAs, each with the vocabulary rows v = owner (mod owners):
 //          frequent tokens, which lie side by side in most vocabularies, go to
-//          different CTAs.  Each CTA looks through all the tokens (8 T bytes from
-//          L2: no histogram or prefix crosses CTAs, one launch), counts its rows'
-//          and all lower owners' tokens, and places its own in order.
-//   sum    a CTA a chunk of sorted places, threads across the row; other CTAs zero
-//          the rows without a token.
+//          different CTAs.  Each CTA looks through all the tokens twice (8 T bytes
+//          from L2: no histogram or prefix crosses CTAs, one launch), counts its
+//          rows' and all lower owners' tokens, and places its own in order.
+//   sum    a CTA a chunk of 16 sorted places and 1024 columns; other CTAs zero the
+//          rows without a token.
 //   join   rows that reach over a chunk's end.
 #include <algorithm>
 
@@ -62,148 +62,153 @@ __global__ void __launch_bounds__(256) embedding_fwd_kernel(const EmbedArgs a) {
     }
 }
 
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortRows = 4096;     // vocabulary rows of an owner, at most
-constexpr int kSortList = 8192;     // tokens of an owner that it places from shared memory
+constexpr int kSortWarps = 32;
+constexpr int kSortRows = 1024;     // vocabulary rows of an owner, at most
 constexpr int kOwners = 128;        // a power of two, as are the owners of larger vocabularies
-constexpr int kEmbedChunk = 32;     // sorted places of a CTA of the sum
+constexpr int kEmbedChunk = 16;     // sorted places of a CTA of the sum
+constexpr int kSumThreads = 128;    // of it, 8 columns each
+constexpr int kJoinParts = 4;       // of the joined row's chunks, summed side by side
 
-__global__ void __launch_bounds__(kSortThreads) embedding_sort_kernel(const EmbedBwdArgs a, int rows) {
-    extern __shared__ __align__(16) uint8_t buf[];
-    int2* held = reinterpret_cast<int2*>(buf);              // [kSortList]
-    int* hist = reinterpret_cast<int*>(held + kSortList);   // [rows]: counts, then the next free place of each row
-    __shared__ int mine[kSortWarps], lower[kSortWarps], bad;
+// Tokens t (even, counted from a 16-byte boundary) and t + 1; -1 outside the array.
+__device__ __forceinline__ longlong2 two_tokens(const EmbedBwdArgs& a, long long t) {
+    if (t >= 0 && t + 1 < a.T) return __ldg(reinterpret_cast<const longlong2*>(a.tokens + t));
+    return make_longlong2(t >= 0 ? __ldg(a.tokens + t) : -1, t + 1 < a.T ? __ldg(a.tokens + t + 1) : -1);
+}
+
+// A warp takes consecutive tokens, so that a stable sort needs no order between
+// threads: it counts its tokens of each row, a row's counts are added up over the
+// warps, and the warp places its tokens from there on.
+__global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const EmbedBwdArgs a, int rows) {
+    extern __shared__ __align__(16) int count[];   // [kSortWarps][rows], then each warp's next place in a row
+    __shared__ int lower[kSortWarps], sums[kSortWarps], bad;
     pdl_trigger();
     pdl_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, own = blockIdx.x, owners = a.owners, shift = 31 - __clz(owners);
-    for (int i = tid; i < rows; i += kSortThreads) hist[i] = 0;
+    for (int i = tid; i < kSortWarps * rows; i += kSortWarps * 32) count[i] = 0;
     if (tid == 0) bad = 0;
     __syncthreads();
-    // a warp's tokens are consecutive
-    const int per = ((a.T + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-    const long long begin = (long long)warp * per, end = min((long long)a.T, begin + per);
-    int n = 0, less = 0;
+    int* mine = count + warp * rows;
+    // tokens are read in pairs on 16-byte boundaries; `odd`: the first pair begins one before the array
+    const int odd = (int)(reinterpret_cast<uintptr_t>(a.tokens) >> 3 & 1u);
+    const long long all = (long long)a.T + odd, per = (all + kSortWarps * 64 - 1) / (kSortWarps * 64) * 64;
+    const long long begin = warp * per, end = min(all, begin + per);
+    int less = 0;
 #pragma unroll 4
-    for (long long t = begin + lane; t < end; t += 32) {
-        const long long v = __ldg(a.tokens + t);
-        if (v < 0) continue;
-        if (v >= a.V) {
-            bad = 1;
-            continue;
-        }
-        const int o = (int)v & (owners - 1);
-        less += o < own;
-        if (o == own) {
-            ++n;
-            atomicAdd(&hist[(int)v >> shift], 1);
-        }
-    }
-    n = __reduce_add_sync(0xffffffffu, n);
-    less = __reduce_add_sync(0xffffffffu, less);
-    if (lane == 0) {
-        mine[warp] = n;
-        lower[warp] = less;
-    }
-    __syncthreads();
-    int base = 0, before = 0, total = 0;   // places of lower owners, of this owner's earlier warps, of all its warps
-    for (int w = 0; w < kSortWarps; ++w) {
-        base += lower[w];
-        if (w < warp) before += mine[w];
-        total += mine[w];
-    }
-    // counts to first places, a run of rows a thread
-    {
-        __shared__ int sums[kSortWarps];
-        const int run = (rows + kSortThreads - 1) / kSortThreads, r0 = tid * run;
-        int s = 0;
-        for (int i = r0; i < min(rows, r0 + run); ++i) s += hist[i];
-        int inc = s;
+    for (long long t = begin + 2 * lane; t < end; t += 64) {
+        const longlong2 q = two_tokens(a, t - odd);
+        const long long v[2] = {q.x, q.y};
 #pragma unroll
-        for (int m = 1; m < 32; m <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, inc, m);
-            if (lane >= m) inc += o;
+        for (int e = 0; e < 2; ++e) {
+            if (v[e] >= a.V) bad = 1;
+            if (v[e] < 0 || v[e] >= a.V) continue;
+            const int o = (int)v[e] & (owners - 1);
+            less += o < own;
+            if (o == own) atomicAdd(&mine[(int)v[e] >> shift], 1);
         }
-        if (lane == 31) sums[warp] = inc;
-        __syncthreads();
-        int at = base + inc - s;
-        for (int w = 0; w < warp; ++w) at += sums[w];
-        for (int i = r0; i < min(rows, r0 + run); ++i) {
-            const int c = hist[i];
-            hist[i] = at;
-            a.first[(long long)own * rows + i] = at;
+    }
+    less = __reduce_add_sync(0xffffffffu, less);
+    if (lane == 0) lower[warp] = less;
+    __syncthreads();
+    // a thread a row: the row's tokens, and where its first one goes
+    int n = 0;
+    if (tid < rows)
+        for (int w = 0; w < kSortWarps; ++w) n += count[w * rows + tid];
+    int inc = n;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, m);
+        if (lane >= m) inc += o;
+    }
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    // places before: the lower owners', and the warps' before
+    const int before = __reduce_add_sync(0xffffffffu, lower[lane] + (lane < warp ? sums[lane] : 0));
+    int at = before + inc - n;
+    if (tid < rows) {
+        a.first[(long long)own * rows + tid] = at;
+        if (own == owners - 1 && tid == rows - 1) {
+            a.first[(long long)owners * rows] = at + n;
+            *a.count = at + n;
+        }
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int c = count[w * rows + tid];
+            count[w * rows + tid] = at;
             at += c;
         }
     }
-    if (tid == 0 && own == owners - 1) {
-        a.first[(long long)owners * rows] = base + total;
-        *a.count = base + total;
-    }
     if (tid == 0 && own == 0) *a.status = bad ? kStatusTarget : 0u;
-    // this owner's tokens in order, in the places that they will take
-    int2* list = total <= kSortList ? held : a.list + base;
-    int at = before;
-#pragma unroll 4
-    for (long long t = begin; t < end; t += 32) {
-        const long long v = t + lane < end ? __ldg(a.tokens + t + lane) : -1;
-        const bool hit = v >= 0 && v < a.V && ((int)v & (owners - 1)) == own;
-        const uint32_t m = __ballot_sync(0xffffffffu, hit);
-        if (hit) list[at + __popc(m & ((1u << lane) - 1u))] = make_int2((int)(t + lane), (int)v >> shift);
-        at += __popc(m);
-    }
     __syncthreads();
-    if (warp != 0) return;
-    // each to its row's next place: 32 at a time, equal rows in the order of their lanes
-    int2 next = lane < total ? list[lane] : make_int2(0, 0);
-    for (int i = 0; i < total; i += 32) {
-        const bool on = i + lane < total;
-        const int2 e = on ? next : make_int2(0, -1 - lane);
-        if (i + 32 + lane < total) next = list[i + 32 + lane];
-        const uint32_t same = __match_any_sync(0xffffffffu, e.y);
-        const int rank = __popc(same & ((1u << lane) - 1u));
-        if (on) {
-            const int place = hist[e.y] + rank;
-            a.place[place] = make_int2(e.x, own * rows + e.y);
+#pragma unroll 4
+    for (long long t = begin; t < end; t += 64) {
+        const longlong2 q = t + 2 * lane < end ? two_tokens(a, t + 2 * lane - odd) : make_longlong2(-1, -1);
+        const long long v[2] = {q.x, q.y};
+        bool hit[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) hit[e] = v[e] >= 0 && v[e] < a.V && ((int)v[e] & (owners - 1)) == own;
+        // few lanes of a warp find one of this owner's tokens: they place theirs in turn
+        for (uint32_t m = __ballot_sync(0xffffffffu, hit[0] || hit[1]); m != 0u; m &= m - 1u) {
+            if (lane == __ffs(m) - 1) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (hit[e]) {
+                        const int row = (int)v[e] >> shift;
+                        a.place[mine[row]++] = make_int2((int)(t + 2 * lane + e - odd), own * rows + row);
+                    }
+            }
+            __syncwarp();
         }
-        __syncwarp();
-        if (on && rank == 0) hist[e.y] += __popc(same);
-        __syncwarp();
     }
 }
 
-// 8 columns of a row of dw: scale v, onto what is there (accumulate).
-__device__ __forceinline__ void put_row(const EmbedBwdArgs& a, long long row, int v8, const f2x (&v)[4]) {
-    const long long at = row * a.D + 8LL * v8;
+// 8 columns of a row of dw (`old`: what they hold where the gradient is added to it).
+struct Old {
+    uint4 q[2];
+};
+__device__ __forceinline__ Old old_row(const EmbedBwdArgs& a, long long row, int v8) {
+    Old o;
+    o.q[0] = o.q[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (!a.accumulate) return o;
+    const uint4* p = static_cast<const uint4*>(a.dw) + (row * (a.D / 8) + v8) * (a.f32 ? 2 : 1);
+    o.q[0] = p[0];
+    if (a.f32) o.q[1] = p[1];
+    return o;
+}
+__device__ __forceinline__ f2x word_pair(uint32_t lo, uint32_t hi) { return pk2(__uint_as_float(lo), __uint_as_float(hi)); }
+__device__ __forceinline__ void put_row(const EmbedBwdArgs& a, long long row, int v8, const f2x (&v)[4], const Old& old) {
     const f2x s = dup2(a.scale);
-    f2x o[4] = {0ull, 0ull, 0ull, 0ull};
+    uint4* p = static_cast<uint4*>(a.dw) + (row * (a.D / 8) + v8) * (a.f32 ? 2 : 1);
+    f2x o[4];
     if (a.f32) {
-        float* p = static_cast<float*>(a.dw) + at;
-        if (a.accumulate) read_pairs(p, o);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fma2(s, v[e], o[e]);
-        store_pairs(p, o);
+        o[0] = word_pair(old.q[0].x, old.q[0].y);
+        o[1] = word_pair(old.q[0].z, old.q[0].w);
+        o[2] = word_pair(old.q[1].x, old.q[1].y);
+        o[3] = word_pair(old.q[1].z, old.q[1].w);
     } else {
-        uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dw) + at);
-        if (a.accumulate) unpack_pairs(*p, o);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = fma2(s, v[e], o[e]);
-        *p = make_uint4(x2bf(o[0]), x2bf(o[1]), x2bf(o[2]), x2bf(o[3]));
+        unpack_pairs(old.q[0], o);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = fma2(s, v[e], o[e]);
+    if (a.f32)
+        put_pairs(reinterpret_cast<float*>(p), o);
+    else
+        *p = make_uint4(x2bf(o[0]), x2bf(o[1]), x2bf(o[2]), x2bf(o[3]));
 }
 // Vocabulary row of a row in sorted order.
 __device__ __forceinline__ long long vocabulary_row(const EmbedBwdArgs& a, int rows, int s) {
     return (long long)(s % rows) * a.owners + s / rows;
 }
 
-__global__ void __launch_bounds__(256) embedding_sum_kernel(const EmbedBwdArgs a, int rows, int chunks) {
+// Sums of a chunk's rows (blockIdx.x < chunks) in columns blockIdx.y, 8 a thread; zeros for the rows without a token.
+__global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedBwdArgs a, int rows, int chunks) {
     __shared__ int2 place[kEmbedChunk];
+    __shared__ uint32_t empty;
     pdl_trigger();
     pdl_wait();
-    const int nv = a.D / 8;
+    const int nv = a.D / 8, v = blockIdx.y * kSumThreads + threadIdx.x;
     if ((int)blockIdx.x >= chunks) {
-        // rows without a token: 32 looked up at a time, then written
-        __shared__ uint32_t empty;
-        const int all = a.owners * rows, step = (gridDim.x - chunks) * 32, words = nv * (a.f32 ? 2 : 1);
+        // 32 rows looked up at a time, then written
+        const f2x none[4] = {0ull, 0ull, 0ull, 0ull};
+        const int all = a.owners * rows, step = (gridDim.x - chunks) * 32, width = a.f32 ? 2 : 1;
         for (int s0 = (blockIdx.x - chunks) * 32; s0 < all; s0 += step) {
             if (threadIdx.x < 32) {
                 const int s = s0 + threadIdx.x;
@@ -212,11 +217,14 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const EmbedBwdArgs a
                 if (threadIdx.x == 0) empty = m;
             }
             __syncthreads();
-            for (uint32_t m = empty; m != 0u; m &= m - 1u) {
-                const long long row = vocabulary_row(a, rows, s0 + __ffs(m) - 1);
-                uint4* p = reinterpret_cast<uint4*>(a.dw) + row * words;
-                for (int v = threadIdx.x; v < words; v += blockDim.x) p[v] = make_uint4(0u, 0u, 0u, 0u);
-            }
+            if (v < nv)
+                for (uint32_t m = empty; m != 0u; m &= m - 1u) {
+                    uint4* p = static_cast<uint4*>(a.dw) + (vocabulary_row(a, rows, s0 + __ffs(m) - 1) * nv + v) * width;
+                    if (a.f32)
+                        put_pairs(reinterpret_cast<float*>(p), none);
+                    else
+                        *p = make_uint4(0u, 0u, 0u, 0u);
+                }
             __syncthreads();
         }
         return;
@@ -225,63 +233,80 @@ __global__ void __launch_bounds__(256) embedding_sum_kernel(const EmbedBwdArgs a
     if (n <= 0) return;
     if ((int)threadIdx.x < n) place[threadIdx.x] = __ldcg(a.place + i0 + threadIdx.x);
     __syncthreads();
+    if (v >= nv) return;
     // what of the chunk's first and last row lies in other chunks
-    const bool from = __ldcg(a.first + place[0].y) < i0, to = __ldcg(a.first + place[n - 1].y + 1) > i0 + n;
     const int head = place[0].y, tail = place[n - 1].y;
-    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-        f2x s[4] = {0ull, 0ull, 0ull, 0ull};
-        constexpr int AHEAD = 8;
-        for (int i = 0; i < n; i += AHEAD) {
-            uint4 q[AHEAD];
+    const bool from = __ldcg(a.first + head) < i0, to = __ldcg(a.first + tail + 1) > i0 + n;
+    f2x s[4] = {0ull, 0ull, 0ull, 0ull};
+    constexpr int AHEAD = 4;
+#pragma unroll 1
+    for (int i = 0; i < n; i += AHEAD) {
+        uint4 q[AHEAD];
+        Old old[AHEAD];
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k)
-                if (i + k < n) q[k] = __ldg(reinterpret_cast<const uint4*>(a.dy) + (long long)place[i + k].x * nv + v);
+        for (int k = 0; k < AHEAD; ++k) {
+            if (i + k >= n) continue;
+            q[k] = __ldg(reinterpret_cast<const uint4*>(a.dy) + (long long)place[i + k].x * nv + v);
+            if (a.accumulate && (i + k + 1 == n || place[i + k + 1].y != place[i + k].y))
+                old[k] = old_row(a, vocabulary_row(a, rows, place[i + k].y), v);
+        }
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) {
-                if (i + k >= n) break;
-                const int row = place[i + k].y;
-                f2x d[4];
-                unpack_pairs(q[k], d);
+        for (int k = 0; k < AHEAD; ++k) {
+            if (i + k >= n) break;
+            const int row = place[i + k].y;
+            f2x d[4];
+            unpack_pairs(q[k], d);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = add2(s[e], d[e]);
-                if (i + k + 1 < n && place[i + k + 1].y == row) continue;
-                // the row ends here, or the chunk does: slot 0 for a row from an earlier chunk, 1 for one that goes on
-                if (row == head && from)
-                    store_pairs(a.part + (2LL * blockIdx.x) * a.D + 8 * v, s);
-                else if (row == tail && to)
-                    store_pairs(a.part + (2LL * blockIdx.x + 1) * a.D + 8 * v, s);
-                else
-                    put_row(a, vocabulary_row(a, rows, row), v, s);
+            for (int e = 0; e < 4; ++e) s[e] = add2(s[e], d[e]);
+            if (i + k + 1 < n && place[i + k + 1].y == row) continue;
+            // the row ends here, or the chunk does: slot 0 for a row from an earlier chunk, 1 for one that goes on
+            if (row == head && from)
+                put_pairs(a.part + (2LL * blockIdx.x) * a.D + 8 * v, s);
+            else if (row == tail && to)
+                put_pairs(a.part + (2LL * blockIdx.x + 1) * a.D + 8 * v, s);
+            else
+                put_row(a, vocabulary_row(a, rows, row), v, s, a.accumulate ? old[k] : Old{});
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = 0ull;
-            }
+            for (int e = 0; e < 4; ++e) s[e] = 0ull;
         }
     }
 }
 
-// The row that begins in chunk blockIdx.x and goes on past it.
-__global__ void __launch_bounds__(256) embedding_join_kernel(const EmbedBwdArgs a, int rows) {
+// The row that begins in chunk blockIdx.x and goes on past it: threadIdx.y takes a quarter of its chunks.
+__global__ void __launch_bounds__(kSumThreads * kJoinParts) embedding_join_kernel(const EmbedBwdArgs a, int rows) {
+    __shared__ f2x acc[kJoinParts][4][kSumThreads];
     pdl_trigger();
     pdl_wait();
-    const int nv = a.D / 8, count = __ldcg(a.count);
+    const int nv = a.D / 8, v = blockIdx.y * kSumThreads + threadIdx.x, count = __ldcg(a.count), y = threadIdx.y;
     const int end = (blockIdx.x + 1) * kEmbedChunk;
     if (end >= count) return;
     const int row = __ldcg(a.place + end - 1).y;
     const int begin = __ldcg(a.first + row), last = __ldcg(a.first + row + 1);
     if (last <= end || begin < end - kEmbedChunk) return;
-    const int more = (last - 1) / kEmbedChunk;   // its last chunk
-    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
-        f2x s[4];
-        read_pairs(a.part + (2LL * blockIdx.x + 1) * a.D + 8 * v, s);
-#pragma unroll 4
-        for (int c = blockIdx.x + 1; c <= more; ++c) {
+    // its parts: slot 1 of this chunk, slot 0 of those after it
+    const int parts = (last - 1) / kEmbedChunk - blockIdx.x + 1, per = (parts + kJoinParts - 1) / kJoinParts;
+    f2x s[4] = {0ull, 0ull, 0ull, 0ull};
+    if (v < nv) {
+        const int stop = min(parts, (y + 1) * per);
+#pragma unroll 8
+        for (int c = y * per; c < stop; ++c) {
             f2x d[4];
-            read_pairs(a.part + 2LL * c * a.D + 8 * v, d);
+            read_pairs(a.part + (2LL * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * a.D + 8 * v, d);
 #pragma unroll
             for (int e = 0; e < 4; ++e) s[e] = add2(s[e], d[e]);
         }
-        put_row(a, vocabulary_row(a, rows, row), v, s);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[y][e][threadIdx.x] = s[e];
+    __syncthreads();
+    if (y != 0 || v >= nv) return;
+    const long long out = vocabulary_row(a, rows, row);
+    const Old old = old_row(a, out, v);
+#pragma unroll
+    for (int k = 1; k < kJoinParts; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[e] = add2(s[e], acc[k][e][threadIdx.x]);
+    put_row(a, out, v, s, old);
 }
 
 int lanes_of(int D) { return std::min(256, (D / 8 + 31) / 32 * 32); }
@@ -312,19 +337,21 @@ cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s, bool pdl) {
 }
 cudaError_t launch_embedding_sort(const EmbedBwdArgs& a, cudaStream_t s, bool pdl) {
     const int rows = owner_rows(a);
-    constexpr size_t held = kSortList * sizeof(int2);
     static std::atomic<bool> allowed[64];
-    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(embedding_sort_kernel), held + kSortRows * sizeof(int), allowed);
+    const cudaError_t e = allow_smem(reinterpret_cast<const void*>(embedding_sort_kernel), kSortWarps * kSortRows * sizeof(int), allowed);
     if (e != cudaSuccess) return e;
-    return launch_ex(embedding_sort_kernel, dim3((unsigned)a.owners), dim3(kSortThreads), held + rows * sizeof(int), s, pdl, a, rows);
+    return launch_ex(embedding_sort_kernel, dim3((unsigned)a.owners), dim3(kSortWarps * 32), kSortWarps * rows * sizeof(int), s, pdl, a,
+                     rows);
 }
 cudaError_t launch_embedding_sum(const EmbedBwdArgs& a, cudaStream_t s, bool pdl) {
-    const int rows = owner_rows(a), chunks = (int)embed_chunks(a.T);
+    const int rows = owner_rows(a), chunks = (int)embed_chunks(a.T), blocks = (a.D / 8 + kSumThreads - 1) / kSumThreads;
     const int zero = a.accumulate ? 0 : std::min((a.owners * rows + 31) / 32, 152 * 8);
-    return launch_ex(embedding_sum_kernel, dim3((unsigned)(chunks + zero)), dim3((unsigned)lanes_of(a.D)), 0, s, pdl, a, rows, chunks);
+    return launch_ex(embedding_sum_kernel, dim3((unsigned)(chunks + zero), (unsigned)blocks), dim3(kSumThreads), 0, s, pdl, a, rows,
+                     chunks);
 }
 cudaError_t launch_embedding_join(const EmbedBwdArgs& a, cudaStream_t s, bool pdl) {
-    return launch_ex(embedding_join_kernel, dim3((unsigned)embed_chunks(a.T)), dim3((unsigned)lanes_of(a.D)), 0, s, pdl, a,
+    const int blocks = (a.D / 8 + kSumThreads - 1) / kSumThreads;
+    return launch_ex(embedding_join_kernel, dim3((unsigned)embed_chunks(a.T), (unsigned)blocks), dim3(kSumThreads, kJoinParts), 0, s, pdl, a,
                      owner_rows(a));
 }
 

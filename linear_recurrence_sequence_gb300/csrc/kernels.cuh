@@ -726,7 +726,7 @@ struct ConvBwdArgs {
     float* part;                 // [parts][W + 1][D]
     float *dw, *dbias;
 };
-int conv_bwd_parts(int B, int L, int D);
+int conv_bwd_parts(int B, int L, int D);   // CTAs along time of both directions
 cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& a, cudaStream_t s, bool pdl);
@@ -751,7 +751,6 @@ struct EmbedBwdArgs {
     int f32, accumulate;
     uint32_t* status;
     int owners;                  // CTAs that share out the vocabulary
-    int2* list;                  // [T]: an owner's positions and rows, in the tokens' order
     int2* place;                 // [T]: positions and rows (in the owners' order), sorted
     int* count;                  // [1]: of them
     int* first;                  // [owners rows + 1]: each row's first place

@@ -93,6 +93,15 @@ __device__ __forceinline__ void store_pairs(float* p, const f2x (&v)[4]) {
     reinterpret_cast<float4*>(p)[0] = a;
     reinterpret_cast<float4*>(p)[1] = b;
 }
+// The same to global memory: 32 bytes at once where they may be (two 16-byte stores of a warp would each fill half of
+// every sector that they touch).
+__device__ __forceinline__ void put_pairs(float* p, const f2x (&v)[4]) {
+    if ((reinterpret_cast<uintptr_t>(p) & 31u) != 0) {
+        store_pairs(p, v);
+        return;
+    }
+    asm volatile("st.global.v4.b64 [%0], {%1, %2, %3, %4};" ::"l"(p), "l"(v[0]), "l"(v[1]), "l"(v[2]), "l"(v[3]) : "memory");
+}
 __device__ __forceinline__ void read_pairs(const float* p, f2x (&v)[4]) {
     const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
     v[0] = pk2(a.x, a.y);

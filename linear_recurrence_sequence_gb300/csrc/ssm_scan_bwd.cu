@@ -368,7 +368,7 @@ __device__ __forceinline__ void back(BwdTile<LN>& s, int t, uint32_t at, int lan
 
 __device__ __forceinline__ void put8(void* p, long long at, bool f32, const f2x (&v)[4]) {
     if (f32)
-        store_pairs(static_cast<float*>(p) + at, v);
+        put_pairs(static_cast<float*>(p) + at, v);
     else
         *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = make_uint4(x2bf(v[0]), x2bf(v[1]), x2bf(v[2]), x2bf(v[3]));
 }

@@ -1,8 +1,8 @@
 """The embedding lookup and its gradient by sorted tokens against elementary operations.
 
-The lookup is one product and one rounding: equal bits.  A row's gradient adds runs of 32 tokens one after another and
-joins the runs in order: at most 32 + count / 32 roundings of 2^-24 of the absolute sum, below 2^-18 for up to 1000
-occurrences (2^-24 (32 + count / 32) is used for more); one rounding to BF16 (2^-8) or of the scaled sum (2^-23)."""
+The lookup is one product and one rounding: equal bits.  A row's gradient adds runs of up to 16 tokens one after another
+and joins the runs in order: at most 16 + count / 16 + 1 roundings of 2^-24 of the absolute sum; one rounding to BF16
+(2^-8) or of the scaled sum (2^-23)."""
 import pytest
 import torch
 
@@ -44,7 +44,7 @@ def _check_dw(dw, dy, tokens, V, scale, old=None):
     count = torch.zeros(V, device=DEV).index_add(0, t, torch.ones_like(t, dtype=torch.float32)).double()[:, None]
     if old is not None:
         want, terms = want + old.double(), terms + old.double().abs()
-    most = 2.0 ** -24 * (34 + count / 32) * terms
+    most = 2.0 ** -24 * (18 + count / 16) * terms
     most = most + (2.0 ** -8 if dw.dtype == BF else 2.0 ** -23) * want.abs() + 2.0 ** -134
     if old is None:
         assert float(dw[count[:, 0] == 0].abs().max() if bool((count == 0).any()) else 0) == 0

@@ -115,7 +115,7 @@ int lrs_selftest_wait_timeout(void* scratch, cudaStream_t stream);
  * forward maps, 29 its prefixes, 30 its replay, 31 its step, 32 its reverse maps,
  * 33 its backward, 34 its gradient sums, 35 the causal convolution, 36 its step,
  * 37 its backward, 38 its gradient sums, 39 the embedding lookup, 40 the sort of its
- * tokens, 41 its gradient's sums, 42 the rows joined from several; 9 also covers
+ * tokens, 41 its gradient's sums; 9 also covers
  * the bias-gradient reductions) and duration in
  * milliseconds; *count receives the number of
  * kernels launched while profiling was on.  Not thread-safe: one profiling

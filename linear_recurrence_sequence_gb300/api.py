@@ -1235,7 +1235,6 @@ KERNEL_NAMES = {
     32: "ssm_rmaps_kernel", 33: "ssm_bwd_kernel", 34: "ssm_finish_kernel", 35: "causal_conv_fwd_kernel",
     36: "causal_conv_step_kernel", 37: "causal_conv_bwd_kernel", 38: "causal_conv_sum_kernel",
     39: "embedding_fwd_kernel", 40: "embedding_sort_kernel", 41: "embedding_sum_kernel",
-    42: "embedding_join_kernel",
 }
 
 

@@ -86,7 +86,7 @@ enum {
     KID_RGLRU_PROJ_PACK, KID_BLOCK_GEMM, KID_BLOCK_NORM, KID_BLOCK_CONV, KID_BLOCK_JOIN, KID_BLOCK_SUM, KID_CE_GEMM,
     KID_CE_ROWS, KID_GATED_NORM, KID_GATED_NORM_SUM, KID_ADAMW_NORM, KID_ADAMW_UPDATE, KID_SSM_MAPS, KID_SSM_PREFIX,
     KID_SSM_REPLAY, KID_SSM_STEP, KID_SSM_BWD_MAPS, KID_SSM_BWD, KID_SSM_FINISH, KID_CONV_FWD, KID_CONV_STEP,
-    KID_CONV_BWD, KID_CONV_SUM, KID_EMBED_FWD, KID_EMBED_SORT, KID_EMBED_SUM, KID_EMBED_JOIN
+    KID_CONV_BWD, KID_CONV_SUM, KID_EMBED_FWD, KID_EMBED_SORT, KID_EMBED_SUM
 };
 
 #define LRS_LAUNCH(id, stream, expr)            \
@@ -1779,14 +1779,15 @@ int check_embed_shape(int T, int V, int D) {
 }
 
 struct EmbedScratch {
-    size_t place, first, part, total;
+    size_t place, first, done, part, total;
 };
 EmbedScratch embed_scratch(int T, int V, int D) {
     EmbedScratch s;
     const long long owners = embed_owners(V), rows = (V + owners - 1) / owners;
     s.place = 256;
     s.first = s.place + up256((size_t)T * sizeof(int2));
-    s.part = s.first + up256((size_t)(owners * rows + 1) * sizeof(int));
+    s.done = s.first + up256((size_t)(owners * rows + 1) * sizeof(int));
+    s.part = s.done + up256((size_t)embed_dones(T, D) * sizeof(int));
     s.total = s.part + up256((size_t)2 * embed_chunks(T) * D * sizeof(float));
     return s;
 }
@@ -1838,9 +1839,9 @@ int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int 
     a.count = at<int>(scratch, 64);
     a.first = at<int>(scratch, l.first);
     a.part = at<float>(scratch, l.part);
+    a.done = at<int>(scratch, l.done);
     LRS_LAUNCH(KID_EMBED_SORT, stream, launch_embedding_sort(a, stream, pdl_ok()));
     LRS_LAUNCH(KID_EMBED_SUM, stream, launch_embedding_sum(a, stream, pdl_ok()));
-    LRS_LAUNCH(KID_EMBED_JOIN, stream, launch_embedding_join(a, stream, pdl_ok()));
     return LRS_OK;
 }
 

@@ -11,9 +11,8 @@
 // time through a run of tokens of 4 channels, the last W inputs in
 // registers, and asks for 8 rows at a time.  The backward
 // forms pre again (x is read anyway, pre is not kept) and keeps the sums of the
-// dx of the last W tokens.  Runs are 32 tokens long where that leaves 16 warps an SM
-// (W - 1 rows before a run, and backward W - 1 tokens after it, are gone through
-// twice), else 8.
+// dx of the last W tokens.  Runs are up to 64 tokens long (W - 1 rows before a run,
+// and backward W - 1 tokens after it, are gone through twice).
 #include <algorithm>
 #include <type_traits>
 
@@ -24,14 +23,15 @@ namespace lrs {
 namespace {
 
 constexpr int kConvStep = 8;      // rows that a thread asks for at a time
-constexpr int kConvWarps = 8;     // runs of a CTA
+constexpr int kConvWarps = 4;     // runs of a CTA
 constexpr int kConvPairs = 2;   // of channels, a thread
 constexpr int kConvSms = 152;
 
-// A run's tokens, by the batch and the length of a row.
+// A run's tokens: as long as leaves 12 warps an SM (4 x 4096 x 1024 forward + backward 64: 52 us, 32: 53, 16: 60).
 int conv_run(int B, int L, int D) {
-    const long long warps = (long long)B * ((L + 31) / 32) * ((D + 127) / 128);
-    return warps >= 16 * kConvSms ? 32 : kConvStep;
+    for (int run = 64; run > kConvStep; run /= 2)
+        if ((long long)B * ((L + run - 1) / run) * ((D + 64 * kConvPairs - 1) / (64 * kConvPairs)) >= 12 * kConvSms) return run;
+    return kConvStep;
 }
 
 // P pairs of channels of a row: BF16 words, FP32 pairs.
@@ -153,8 +153,27 @@ __device__ __forceinline__ void conv_sum(const f2x (&w)[W][P], const f2x (&bias)
     }
 }
 
+// kConvStep tokens forward.  PLAIN: all of them there, and no start reaches their
+// taps (a group without branches: with a test a token it took twice the instructions).
+template <int W, int P, bool SILU, bool PLAIN>
+__device__ __forceinline__ void conv_group(const Words<P> (&q)[kConvStep], int n, uint32_t history, const f2x (&w)[W][P],
+                                           const f2x (&bias)[P], f2x (&v)[W][P], uint16_t* py, long long ld) {
+#pragma unroll
+    for (int r = 0; r < kConvStep; ++r) {
+        shift_in(v);
+        unpack_words(q[r], v[0]);
+        if (!PLAIN && r >= n) continue;
+        f2x acc[P];
+        conv_sum<W, P, !PLAIN>(w, bias, v, history >> (kConvStep - 1 - r), acc);
+        Words<P> o;
+#pragma unroll
+        for (int e = 0; e < P; ++e) o.w[e] = x2bf(SILU ? silu2(acc[e]) : acc[e]);
+        store_words(py + r * ld, o);
+    }
+}
+
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps, 3) causal_conv_fwd_kernel(const ConvArgs a, int run) {
+__global__ void __launch_bounds__(32 * kConvWarps, 6) causal_conv_fwd_kernel(const ConvArgs a, int run) {
     constexpr int H = W - 1, P = kConvPairs;
     pdl_trigger();
     pdl_wait();
@@ -177,21 +196,10 @@ __global__ void __launch_bounds__(32 * kConvWarps, 3) causal_conv_fwd_kernel(con
 #pragma unroll
         for (int r = 0; r < kConvStep; ++r) q[r] = r < n ? load_words<P>(px + r * a.x.st) : no_words<P>();
         history = (history & ((1u << H) - 1u)) << kConvStep | starts_of<kConvStep>(a.reset, row, t, a.L);
-#pragma unroll
-        for (int r = 0; r < kConvStep; ++r) {
-            shift_in(v);
-            unpack_words(q[r], v[0]);
-            if (r >= n) continue;
-            f2x acc[P];
-            if (history == 0u)
-                conv_sum<W, P, false>(w, bias, v, 0u, acc);
-            else
-                conv_sum<W, P, true>(w, bias, v, history >> (kConvStep - 1 - r), acc);
-            Words<P> o;
-#pragma unroll
-            for (int e = 0; e < P; ++e) o.w[e] = x2bf(SILU ? silu2(acc[e]) : acc[e]);
-            store_words(py + (long long)r * a.D, o);
-        }
+        if (n >= kConvStep && history == 0u)
+            conv_group<W, P, SILU, true>(q, n, 0u, w, bias, v, py, a.D);
+        else
+            conv_group<W, P, SILU, false>(q, n, history, w, bias, v, py, a.D);
     }
     // the row's last inputs, as far as they belong to its last sequence
     if (a.state_out != nullptr && p.end == a.L) {
@@ -257,11 +265,16 @@ __device__ __forceinline__ void put_channels_of(void* p, long long at, bool f32,
     }
 }
 
+// The gradients that a thread adds up along its run, and the sums of dx of the last W tokens.
+template <int W, int P>
+struct ConvSums {
+    f2x dw[W][P], db[P], dx[W][P];
+};
 // One token backward: d becomes dpre; dx[H - j] of the token j earlier, and the
 // weights' sums (in: the token is the run's own).
 template <int W, int P, bool SILU, bool CUT>
 __device__ __forceinline__ void conv_token_back(const f2x (&w)[W][P], const f2x (&bias)[P], const f2x (&v)[W][P], uint32_t history,
-                                                bool in, f2x (&d)[P], f2x (&dx)[W][P], f2x (&dw)[W][P], f2x (&db)[P]) {
+                                                bool in, f2x (&d)[P], ConvSums<W, P>& s) {
     if (SILU) {
         f2x pre[P];
         conv_sum<W, P, CUT>(w, bias, v, history, pre);
@@ -269,23 +282,54 @@ __device__ __forceinline__ void conv_token_back(const f2x (&w)[W][P], const f2x 
         for (int e = 0; e < P; ++e) {
             float p0, p1;
             up2(pre[e], p0, p1);
-            const f2x s = pk2(ssm_sigmoid(p0), ssm_sigmoid(p1)), one = dup2(1.f);
-            d[e] = mul2(d[e], mul2(s, fma2(pre[e], sub2(one, s), one)));
+            const f2x g = pk2(ssm_sigmoid(p0), ssm_sigmoid(p1)), one = dup2(1.f);
+            d[e] = mul2(d[e], mul2(g, fma2(pre[e], sub2(one, g), one)));
         }
     }
 #pragma unroll
     for (int j = 0; j < W; ++j) {
         if (CUT && !tap_live(history, j)) break;
-        add_product(dx[W - 1 - j], w[j], d);
-        if (in) add_product(dw[j], d, v[j]);
+        add_product(s.dx[W - 1 - j], w[j], d);
+        if (in) add_product(s.dw[j], d, v[j]);
     }
     if (in)
 #pragma unroll
-        for (int e = 0; e < P; ++e) db[e] = add2(db[e], d[e]);
+        for (int e = 0; e < P; ++e) s.db[e] = add2(s.db[e], d[e]);
+}
+// kConvStep tokens backward, of which n are there and `own` the run's own; the first is token `from` of the run.
+// PLAIN: all of both, and no start reaches their taps.
+template <int W, int P, bool SILU, bool PLAIN>
+__device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const ConvPlace& p, const Words<P> (&q)[kConvStep],
+                                                const Words<P> (&qd)[kConvStep], int n, int own, int from, uint32_t history,
+                                                const f2x (&w)[W][P], const f2x (&bias)[P], f2x (&v)[W][P], ConvSums<W, P>& s) {
+    constexpr int H = W - 1;
+    const long long at = (long long)p.b * g.dx.sb + (long long)(p.t0 + from - H) * g.dx.st + p.c;
+#pragma unroll
+    for (int r = 0; r < kConvStep; ++r) {
+        if (!PLAIN && r >= own + H) break;
+        shift_in(v);
+        unpack_words(q[r], v[0]);
+        if (PLAIN || r < n) {
+            f2x d[P];
+            unpack_words(qd[r], d);
+            conv_token_back<W, P, SILU, !PLAIN>(w, bias, v, history >> (kConvStep - 1 - r), PLAIN || r < own, d, s);
+        }
+        // dx[0] is whole now: the token H earlier.  Before the run it is another thread's, before the row an
+        // input carried in.
+        if (r >= H || from > 0)
+            put_channels_of(g.dx.p, at + r * g.dx.st, g.f32, s.dx[0]);
+        else if (p.t0 == 0 && g.dstate != nullptr)
+            put_channels_of(g.dstate, ((long long)p.b * H + r) * g.f.D + p.c, g.f32, s.dx[0]);
+#pragma unroll
+        for (int j = 0; j < H; ++j)
+#pragma unroll
+            for (int e = 0; e < P; ++e) s.dx[j][e] = s.dx[j + 1][e];
+        clear(s.dx[H]);
+    }
 }
 
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps, 2) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
+__global__ void __launch_bounds__(32 * kConvWarps, 4) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
     constexpr int H = W - 1, P = kConvPairs;
     __shared__ f2x acc[kConvWarps][W + 1][32][P];
     pdl_trigger();
@@ -293,32 +337,30 @@ __global__ void __launch_bounds__(32 * kConvWarps, 2) causal_conv_bwd_kernel(con
     const ConvArgs& a = g.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const ConvPlace p = conv_place(a, run, 64 * P);
-    f2x dw[W][P], db[P];
-    clear(db);
+    ConvSums<W, P> s;
+    clear(s.db);
 #pragma unroll
-    for (int j = 0; j < W; ++j) clear(dw[j]);
+    for (int j = 0; j < W; ++j) {
+        clear(s.dw[j]);
+        clear(s.dx[j]);
+    }
     if (p.on) {
-        f2x w[W][P], bias[P], v[W][P], dx[W][P];
+        f2x w[W][P], bias[P], v[W][P];
         clear(bias);
+        clear(v[H]);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            load_vector(a.w + (long long)j * a.D + p.c, w[j]);
-            clear(v[j]);
-            clear(dx[j]);
-        }
+        for (int j = 0; j < W; ++j) load_vector(a.w + (long long)j * a.D + p.c, w[j]);
         if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
         for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
         const long long row = (long long)p.b * a.L;
         uint32_t history = starts_of<H>(a.reset, row, p.t0 - H, a.L);
-        // the run's tokens, then the H after it, whose taps reach into it
-        const int stop = p.end + H;
         const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
         const uint16_t* py = g.dy + (row + p.t0) * a.D + p.c;
-        const long long odx = (long long)p.b * g.dx.sb + p.c;
-        for (int t = p.t0; t < stop; t += kConvStep, px += kConvStep * a.x.st, py += (long long)kConvStep * a.D) {
+        // the run's tokens, then the H after it, whose taps reach into it
+        for (int t = p.t0; t < p.end + H; t += kConvStep, px += kConvStep * a.x.st, py += (long long)kConvStep * a.D) {
             Words<P> q[kConvStep], qd[kConvStep];
-            const int n = min(a.L, stop) - t;   // tokens that there are (may be none)
+            const int n = min(a.L, p.end + H) - t, own = p.end - t;   // (may be none)
 #pragma unroll
             for (int r = 0; r < kConvStep; ++r) {
                 q[r] = qd[r] = no_words<P>();
@@ -328,49 +370,26 @@ __global__ void __launch_bounds__(32 * kConvWarps, 2) causal_conv_bwd_kernel(con
                 }
             }
             history = (history & ((1u << H) - 1u)) << kConvStep | starts_of<kConvStep>(a.reset, row, t, a.L);
-#pragma unroll
-            for (int r = 0; r < kConvStep; ++r) {
-                if (t + r >= stop) break;
-                shift_in(v);
-                unpack_words(q[r], v[0]);
-                if (r < n) {
-                    f2x d[P];
-                    unpack_words(qd[r], d);
-                    const bool in = t + r < p.end;
-                    if (history == 0u)
-                        conv_token_back<W, P, SILU, false>(w, bias, v, 0u, in, d, dx, dw, db);
-                    else
-                        conv_token_back<W, P, SILU, true>(w, bias, v, history >> (kConvStep - 1 - r), in, d, dx, dw, db);
-                }
-                // dx[0] is whole now: the token H earlier.  Before the run it is another thread's, before the row an
-                // input carried in.
-                const int at = t + r - H;
-                if (at >= p.t0)
-                    put_channels_of(g.dx.p, odx + (long long)at * g.dx.st, g.f32, dx[0]);
-                else if (p.t0 == 0 && g.dstate != nullptr)
-                    put_channels_of(g.dstate, ((long long)p.b * H + H + at) * a.D + p.c, g.f32, dx[0]);
-#pragma unroll
-                for (int j = 0; j < H; ++j)
-#pragma unroll
-                    for (int e = 0; e < P; ++e) dx[j][e] = dx[j + 1][e];
-                clear(dx[H]);
-            }
+            if (own >= kConvStep && history == 0u)
+                conv_group_back<W, P, SILU, true>(g, p, q, qd, n, own, t - p.t0, 0u, w, bias, v, s);
+            else
+                conv_group_back<W, P, SILU, false>(g, p, q, qd, n, own, t - p.t0, history, w, bias, v, s);
         }
     }
 #pragma unroll
     for (int j = 0; j <= W; ++j)
 #pragma unroll
-        for (int e = 0; e < P; ++e) acc[warp][j][lane][e] = j < W ? dw[j < W ? j : 0][e] : db[e];
+        for (int e = 0; e < P; ++e) acc[warp][j][lane][e] = j < W ? s.dw[j < W ? j : 0][e] : s.db[e];
     __syncthreads();
     const int width = 64 * P, spans = (a.D + width - 1) / width;
     for (int i = threadIdx.x; i < (W + 1) * 32 * P; i += 32 * kConvWarps) {
         const int j = i / (32 * P), l = i % (32 * P), c = (int)(blockIdx.x % spans) * width + l * 2;
         if (c >= a.D) continue;
-        f2x s = acc[0][j][l / P][l % P];
+        f2x sum = acc[0][j][l / P][l % P];
 #pragma unroll
-        for (int k = 1; k < kConvWarps; ++k) s = add2(s, acc[k][j][l / P][l % P]);
+        for (int k = 1; k < kConvWarps; ++k) sum = add2(sum, acc[k][j][l / P][l % P]);
         float2 o;
-        up2(s, o.x, o.y);
+        up2(sum, o.x, o.y);
         *reinterpret_cast<float2*>(g.part + (p.tile * (W + 1) + j) * a.D + c) = o;
     }
 }

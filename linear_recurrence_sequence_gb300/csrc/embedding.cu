@@ -12,9 +12,9 @@
 //          different CTAs.  Each CTA looks through all the tokens twice (8 T bytes
 //          from L2: no histogram or prefix crosses CTAs, one launch), counts its
 //          rows' and all lower owners' tokens, and places its own in order.
-//   sum    a CTA a chunk of 16 sorted places and 1024 columns; other CTAs zero the
-//          rows without a token.
-//   join   rows that reach over a chunk's end.
+//   sum    a CTA a chunk of 16 sorted places and 1024 columns; the parts of a row
+//          that reaches over chunks are joined, in their order, by whichever of its
+//          CTAs is done last; other CTAs zero the rows without a token.
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -67,7 +67,6 @@ constexpr int kSortRows = 1024;     // vocabulary rows of an owner, at most
 constexpr int kOwners = 128;        // a power of two, as are the owners of larger vocabularies
 constexpr int kEmbedChunk = 16;     // sorted places of a CTA of the sum
 constexpr int kSumThreads = 128;    // of it, 8 columns each
-constexpr int kJoinParts = 4;       // of the joined row's chunks, summed side by side
 
 // Tokens t (even, counted from a 16-byte boundary) and t + 1; -1 outside the array.
 __device__ __forceinline__ longlong2 two_tokens(const EmbedBwdArgs& a, long long t) {
@@ -78,7 +77,7 @@ __device__ __forceinline__ longlong2 two_tokens(const EmbedBwdArgs& a, long long
 // A warp takes consecutive tokens, so that a stable sort needs no order between
 // threads: it counts its tokens of each row, a row's counts are added up over the
 // warps, and the warp places its tokens from there on.
-__global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const EmbedBwdArgs a, int rows) {
+__global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const EmbedBwdArgs a, int rows, int dones) {
     extern __shared__ __align__(16) int count[];   // [kSortWarps][rows], then each warp's next place in a row
     __shared__ int lower[kSortWarps], sums[kSortWarps], bad;
     pdl_trigger();
@@ -86,6 +85,7 @@ __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const E
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, own = blockIdx.x, owners = a.owners, shift = 31 - __clz(owners);
     for (int i = tid; i < kSortWarps * rows; i += kSortWarps * 32) count[i] = 0;
     if (tid == 0) bad = 0;
+    for (int i = own * kSortWarps * 32 + tid; i < dones; i += owners * kSortWarps * 32) a.done[i] = 0;
     __syncthreads();
     int* mine = count + warp * rows;
     // tokens are read in pairs on 16-byte boundaries; `odd`: the first pair begins one before the array
@@ -198,10 +198,20 @@ __device__ __forceinline__ long long vocabulary_row(const EmbedBwdArgs& a, int r
     return (long long)(s % rows) * a.owners + s / rows;
 }
 
+// A row's parts: slot 1 of the chunk where it begins, slot 0 of those after it.
+struct RowParts {
+    int first, count;   // chunks
+};
+__device__ __forceinline__ RowParts parts_of(const EmbedBwdArgs& a, int row) {
+    const int begin = __ldcg(a.first + row), last = __ldcg(a.first + row + 1);
+    return {begin / kEmbedChunk, (last - 1) / kEmbedChunk - begin / kEmbedChunk + 1};
+}
+
 // Sums of a chunk's rows (blockIdx.x < chunks) in columns blockIdx.y, 8 a thread; zeros for the rows without a token.
 __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedBwdArgs a, int rows, int chunks) {
     __shared__ int2 place[kEmbedChunk];
     __shared__ uint32_t empty;
+    __shared__ int join[2];
     pdl_trigger();
     pdl_wait();
     const int nv = a.D / 8, v = blockIdx.y * kSumThreads + threadIdx.x;
@@ -233,14 +243,13 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedB
     if (n <= 0) return;
     if ((int)threadIdx.x < n) place[threadIdx.x] = __ldcg(a.place + i0 + threadIdx.x);
     __syncthreads();
-    if (v >= nv) return;
     // what of the chunk's first and last row lies in other chunks
     const int head = place[0].y, tail = place[n - 1].y;
     const bool from = __ldcg(a.first + head) < i0, to = __ldcg(a.first + tail + 1) > i0 + n;
     f2x s[4] = {0ull, 0ull, 0ull, 0ull};
     constexpr int AHEAD = 4;
 #pragma unroll 1
-    for (int i = 0; i < n; i += AHEAD) {
+    for (int i = 0; i < n && v < nv; i += AHEAD) {
         uint4 q[AHEAD];
         Old old[AHEAD];
 #pragma unroll
@@ -270,43 +279,41 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedB
             for (int e = 0; e < 4; ++e) s[e] = 0ull;
         }
     }
-}
-
-// The row that begins in chunk blockIdx.x and goes on past it: threadIdx.y takes a quarter of its chunks.
-__global__ void __launch_bounds__(kSumThreads * kJoinParts) embedding_join_kernel(const EmbedBwdArgs a, int rows) {
-    __shared__ f2x acc[kJoinParts][4][kSumThreads];
-    pdl_trigger();
-    pdl_wait();
-    const int nv = a.D / 8, v = blockIdx.y * kSumThreads + threadIdx.x, count = __ldcg(a.count), y = threadIdx.y;
-    const int end = (blockIdx.x + 1) * kEmbedChunk;
-    if (end >= count) return;
-    const int row = __ldcg(a.place + end - 1).y;
-    const int begin = __ldcg(a.first + row), last = __ldcg(a.first + row + 1);
-    if (last <= end || begin < end - kEmbedChunk) return;
-    // its parts: slot 1 of this chunk, slot 0 of those after it
-    const int parts = (last - 1) / kEmbedChunk - blockIdx.x + 1, per = (parts + kJoinParts - 1) / kJoinParts;
-    f2x s[4] = {0ull, 0ull, 0ull, 0ull};
-    if (v < nv) {
-        const int stop = min(parts, (y + 1) * per);
-#pragma unroll 8
-        for (int c = y * per; c < stop; ++c) {
-            f2x d[4];
-            read_pairs(a.part + (2LL * (blockIdx.x + c) + (c == 0 ? 1 : 0)) * a.D + 8 * v, d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[e] = add2(s[e], d[e]);
-        }
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[y][e][threadIdx.x] = s[e];
+    if (!from && !to) return;
+    // this CTA's parts are written: whether they were the last of their rows
+    __threadfence();
     __syncthreads();
-    if (y != 0 || v >= nv) return;
-    const long long out = vocabulary_row(a, rows, row);
-    const Old old = old_row(a, out, v);
+    if (threadIdx.x < 2) {
+        const int row = threadIdx.x == 0 ? head : tail;
+        bool last = false;
+        if (threadIdx.x == 0 ? from : to && !(from && head == tail)) {
+            const RowParts r = parts_of(a, row);
+            last = atomicAdd(a.done + (long long)r.first * gridDim.y + blockIdx.y, 1) == r.count - 1;
+        }
+        join[threadIdx.x] = last ? row : -1;
+    }
+    __syncthreads();
+    if (v >= nv || (join[0] < 0 && join[1] < 0)) return;
+    __threadfence();
+#pragma unroll 1
+    for (int w = 0; w < 2; ++w) {
+        if (join[w] < 0) continue;
+        const RowParts r = parts_of(a, join[w]);
+        const long long out = vocabulary_row(a, rows, join[w]);
+        const Old old = old_row(a, out, v);
 #pragma unroll
-    for (int k = 1; k < kJoinParts; ++k)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = add2(s[e], acc[k][e][threadIdx.x]);
-    put_row(a, out, v, s, old);
+        for (int e = 0; e < 4; ++e) s[e] = 0ull;
+#pragma unroll 8
+        for (int c = 0; c < r.count; ++c) {
+            const float4* p = reinterpret_cast<const float4*>(a.part + (2LL * (r.first + c) + (c == 0 ? 1 : 0)) * a.D + 8 * v);
+            const float4 q0 = __ldcg(p), q1 = __ldcg(p + 1);
+            s[0] = add2(s[0], pk2(q0.x, q0.y));
+            s[1] = add2(s[1], pk2(q0.z, q0.w));
+            s[2] = add2(s[2], pk2(q1.x, q1.y));
+            s[3] = add2(s[3], pk2(q1.z, q1.w));
+        }
+        put_row(a, out, v, s, old);
+    }
 }
 
 int lanes_of(int D) { return std::min(256, (D / 8 + 31) / 32 * 32); }
@@ -330,6 +337,7 @@ int embed_owners(int V) {
     while ((long long)n * kSortRows < V) n *= 2;
     return n;
 }
+long long embed_dones(long long T, int D) { return embed_chunks(T) * ((D / 8 + kSumThreads - 1) / kSumThreads); }
 long long embed_chunks(long long T) { return (T + kEmbedChunk - 1) / kEmbedChunk; }
 
 cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s, bool pdl) {
@@ -341,18 +349,13 @@ cudaError_t launch_embedding_sort(const EmbedBwdArgs& a, cudaStream_t s, bool pd
     const cudaError_t e = allow_smem(reinterpret_cast<const void*>(embedding_sort_kernel), kSortWarps * kSortRows * sizeof(int), allowed);
     if (e != cudaSuccess) return e;
     return launch_ex(embedding_sort_kernel, dim3((unsigned)a.owners), dim3(kSortWarps * 32), kSortWarps * rows * sizeof(int), s, pdl, a,
-                     rows);
+                     rows, (int)embed_dones(a.T, a.D));
 }
 cudaError_t launch_embedding_sum(const EmbedBwdArgs& a, cudaStream_t s, bool pdl) {
     const int rows = owner_rows(a), chunks = (int)embed_chunks(a.T), blocks = (a.D / 8 + kSumThreads - 1) / kSumThreads;
     const int zero = a.accumulate ? 0 : std::min((a.owners * rows + 31) / 32, 152 * 8);
     return launch_ex(embedding_sum_kernel, dim3((unsigned)(chunks + zero), (unsigned)blocks), dim3(kSumThreads), 0, s, pdl, a, rows,
                      chunks);
-}
-cudaError_t launch_embedding_join(const EmbedBwdArgs& a, cudaStream_t s, bool pdl) {
-    const int blocks = (a.D / 8 + kSumThreads - 1) / kSumThreads;
-    return launch_ex(embedding_join_kernel, dim3((unsigned)embed_chunks(a.T), (unsigned)blocks), dim3(kSumThreads, kJoinParts), 0, s, pdl, a,
-                     owner_rows(a));
 }
 
 }  // namespace lrs

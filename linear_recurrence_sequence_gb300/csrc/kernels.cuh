@@ -755,12 +755,13 @@ struct EmbedBwdArgs {
     int* count;                  // [1]: of them
     int* first;                  // [owners rows + 1]: each row's first place
     float* part;                 // [2 chunks][D]
+    int* done;                   // [embed_dones]: parts of the row that begins in a chunk that are written
 };
 int embed_owners(int V);
+long long embed_dones(long long T, int D);
 long long embed_chunks(long long T);
 cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_embedding_sort(const EmbedBwdArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_embedding_sum(const EmbedBwdArgs& a, cudaStream_t s, bool pdl);
-cudaError_t launch_embedding_join(const EmbedBwdArgs& a, cudaStream_t s, bool pdl);
 
 }  // namespace lrs

@@ -1589,15 +1589,15 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
 // ---------------------------------------------------------------------------
 namespace {
 
-// Warps an SM that the chunks are to give: what the kernels' registers leave room for.
-constexpr int kSsmFwdWarps = 16, kSsmBwdWarps = 8;
+// Resident per SM, by registers (the backward's main kernel: by tensor memory).
+constexpr int kSsmFwdWarps = 16, kSsmBwdCtas = 2;
 
 int check_ssm_shape(int B, int L, int D, int N) {
     if (B < 1 || L < 1 || D < 1 || N < 1) return LRS_ERR_ARG;
     if (D % 8 != 0 || N > 64 || (long long)B * L > (1LL << 30) || (long long)B * L * D > (1LL << 40) ||
         (long long)B * D * N > (1LL << 40))
         return LRS_ERR_UNSUPPORTED;
-    // CTAs of the launches: a warp's channels and 16 tokens each at least
+    // CTAs of the launches: a warp's channels and 16 tokens each at least, or one of 8
     const SsmSplit w = ssm_split(D, N);
     if ((long long)B * ((L + 15) / 16) * w.groups > 0x7fffffffLL) return LRS_ERR_UNSUPPORTED;
     return LRS_OK;
@@ -1610,14 +1610,24 @@ size_t ssm_keep_bytes(int B, int L, int D, int N) {
 
 // Scratch of a direction: the chunks' states and sums of dt; the backward's partial sums.
 struct SsmScratch {
-    int chunk, nchunk;
+    int chunk, nchunk, main_chunk, main_nchunk, per;
     long long part_len;
     size_t maps, sums, dbc, part, total;
 };
 SsmScratch ssm_scratch(int B, int L, int D, int N, bool backward) {
     SsmScratch s;
     const SsmSplit w = ssm_split(D, N);
-    ssm_chunks(B, L, D, N, backward ? kSsmBwdWarps : kSsmFwdWarps, &s.chunk, &s.nchunk);
+    ssm_chunks(B, L, D, N, backward ? kSsmBwdCtas : kSsmFwdWarps / w.warps, &s.chunk, &s.nchunk);
+    s.main_chunk = s.chunk;
+    s.main_nchunk = s.nchunk;
+    s.per = 1;
+    // The backward's maps have room for twice the warps of its main kernel: by half chunks where there is work for them
+    // (4 x 4096 x 1024: 70 -> 66 us; more chunks are more to go through in a row for the prefix)
+    if (backward && s.nchunk > 1 && s.chunk >= 64 && s.chunk % 16 == 0) {
+        s.per = 2;
+        s.chunk /= 2;
+        s.nchunk = (L + s.chunk - 1) / s.chunk;
+    }
     const size_t chunks = s.nchunk > 1 ? (size_t)B * s.nchunk : 0;
     s.maps = 256;
     s.sums = s.maps + up256(chunks * ssm_tile_bytes(D, N));
@@ -1626,7 +1636,7 @@ SsmScratch ssm_scratch(int B, int L, int D, int N, bool backward) {
     s.part_len = (long long)w.groups * (256 + w.channels / 2);
     if (backward) {
         s.part = s.dbc + up256((size_t)B * L * w.ctas * 2 * (8 * w.lanes) * sizeof(float));
-        s.total = s.part + up256((size_t)B * s.nchunk * s.part_len * sizeof(float4));
+        s.total = s.part + up256((size_t)B * s.main_nchunk * s.part_len * sizeof(float4));
     }
     return s;
 }
@@ -1740,6 +1750,9 @@ int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x,
     SsmBwdArgs g = {};
     g.f = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);
     ssm_place(g.f, l, scratch);
+    g.chunk = l.main_chunk;
+    g.nchunk = l.main_nchunk;
+    g.per = l.per;
     g.f.h0 = dhT;
     g.f.keep = static_cast<float4*>(const_cast<void*>(saved));
     g.dy = static_cast<const uint16_t*>(dy);

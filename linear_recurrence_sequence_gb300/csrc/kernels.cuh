@@ -671,7 +671,7 @@ struct SsmArgs {
     int groups, ngq;             // warps' groups of channels; CTAs that they take
     int words;                   // b and c can be read two states at a time
     int quads, rate_quads;       // [.., D, N] rows four at a time: states, a_log
-    int chunk, nchunk;           // tokens of a chunk (a multiple of 16), chunks
+    int chunk, nchunk;           // tokens of a chunk (a multiple of 8), chunks
     float4* maps;                // [B][nchunk][groups][8][32]
     float* sums;                 // [B][nchunk][groups * channels of a warp]
     uint16_t* y;                 // [B][L][D]
@@ -683,9 +683,10 @@ struct SsmBwdArgs {
     const uint16_t* dy;          // [B][L][D]
     SsmOutRows dx, ddelta, dgate;
     int f32;                     // they and db, dc in FP32
+    int chunk, nchunk, per;      // of the main kernel: `per` of f's chunks each
     void *db, *dc;               // [B][L][N]
     float* dbc;                  // [B L][ngq][2 padded N]
-    float4* part;                // [B nchunk][part_len]
+    float4* part;                // [B nchunk][part_len], the main kernel's chunks
     long long part_len;
     float *da_log, *dd_skip, *ddelta_bias, *dh0;   // the last three may be null
 };
@@ -694,7 +695,7 @@ struct SsmSplit {
     int groups, ctas, warps;     // warps that span D; CTAs of a row, their warps
 };
 SsmSplit ssm_split(int D, int N);
-void ssm_chunks(int B, int L, int D, int N, int warps, int* chunk, int* nchunk);
+void ssm_chunks(int B, int L, int D, int N, int ctas, int* chunk, int* nchunk);
 cudaError_t launch_ssm_maps(const SsmArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_ssm_prefix(const SsmArgs& a, bool reverse, cudaStream_t s, bool pdl);
 cudaError_t launch_ssm_replay(const SsmArgs& a, cudaStream_t s, bool pdl);

@@ -478,14 +478,14 @@ SsmSplit ssm_split(int D, int N) {
     w.warps = (w.groups + w.ctas - 1) / w.ctas;
     return w;
 }
-// As many chunks as give `warps` warps an SM, each of two tiles of 16 tokens at
-// least; one where three would not fit.
-void ssm_chunks(int B, int L, int D, int N, int warps, int* chunk, int* nchunk) {
+// As many chunks as give every SM `ctas` CTAs, of 16 tokens at least; one where
+// three would not fit.
+void ssm_chunks(int B, int L, int D, int N, int ctas, int* chunk, int* nchunk) {
     const SsmSplit w = ssm_split(D, N);
-    const long long most = (long long)kSsmSms * warps / ((long long)B * w.ctas * w.warps);
-    long long n = std::min<long long>(most, (L + 31) / 32);
+    const long long most = (long long)kSsmSms * ctas / ((long long)B * w.ctas);
+    long long n = std::min<long long>(most, (L + 15) / 16);
     if (n < 3) n = 1;
-    *chunk = (int)(((L + n - 1) / n + 15) / 16 * 16);
+    *chunk = (int)(((L + n - 1) / n + 7) / 8 * 8);
     *nchunk = (L + *chunk - 1) / *chunk;
 }
 cudaError_t launch_ssm_maps(const SsmArgs& a, cudaStream_t s, bool pdl) { return fwd(a, 0, s, pdl); }

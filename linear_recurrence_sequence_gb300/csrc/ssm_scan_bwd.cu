@@ -52,6 +52,7 @@ struct BwdPlace {
     int b, chunk, group, warp;
     bool on;
 };
+// chunks: of a row; the first of them is number `first`
 __device__ __forceinline__ BwdPlace bwd_place(const SsmArgs& a, int chunks, int first) {
     BwdPlace p;
     const long long i = blockIdx.x;
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     pdl_wait();
     const SsmArgs& a = g.f;
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
-    const BwdPlace p = bwd_place(a, a.nchunk, 0);
+    const BwdPlace p = bwd_place(a, g.nchunk, 0);
     BwdTile<LN>* tiles = reinterpret_cast<BwdTile<LN>*>(buf);
     BwdTile<LN>& s = tiles[p.warp];
     const uint32_t tmem = s_tmem + ((uint32_t)p.warp << 21);   // the warp's 32 lanes
@@ -395,14 +396,15 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     const bool on = p.on && c0 + c8 < a.D;
     SsmStates A, u, dA;
     load_rates(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
-    const long long slot = ((long long)p.b * a.nchunk + p.chunk) * a.groups + p.group;
+    // the chunk ends where the last of its maps does
+    const long long slot = ((long long)p.b * a.nchunk + min((p.chunk + 1) * g.per, a.nchunk) - 1) * a.groups + p.group;
     if (a.nchunk > 1 && p.on)
         load_tile_state(a.maps + slot * (kSsmVec * 32), lane, u);
     else
         load_state(a.h0, a.quads, p.b, ch, ln * kSsmSt, a.D, a.N, u);   // here h0 is the cotangent of the last state
     clear_states(dA);
     f2x dskip[4] = {0ull, 0ull, 0ull, 0ull}, dbias[4] = {0ull, 0ull, 0ull, 0ull};
-    const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
+    const int begin = p.chunk * g.chunk, end = min(a.L, begin + g.chunk);
     const int last = begin + (end - 1 - begin) / kBT * kBT;
     const long long stride = (long long)a.groups * (kSsmVec * 32);   // of the kept states, a tile back
     const float4* kept = a.keep + ((long long)p.b * ((a.L + kBT - 1) / kBT) + last / kBT) * stride + (long long)p.group * (kSsmVec * 32);
@@ -552,7 +554,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     tmem_fence_after_sync();
     if (threadIdx.x < 32) tmem_dealloc(s_tmem, kBwdTmem);
     if (!p.on) return;
-    const long long part = (long long)p.b * a.nchunk + p.chunk;
+    const long long part = (long long)p.b * g.nchunk + p.chunk;
     // a part: dA [groups][kSsmVec][32] float4, then the two vectors [2][groups CW]
     float4* out = g.part + part * g.part_len;
     store_tile_state(out + (long long)p.group * (kSsmVec * 32), lane, dA);
@@ -608,7 +610,7 @@ __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdArgs g, int
     const long long col = (long long)blockIdx.x * 32 + lane;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (col < g.part_len) {
-        const long long parts = (long long)a.B * a.nchunk;
+        const long long parts = (long long)a.B * g.nchunk;
 #pragma unroll 4
         for (long long i = w; i < parts; i += 8) {
             const float4 q = __ldcg(g.part + i * g.part_len + col);
@@ -663,7 +665,7 @@ cudaError_t bwd_as(const SsmBwdArgs& g, int what, cudaStream_t s, bool pdl) {
     }
     if (what == 1) {
         const size_t smem = w.warps * sizeof(BwdTile<LN>), most = kBwdWarps * sizeof(BwdTile<LN>);
-        const dim3 grid((unsigned)((long long)a.B * a.nchunk * a.ngq));
+        const dim3 grid((unsigned)((long long)a.B * g.nchunk * a.ngq));
         if (a.gate.p != nullptr) {
             static std::atomic<bool> allowed[64];
             const cudaError_t e = allow_smem(reinterpret_cast<const void*>(ssm_bwd_kernel<LN, true>), most, allowed);

@@ -71,7 +71,7 @@ class Model:
     def forward(self, tokens, target):
         """The loss and what the backward needs of each layer."""
         B, L = tokens.shape
-        x = self.params["embed"][tokens]
+        x = api.embedding_forward(tokens, self.params["embed"])["y"]
         first = api.gated_norm_forward(x, gamma_pre=self.params["gamma_in"])
         h, kept = first["h"], []
         for i in range(self.layers):
@@ -106,8 +106,7 @@ class Model:
         x0 = kept[0][0]
         n = api.gated_norm_backward(dx, dh, x0, None, None, None, None, self.params["gamma_in"], first["saved"])
         grads["gamma_in"] = n["dgamma_pre"]
-        grads["embed"] = torch.zeros(self.V, self.D, device=self.device).index_add_(
-            0, tokens.view(-1), n["dx"].view(-1, self.D).float())
+        grads["embed"] = api.embedding_backward(n["dx"], tokens, self.V, grad_fp32=True)["dw"]
         return grads
 
     def train_step(self, tokens, target):

@@ -802,28 +802,41 @@ def _rows(t, name, dtype, device, shape, vector=True):
         raise ValueError(f"{name}: expected device {device}, got {t.device}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    p = t.data_ptr()
+    if t.is_contiguous() and not (vector and p % 16):
+        width = shape[-1]
+        return _Rows(p, shape[1] * width, width) if len(shape) == 3 else _Rows(p, width, 0)
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must be contiguous within a row")
     # the stride of a dimension of one has no meaning
     batch = st[0] if shape[0] > 1 else 0
     token = st[1] if len(shape) == 3 and shape[1] > 1 else 0
-    if vector and (batch % 8 or token % 8 or t.data_ptr() % 16):
+    if vector and (batch % 8 or token % 8 or p % 16):
         raise ValueError(f"{name}: rows must start on 16-byte boundaries (strides that are multiples of 8)")
-    return _Rows(t.data_ptr(), batch, token)
+    return _Rows(p, batch, token)
 
 
-def _out_rows(shape, dtype, device, out, key):
+def _same(t, out, key, shape, dtype, device):
+    """A contiguous output of that shape and type; t: a tensor that may have both (cheaper to allocate by), or None."""
+    if out is not None and out.get(key) is not None:
+        return _need(out[key], key, dtype, device, shape)
+    if t is not None and t.dtype is dtype and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out_rows(t, shape, dtype, device, out, key):
     """An output of rows: (tensor, lrs_rows).  The caller's may have strides between rows that do not overlap."""
     if out is None or out.get(key) is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
-        return t, _Rows(t.data_ptr(), shape[1] * shape[2], shape[2])
-    t = out[key]
-    r = _rows(t, key, dtype, device, shape)
+        o = _same(t, None, key, shape, dtype, device)
+        return o, _Rows(o.data_ptr(), shape[1] * shape[2], shape[2])
+    o = out[key]
+    r = _rows(o, key, dtype, device, shape)
     B, L, width = shape
     if (L > 1 and r.token_stride < width) or (B > 1 and r.batch_stride < (L - 1) * r.token_stride + width):
         raise ValueError(f"{key}: rows overlap")
-    return t, r
+    return o, r
 
 
 def _ref(rows):
@@ -863,8 +876,8 @@ def causal_conv_forward(x, weight, bias=None, state=None, reset=None, *, silu=Tr
     earlier; bias: [D] FP32; state: [B, W - 1, D] BF16, the inputs before x; reset: [B, L] uint8, sequence starts.
     Returns dict(y, state), the state after x in a buffer of its own."""
     dev, B, L, D, W, xr = _conv_inputs(x, weight, bias, state, reset)
-    y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
-    after = _empty((B, W - 1, D), torch.bfloat16, dev, out, "state")
+    y = _same(x, out, "y", x.shape, torch.bfloat16, dev)
+    after = _same(state, out, "state", (B, W - 1, D), torch.bfloat16, dev)
     st = _load().causal_conv_forward(_ref(xr), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), B, L, D, W,
                                      1 if silu else 0, y.data_ptr(), after.data_ptr(), _stream(dev))
     if st:
@@ -887,7 +900,7 @@ def causal_conv_step(x, weight, bias, state, reset=None, *, silu=True, out=None)
     _opt(bias, "bias", torch.float32, dev, (D,))
     _need(state, "state", torch.bfloat16, dev, (B, W - 1, D))
     _opt(reset, "reset", torch.uint8, dev, (B,))
-    y = _empty(shape, torch.bfloat16, dev, out, "y")
+    y = _same(x, out, "y", shape, torch.bfloat16, dev)
     st = _load().causal_conv_step(_ref(xr), weight.data_ptr(), _ptr(bias), state.data_ptr(), _ptr(reset), B, D, W,
                                   1 if silu else 0, y.data_ptr(), _stream(dev))
     if st:
@@ -904,10 +917,9 @@ def causal_conv_backward(dy, x, weight, bias=None, state=None, reset=None, *, si
     dev, B, L, D, W, xr = _conv_inputs(x, weight, bias, state, reset)
     _need(dy, "dy", torch.bfloat16, dev, (B, L, D))
     gdt = torch.float32 if grad_fp32 else torch.bfloat16
-    dx, dxr = _out_rows((B, L, D), gdt, dev, out, "dx")
-    o = {"dx": dx, "dweight": _empty((W, D), torch.float32, dev, out, "dweight"),
-         "dbias": None if bias is None else _empty((D,), torch.float32, dev, out, "dbias"),
-         "dstate": None if state is None else _empty((B, W - 1, D), gdt, dev, out, "dstate")}
+    dx, dxr = _out_rows(dy, dy.shape, gdt, dev, out, "dx")
+    o = {"dx": dx, "dweight": _like(weight, out, "dweight"), "dbias": None if bias is None else _like(bias, out, "dbias"),
+         "dstate": None if state is None else _same(state, out, "dstate", (B, W - 1, D), gdt, dev)}
     scratch = _buffer(scratch, "scratch", causal_conv_workspace_bytes(B, L, D, W), dev)
     st = _load().causal_conv_backward(dy.data_ptr(), _ref(xr), weight.data_ptr(), _ptr(bias), _ptr(state), _ptr(reset), B,
                                       L, D, W, 1 if silu else 0, _ref(dxr), o["dweight"].data_ptr(), _ptr(o["dbias"]),
@@ -963,8 +975,8 @@ def selective_scan_forward(x, delta, a_log, b, c, d_skip=None, delta_bias=None, 
     _opt(h0, "h0", torch.float32, dev, (B, D, N))
     _opt(reset, "reset", torch.uint8, dev, (B, L))
     nsaved, nscratch, _ = selective_scan_workspace_bytes(B, L, D, N)
-    y = _empty((B, L, D), torch.bfloat16, dev, out, "y")
-    hT = _empty((B, D, N), torch.float32, dev, out, "hT")
+    y = _same(delta, out, "y", x.shape, torch.bfloat16, dev)
+    hT = _same(h0, out, "hT", (B, D, N), torch.float32, dev)
     saved = _buffer(saved, "saved", nsaved, dev) if keep else None
     scratch = _buffer(scratch, "scratch", nscratch, dev)
     st = _load().selective_scan_forward(_ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr), _ptr(d_skip),
@@ -982,7 +994,7 @@ def selective_scan_step(x, delta, a_log, b, c, d_skip, delta_bias, gate, state, 
     B = x.shape[0]
     _need(state, "state", torch.float32, dev, (B, D, N))
     _opt(reset, "reset", torch.uint8, dev, (B,))
-    y = _empty((B, D), torch.bfloat16, dev, out, "y")
+    y = _same(delta, out, "y", x.shape, torch.bfloat16, dev)
     st = _load().selective_scan_step(_ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr), _ptr(d_skip),
                                      _ptr(delta_bias), _ref(gr), state.data_ptr(), _ptr(reset), B, D, N, y.data_ptr(),
                                      _stream(dev))
@@ -1007,14 +1019,14 @@ def selective_scan_backward(dy, dhT, x, delta, a_log, b, c, d_skip, delta_bias, 
     _saved(saved, nsaved, dev)
     scratch = _buffer(scratch, "scratch", nscratch, dev)
     gdt, f32 = torch.float32 if grad_fp32 else torch.bfloat16, torch.float32
-    dx, dxr = _out_rows((B, L, D), gdt, dev, out, "dx")
-    dd, ddr = _out_rows((B, L, D), gdt, dev, out, "ddelta")
-    dg, dgr = (None, None) if gate is None else _out_rows((B, L, D), gdt, dev, out, "dgate")
-    o = {"dx": dx, "ddelta": dd, "da_log": _empty((D, N), f32, dev, out, "da_log"),
-         "db": _empty((B, L, N), gdt, dev, out, "db"), "dc": _empty((B, L, N), gdt, dev, out, "dc"),
-         "dd_skip": None if d_skip is None else _empty((D,), f32, dev, out, "dd_skip"),
-         "ddelta_bias": None if delta_bias is None else _empty((D,), f32, dev, out, "ddelta_bias"), "dgate": dg,
-         "dh0": None if h0 is None else _empty((B, D, N), f32, dev, out, "dh0")}
+    shape, states = dy.shape, (B, L, N)
+    dx, dxr = _out_rows(dy, shape, gdt, dev, out, "dx")
+    dd, ddr = _out_rows(dy, shape, gdt, dev, out, "ddelta")
+    dg, dgr = (None, None) if gate is None else _out_rows(dy, shape, gdt, dev, out, "dgate")
+    o = {"dx": dx, "ddelta": dd, "da_log": _like(a_log, out, "da_log"), "db": _same(b, out, "db", states, gdt, dev),
+         "dc": _same(c, out, "dc", states, gdt, dev), "dd_skip": None if d_skip is None else _like(d_skip, out, "dd_skip"),
+         "ddelta_bias": None if delta_bias is None else _like(delta_bias, out, "ddelta_bias"), "dgate": dg,
+         "dh0": None if h0 is None else _same(h0, out, "dh0", (B, D, N), f32, dev)}
     st = _load().selective_scan_backward(dy.data_ptr(), _ptr(dhT), _ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr),
                                          _ptr(d_skip), _ptr(delta_bias), _ref(gr), _ptr(reset), B, L, D, N,
                                          saved.data_ptr(), _ref(dxr), _ref(ddr), o["da_log"].data_ptr(),

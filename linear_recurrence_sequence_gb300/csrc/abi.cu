@@ -1472,9 +1472,10 @@ bool rows_out_ok(const lrs_rows* r, int B, int L, int width) {
     return rows_in_ok(r) && (L == 1 || r->token_stride >= width) &&
            (B == 1 || r->batch_stride >= (long long)(L - 1) * r->token_stride + width);
 }
-// Whether pairs of a row's values are 4-byte words.
-bool rows_in_words(const lrs_rows* r, int width) {
-    return width % 2 == 0 && (reinterpret_cast<uintptr_t>(r->data) & 3u) == 0 && r->batch_stride % 2 == 0 && r->token_stride % 2 == 0;
+// Whether n of a row's values are a word of 2 n bytes, everywhere.
+bool rows_in_words(const lrs_rows* r, int width, int n) {
+    return width % n == 0 && reinterpret_cast<uintptr_t>(r->data) % (2 * n) == 0 && r->batch_stride % n == 0 &&
+           r->token_stride % n == 0;
 }
 SsmRows rows_in(const lrs_rows* r) {
     SsmRows o = {};
@@ -1670,9 +1671,10 @@ SsmArgs ssm_args(const lrs_rows* x, const lrs_rows* delta, const float* a_log, c
     const SsmSplit w = ssm_split(D, N);
     a.groups = w.groups;
     a.ngq = w.ctas;
-    a.words = rows_in_words(b, N) && rows_in_words(c, N);
+    a.words = rows_in_words(b, N, 2) && rows_in_words(c, N, 2);
     a.quads = N % 4 == 0;   // the states are on 16-byte boundaries
     a.rate_quads = a.quads && aligned16(a_log);
+    a.state_words = a.quads && rows_in_words(b, N, 4) && rows_in_words(c, N, 4);
     return a;
 }
 void ssm_place(SsmArgs& a, const SsmScratch& l, void* scratch) {

@@ -671,6 +671,7 @@ struct SsmArgs {
     int groups, ngq;             // warps' groups of channels; CTAs that they take
     int words;                   // b and c can be read two states at a time
     int quads, rate_quads;       // [.., D, N] rows four at a time: states, a_log
+    int state_words;             // states, b and c four at a time
     int chunk, nchunk;           // tokens of a chunk (a multiple of 8), chunks
     float4* maps;                // [B][nchunk][groups][8][32]
     float* sums;                 // [B][nchunk][groups * channels of a warp]

@@ -352,11 +352,14 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
 }
 
 // One token of each of B sequences: LQ lanes share a channel, four states each
-// (16 bytes of the state row), and go through the batch.  Bound by the state,
-// read and written once in FP32.
-constexpr int kStepThreads = 256;
+// (16 bytes of the state row), and go through the batch.  Bound by the state, read
+// and written once in FP32 (256 sequences of 2048 channels and 16 states: 67 MB).
+// Warps enough to hide the loads are worth more than loads in flight a thread (two
+// sequences at a time 18.9 us, four 23.1, one 14.9).
+constexpr int kStepThreads = 256, kStepCtas = 5;
+// VEC: the state, b and c four at a time.
 template <int LQ, bool VEC>
-__global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
+__global__ void __launch_bounds__(kStepThreads, kStepCtas) ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
     pdl_trigger();
     pdl_wait();
     const int n0 = threadIdx.x % LQ * 4, c = blockIdx.x * (kStepThreads / LQ) + threadIdx.x / LQ;
@@ -372,21 +375,30 @@ __global__ void __launch_bounds__(kStepThreads) ssm_step_kernel(const SsmArgs a,
     const float skip = on && a.d_skip != nullptr ? __ldg(a.d_skip + c) : 0.f;
     for (long long b = blockIdx.y; b < a.B; b += gridDim.y) {
         float* ps = state + (b * a.D + c) * a.N + n0;
-        float h[4] = {0.f, 0.f, 0.f, 0.f}, bb[4], cc[4], x = 0.f, raw = 0.f, z = 0.f;
+        const uint16_t *pb = a.b.p + b * a.b.sb + n0, *pc = a.c.p + b * a.c.sb + n0;
+        float h[4] = {0.f, 0.f, 0.f, 0.f}, bb[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f};
+        float x = 0.f, raw = 0.f, z = 0.f;
         if (VEC) {
             if (live[0]) {
                 const float4 v = *reinterpret_cast<const float4*>(ps);
+                const uint2 vb = __ldg(reinterpret_cast<const uint2*>(pb)), vc = __ldg(reinterpret_cast<const uint2*>(pc));
                 h[0] = v.x;
                 h[1] = v.y;
                 h[2] = v.z;
                 h[3] = v.w;
+                up2(bf2x(vb.x), bb[0], bb[1]);
+                up2(bf2x(vb.y), bb[2], bb[3]);
+                up2(bf2x(vc.x), cc[0], cc[1]);
+                up2(bf2x(vc.y), cc[2], cc[3]);
             }
-        }
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!VEC && live[e]) h[e] = ps[e];
-            bb[e] = live[e] ? bf_up(__ldg(a.b.p + b * a.b.sb + n0 + e)) : 0.f;
-            cc[e] = live[e] ? bf_up(__ldg(a.c.p + b * a.c.sb + n0 + e)) : 0.f;
+            for (int e = 0; e < 4; ++e)
+                if (live[e]) {
+                    h[e] = ps[e];
+                    bb[e] = bf_up(__ldg(pb + e));
+                    cc[e] = bf_up(__ldg(pc + e));
+                }
         }
         if (on) {
             x = bf_up(__ldg(a.x.p + b * a.x.sb + c));
@@ -460,10 +472,10 @@ cudaError_t fwd(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
 template <int LQ>
 cudaError_t step_as(const SsmArgs& a, float* state, cudaStream_t s, bool pdl) {
     const int across = (a.D + kStepThreads / LQ - 1) / (kStepThreads / LQ);
-    // eight CTAs an SM hold all their threads; the rest of the batch in turns
-    const int rows = std::max(1, std::min(a.B, std::min(65535, 8 * kSsmSms / across)));
-    const dim3 grid((unsigned)across, (unsigned)rows);
-    if (a.N % 4 == 0) return launch_ex(ssm_step_kernel<LQ, true>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
+    // what the SMs hold at once, the batch in equal turns
+    const int most = std::max(1, std::min(65535, kStepCtas * kSsmSms / across)), turns = (a.B + most - 1) / most;
+    const dim3 grid((unsigned)across, (unsigned)((a.B + turns - 1) / turns));
+    if (a.state_words) return launch_ex(ssm_step_kernel<LQ, true>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
     return launch_ex(ssm_step_kernel<LQ, false>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
 }
 

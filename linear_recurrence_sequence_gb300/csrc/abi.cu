@@ -1618,7 +1618,7 @@ struct SsmScratch {
 SsmScratch ssm_scratch(int B, int L, int D, int N, bool backward) {
     SsmScratch s;
     const SsmSplit w = ssm_split(D, N);
-    ssm_chunks(B, L, D, N, backward ? kSsmBwdCtas : kSsmFwdWarps / w.warps, &s.chunk, &s.nchunk);
+    ssm_chunks(B, L, D, N, backward ? kSsmBwdCtas : kSsmFwdWarps / w.warps, backward ? 2 : 3, &s.chunk, &s.nchunk);
     s.main_chunk = s.chunk;
     s.main_nchunk = s.nchunk;
     s.per = 1;

@@ -9,9 +9,9 @@
 // that reach over chunks are joined from partial sums in their order.
 //   sort   `owners` CTAs, each with the vocabulary rows v = owner (mod owners):
 //          frequent tokens, which lie side by side in most vocabularies, go to
-//          different CTAs.  Each CTA looks through all the tokens twice (8 T bytes
-//          from L2: no histogram or prefix crosses CTAs, one launch), counts its
-//          rows' and all lower owners' tokens, and places its own in order.
+//          different CTAs.  Each CTA looks through all the tokens (8 T bytes from
+//          L2: no histogram or prefix crosses CTAs, one launch), counts its rows'
+//          and all lower owners' tokens, and places its own in order.
 //   sum    a CTA a chunk of 16 sorted places and 1024 columns; the parts of a row
 //          that reaches over chunks are joined, in their order, by whichever of its
 //          CTAs is done last; other CTAs zero the rows without a token.
@@ -64,21 +64,27 @@ __global__ void __launch_bounds__(256) embedding_fwd_kernel(const EmbedArgs a) {
 
 constexpr int kSortWarps = 32;
 constexpr int kSortRows = 1024;     // vocabulary rows of an owner, at most
+constexpr int kSortNotes = 96;      // tokens that a warp notes
 constexpr int kOwners = 128;        // a power of two, as are the owners of larger vocabularies
 constexpr int kEmbedChunk = 16;     // sorted places of a CTA of the sum
 constexpr int kSumThreads = 128;    // of it, 8 columns each
 
-// Tokens t (even, counted from a 16-byte boundary) and t + 1; -1 outside the array.
-__device__ __forceinline__ longlong2 two_tokens(const EmbedBwdArgs& a, long long t) {
-    if (t >= 0 && t + 1 < a.T) return __ldg(reinterpret_cast<const longlong2*>(a.tokens + t));
-    return make_longlong2(t >= 0 ? __ldg(a.tokens + t) : -1, t + 1 < a.T ? __ldg(a.tokens + t + 1) : -1);
+// Tokens t (even, counted from a 16-byte boundary) and t + 1 as {low, high} words; -1 outside the array.
+__device__ __forceinline__ int4 two_tokens(const EmbedBwdArgs& a, long long t) {
+    if (t >= 0 && t + 1 < a.T) return __ldg(reinterpret_cast<const int4*>(a.tokens + t));
+    const int2* p = reinterpret_cast<const int2*>(a.tokens);
+    const int2 none = make_int2(-1, -1), x = t >= 0 && t < a.T ? __ldg(p + t) : none, y = t + 1 < a.T ? __ldg(p + t + 1) : none;
+    return make_int4(x.x, x.y, y.x, y.y);
 }
 
 // A warp takes consecutive tokens, so that a stable sort needs no order between
 // threads: it counts its tokens of each row, a row's counts are added up over the
-// warps, and the warp places its tokens from there on.
+// warps, and the warp places its tokens from there on.  What it finds (one token of
+// 128 is this owner's) it notes, to go through the tokens once; where that is more
+// than it has room for, it looks for them again.
 __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const EmbedBwdArgs a, int rows, int dones) {
     extern __shared__ __align__(16) int count[];   // [kSortWarps][rows], then each warp's next place in a row
+    __shared__ int2 noted[kSortWarps][kSortNotes];
     __shared__ int lower[kSortWarps], sums[kSortWarps], bad;
     pdl_trigger();
     pdl_wait();
@@ -92,20 +98,32 @@ __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const E
     const int odd = (int)(reinterpret_cast<uintptr_t>(a.tokens) >> 3 & 1u);
     const long long all = (long long)a.T + odd, per = (all + kSortWarps * 64 - 1) / (kSortWarps * 64) * 64;
     const long long begin = warp * per, end = min(all, begin + per);
-    int less = 0;
-#pragma unroll 4
-    for (long long t = begin + 2 * lane; t < end; t += 64) {
-        const longlong2 q = two_tokens(a, t - odd);
-        const long long v[2] = {q.x, q.y};
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            if (v[e] >= a.V) bad = 1;
-            if (v[e] < 0 || v[e] >= a.V) continue;
-            const int o = (int)v[e] & (owners - 1);
-            less += o < own;
-            if (o == own) atomicAdd(&mine[(int)v[e] >> shift], 1);
+    const uint32_t V = (uint32_t)a.V, before_me = (1u << lane) - 1u;
+    int less = 0, found = 0;
+    bool past = false;
+#pragma unroll 8
+    for (long long t = begin; t < end; t += 64) {
+        const int4 q = t + 2 * lane < end ? two_tokens(a, t + 2 * lane - odd) : make_int4(-1, -1, -1, -1);
+        const bool in0 = q.y == 0 && (uint32_t)q.x < V, in1 = q.w == 0 && (uint32_t)q.z < V;
+        past |= (q.y >= 0 && !in0) | (q.w >= 0 && !in1);
+        const int o0 = q.x & (owners - 1), o1 = q.z & (owners - 1);
+        less += (in0 && o0 < own) + (in1 && o1 < own);
+        const bool hit0 = in0 && o0 == own, hit1 = in1 && o1 == own;
+        const uint32_t m0 = __ballot_sync(0xffffffffu, hit0), m1 = __ballot_sync(0xffffffffu, hit1);
+        if ((m0 | m1) == 0u) continue;
+        const int at = found + __popc(m0 & before_me) + __popc(m1 & before_me);
+        const int pos = (int)(t - odd) + 2 * lane;
+        if (hit0) {
+            atomicAdd(&mine[q.x >> shift], 1);
+            if (at < kSortNotes) noted[warp][at] = make_int2(pos, q.x >> shift);
         }
+        if (hit1) {
+            atomicAdd(&mine[q.z >> shift], 1);
+            if (at + hit0 < kSortNotes) noted[warp][at + hit0] = make_int2(pos + 1, q.z >> shift);
+        }
+        found += __popc(m0) + __popc(m1);
     }
+    if (past) bad = 1;
     less = __reduce_add_sync(0xffffffffu, less);
     if (lane == 0) lower[warp] = less;
     __syncthreads();
@@ -138,22 +156,29 @@ __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const E
     }
     if (tid == 0 && own == 0) *a.status = bad ? kStatusTarget : 0u;
     __syncthreads();
-#pragma unroll 4
+    if (found <= kSortNotes) {
+        for (int i = 0; i < found; i += 32) {
+            // equal rows in the order of their lanes
+            const bool on = i + lane < found;
+            const int2 e = on ? noted[warp][i + lane] : make_int2(0, -1 - lane);
+            const uint32_t same = __match_any_sync(0xffffffffu, e.y);
+            if (on) a.place[mine[e.y] + __popc(same & before_me)] = make_int2(e.x, own * rows + e.y);
+            __syncwarp();
+            if (on && (same & before_me) == 0u) mine[e.y] += __popc(same);
+            __syncwarp();
+        }
+        return;
+    }
     for (long long t = begin; t < end; t += 64) {
-        const longlong2 q = t + 2 * lane < end ? two_tokens(a, t + 2 * lane - odd) : make_longlong2(-1, -1);
-        const long long v[2] = {q.x, q.y};
-        bool hit[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) hit[e] = v[e] >= 0 && v[e] < a.V && ((int)v[e] & (owners - 1)) == own;
-        // few lanes of a warp find one of this owner's tokens: they place theirs in turn
-        for (uint32_t m = __ballot_sync(0xffffffffu, hit[0] || hit[1]); m != 0u; m &= m - 1u) {
+        const int4 q = t + 2 * lane < end ? two_tokens(a, t + 2 * lane - odd) : make_int4(-1, -1, -1, -1);
+        const bool hit0 = q.y == 0 && (uint32_t)q.x < V && (q.x & (owners - 1)) == own;
+        const bool hit1 = q.w == 0 && (uint32_t)q.z < V && (q.z & (owners - 1)) == own;
+        // the lanes that find one place theirs in turn
+        for (uint32_t m = __ballot_sync(0xffffffffu, hit0 || hit1); m != 0u; m &= m - 1u) {
             if (lane == __ffs(m) - 1) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (hit[e]) {
-                        const int row = (int)v[e] >> shift;
-                        a.place[mine[row]++] = make_int2((int)(t + 2 * lane + e - odd), own * rows + row);
-                    }
+                const int pos = (int)(t - odd) + 2 * lane;
+                if (hit0) a.place[mine[q.x >> shift]++] = make_int2(pos, own * rows + (q.x >> shift));
+                if (hit1) a.place[mine[q.z >> shift]++] = make_int2(pos + 1, own * rows + (q.z >> shift));
             }
             __syncwarp();
         }
@@ -214,7 +239,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedB
     __shared__ int join[2];
     pdl_trigger();
     pdl_wait();
-    const int nv = a.D / 8, v = blockIdx.y * kSumThreads + threadIdx.x;
+    const int nv = a.D / 8, v = blockIdx.y * blockDim.x + threadIdx.x;
     if ((int)blockIdx.x >= chunks) {
         // 32 rows looked up at a time, then written
         const f2x none[4] = {0ull, 0ull, 0ull, 0ull};
@@ -354,8 +379,9 @@ cudaError_t launch_embedding_sort(const EmbedBwdArgs& a, cudaStream_t s, bool pd
 cudaError_t launch_embedding_sum(const EmbedBwdArgs& a, cudaStream_t s, bool pdl) {
     const int rows = owner_rows(a), chunks = (int)embed_chunks(a.T), blocks = (a.D / 8 + kSumThreads - 1) / kSumThreads;
     const int zero = a.accumulate ? 0 : std::min((a.owners * rows + 31) / 32, 152 * 8);
-    return launch_ex(embedding_sum_kernel, dim3((unsigned)(chunks + zero), (unsigned)blocks), dim3(kSumThreads), 0, s, pdl, a, rows,
-                     chunks);
+    const int threads = std::min(kSumThreads, lanes_of(a.D));
+    return launch_ex(embedding_sum_kernel, dim3((unsigned)(chunks + zero), (unsigned)blocks), dim3((unsigned)threads), 0, s, pdl, a,
+                     rows, chunks);
 }
 
 }  // namespace lrs

@@ -696,7 +696,7 @@ struct SsmSplit {
     int groups, ctas, warps;     // warps that span D; CTAs of a row, their warps
 };
 SsmSplit ssm_split(int D, int N);
-void ssm_chunks(int B, int L, int D, int N, int ctas, int* chunk, int* nchunk);
+void ssm_chunks(int B, int L, int D, int N, int ctas, int fewest, int* chunk, int* nchunk);
 cudaError_t launch_ssm_maps(const SsmArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_ssm_prefix(const SsmArgs& a, bool reverse, cudaStream_t s, bool pdl);
 cudaError_t launch_ssm_replay(const SsmArgs& a, cudaStream_t s, bool pdl);

@@ -23,6 +23,7 @@
 // the lanes that share a channel read them; the next tokens' rows are copied
 // meanwhile.  No barrier between warps.
 #include <algorithm>
+#include <cmath>
 
 #include "ssm.cuh"
 
@@ -472,8 +473,19 @@ cudaError_t fwd(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
 template <int LQ>
 cudaError_t step_as(const SsmArgs& a, float* state, cudaStream_t s, bool pdl) {
     const int across = (a.D + kStepThreads / LQ - 1) / (kStepThreads / LQ);
-    // what the SMs hold at once, the batch in equal turns
-    const int most = std::max(1, std::min(65535, kStepCtas * kSsmSms / across)), turns = (a.B + most - 1) / most;
+    // what the SMs hold at once (or, where that leaves many places empty, a few times over), the batch in equal turns
+    const int places = kStepCtas * kSsmSms;
+    int most = 1;
+    double best = 0.0;
+    for (int waves = 1; waves <= 4; ++waves) {
+        const int n = std::max(1, std::min(65535, places * waves / across));
+        const double used = (double)across * n / ((double)places * waves) - 0.1 * (waves - 1);
+        if (used > best) {
+            best = used;
+            most = n;
+        }
+    }
+    const int turns = (a.B + most - 1) / most;
     const dim3 grid((unsigned)across, (unsigned)((a.B + turns - 1) / turns));
     if (a.state_words) return launch_ex(ssm_step_kernel<LQ, true>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
     return launch_ex(ssm_step_kernel<LQ, false>, grid, dim3(kStepThreads), 0, s, pdl, a, state);
@@ -491,12 +503,16 @@ SsmSplit ssm_split(int D, int N) {
     return w;
 }
 // As many chunks as give every SM `ctas` CTAs, of 16 tokens at least; one where
-// three would not fit.
-void ssm_chunks(int B, int L, int D, int N, int ctas, int* chunk, int* nchunk) {
+// `fewest` would not fit (the maps cost more than they bring).  Not more than
+// sqrt(2.5 L): a warp alone takes about 0.3 us for a token of its chunk (maps and
+// replay), the prefix 0.12 us for a chunk (1 x 32768 x 8 with 16 states: 2048 chunks
+// 247 us, 282 of them 102).
+void ssm_chunks(int B, int L, int D, int N, int ctas, int fewest, int* chunk, int* nchunk) {
     const SsmSplit w = ssm_split(D, N);
     const long long most = (long long)kSsmSms * ctas / ((long long)B * w.ctas);
     long long n = std::min<long long>(most, (L + 15) / 16);
-    if (n < 3) n = 1;
+    n = std::min<long long>(n, std::max(1LL, (long long)std::sqrt(2.5 * L)));
+    if (n < fewest) n = 1;
     *chunk = (int)(((L + n - 1) / n + 7) / 8 * 8);
     *nchunk = (L + *chunk - 1) / *chunk;
 }

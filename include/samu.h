@@ -616,7 +616,9 @@ int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, co
  * projection's output need not be copied out.  Strides in elements.  Where an
  * entry reads rows 16 bytes at a time (all but b and c of the scan), data is
  * 16-byte aligned and both strides are multiples of 8; an input's strides may be
- * 0 (one row for all), an output's rows must not overlap. */
+ * 0 (one row for all), an output's rows must not overlap.  The outputs of the
+ * entries below overlap neither each other nor an input, but where an entry says so;
+ * outputs of rows that begin where an input or another of them does are refused. */
 typedef struct {
     void* data;
     int64_t batch_stride, token_stride;
@@ -650,13 +652,13 @@ int causal_conv_workspace_bytes(int B, int L, int D, int W, size_t* backward_byt
  * Rows padded on the left, with a reset at the first token, give every sequence its
  * own state_out.
  * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a shape below 1, state_out
- * equal to state), LRS_ERR_UNSUPPORTED (D not a multiple of 8, W not 2 to 4, over
+ * equal to state, y to x), LRS_ERR_UNSUPPORTED (D not a multiple of 8, W not 2 to 4, over
  * 2^30 tokens or 2^40 values), LRS_ERR_CUDA. */
 int causal_conv_forward(const lrs_rows* x, const float* weight, const float* bias, const void* state,
                         const uint8_t* reset, int B, int L, int D, int W, int silu, void* y, void* state_out,
                         cudaStream_t stream);
 
-/* One token of each of B sequences: x is [B] rows (token_stride is not used),
+/* One token of each of B sequences: x is [B] rows (token_stride: 0),
  * reset [B], y [B,D]; the state moves on in place.  Bit for bit what the forward
  * gives for the same inputs.  Errors: as the forward. */
 int causal_conv_step(const lrs_rows* x, const float* weight, const float* bias, void* state, const uint8_t* reset,
@@ -669,7 +671,7 @@ int causal_conv_step(const lrs_rows* x, const float* weight, const float* bias, 
  *   dweight  [W,D] FP32 (out);  dbias [D] FP32 (out) or NULL
  *   scratch  causal_conv_workspace_bytes() bytes
  * Sums in a fixed order.  Errors: as the forward, plus LRS_ERR_ARG for dstate
- * without state and for an unknown grad_dtype. */
+ * without state, for dx equal to dy or x and for an unknown grad_dtype. */
 int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight, const float* bias, const void* state,
                          const uint8_t* reset, int B, int L, int D, int W, int silu, const lrs_rows* dx, float* dweight,
                          float* dbias, void* dstate, int grad_dtype, void* scratch, cudaStream_t stream);
@@ -684,9 +686,9 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
  *   h_tn  = a_tn h_{t-1,n} + dt_t x_t b_tn    (a_tn = 0 where reset[b,t] != 0)
  *   y_t   = (sum_n c_tn h_tn + d_skip x_t) SiLU(gate_t).
  * dt, x, gate and d_skip are a channel's own, b and c are shared by a token's
- * channels.  A token whose delta is -inf has dt = 0: it leaves the state as it is
- * (padding behind a sequence; padding ahead of one is cut off by a reset at its
- * first token).  D channels, N from 1 to 64.
+ * channels.  A token whose delta is -inf and whose x and b are finite has dt = 0: it
+ * leaves the state as it is (padding behind a sequence; padding ahead of one is cut
+ * off by a reset at its first token, whatever it holds).  D channels, N from 1 to 64.
  * FP32 arithmetic: exponentials by the GPU's fast one (2^-22 relative each), dt within
  * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0); y is rounded
  * to BF16 once.  Everything runs in a fixed order.
@@ -712,16 +714,16 @@ int selective_scan_workspace_bytes(int B, int L, int D, int N, size_t* saved_byt
  *               backward follows
  *   scratch     .forward bytes
  * One launch, or three where batch and channels alone leave the GPU short of work.
- * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a shape below 1),
- * LRS_ERR_UNSUPPORTED (D not a multiple of 8, N over 64, over 2^30 tokens or 2^40
- * values or states), LRS_ERR_CUDA. */
+ * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a token_stride over 2^26,
+ * a shape below 1, y where x, delta or gate begins), LRS_ERR_UNSUPPORTED (D not a
+ * multiple of 8, N over 64, over 2^30 tokens or 2^40 values or states), LRS_ERR_CUDA. */
 int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
                            const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
                            const float* h0, const uint8_t* reset, int B, int L, int D, int N, void* y, float* hT,
                            void* saved, void* scratch, cudaStream_t stream);
 
-/* One token of each of B sequences: x, delta, b, c, gate are [B] rows (token_stride
- * is not used), reset [B], y [B,D] BF16 (out); state [B,D,N] FP32 moves on in place.
+/* One token of each of B sequences: x, delta, b, c, gate are [B] rows (token_stride:
+ * 0), reset [B], y [B,D] BF16 (out); state [B,D,N] FP32 moves on in place.
  * One launch.  Errors: as the forward. */
 int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
                         const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
@@ -734,10 +736,10 @@ int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a
  *            grad_dtype.  dgate is NULL without a gate.
  *   da_log   [D,N] FP32 (out)
  *   dd_skip, ddelta_bias  [D] FP32 (out) or NULL (and NULL without the vector)
- *   dh0      [B,D,N] FP32 (out) or NULL
+ *   dh0      [B,D,N] FP32 (out; may be dhT) or NULL
  *   scratch  selective_scan_workspace_bytes().backward bytes
- * Errors: as the forward, plus LRS_ERR_ARG for an output without its input and for an
- * unknown grad_dtype. */
+ * Errors: as the forward, plus LRS_ERR_ARG for an output without its input, for one
+ * that begins where an input or another begins and for an unknown grad_dtype. */
 int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x, const lrs_rows* delta,
                             const float* a_log, const lrs_rows* b, const lrs_rows* c, const float* d_skip,
                             const float* delta_bias, const lrs_rows* gate, const uint8_t* reset, int B, int L, int D,

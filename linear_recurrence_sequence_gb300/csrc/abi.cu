@@ -1,6 +1,7 @@
 // extern "C" entry points declared in include/samu.h: argument checks,
 // workspace carving and kernel launches.  No allocation, no synchronisation
 // (except lrs_device_status, which documents that it synchronises).
+#include <initializer_list>
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -1477,6 +1478,14 @@ bool rows_in_words(const lrs_rows* r, int width, int n) {
     return width % n == 0 && reinterpret_cast<uintptr_t>(r->data) % (2 * n) == 0 && r->batch_stride % n == 0 &&
            r->token_stride % n == 0;
 }
+// Whether no two of these begin at the same place (NULL: not there).
+bool apart(std::initializer_list<const void*> list) {
+    for (auto i = list.begin(); i != list.end(); ++i)
+        for (auto j = list.begin(); j != i; ++j)
+            if (*i != nullptr && *i == *j) return false;
+    return true;
+}
+const void* data_of(const lrs_rows* r) { return r == nullptr ? nullptr : r->data; }
 SsmRows rows_in(const lrs_rows* r) {
     SsmRows o = {};
     if (r != nullptr) o = {static_cast<const uint16_t*>(r->data), r->batch_stride, r->token_stride};
@@ -1538,7 +1547,7 @@ int causal_conv_forward(const lrs_rows* x, const float* weight, const float* bia
     const int st = check_conv_shape(B, L, D, W);
     if (st != LRS_OK) return st;
     if (!rows_in_ok(x) || !req(weight) || !opt(bias) || !opt(state) || !req(y) || !opt(state_out) ||
-        (state != nullptr && state_out == state))
+        (state != nullptr && state_out == state) || y == x->data)
         return LRS_ERR_ARG;
     ConvArgs a = conv_args(x, weight, bias, state, reset, B, L, D, W, silu);
     a.y = static_cast<uint16_t*>(y);
@@ -1566,7 +1575,7 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
     if (st != LRS_OK) return st;
     if (!req(dy) || !rows_in_ok(x) || !req(weight) || !opt(bias) || !opt(state) || !rows_out_ok(dx, B, L, D) ||
         !req(dweight) || !opt(dbias) || !opt(dstate) || (state == nullptr && dstate != nullptr) || !req(scratch) ||
-        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32))
+        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) || dx->data == dy || dx->data == x->data)
         return LRS_ERR_ARG;
     ConvBwdArgs g = {};
     g.f = conv_args(x, weight, bias, state, reset, B, L, D, W, silu);
@@ -1705,7 +1714,7 @@ int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float
     const int st = check_ssm_shape(B, L, D, N);
     if (st != LRS_OK) return st;
     if (!ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !opt(h0) || !req(y) || !req(hT) ||
-        !opt(saved) || !req(scratch))
+        !opt(saved) || !req(scratch) || y == x->data || y == delta->data || y == data_of(gate))
         return LRS_ERR_ARG;
     SsmArgs a = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);
     ssm_place(a, ssm_scratch(B, L, D, N, false), scratch);
@@ -1748,6 +1757,10 @@ int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x,
         (gate != nullptr ? !rows_out_ok(dgate, B, L, D) : dgate != nullptr) || !opt(dh0) || !req(scratch) ||
         (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32))
         return LRS_ERR_ARG;
+    // (the inputs among themselves may lie where they like)
+    for (const void* in : {dy, (const void*)x->data, (const void*)delta->data, (const void*)b->data, (const void*)c->data,
+                           data_of(gate)})
+        if (!apart({in, dx->data, ddelta->data, data_of(dgate), db, dc})) return LRS_ERR_ARG;
     const SsmScratch l = ssm_scratch(B, L, D, N, true);
     SsmBwdArgs g = {};
     g.f = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);

@@ -85,6 +85,18 @@ def test_gradient(T, V, D, kind):
         _check_dw(dw, dy, tokens, V, 1.5, old)
 
 
+@pytest.mark.parametrize("T,V", [(1, 3), (2, 3), (63, 40), (9000, 129), (9001, 129), (20001, 5000)])
+@pytest.mark.parametrize("kind", ["uniform", "one", "mixed"])
+def test_tokens_on_any_word(T, V, kind):
+    gen = _gen(T)
+    tokens = torch.cat([torch.full((1,), V, device=DEV), _tokens(gen, T, V, kind)])[1:]   # 8 bytes past a boundary of 16
+    dy = _randn(gen, T, 72, dtype=BF)
+    g = api.embedding_backward(dy, tokens, V, grad_fp32=True)
+    _check_dw(g["dw"], dy, tokens, V, 1.0)
+    assert api.device_status(g["scratch"]) == 0
+    assert torch.equal(g["dw"], api.embedding_backward(dy, tokens.clone(), V, grad_fp32=True)["dw"])
+
+
 def test_many_occurrences():
     """A token that fills thousands of runs; an owner with more tokens than shared memory holds."""
     gen = _gen(3)

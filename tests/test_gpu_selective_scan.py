@@ -57,6 +57,15 @@ def test_matches_the_definition(B, L, D, N, fp32):
         assert got[k].dtype == (torch.float32 if fp32 else BF)
 
 
+@pytest.mark.parametrize("B,L,D,N", [(8, 2390, 8, 5), (8, 2432, 40, 16), (8, 2390, 16, 64), (19, 1024, 256, 16)])
+@pytest.mark.parametrize("resets", [0.0, 0.002])
+def test_chunks_of_several_tiles(B, L, D, N, resets):
+    """Chunks of 64 tokens, whose reverse maps are those of their halves; at 2390 tokens the last chunk has one half."""
+    i, dy, dhT = _inputs(B, L, D, N, seed=N, resets=resets)
+    i["delta_bias"] = i["delta_bias"] - 2.0   # states that reach over several chunks
+    ref.check(_run(i, dy, dhT), ref.scan(**i, dy=dy, dhT=dhT))
+
+
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("skip,bias", [(False, True), (True, False), (False, False)])
 @pytest.mark.parametrize("h0", [False, True])

@@ -52,17 +52,19 @@ def test_causal_conv_shapes(lib, B, L, D, W, expect):
 def test_causal_conv_bad_arguments(lib):
     # x, weight, bias, state, reset, B, L, D, W, silu, y, state_out, stream
     Q = ctypes.c_void_p(AT + 4096)
-    fwd = [R(), P, P, P, P, 2, 8, 64, 4, 1, P, Q, None]
+    fwd = [R(), P, P, P, P, 2, 8, 64, 4, 1, Q, Q, None]
     _refused(lib.causal_conv_forward, fwd, [
         (0, None), (0, R(data=None)), (0, R(data=AT + 2)), (0, R(batch=-8)), (0, R(token=-8)), (0, R(batch=4)),
-        (0, R(token=68)), (1, None), (1, ODD), (2, ODD), (3, ODD), (6, 0), (10, None), (10, ODD), (11, ODD), (11, P)])
+        (0, R(token=68)), (1, None), (1, ODD), (2, ODD), (3, ODD), (6, 0), (10, None), (10, ODD), (10, P), (11, ODD), (11, P)])
     # x, weight, bias, state, reset, B, D, W, silu, y, stream
     step = [R(), P, P, P, P, 2, 64, 4, 1, P, None]
     _refused(lib.causal_conv_step, step, [(0, None), (0, R(batch=12)), (1, None), (2, ODD), (3, None), (3, ODD), (9, None)])
     # dy, x, weight, bias, state, reset, B, L, D, W, silu, dx, dweight, dbias, dstate, grad_dtype, scratch, stream
-    bwd = [P, R(), P, P, P, P, 2, 8, 64, 4, 1, R(), P, P, P, 0, P, None]
+    bwd = [P, R(data=AT + 64), P, P, P, P, 2, 8, 64, 4, 1, R(data=AT + 4096), P, P, P, 0, P, None]
+    out = dict(data=AT + 4096)
     _refused(lib.causal_conv_backward, bwd, [
-        (0, None), (1, None), (2, None), (4, None), (11, None), (11, R(token=56)), (11, R(batch=8 * 64 - 8)), (11, R(batch=0)),
+        (0, None), (1, None), (2, None), (4, None), (11, None), (11, R(token=56, **out)), (11, R(batch=8 * 64 - 8, **out)),
+        (11, R(batch=0, **out)), (11, R()), (11, R(data=AT + 64)),   # (at dy, at x)
         (12, None), (13, ODD), (14, ODD), (15, 2), (16, None)])   # (4: a gradient of a state that is not there)
 
 
@@ -86,16 +88,25 @@ def test_selective_scan_bad_arguments(lib):
     ins = [R(), R(), P, S, S, P, P, R()]
     rows = [(0, None), (0, R(data=AT + 2)), (1, None), (1, R(token=4)), (2, None), (3, None), (3, R(data=AT + 1)),
             (3, R(token=-1)), (4, None), (4, R(batch=-1)), (5, ODD), (6, ODD), (7, R(batch=2))]
-    fwd = ins + [P, P, 2, 8, 64, 16, P, P, P, P, None]
-    _refused(lib.selective_scan_forward, fwd, rows + [(8, ODD), (13, 0), (14, None), (15, None), (15, ODD), (16, ODD), (17, None)])
+    rows += [(i, R(token=(1 << 26) + 8)) for i in (0, 1, 3, 4, 7)]
+    outs = [AT + 4096 * i for i in range(1, 7)]
+    o = [ctypes.c_void_p(v) for v in outs]
+    fwd = ins + [P, P, 2, 8, 64, 16, o[0], P, P, P, None]
+    _refused(lib.selective_scan_forward, fwd, rows + [(8, ODD), (13, 0), (14, None), (14, P), (15, None), (15, ODD), (16, ODD),
+                                                      (17, None)])
     # .., state, reset, B, D, N, y, stream
     step = ins + [P, P, 2, 64, 16, P, None]
     _refused(lib.selective_scan_step, step, rows + [(8, None), (8, ODD), (13, None)])
     # dy, dhT, .., reset, B, L, D, N, saved, dx, ddelta, da_log, db, dc, dd_skip, ddelta_bias, dgate, dh0, grad_dtype, scratch
-    bwd = [P, P] + ins + [P, 2, 8, 64, 16, P, R(), R(), P, P, P, P, P, R(), P, 1, P, None]
+    dx, dd, dg = (R(data=v) for v in outs[:3])
+    bwd = [P, P] + ins + [P, 2, 8, 64, 16, P, dx, dd, P, o[3], o[4], P, P, dg, P, 1, P, None]
     _refused(lib.selective_scan_backward, bwd, [(i + 2, v) for i, v in rows if not (i in (5, 6) and v is None)] + [
-        (0, None), (0, ODD), (1, ODD), (15, None), (16, None), (16, R(token=32)), (17, None), (17, R(batch=0)), (18, None),
-        (19, None), (20, ODD), (21, ODD), (22, ODD), (23, None), (23, R(token=0)), (24, ODD), (25, 7), (26, None)])
+        (0, None), (0, ODD), (1, ODD), (15, None), (16, None), (16, R(data=outs[0], token=32)), (17, None),
+        (17, R(data=outs[1], batch=0)), (18, None), (19, None), (20, ODD), (21, ODD), (22, ODD), (23, None),
+        (23, R(data=outs[2], token=0)), (24, ODD), (25, 7), (26, None)])
+    # two outputs at one place, an output at an input
+    _refused(lib.selective_scan_backward, bwd, [(16, dd), (17, dg), (23, dx), (19, o[0]), (20, o[3]), (16, R()), (17, R()),
+                                                (23, R()), (19, P), (20, P)])
     for gone in (7, 8, 9):   # an output whose input is not there
         a = list(bwd)
         a[gone] = None

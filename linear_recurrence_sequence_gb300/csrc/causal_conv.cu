@@ -7,12 +7,16 @@
 //   y_t   = SiLU(pre_t), or pre_t
 //   dpre  = dy SiLU'(pre),  dx_t = sum_j w_j dpre_(t+j),  dw_j = sum_t dpre_t x_(t-j)
 //
-// Bound by bandwidth: 4 bytes a value forward, 6 backward.  A thread walks along
-// time through a run of tokens of 4 channels, the last W inputs in
-// registers, and asks for 8 rows at a time.  The backward
-// forms pre again (x is read anyway, pre is not kept) and keeps the sums of the
-// dx of the last W tokens.  Runs are up to 64 tokens long (W - 1 rows before a run,
-// and backward W - 1 tokens after it, are gone through twice).
+// 4 bytes a value forward, 6 backward.  A thread walks along time through a run of
+// tokens of 4 channels, the last W inputs in registers, and asks for 8 rows at a
+// time, forward for the next 8 while it computes these.  The backward forms pre
+// again (x is read anyway, pre is not kept) and keeps the sums of the dx of the last
+// W tokens.  A run's first W - 1 rows, and backward the W - 1 after it, are gone
+// through twice.
+//   16 x 4096 x 1024, W = 4: forward 51 us, 5.2 TB/s (0.77 of a copy's measured 6.8);
+//   backward 113 us, 3.6 TB/s: about 25 instructions a value, bound by their issue.
+//   4 x 4096 x 1024: 17 and 33 us, of which the launches' start and end are 3 us each.
+// With 2 channels a thread (twice the warps) 4 x 4096 x 1024 took 23 and 39 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -24,14 +28,30 @@ namespace {
 
 constexpr int kConvStep = 8;      // rows that a thread asks for at a time
 constexpr int kConvWarps = 4;     // runs of a CTA
-constexpr int kConvPairs = 2;   // of channels, a thread
+constexpr int kConvPairs = 2;     // of channels, a thread
+constexpr int kConvRun = 80;       // tokens of a run at most
 constexpr int kConvSms = 152;
+constexpr int kConvFwdCtas = 5, kConvBwdCtas = 4;   // resident per SM, by registers
 
-// A run's tokens: as long as leaves 12 warps an SM (4 x 4096 x 1024 forward + backward 64: 52 us, 32: 53, 16: 60).
-int conv_run(int B, int L, int D) {
-    for (int run = 64; run > kConvStep; run /= 2)
-        if ((long long)B * ((L + run - 1) / run) * ((D + 64 * kConvPairs - 1) / (64 * kConvPairs)) >= 12 * kConvSms) return run;
-    return kConvStep;
+// A launch's CTAs: runs of a batch row by spans of channels.
+long long conv_tiles(int B, int L, int run) { return (long long)B * (((long long)L + run * kConvWarps - 1) / (run * kConvWarps)); }
+long long conv_spans(int D) { return (D + 64 * kConvPairs - 1) / (64 * kConvPairs); }
+// A run's tokens: those that end soonest, by the rounds that the SMs take with `ctas` CTAs each and a run's own cost, about
+// a step (1 x 8192 x 2560: 72 tokens, one round, 39 us backward, 64 tokens 49; 16 x 4096 x 1024: 64 tokens 51 us forward, 80
+// tokens 55).  kConvRun at most: what the words of Starts cover.
+int conv_run(int B, int L, int D, int ctas) {
+    const long long places = (long long)ctas * kConvSms;
+    int best = kConvStep;
+    long long least = -1;
+    for (int run = kConvStep; run <= kConvRun; run += kConvStep) {
+        const long long n = conv_tiles(B, L, run) * conv_spans(D);
+        const long long cost = (n + places - 1) / places * (run + kConvStep);
+        if (least < 0 || cost < least) {
+            least = cost;
+            best = run;
+        }
+    }
+    return best;
 }
 
 // P pairs of channels of a row: BF16 words, FP32 pairs.
@@ -96,15 +116,32 @@ __device__ __forceinline__ void shift_in(f2x (&v)[W][P]) {
 #pragma unroll
         for (int e = 0; e < P; ++e) v[j][e] = v[j - 1][e];
 }
-// The starts of tokens t .. t + n - 1 of a row as bits, the last token's lowest (the order in which a
-// history shifts them in); none outside the row.
-template <int n>
-__device__ __forceinline__ uint32_t starts_of(const uint8_t* reset, long long row, int t, int L) {
-    uint32_t st = 0u;
-    if (reset != nullptr)
+// The starts of a run's tokens and of those around it, as bits of three words: bit 0 is the token 8 before the step that
+// the thread is at.  All of the run's are asked for at once (a step's own, asked for with its rows, would be waited for).
+struct Starts {
+    uint32_t m[3];
+};
+// (by a whole warp; none outside the row)
+__device__ __forceinline__ Starts starts_of(const uint8_t* reset, long long row, int t0, int L, int lane) {
+    Starts s = {{0u, 0u, 0u}};
+    if (reset == nullptr) return s;
+    bool on[3];
 #pragma unroll
-        for (int i = 0; i < n; ++i) st = st << 1 | (t + i >= 0 && t + i < L && __ldg(reset + row + t + i) != 0 ? 1u : 0u);
-    return st;
+    for (int k = 0; k < 3; ++k) {
+        const int t = t0 - 8 + 32 * k + lane;
+        on[k] = t >= 0 && t < L && __ldg(reset + row + t) != 0;
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s.m[k] = __ballot_sync(0xffffffffu, on[k]);
+    return s;
+}
+// The starts of a step's tokens and the H before, the last token's lowest; moves on by a step.
+template <int H>
+__device__ __forceinline__ uint32_t next_starts(Starts& s) {
+    const uint32_t history = __brev(s.m[0]) >> 16 & ((1u << (kConvStep + H)) - 1u);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) s.m[k] = __funnelshift_r(s.m[k], k < 2 ? s.m[k < 2 ? k + 1 : 2] : 0u, kConvStep);
+    return history;
 }
 // Whether tap j is inside its sequence: no start at the last j tokens of the history.
 __device__ __forceinline__ bool tap_live(uint32_t history, int j) { return (history & ((1u << j) - 1u)) == 0u; }
@@ -173,11 +210,13 @@ __device__ __forceinline__ void conv_group(const Words<P> (&q)[kConvStep], int n
 }
 
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps, 6) causal_conv_fwd_kernel(const ConvArgs a, int run) {
+__global__ void __launch_bounds__(32 * kConvWarps, kConvFwdCtas) causal_conv_fwd_kernel(const ConvArgs a, int run) {
     constexpr int H = W - 1, P = kConvPairs;
     pdl_trigger();
     pdl_wait();
     const ConvPlace p = conv_place(a, run, 64 * P);
+    const long long row = (long long)p.b * a.L;
+    Starts starts = starts_of(a.reset, row, p.t0, a.L, threadIdx.x & 31);
     if (!p.on) return;
     f2x w[W][P], bias[P], v[W][P];
     clear(bias);
@@ -186,16 +225,21 @@ __global__ void __launch_bounds__(32 * kConvWarps, 6) causal_conv_fwd_kernel(con
     if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
     for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
-    const long long row = (long long)p.b * a.L;
-    uint32_t history = starts_of<H>(a.reset, row, p.t0 - H, a.L);
     const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
     uint16_t* py = a.y + (row + p.t0) * a.D + p.c;
-    for (int t = p.t0; t < p.end; t += kConvStep, px += kConvStep * a.x.st, py += (long long)kConvStep * a.D) {
+    Words<P> next[kConvStep];
+#pragma unroll
+    for (int r = 0; r < kConvStep; ++r) next[r] = r < p.end - p.t0 ? load_words<P>(px + r * a.x.st) : no_words<P>();
+    for (int t = p.t0; t < p.end; t += kConvStep, py += (long long)kConvStep * a.D) {
         const int n = p.end - t;
         Words<P> q[kConvStep];
+        px += kConvStep * a.x.st;
 #pragma unroll
-        for (int r = 0; r < kConvStep; ++r) q[r] = r < n ? load_words<P>(px + r * a.x.st) : no_words<P>();
-        history = (history & ((1u << H) - 1u)) << kConvStep | starts_of<kConvStep>(a.reset, row, t, a.L);
+        for (int r = 0; r < kConvStep; ++r) {
+            q[r] = next[r];
+            next[r] = r + kConvStep < n ? load_words<P>(px + r * a.x.st) : no_words<P>();
+        }
+        const uint32_t history = next_starts<H>(starts);
         if (n >= kConvStep && history == 0u)
             conv_group<W, P, SILU, true>(q, n, 0u, w, bias, v, py, a.D);
         else
@@ -203,7 +247,11 @@ __global__ void __launch_bounds__(32 * kConvWarps, 6) causal_conv_fwd_kernel(con
     }
     // the row's last inputs, as far as they belong to its last sequence
     if (a.state_out != nullptr && p.end == a.L) {
-        history = starts_of<H>(a.reset, row, a.L - H, a.L);
+        uint32_t history = 0u;
+        if (a.reset != nullptr)
+#pragma unroll
+            for (int k = 0; k < H; ++k)
+                if (a.L > k && __ldg(a.reset + row + a.L - 1 - k) != 0) history |= 1u << k;
 #pragma unroll
         for (int k = 0; k < H; ++k)   // the input k tokens before the last
             store_words(a.state_out + ((long long)p.b * H + H - 1 - k) * a.D + p.c,
@@ -329,7 +377,7 @@ __device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const Conv
 }
 
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps, 4) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
+__global__ void __launch_bounds__(32 * kConvWarps, kConvBwdCtas) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
     constexpr int H = W - 1, P = kConvPairs;
     __shared__ f2x acc[kConvWarps][W + 1][32][P];
     pdl_trigger();
@@ -337,6 +385,8 @@ __global__ void __launch_bounds__(32 * kConvWarps, 4) causal_conv_bwd_kernel(con
     const ConvArgs& a = g.f;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const ConvPlace p = conv_place(a, run, 64 * P);
+    const long long row = (long long)p.b * a.L;
+    Starts starts = starts_of(a.reset, row, p.t0, a.L, lane);
     ConvSums<W, P> s;
     clear(s.db);
 #pragma unroll
@@ -353,8 +403,6 @@ __global__ void __launch_bounds__(32 * kConvWarps, 4) causal_conv_bwd_kernel(con
         if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
         for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
-        const long long row = (long long)p.b * a.L;
-        uint32_t history = starts_of<H>(a.reset, row, p.t0 - H, a.L);
         const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
         const uint16_t* py = g.dy + (row + p.t0) * a.D + p.c;
         // the run's tokens, then the H after it, whose taps reach into it
@@ -369,7 +417,7 @@ __global__ void __launch_bounds__(32 * kConvWarps, 4) causal_conv_bwd_kernel(con
                     qd[r] = load_words<P>(py + (long long)r * a.D);
                 }
             }
-            history = (history & ((1u << H) - 1u)) << kConvStep | starts_of<kConvStep>(a.reset, row, t, a.L);
+            const uint32_t history = next_starts<H>(starts);
             if (own >= kConvStep && history == 0u)
                 conv_group_back<W, P, SILU, true>(g, p, q, qd, n, own, t - p.t0, 0u, w, bias, v, s);
             else
@@ -433,14 +481,11 @@ cudaError_t by_width(int W, int silu, F&& f) {
 
 }  // namespace
 
-int conv_bwd_parts(int B, int L, int D) {
-    const int tokens = conv_run(B, L, D) * kConvWarps;
-    return B * ((L + tokens - 1) / tokens);
-}
+int conv_bwd_parts(int B, int L, int D) { return (int)conv_tiles(B, L, conv_run(B, L, D, kConvBwdCtas)); }
 
 cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl) {
-    const int run = conv_run(a.B, a.L, a.D);
-    const dim3 grid((unsigned)((long long)conv_bwd_parts(a.B, a.L, a.D) * ((a.D + 64 * kConvPairs - 1) / (64 * kConvPairs))));
+    const int run = conv_run(a.B, a.L, a.D, kConvFwdCtas);
+    const dim3 grid((unsigned)(conv_tiles(a.B, a.L, run) * conv_spans(a.D)));
     return by_width(a.W, a.silu, [&](auto w, auto silu) {
         return launch_ex(causal_conv_fwd_kernel<decltype(w)::value, decltype(silu)::value>, grid, dim3(32 * kConvWarps), 0, s,
                          pdl, a, run);
@@ -454,7 +499,7 @@ cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl)
 }
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& g, cudaStream_t s, bool pdl) {
     const dim3 grid((unsigned)((long long)g.parts * ((g.f.D + 64 * kConvPairs - 1) / (64 * kConvPairs))));
-    const int run = conv_run(g.f.B, g.f.L, g.f.D);
+    const int run = conv_run(g.f.B, g.f.L, g.f.D, kConvBwdCtas);
     return by_width(g.f.W, g.f.silu, [&](auto w, auto silu) {
         return launch_ex(causal_conv_bwd_kernel<decltype(w)::value, decltype(silu)::value>, grid, dim3(32 * kConvWarps), 0, s,
                          pdl, g, run);

@@ -45,6 +45,17 @@ def test_matches_the_definition(B, L, D, W, silu, fp32):
     assert got["dx"].dtype == got["dstate"].dtype == (torch.float32 if fp32 else BF)
 
 
+@pytest.mark.parametrize("B,L,D,W", [(600, 318, 16, 4), (600, 320, 16, 3), (1100, 250, 8, 2)])
+@pytest.mark.parametrize("resets", [0.0, 0.02])
+def test_long_runs(B, L, D, W, resets):
+    """Batch enough for runs of up to 80 tokens, the last one shorter; starts on either side of a run's ends."""
+    i, dy = _inputs(B, L, D, W, seed=W, resets=resets)
+    if resets:
+        i["reset"][::2, 75:85] = 1
+        i["reset"][1::2, 80] = 1
+    ref.check(_run(i, dy, True, True), ref.conv(*i.values(), dy=dy))
+
+
 @pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("state", [False, True])
 def test_missing_inputs(bias, state):

@@ -169,20 +169,27 @@ __device__ __forceinline__ void ask_states(const uint16_t* p, long long st, int 
         if (T * NP / 2 % 32 == 0 || t < T) copy4(dst + 2 * i, on ? p + t * (int)st + n : p, on);
     }
 }
-// The rows as FP32, every value twice: from what ask_states brought, or (not `words`) a value at a time.
+// Where two of a token's b or c wait (states j and j + 1 of lane ln, every value twice): the LN lanes' side by side, so that
+// they read them without a bank conflict (64 states, 4 x 4096 x 256: a lane's states in a row 236 us
+// forward and 718 with the backward, so 169 and 533).
+template <int LN>
+__device__ __forceinline__ constexpr int state_at(int ln, int j) {
+    return 4 * (j / 2 * LN + ln);
+}
+// The rows as FP32, in that order: from what ask_states brought, or (not `words`) a value at a time.
 template <int LN, int T>
 __device__ __forceinline__ void stage_states(const uint16_t* p, long long st, bool words, int nt, int N, const uint16_t* raw,
                                              float* dst, int lane) {
     constexpr int NP = SsmWarp<LN>::NP, K = (T * NP / 2 + 31) / 32;
     uint32_t v[K];
-    if (words) {
 #pragma unroll
-        for (int k = 0; k < K; ++k)
-            if (T * NP / 2 % 32 == 0 || k * 32 + lane < T * NP / 2) v[k] = reinterpret_cast<const uint32_t*>(raw)[k * 32 + lane];
-    } else {
-#pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int i = k * 32 + lane, t = i / (NP / 2), n = i % (NP / 2) * 2;
+    for (int k = 0; k < K; ++k) {
+        const int i = k * 32 + lane, t = i / (NP / 2), q = i % (NP / 2), n = q % LN * kSsmSt + q / LN * 2;
+        v[k] = 0u;
+        if (T * NP / 2 % 32 != 0 && t >= T) continue;
+        if (words) {
+            v[k] = *reinterpret_cast<const uint32_t*>(raw + t * NP + n);
+        } else {
             uint32_t lo = 0u, hi = 0u;
             if (t < nt && n < N) lo = __ldg(p + t * (int)st + n);
             if (t < nt && n + 1 < N) hi = __ldg(p + t * (int)st + n + 1);

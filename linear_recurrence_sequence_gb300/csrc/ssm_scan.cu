@@ -40,7 +40,8 @@ constexpr int kSsmSms = 152;
 // only the outputs need.
 template <int LN, bool Y>
 struct FwdTile {
-    static constexpr int T = LN == 1 ? 4 : 8;   // tokens
+    // tokens: what leaves an SM four CTAs' room (64 states, 4 x 4096 x 256: 8 tokens 183 us, 4 tokens 169)
+    static constexpr int T = LN == 1 || LN == 8 ? 4 : 8;
     using W = SsmWarp<LN>;
     float bias[W::CW];
     float dt[T][W::CW];    // then the sums over the states
@@ -125,8 +126,8 @@ __device__ __forceinline__ void advance(const FwdTile<LN, Y>& s, int t, int lc, 
 #pragma unroll
     for (int j = 0; j < kSsmSt; j += 2) {
         f2x b[2], c[2];
-        read_twice(&s.b[t][2 * (ln * kSsmSt + j)], b[0], b[1]);
-        if (Y) read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
+        read_twice(&s.b[t][state_at<LN>(ln, j)], b[0], b[1]);
+        if (Y) read_twice(&s.c[t][state_at<LN>(ln, j)], c[0], c[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -355,10 +356,54 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
 // One token of each of B sequences: LQ lanes share a channel, four states each
 // (16 bytes of the state row), and go through the batch.  Bound by the state, read
 // and written once in FP32 (256 sequences of 2048 channels and 16 states: 67 MB).
-// Warps enough to hide the loads are worth more than loads in flight a thread (two
-// sequences at a time 18.9 us, four 23.1, one 14.9).
-constexpr int kStepThreads = 256, kStepCtas = 5;
+// While it computes a sequence a thread asks for the next one's inputs (1024 sequences of
+// 4096 channels and 64 states, 2.1 GB: 454 us, 4.7 TB/s of a copy's 6.8, else 559; the 67
+// MB above, which stay in L2 between calls, 15 us, else 17).  Asking further ahead costs
+// warps and is slower (two sequences ahead 19 us and 491).
+constexpr int kStepThreads = 256, kStepCtas = 4;
+// What a thread reads of a sequence; b and c as BF16 pairs.
+struct StepInputs {
+    float h[4];
+    uint32_t b[2], c[2];
+    uint16_t x, delta, z;
+    uint8_t start;
+};
 // VEC: the state, b and c four at a time.
+template <bool VEC>
+__device__ __forceinline__ void load_step(const SsmArgs& a, const float* state, long long b, int c, int n0, bool on,
+                                          const bool (&live)[4], StepInputs& q) {
+    const float* ps = state + (b * a.D + c) * a.N + n0;
+    const uint16_t *pb = a.b.p + b * a.b.sb + n0, *pc = a.c.p + b * a.c.sb + n0;
+    q = {};
+    if (VEC) {
+        if (live[0]) {
+            const float4 v = *reinterpret_cast<const float4*>(ps);
+            const uint2 vb = __ldg(reinterpret_cast<const uint2*>(pb)), vc = __ldg(reinterpret_cast<const uint2*>(pc));
+            q.h[0] = v.x;
+            q.h[1] = v.y;
+            q.h[2] = v.z;
+            q.h[3] = v.w;
+            q.b[0] = vb.x;
+            q.b[1] = vb.y;
+            q.c[0] = vc.x;
+            q.c[1] = vc.y;
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (live[e]) {
+                q.h[e] = ps[e];
+                q.b[e / 2] |= (uint32_t)__ldg(pb + e) << (e % 2 * 16);
+                q.c[e / 2] |= (uint32_t)__ldg(pc + e) << (e % 2 * 16);
+            }
+    }
+    if (on) {
+        q.x = __ldg(a.x.p + b * a.x.sb + c);
+        q.delta = __ldg(a.delta.p + b * a.delta.sb + c);
+        if (a.gate.p != nullptr) q.z = __ldg(a.gate.p + b * a.gate.sb + c);
+    }
+    if (a.reset != nullptr) q.start = __ldg(a.reset + b);
+}
 template <int LQ, bool VEC>
 __global__ void __launch_bounds__(kStepThreads, kStepCtas) ssm_step_kernel(const SsmArgs a, float* __restrict__ state) {
     pdl_trigger();
@@ -374,54 +419,34 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) ssm_step_kernel(const
     }
     const float bias = on && a.delta_bias != nullptr ? __ldg(a.delta_bias + c) : 0.f;
     const float skip = on && a.d_skip != nullptr ? __ldg(a.d_skip + c) : 0.f;
+    StepInputs next = {};
+    if (blockIdx.y < a.B) load_step<VEC>(a, state, blockIdx.y, c, n0, on, live, next);
     for (long long b = blockIdx.y; b < a.B; b += gridDim.y) {
-        float* ps = state + (b * a.D + c) * a.N + n0;
-        const uint16_t *pb = a.b.p + b * a.b.sb + n0, *pc = a.c.p + b * a.c.sb + n0;
-        float h[4] = {0.f, 0.f, 0.f, 0.f}, bb[4] = {0.f, 0.f, 0.f, 0.f}, cc[4] = {0.f, 0.f, 0.f, 0.f};
-        float x = 0.f, raw = 0.f, z = 0.f;
-        if (VEC) {
-            if (live[0]) {
-                const float4 v = *reinterpret_cast<const float4*>(ps);
-                const uint2 vb = __ldg(reinterpret_cast<const uint2*>(pb)), vc = __ldg(reinterpret_cast<const uint2*>(pc));
-                h[0] = v.x;
-                h[1] = v.y;
-                h[2] = v.z;
-                h[3] = v.w;
-                up2(bf2x(vb.x), bb[0], bb[1]);
-                up2(bf2x(vb.y), bb[2], bb[3]);
-                up2(bf2x(vc.x), cc[0], cc[1]);
-                up2(bf2x(vc.y), cc[2], cc[3]);
-            }
-        } else {
+        StepInputs q = next;
+        if (b + gridDim.y < a.B) load_step<VEC>(a, state, b + gridDim.y, c, n0, on, live, next);
+        float bb[4], cc[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (live[e]) {
-                    h[e] = ps[e];
-                    bb[e] = bf_up(__ldg(pb + e));
-                    cc[e] = bf_up(__ldg(pc + e));
-                }
+        for (int e = 0; e < 2; ++e) {
+            up2(bf2x(q.b[e]), bb[2 * e], bb[2 * e + 1]);
+            up2(bf2x(q.c[e]), cc[2 * e], cc[2 * e + 1]);
         }
-        if (on) {
-            x = bf_up(__ldg(a.x.p + b * a.x.sb + c));
-            raw = bf_up(__ldg(a.delta.p + b * a.delta.sb + c)) + bias;
-            if (a.gate.p != nullptr) z = bf_up(__ldg(a.gate.p + b * a.gate.sb + c));
-        }
-        const bool start = a.reset != nullptr && __ldg(a.reset + b) != 0;
+        const float x = bf_up(q.x), z = bf_up(q.z);
         float dt, unused;
-        up2(softplus2(dup2(raw)), dt, unused);
+        up2(softplus2(dup2(bf_up(q.delta) + bias)), dt, unused);
         const float k = dt * x;
         float y = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            h[e] = start ? k * bb[e] : fmaf(ex2_approx(A[e] * dt), h[e], k * bb[e]);
-            y = fmaf(h[e], cc[e], y);
+            q.h[e] = q.start != 0 ? k * bb[e] : fmaf(ex2_approx(A[e] * dt), q.h[e], k * bb[e]);
+            y = fmaf(q.h[e], cc[e], y);
         }
+        float* ps = state + (b * a.D + c) * a.N + n0;
         if (VEC) {
-            if (live[0]) *reinterpret_cast<float4*>(ps) = make_float4(h[0], h[1], h[2], h[3]);
+            if (live[0]) *reinterpret_cast<float4*>(ps) = make_float4(q.h[0], q.h[1], q.h[2], q.h[3]);
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (live[e]) ps[e] = h[e];
+                if (live[e]) ps[e] = q.h[e];
         }
 #pragma unroll
         for (int m = LQ / 2; m >= 1; m >>= 1) y += __shfl_xor_sync(0xffffffffu, y, m);

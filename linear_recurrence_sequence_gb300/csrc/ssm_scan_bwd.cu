@@ -118,7 +118,7 @@ __device__ __forceinline__ void retreat(const RevTile<LN>& s, int t, int lc, int
 #pragma unroll
     for (int j = 0; j < kSsmSt; j += 2) {
         f2x c[2];
-        read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
+        read_twice(&s.c[t][state_at<LN>(ln, j)], c[0], c[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -298,8 +298,8 @@ __device__ __forceinline__ void forth(BwdTile<LN>& s, int t, uint32_t at, int la
 #pragma unroll
     for (int j = 0; j < kSsmSt; j += 2) {
         f2x b[2], c[2];
-        read_twice(&s.b[t][2 * (ln * kSsmSt + j)], b[0], b[1]);
-        if (GATE) read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
+        read_twice(&s.b[t][state_at<LN>(ln, j)], b[0], b[1]);
+        if (GATE) read_twice(&s.c[t][state_at<LN>(ln, j)], c[0], c[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             f2x d = 0ull;
@@ -334,8 +334,8 @@ __device__ __forceinline__ void back(BwdTile<LN>& s, int t, uint32_t at, int lan
 #pragma unroll
     for (int j = 0; j < kSsmSt; j += 2) {
         f2x b[2], c[2];
-        read_twice(&s.b[t][2 * (ln * kSsmSt + j)], b[0], b[1]);
-        read_twice(&s.c[t][2 * (ln * kSsmSt + j)], c[0], c[1]);
+        read_twice(&s.b[t][state_at<LN>(ln, j)], b[0], b[1]);
+        read_twice(&s.c[t][state_at<LN>(ln, j)], c[0], c[1]);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             f2x d = 0ull;

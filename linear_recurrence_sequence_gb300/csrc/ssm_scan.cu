@@ -218,12 +218,15 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(cons
 
 // Entry states of the chunks, in place of their end states: one float4 of a
 // warp's states a thread.  Backward (REV): the adjoints that reach a chunk's
-// end, from the last chunk to the first.
+// end, from the last chunk to the first.  Bound by the loads' latency: CTAs of a warp,
+// on as many SMs, and 24 chunks asked for at a time (1 x 32768 x 8, 286 chunks: 256
+// threads and 8 chunks 103 us forward, 32 and 24 88; 32 chunks do not fit the registers).
+constexpr int kPrefixThreads = 32;
 template <int LN, bool REV>
-__global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a) {
+__global__ void __launch_bounds__(kPrefixThreads) ssm_prefix_kernel(const SsmArgs a) {
     using W = SsmWarp<LN>;
     pdl_wait();
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+    const long long i = (long long)blockIdx.x * kPrefixThreads + threadIdx.x;
     const int lane = (int)(i & 31), k = (int)(i >> 5) & (kSsmVec - 1);
     const long long bg = i / (32 * kSsmVec);
     const int g = (int)(bg % a.groups);
@@ -243,7 +246,7 @@ __global__ void __launch_bounds__(256) ssm_prefix_kernel(const SsmArgs a) {
     const long long first = (b * a.nchunk + (REV ? a.nchunk - 1 : 0)) * a.groups + g;
     float4* m = a.maps + first * (kSsmVec * 32) + k * 32 + lane;
     const float4* sums = reinterpret_cast<const float4*>(a.sums + first * W::CW + cw);
-    constexpr int AHEAD = 8;
+    constexpr int AHEAD = 24;
     for (int q = 0; q < a.nchunk; q += AHEAD) {
         float4 v[AHEAD], s[AHEAD];
 #pragma unroll
@@ -470,9 +473,9 @@ cudaError_t fwd_as(const SsmArgs& a, int what, cudaStream_t s, bool pdl) {
         return launch_ex(ssm_maps_kernel<LN>, dim3((unsigned)((long long)a.B * (a.nchunk - 1) * a.ngq)), block, smem, s, pdl, a);
     }
     if (what == 1)
-        return launch_ex(ssm_prefix_kernel<LN, false>, dim3((unsigned)((long long)a.B * a.groups)), dim3(256), 0, s, pdl, a);
+        return launch_ex(ssm_prefix_kernel<LN, false>, dim3((unsigned)((long long)a.B * a.groups * (kSsmVec * 32 / kPrefixThreads))), dim3(kPrefixThreads), 0, s, pdl, a);
     if (what == 2)
-        return launch_ex(ssm_prefix_kernel<LN, true>, dim3((unsigned)((long long)a.B * a.groups)), dim3(256), 0, s, pdl, a);
+        return launch_ex(ssm_prefix_kernel<LN, true>, dim3((unsigned)((long long)a.B * a.groups * (kSsmVec * 32 / kPrefixThreads))), dim3(kPrefixThreads), 0, s, pdl, a);
     const size_t smem = w.warps * sizeof(FwdTile<LN, true>), most = kSsmWarps * sizeof(FwdTile<LN, true>);
     const dim3 grid((unsigned)((long long)a.B * a.nchunk * a.ngq));
     if (a.keep != nullptr) {
@@ -529,14 +532,14 @@ SsmSplit ssm_split(int D, int N) {
 }
 // As many chunks as give every SM `ctas` CTAs, of 16 tokens at least; one where
 // `fewest` would not fit (the maps cost more than they bring).  Not more than
-// sqrt(2.5 L): a warp alone takes about 0.3 us for a token of its chunk (maps and
-// replay), the prefix 0.12 us for a chunk (1 x 32768 x 8 with 16 states: 2048 chunks
-// 247 us, 282 of them 102).
+// sqrt(10 L): a warp alone takes about 0.3 us for a token of its chunk (maps and
+// replay), the prefix 0.03 us for a chunk (1 x 32768 x 8 with 16 states: 572 chunks
+// 77 us, 286 of them 93, 724 of them 85).
 void ssm_chunks(int B, int L, int D, int N, int ctas, int fewest, int* chunk, int* nchunk) {
     const SsmSplit w = ssm_split(D, N);
     const long long most = (long long)kSsmSms * ctas / ((long long)B * w.ctas);
     long long n = std::min<long long>(most, (L + 15) / 16);
-    n = std::min<long long>(n, std::max(1LL, (long long)std::sqrt(2.5 * L)));
+    n = std::min<long long>(n, std::max(1LL, (long long)std::sqrt(10.0 * L)));
     if (n < fewest) n = 1;
     *chunk = (int)(((L + n - 1) / n + 7) / 8 * 8);
     *nchunk = (L + *chunk - 1) / *chunk;

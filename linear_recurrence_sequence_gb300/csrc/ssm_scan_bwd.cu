@@ -144,7 +144,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
     clear_states(u);
     f2x sum[2] = {0ull, 0ull};
     bool cut = false;
-    const int begin = p.chunk * a.chunk, end = min(a.L, begin + a.chunk);
+    // part k of the main kernel's chunk: a.chunk tokens, what is left for the last
+    const int part = p.chunk % g.per, chunk0 = p.chunk / g.per * g.chunk, begin = chunk0 + part * a.chunk;
+    const int end = min(a.L, part == g.per - 1 ? chunk0 + g.chunk : begin + a.chunk);
     const int last = begin + (end - 1 - begin) / T * T;
     stage_bias<LN>(a.delta_bias, c0, a.D, s.bias, lane);
     RevRows rows = rows_from(g, p.b, last, c0);

@@ -57,10 +57,12 @@ def test_matches_the_definition(B, L, D, N, fp32):
         assert got[k].dtype == (torch.float32 if fp32 else BF)
 
 
-@pytest.mark.parametrize("B,L,D,N", [(8, 2390, 8, 5), (8, 2432, 40, 16), (8, 2390, 16, 64), (19, 1024, 256, 16)])
+@pytest.mark.parametrize("B,L,D,N", [(8, 2390, 8, 5), (8, 2432, 40, 16), (8, 2390, 16, 64), (19, 1024, 256, 16),
+                                     (8, 2690, 40, 16), (8, 2710, 8, 3), (8, 2700, 72, 30)])
 @pytest.mark.parametrize("resets", [0.0, 0.002])
 def test_chunks_of_several_tiles(B, L, D, N, resets):
-    """Chunks of 64 tokens, whose reverse maps are those of their halves; at 2390 tokens the last chunk has one half."""
+    """Chunks of 64 tokens and of 72, whose reverse maps are those of their halves (of 32, of 40 and 32 tokens); at 2390 and
+    2690 tokens the last chunk has one half."""
     i, dy, dhT = _inputs(B, L, D, N, seed=N, resets=resets)
     i["delta_bias"] = i["delta_bias"] - 2.0   # states that reach over several chunks
     ref.check(_run(i, dy, dhT), ref.scan(**i, dy=dy, dhT=dhT))

@@ -15,6 +15,11 @@
 //   sum    a CTA a chunk of 16 sorted places and 1024 columns; the parts of a row
 //          that reaches over chunks are joined, in their order, by whichever of its
 //          CTAs is done last; other CTAs zero the rows without a token.
+// 16384 tokens, 32768 x 1024: lookup 14 us (67 MB, 4.7 TB/s), with FP32 gradients sort 12,
+// sum 39 (168 MB, 4.3 TB/s).  The sort is bound by the latency of its pass over the tokens
+// (65536 of them: 47 us).  Chunks of 32 places without the join in the same kernel, 69 us
+// in all where it is 50 now; a second pass over the tokens instead of the notes, 17 us of
+// sort.
 #include <algorithm>
 
 #include "ssm.cuh"

@@ -16,12 +16,18 @@
 //           states of the eight tokens again from the state that the forward
 //           kept before them, then the adjoint back through them;
 //   finish  the sums over chunks and over the CTAs of a token, in a fixed order.
-// In main the states before tokens 0, 2, 4, 6 wait in shared memory (16 KB a
-// warp), a state before an odd token is formed again from the one before it: a
-// store and a load of every state would take more of shared memory's bandwidth
-// than the two operations take of the FP32 pipe.  13 multiply-adds and two
-// exponentials a (token, channel, state) there, 3 and one in rmaps: bound by the
-// FP32 pipe, with the sums across lanes (one shuffle a state) beside it.
+// In main the states before the tile's eight tokens wait in tensor memory, 32 columns a
+// token (a lane's 4 x 8 states), so that shared memory (43% busy) keeps to the operands,
+// which every lane of a channel reads, and 250 registers a thread hold the rates, the
+// adjoint and dA: 2 CTAs an SM.  13 multiply-adds and two exponentials a (token, channel,
+// state) there, 3 and one in rmaps.
+//   4 x 4096 x 1024, 16 states: rmaps 66 us, prefix 10, main 271, finish 10.
+// Main issues 20 instructions for 32 states, 0.56 a clock and scheduler with 2 warps each:
+// 7 of them two-wide FP32 ones, which take the pipe and the register file 2 to 4 clocks, 2.4
+// exponentials, 3 of the sums across lanes.  Other forms of main measured there: 4 x 4 states
+// a lane (4 CTAs an SM, each operand read twice as often) 299 us, 3 CTAs (168 registers,
+// spills) 319, scalar FP32 303, the sums of all eight tokens after the tile 297, 4 tokens
+// unrolled 293, one 287; the states written in pairs or fours of columns 269 to 275.
 #include <algorithm>
 
 #include "ssm.cuh"

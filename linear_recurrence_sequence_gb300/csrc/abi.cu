@@ -1537,7 +1537,7 @@ int causal_conv_workspace_bytes(int B, int L, int D, int W, size_t* backward_byt
     const int st = check_conv_shape(B, L, D, W);
     if (st != LRS_OK) return st;
     if (backward_bytes != nullptr)
-        *backward_bytes = up256((size_t)conv_bwd_parts(B, L, D) * (W + 1) * D * sizeof(float));
+        *backward_bytes = 256 + up256((size_t)conv_bwd_parts(B, L, D) * (W + 1) * D * sizeof(float));
     return LRS_OK;
 }
 
@@ -1584,7 +1584,8 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
     g.dstate = dstate;
     g.f32 = grad_dtype == LRS_GRAD_FP32;
     g.parts = conv_bwd_parts(B, L, D);
-    g.part = static_cast<float*>(scratch);
+    g.status = at<uint32_t>(scratch, 0);
+    g.part = at<float>(scratch, 256);
     g.dw = dweight;
     g.dbias = dbias;
     LRS_LAUNCH(KID_CONV_BWD, stream, launch_causal_conv_bwd(g, stream, pdl_ok()));
@@ -1690,6 +1691,7 @@ SsmArgs ssm_args(const lrs_rows* x, const lrs_rows* delta, const float* a_log, c
 void ssm_place(SsmArgs& a, const SsmScratch& l, void* scratch) {
     a.chunk = l.chunk;
     a.nchunk = l.nchunk;
+    a.status = at<uint32_t>(scratch, 0);
     a.maps = at<float4>(scratch, l.maps);
     a.sums = at<float>(scratch, l.sums);
 }

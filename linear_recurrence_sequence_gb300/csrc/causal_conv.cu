@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(1024) causal_conv_sum_kernel(const ConvBwdArgs
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, k = threadIdx.x >> 5, W = g.f.W, D = g.f.D;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = 0u;
     const long long cols = (long long)(W + 1) * D, c = (long long)blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < cols) {

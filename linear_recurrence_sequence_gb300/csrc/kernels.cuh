@@ -678,6 +678,7 @@ struct SsmArgs {
     uint16_t* y;                 // [B][L][D]
     float* hT;                   // [B][D][N]
     float4* keep;                // [B][ceil(L / kSsmKeep)][groups][8][32] or null
+    uint32_t* status;            // cleared (nothing here waits on other CTAs); null in a step
 };
 struct SsmBwdArgs {
     SsmArgs f;
@@ -727,8 +728,9 @@ struct ConvBwdArgs {
     int parts;
     float* part;                 // [parts][W + 1][D]
     float *dw, *dbias;
+    uint32_t* status;            // cleared
 };
-int conv_bwd_parts(int B, int L, int D);   // CTAs along time of both directions
+int conv_bwd_parts(int B, int L, int D);   // its CTAs along time
 cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& a, cudaStream_t s, bool pdl);

@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
         }
     }
     pdl_trigger();   // not before: see ssm_maps_kernel
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
     if (p.chunk == a.nchunk - 1) store_state(a.hT, a.quads, p.b, ch, ln * kSsmSt, a.D, a.N, h);
 }
 

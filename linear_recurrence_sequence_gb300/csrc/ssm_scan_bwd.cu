@@ -595,6 +595,7 @@ __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdArgs g, int
     using W = SsmWarp<LN>;
     pdl_wait();   // no early trigger: the next call's CTAs would take these ones' places
     const SsmArgs& a = g.f;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0u;
     if ((int)blockIdx.x >= columns) {
         const long long n = (long long)a.B * a.L * 2 * W::NP;
         for (long long i = (long long)(blockIdx.x - columns) * 256 + threadIdx.x; i < n;

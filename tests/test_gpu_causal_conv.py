@@ -162,6 +162,7 @@ def test_a_captured_step():
         assert torch.equal(out[k], want[k]), k
     assert torch.equal(y1, want["y"][:, 0])
     assert torch.equal(state, torch.cat([i["state"][:, 1:], x1[:, None]], 1))
+    assert api.device_status(scratch) == 0   # (it held 0xff)
 
 
 def test_more_than_2_31_values():

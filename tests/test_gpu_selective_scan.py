@@ -265,6 +265,19 @@ def test_a_captured_training_step_and_its_workspaces():
         assert torch.equal(out[k], again[k]), k
 
 
+@pytest.mark.parametrize("B,L,D,N", [(900, 8, 8, 4), (2, 300, 128, 16)])
+def test_status_word(B, L, D, N):
+    """Whatever the scratch held before: one chunk and several."""
+    i, dy, dhT = _inputs(B, L, D, N, seed=5)
+    n = api.selective_scan_workspace_bytes(B, L, D, N)
+    scratch = torch.full((max(n[1:]),), 0xff, dtype=torch.uint8, device=DEV)
+    saved = api.selective_scan_forward(**i, scratch=scratch)["saved"]
+    assert api.device_status(scratch) == 0
+    scratch.fill_(0xff)
+    api.selective_scan_backward(dy, dhT, *i.values(), saved, scratch=scratch)
+    assert api.device_status(scratch) == 0
+
+
 def test_state_in_place():
     """hT may be h0 (a server's slot): one chunk and several."""
     for L in (40, 400):

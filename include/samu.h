@@ -767,7 +767,7 @@ int embedding_workspace_bytes(int T, int V, int D, size_t* backward_bytes);
  *   y        [T,D] BF16 (out), rounded once
  * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, unknown w_dtype,
  * scale not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8 or over 2^16, V over
- * 2^23, T over 2^28), LRS_ERR_CUDA. */
+ * 2^23, T over 2^28, T D over 2^40), LRS_ERR_CUDA. */
 int embedding_forward(const int64_t* tokens, const void* w, int w_dtype, int T, int V, int D, float scale, void* y,
                       cudaStream_t stream);
 
@@ -776,7 +776,8 @@ int embedding_forward(const int64_t* tokens, const void* w, int w_dtype, int T, 
  *            is added to what dw holds, rows without a token are left as they are: a
  *            matrix that the head shares, or several batches)
  *   scratch  embedding_workspace_bytes() bytes
- * FP32 sums in a fixed order (the tokens', in runs of 16), rounded once.
+ * FP32 sums in a fixed order (the tokens', in runs of 16 and 32 such runs at a time),
+ * rounded once.
  * Errors: as the forward, plus LRS_ERR_ARG for an unknown grad_dtype. */
 int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int D, float scale, void* dw, int grad_dtype,
                        int accumulate, void* scratch, cudaStream_t stream);

@@ -1805,7 +1805,8 @@ namespace {
 
 int check_embed_shape(int T, int V, int D) {
     if (T < 1 || V < 1 || D < 1) return LRS_ERR_ARG;
-    if (D % 8 != 0 || T > (1 << 28) || V > (1 << 23) || D > (1 << 16)) return LRS_ERR_UNSUPPORTED;
+    if (D % 8 != 0 || T > (1 << 28) || V > (1 << 23) || D > (1 << 16) || (long long)T * D > (1LL << 40))
+        return LRS_ERR_UNSUPPORTED;
     return LRS_OK;
 }
 

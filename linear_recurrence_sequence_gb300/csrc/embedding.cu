@@ -13,13 +13,15 @@
 //          L2: no histogram or prefix crosses CTAs, one launch), counts its rows'
 //          and all lower owners' tokens, and places its own in order.
 //   sum    a CTA a chunk of 16 sorted places and 1024 columns; the parts of a row
-//          that reaches over chunks are joined, in their order, by whichever of its
-//          CTAs is done last; other CTAs zero the rows without a token.
-// 16384 tokens, 32768 x 1024: lookup 14 us (67 MB, 4.7 TB/s), with FP32 gradients sort 12,
-// sum 39 (168 MB, 4.3 TB/s).  The sort is bound by the latency of its pass over the tokens
-// (65536 of them: 47 us).  Chunks of 32 places without the join in the same kernel, 69 us
-// in all where it is 50 now; a second pass over the tokens instead of the notes, 17 us of
-// sort.
+//          that reaches over chunks are joined, in their order and 32 at a time, by
+//          whichever of their CTAs is done last, and those sums by whichever group is
+//          (one CTA for all parts: 65536 tokens of two rows 303 us, so 56); other CTAs
+//          zero the rows without a token.
+// 16384 tokens, 32768 x 1024: lookup 14 us (67 MB, 4.7 TB/s), with FP32 gradients sort 10,
+// sum 37 (168 MB, 4.5 TB/s; 6 CTAs an SM, 5 with the registers that it would take: 65536
+// tokens 65 us, so 62).  The sort is bound by its pass over the tokens and by what its
+// busiest CTA finds (65536 tokens 29 us, none frequent 15; with a lane after the other in
+// place of whole warps where a token is frequent 47).
 #include <algorithm>
 
 #include "ssm.cuh"
@@ -69,24 +71,58 @@ __global__ void __launch_bounds__(256) embedding_fwd_kernel(const EmbedArgs a) {
 
 constexpr int kSortWarps = 32;
 constexpr int kSortRows = 1024;     // vocabulary rows of an owner, at most
-constexpr int kSortNotes = 96;      // tokens that a warp notes
+constexpr int kSortNotes = 96;      // tokens that a warp notes, 31 + 64 at least
+constexpr int kSortAhead = 4;       // times 64 tokens that it asks for at once
 constexpr int kOwners = 128;        // a power of two, as are the owners of larger vocabularies
 constexpr int kEmbedChunk = 16;     // sorted places of a CTA of the sum
+constexpr int kJoin = 32;           // parts of a row that one CTA joins
 constexpr int kSumThreads = 128;    // of it, 8 columns each
 
-// Tokens t (even, counted from a 16-byte boundary) and t + 1 as {low, high} words; -1 outside the array.
-__device__ __forceinline__ int4 two_tokens(const EmbedBwdArgs& a, long long t) {
-    if (t >= 0 && t + 1 < a.T) return __ldg(reinterpret_cast<const int4*>(a.tokens + t));
-    const int2* p = reinterpret_cast<const int2*>(a.tokens);
-    const int2 none = make_int2(-1, -1), x = t >= 0 && t < a.T ? __ldg(p + t) : none, y = t + 1 < a.T ? __ldg(p + t + 1) : none;
-    return make_int4(x.x, x.y, y.x, y.y);
+// N times 64 tokens from t on (counted from a 16-byte boundary, `odd` before the array), two a lane and step, as {low, high}
+// words; -1 from `end` on and outside the array.  All are asked for before one is used.
+template <int N>
+__device__ __forceinline__ void load_tokens(const EmbedBwdArgs& a, long long t, long long end, int odd, int lane, int4 (&q)[N]) {
+    const int2* p = reinterpret_cast<const int2*>(a.tokens) - odd;
+    bool cut = false;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+        const long long i = t + 64 * u + 2 * lane;
+        const bool whole = i >= odd && i + 1 < end;
+        cut |= !whole;
+        q[u] = make_int4(-1, -1, -1, -1);
+        if (whole) q[u] = __ldg(reinterpret_cast<const int4*>(p + i));
+    }
+    if (!cut) return;
+#pragma unroll
+    for (int u = 0; u < N; ++u) {   // the array's first and last token may lie alone in their pair
+        const long long i = t + 64 * u + 2 * lane;
+        if (i < odd && i + 1 < end) {
+            const int2 v = __ldg(p + i + 1);
+            q[u].z = v.x;
+            q[u].w = v.y;
+        } else if (i >= odd && i + 1 == end) {
+            const int2 v = __ldg(p + i);
+            q[u].x = v.x;
+            q[u].y = v.y;
+        }
+    }
 }
 
+// Which of two tokens are this owner's; how many a lower owner's; whether one has no row.
+struct Hits {
+    bool h0, h1, past;
+    int less;
+};
+__device__ __forceinline__ Hits hits_of(int4 q, uint32_t V, int own, int owners) {
+    const bool in0 = q.y == 0 && (uint32_t)q.x < V, in1 = q.w == 0 && (uint32_t)q.z < V;
+    const int o0 = q.x & (owners - 1), o1 = q.z & (owners - 1);
+    return {in0 && o0 == own, in1 && o1 == own, (q.y >= 0 && !in0) || (q.w >= 0 && !in1), (in0 && o0 < own) + (in1 && o1 < own)};
+}
 // A warp takes consecutive tokens, so that a stable sort needs no order between
 // threads: it counts its tokens of each row, a row's counts are added up over the
 // warps, and the warp places its tokens from there on.  What it finds (one token of
 // 128 is this owner's) it notes, to go through the tokens once; where that is more
-// than it has room for, it looks for them again.
+// than it has room for (a frequent token's), it looks for them again.
 __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const EmbedBwdArgs a, int rows, int dones) {
     extern __shared__ __align__(16) int count[];   // [kSortWarps][rows], then each warp's next place in a row
     __shared__ int2 noted[kSortWarps][kSortNotes];
@@ -106,27 +142,30 @@ __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const E
     const uint32_t V = (uint32_t)a.V, before_me = (1u << lane) - 1u;
     int less = 0, found = 0;
     bool past = false;
-#pragma unroll 8
-    for (long long t = begin; t < end; t += 64) {
-        const int4 q = t + 2 * lane < end ? two_tokens(a, t + 2 * lane - odd) : make_int4(-1, -1, -1, -1);
-        const bool in0 = q.y == 0 && (uint32_t)q.x < V, in1 = q.w == 0 && (uint32_t)q.z < V;
-        past |= (q.y >= 0 && !in0) | (q.w >= 0 && !in1);
-        const int o0 = q.x & (owners - 1), o1 = q.z & (owners - 1);
-        less += (in0 && o0 < own) + (in1 && o1 < own);
-        const bool hit0 = in0 && o0 == own, hit1 = in1 && o1 == own;
-        const uint32_t m0 = __ballot_sync(0xffffffffu, hit0), m1 = __ballot_sync(0xffffffffu, hit1);
-        if ((m0 | m1) == 0u) continue;
-        const int at = found + __popc(m0 & before_me) + __popc(m1 & before_me);
-        const int pos = (int)(t - odd) + 2 * lane;
-        if (hit0) {
-            atomicAdd(&mine[q.x >> shift], 1);
-            if (at < kSortNotes) noted[warp][at] = make_int2(pos, q.x >> shift);
+    for (long long t = begin; t < end; t += 64 * kSortAhead) {
+        int4 qs[kSortAhead];
+        load_tokens(a, t, end, odd, lane, qs);
+#pragma unroll
+        for (int u = 0; u < kSortAhead; ++u) {
+            const int4 q = qs[u];
+            const Hits h = hits_of(q, V, own, owners);
+            past |= h.past;
+            less += h.less;
+            const bool hit0 = h.h0, hit1 = h.h1;
+            const uint32_t m0 = __ballot_sync(0xffffffffu, hit0), m1 = __ballot_sync(0xffffffffu, hit1);
+            if ((m0 | m1) == 0u) continue;
+            const int at = found + __popc(m0 & before_me) + __popc(m1 & before_me);
+            const int pos = (int)(t - odd) + 64 * u + 2 * lane;
+            if (hit0) {
+                atomicAdd(&mine[q.x >> shift], 1);
+                if (at < kSortNotes) noted[warp][at] = make_int2(pos, q.x >> shift);
+            }
+            if (hit1) {
+                atomicAdd(&mine[q.z >> shift], 1);
+                if (at + hit0 < kSortNotes) noted[warp][at + hit0] = make_int2(pos + 1, q.z >> shift);
+            }
+            found += __popc(m0) + __popc(m1);
         }
-        if (hit1) {
-            atomicAdd(&mine[q.z >> shift], 1);
-            if (at + hit0 < kSortNotes) noted[warp][at + hit0] = make_int2(pos + 1, q.z >> shift);
-        }
-        found += __popc(m0) + __popc(m1);
     }
     if (past) bad = 1;
     less = __reduce_add_sync(0xffffffffu, less);
@@ -161,33 +200,49 @@ __global__ void __launch_bounds__(kSortWarps * 32) embedding_sort_kernel(const E
     }
     if (tid == 0 && own == 0) *a.status = bad ? kStatusTarget : 0u;
     __syncthreads();
+    // equal rows in the order of their lanes
+    const auto put = [&](bool on, int2 e) {
+        if (!on) e.y = -1 - lane;
+        const uint32_t same = __match_any_sync(0xffffffffu, e.y);
+        if (on) a.place[mine[e.y] + __popc(same & before_me)] = make_int2(e.x, own * rows + e.y);
+        __syncwarp();
+        if (on && (same & before_me) == 0u) mine[e.y] += __popc(same);
+        __syncwarp();
+    };
+    int2* note = noted[warp];
     if (found <= kSortNotes) {
-        for (int i = 0; i < found; i += 32) {
-            // equal rows in the order of their lanes
-            const bool on = i + lane < found;
-            const int2 e = on ? noted[warp][i + lane] : make_int2(0, -1 - lane);
-            const uint32_t same = __match_any_sync(0xffffffffu, e.y);
-            if (on) a.place[mine[e.y] + __popc(same & before_me)] = make_int2(e.x, own * rows + e.y);
-            __syncwarp();
-            if (on && (same & before_me) == 0u) mine[e.y] += __popc(same);
-            __syncwarp();
-        }
+        for (int i = 0; i < found; i += 32) put(i + lane < found, note[min(i + lane, kSortNotes - 1)]);
         return;
     }
-    for (long long t = begin; t < end; t += 64) {
-        const int4 q = t + 2 * lane < end ? two_tokens(a, t + 2 * lane - odd) : make_int4(-1, -1, -1, -1);
-        const bool hit0 = q.y == 0 && (uint32_t)q.x < V && (q.x & (owners - 1)) == own;
-        const bool hit1 = q.w == 0 && (uint32_t)q.z < V && (q.z & (owners - 1)) == own;
-        // the lanes that find one place theirs in turn
-        for (uint32_t m = __ballot_sync(0xffffffffu, hit0 || hit1); m != 0u; m &= m - 1u) {
-            if (lane == __ffs(m) - 1) {
-                const int pos = (int)(t - odd) + 2 * lane;
-                if (hit0) a.place[mine[q.x >> shift]++] = make_int2(pos, own * rows + (q.x >> shift));
-                if (hit1) a.place[mine[q.z >> shift]++] = make_int2(pos + 1, own * rows + (q.z >> shift));
-            }
+    int kept = 0;
+    for (long long t = begin; t < end; t += 64 * kSortAhead) {
+        int4 qs[kSortAhead];
+        load_tokens(a, t, end, odd, lane, qs);
+#pragma unroll 1
+        for (int u = 0; u < kSortAhead; ++u) {
+            const int4 q = qs[0];
+#pragma unroll
+            for (int k = 0; k + 1 < kSortAhead; ++k) qs[k] = qs[k + 1];
+            const Hits h = hits_of(q, V, own, owners);
+            const uint32_t m0 = __ballot_sync(0xffffffffu, h.h0), m1 = __ballot_sync(0xffffffffu, h.h1);
+            const int at = kept + __popc(m0 & before_me) + __popc(m1 & before_me), pos = (int)(t - odd) + 64 * u + 2 * lane;
+            if (h.h0) note[at] = make_int2(pos, q.x >> shift);
+            if (h.h1) note[at + h.h0] = make_int2(pos + 1, q.z >> shift);
+            kept += __popc(m0) + __popc(m1);
+            if (kept < 32) continue;
+            // whole warps of notes go to their places, the rest (31 at most, and 64 come with the next tokens) to the front
+            __syncwarp();
+            int i = 0;
+            for (; i + 32 <= kept; i += 32) put(true, note[i + lane]);
+            kept -= i;
+            const int2 e = note[i + min(lane, kSortNotes - 1 - i)];
+            __syncwarp();
+            if (lane < kept) note[lane] = e;
             __syncwarp();
         }
     }
+    __syncwarp();
+    put(lane < kept, note[lane]);
 }
 
 // 8 columns of a row of dw (`old`: what they hold where the gradient is added to it).
@@ -237,11 +292,35 @@ __device__ __forceinline__ RowParts parts_of(const EmbedBwdArgs& a, int row) {
     return {begin / kEmbedChunk, (last - 1) / kEmbedChunk - begin / kEmbedChunk + 1};
 }
 
+__device__ __forceinline__ float* part_at(const EmbedBwdArgs& a, const RowParts& r, int i, int v) {
+    return a.part + (2LL * (r.first + i) + (i == 0 ? 1 : 0)) * a.D + 8 * v;
+}
+// s: the sum of the parts from, from + step, .. before to, in that order
+__device__ __forceinline__ void add_parts(const EmbedBwdArgs& a, const RowParts& r, int from, int to, int step, int v, f2x (&s)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] = 0ull;
+#pragma unroll 8
+    for (int i = from; i < to; i += step) {
+        const float4* p = reinterpret_cast<const float4*>(part_at(a, r, i, v));
+        const float4 q0 = __ldcg(p), q1 = __ldcg(p + 1);
+        s[0] = add2(s[0], pk2(q0.x, q0.y));
+        s[1] = add2(s[1], pk2(q0.z, q0.w));
+        s[2] = add2(s[2], pk2(q1.x, q1.y));
+        s[3] = add2(s[3], pk2(q1.z, q1.w));
+    }
+}
+// Counters of a chunk: 0 of a group of parts whose first is there and not the row's first, 1 of the first group of the row
+// that begins there, 2 of that row's groups.  How many were done before.
+__device__ __forceinline__ int done_here(const EmbedBwdArgs& a, int chunk, int which) {
+    return atomicAdd(a.done + (3LL * chunk + which) * gridDim.y + blockIdx.y, 1);
+}
+
 // Sums of a chunk's rows (blockIdx.x < chunks) in columns blockIdx.y, 8 a thread; zeros for the rows without a token.
-__global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedBwdArgs a, int rows, int chunks) {
+__global__ void __launch_bounds__(kSumThreads, 6) embedding_sum_kernel(const EmbedBwdArgs a, int rows, int chunks) {
     __shared__ int2 place[kEmbedChunk];
     __shared__ uint32_t empty;
     __shared__ int join[2];
+    __shared__ bool last_group;
     pdl_trigger();
     pdl_wait();
     const int nv = a.D / 8, v = blockIdx.y * blockDim.x + threadIdx.x;
@@ -310,7 +389,7 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedB
         }
     }
     if (!from && !to) return;
-    // this CTA's parts are written: whether they were the last of their rows
+    // this CTA's parts are written: whether they were the last of their rows, or of a group of them
     __threadfence();
     __syncthreads();
     if (threadIdx.x < 2) {
@@ -318,31 +397,38 @@ __global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const EmbedB
         bool last = false;
         if (threadIdx.x == 0 ? from : to && !(from && head == tail)) {
             const RowParts r = parts_of(a, row);
-            last = atomicAdd(a.done + (long long)r.first * gridDim.y + blockIdx.y, 1) == r.count - 1;
+            const int g = (blockIdx.x - r.first) / kJoin * kJoin;
+            last = done_here(a, r.first + g, g == 0 ? 1 : 0) == min(kJoin, r.count - g) - 1;
         }
         join[threadIdx.x] = last ? row : -1;
     }
     __syncthreads();
-    if (v >= nv || (join[0] < 0 && join[1] < 0)) return;
-    __threadfence();
 #pragma unroll 1
     for (int w = 0; w < 2; ++w) {
-        if (join[w] < 0) continue;
-        const RowParts r = parts_of(a, join[w]);
-        const long long out = vocabulary_row(a, rows, join[w]);
-        const Old old = old_row(a, out, v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[e] = 0ull;
-#pragma unroll 8
-        for (int c = 0; c < r.count; ++c) {
-            const float4* p = reinterpret_cast<const float4*>(a.part + (2LL * (r.first + c) + (c == 0 ? 1 : 0)) * a.D + 8 * v);
-            const float4 q0 = __ldcg(p), q1 = __ldcg(p + 1);
-            s[0] = add2(s[0], pk2(q0.x, q0.y));
-            s[1] = add2(s[1], pk2(q0.z, q0.w));
-            s[2] = add2(s[2], pk2(q1.x, q1.y));
-            s[3] = add2(s[3], pk2(q1.z, q1.w));
+        const int row = join[w];
+        if (row < 0) continue;
+        const RowParts r = parts_of(a, row);
+        const int g = (blockIdx.x - r.first) / kJoin * kJoin;
+        const long long out = vocabulary_row(a, rows, row);
+        Old old = {};   // (asked for ahead of the parts)
+        __threadfence();
+        if (r.count <= kJoin && v < nv) old = old_row(a, out, v);
+        if (v < nv) add_parts(a, r, g, min(r.count, g + kJoin), 1, v, s);
+        if (r.count > kJoin) {
+            // the group's sum takes the place of its first part
+            if (v < nv) put_pairs(part_at(a, r, g, v), s);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) last_group = done_here(a, r.first, 2) == (r.count - 1) / kJoin;
+            __syncthreads();
+            if (!last_group) continue;
+            __threadfence();
+            if (v < nv) {
+                old = old_row(a, out, v);
+                add_parts(a, r, 0, r.count, kJoin, v, s);
+            }
         }
-        put_row(a, out, v, s, old);
+        if (v < nv) put_row(a, out, v, s, old);
     }
 }
 
@@ -367,7 +453,7 @@ int embed_owners(int V) {
     while ((long long)n * kSortRows < V) n *= 2;
     return n;
 }
-long long embed_dones(long long T, int D) { return embed_chunks(T) * ((D / 8 + kSumThreads - 1) / kSumThreads); }
+long long embed_dones(long long T, int D) { return 3 * embed_chunks(T) * ((D / 8 + kSumThreads - 1) / kSumThreads); }
 long long embed_chunks(long long T) { return (T + kEmbedChunk - 1) / kEmbedChunk; }
 
 cudaError_t launch_embedding(const EmbedArgs& a, cudaStream_t s, bool pdl) {

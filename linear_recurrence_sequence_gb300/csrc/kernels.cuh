@@ -759,7 +759,7 @@ struct EmbedBwdArgs {
     int* count;                  // [1]: of them
     int* first;                  // [owners rows + 1]: each row's first place
     float* part;                 // [2 chunks][D]
-    int* done;                   // [embed_dones]: parts of the row that begins in a chunk that are written
+    int* done;                   // [embed_dones]: what is done of a row's parts, three counters a chunk
 };
 int embed_owners(int V);
 long long embed_dones(long long T, int D);

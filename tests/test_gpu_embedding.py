@@ -107,6 +107,21 @@ def test_many_occurrences():
     _check_dw(api.embedding_backward(dy, tokens, V, grad_fp32=True)["dw"], dy, tokens, V, 1.0)
 
 
+@pytest.mark.parametrize("first", [0, 1, 15, 16, 40])
+@pytest.mark.parametrize("D", [72, 1032])
+def test_rows_of_many_runs(first, D):
+    """Rows whose runs of 16 fill groups of 32, less and more than one, side by side in the sorted order."""
+    gen = _gen(first)
+    # (rows 128 apart lie next to each other)
+    counts = [first, 500, 12, 512, 513, 528, 1, 1040, 16, 0, 1600, 511, 17, 16384]
+    tokens = torch.cat([torch.full((n,), 128 * k, device=DEV) for k, n in enumerate(counts)])
+    tokens = tokens[torch.randperm(tokens.numel(), generator=gen, device=DEV)]
+    V, dy = 128 * len(counts), _randn(gen, tokens.numel(), D, dtype=BF)
+    dw = api.embedding_backward(dy, tokens, V, grad_fp32=True)["dw"]
+    _check_dw(dw, dy, tokens, V, 1.0)
+    assert torch.equal(dw, api.embedding_backward(dy, tokens, V, grad_fp32=True)["dw"])
+
+
 def test_tokens_without_a_row():
     gen = _gen(5)
     w, dy = _randn(gen, 50, 64, dtype=BF), _randn(gen, 40, 64, dtype=BF)

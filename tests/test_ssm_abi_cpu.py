@@ -117,7 +117,7 @@ def test_selective_scan_bad_arguments(lib):
 @pytest.mark.parametrize("T,V,D,expect", [
     (1, 1, 8, OK), (16384, 32768, 1024, OK), (5001, 50021, 2560, OK), (7, 1 << 23, 8, OK), (0, 5, 8, ARG), (5, 0, 8, ARG),
     (5, 5, 0, ARG), (5, 5, 12, UNSUPPORTED), (5, (1 << 23) + 1, 8, UNSUPPORTED), (5, 5, (1 << 16) + 8, UNSUPPORTED),
-    ((1 << 28) + 1, 5, 8, UNSUPPORTED)])
+    ((1 << 28) + 1, 5, 8, UNSUPPORTED), (1 << 28, 5, (1 << 12) + 8, UNSUPPORTED)])
 def test_embedding_shapes(lib, T, V, D, expect):
     n = ctypes.c_size_t(0)
     assert lib.embedding_workspace_bytes(T, V, D, ctypes.byref(n)) == expect

@@ -1537,7 +1537,7 @@ int causal_conv_workspace_bytes(int B, int L, int D, int W, size_t* backward_byt
     const int st = check_conv_shape(B, L, D, W);
     if (st != LRS_OK) return st;
     if (backward_bytes != nullptr)
-        *backward_bytes = 256 + up256((size_t)conv_bwd_parts(B, L, D) * (W + 1) * D * sizeof(float));
+        *backward_bytes = 256 + up256((size_t)conv_bwd_parts(B, L, D, W) * (W + 1) * D * sizeof(float));
     return LRS_OK;
 }
 
@@ -1583,7 +1583,7 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
     g.dx = rows_out(dx);
     g.dstate = dstate;
     g.f32 = grad_dtype == LRS_GRAD_FP32;
-    g.parts = conv_bwd_parts(B, L, D);
+    g.parts = conv_bwd_parts(B, L, D, W);
     g.status = at<uint32_t>(scratch, 0);
     g.part = at<float>(scratch, 256);
     g.dw = dweight;

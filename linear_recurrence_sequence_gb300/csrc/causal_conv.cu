@@ -9,13 +9,12 @@
 //
 // 4 bytes a value forward, 6 backward.  A thread walks along time through a run of
 // tokens of 4 channels, the last W inputs in registers, and asks for 8 rows at a
-// time, forward for the next 8 while it computes these.  The backward forms pre
-// again (x is read anyway, pre is not kept) and keeps the sums of the dx of the last
-// W tokens.  A run's first W - 1 rows, and backward the W - 1 after it, are gone
-// through twice.
+// time, the next 8 while it computes these.  The backward forms pre again (x is read
+// anyway, pre is not kept) and keeps the sums of the dx of the last W tokens.  A run's
+// first W - 1 rows, and backward the W - 1 after it, are gone through twice.
 //   16 x 4096 x 1024, W = 4: forward 51 us, 5.2 TB/s (0.77 of a copy's measured 6.8);
-//   backward 113 us, 3.6 TB/s: about 25 instructions a value, bound by their issue.
-//   4 x 4096 x 1024: 17 and 33 us, of which the launches' start and end are 3 us each.
+//   backward 104 us, 3.9 TB/s: about 25 instructions a value, by 8 warps an SM.
+//   4 x 4096 x 1024: 17 and 30 us, of which the launches' start and end are 3 us each.
 // With 2 channels a thread (twice the warps) 4 x 4096 x 1024 took 23 and 39 us.
 #include <algorithm>
 #include <type_traits>
@@ -31,13 +30,16 @@ constexpr int kConvWarps = 4;     // runs of a CTA
 constexpr int kConvPairs = 2;     // of channels, a thread
 constexpr int kConvRun = 80;       // tokens of a run at most
 constexpr int kConvSms = 152;
-constexpr int kConvFwdCtas = 5, kConvBwdCtas = 4;   // resident per SM, by registers
+// Resident per SM, by registers.  Backward with 3 at W = 4 (spills) 4 x 4096 x 1024 takes 32 us, 2 x 32768 x 1024 with
+// 2 at W = 3 95 us, so 30 and 82.
+constexpr int kConvFwdCtas = 5;
+constexpr int conv_bwd_ctas(int W) { return W == 4 ? 2 : 3; }
 
 // A launch's CTAs: runs of a batch row by spans of channels.
 long long conv_tiles(int B, int L, int run) { return (long long)B * (((long long)L + run * kConvWarps - 1) / (run * kConvWarps)); }
 long long conv_spans(int D) { return (D + 64 * kConvPairs - 1) / (64 * kConvPairs); }
 // A run's tokens: those that end soonest, by the rounds that the SMs take with `ctas` CTAs each and a run's own cost, about
-// a step (1 x 8192 x 2560: 72 tokens, one round, 39 us backward, 64 tokens 49; 16 x 4096 x 1024: 64 tokens 51 us forward, 80
+// a step (1 x 8192 x 2560: 72 tokens, one round of 4 CTAs an SM, 39 us backward, 64 tokens 49; 16 x 4096 x 1024: 64 tokens 51 us forward, 80
 // tokens 55).  kConvRun at most: what the words of Starts cover.
 int conv_run(int B, int L, int D, int ctas) {
     const long long places = (long long)ctas * kConvSms;
@@ -377,7 +379,7 @@ __device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const Conv
 }
 
 template <int W, bool SILU>
-__global__ void __launch_bounds__(32 * kConvWarps, kConvBwdCtas) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
+__global__ void __launch_bounds__(32 * kConvWarps, conv_bwd_ctas(W)) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
     constexpr int H = W - 1, P = kConvPairs;
     __shared__ f2x acc[kConvWarps][W + 1][32][P];
     pdl_trigger();
@@ -406,15 +408,29 @@ __global__ void __launch_bounds__(32 * kConvWarps, kConvBwdCtas) causal_conv_bwd
         const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
         const uint16_t* py = g.dy + (row + p.t0) * a.D + p.c;
         // the run's tokens, then the H after it, whose taps reach into it
-        for (int t = p.t0; t < p.end + H; t += kConvStep, px += kConvStep * a.x.st, py += (long long)kConvStep * a.D) {
+        Words<P> nq[kConvStep], nqd[kConvStep];
+        const int total = min(a.L, p.end + H) - p.t0;
+#pragma unroll
+        for (int r = 0; r < kConvStep; ++r) {
+            nq[r] = nqd[r] = no_words<P>();
+            if (r < total) {
+                nq[r] = load_words<P>(px + r * a.x.st);
+                nqd[r] = load_words<P>(py + (long long)r * a.D);
+            }
+        }
+        for (int t = p.t0; t < p.end + H; t += kConvStep) {
             Words<P> q[kConvStep], qd[kConvStep];
             const int n = min(a.L, p.end + H) - t, own = p.end - t;   // (may be none)
+            px += kConvStep * a.x.st;
+            py += (long long)kConvStep * a.D;
 #pragma unroll
             for (int r = 0; r < kConvStep; ++r) {
-                q[r] = qd[r] = no_words<P>();
-                if (r < n) {
-                    q[r] = load_words<P>(px + r * a.x.st);
-                    qd[r] = load_words<P>(py + (long long)r * a.D);
+                q[r] = nq[r];
+                qd[r] = nqd[r];
+                nq[r] = nqd[r] = no_words<P>();
+                if (r + kConvStep < n) {
+                    nq[r] = load_words<P>(px + r * a.x.st);
+                    nqd[r] = load_words<P>(py + (long long)r * a.D);
                 }
             }
             const uint32_t history = next_starts<H>(starts);
@@ -482,7 +498,7 @@ cudaError_t by_width(int W, int silu, F&& f) {
 
 }  // namespace
 
-int conv_bwd_parts(int B, int L, int D) { return (int)conv_tiles(B, L, conv_run(B, L, D, kConvBwdCtas)); }
+int conv_bwd_parts(int B, int L, int D, int W) { return (int)conv_tiles(B, L, conv_run(B, L, D, conv_bwd_ctas(W))); }
 
 cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl) {
     const int run = conv_run(a.B, a.L, a.D, kConvFwdCtas);
@@ -500,7 +516,7 @@ cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl)
 }
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& g, cudaStream_t s, bool pdl) {
     const dim3 grid((unsigned)((long long)g.parts * ((g.f.D + 64 * kConvPairs - 1) / (64 * kConvPairs))));
-    const int run = conv_run(g.f.B, g.f.L, g.f.D, kConvBwdCtas);
+    const int run = conv_run(g.f.B, g.f.L, g.f.D, conv_bwd_ctas(g.f.W));
     return by_width(g.f.W, g.f.silu, [&](auto w, auto silu) {
         return launch_ex(causal_conv_bwd_kernel<decltype(w)::value, decltype(silu)::value>, grid, dim3(32 * kConvWarps), 0, s,
                          pdl, g, run);

@@ -730,7 +730,7 @@ struct ConvBwdArgs {
     float *dw, *dbias;
     uint32_t* status;            // cleared
 };
-int conv_bwd_parts(int B, int L, int D);   // its CTAs along time
+int conv_bwd_parts(int B, int L, int D, int W);   // its CTAs along time
 cudaError_t launch_causal_conv(const ConvArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl);
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& a, cudaStream_t s, bool pdl);

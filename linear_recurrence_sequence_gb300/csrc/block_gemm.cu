@@ -300,9 +300,9 @@ __global__ void __launch_bounds__(kBgThreads, 1)
         tmem_alloc(&s_tmem, kBgTmemCols);
         tmem_fence_before_sync();
     }
-    pdl_trigger();
-    pdl_wait();
     __syncthreads();
+    pdl_trigger();   // not before the allocation: see umma.cuh
+    pdl_wait();
     if (MC) cluster_sync();   // both CTAs' barriers exist before either reaches the other's
     tmem_fence_after_sync();
     const uint32_t tmem = s_tmem;

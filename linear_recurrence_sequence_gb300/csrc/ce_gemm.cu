@@ -352,11 +352,11 @@ __global__ void __launch_bounds__(kCeThreads, 1)
         tmem_alloc2(&s_tmem, kCeTmemCols);
         tmem_fence_before_sync();
     }
-    pdl_trigger();
+    __syncthreads();
+    pdl_trigger();   // not before the allocation: see umma.cuh
     pdl_wait();
     // a call's first kernel clears the status word and the rows' ticket (a wait gives up 0.2 s from here at the soonest)
     if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) a.status[0] = a.status[1] = 0u;
-    __syncthreads();
     cluster_sync();   // the pair's barriers and tensor memory exist
     tmem_fence_after_sync();
     const uint32_t tmem = s_tmem;

@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(kPgThreads, 1)
         tmem_alloc(&s_tmem, tcols);
         tmem_fence_before_sync();
     }
-    pdl_trigger();
-    pdl_wait();
     __syncthreads();
+    pdl_trigger();   // not before the allocation: see umma.cuh
+    pdl_wait();
     tmem_fence_after_sync();
     const uint32_t tmem = s_tmem;
     volatile int* abort_flag = &s_abort;

@@ -388,11 +388,11 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     constexpr int IT = (kBT + W::RPI - 1) / W::RPI;
     extern __shared__ __align__(16) uint8_t buf[];
     __shared__ uint32_t s_tmem;
-    if (threadIdx.x < 32) tmem_alloc(&s_tmem, kBwdTmem);
+    pdl_wait();
+    if (threadIdx.x < 32) tmem_alloc(&s_tmem, kBwdTmem);   // not before the wait: see umma.cuh
     tmem_fence_before_sync();
     __syncthreads();
     tmem_fence_after_sync();
-    pdl_wait();
     const SsmArgs& a = g.f;
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
     const BwdPlace p = bwd_place(a, g.nchunk, 0);
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
             g.dbc[((row + t) * a.ngq + gq) * (2 * W::NP) + n] = v;
         }
     }
-    // late, as in ssm_maps_kernel (and a dependent kernel that asks for tensor memory finds every CTA of this one with its own)
+    // late, as in ssm_maps_kernel
     pdl_trigger();
     tmem_fence_before_sync();
     __syncthreads();

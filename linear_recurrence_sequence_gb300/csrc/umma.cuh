@@ -39,7 +39,12 @@ __host__ __device__ constexpr uint32_t umma_idesc_bf16(int M, int N) {
 }
 
 // Tensor-memory allocation of `ncols` columns (a power of two >= 32) by one
-// whole warp; the base address is written to *slot (shared memory).
+// whole warp; the base address is written to *slot (shared memory).  It waits
+// until the SM has the columns free.  A CTA that holds columns while it waits for
+// the kernel ahead must not be able to keep a CTA of that kernel waiting for its
+// own.  So a kernel issues pdl_trigger() only behind a barrier after its
+// allocation (what starts then finds every CTA ahead with its columns), and one that leaves
+// the SM room for other kernels' CTAs, which may be a library's, allocates after pdl_wait().
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)),
                  "r"(ncols)

@@ -1026,7 +1026,7 @@ def selective_scan_backward(dy, dhT, x, delta, a_log, b, c, d_skip, delta_bias, 
     o = {"dx": dx, "ddelta": dd, "da_log": _like(a_log, out, "da_log"), "db": _same(b, out, "db", states, gdt, dev),
          "dc": _same(c, out, "dc", states, gdt, dev), "dd_skip": None if d_skip is None else _like(d_skip, out, "dd_skip"),
          "ddelta_bias": None if delta_bias is None else _like(delta_bias, out, "ddelta_bias"), "dgate": dg,
-         "dh0": None if h0 is None else _same(h0, out, "dh0", (B, D, N), f32, dev)}
+         "dh0": None if h0 is None else _same(dhT, out, "dh0", (B, D, N), f32, dev)}
     st = _load().selective_scan_backward(dy.data_ptr(), _ptr(dhT), _ref(xr), _ref(dr), a_log.data_ptr(), _ref(br), _ref(cr),
                                          _ptr(d_skip), _ptr(delta_bias), _ref(gr), _ptr(reset), B, L, D, N,
                                          saved.data_ptr(), _ref(dxr), _ref(ddr), o["da_log"].data_ptr(),

@@ -1478,11 +1478,16 @@ bool rows_in_words(const lrs_rows* r, int width, int n) {
     return width % n == 0 && reinterpret_cast<uintptr_t>(r->data) % (2 * n) == 0 && r->batch_stride % n == 0 &&
            r->token_stride % n == 0;
 }
-// Whether no two of these begin at the same place (NULL: not there).
-bool apart(std::initializer_list<const void*> list) {
-    for (auto i = list.begin(); i != list.end(); ++i)
-        for (auto j = list.begin(); j != i; ++j)
-            if (*i != nullptr && *i == *j) return false;
+// Whether none of the outputs begins where an input or another output does (NULL: not there; the inputs among
+// themselves may lie where they like).
+bool apart(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        if (*o == nullptr) continue;
+        for (auto p = outs.begin(); p != o; ++p)
+            if (*p == *o) return false;
+        for (const void* i : ins)
+            if (i == *o) return false;
+    }
     return true;
 }
 const void* data_of(const lrs_rows* r) { return r == nullptr ? nullptr : r->data; }
@@ -1547,7 +1552,7 @@ int causal_conv_forward(const lrs_rows* x, const float* weight, const float* bia
     const int st = check_conv_shape(B, L, D, W);
     if (st != LRS_OK) return st;
     if (!rows_in_ok(x) || !req(weight) || !opt(bias) || !opt(state) || !req(y) || !opt(state_out) ||
-        (state != nullptr && state_out == state) || y == x->data)
+        !apart({y, state_out}, {x->data, weight, bias, state, reset}))
         return LRS_ERR_ARG;
     ConvArgs a = conv_args(x, weight, bias, state, reset, B, L, D, W, silu);
     a.y = static_cast<uint16_t*>(y);
@@ -1560,7 +1565,9 @@ int causal_conv_step(const lrs_rows* x, const float* weight, const float* bias, 
                      int B, int D, int W, int silu, void* y, cudaStream_t stream) {
     const int st = check_conv_shape(B, 1, D, W);
     if (st != LRS_OK) return st;
-    if (!rows_in_ok(x) || !req(weight) || !opt(bias) || !req(state) || !req(y)) return LRS_ERR_ARG;
+    if (!rows_in_ok(x) || !req(weight) || !opt(bias) || !req(state) || !req(y) ||
+        !apart({y, state}, {x->data, weight, bias, reset}))
+        return LRS_ERR_ARG;
     ConvArgs a = conv_args(x, weight, bias, nullptr, reset, B, 1, D, W, silu);
     a.y = static_cast<uint16_t*>(y);
     a.state_out = static_cast<uint16_t*>(state);
@@ -1575,7 +1582,8 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
     if (st != LRS_OK) return st;
     if (!req(dy) || !rows_in_ok(x) || !req(weight) || !opt(bias) || !opt(state) || !rows_out_ok(dx, B, L, D) ||
         !req(dweight) || !opt(dbias) || !opt(dstate) || (state == nullptr && dstate != nullptr) || !req(scratch) ||
-        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) || dx->data == dy || dx->data == x->data)
+        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) ||
+        !apart({dx->data, dstate}, {dy, x->data, weight, bias, state, reset}))
         return LRS_ERR_ARG;
     ConvBwdArgs g = {};
     g.f = conv_args(x, weight, bias, state, reset, B, L, D, W, silu);
@@ -1717,7 +1725,8 @@ int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float
     const int st = check_ssm_shape(B, L, D, N);
     if (st != LRS_OK) return st;
     if (!ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !opt(h0) || !req(y) || !req(hT) ||
-        !opt(saved) || !req(scratch) || y == x->data || y == delta->data || y == data_of(gate))
+        !opt(saved) || !req(scratch) ||
+        !apart({y}, {x->data, delta->data, a_log, b->data, c->data, d_skip, delta_bias, data_of(gate), h0, reset, hT}))
         return LRS_ERR_ARG;
     SsmArgs a = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);
     ssm_place(a, ssm_scratch(B, L, D, N, false), scratch);
@@ -1738,7 +1747,9 @@ int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a
                         float* state, const uint8_t* reset, int B, int D, int N, void* y, cudaStream_t stream) {
     const int st = check_ssm_shape(B, 1, D, N);
     if (st != LRS_OK) return st;
-    if (!ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !req(state) || !req(y)) return LRS_ERR_ARG;
+    if (!ssm_inputs_ok(x, delta, a_log, b, c, d_skip, delta_bias, gate) || !req(state) || !req(y) ||
+        !apart({y, state}, {x->data, delta->data, a_log, b->data, c->data, d_skip, delta_bias, data_of(gate), reset}))
+        return LRS_ERR_ARG;
     SsmArgs a = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, 1, D, N);
     a.y = static_cast<uint16_t*>(y);
     LRS_LAUNCH(KID_SSM_STEP, stream, launch_ssm_step(a, state, stream, pdl_ok()));
@@ -1760,10 +1771,9 @@ int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x,
         (gate != nullptr ? !rows_out_ok(dgate, B, L, D) : dgate != nullptr) || !opt(dh0) || !req(scratch) ||
         (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32))
         return LRS_ERR_ARG;
-    // (the inputs among themselves may lie where they like)
-    for (const void* in : {dy, (const void*)x->data, (const void*)delta->data, (const void*)b->data, (const void*)c->data,
-                           data_of(gate)})
-        if (!apart({in, dx->data, ddelta->data, data_of(dgate), db, dc})) return LRS_ERR_ARG;
+    if (!apart({dx->data, ddelta->data, data_of(dgate), db, dc},
+               {dy, x->data, delta->data, a_log, b->data, c->data, d_skip, delta_bias, data_of(gate), reset}))
+        return LRS_ERR_ARG;
     const SsmScratch l = ssm_scratch(B, L, D, N, true);
     SsmBwdArgs g = {};
     g.f = ssm_args(x, delta, a_log, b, c, d_skip, delta_bias, gate, reset, B, L, D, N);
@@ -1840,7 +1850,7 @@ int embedding_forward(const int64_t* tokens, const void* w, int w_dtype, int T, 
     const int st = check_embed_shape(T, V, D);
     if (st != LRS_OK) return st;
     if (!req_each(tokens) || !req(w) || !req(y) || (w_dtype != LRS_GRAD_BF16 && w_dtype != LRS_GRAD_FP32) ||
-        !std::isfinite(scale))
+        !std::isfinite(scale) || !apart({y}, {tokens, w}))
         return LRS_ERR_ARG;
     EmbedArgs a = {tokens, w, T, V, D, w_dtype == LRS_GRAD_FP32, scale, static_cast<uint16_t*>(y)};
     LRS_LAUNCH(KID_EMBED_FWD, stream, launch_embedding(a, stream, pdl_ok()));
@@ -1852,7 +1862,8 @@ int embedding_backward(const void* dy, const int64_t* tokens, int T, int V, int 
     const int st = check_embed_shape(T, V, D);
     if (st != LRS_OK) return st;
     if (!req(dy) || !req_each(tokens) || !req(dw) || !req(scratch) ||
-        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) || !std::isfinite(scale))
+        (grad_dtype != LRS_GRAD_BF16 && grad_dtype != LRS_GRAD_FP32) || !std::isfinite(scale) ||
+        !apart({dw}, {dy, tokens}))
         return LRS_ERR_ARG;
     const EmbedScratch l = embed_scratch(T, V, D);
     EmbedBwdArgs a = {};

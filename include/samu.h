@@ -486,6 +486,289 @@ int linear_ce_workspace_bytes(int T, int V, int D, int grad_dtype, size_t* forwa
  * (a logit is within about 1.3e-6 of its partial sums' size, chains of 1024 products
  * being added up apart); exponentials are the GPU's fast ones (2^-22) and their sums
  * FP32; the sum of the losses is right to its last FP32 bit; all in a fixed order.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, softcap
+ * negative or not finite), LRS_ERR_UNSUPPORTED (D not a multiple of 8, T or V
+ * over 2^23, D over 2^16), LRS_ERR_CUDA. */
+int linear_ce_forward(const void* h, const void* w, const int64_t* target, int T, int V, int D, float softcap,
+                      float* loss, float* lse, float* total, void* scratch, cudaStream_t stream);
+
+/* Backward: for the cotangents dloss of the losses
+ *   dz'_tv = dloss_t (e^{z'_tv - lse_t} - [v = target_t]),  dz = dz' (1 - (z'/c)^2),
+ *   dh = dz w,  dw = dz^T h,
+ * with the logits formed again, one piece of the vocabulary at a time.
+ *   h, w, target, T, V, D, softcap: the forward's (in)
+ *   lse      [T] FP32 (in; 4-byte aligned, as total here)
+ *   dloss    [T] FP32 (in), or NULL for the mean over the tokens counted
+ *            (1 / total[1] each; total is the forward's and may be NULL only
+ *            if dloss is given)
+ *   dh [T,D], dw [V,D]: BF16 or FP32 by grad_dtype (out)
+ *   scratch  linear_ce_workspace_bytes().backward bytes
+ * dz enters the two contractions in BF16 (LRS_GRAD_BF16: the results are
+ * rounded to BF16 themselves; weights that differ cost them a third more error than
+ * that rounding), or as the sum of three BF16 parts (LRS_GRAD_FP32: 24 significant
+ * bits, three times the products).  A dloss that is not finite reaches its own row of
+ * dh, and dw.  Deterministic:
+ * every sum runs in a fixed order.  Errors: as the forward, plus LRS_ERR_ARG
+ * for an unknown grad_dtype. */
+int linear_ce_backward(const void* h, const void* w, const int64_t* target, const float* lse, const float* dloss,
+                       const float* total, int T, int V, int D, float softcap, void* dh, void* dw, int grad_dtype,
+                       void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Norms before and after a residual branch, with its gate and scale         */
+/* ======================================================================== */
+
+/* Joins a bare mixer to the residual stream and forms the next layer's input:
+ *   u = scale * GeLU(gate) * RMSNorm(y; gamma_post),  r = x + u,
+ *   h = RMSNorm(r; gamma_pre),   RMSNorm(a; g) = a / sqrt(mean(a^2) + eps) * g,
+ * row by row over [T,D], with the block's GeLU (tanh form).  FP32 arithmetic
+ * throughout (the GeLU, by the GPU's fast exponential, within 2^-20); r and h are rounded to BF16 once (h is formed from the unrounded r).
+ * With y NULL there is no branch: h = RMSNorm(x; gamma_pre), the norm ahead of
+ * a head; gate, gamma_post, scale and r are then NULL too.
+ *
+ * Bytes of `saved` (the rows' two reciprocal norms) and `scratch` (the
+ * backward's partial sums).  Pure host function. */
+int gated_norm_workspace_bytes(int T, int D, size_t* saved_bytes, size_t* scratch_bytes);
+
+/* Forward.
+ *   x          [T,D] BF16 (in): the residual stream
+ *   y          [T,D] BF16 (in): the branch, or NULL
+ *   gate       [T,D] BF16 (in), or NULL for 1 in place of GeLU(gate)
+ *   gamma_post, scale, gamma_pre   [D] FP32 (in), or NULL for ones
+ *   eps        in (0, 1]
+ *   r          [T,D] BF16 (out);  h [T,D] BF16 (out)
+ *   saved      gated_norm_workspace_bytes().saved bytes (out), or NULL where no
+ *              backward follows
+ * One launch; a decoding step is T = the number of sequences.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, T or D < 1, eps out of
+ * range, a gate, gamma_post, scale or r without a branch), LRS_ERR_UNSUPPORTED
+ * (D not a multiple of 8, or D > 8192), LRS_ERR_CUDA. */
+int gated_norm_forward(const void* x, const void* y, const void* gate, const float* gamma_post, const float* scale,
+                       const float* gamma_pre, int T, int D, float eps, void* r, void* h, void* saved,
+                       cudaStream_t stream);
+
+/* Backward for the cotangents dr (or NULL for zero) and dh, [T,D] BF16.
+ *   x ... eps  the forward's (in);  saved: the forward's
+ *   dx, dy, dgate [T,D] BF16 (out);  dgamma_post, dscale, dgamma_pre [D] FP32
+ *              (out, in a fixed order of summation).  dy, dgamma_post, dscale
+ *              are NULL without a branch, dgate without a gate; the gradient of
+ *              a vector that was NULL (ones) is written all the same.
+ *   scratch    gated_norm_workspace_bytes().scratch bytes
+ * Errors: as the forward. */
+int gated_norm_backward(const void* dr, const void* dh, const void* x, const void* y, const void* gate,
+                        const float* gamma_post, const float* scale, const float* gamma_pre, int T, int D, float eps,
+                        const void* saved, void* dx, void* dy, void* dgate, float* dgamma_post, float* dscale,
+                        float* dgamma_pre, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* AdamW over many tensors                                                   */
+/* ======================================================================== */
+
+/* One parameter tensor of n values and its optimiser state (device pointers).
+ *   param   FP32, or BF16 if master is given (then the rounded copy that the
+ *           layers read; the FP32 master is what the step updates)
+ *   grad    FP32 or BF16 by grad_dtype (LRS_GRAD_*)
+ *   m, v    FP32 first and second moments; or, with m_scale and v_scale, E4M3
+ *           codes with one FP32 scale for every 256 consecutive values
+ *           (ceil(n / 256) of them): m = scale code, sqrt(v) = scale code, the
+ *           scale being the largest magnitude of the 256 divided by 448.  A
+ *           sqrt(v) above 0 never rounds to 0; 256 values below 2^-100 are
+ *           stored as zeros.  All of them start as zeros.
+ *   weight_decay  of this tensor */
+typedef struct {
+    void* param; float* master; const void* grad; void* m; void* v; float* m_scale; float* v_scale;
+    int64_t n; float weight_decay; int grad_dtype;
+} lrs_adamw_tensor;
+
+/* Scratch bytes of a step over `count` tensors.  Errors: LRS_ERR_ARG. */
+int lrs_adamw_scratch_bytes(int count, size_t* bytes);
+
+/* One AdamW step over every tensor of the list (a host array, read before the
+ * call returns):
+ *   t = step + 1;  N = sqrt(sum of g^2 over every tensor);
+ *   k = max_norm / N where N > max_norm > 0, else 1;
+ *   m = b1 m + (1 - b1) k g;  v = b2 v + (1 - b2) (k g)^2;
+ *   p = p (1 - lr wd) - lr (m / (1 - b1^t)) / (sqrt(v / (1 - b2^t)) + eps).
+ *   step      one int32 (device, in/out): steps taken so far
+ *   lr        one FP32 (device, in)
+ *   max_norm  0 for no clipping; otherwise a step whose N is not finite
+ *             changes nothing (parameters, states and step keep their values)
+ *   norm      one FP32 (device, out): N; may be NULL without clipping (then it
+ *             is not written)
+ *   scratch   lrs_adamw_scratch_bytes() bytes
+ * FP32 arithmetic; the norm in a fixed order of summation, within 2^-19 of its
+ * value wherever FP32 holds that value (squares above FP32's range are scaled; of
+ * gradients whose root mean square is below 2^-65, squares are lost); the
+ * quotient by the root, and the root itself with 32-bit states, within 2^-22 of the
+ * step (the GPU's fast forms).  Everything that changes from step to step is on the device: a
+ * captured graph steps correctly.  Two launches for up to 400 tensors.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer, n < 1, one scale without
+ * the other, a negative weight decay, betas outside [0, 1), eps <= 0),
+ * LRS_ERR_UNSUPPORTED (over 2^40 values), LRS_ERR_CUDA. */
+int lrs_adamw_step(const lrs_adamw_tensor* tensors, int count, int32_t* step, const float* lr, double beta1,
+                   double beta2, float eps, float max_norm, float* norm, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Rows with strides                                                         */
+/* ======================================================================== */
+
+/* [B,L] rows of values that are contiguous within a row: a part of a wider
+ * projection's output need not be copied out.  Strides in elements.  Where an
+ * entry reads rows 16 bytes at a time (all but b and c of the scan), data is
+ * 16-byte aligned and both strides are multiples of 8; an input's strides may be
+ * 0 (one row for all), an output's rows must not overlap.  The outputs of the
+ * entries below overlap neither each other nor an input, but where an entry says so
+ * (other threads may still read what one writes); those that hold a value a token or a
+ * carried input (y, state_out, dx, ddelta, dgate, db, dc, dstate, and the embedding's dw)
+ * are refused where they begin at an input or another of them. */
+typedef struct {
+    void* data;
+    int64_t batch_stride, token_stride;
+} lrs_rows;
+
+/* ======================================================================== */
+/* Short causal convolution                                                  */
+/* ======================================================================== */
+
+/* The convolution ahead of a recurrent mixer, every channel with its own taps:
+ *   pre_t = bias + sum_{j < W} w_j x_{t-j},   y_t = SiLU(pre_t) (silu != 0) or pre_t.
+ * A sequence start (reset[b,t] != 0) at t - j + 1 .. t cuts tap j, as in the
+ * RecurrentBlock.  Inputs before the row come from `state`: its rows are the W - 1
+ * inputs before the first token, in their order (NULL: zeros).  W is 2, 3 or 4.
+ * FP32 arithmetic, one rounding to BF16 (SiLU by the GPU's fast exponential and
+ * reciprocal, 2^-20 relative).
+ *
+ * Scratch bytes of the backward.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as causal_conv_forward. */
+int causal_conv_workspace_bytes(int B, int L, int D, int W, size_t* backward_bytes);
+
+/* Forward.
+ *   x          [B,L] rows of D BF16 (in)
+ *   weight     [W,D] FP32 (in): row j multiplies the input j tokens earlier
+ *   bias       [D] FP32 (in) or NULL
+ *   state      [B,W-1,D] BF16 (in) or NULL
+ *   reset      [B,L] bytes (in) or NULL
+ *   y          [B,L,D] BF16 (out)
+ *   state_out  [B,W-1,D] BF16 (out) or NULL: the state after the row, zeros in
+ *              place of inputs before the last sequence's start.  Not `state` itself.
+ * Rows padded on the left, with a reset at the first token, give every sequence its
+ * own state_out.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a shape below 1, y or
+ * state_out where an input or the other begins), LRS_ERR_UNSUPPORTED (D not a multiple
+ * of 8, W not 2 to 4, over 2^30 tokens or 2^40 values), LRS_ERR_CUDA. */
+int causal_conv_forward(const lrs_rows* x, const float* weight, const float* bias, const void* state,
+                        const uint8_t* reset, int B, int L, int D, int W, int silu, void* y, void* state_out,
+                        cudaStream_t stream);
+
+/* One token of each of B sequences: x is [B] rows (token_stride: 0),
+ * reset [B], y [B,D]; the state moves on in place.  Bit for bit what the forward
+ * gives for the same inputs.  Errors: as the forward (y and state where an input or the
+ * other begins). */
+int causal_conv_step(const lrs_rows* x, const float* weight, const float* bias, void* state, const uint8_t* reset,
+                     int B, int D, int W, int silu, void* y, cudaStream_t stream);
+
+/* Backward for the cotangent dy [B,L,D] BF16.
+ *   x ... silu  the forward's (in)
+ *   dx       [B,L] rows (out), dstate [B,W-1,D] (out) or NULL: BF16 or FP32 by
+ *            grad_dtype.  A cotangent of state_out is the caller's to add to dx.
+ *   dweight  [W,D] FP32 (out);  dbias [D] FP32 (out) or NULL
+ *   scratch  causal_conv_workspace_bytes() bytes
+ * Sums in a fixed order.  Errors: as the forward, plus LRS_ERR_ARG for dstate
+ * without state, for dx or dstate where an input or the other begins and for an unknown
+ * grad_dtype. */
+int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight, const float* bias, const void* state,
+                         const uint8_t* reset, int B, int L, int D, int W, int silu, const lrs_rows* dx, float* dweight,
+                         float* dbias, void* dstate, int grad_dtype, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Selective state space scan                                                */
+/* ======================================================================== */
+
+/* A recurrent mixer beside SAMU and the RG-LRU: every channel has N real states
+ * whose decay and input follow the token,
+ *   dt_t  = softplus(delta_t + delta_bias),   a_tn = e^(-e^(a_log_n) dt_t)
+ *   h_tn  = a_tn h_{t-1,n} + dt_t x_t b_tn    (a_tn = 0 where reset[b,t] != 0)
+ *   y_t   = (sum_n c_tn h_tn + d_skip x_t) SiLU(gate_t).
+ * dt, x, gate and d_skip are a channel's own, b and c are shared by a token's
+ * channels.  A token whose delta is -inf and whose x and b are finite has dt = 0: it
+ * leaves the state as it is (padding behind a sequence; padding ahead of one is cut
+ * off by a reset at its first token, whatever it holds).  D channels, N from 1 to 64.
+ * FP32 arithmetic: exponentials by the GPU's fast one (2^-22 relative each), dt within
+ * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0); y is rounded
+ * to BF16 once.  Everything runs in a fixed order.
+ *
+ * Bytes of `saved` (what the forward keeps for a backward: the states before every
+ * eighth token, 4 N bytes for 8 values of x), of the forward's and of the backward's
+ * scratch.  Any output pointer may be NULL.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as selective_scan_forward. */
+int selective_scan_workspace_bytes(int B, int L, int D, int N, size_t* saved_bytes, size_t* forward_bytes,
+                                   size_t* backward_bytes);
+
+/* Forward.
+ *   x, delta    [B,L] rows of D BF16 (in)
+ *   a_log       [D,N] FP32 (in)
+ *   b, c        [B,L] rows of N BF16 (in; any alignment and strides)
+ *   d_skip      [D] FP32 (in) or NULL for zeros
+ *   delta_bias  [D] FP32 (in) or NULL for zeros
+ *   gate        [B,L] rows of D BF16 (in), or NULL for 1 in place of SiLU(gate)
+ *   h0          [B,D,N] FP32 (in) or NULL for zeros
+ *   reset       [B,L] bytes (in) or NULL
+ *   y           [B,L,D] BF16 (out);  hT [B,D,N] FP32 (out; may be h0)
+ *   saved       selective_scan_workspace_bytes().saved bytes (out), or NULL where no
+ *               backward follows
+ *   scratch     .forward bytes
+ * One launch, or three where batch and channels alone leave the GPU short of work.
+ * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a token_stride over 2^26,
+ * a shape below 1, y where an input or hT begins), LRS_ERR_UNSUPPORTED (D not a multiple
+ * of 8, N over 64, over 2^30 tokens or 2^40 values or states), LRS_ERR_CUDA. */
+int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
+                           const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
+                           const float* h0, const uint8_t* reset, int B, int L, int D, int N, void* y, float* hT,
+                           void* saved, void* scratch, cudaStream_t stream);
+
+/* One token of each of B sequences: x, delta, b, c, gate are [B] rows (token_stride:
+ * 0), reset [B], y [B,D] BF16 (out); state [B,D,N] FP32 moves on in place.
+ * One launch.  Errors: as the forward (y and state where an input or the other begins). */
+int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
+                        const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
+                        float* state, const uint8_t* reset, int B, int D, int N, void* y, cudaStream_t stream);
+
+/* Backward for the cotangents dy [B,L,D] BF16 of y and dhT [B,D,N] FP32 of hT (or
+ * NULL for zeros).
+ *   x ... reset  the forward's (in; h0 is not read: saved holds it);  saved: the forward's
+ *   dx, ddelta, dgate  [B,L] rows of D (out), db, dc [B,L,N] (out): BF16 or FP32 by
+ *            grad_dtype.  dgate is NULL without a gate.
+ *   da_log   [D,N] FP32 (out)
+ *   dd_skip, ddelta_bias  [D] FP32 (out) or NULL (and NULL without the vector)
+ *   dh0      [B,D,N] FP32 (out; may be dhT) or NULL
+ *   scratch  selective_scan_workspace_bytes().backward bytes
+ * Errors: as the forward, plus LRS_ERR_ARG for an output without its input, for one
+ * that begins where an input or another begins and for an unknown grad_dtype. */
+int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x, const lrs_rows* delta,
+                            const float* a_log, const lrs_rows* b, const lrs_rows* c, const float* d_skip,
+                            const float* delta_bias, const lrs_rows* gate, const uint8_t* reset, int B, int L, int D,
+                            int N, const void* saved, const lrs_rows* dx, const lrs_rows* ddelta, float* da_log, void* db,
+                            void* dc, float* dd_skip, float* ddelta_bias, const lrs_rows* dgate, float* dh0,
+                            int grad_dtype, void* scratch, cudaStream_t stream);
+
+/* ======================================================================== */
+/* Embedding                                                                 */
+/* ======================================================================== */
+
+/* The lookup at the bottom of a stack, y_t = scale w[token_t], and its gradient,
+ *   dw[v] = scale sum of dy_t over the tokens t with token_t = v.
+ * A negative token is padding: a row of zeros that reaches no gradient.  A token
+ * >= V has no row: its y is NaN, it reaches no gradient, and lrs_device_status
+ * returns LRS_ERR_ARG for the backward's scratch.
+ *
+ * Scratch bytes of the backward.  Pure host function.
+ * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as embedding_forward. */
+int embedding_workspace_bytes(int T, int V, int D, size_t* backward_bytes);
+
+/* Forward.
+ *   tokens   [T] int64 (in; 8-byte aligned)
+ *   w        [V,D] (in), BF16 or FP32 by w_dtype (LRS_GRAD_BF16, LRS_GRAD_FP32)
+ *   y        [T,D] BF16 (out), rounded once
  * Errors: LRS_ERR_ARG (null or misaligned pointer, T, V or D < 1, unknown w_dtype,
  * scale not finite, y where an input begins), LRS_ERR_UNSUPPORTED (D not a multiple of
  * 8 or over 2^16, V over 2^23, T over 2^28, T D over 2^40), LRS_ERR_CUDA. */
@@ -562,6 +845,3 @@ int samu_forward_noalloc_status(int* status, cudaStream_t stream);
 #endif
 
 #endif /* LRS_SAMU_H */
- * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a token_stride over 2^26,
- * a shape below 1, y where an input or hT begins), LRS_ERR_UNSUPPORTED (D not a multiple
- * of 8, N over 64, over 2^30 tokens or 2^40 values or states), LRS_ERR_CUDA. */

@@ -720,7 +720,8 @@ int selective_scan_workspace_bytes(int B, int L, int D, int N, size_t* saved_byt
  * One launch, or three where batch and channels alone leave the GPU short of work.
  * Errors: LRS_ERR_ARG (null or misaligned pointer or stride, a token_stride over 2^26,
  * a shape below 1, y where an input or hT begins), LRS_ERR_UNSUPPORTED (D not a multiple
- * of 8, N over 64, over 2^30 tokens or 2^40 values or states), LRS_ERR_CUDA. */
+ * of 8 or, of more than one token, over 2^26, N over 64, over 2^30 tokens or 2^40 values
+ * or states), LRS_ERR_CUDA. */
 int selective_scan_forward(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b,
                            const lrs_rows* c, const float* d_skip, const float* delta_bias, const lrs_rows* gate,
                            const float* h0, const uint8_t* reset, int B, int L, int D, int N, void* y, float* hT,

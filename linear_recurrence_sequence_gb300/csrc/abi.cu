@@ -1610,12 +1610,16 @@ namespace {
 
 // Resident per SM, by registers (the backward's main kernel: by tensor memory).
 constexpr int kSsmFwdWarps = 16, kSsmBwdCtas = 2;
+// From a token's row to the next's at most: rows are addressed from the first of a tile's (eight at most) with 32 bits.
+constexpr int kSsmTokenStride = 1 << 26;
 
 int check_ssm_shape(int B, int L, int D, int N) {
     if (B < 1 || L < 1 || D < 1 || N < 1) return LRS_ERR_ARG;
     if (D % 8 != 0 || N > 64 || (long long)B * L > (1LL << 30) || (long long)B * L * D > (1LL << 40) ||
         (long long)B * D * N > (1LL << 40))
         return LRS_ERR_UNSUPPORTED;
+    // the rows of a tile of dy, which are D apart, are addressed with 32 bits (as are those with strides: ssm_rows_ok)
+    if (L > 1 && D > kSsmTokenStride) return LRS_ERR_UNSUPPORTED;
     // CTAs of the launches: a warp's channels and 16 tokens each at least, or one of 8
     const SsmSplit w = ssm_split(D, N);
     if ((long long)B * ((L + 15) / 16) * w.groups > 0x7fffffffLL) return LRS_ERR_UNSUPPORTED;
@@ -1661,9 +1665,8 @@ SsmScratch ssm_scratch(int B, int L, int D, int N, bool backward) {
     return s;
 }
 
-// Rows are addressed from the first of a tile's with 32 bits.
 bool ssm_rows_ok(const lrs_rows* r, bool each) {
-    return (each ? rows_each_ok(r) : rows_in_ok(r)) && r->token_stride <= (1LL << 26);
+    return (each ? rows_each_ok(r) : rows_in_ok(r)) && r->token_stride <= kSsmTokenStride;
 }
 bool ssm_inputs_ok(const lrs_rows* x, const lrs_rows* delta, const float* a_log, const lrs_rows* b, const lrs_rows* c,
                    const float* d_skip, const float* delta_bias, const lrs_rows* gate) {

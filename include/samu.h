@@ -693,6 +693,8 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
  * channels.  A token whose delta is -inf and whose x and b are finite has dt = 0: it
  * leaves the state as it is (padding behind a sequence; padding ahead of one is cut
  * off by a reset at its first token, whatever it holds).  D channels, N from 1 to 64.
+ * e^a_log ends at FP32's largest value (a_log from 88 on: nothing of a state outlasts a
+ * token but one with dt = 0); the backward of a token with dt = 0 takes a_log up to 80.
  * FP32 arithmetic: exponentials by the GPU's fast one (2^-22 relative each), dt within
  * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0); y is rounded
  * to BF16 once.  Everything runs in a fixed order.

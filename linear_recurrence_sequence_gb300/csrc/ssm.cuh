@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <cfloat>
 
 #include "kernels.cuh"
 
@@ -61,8 +62,14 @@ __device__ __forceinline__ f2x softplus2(f2x raw) {
 // 1 / (1 + e^-r)
 __device__ __forceinline__ float ssm_sigmoid(float r) { return rcp_approx(1.f + ex2_approx(-r * kLog2e)); }
 
+// A rate (negative), FP32's largest in place of infinity, whose product with a step of 0 would be NaN.  NaN stays.
+__device__ __forceinline__ float finite_rate(float r) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(r), "f"(-FLT_MAX));
+    return o;
+}
 // log2 of what a state keeps in a unit of time: -e^a_log log2 e.
-__device__ __forceinline__ float ssm_rate(float a_log) { return -expf(a_log) * kLog2e; }
+__device__ __forceinline__ float ssm_rate(float a_log) { return finite_rate(-expf(a_log) * kLog2e); }
 
 // 8 BF16 values as FP32 pairs.
 __device__ __forceinline__ void unpack_pairs(const uint4 q, f2x (&v)[4]) {
@@ -240,14 +247,14 @@ __device__ __forceinline__ void load_states(const float* m, bool quads, int c0, 
         }
     }
 }
-// The rates of a lane's states (0 past N and D, where the other operands are zeros too).
+// The rates of a lane's states (1 past N and D, where the states and all that is added to them are zeros).
 __device__ __forceinline__ void load_rates(const float* a_log, bool quads, int c0, int n0, int D, int N, SsmStates& A) {
     float v[kSsmCh][kSsmSt];
     load_states(a_log, quads, c0, n0, D, N, v);
 #pragma unroll
     for (int i = 0; i < kSsmCh; ++i)
 #pragma unroll
-        for (int j = 0; j < kSsmSt; ++j) v[i][j] = c0 + i < D && n0 + j < N ? ssm_rate(v[i][j]) : 0.f;
+        for (int j = 0; j < kSsmSt; ++j) v[i][j] = ssm_rate(v[i][j]);
 #pragma unroll
     for (int j = 0; j < kSsmSt; ++j) {
         A[j][0] = pk2(v[0][j], v[1][j]);

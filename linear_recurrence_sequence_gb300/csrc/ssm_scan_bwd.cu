@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(256) ssm_finish_kernel(const SsmBwdArgs g, int
         const int n = sl % LN * kSsmSt + k;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (c + j < a.D && n < a.N) g.da_log[(c + j) * a.N + n] = -expf(__ldg(a.a_log + (c + j) * a.N + n)) * e[j];
+            if (c + j < a.D && n < a.N) g.da_log[(c + j) * a.N + n] = finite_rate(-expf(__ldg(a.a_log + (c + j) * a.N + n))) * e[j];
         return;
     }
     const long long at = (col - states) * 4, width = (long long)a.groups * W::CW;

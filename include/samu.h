@@ -636,7 +636,8 @@ typedef struct {
  * RecurrentBlock.  Inputs before the row come from `state`: its rows are the W - 1
  * inputs before the first token, in their order (NULL: zeros).  W is 2, 3 or 4.
  * FP32 arithmetic, one rounding to BF16 (SiLU by the GPU's fast exponential and
- * reciprocal, 2^-20 relative).
+ * reciprocal: 2^-20 relative, 2^-23 |pre| more where pre is far below 0, and 0 below
+ * about -87, where the sigmoid leaves FP32's normal range).
  *
  * Scratch bytes of the backward.  Pure host function.
  * Errors: LRS_ERR_ARG, LRS_ERR_UNSUPPORTED as causal_conv_forward. */
@@ -696,8 +697,8 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
  * e^a_log ends at FP32's largest value (a_log from 88 on: nothing of a state outlasts a
  * token but one with dt = 0); the backward of a token with dt = 0 takes a_log up to 80.
  * FP32 arithmetic: exponentials by the GPU's fast one (2^-22 relative each), dt within
- * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0); y is rounded
- * to BF16 once.  Everything runs in a fixed order.
+ * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0), SiLU as the
+ * convolution's; y is rounded to BF16 once.  Everything runs in a fixed order.
  *
  * Bytes of `saved` (what the forward keeps for a backward: the states before every
  * eighth token, 4 N bytes for 8 values of x), of the forward's and of the backward's

@@ -59,7 +59,7 @@ __device__ __forceinline__ f2x softplus2(f2x raw) {
     return fma2(p, w, pk2(fmaxf(a, 0.f), fmaxf(b, 0.f)));
 }
 
-// 1 / (1 + e^-r)
+// 1 / (1 + e^-r) within 2^-20 + 2^-23 max(-r, 0); 0 where it is below 2^-126.
 __device__ __forceinline__ float ssm_sigmoid(float r) { return rcp_approx(1.f + ex2_approx(-r * kLog2e)); }
 
 // A rate (negative), FP32's largest in place of infinity, whose product with a step of 0 would be NaN.  NaN stays.

@@ -33,6 +33,7 @@
  *    by the forward, read by the backward) and `scratch`; sizes come from the
  *    *_workspace_bytes query.  The library never allocates, never frees and
  *    never synchronises the stream.
+ *  - The pointers and the stream belong to the current device.
  *  - Every call is asynchronous on `stream`; outputs are overwritten, never
  *    accumulated.  A scratch buffer must not be used by two calls that may
  *    run concurrently.  `saved` must come from a forward with the same inputs.

@@ -150,10 +150,16 @@ def _ptr(t):
 
 
 def _stream(device) -> int:
-    index = getattr(device, "index", None)
+    """The current stream's handle on `device`, which is the current device (a launch goes there)."""
+    index = device.index if isinstance(device, torch.device) else None
     if index is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    return torch._C._cuda_getCurrentRawStream(index)   # the same handle, without building a Stream object
+        stream = torch.cuda.current_stream(device)
+        index, handle = stream.device.index, stream.cuda_stream
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(index)   # the same, without building a Stream object
+    if index != torch._C._cuda_getDevice():
+        raise ValueError(f"cuda:{index} is not the current device: call under torch.cuda.device({index})")
+    return handle
 
 
 def _need(t, name, dtype, device, shape=None):

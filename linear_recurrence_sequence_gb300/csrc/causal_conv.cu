@@ -27,7 +27,7 @@ namespace {
 
 constexpr int kConvStep = 8;      // rows that a thread asks for at a time
 constexpr int kConvWarps = 4;     // runs of a CTA
-constexpr int kConvPairs = 2;     // of channels, a thread
+constexpr int P = 2;              // pairs of channels, a thread
 constexpr int kConvRun = 80;       // tokens of a run at most
 constexpr int kConvSms = 152;
 // Resident per SM, by registers.  Backward with 3 at W = 4 (spills) 4 x 4096 x 1024 takes 32 us, 2 x 32768 x 1024 with
@@ -37,7 +37,7 @@ constexpr int conv_bwd_ctas(int W) { return W == 4 ? 2 : 3; }
 
 // A launch's CTAs: runs of a batch row by spans of channels.
 long long conv_tiles(int B, int L, int run) { return (long long)B * (((long long)L + run * kConvWarps - 1) / (run * kConvWarps)); }
-long long conv_spans(int D) { return (D + 64 * kConvPairs - 1) / (64 * kConvPairs); }
+long long conv_spans(int D) { return (D + 64 * P - 1) / (64 * P); }
 // A run's tokens: those that end soonest, by the rounds that the SMs take with `ctas` CTAs each and a run's own cost, about
 // a step (1 x 8192 x 2560: 72 tokens, one round of 4 CTAs an SM, 39 us backward, 64 tokens 49; 16 x 4096 x 1024: 64 tokens 51 us forward, 80
 // tokens 55).  kConvRun at most: what the words of Starts cover.
@@ -56,43 +56,27 @@ int conv_run(int B, int L, int D, int ctas) {
     return best;
 }
 
-// P pairs of channels of a row: BF16 words, FP32 pairs.
-template <int P>
+// A thread's channels of a row: BF16 words, FP32 pairs.
 struct Words {
     uint32_t w[P];
 };
-template <int P>
-__device__ __forceinline__ Words<P> no_words() {
-    Words<P> o;
+__device__ __forceinline__ Words no_words() {
+    Words o;
 #pragma unroll
     for (int e = 0; e < P; ++e) o.w[e] = 0u;
     return o;
 }
-template <int P>
-__device__ __forceinline__ Words<P> load_words(const uint16_t* p) {
-    Words<P> o;
-    if (P == 2) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-        o.w[0] = q.x;
-        o.w[P - 1] = q.y;
-    } else {
-        o.w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-    }
-    return o;
+__device__ __forceinline__ Words load_words(const uint16_t* p) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+    return {{q.x, q.y}};
 }
-template <int P>
-__device__ __forceinline__ void store_words(uint16_t* p, const Words<P>& o) {
-    if (P == 2)
-        *reinterpret_cast<uint2*>(p) = make_uint2(o.w[0], o.w[P - 1]);
-    else
-        *reinterpret_cast<uint32_t*>(p) = o.w[0];
+__device__ __forceinline__ void store_words(uint16_t* p, const Words& o) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(o.w[0], o.w[1]);
 }
-template <int P>
-__device__ __forceinline__ void unpack_words(const Words<P>& q, f2x (&v)[P]) {
+__device__ __forceinline__ void unpack_words(const Words& q, f2x (&v)[P]) {
 #pragma unroll
     for (int e = 0; e < P; ++e) v[e] = bf2x(q.w[e]);
 }
-template <int P>
 __device__ __forceinline__ void load_vector(const float* p, f2x (&v)[P]) {
 #pragma unroll
     for (int e = 0; e < P; ++e) {
@@ -100,18 +84,16 @@ __device__ __forceinline__ void load_vector(const float* p, f2x (&v)[P]) {
         v[e] = pk2(q.x, q.y);
     }
 }
-template <int P>
 __device__ __forceinline__ void clear(f2x (&v)[P]) {
 #pragma unroll
     for (int e = 0; e < P; ++e) v[e] = 0ull;
 }
-template <int P>
 __device__ __forceinline__ void add_product(f2x (&acc)[P], const f2x (&a)[P], const f2x (&b)[P]) {
 #pragma unroll
     for (int e = 0; e < P; ++e) acc[e] = fma2(a[e], b[e], acc[e]);
 }
 // A window moves on by a token: v[1 ..] <- v[0 ..].
-template <int P, int W>
+template <int W>
 __device__ __forceinline__ void shift_in(f2x (&v)[W][P]) {
 #pragma unroll
     for (int j = W - 1; j > 0; --j)
@@ -172,15 +154,15 @@ __device__ __forceinline__ ConvPlace conv_place(const ConvArgs& a, int run, int 
     return p;
 }
 // The input at token t of the row (before it: the carried ones).
-template <int W, int P>
-__device__ __forceinline__ Words<P> conv_input(const ConvArgs& a, int b, int c, int t) {
-    if (t >= 0) return load_words<P>(a.x.p + (long long)b * a.x.sb + (long long)t * a.x.st + c);
-    if (a.state != nullptr) return load_words<P>(a.state + ((long long)b * (W - 1) + W - 1 + t) * a.D + c);
-    return no_words<P>();
+template <int W>
+__device__ __forceinline__ Words conv_input(const ConvArgs& a, int b, int c, int t) {
+    if (t >= 0) return load_words(a.x.p + (long long)b * a.x.sb + (long long)t * a.x.st + c);
+    if (a.state != nullptr) return load_words(a.state + ((long long)b * (W - 1) + W - 1 + t) * a.D + c);
+    return no_words();
 }
 
 // bias + the taps that are live; v holds the last W inputs, the newest first.
-template <int W, int P, bool CUT>
+template <int W, bool CUT>
 __device__ __forceinline__ void conv_sum(const f2x (&w)[W][P], const f2x (&bias)[P], const f2x (&v)[W][P], uint32_t history,
                                          f2x (&acc)[P]) {
 #pragma unroll
@@ -194,8 +176,8 @@ __device__ __forceinline__ void conv_sum(const f2x (&w)[W][P], const f2x (&bias)
 
 // kConvStep tokens forward.  PLAIN: all of them there, and no start reaches their
 // taps (a group without branches: with a test a token it took twice the instructions).
-template <int W, int P, bool SILU, bool PLAIN>
-__device__ __forceinline__ void conv_group(const Words<P> (&q)[kConvStep], int n, uint32_t history, const f2x (&w)[W][P],
+template <int W, bool SILU, bool PLAIN>
+__device__ __forceinline__ void conv_group(const Words (&q)[kConvStep], int n, uint32_t history, const f2x (&w)[W][P],
                                            const f2x (&bias)[P], f2x (&v)[W][P], uint16_t* py, long long ld) {
 #pragma unroll
     for (int r = 0; r < kConvStep; ++r) {
@@ -203,8 +185,8 @@ __device__ __forceinline__ void conv_group(const Words<P> (&q)[kConvStep], int n
         unpack_words(q[r], v[0]);
         if (!PLAIN && r >= n) continue;
         f2x acc[P];
-        conv_sum<W, P, !PLAIN>(w, bias, v, history >> (kConvStep - 1 - r), acc);
-        Words<P> o;
+        conv_sum<W, !PLAIN>(w, bias, v, history >> (kConvStep - 1 - r), acc);
+        Words o;
 #pragma unroll
         for (int e = 0; e < P; ++e) o.w[e] = x2bf(SILU ? silu2(acc[e]) : acc[e]);
         store_words(py + r * ld, o);
@@ -213,7 +195,7 @@ __device__ __forceinline__ void conv_group(const Words<P> (&q)[kConvStep], int n
 
 template <int W, bool SILU>
 __global__ void __launch_bounds__(32 * kConvWarps, kConvFwdCtas) causal_conv_fwd_kernel(const ConvArgs a, int run) {
-    constexpr int H = W - 1, P = kConvPairs;
+    constexpr int H = W - 1;
     pdl_trigger();
     pdl_wait();
     const ConvPlace p = conv_place(a, run, 64 * P);
@@ -226,26 +208,26 @@ __global__ void __launch_bounds__(32 * kConvWarps, kConvFwdCtas) causal_conv_fwd
     for (int j = 0; j < W; ++j) load_vector(a.w + (long long)j * a.D + p.c, w[j]);
     if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
-    for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
+    for (int j = 0; j < H; ++j) unpack_words(conv_input<W>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
     const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
     uint16_t* py = a.y + (row + p.t0) * a.D + p.c;
-    Words<P> next[kConvStep];
+    Words next[kConvStep];
 #pragma unroll
-    for (int r = 0; r < kConvStep; ++r) next[r] = r < p.end - p.t0 ? load_words<P>(px + r * a.x.st) : no_words<P>();
+    for (int r = 0; r < kConvStep; ++r) next[r] = r < p.end - p.t0 ? load_words(px + r * a.x.st) : no_words();
     for (int t = p.t0; t < p.end; t += kConvStep, py += (long long)kConvStep * a.D) {
         const int n = p.end - t;
-        Words<P> q[kConvStep];
+        Words q[kConvStep];
         px += kConvStep * a.x.st;
 #pragma unroll
         for (int r = 0; r < kConvStep; ++r) {
             q[r] = next[r];
-            next[r] = r + kConvStep < n ? load_words<P>(px + r * a.x.st) : no_words<P>();
+            next[r] = r + kConvStep < n ? load_words(px + r * a.x.st) : no_words();
         }
         const uint32_t history = next_starts<H>(starts);
         if (n >= kConvStep && history == 0u)
-            conv_group<W, P, SILU, true>(q, n, 0u, w, bias, v, py, a.D);
+            conv_group<W, SILU, true>(q, n, 0u, w, bias, v, py, a.D);
         else
-            conv_group<W, P, SILU, false>(q, n, history, w, bias, v, py, a.D);
+            conv_group<W, SILU, false>(q, n, history, w, bias, v, py, a.D);
     }
     // the row's last inputs, as far as they belong to its last sequence
     if (a.state_out != nullptr && p.end == a.L) {
@@ -257,7 +239,7 @@ __global__ void __launch_bounds__(32 * kConvWarps, kConvFwdCtas) causal_conv_fwd
 #pragma unroll
         for (int k = 0; k < H; ++k)   // the input k tokens before the last
             store_words(a.state_out + ((long long)p.b * H + H - 1 - k) * a.D + p.c,
-                        tap_live(history, k) ? conv_input<W, P>(a, p.b, p.c, a.L - 1 - k) : no_words<P>());
+                        tap_live(history, k) ? conv_input<W>(a, p.b, p.c, a.L - 1 - k) : no_words());
     }
 }
 
@@ -298,10 +280,9 @@ __global__ void __launch_bounds__(128) causal_conv_step_kernel(const ConvArgs a)
     for (int k = 0; k < H; ++k) *reinterpret_cast<uint4*>(a.state_out + (b * H + k) * a.D + c) = rows[k + 1];
 }
 
-template <int P>
 __device__ __forceinline__ void put_channels_of(void* p, long long at, bool f32, const f2x (&v)[P]) {
     if (!f32) {
-        Words<P> o;
+        Words o;
 #pragma unroll
         for (int e = 0; e < P; ++e) o.w[e] = x2bf(v[e]);
         store_words(static_cast<uint16_t*>(p) + at, o);
@@ -316,18 +297,18 @@ __device__ __forceinline__ void put_channels_of(void* p, long long at, bool f32,
 }
 
 // The gradients that a thread adds up along its run, and the sums of dx of the last W tokens.
-template <int W, int P>
+template <int W>
 struct ConvSums {
     f2x dw[W][P], db[P], dx[W][P];
 };
 // One token backward: d becomes dpre; dx[H - j] of the token j earlier, and the
 // weights' sums (in: the token is the run's own).
-template <int W, int P, bool SILU, bool CUT>
+template <int W, bool SILU, bool CUT>
 __device__ __forceinline__ void conv_token_back(const f2x (&w)[W][P], const f2x (&bias)[P], const f2x (&v)[W][P], uint32_t history,
-                                                bool in, f2x (&d)[P], ConvSums<W, P>& s) {
+                                                bool in, f2x (&d)[P], ConvSums<W>& s) {
     if (SILU) {
         f2x pre[P];
-        conv_sum<W, P, CUT>(w, bias, v, history, pre);
+        conv_sum<W, CUT>(w, bias, v, history, pre);
 #pragma unroll
         for (int e = 0; e < P; ++e) {
             float p0, p1;
@@ -348,10 +329,10 @@ __device__ __forceinline__ void conv_token_back(const f2x (&w)[W][P], const f2x 
 }
 // kConvStep tokens backward, of which n are there and `own` the run's own; the first is token `from` of the run.
 // PLAIN: all of both, and no start reaches their taps.
-template <int W, int P, bool SILU, bool PLAIN>
-__device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const ConvPlace& p, const Words<P> (&q)[kConvStep],
-                                                const Words<P> (&qd)[kConvStep], int n, int own, int from, uint32_t history,
-                                                const f2x (&w)[W][P], const f2x (&bias)[P], f2x (&v)[W][P], ConvSums<W, P>& s) {
+template <int W, bool SILU, bool PLAIN>
+__device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const ConvPlace& p, const Words (&q)[kConvStep],
+                                                const Words (&qd)[kConvStep], int n, int own, int from, uint32_t history,
+                                                const f2x (&w)[W][P], const f2x (&bias)[P], f2x (&v)[W][P], ConvSums<W>& s) {
     constexpr int H = W - 1;
     const long long at = (long long)p.b * g.dx.sb + (long long)(p.t0 + from - H) * g.dx.st + p.c;
 #pragma unroll
@@ -362,7 +343,7 @@ __device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const Conv
         if (PLAIN || r < n) {
             f2x d[P];
             unpack_words(qd[r], d);
-            conv_token_back<W, P, SILU, !PLAIN>(w, bias, v, history >> (kConvStep - 1 - r), PLAIN || r < own, d, s);
+            conv_token_back<W, SILU, !PLAIN>(w, bias, v, history >> (kConvStep - 1 - r), PLAIN || r < own, d, s);
         }
         // dx[0] is whole now: the token H earlier.  Before the run it is another thread's, before the row an
         // input carried in.
@@ -380,7 +361,7 @@ __device__ __forceinline__ void conv_group_back(const ConvBwdArgs& g, const Conv
 
 template <int W, bool SILU>
 __global__ void __launch_bounds__(32 * kConvWarps, conv_bwd_ctas(W)) causal_conv_bwd_kernel(const ConvBwdArgs g, int run) {
-    constexpr int H = W - 1, P = kConvPairs;
+    constexpr int H = W - 1;
     __shared__ f2x acc[kConvWarps][W + 1][32][P];
     pdl_trigger();
     pdl_wait();
@@ -389,7 +370,7 @@ __global__ void __launch_bounds__(32 * kConvWarps, conv_bwd_ctas(W)) causal_conv
     const ConvPlace p = conv_place(a, run, 64 * P);
     const long long row = (long long)p.b * a.L;
     Starts starts = starts_of(a.reset, row, p.t0, a.L, lane);
-    ConvSums<W, P> s;
+    ConvSums<W> s;
     clear(s.db);
 #pragma unroll
     for (int j = 0; j < W; ++j) {
@@ -404,22 +385,22 @@ __global__ void __launch_bounds__(32 * kConvWarps, conv_bwd_ctas(W)) causal_conv
         for (int j = 0; j < W; ++j) load_vector(a.w + (long long)j * a.D + p.c, w[j]);
         if (a.bias != nullptr) load_vector(a.bias + p.c, bias);
 #pragma unroll
-        for (int j = 0; j < H; ++j) unpack_words(conv_input<W, P>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
+        for (int j = 0; j < H; ++j) unpack_words(conv_input<W>(a, p.b, p.c, p.t0 - 1 - j), v[j]);
         const uint16_t* px = a.x.p + (long long)p.b * a.x.sb + (long long)p.t0 * a.x.st + p.c;
         const uint16_t* py = g.dy + (row + p.t0) * a.D + p.c;
         // the run's tokens, then the H after it, whose taps reach into it
-        Words<P> nq[kConvStep], nqd[kConvStep];
+        Words nq[kConvStep], nqd[kConvStep];
         const int total = min(a.L, p.end + H) - p.t0;
 #pragma unroll
         for (int r = 0; r < kConvStep; ++r) {
-            nq[r] = nqd[r] = no_words<P>();
+            nq[r] = nqd[r] = no_words();
             if (r < total) {
-                nq[r] = load_words<P>(px + r * a.x.st);
-                nqd[r] = load_words<P>(py + (long long)r * a.D);
+                nq[r] = load_words(px + r * a.x.st);
+                nqd[r] = load_words(py + (long long)r * a.D);
             }
         }
         for (int t = p.t0; t < p.end + H; t += kConvStep) {
-            Words<P> q[kConvStep], qd[kConvStep];
+            Words q[kConvStep], qd[kConvStep];
             const int n = min(a.L, p.end + H) - t, own = p.end - t;   // (may be none)
             px += kConvStep * a.x.st;
             py += (long long)kConvStep * a.D;
@@ -427,17 +408,17 @@ __global__ void __launch_bounds__(32 * kConvWarps, conv_bwd_ctas(W)) causal_conv
             for (int r = 0; r < kConvStep; ++r) {
                 q[r] = nq[r];
                 qd[r] = nqd[r];
-                nq[r] = nqd[r] = no_words<P>();
+                nq[r] = nqd[r] = no_words();
                 if (r + kConvStep < n) {
-                    nq[r] = load_words<P>(px + r * a.x.st);
-                    nqd[r] = load_words<P>(py + (long long)r * a.D);
+                    nq[r] = load_words(px + r * a.x.st);
+                    nqd[r] = load_words(py + (long long)r * a.D);
                 }
             }
             const uint32_t history = next_starts<H>(starts);
             if (own >= kConvStep && history == 0u)
-                conv_group_back<W, P, SILU, true>(g, p, q, qd, n, own, t - p.t0, 0u, w, bias, v, s);
+                conv_group_back<W, SILU, true>(g, p, q, qd, n, own, t - p.t0, 0u, w, bias, v, s);
             else
-                conv_group_back<W, P, SILU, false>(g, p, q, qd, n, own, t - p.t0, history, w, bias, v, s);
+                conv_group_back<W, SILU, false>(g, p, q, qd, n, own, t - p.t0, history, w, bias, v, s);
         }
     }
 #pragma unroll
@@ -515,7 +496,7 @@ cudaError_t launch_causal_conv_step(const ConvArgs& a, cudaStream_t s, bool pdl)
     });
 }
 cudaError_t launch_causal_conv_bwd(const ConvBwdArgs& g, cudaStream_t s, bool pdl) {
-    const dim3 grid((unsigned)((long long)g.parts * ((g.f.D + 64 * kConvPairs - 1) / (64 * kConvPairs))));
+    const dim3 grid((unsigned)((long long)g.parts * ((g.f.D + 64 * P - 1) / (64 * P))));
     const int run = conv_run(g.f.B, g.f.L, g.f.D, conv_bwd_ctas(g.f.W));
     return by_width(g.f.W, g.f.silu, [&](auto w, auto silu) {
         return launch_ex(causal_conv_bwd_kernel<decltype(w)::value, decltype(silu)::value>, grid, dim3(32 * kConvWarps), 0, s,

@@ -220,6 +220,25 @@ __device__ __forceinline__ void stage_bias(const float* bias, int c0, int D, flo
 // The warp's number in its CTA, the same in all its lanes for the compiler too.
 __device__ __forceinline__ int warp_of() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 
+struct SsmPlace {
+    int b, chunk, group, warp;
+    bool on;
+};
+// CTAs: chunk by chunk (`chunks` of a row, from number `first` on), then the groups of a row side by side (they share b
+// and c in L1).
+__device__ __forceinline__ SsmPlace place(const SsmArgs& a, int chunks, int first) {
+    SsmPlace p;
+    const long long i = blockIdx.x;
+    const int gq = (int)(i % a.ngq);
+    const long long r = i / a.ngq;
+    p.chunk = first + (int)(r % chunks);
+    p.b = (int)(r / chunks);
+    p.warp = warp_of();
+    p.group = gq * (blockDim.x >> 5) + p.warp;
+    p.on = p.group < a.groups;
+    return p;
+}
+
 // The first of the rows of batch row b from token t on, from channel c on.
 __device__ __forceinline__ const uint16_t* row_at(const SsmRows& r, int b, int t, int c) {
     return r.p + (long long)b * r.sb + (long long)t * r.st + c;

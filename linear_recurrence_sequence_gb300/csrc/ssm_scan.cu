@@ -141,24 +141,6 @@ __device__ __forceinline__ void advance(const FwdTile<LN, Y>& s, int t, int lc, 
     }
 }
 
-struct SsmPlace {
-    int b, chunk, group, warp;
-    bool on;
-};
-// CTAs: chunk by chunk, then the groups of a row side by side (they share b and c in L1).
-__device__ __forceinline__ SsmPlace place(const SsmArgs& a, int chunks) {
-    SsmPlace p;
-    const long long i = blockIdx.x;
-    const int gq = (int)(i % a.ngq);
-    const long long r = i / a.ngq;
-    p.chunk = (int)(r % chunks);
-    p.b = (int)(r / chunks);
-    p.warp = warp_of();
-    p.group = gq * (blockDim.x >> 5) + p.warp;
-    p.on = p.group < a.groups;
-    return p;
-}
-
 template <int LN>
 __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(const SsmArgs a) {
     using W = SsmWarp<LN>;
@@ -166,7 +148,7 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_maps_kernel(cons
     extern __shared__ __align__(16) uint8_t buf[];
     pdl_wait();
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
-    const SsmPlace p = place(a, a.nchunk - 1);
+    const SsmPlace p = place(a, a.nchunk - 1, 0);
     if (!p.on) return;
     FwdTile<LN, false>& s = reinterpret_cast<FwdTile<LN, false>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
@@ -277,7 +259,7 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
     extern __shared__ __align__(16) uint8_t buf[];
     pdl_wait();
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
-    const SsmPlace p = place(a, a.nchunk);
+    const SsmPlace p = place(a, a.nchunk, 0);
     if (!p.on) return;
     FwdTile<LN, true>& s = reinterpret_cast<FwdTile<LN, true>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;

@@ -54,24 +54,6 @@ __device__ __forceinline__ void gated(const uint4 qy, const uint4 qz, bool gate,
     }
 }
 
-struct BwdPlace {
-    int b, chunk, group, warp;
-    bool on;
-};
-// chunks: of a row; the first of them is number `first`
-__device__ __forceinline__ BwdPlace bwd_place(const SsmArgs& a, int chunks, int first) {
-    BwdPlace p;
-    const long long i = blockIdx.x;
-    const int gq = (int)(i % a.ngq);
-    const long long r = i / a.ngq;
-    p.chunk = first + (int)(r % chunks);
-    p.b = (int)(r / chunks);
-    p.warp = warp_of();
-    p.group = gq * (blockDim.x >> 5) + p.warp;
-    p.on = p.group < a.groups;
-    return p;
-}
-
 template <int LN>
 struct RevTile {
     static constexpr int T = LN == 1 ? 4 : 8;
@@ -140,7 +122,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 4) ssm_rmaps_kernel(const SsmB
     pdl_wait();
     const SsmArgs& a = g.f;
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
-    const BwdPlace p = bwd_place(a, a.nchunk - 1, 1);
+    const SsmPlace p = place(a, a.nchunk - 1, 1);
     if (!p.on) return;
     RevTile<LN>& s = reinterpret_cast<RevTile<LN>*>(buf)[p.warp];
     const int c0 = p.group * W::CW, ch = c0 + lc * kSsmCh;
@@ -395,7 +377,7 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     tmem_fence_after_sync();
     const SsmArgs& a = g.f;
     const int lane = threadIdx.x & 31, ln = lane % LN, lc = lane / LN;
-    const BwdPlace p = bwd_place(a, g.nchunk, 0);
+    const SsmPlace p = place(a, g.nchunk, 0);
     BwdTile<LN>* tiles = reinterpret_cast<BwdTile<LN>*>(buf);
     BwdTile<LN>& s = tiles[p.warp];
     const uint32_t tmem = s_tmem + ((uint32_t)p.warp << 21);   // the warp's 32 lanes

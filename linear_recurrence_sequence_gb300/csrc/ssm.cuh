@@ -266,14 +266,15 @@ __device__ __forceinline__ void load_states(const float* m, bool quads, int c0, 
         }
     }
 }
-// The rates of a lane's states (1 past N and D, where the states and all that is added to them are zeros).
+// The rates of a lane's states (1 past N and D, where the states and all that is added to them are zeros; ZERO: 0 there).
+template <bool ZERO = false>
 __device__ __forceinline__ void load_rates(const float* a_log, bool quads, int c0, int n0, int D, int N, SsmStates& A) {
     float v[kSsmCh][kSsmSt];
     load_states(a_log, quads, c0, n0, D, N, v);
 #pragma unroll
     for (int i = 0; i < kSsmCh; ++i)
 #pragma unroll
-        for (int j = 0; j < kSsmSt; ++j) v[i][j] = ssm_rate(v[i][j]);
+        for (int j = 0; j < kSsmSt; ++j) v[i][j] = !ZERO || (c0 + i < D && n0 + j < N) ? ssm_rate(v[i][j]) : 0.f;
 #pragma unroll
     for (int j = 0; j < kSsmSt; ++j) {
         A[j][0] = pk2(v[0][j], v[1][j]);

@@ -385,7 +385,9 @@ __global__ void __launch_bounds__(kBwdWarps * 32, 2) ssm_bwd_kernel(const SsmBwd
     const int c8 = lane % W::RL * 8, r0 = lane / W::RL;
     const bool on = p.on && c0 + c8 < a.D;
     SsmStates A, u, dA;
-    load_rates(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
+    // (zeros where they need not be: for 9 to 16 states the compiler then keeps to 236 registers, else 255 and spills,
+    // 1 x 8192 x 2560 backward 437 us against 433)
+    load_rates<LN == 2>(a.a_log, a.rate_quads, ch, ln * kSsmSt, a.D, a.N, A);
     // the chunk ends where the last of its maps does
     const long long slot = ((long long)p.b * a.nchunk + min((p.chunk + 1) * g.per, a.nchunk) - 1) * a.groups + p.group;
     if (a.nchunk > 1 && p.on)

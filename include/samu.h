@@ -747,6 +747,8 @@ int selective_scan_step(const lrs_rows* x, const lrs_rows* delta, const float* a
  *   dd_skip, ddelta_bias  [D] FP32 (out) or NULL (and NULL without the vector)
  *   dh0      [B,D,N] FP32 (out; may be dhT) or NULL
  *   scratch  selective_scan_workspace_bytes().backward bytes
+ * Every token, padding too, takes part in the parameters' gradients: finite inputs with
+ * dy = 0 add nothing to them, NaN or infinity would.
  * Errors: as the forward, plus LRS_ERR_ARG for an output without its input, for one
  * that begins where an input or another begins and for an unknown grad_dtype. */
 int selective_scan_backward(const void* dy, const float* dhT, const lrs_rows* x, const lrs_rows* delta,

@@ -1608,7 +1608,8 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
 // ---------------------------------------------------------------------------
 namespace {
 
-// Resident per SM, by registers (the backward's main kernel: by tensor memory).
+// Resident per SM, by registers (the backward's main kernel: by tensor memory; up to 8 states, where its four warps' tiles
+// take 156 KB of shared memory, it is one, and its CTAs come in two rounds).
 constexpr int kSsmFwdWarps = 16, kSsmBwdCtas = 2;
 // From a token's row to the next's at most: rows are addressed from the first of a tile's (eight at most) with 32 bits.
 constexpr int kSsmTokenStride = 1 << 26;

@@ -697,7 +697,7 @@ int causal_conv_backward(const void* dy, const lrs_rows* x, const float* weight,
  * off by a reset at its first token, whatever it holds).  D channels, N from 1 to 64.
  * e^a_log ends at FP32's largest value (a_log from 88 on: nothing of a state outlasts a
  * token but one with dt = 0); the backward of a token with dt = 0 takes a_log up to 80.
- * FP32 arithmetic: exponentials by the GPU's fast one (2^-22 relative each), dt within
+ * FP32 arithmetic: decays by the GPU's fast exponential (2^-21.9 relative each), dt within
  * 2^-21 relative (2^-23 |r| more where r = delta + delta_bias is far below 0), SiLU as the
  * convolution's; y is rounded to BF16 once.  Everything runs in a fixed order.
  *

@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kStepThreads, kStepCtas) ssm_step_kernel(const
         float y = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            q.h[e] = q.start != 0 ? k * bb[e] : fmaf(ex2_approx(A[e] * dt), q.h[e], k * bb[e]);
+            q.h[e] = q.start != 0 ? k * bb[e] : fmaf(ex2_approx(fmaf(A[e], dt, kEx2Low)), q.h[e], k * bb[e]);
             y = fmaf(q.h[e], cc[e], y);
         }
         float* ps = state + (b * a.D + c) * a.N + n0;

@@ -21,10 +21,10 @@
 // bytes of a row at N = 16), dt and dt x as FP32 in shared memory, from where
 // the lanes that share a channel read them; the next tokens' rows are copied
 // meanwhile.  No barrier between warps.
-//   4 x 4096 x 1024, 16 states: maps 62 us (SFU 53%, FP32 pipe 51%), prefix 9, replay
-//   92 with the states that the backward needs (FP32 pipe 46%, shared memory 53%); the
+//   4 x 4096 x 1024, 16 states: maps 59 us (SFU 54%, FP32 pipe 51%), prefix 10, replay
+//   88 with the states that the backward needs (FP32 pipe 47%, shared memory 48%); the
 //   rest are the two-wide FP32 instructions' register reads and the staging.
-//   1 x 8192 x 2560: 76, 11 and 108 us.
+//   1 x 8192 x 2560: 76, 12 and 106 us.
 #include <algorithm>
 #include <cmath>
 
@@ -346,7 +346,7 @@ __global__ void __launch_bounds__(kSsmWarps * 32, kSsmCtas) ssm_replay_kernel(co
 // (16 bytes of the state row), and go through the batch.  Bound by the state, read
 // and written once in FP32 (256 sequences of 2048 channels and 16 states: 67 MB).
 // While it computes a sequence a thread asks for the next one's inputs (1024 sequences of
-// 4096 channels and 64 states, 2.1 GB: 454 us, 4.7 TB/s of a copy's 6.8, else 559; the 67
+// 4096 channels and 64 states, 2.1 GB: 440 us, 4.9 TB/s of a copy's 6.8, else 559; the 67
 // MB above, which stay in L2 between calls, 15 us, else 17).  Asking further ahead costs
 // warps and is slower (two sequences ahead 19 us and 491).
 constexpr int kStepThreads = 256, kStepCtas = 4;

@@ -17,13 +17,13 @@
 //           kept before them, then the adjoint back through them;
 //   finish  the sums over chunks and over the CTAs of a token, in a fixed order.
 // In main the states before the tile's eight tokens wait in tensor memory, 32 columns a
-// token (a lane's 4 x 8 states), so that shared memory (43% busy) keeps to the operands,
-// which every lane of a channel reads, and 250 registers a thread hold the rates, the
+// token (a lane's 4 x 8 states), so that shared memory (42% busy) keeps to the operands,
+// which every lane of a channel reads, and 236 to 255 registers a thread hold the rates, the
 // adjoint and dA: 2 CTAs an SM, by tensor memory however few warps they have (2 warps an SM
 // where D is one group of channels).  Up to 8 states a warp's tile is 39 KB and a CTA of four
 // takes 156: one an SM, though time is cut for two.  13 multiply-adds and two exponentials a
 // (token, channel, state) there, 3 and one in rmaps.
-//   4 x 4096 x 1024, 16 states: rmaps 66 us, prefix 10, main 271, finish 10.
+//   4 x 4096 x 1024, 16 states: rmaps 65 us, prefix 10, main 272, finish 10.
 // Main issues 20 instructions for 32 states, 0.56 a clock and scheduler with 2 warps each:
 // 7 of them two-wide FP32 ones, which take the pipe and the register file 2 to 4 clocks, 2.4
 // exponentials, 3 of the sums across lanes.  Other forms of main measured there: 4 x 4 states
